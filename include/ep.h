@@ -1,6 +1,7 @@
 /*
  * transformer_epilogue_gb300 — C ABI of the fused transformer-block epilogue ops
- * (SkipLayerNormalization, BiasSoftmax, BiasAdd, QuickGelu) for one NVIDIA GB300
+ * (SkipLayerNormalization, BiasSoftmax, BiasAdd, QuickGelu, GroupNorm and
+ * BiasDropout, the last two with their gradients) for one NVIDIA GB300
  * (sm_103a) GPU.
  *
  * The ops are the com.microsoft ONNX Runtime contrib ops whose definitions are
@@ -8,7 +9,9 @@
  * "com.microsoft.BiasSoftmax", "com.microsoft.BiasAdd" and
  * "com.microsoft.QuickGelu" (sections `description`, `inputs`, `outputs`,
  * `attributes`, `derive`).  Each entry point below cites the section that
- * defines what it computes.
+ * defines what it computes.  GroupNorm and BiasDropout are ops of the same
+ * contrib family that have no manifest page; their declarations state the whole
+ * definition.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -23,18 +26,18 @@
  *    scheduled while that work drains, but no block reads or writes global
  *    memory before every kernel ahead of it in the stream has completed, so the
  *    ordering seen by the caller is ordinary stream order.  Calls may be
- *    captured into CUDA graphs (the split-row workspace must then outlive the
- *    graph).
+ *    captured into CUDA graphs (a workspace must then outlive the graph).
  *  - All validation happens before anything is enqueued.  A contract violation
  *    returns EP_ERR_INVALID_ARG, a legal op this library does not implement
  *    (another element type, an unsupported rank) returns EP_ERR_UNSUPPORTED, a
- *    split-row BiasSoftmax without enough workspace returns EP_ERR_WORKSPACE, and
+ *    call without the workspace it needs returns EP_ERR_WORKSPACE, and
  *    a launch error reported by the CUDA runtime returns EP_ERR_CUDA.  On any
  *    non-OK status nothing has been enqueued, except for EP_ERR_CUDA (the
  *    runtime's state is then whatever the failing launch left).  ep_last_error()
  *    gives a message for the calling thread's last non-OK status.
  *  - Empty tensors (numel 0) return EP_OK without launching anything; their
- *    pointers may be NULL.
+ *    pointers may be NULL.  (Sums over them, dgamma, dbeta and dbias, are set
+ *    to 0 on the stream.)
  *  - Pointers must be aligned to sizeof(T).  16-byte alignment is not
  *    required: it selects the 128-bit vector path (BiasAdd and QuickGelu also
  *    when X, skip and Y share one offset within 16 bytes), and other alignments
@@ -69,7 +72,7 @@ typedef enum {
   EP_OK = 0,
   EP_ERR_INVALID_ARG = 1,   /* shape, attribute, pointer or overlap contract violated   */
   EP_ERR_UNSUPPORTED = 2,   /* legal for the op, not implemented here (dtype, rank)     */
-  EP_ERR_WORKSPACE = 3,     /* split-row BiasSoftmax: workspace NULL or too small       */
+  EP_ERR_WORKSPACE = 3,     /* a needed workspace is NULL, too small, misaligned or overlapping */
   EP_ERR_CUDA = 4           /* the CUDA runtime reported an error for a launch          */
 } ep_status;
 
@@ -264,6 +267,137 @@ ep_status ep_bias_add(ep_dtype t, const void* X, const int64_t* shape,
  */
 ep_status ep_quick_gelu(ep_dtype t, const void* X, int64_t numel, float alpha,
                         void* Y, ep_stream_t stream);
+
+/* Activation of GroupNorm (the contrib op's `activation` attribute). */
+typedef enum { EP_ACT_NONE = 0, EP_ACT_SILU = 1 } ep_activation;
+
+/*
+ * GroupNorm
+ *   The GroupNorm op of the com.microsoft contrib family with channels_last = 1.
+ *   The channels of X form `groups` groups of D = C / groups neighbours; per
+ *   sample n and group g, over its S * D values:
+ *
+ *   mu = mean(X), var = mean((X - mu)^2)          (population)
+ *   u[n, s, c] = (X[n, s, c] - mu) / sqrt(var + epsilon) * gamma[c] + beta[c]
+ *   Y = u (EP_ACT_NONE) or u * sigmoid(u) (EP_ACT_SILU)
+ *
+ * shape        3 dims (N, S, C) of X and Y; S is the product of the spatial
+ *              sizes (1: a norm over each token's groups of channels).  C is at
+ *              most 2^24.
+ * gamma        C elements (required).  beta: C elements or NULL.
+ * groups       > 0, divides C.
+ * epsilon      >= 0 (the op's default is 1e-5).
+ * mean, inv_std_dev   NULL, or N * groups float32 values: mu and
+ *              1/sqrt(var + epsilon), which ep_group_norm_grad takes.
+ * workspace    device scratch of ep_group_norm_workspace_size() bytes (may be
+ *              NULL when that is 0), 16-byte aligned; its contents on entry do
+ *              not matter.  Calls that may overlap on the GPU (other streams,
+ *              concurrently replayed graphs) need one each.
+ * Y may be X.  Of an empty tensor nothing is written, mean and inv_std_dev
+ * included.
+ *
+ * Errors: EP_ERR_UNSUPPORTED for another dtype or C > 2^24; EP_ERR_INVALID_ARG
+ * for negative dims, groups that do not divide C, a negative or NaN epsilon, another
+ * activation, NULL/misaligned pointers or overlaps; EP_ERR_WORKSPACE.
+ */
+ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape,
+                        const void* gamma, const void* beta,
+                        int64_t groups, float epsilon, int activation,
+                        void* Y, float* mean, float* inv_std_dev,
+                        void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Workspace bytes ep_group_norm needs; 0 as well for arguments it rejects.
+ * They depend on the arguments alone. */
+size_t ep_group_norm_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups);
+
+/*
+ * Gradient of ep_group_norm.
+ *   With h = (X - mean) * inv_std_dev, u = h * gamma + beta, s = sigmoid(u):
+ *
+ *   du = dY (EP_ACT_NONE) or dY * s * (1 + u * (1 - s)) (EP_ACT_SILU)
+ *   dbeta[c] = sum over n, s of du,  dgamma[c] = sum over n, s of du * h
+ *   dX = inv_std_dev * (du * gamma - m1 - h * m2),
+ *   m1 = mean over the group of du * gamma, m2 of du * gamma * h
+ *
+ * dY, X, dX    (N, S, C).  dX may be dY or X.
+ * gamma, beta, groups, activation   as in the forward call (beta NULL if it was).
+ * mean, inv_std_dev   N * groups float32 values, as ep_group_norm wrote them.
+ * dgamma, dbeta   C elements of T each, or NULL where not wanted.  The sums
+ *              are float32 in a fixed order (the same call gives the same
+ *              bits), rounded once.  Of an empty tensor they are set to 0.
+ * workspace    ep_group_norm_grad_workspace_size() bytes, as for ep_group_norm.
+ *
+ * Errors: as ep_group_norm.
+ */
+ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const int64_t* shape,
+                             const void* gamma, const void* beta, int64_t groups, int activation,
+                             const float* mean, const float* inv_std_dev,
+                             void* dX, void* dgamma, void* dbeta,
+                             void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Workspace bytes ep_group_norm_grad needs; 0 as well for arguments it rejects. */
+size_t ep_group_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups);
+
+/*
+ * BiasDropout
+ *   The BiasDropout op of the com.microsoft contrib family, with its mask a
+ *   function of the element's index instead of an output:
+ *
+ *   Y[i] = residual[i] + keep(i) * (X[i] + bias[i mod C]) / (1 - ratio)
+ *   keep(i) = word(i) < K,  K = round((1 - ratio) * 2^32)
+ *   word(i) = 32-bit word number i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror
+ *             and Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011)
+ *             with the counter words (i/4 low, i/4 high, offset low, offset
+ *             high) and the key words (seed low, seed high)
+ *
+ *   i is the flat index in X.  The same seed, offset and shape give the same
+ *   mask in every call, whatever the element type, and in the gradient; each
+ *   dropout of a step takes an offset (or seed) of its own.
+ *
+ * X, Y         `rank` dims given by `shape` (1 <= rank <= 16), C the last.
+ * bias         C elements or NULL.  residual: the shape of X, or NULL.
+ * ratio        0 <= ratio < 1; 0 keeps everything.
+ * offset_device   NULL, or a device pointer to a 64-bit number that is added
+ *              to offset (modulo 2^64) when the kernel runs: a captured graph
+ *              draws another mask on each replay if the number is changed in
+ *              between.
+ * A dropped element is the residual (or 0) whatever X holds there, infinities
+ * and NaN included.  Y may be X or residual.
+ *
+ * Errors: EP_ERR_UNSUPPORTED for another dtype or rank > 16; EP_ERR_INVALID_ARG
+ * for negative dims, a ratio outside [0, 1), NULL/misaligned pointers or
+ * overlaps.
+ */
+ep_status ep_bias_dropout(ep_dtype t, const void* X, const int64_t* shape, int rank,
+                          const void* bias, const void* residual,
+                          double ratio, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
+                          void* Y, ep_stream_t stream);
+
+/*
+ * Gradient of ep_bias_dropout (that of the residual is dY itself).
+ *
+ *   dX[i] = keep(i) * dY[i] / (1 - ratio),  dbias[c] = sum over rows of dX[., c]
+ *
+ * ratio, seed, offset, offset_device   as in the forward call (*offset_device
+ *              too must still hold the forward call's number).
+ * dX           the shape of dY; may be dY.
+ * dbias        C elements of T, or NULL.  The sum is float32, over the values
+ *              before they are rounded to T, in a fixed order, rounded once.
+ *              Of an empty tensor it is set to 0.
+ * workspace    with dbias: ep_bias_dropout_grad_workspace_size() bytes, 16-byte
+ *              aligned; its contents on entry do not matter.  Calls that may
+ *              overlap on the GPU need one each.
+ *
+ * Errors: as ep_bias_dropout; EP_ERR_WORKSPACE.
+ */
+ep_status ep_bias_dropout_grad(ep_dtype t, const void* dY, const int64_t* shape, int rank,
+                               double ratio, uint64_t seed, uint64_t offset, const uint64_t* offset_device,
+                               void* dX, void* dbias,
+                               void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Workspace bytes ep_bias_dropout_grad needs for dbias; 0 as well for
+ * arguments it rejects. */
+size_t ep_bias_dropout_grad_workspace_size(ep_dtype t, const int64_t* shape, int rank);
 
 #ifdef __cplusplus
 }  /* extern "C" */

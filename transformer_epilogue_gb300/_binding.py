@@ -8,6 +8,7 @@ no CPU or PyTorch fallback.  A non-OK status raises ``EpError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -21,10 +22,13 @@ EP_OK, EP_ERR_INVALID_ARG, EP_ERR_UNSUPPORTED, EP_ERR_WORKSPACE, EP_ERR_CUDA = 0
 STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_UNSUPPORTED", 3: "EP_ERR_WORKSPACE",
                 4: "EP_ERR_CUDA"}
 
+EP_ACT_NONE, EP_ACT_SILU = 0, 1
+
 # Attribute defaults of the op definitions (manifest `attributes` sections).
 DEFAULT_EPSILON = 9.999999960041972e-13   # SkipLayerNormalization
 DEFAULT_ALPHA = 1.702                     # QuickGelu
 DEFAULT_AXIS = 1                          # BiasSoftmax
+DEFAULT_GROUP_NORM_EPSILON = 1e-5         # GroupNorm (contrib op schema)
 
 _TORCH_TO_EP = {torch.float32: EP_F32, torch.float16: EP_F16, torch.bfloat16: EP_BF16}
 
@@ -53,6 +57,18 @@ _SIGNATURES = {
                                                ctypes.c_int, ctypes.c_int, _vp, _vp]),
     "ep_bias_add": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, _vp, _vp, _vp, _vp]),
     "ep_quick_gelu": (ctypes.c_int, [ctypes.c_int, _vp, ctypes.c_int64, ctypes.c_float, _vp, _vp]),
+    "ep_group_norm": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, _vp, _vp, ctypes.c_int64, ctypes.c_float,
+                                     ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ep_group_norm_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
+    "ep_group_norm_grad": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _i64p, _vp, _vp, ctypes.c_int64, ctypes.c_int,
+                                          _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ep_group_norm_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
+    "ep_bias_dropout": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, _vp, _vp, ctypes.c_double,
+                                       ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _vp]),
+    "ep_bias_dropout_grad": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, ctypes.c_double,
+                                            ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                            _vp]),
+    "ep_bias_dropout_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int]),
 }
 
 
@@ -294,3 +310,237 @@ def ep_quick_gelu(X, alpha=DEFAULT_ALPHA, Y=None, stream=None):
     st = lib.ep_quick_gelu(_dtype(X), _ptr(X), int(X.numel()), float(alpha), _ptr(Y), _stream(stream, X.device))
     _check(st)
     return Y
+
+
+# ---------------------------------------------------------------------------
+# GroupNorm and BiasDropout, with their gradients.  Operands are checked against
+# the first one (device, dtype, shape) before their addresses are passed on, and
+# a workspace that is allocated here belongs to the stream the call runs on.
+# ---------------------------------------------------------------------------
+
+def _operand(name, t, like, shape=None, dtype=None):
+    """t, checked to be a contiguous CUDA tensor on like's device with the given
+    dtype (like's if None) and shape (any if None)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise TypeError(f"{name} must have dtype {like.dtype if dtype is None else dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _on_stream(stream, device):
+    """A context in which `stream` (the device's current one if None) and its
+    device are current, so that what is allocated inside belongs to it."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _scratch(workspace, need, like):
+    """(pointer, bytes) of the caller's workspace, or of one allocated for this
+    call (and the tensor, to be kept until the call has been enqueued)."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the operands' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _u64(name, v):
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{name} must be an unsigned 64-bit number")
+    return v
+
+
+def _nsc(X):
+    """(N, S, C) of a channels-last tensor: the dimensions between the first and
+    the last are positions."""
+    if X.dim() < 3:
+        raise ValueError("X must have the shape (N, positions..., C)")
+    n, c = X.shape[0], X.shape[-1]
+    s = 1
+    for d in X.shape[1:-1]:
+        s *= d
+    return (ctypes.c_int64 * 3)(n, s, c)
+
+
+def ep_group_norm_workspace_size(dtype, shape, groups) -> int:
+    """Workspace bytes of ep_group_norm for a channels-last (N, S, C) shape."""
+    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load_library().ep_group_norm_workspace_size(code, _shape(shape), int(groups)))
+
+
+def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_EPSILON, activation=EP_ACT_NONE,
+                  Y=None, mean=None, inv_std_dev=None, workspace=None, stream=None):
+    """GroupNorm of a channels-last X (N, positions..., C), optionally followed
+    by a SiLU (``EP_ACT_SILU``).  ``groups`` is required (the op definition has
+    no default for it).  ``mean`` / ``inv_std_dev``: float32 tensors of
+    N * groups elements to fill, True to allocate (N, groups), or None.
+    Returns (Y, mean, inv_std_dev), the last two None when not requested."""
+    if groups is None:
+        raise ValueError("groups is required")
+    lib = load_library()
+    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
+    code, shape = _dtype(X), _nsc(X)
+    n, channels = X.shape[0], X.shape[-1:]
+    groups = int(groups)
+    _operand("gamma", gamma, X, channels)
+    if beta is not None:
+        _operand("beta", beta, X, channels)
+    with _on_stream(stream, X.device):
+        if Y is None:
+            Y = torch.empty_like(X)
+        else:
+            _operand("Y", Y, X, X.shape)
+        mean = _group_stats("mean", mean, X, n, groups)
+        inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, n, groups)
+        ws, wbytes, _keep = _scratch(workspace, lib.ep_group_norm_workspace_size(code, shape, groups), X)
+        _check(lib.ep_group_norm(code, X.data_ptr(), shape, gamma.data_ptr(), _addr(beta), groups, float(epsilon),
+                                 int(activation), Y.data_ptr(), _addr(mean), _addr(inv_std_dev), ws, wbytes,
+                                 torch.cuda.current_stream(X.device).cuda_stream))
+    return Y, mean, inv_std_dev
+
+
+def _group_stats(name, t, X, n, groups):
+    if t is None or t is False:
+        return None
+    if t is True:
+        return torch.empty((n, max(0, groups)), dtype=torch.float32, device=X.device)
+    _operand(name, t, X, dtype=torch.float32)
+    if t.numel() != n * groups:
+        raise ValueError(f"{name} must have {n * groups} elements")
+    return t
+
+
+def ep_group_norm_grad_workspace_size(dtype, shape, groups) -> int:
+    """Workspace bytes of ep_group_norm_grad for a channels-last (N, S, C) shape."""
+    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load_library().ep_group_norm_grad_workspace_size(code, _shape(shape), int(groups)))
+
+
+def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activation=EP_ACT_NONE, dX=None,
+                       dgamma=True, dbeta=True, workspace=None, stream=None):
+    """Gradient of ep_group_norm, from the statistics it returned (``beta``: None
+    where the forward call had none).  ``dgamma`` / ``dbeta``: tensors to fill,
+    True to allocate, or None.  Returns (dX, dgamma, dbeta), the last two None
+    when not requested."""
+    if groups is None:
+        raise ValueError("groups is required")
+    lib = load_library()
+    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
+    code, shape = _dtype(X), _nsc(X)
+    n, channels = X.shape[0], X.shape[-1:]
+    groups = int(groups)
+    _operand("dY", dY, X, X.shape)
+    _operand("gamma", gamma, X, channels)
+    if beta is not None:
+        _operand("beta", beta, X, channels)
+    for name, t in (("mean", mean), ("inv_std_dev", inv_std_dev)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} is required")
+        _group_stats(name, t, X, n, groups)
+    with _on_stream(stream, X.device):
+        if dX is None:
+            dX = torch.empty_like(X)
+        else:
+            _operand("dX", dX, X, X.shape)
+        dgamma = _param_grad("dgamma", dgamma, X, channels)
+        dbeta = _param_grad("dbeta", dbeta, X, channels)
+        ws, wbytes, _keep = _scratch(workspace, lib.ep_group_norm_grad_workspace_size(code, shape, groups), X)
+        _check(lib.ep_group_norm_grad(code, dY.data_ptr(), X.data_ptr(), shape, gamma.data_ptr(), _addr(beta), groups,
+                                      int(activation), mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(),
+                                      _addr(dgamma), _addr(dbeta), ws, wbytes,
+                                      torch.cuda.current_stream(X.device).cuda_stream))
+    return dX, dgamma, dbeta
+
+
+def _param_grad(name, t, X, channels):
+    if t is None or t is False:
+        return None
+    if t is True:
+        return torch.empty(channels, dtype=X.dtype, device=X.device)
+    return _operand(name, t, X, channels)
+
+
+def _offset_device(t, like):
+    """A device number added to the offset: one int64 or uint64 element."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device or t.numel() != 1 \
+            or t.dtype not in (torch.int64, torch.uint64):
+        raise ValueError("offset_device must be one int64 or uint64 element on the operands' device")
+    return t.data_ptr()
+
+
+def ep_bias_dropout(X, ratio, seed, offset=0, bias=None, residual=None, offset_device=None, Y=None, stream=None):
+    """BiasDropout: residual + keep * (X + bias) / (1 - ratio), the mask made
+    from (seed, offset) and the element's index.  ``offset_device``: a one-element
+    int64 CUDA tensor added to ``offset`` when the kernel runs (for captured
+    graphs).  Returns Y."""
+    lib = load_library()
+    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
+    code = _dtype(X)
+    if X.dim() < 1:
+        raise ValueError("X must have a last dimension")
+    if bias is not None:
+        _operand("bias", bias, X, X.shape[-1:])
+    if residual is not None:
+        _operand("residual", residual, X, X.shape)
+    od = _offset_device(offset_device, X)
+    with _on_stream(stream, X.device):
+        if Y is None:
+            Y = torch.empty_like(X)
+        else:
+            _operand("Y", Y, X, X.shape)
+        _check(lib.ep_bias_dropout(code, X.data_ptr(), _shape(X.shape), X.dim(), _addr(bias), _addr(residual),
+                                   float(ratio), _u64("seed", seed), _u64("offset", offset), od, Y.data_ptr(),
+                                   torch.cuda.current_stream(X.device).cuda_stream))
+    return Y
+
+
+def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
+    """Workspace bytes of ep_bias_dropout_grad with dbias."""
+    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load_library().ep_bias_dropout_grad_workspace_size(code, _shape(shape), len(shape)))
+
+
+def ep_bias_dropout_grad(dY, ratio, seed, offset=0, offset_device=None, dX=None, dbias=None, workspace=None,
+                         stream=None):
+    """Gradient of ep_bias_dropout (the residual's is dY itself).  ``dbias``: a
+    tensor to fill, True to allocate, or None.  Returns (dX, dbias or None)."""
+    lib = load_library()
+    _operand("dY", dY, dY, dtype=dY.dtype if isinstance(dY, torch.Tensor) else None)
+    code = _dtype(dY)
+    if dY.dim() < 1:
+        raise ValueError("dY must have a last dimension")
+    shape, rank = _shape(dY.shape), dY.dim()
+    od = _offset_device(offset_device, dY)
+    with _on_stream(stream, dY.device):
+        if dX is None:
+            dX = torch.empty_like(dY)
+        else:
+            _operand("dX", dX, dY, dY.shape)
+        dbias = _param_grad("dbias", dbias, dY, dY.shape[-1:])
+        need = 0 if dbias is None else lib.ep_bias_dropout_grad_workspace_size(code, shape, rank)
+        ws, wbytes, _keep = _scratch(workspace, need, dY)
+        _check(lib.ep_bias_dropout_grad(code, dY.data_ptr(), shape, rank, float(ratio), _u64("seed", seed),
+                                        _u64("offset", offset), od, dX.data_ptr(), _addr(dbias), ws, wbytes,
+                                        torch.cuda.current_stream(dY.device).cuda_stream))
+    return dX, dbias

@@ -1,0 +1,292 @@
+// BiasDropout and its gradient.
+//
+// Definition (the BiasDropout op of the contrib family that BiasAdd belongs to,
+// with the mask given by a counter instead of stored):
+//   Y[i]  = residual[i] + keep(i) * (X[i] + bias[i mod C]) / (1 - ratio)
+//   dX[i] = keep(i) * dY[i] / (1 - ratio),  dbias[c] = sum over rows of dX
+//   keep(i) = word(i) < K,  K = round((1 - ratio) 2^32)
+//   word(i) = word i mod 4 of Philox4x32-10 at counter (i / 4, offset), key seed
+// (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel random numbers: as easy as
+// 1, 2, 3", SC 2011: ten rounds of two 32x32 -> 64-bit products each).  The mask
+// is a function of the element's index, so the gradient makes it again and
+// nothing of it is stored or read.
+//
+// Arithmetic is float32: X + bias and its product with 1 / (1 - ratio), then one
+// fused multiply-add with the residual; one rounding to T at the store.
+#include <algorithm>
+#include <climits>
+
+#include "column_walk.cuh"
+#include "device_common.cuh"
+#include "ep_internal.h"
+#include "launch_util.h"
+
+namespace ep {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The generator's state of one call: the key, the offset (plus *offset_dev, read
+// when the kernel runs, so that a captured graph draws anew on every replay)
+// and the last word that keeps an element.
+struct DropRng {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_dev;
+  uint32_t last_kept;
+  float scale;
+};
+
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+  uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
+  uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
+    c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
+    c1 = uint32_t(p1);
+    c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
+    c3 = uint32_t(p0);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// keep(i) of the VW elements from index i0 (a multiple of 4) on, as bits.
+template <int VW>
+__device__ __forceinline__ uint32_t keep_bits(int64_t i0, uint64_t offset, const DropRng& g) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int b = 0; b < VW / 4; ++b) {
+    const uint4 w = philox(uint64_t(i0) / 4 + b, offset, g.seed);
+    m |= (uint32_t(w.x <= g.last_kept) | uint32_t(w.y <= g.last_kept) << 1 | uint32_t(w.z <= g.last_kept) << 2 |
+          uint32_t(w.w <= g.last_kept) << 3)
+         << (4 * b);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint64_t offset_of(const DropRng& g) {
+  return g.offset + (g.offset_dev != nullptr ? *g.offset_dev : 0ull);
+}
+
+// BIAS 0: none; 1: C % VW == 0 and the bias 16-byte aligned (a fragment's bias
+// is one 16-byte read); 2: any other.  VEC: X, residual and Y 16-byte aligned.
+// Flat fragments: rows of any C, the last fragment may be partial.
+template <typename T, int BIAS, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, int64_t n, int64_t C,
+               int64_t col_step, DropRng g) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const uint64_t offset = offset_of(g);
+  const int64_t nfrag = (n + VW - 1) / VW;
+  const int64_t stride = int64_t(gridDim.x) * kThreads;
+  const int64_t f00 = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  int64_t col = BIAS ? (f00 * VW) % C : 0;
+  for (int64_t f0 = f00; f0 < nfrag; f0 += stride * U) {
+    float a[U][VW], r[U][VW];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t f = f0 + u * stride;
+      if (f < nfrag) {
+        dev::load_frag<T, VEC>(x, f * VW, n, a[u]);
+        if (residual != nullptr) dev::load_frag<T, VEC>(residual, f * VW, n, r[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t f = f0 + u * stride;
+      if (f < nfrag) {
+        if constexpr (BIAS == 1) {
+          float b[VW];
+          dev::Conv<T>::unpack(dev::ld16_keep(bias + col), b);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) a[u][e] = __fadd_rn(a[u][e], b[e]);
+        } else if constexpr (BIAS == 2) {
+          int64_t c = col;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            a[u][e] = __fadd_rn(a[u][e], dev::ld1_keep(bias + c));
+            if (++c == C) c = 0;
+          }
+        }
+        const uint32_t keep = keep_bits<VW>(f * VW, offset, g);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const float res = residual != nullptr ? r[u][e] : 0.f;
+          a[u][e] = (keep >> e & 1u) ? (residual != nullptr ? fmaf(a[u][e], g.scale, res) : a[u][e] * g.scale) : res;
+        }
+        dev::store_frag<T, VEC>(y, f * VW, n, a[u]);
+        if constexpr (BIAS != 0) {
+          col += col_step;
+          if (col >= C) col -= C;
+        }
+      }
+    }
+  }
+}
+
+// Gradient with dbias: every thread walks one fragment column (column_walk.cuh),
+// adds the dX it writes, in float32 and before they are rounded, to its VW
+// sums, and leaves the sums of its chunk in `partial`: [chunk][C] where one tile covers a
+// walk row (the block adds the repeats of a channel up), else [chunk][walk row].
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads)
+k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRng g, float* partial) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  __shared__ float sums[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const uint64_t offset = offset_of(g);
+  const int tile = blockIdx.x % p.tiles;
+  const int64_t chunk = blockIdx.x / p.tiles;
+  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
+  const bool mine = int(threadIdx.x) < p.tile_frags && j < p.row_frags;
+  float acc[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) acc[e] = 0.f;
+  if (mine) {
+    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
+    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
+      float v[U][VW];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r0 + u < r1) dev::load_frag<T, VEC>(dy, ((r0 + u) * p.row_frags + j) * VW, n, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i0 = ((r0 + u) * p.row_frags + j) * VW;
+        if (r0 + u < r1 && i0 < n) {
+          const uint32_t keep = keep_bits<VW>(i0, offset, g);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            v[u][e] = (keep >> e & 1u) ? v[u][e] * g.scale : 0.f;
+            acc[e] += v[u][e];
+          }
+          dev::store_frag<T, VEC>(dx, i0, n, v[u]);
+        }
+      }
+    }
+  }
+  if (p.tiles > 1) {
+    if (mine) {
+      float* out = partial + (chunk * p.row_frags + j) * VW;
+#pragma unroll
+      for (int e = 0; e < VW; e += 4)
+        *reinterpret_cast<float4*>(out + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+    }
+    return;
+  }
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sums[threadIdx.x * VW + e] = acc[e];
+  }
+  __syncthreads();
+  const int c32 = static_cast<int>(C), reps = static_cast<int>(p.reps);
+  if (reps <= 16) {
+    for (int c = threadIdx.x; c < c32; c += blockDim.x) {
+      float s = 0.f;
+      for (int k = 0; k < reps; ++k) s += sums[c + k * c32];
+      partial[chunk * C + c] = s;
+    }
+  } else {  // few channels, many repeats: a warp each
+    const int lane = threadIdx.x & 31;
+    for (int c = threadIdx.x >> 5; c < c32; c += blockDim.x >> 5) {
+      float s = 0.f;
+      for (int k = lane; k < reps; k += 32) s += sums[c + k * c32];
+      s = dev::warp_sum(s);
+      if (lane == 0) partial[chunk * C + c] = s;
+    }
+  }
+}
+
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline DropRng rng_of(const BiasDropoutArgs& a) {
+  return DropRng{a.seed, a.offset, a.offset_dev, a.last_kept, a.scale};
+}
+
+template <typename T, int BIAS, bool VEC>
+cudaError_t launch_fwd(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  constexpr int VW = dev::Vec16<T>::N;
+  const int64_t nfrag = (a.n + VW - 1) / VW;
+  const int64_t need = (nfrag + kThreads - 1) / kThreads;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(need, int64_t(sm_count) * 8));
+  const int64_t step = BIAS ? (grid * kThreads * VW) % a.C : 0;
+  cudaError_t e = launch(k_bias_dropout<T, BIAS, VEC>, dim3(unsigned(grid)), dim3(kThreads), 0, stream,
+                         static_cast<const T*>(a.x), static_cast<const T*>(a.bias),
+                         static_cast<const T*>(a.residual), static_cast<T*>(a.y), a.n, a.C, step, rng_of(a));
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+template <typename T>
+cudaError_t bias_dropout_t(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  constexpr int VW = dev::Vec16<T>::N;
+  const bool vec = al16(a.x) && al16(a.y) && (a.residual == nullptr || al16(a.residual));
+  const int bias = a.bias == nullptr ? 0 : (a.C % VW == 0 && al16(a.bias)) ? 1 : 2;
+  if (vec) {
+    if (bias == 0) return launch_fwd<T, 0, true>(a, sm_count, stream, launches);
+    if (bias == 1) return launch_fwd<T, 1, true>(a, sm_count, stream, launches);
+    return launch_fwd<T, 2, true>(a, sm_count, stream, launches);
+  }
+  if (bias == 0) return launch_fwd<T, 0, false>(a, sm_count, stream, launches);
+  return launch_fwd<T, 2, false>(a, sm_count, stream, launches);
+}
+
+WalkPlan grad_walk(DType t, int64_t n, int64_t C) {
+  return make_walk(n, C, t == DType::F32 ? 4 : 8, 1, kPlanSms * 4, 4);
+}
+
+template <typename T>
+cudaError_t bias_dropout_grad_t(const BiasDropoutArgs& a, cudaStream_t stream, int* launches) {
+  const WalkPlan p = grad_walk(a.t, a.n, a.C);
+  float* partial = static_cast<float*>(a.workspace);
+  const dim3 grid(unsigned(int64_t(p.tiles) * p.chunks));
+  cudaError_t e;
+  if (al16(a.x) && al16(a.y))
+    e = launch(k_bias_dropout_grad<T, true>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
+               static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
+  else
+    e = launch(k_bias_dropout_grad<T, false>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
+               static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  const int64_t jobs = std::min<int64_t>((a.C + 31) / 32, INT_MAX);
+  e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, partial, int64_t(p.chunks),
+             p.tiles > 1 ? p.reps : int64_t(1), a.C, 1, static_cast<T*>(a.dbias), static_cast<T*>(nullptr));
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_bias_dropout(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  switch (a.t) {
+    case DType::F32: return bias_dropout_t<float>(a, sm_count, stream, launches);
+    case DType::F16: return bias_dropout_t<__half>(a, sm_count, stream, launches);
+    default: return bias_dropout_t<__nv_bfloat16>(a, sm_count, stream, launches);
+  }
+}
+
+cudaError_t launch_bias_dropout_grad(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  // without dbias the gradient is the forward pass of dY, without bias and residual
+  if (a.dbias == nullptr) return launch_bias_dropout(a, sm_count, stream, launches);
+  switch (a.t) {
+    case DType::F32: return bias_dropout_grad_t<float>(a, stream, launches);
+    case DType::F16: return bias_dropout_grad_t<__half>(a, stream, launches);
+    default: return bias_dropout_grad_t<__nv_bfloat16>(a, stream, launches);
+  }
+}
+
+size_t bias_dropout_grad_workspace_bytes(DType t, int64_t n, int64_t C) {
+  const WalkPlan p = grad_walk(t, n, C);
+  const int64_t width = p.tiles > 1 ? p.row_frags * (t == DType::F32 ? 4 : 8) : C;
+  return size_t(p.chunks) * size_t(width) * sizeof(float);
+}
+
+}  // namespace ep

@@ -3,7 +3,9 @@
 // the launch counter.  Kernels and their launch planning live in the .cu files.
 #include "ep.h"
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -414,6 +416,259 @@ ep_status ep_quick_gelu(ep_dtype t, const void* X, int64_t numel, float alpha, v
   int launches = 0;
   cudaError_t e = ep::launch_quick_gelu(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches, "quick_gelu");
+}
+
+namespace {
+
+struct GnShape {
+  int64_t N, S, C, n;
+};
+
+ep_status gn_shape(const char* op, ep_dtype t, const int64_t* shape, int64_t groups, GnShape* g) {
+  if (!valid_dtype(t)) return fail(EP_ERR_UNSUPPORTED, "%s: dtype %d is not float32/float16/bfloat16", op, int(t));
+  if (shape == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: NULL shape array", op);
+  if (!dims_product(shape, 0, 3, &g->n)) return fail(EP_ERR_INVALID_ARG, "%s: negative or overflowing dims", op);
+  g->N = shape[0];
+  g->S = shape[1];
+  g->C = shape[2];
+  if (groups <= 0 || g->C % groups != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: groups %lld must be positive and divide the %lld channels", op,
+                (long long)groups, (long long)g->C);
+  if (g->C > ep::kMaxGroupNormChannels)
+    return fail(EP_ERR_UNSUPPORTED, "%s: %lld channels (at most %lld)", op, (long long)g->C,
+                (long long)ep::kMaxGroupNormChannels);
+  return EP_OK;
+}
+
+ep_status check_activation(const char* op, int activation) {
+  if (activation != EP_ACT_NONE && activation != EP_ACT_SILU)
+    return fail(EP_ERR_INVALID_ARG, "%s: activation %d is neither EP_ACT_NONE nor EP_ACT_SILU", op, activation);
+  return EP_OK;
+}
+
+// The generator's limits of `ratio`: 0 <= ratio < 1, K = round((1 - ratio) 2^32),
+// of which the kernels compare with K - 1 (K >= 1: a ratio within 2^-33 of 1 keeps the word 0).
+ep_status dropout_ratio(const char* op, double ratio, uint32_t* last_kept, float* scale) {
+  if (!(ratio >= 0.0 && ratio < 1.0)) return fail(EP_ERR_INVALID_ARG, "%s: ratio must be in [0, 1)", op);
+  const double k = std::nearbyint((1.0 - ratio) * 4294967296.0);
+  *last_kept = static_cast<uint32_t>(std::max(k, 1.0) - 1.0);
+  *scale = static_cast<float>(1.0 / (1.0 - ratio));
+  return EP_OK;
+}
+
+// Zeroes the parameter gradients of an empty tensor (a sum over nothing).
+ep_status zero_fill(const char* op, void* p, int64_t bytes, ep_stream_t stream) {
+  if (p == nullptr || bytes <= 0) return EP_OK;
+  const cudaError_t e = cudaMemsetAsync(p, 0, size_t(bytes), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(EP_ERR_CUDA, "%s: cudaMemsetAsync: %s", op, cudaGetErrorString(e));
+  return EP_OK;
+}
+
+// A workspace of `need` bytes that overlaps none of the operands.
+ep_status check_workspace(const char* op, const void* workspace, size_t bytes, size_t need, const Span* spans,
+                          int n) {
+  if (need == 0) return EP_OK;
+  if (workspace == nullptr || bytes < need || !aligned(workspace, 16))
+    return fail(EP_ERR_WORKSPACE, "%s: needs %zu bytes of 16-byte-aligned workspace, got %zu%s", op, need,
+                workspace == nullptr ? size_t(0) : bytes,
+                (workspace != nullptr && !aligned(workspace, 16)) ? " (misaligned)" : "");
+  const Span ws{workspace, int64_t(need)};
+  for (int i = 0; i < n; ++i)
+    if (overlap(ws, spans[i])) return fail(EP_ERR_WORKSPACE, "%s: workspace overlaps an operand", op);
+  return EP_OK;
+}
+
+}  // namespace
+
+size_t ep_group_norm_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups) {
+  GnShape g;
+  char saved[sizeof(g_err)];
+  std::memcpy(saved, g_err, sizeof(g_err));
+  const ep_status s = gn_shape("group_norm_workspace_size", t, shape, groups, &g);
+  std::memcpy(g_err, saved, sizeof(g_err));
+  if (s != EP_OK || g.n == 0) return 0;
+  return ep::group_norm_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+}
+
+ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape, const void* gamma, const void* beta,
+                        int64_t groups, float epsilon, int activation, void* Y, float* mean, float* inv_std_dev,
+                        void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+  GnShape g;
+  if (ep_status s = gn_shape("group_norm", t, shape, groups, &g); s != EP_OK) return s;
+  if (!(epsilon >= 0.0f)) return fail(EP_ERR_INVALID_ARG, "group_norm: epsilon must be >= 0");
+  if (ep_status s = check_activation("group_norm", activation); s != EP_OK) return s;
+  if (g.n == 0) return ok();
+  if (X == nullptr || gamma == nullptr || Y == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "group_norm: X, gamma and Y are required");
+  const int es = esize(t);
+  const void* ptrs[] = {X, gamma, beta, Y};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned(p, es))
+      return fail(EP_ERR_INVALID_ARG, "group_norm: pointer %p is not aligned to the element size", p);
+  if ((mean != nullptr && !aligned(mean, 4)) || (inv_std_dev != nullptr && !aligned(inv_std_dev, 4)))
+    return fail(EP_ERR_INVALID_ARG, "group_norm: mean / inv_std_dev must be 4-byte aligned");
+  const int64_t nb = g.n * es, cb = g.C * es, sb = g.N * groups * 4;
+  const Span x{X, nb}, y{Y, nb}, ga{gamma, cb}, be{beta, cb}, mn{mean, sb}, iv{inv_std_dev, sb};
+  if (bad_overlap_inplace_ok(y, x) || overlap(y, ga) || overlap(y, be))
+    return fail(EP_ERR_INVALID_ARG, "group_norm: Y overlaps an input other than as an exact alias of X");
+  const Span others[] = {x, y, ga, be};
+  for (const Span& o : others)
+    if (overlap(mn, o) || overlap(iv, o))
+      return fail(EP_ERR_INVALID_ARG, "group_norm: mean / inv_std_dev overlap another operand");
+  if (overlap(mn, iv)) return fail(EP_ERR_INVALID_ARG, "group_norm: mean and inv_std_dev overlap");
+  const size_t need = ep::group_norm_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  const Span all[] = {x, y, ga, be, mn, iv};
+  if (ep_status s = check_workspace("group_norm", workspace, workspace_bytes, need, all, 6); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  ep::GroupNormArgs a{to_dtype(t), X, gamma, beta, Y, mean, inv_std_dev, g.N, g.S, g.C, groups, epsilon,
+                      activation == EP_ACT_SILU, workspace};
+  int launches = 0;
+  cudaError_t e = ep::launch_group_norm(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, "group_norm");
+}
+
+size_t ep_group_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups) {
+  GnShape g;
+  char saved[sizeof(g_err)];
+  std::memcpy(saved, g_err, sizeof(g_err));
+  const ep_status s = gn_shape("group_norm_grad_workspace_size", t, shape, groups, &g);
+  std::memcpy(g_err, saved, sizeof(g_err));
+  if (s != EP_OK || g.n == 0) return 0;
+  return ep::group_norm_grad_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+}
+
+ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const int64_t* shape, const void* gamma,
+                             const void* beta, int64_t groups, int activation, const float* mean,
+                             const float* inv_std_dev, void* dX, void* dgamma, void* dbeta, void* workspace,
+                             size_t workspace_bytes, ep_stream_t stream) {
+  GnShape g;
+  if (ep_status s = gn_shape("group_norm_grad", t, shape, groups, &g); s != EP_OK) return s;
+  if (ep_status s = check_activation("group_norm_grad", activation); s != EP_OK) return s;
+  const int es = esize(t);
+  const void* ptrs[] = {dY, X, gamma, beta, dX, dgamma, dbeta};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned(p, es))
+      return fail(EP_ERR_INVALID_ARG, "group_norm_grad: pointer %p is not aligned to the element size", p);
+  const int64_t nb = g.n * es, cb = g.C * es, sb = g.N * groups * 4;
+  const Span dy{dY, nb}, x{X, nb}, ga{gamma, cb}, be{beta, cb}, mn{mean, sb}, iv{inv_std_dev, sb}, dx{dX, nb},
+      dg{dgamma, cb}, db{dbeta, cb};
+  const Span all[] = {dy, x, ga, be, mn, iv, dx, dg, db};
+  for (int i = 0; i < 9; ++i)
+    if ((i != 7 && overlap(dg, all[i])) || (i != 8 && overlap(db, all[i])))
+      return fail(EP_ERR_INVALID_ARG, "group_norm_grad: dgamma / dbeta overlap another operand");
+  if (g.n == 0) {
+    if (ep_status s = zero_fill("group_norm_grad", dgamma, cb, stream); s != EP_OK) return s;
+    if (ep_status s = zero_fill("group_norm_grad", dbeta, cb, stream); s != EP_OK) return s;
+    return ok();
+  }
+  if (dY == nullptr || X == nullptr || gamma == nullptr || mean == nullptr || inv_std_dev == nullptr || dX == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "group_norm_grad: dY, X, gamma, mean, inv_std_dev and dX are required");
+  if (!aligned(mean, 4) || !aligned(inv_std_dev, 4))
+    return fail(EP_ERR_INVALID_ARG, "group_norm_grad: mean / inv_std_dev must be 4-byte aligned");
+  if (bad_overlap_inplace_ok(dx, dy) || bad_overlap_inplace_ok(dx, x) || overlap(dx, ga) || overlap(dx, be) ||
+      overlap(dx, mn) || overlap(dx, iv))
+    return fail(EP_ERR_INVALID_ARG, "group_norm_grad: dX overlaps an input other than as an exact alias of dY or X");
+  const size_t need = ep::group_norm_grad_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  if (ep_status s = check_workspace("group_norm_grad", workspace, workspace_bytes, need, all, 9); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  ep::GroupNormGradArgs a{to_dtype(t), dY, X, gamma, beta, mean, inv_std_dev, dX, dgamma, dbeta,
+                          g.N, g.S, g.C, groups, activation == EP_ACT_SILU, workspace};
+  int launches = 0;
+  cudaError_t e = ep::launch_group_norm_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, "group_norm_grad");
+}
+
+namespace {
+
+// rows x C of a tensor whose last dimension is C.
+ep_status dropout_shape(const char* op, ep_dtype t, const int64_t* shape, int rank, int64_t* n, int64_t* C) {
+  if (!valid_dtype(t)) return fail(EP_ERR_UNSUPPORTED, "%s: dtype %d is not float32/float16/bfloat16", op, int(t));
+  if (rank < 1) return fail(EP_ERR_INVALID_ARG, "%s: rank must be >= 1", op);
+  if (rank > kMaxRank) return fail(EP_ERR_UNSUPPORTED, "%s: rank %d > %d", op, rank, kMaxRank);
+  if (shape == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: NULL shape array", op);
+  if (!dims_product(shape, 0, rank, n)) return fail(EP_ERR_INVALID_ARG, "%s: negative or overflowing dims", op);
+  *C = shape[rank - 1];
+  return EP_OK;
+}
+
+}  // namespace
+
+ep_status ep_bias_dropout(ep_dtype t, const void* X, const int64_t* shape, int rank, const void* bias,
+                          const void* residual, double ratio, uint64_t seed, uint64_t offset,
+                          const uint64_t* offset_device, void* Y, ep_stream_t stream) {
+  int64_t n = 0, C = 0;
+  if (ep_status s = dropout_shape("bias_dropout", t, shape, rank, &n, &C); s != EP_OK) return s;
+  uint32_t last_kept = 0;
+  float scale = 1.f;
+  if (ep_status s = dropout_ratio("bias_dropout", ratio, &last_kept, &scale); s != EP_OK) return s;
+  if (n == 0) return ok();
+  if (X == nullptr || Y == nullptr) return fail(EP_ERR_INVALID_ARG, "bias_dropout: X and Y are required");
+  const int es = esize(t);
+  const void* ptrs[] = {X, bias, residual, Y};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned(p, es))
+      return fail(EP_ERR_INVALID_ARG, "bias_dropout: pointer %p is not aligned to the element size", p);
+  if (!aligned(offset_device, 8)) return fail(EP_ERR_INVALID_ARG, "bias_dropout: offset_device must be 8-byte aligned");
+  const Span x{X, n * es}, b{bias, C * es}, r{residual, n * es}, y{Y, n * es}, o{offset_device, 8};
+  if (bad_overlap_inplace_ok(y, x) || bad_overlap_inplace_ok(y, r) || overlap(y, b) || overlap(y, o))
+    return fail(EP_ERR_INVALID_ARG, "bias_dropout: Y overlaps an input other than as an exact alias of X or residual");
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  ep::BiasDropoutArgs a{to_dtype(t), X, bias, residual, Y, nullptr, n, C, seed, offset, offset_device,
+                        last_kept, scale, nullptr};
+  int launches = 0;
+  cudaError_t e = ep::launch_bias_dropout(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, "bias_dropout");
+}
+
+size_t ep_bias_dropout_grad_workspace_size(ep_dtype t, const int64_t* shape, int rank) {
+  int64_t n = 0, C = 0;
+  char saved[sizeof(g_err)];
+  std::memcpy(saved, g_err, sizeof(g_err));
+  const ep_status s = dropout_shape("bias_dropout_grad_workspace_size", t, shape, rank, &n, &C);
+  std::memcpy(g_err, saved, sizeof(g_err));
+  if (s != EP_OK || n == 0) return 0;
+  return ep::bias_dropout_grad_workspace_bytes(to_dtype(t), n, C);
+}
+
+ep_status ep_bias_dropout_grad(ep_dtype t, const void* dY, const int64_t* shape, int rank, double ratio,
+                               uint64_t seed, uint64_t offset, const uint64_t* offset_device, void* dX, void* dbias,
+                               void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+  int64_t n = 0, C = 0;
+  if (ep_status s = dropout_shape("bias_dropout_grad", t, shape, rank, &n, &C); s != EP_OK) return s;
+  uint32_t last_kept = 0;
+  float scale = 1.f;
+  if (ep_status s = dropout_ratio("bias_dropout_grad", ratio, &last_kept, &scale); s != EP_OK) return s;
+  const int es = esize(t);
+  const void* ptrs[] = {dY, dX, dbias};
+  for (const void* p : ptrs)
+    if (p != nullptr && !aligned(p, es))
+      return fail(EP_ERR_INVALID_ARG, "bias_dropout_grad: pointer %p is not aligned to the element size", p);
+  if (!aligned(offset_device, 8))
+    return fail(EP_ERR_INVALID_ARG, "bias_dropout_grad: offset_device must be 8-byte aligned");
+  if (n == 0) {
+    if (ep_status s = zero_fill("bias_dropout_grad", dbias, C * es, stream); s != EP_OK) return s;
+    return ok();
+  }
+  if (dY == nullptr || dX == nullptr) return fail(EP_ERR_INVALID_ARG, "bias_dropout_grad: dY and dX are required");
+  const Span dy{dY, n * es}, dx{dX, n * es}, db{dbias, C * es}, o{offset_device, 8};
+  if (bad_overlap_inplace_ok(dx, dy) || overlap(dx, o) || overlap(db, dy) || overlap(db, dx) || overlap(db, o))
+    return fail(EP_ERR_INVALID_ARG, "bias_dropout_grad: an output overlaps an operand other than dX exactly dY");
+  if (dbias != nullptr) {
+    const size_t need = ep::bias_dropout_grad_workspace_bytes(to_dtype(t), n, C);
+    const Span all[] = {dy, dx, db, o};
+    if (ep_status s = check_workspace("bias_dropout_grad", workspace, workspace_bytes, need, all, 4); s != EP_OK)
+      return s;
+  }
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  ep::BiasDropoutArgs a{to_dtype(t), dY, nullptr, nullptr, dX, dbias, n, C, seed, offset, offset_device,
+                        last_kept, scale, workspace};
+  int launches = 0;
+  cudaError_t e = ep::launch_bias_dropout_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, "bias_dropout_grad");
 }
 
 }  // extern "C"

@@ -1,0 +1,720 @@
+// GroupNorm over channels-last (N, S, C) tensors, with an optional SiLU, and
+// its gradient.
+//
+// Definition (com.microsoft.GroupNorm of the contrib family, channels_last = 1):
+// G groups of D = C / G neighbouring channels, M = S * D values each;
+//   mu = mean(x), var = mean((x - mu)^2), r = 1 / sqrt(var + epsilon)   per (n, g)
+//   h = (x - mu) r,  u = h * gamma[c] + beta[c],  y = u or u * sigmoid(u)
+// and the gradient, from dy and the saved mu and r:
+//   du = dy or dy * s (1 + u (1 - s)), s = sigmoid(u)
+//   dbeta[c] = sum du,  dgamma[c] = sum du * h                          over n and positions
+//   m1 = mean(du * gamma), m2 = mean(du * gamma * h)                    per (n, g)
+//   dx = r (du * gamma - m1 - h m2)
+//
+// Split form (this file's general path, any C, S and alignment): the walk of
+// column_walk.cuh over each sample.  Pass 1 leaves (count, mean, sum of squared
+// distances) per chunk and group, a small kernel joins the chunks, pass 2 reads
+// x again (from L2 where it fits) and writes y.  Values are taken relative to
+// the group's first one, and each channel's mean and M2 are carried as Welford's
+// and joined with Chan's formula, so that neither a large mean nor a first
+// value that is far off costs the variance its digits.  The gradient has the same three steps, with per-channel sums of du
+// and du * h beside the groups' sums.
+//
+// All sums and statistics are float32; results are rounded once, to T.
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+#include "column_walk.cuh"
+#include "device_common.cuh"
+#include "ep_internal.h"
+#include "launch_util.h"
+
+namespace ep {
+namespace {
+
+// u * sigmoid(u).  float32: the library exponential and a rounded division.
+// 16-bit results: 2^x and 1/x by the hardware approximations, whose errors (a
+// few float32 ulp) are far below the result's rounding; below u = -88.7 the
+// exponential overflows and the result, above -1e-36, is -0.
+template <typename T>
+__device__ __forceinline__ float silu(float u) {
+  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(u, 1.0f + expf(-u));
+  else return u * dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
+}
+
+template <typename T>
+__device__ __forceinline__ float sigmoid(float u) {
+  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(1.0f, 1.0f + expf(-u));
+  else return dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
+}
+
+// du of the definition.
+template <typename T, bool SILU>
+__device__ __forceinline__ float act_grad(float dy, float u) {
+  if constexpr (!SILU) return dy;
+  const float s = sigmoid<T>(u);
+  return dy * (s * fmaf(u, 1.0f - s, 1.0f));
+}
+
+// One call's sizes, as every kernel of the split form gets them.
+// (C is at most kMaxGroupNormChannels, so positions in a walk row fit an int.)
+struct GnDims {
+  int64_t N, S, L;  // L = S * C
+  int C, G, D;
+  float eps;
+  WalkPlan p;
+};
+
+// Where a sample's walk row starts: `off` elements before the sample.
+template <typename T, bool VEC>
+__device__ __forceinline__ int walk_offset(const T* sample) {
+  return VEC ? dev::misalignment(sample) : 0;
+}
+
+// The channel of the first element of fragment column j.
+__device__ __forceinline__ int first_channel(int64_t j, int vw, int off, int C) {
+  return static_cast<int>((j * vw + C - off % C) % C);
+}
+
+// The first repeat k of a group whose channels [c0, c0 + D), at the positions
+// off + c + k C of a walk row, reach past position p0 (k < 0: the channels that
+// the walk row's `off` leading positions hold).
+__device__ __forceinline__ int first_repeat(int p0, int off, int c0, int D, int C) {
+  const int a = p0 - off - c0 - D;
+  return (a >= 0 ? a / C : -((-a + C - 1) / C)) + 1;
+}
+
+// Calls f(i, c) for every position p0 + i of a tile of np positions that holds a
+// channel c of the group, by the lanes of a warp in turn: the lanes split into
+// sets of the smallest power of two that holds D channels (at most 32), each set
+// taking the repeats in turn, so that few channels still use (and sum over) all lanes.
+template <typename F>
+__device__ __forceinline__ void for_group(int p0, int np, int off, int c0, int D, int C, F f) {
+  const int lane = threadIdx.x & 31;
+  const int set = D >= 32 ? 32 : D <= 1 ? 1 : 1 << (32 - __clz(D - 1));
+  const int64_t step = int64_t(C) * (32 / set);
+  for (int64_t a = off + c0 + int64_t(first_repeat(p0, off, c0, D, C) + lane / set) * C - p0; a < np; a += step) {
+    const int lo = static_cast<int>(max(int64_t(0), a)), hi = static_cast<int>(min(int64_t(np), a + D));
+    for (int i = lo + (lane & (set - 1)); i < hi; i += set) f(i, c0 + (i - static_cast<int>(a)));
+  }
+}
+
+__device__ __forceinline__ bool group_in_tile(int p0, int np, int off, int c0, int D, int C) {
+  return off + c0 + int64_t(first_repeat(p0, off, c0, D, C)) * C < p0 + np;
+}
+
+// Pass 1.  partial: [item][tile][G] x (count, mean, M2), or, where a sample has
+// one item and one tile, the statistics themselves (partial == nullptr).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  __shared__ float s_cnt[kWalkThreads * VW], s_mean[kWalkThreads * VW], s_m2[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const int tile = blockIdx.x % p.tiles;
+  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
+  const bool mine = int(threadIdx.x) < p.tile_frags && j < p.row_frags;
+  const int p0 = tile * p.tile_frags * VW;
+  const int np = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags)) * VW;
+  const int64_t items = d.N * p.chunks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+
+  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
+    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+    const T* xs = x + n * d.L;
+    const int off = walk_offset<T, VEC>(xs);
+    if (mine) {
+      float mean[VW], m2[VW], cnt = 0.f, extra[VW], shift[VW];
+      int c = first_channel(j, VW, off, d.C);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        mean[e] = m2[e] = extra[e] = 0.f;
+        shift[e] = dev::ld1_keep(xs + c / d.D * d.D);
+        if (++c == d.C) c = 0;
+      }
+      const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
+      for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
+        float v[U][VW];
+        bool whole = r0 + U <= r1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
+          whole = whole && e0 >= 0 && e0 + VW <= d.L;
+          if (r0 + u < r1) {
+            dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+#pragma unroll
+            for (int e = 0; e < VW; ++e) v[u][e] -= shift[e];
+          }
+        }
+        if (whole) {  // U values of every channel: their mean and M2, joined to the running ones
+          const float tot = cnt + float(U), w = float(U) / tot, cw = cnt * w;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            const float mb = ((v[0][e] + v[1][e]) + (v[2][e] + v[3][e])) * (1.0f / U);
+            float q = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const float t = v[u][e] - mb;
+              q = fmaf(t, t, q);
+            }
+            const float t = mb - mean[e];
+            if (extra[e] == 0.f) {
+              mean[e] = fmaf(t, w, mean[e]);
+              m2[e] += fmaf(t * t, cw, q);
+            } else {
+              const float ce = cnt + extra[e], we = float(U) / (ce + float(U));
+              mean[e] = fmaf(t, we, mean[e]);
+              m2[e] += fmaf(t * t, ce * we, q);
+            }
+          }
+          cnt = tot;
+        } else {  // the ends of a sample: one value at a time
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+              if (r0 + u < r1 && e0 + e >= 0 && e0 + e < d.L) {
+                extra[e] += 1.f;
+                const float t = v[u][e] - mean[e];
+                mean[e] += t / (cnt + extra[e]);
+                m2[e] = fmaf(t, v[u][e] - mean[e], m2[e]);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        s_cnt[threadIdx.x * VW + e] = cnt + extra[e];
+        s_mean[threadIdx.x * VW + e] = mean[e];
+        s_m2[threadIdx.x * VW + e] = m2[e];
+      }
+    }
+    __syncthreads();
+    for (int g = warp; g < d.G; g += warps) {
+      if (p.tiles > 1 && !group_in_tile(p0, np, off, g * d.D, d.D, d.C)) {
+        if (lane == 0) {
+          float* out = partial + ((item * p.tiles + tile) * d.G + g) * 3;
+          out[0] = out[1] = out[2] = 0.f;
+        }
+        continue;
+      }
+      float c = 0.f, s = 0.f, q = 0.f;
+      for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int) {
+        c += s_cnt[i];
+        s = fmaf(s_cnt[i], s_mean[i], s);
+      });
+      c = dev::warp_sum(c);
+      s = dev::warp_sum(s);
+      const float mg = c > 0.f ? s / c : 0.f;
+      float res = 0.f;  // what rounding s / c and the sum left out of the mean
+      for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int) {
+        const float t = s_mean[i] - mg;
+        res = fmaf(s_cnt[i], t, res);
+        q += fmaf(s_cnt[i] * t, t, s_m2[i]);
+      });
+      res = dev::warp_sum(res);
+      q = dev::warp_sum(q);
+      if (lane == 0) {
+        const float fix = c > 0.f ? res / c : 0.f;
+        const float mf = mg + fix, m2g = fmaxf(0.f, q - res * fix);
+        if (partial == nullptr) {
+          mean_out[n * d.G + g] = dev::ld1_keep(xs + g * d.D) + mf;
+          inv_out[n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
+        } else {
+          float* out = partial + ((item * p.tiles + tile) * d.G + g) * 3;
+          out[0] = c;
+          out[1] = mf;
+          out[2] = m2g;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins a group's chunks and tiles: one warp for each (n, g).
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_gn_join(const T* x, const float* partial, GnDims d, float* mean_out, float* inv_out) {
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
+  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
+    const float* src = partial + ((i / d.G) * parts * d.G + i % d.G) * 3;
+    float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
+    for (int64_t k = lane; k < parts; k += 32) {
+      const float* e = src + k * d.G * 3;
+      c += __ldcg(e);
+      s = fmaf(__ldcg(e), __ldcg(e + 1), s);
+    }
+    c = dev::warp_sum(c);
+    s = dev::warp_sum(s);
+    const float mg = s / c;
+    for (int64_t k = lane; k < parts; k += 32) {
+      const float* e = src + k * d.G * 3;
+      const float t = __ldcg(e + 1) - mg, n = __ldcg(e);
+      res = fmaf(n, t, res);
+      q += fmaf(n * t, t, __ldcg(e + 2));
+    }
+    res = dev::warp_sum(res);
+    q = dev::warp_sum(q);
+    if (lane == 0) {
+      const float fix = res / c;
+      mean_out[i] = dev::ld1_keep(x + i / d.G * d.L + i % d.G * d.D) + (mg + fix);
+      inv_out[i] = 1.0f / sqrtf(fmaxf(0.f, q - res * fix) / c + d.eps);
+    }
+  }
+}
+
+// Pass 2: y from x and the statistics.
+template <typename T, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean, const float* inv,
+           T* y, GnDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const int tile = blockIdx.x % p.tiles;
+  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
+  if (int(threadIdx.x) >= p.tile_frags || j >= p.row_frags) return;
+  const int64_t items = d.N * p.chunks;
+  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
+    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+    const T* xs = x + n * d.L;
+    T* ys = y + n * d.L;
+    const int off = walk_offset<T, VEC>(xs);
+    float mu[VW], a[VW], b[VW];
+    int c = first_channel(j, VW, off, d.C);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const int64_t g = n * d.G + c / d.D;
+      mu[e] = mean[g];
+      a[e] = inv[g] * dev::ld1_keep(gamma + c);
+      b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+      if (++c == d.C) c = 0;
+    }
+    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
+    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
+      float v[U][VW];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r0 + u < r1) dev::load_frag<T, VEC>(xs, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u < r1) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            const float w = fmaf(v[u][e] - mu[e], a[e], b[e]);
+            v[u][e] = SILU ? silu<T>(w) : w;
+          }
+          dev::store_frag<T, VEC>(ys, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
+        }
+      }
+    }
+  }
+}
+
+// Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
+// groups' sums of each item.  A CTA's items share `off` (the launch sees to
+// it), so a thread's channels stay the same and its sums run on over them.
+//   gpart: [item][tile][G] x (sum du gamma, sum du gamma h)
+//   cpart: 2 x [CTA row][C] (one tile) or 2 x [CTA row][walk row], position 0
+//          being channel 0
+template <typename T, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+               const float* inv, GnDims d, float* gpart, float* cpart) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 2;
+  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const int tile = blockIdx.x % p.tiles;
+  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
+  const bool mine = int(threadIdx.x) < p.tile_frags && j < p.row_frags;
+  const int p0 = tile * p.tile_frags * VW;
+  const int np = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags)) * VW;
+  const int64_t items = d.N * p.chunks, cta_rows = gridDim.x / p.tiles, cta_row = blockIdx.x / p.tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  float tot_a[VW], tot_b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
+  int off = 0;
+
+  for (int64_t item = cta_row; item < items; item += cta_rows) {
+    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+    const T* xs = x + n * d.L;
+    const T* ds = dy + n * d.L;
+    off = walk_offset<T, VEC>(xs);
+    if (mine) {
+      float mu[VW], rs[VW], ga[VW], be[VW], sa[VW], sb[VW];
+      int c = first_channel(j, VW, off, d.C);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const int64_t g = n * d.G + c / d.D;
+        mu[e] = mean[g];
+        rs[e] = inv[g];
+        ga[e] = SILU ? dev::ld1_keep(gamma + c) : 1.f;
+        be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+        sa[e] = sb[e] = 0.f;
+        if (++c == d.C) c = 0;
+      }
+      const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
+      for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
+        float v[U][VW], w[U][VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
+          if (r0 + u < r1) {
+            dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+            dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);  // 0 outside the sample: adds nothing
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (r0 + u < r1) {
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+              const float h = (v[u][e] - mu[e]) * rs[e];
+              const float du = act_grad<T, SILU>(w[u][e], fmaf(h, ga[e], be[e]));
+              sa[e] += du;
+              sb[e] = fmaf(du, h, sb[e]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        s_a[threadIdx.x * VW + e] = sa[e];
+        s_b[threadIdx.x * VW + e] = sb[e];
+        tot_a[e] += sa[e];
+        tot_b[e] += sb[e];
+      }
+    }
+    __syncthreads();
+    for (int g = warp; g < d.G; g += warps) {
+      float a = 0.f, b = 0.f;
+      if (p.tiles == 1 || group_in_tile(p0, np, off, g * d.D, d.D, d.C)) {
+        for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int c) {
+          const float gm = dev::ld1_keep(gamma + c);
+          a = fmaf(gm, s_a[i], a);
+          b = fmaf(gm, s_b[i], b);
+        });
+        a = dev::warp_sum(a);
+        b = dev::warp_sum(b);
+      }
+      if (lane == 0) {
+        float* out = gpart + ((item * p.tiles + tile) * d.G + g) * 2;
+        out[0] = a;
+        out[1] = b;
+      }
+    }
+    __syncthreads();
+  }
+  if (cpart == nullptr) return;
+  if (p.tiles > 1) {
+    if (mine) {
+      const int64_t P = p.row_frags * VW;
+      float* oa = cpart + cta_row * P;
+      float* ob = oa + cta_rows * P;
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const int64_t q = (j * VW + e + P - off) % P;
+        oa[q] = tot_a[e];
+        ob[q] = tot_b[e];
+      }
+    }
+    return;
+  }
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      s_a[threadIdx.x * VW + e] = tot_a[e];
+      s_b[threadIdx.x * VW + e] = tot_b[e];
+    }
+  }
+  __syncthreads();
+  const int c32 = d.C, reps = static_cast<int>(p.reps), P = np;
+  float* oa = cpart + cta_row * d.C;
+  float* ob = oa + cta_rows * d.C;
+  if (reps <= 16) {
+    for (int c = threadIdx.x; c < c32; c += blockDim.x) {
+      float a = 0.f, b = 0.f;
+      for (int k = 0; k < reps; ++k) {
+        int q = c + off + k * c32;
+        if (q >= P) q -= P;
+        a += s_a[q];
+        b += s_b[q];
+      }
+      oa[c] = a;
+      ob[c] = b;
+    }
+  } else {
+    for (int c = warp; c < c32; c += warps) {
+      float a = 0.f, b = 0.f;
+      for (int k = lane; k < reps; k += 32) {
+        int q = c + off + k * c32;
+        if (q >= P) q -= P;
+        a += s_a[q];
+        b += s_b[q];
+      }
+      a = dev::warp_sum(a);
+      b = dev::warp_sum(b);
+      if (lane == 0) {
+        oa[c] = a;
+        ob[c] = b;
+      }
+    }
+  }
+}
+
+// Joins the groups' sums over chunks and tiles: m1, m2 of each (n, g).
+__global__ void __launch_bounds__(256)
+k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
+  const float scale = 1.0f / (float(d.S) * float(d.D));
+  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
+    const float* src = gpart + ((i / d.G) * parts * d.G + i % d.G) * 2;
+    float a = 0.f, b = 0.f;
+    for (int64_t k = lane; k < parts; k += 32) {
+      a += __ldcg(src + k * d.G * 2);
+      b += __ldcg(src + k * d.G * 2 + 1);
+    }
+    a = dev::warp_sum(a);
+    b = dev::warp_sum(b);
+    if (lane == 0) {
+      m1[i] = a * scale;
+      m2[i] = b * scale;
+    }
+  }
+}
+
+// Gradient, pass 2: dx.
+template <typename T, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+                const float* inv, const float* m1, const float* m2, T* dx, GnDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 2;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const int tile = blockIdx.x % p.tiles;
+  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
+  if (int(threadIdx.x) >= p.tile_frags || j >= p.row_frags) return;
+  const int64_t items = d.N * p.chunks;
+  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
+    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+    const T* xs = x + n * d.L;
+    const T* ds = dy + n * d.L;
+    T* os = dx + n * d.L;
+    const int off = walk_offset<T, VEC>(xs);
+    float mu[VW], rs[VW], ga[VW], be[VW], a1[VW], a2[VW];
+    int c = first_channel(j, VW, off, d.C);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const int64_t g = n * d.G + c / d.D;
+      mu[e] = mean[g];
+      rs[e] = inv[g];
+      ga[e] = dev::ld1_keep(gamma + c);
+      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+      a1[e] = __ldcg(m1 + g);
+      a2[e] = __ldcg(m2 + g);
+      if (++c == d.C) c = 0;
+    }
+    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
+    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
+      float v[U][VW], w[U][VW];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
+        if (r0 + u < r1) {
+          dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+          dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u < r1) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            const float h = (v[u][e] - mu[e]) * rs[e];
+            const float du = act_grad<T, SILU>(w[u][e], fmaf(h, ga[e], be[e]));
+            v[u][e] = rs[e] * (fmaf(du, ga[e], -a1[e]) - h * a2[e]);
+          }
+          dev::store_frag<T, VEC>(os, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
+        }
+      }
+    }
+  }
+}
+
+int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
+
+GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
+  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, {}};
+  d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 4, 4);
+  return d;
+}
+
+// CTA rows (of `tiles` CTAs) of a launch over N * chunks items.
+int64_t cta_rows_of(const GnDims& d, int64_t most_ctas) {
+  return std::max<int64_t>(1, std::min(d.N * d.p.chunks, most_ctas / d.p.tiles));
+}
+
+bool split_parts(const GnDims& d) { return d.p.chunks > 1 || d.p.tiles > 1; }
+int64_t grad_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 4); }
+
+// Offset in bytes of the next array in a workspace: each starts on 16 bytes.
+size_t pad16(size_t b) { return (b + 15) / 16 * 16; }
+
+struct GnWorkspace {
+  size_t partial, mean, inv, total;
+};
+GnWorkspace gn_workspace(const GnDims& d) {
+  GnWorkspace w;
+  const size_t stats = pad16(size_t(d.N) * d.G * 4);
+  w.partial = 0;
+  w.mean = split_parts(d) ? pad16(size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 12) : 0;
+  w.inv = w.mean + stats;
+  w.total = w.inv + stats;
+  return w;
+}
+
+struct GnGradWorkspace {
+  size_t gpart, m1, m2, cpart, total;
+};
+GnGradWorkspace gn_grad_workspace(const GnDims& d, DType t) {
+  GnGradWorkspace w;
+  const size_t stats = pad16(size_t(d.N) * d.G * 4);
+  const int64_t width = d.p.tiles > 1 ? d.p.row_frags * vec_width(t) : d.C;
+  w.gpart = 0;
+  w.m1 = pad16(size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 8);
+  w.m2 = w.m1 + stats;
+  w.cpart = w.m2 + stats;
+  w.total = w.cpart + size_t(grad_rows(d)) * width * 8;
+  return w;
+}
+
+inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uintptr_t>(p) & 15u); }
+
+inline unsigned join_grid(const GnDims& d) {
+  return unsigned(std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms * 8));
+}
+
+template <typename T>
+cudaError_t group_norm_t(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps);
+  const GnWorkspace w = gn_workspace(d);
+  char* ws = static_cast<char*>(a.workspace);
+  float* mean = a.mean != nullptr ? a.mean : reinterpret_cast<float*>(ws + w.mean);
+  float* inv = a.inv != nullptr ? a.inv : reinterpret_cast<float*>(ws + w.inv);
+  float* partial = split_parts(d) ? reinterpret_cast<float*>(ws + w.partial) : nullptr;
+  const T* x = static_cast<const T*>(a.x);
+  const T* gamma = static_cast<const T*>(a.gamma);
+  const T* beta = static_cast<const T*>(a.beta);
+  T* y = static_cast<T*>(a.y);
+  const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles)), block(d.p.threads);
+  const bool vec = misalign16(x) == misalign16(y);
+  // statistics need no alignment of y
+  cudaError_t e = launch(k_gn_stats<T, true>, grid, block, 0, stream, x, d, partial, mean, inv);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (partial != nullptr) {
+    e = launch(k_gn_join<T>, dim3(join_grid(d)), dim3(256), 0, stream, x, partial, d, mean, inv);
+    if (e != cudaSuccess) return e;
+    *launches += 1;
+  }
+  auto fn = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
+                : (a.silu ? k_gn_apply<T, false, true> : k_gn_apply<T, false, false>);
+  e = launch(fn, grid, block, 0, stream, x, gamma, beta, mean, inv, y, d);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+template <typename T>
+cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  constexpr int VW = dev::Vec16<T>::N;
+  const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f);
+  const GnGradWorkspace w = gn_grad_workspace(d, a.t);
+  char* ws = static_cast<char*>(a.workspace);
+  float* gpart = reinterpret_cast<float*>(ws + w.gpart);
+  float* m1 = reinterpret_cast<float*>(ws + w.m1);
+  float* m2 = reinterpret_cast<float*>(ws + w.m2);
+  float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? reinterpret_cast<float*>(ws + w.cpart) : nullptr;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* gamma = static_cast<const T*>(a.gamma);
+  const T* beta = static_cast<const T*>(a.beta);
+  T* dx = static_cast<T*>(a.dx);
+  const int64_t rows = grad_rows(d);
+  // whole fragments need x and dy (and dx) at one offset within 16 bytes, and
+  // one walk offset for all the samples that a CTA takes
+  const bool one_off = d.L % VW == 0 || rows >= d.N * d.p.chunks;
+  const bool vec1 = misalign16(x) == misalign16(dy) && one_off;
+  const bool vec2 = misalign16(x) == misalign16(dy) && misalign16(x) == misalign16(dx);
+  auto f1 = vec1 ? (a.silu ? k_gn_grad_sums<T, true, true> : k_gn_grad_sums<T, true, false>)
+                 : (a.silu ? k_gn_grad_sums<T, false, true> : k_gn_grad_sums<T, false, false>);
+  cudaError_t e = launch(f1, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean,
+                         a.inv, d, gpart, cpart);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  e = launch(k_gn_grad_join, dim3(join_grid(d)), dim3(256), 0, stream, gpart, d, m1, m2);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  auto f2 = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
+                 : (a.silu ? k_gn_grad_apply<T, false, true> : k_gn_grad_apply<T, false, false>);
+  const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles));
+  e = launch(f2, grid, dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (cpart != nullptr) {
+    const int64_t jobs = std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, INT_MAX);
+    // the sums of du are dbeta, those of du * h are dgamma
+    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart, rows,
+               d.p.tiles > 1 ? d.p.reps : int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
+    if (e == cudaSuccess) *launches += 1;
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+  return gn_workspace(dims_of(t, N, S, C, G, 0.f)).total;
+}
+
+size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+  return gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total;
+}
+
+cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  switch (a.t) {
+    case DType::F32: return group_norm_t<float>(a, sm_count, stream, launches);
+    case DType::F16: return group_norm_t<__half>(a, sm_count, stream, launches);
+    default: return group_norm_t<__nv_bfloat16>(a, sm_count, stream, launches);
+  }
+}
+
+cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  switch (a.t) {
+    case DType::F32: return group_norm_grad_t<float>(a, sm_count, stream, launches);
+    case DType::F16: return group_norm_grad_t<__half>(a, sm_count, stream, launches);
+    default: return group_norm_grad_t<__nv_bfloat16>(a, sm_count, stream, launches);
+  }
+}
+
+}  // namespace ep
