@@ -8,8 +8,8 @@ no CPU or PyTorch fallback.  A non-OK status raises ``EpError``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -314,46 +314,63 @@ def ep_quick_gelu(X, alpha=DEFAULT_ALPHA, Y=None, stream=None):
 
 # ---------------------------------------------------------------------------
 # GroupNorm and BiasDropout, with their gradients.  Operands are checked against
-# the first one (device, dtype, shape) before their addresses are passed on, and
-# a workspace that is allocated here belongs to the stream the call runs on.
+# the first one (device, dtype, shape) before their addresses are passed on.  The
+# calls run on the current stream, or with `stream` current, so that what is
+# allocated here (outputs, a workspace) belongs to the stream it is used on.
+# Small calls cost what the host costs: shape arrays and workspace sizes are
+# kept by value (shape, dtype), and the checks take a few attribute reads.
 # ---------------------------------------------------------------------------
 
-def _operand(name, t, like, shape=None, dtype=None):
-    """t, checked to be a contiguous CUDA tensor on like's device with the given
-    dtype (like's if None) and shape (any if None)."""
+# the current stream's handle without a Stream object (2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
+def _first(name, t):
+    """The operand that the others are checked against: its device index and dtype code."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != like.device:
+    return t.get_device(), _dtype(t)
+
+
+def _operand(name, t, like, shape=None, dtype=None):
+    """t, checked to be a contiguous CUDA tensor on like's device with the given
+    dtype (like's if None) and shape (any if None)."""
+    dtype = like.dtype if dtype is None else dtype
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise TypeError(f"{name} must have dtype {like.dtype if dtype is None else dtype}, not {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, not {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _on_stream(stream, device):
-    """A context in which `stream` (the device's current one if None) and its
-    device are current, so that what is allocated inside belongs to it."""
+def _elsewhere(stream, index):
+    """None if the call can run as it is, on the current stream of the current
+    device; else a context in which it can."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{index}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return None if _current_device() == index else torch.cuda.device(index)
 
 
 def _scratch(workspace, need, like):
-    """(pointer, bytes) of the caller's workspace, or of one allocated for this
-    call (and the tensor, to be kept until the call has been enqueued)."""
+    """(pointer, bytes, tensor) of the caller's workspace, or of one allocated for this call."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    elif not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the operands' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -369,22 +386,72 @@ def _u64(name, v):
     return v
 
 
-def _nsc(X):
-    """(N, S, C) of a channels-last tensor: the dimensions between the first and
+@functools.lru_cache(maxsize=4096)
+def _dims(shape):
+    """A shape as the C array that the library reads."""
+    return _shape(shape)
+
+
+@functools.lru_cache(maxsize=4096)
+def _nsc(shape):
+    """(N, S, C) of a channels-last shape: the dimensions between the first and
     the last are positions."""
-    if X.dim() < 3:
+    if len(shape) < 3:
         raise ValueError("X must have the shape (N, positions..., C)")
-    n, c = X.shape[0], X.shape[-1]
     s = 1
-    for d in X.shape[1:-1]:
+    for d in shape[1:-1]:
         s *= d
-    return (ctypes.c_int64 * 3)(n, s, c)
+    return _shape((shape[0], s, shape[-1]))
+
+
+@functools.lru_cache(maxsize=4096)
+def _group_norm_need(code, shape, groups, grad):
+    lib = load_library()
+    fn = lib.ep_group_norm_grad_workspace_size if grad else lib.ep_group_norm_workspace_size
+    return int(fn(code, _nsc(shape), groups))
+
+
+@functools.lru_cache(maxsize=4096)
+def _bias_dropout_grad_need(code, shape):
+    return int(load_library().ep_bias_dropout_grad_workspace_size(code, _dims(shape), len(shape)))
+
+
+def _code(dtype):
+    return _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
 
 
 def ep_group_norm_workspace_size(dtype, shape, groups) -> int:
-    """Workspace bytes of ep_group_norm for a channels-last (N, S, C) shape."""
-    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(load_library().ep_group_norm_workspace_size(code, _shape(shape), int(groups)))
+    """Workspace bytes of ep_group_norm for a channels-last shape."""
+    return _group_norm_need(_code(dtype), tuple(shape), int(groups), False)
+
+
+def ep_group_norm_grad_workspace_size(dtype, shape, groups) -> int:
+    """Workspace bytes of ep_group_norm_grad for a channels-last shape."""
+    return _group_norm_need(_code(dtype), tuple(shape), int(groups), True)
+
+
+def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
+    """Workspace bytes of ep_bias_dropout_grad with dbias."""
+    return _bias_dropout_grad_need(_code(dtype), tuple(shape))
+
+
+def _group_stats(name, t, X, n, groups):
+    if t is None or t is False:
+        return None
+    if t is True:
+        return X.new_empty((n, max(0, groups)), dtype=torch.float32)
+    _operand(name, t, X, dtype=torch.float32)
+    if t.numel() != n * groups:
+        raise ValueError(f"{name} must have {n * groups} elements")
+    return t
+
+
+def _param_grad(name, t, X, channels):
+    if t is None or t is False:
+        return None
+    if t is True:
+        return X.new_empty(channels)
+    return _operand(name, t, X, channels)
 
 
 def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_EPSILON, activation=EP_ACT_NONE,
@@ -396,43 +463,24 @@ def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_E
     Returns (Y, mean, inv_std_dev), the last two None when not requested."""
     if groups is None:
         raise ValueError("groups is required")
+    index, code = _first("X", X)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_group_norm(X, gamma, beta, groups, epsilon, activation, Y, mean, inv_std_dev, workspace)
     lib = load_library()
-    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
-    code, shape = _dtype(X), _nsc(X)
-    n, channels = X.shape[0], X.shape[-1:]
-    groups = int(groups)
+    shape, groups = X.shape, int(groups)
+    nsc, channels = _nsc(shape), shape[-1:]
     _operand("gamma", gamma, X, channels)
     if beta is not None:
         _operand("beta", beta, X, channels)
-    with _on_stream(stream, X.device):
-        if Y is None:
-            Y = torch.empty_like(X)
-        else:
-            _operand("Y", Y, X, X.shape)
-        mean = _group_stats("mean", mean, X, n, groups)
-        inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, n, groups)
-        ws, wbytes, _keep = _scratch(workspace, lib.ep_group_norm_workspace_size(code, shape, groups), X)
-        _check(lib.ep_group_norm(code, X.data_ptr(), shape, gamma.data_ptr(), _addr(beta), groups, float(epsilon),
-                                 int(activation), Y.data_ptr(), _addr(mean), _addr(inv_std_dev), ws, wbytes,
-                                 torch.cuda.current_stream(X.device).cuda_stream))
+    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, shape)
+    mean = _group_stats("mean", mean, X, shape[0], groups)
+    inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, shape[0], groups)
+    ws, wbytes, _keep = _scratch(workspace, _group_norm_need(code, shape, groups, False), X)
+    _check(lib.ep_group_norm(code, X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation),
+                             Y.data_ptr(), _addr(mean), _addr(inv_std_dev), ws, wbytes, _raw_stream(index)))
     return Y, mean, inv_std_dev
-
-
-def _group_stats(name, t, X, n, groups):
-    if t is None or t is False:
-        return None
-    if t is True:
-        return torch.empty((n, max(0, groups)), dtype=torch.float32, device=X.device)
-    _operand(name, t, X, dtype=torch.float32)
-    if t.numel() != n * groups:
-        raise ValueError(f"{name} must have {n * groups} elements")
-    return t
-
-
-def ep_group_norm_grad_workspace_size(dtype, shape, groups) -> int:
-    """Workspace bytes of ep_group_norm_grad for a channels-last (N, S, C) shape."""
-    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(load_library().ep_group_norm_grad_workspace_size(code, _shape(shape), int(groups)))
 
 
 def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activation=EP_ACT_NONE, dX=None,
@@ -443,40 +491,31 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
     when not requested."""
     if groups is None:
         raise ValueError("groups is required")
+    index, code = _first("X", X)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups, activation, dX, dgamma, dbeta,
+                                      workspace)
     lib = load_library()
-    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
-    code, shape = _dtype(X), _nsc(X)
-    n, channels = X.shape[0], X.shape[-1:]
-    groups = int(groups)
-    _operand("dY", dY, X, X.shape)
+    shape, groups = X.shape, int(groups)
+    nsc, channels = _nsc(shape), shape[-1:]
+    _operand("dY", dY, X, shape)
     _operand("gamma", gamma, X, channels)
     if beta is not None:
         _operand("beta", beta, X, channels)
     for name, t in (("mean", mean), ("inv_std_dev", inv_std_dev)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} is required")
-        _group_stats(name, t, X, n, groups)
-    with _on_stream(stream, X.device):
-        if dX is None:
-            dX = torch.empty_like(X)
-        else:
-            _operand("dX", dX, X, X.shape)
-        dgamma = _param_grad("dgamma", dgamma, X, channels)
-        dbeta = _param_grad("dbeta", dbeta, X, channels)
-        ws, wbytes, _keep = _scratch(workspace, lib.ep_group_norm_grad_workspace_size(code, shape, groups), X)
-        _check(lib.ep_group_norm_grad(code, dY.data_ptr(), X.data_ptr(), shape, gamma.data_ptr(), _addr(beta), groups,
-                                      int(activation), mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(),
-                                      _addr(dgamma), _addr(dbeta), ws, wbytes,
-                                      torch.cuda.current_stream(X.device).cuda_stream))
+        _group_stats(name, t, X, shape[0], groups)
+    dX = torch.empty_like(X) if dX is None else _operand("dX", dX, X, shape)
+    dgamma = _param_grad("dgamma", dgamma, X, channels)
+    dbeta = _param_grad("dbeta", dbeta, X, channels)
+    ws, wbytes, _keep = _scratch(workspace, _group_norm_need(code, shape, groups, True), X)
+    _check(lib.ep_group_norm_grad(code, dY.data_ptr(), X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups,
+                                  int(activation), mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(), _addr(dgamma),
+                                  _addr(dbeta), ws, wbytes, _raw_stream(index)))
     return dX, dgamma, dbeta
-
-
-def _param_grad(name, t, X, channels):
-    if t is None or t is False:
-        return None
-    if t is True:
-        return torch.empty(channels, dtype=X.dtype, device=X.device)
-    return _operand(name, t, X, channels)
 
 
 def _offset_device(t, like):
@@ -494,53 +533,41 @@ def ep_bias_dropout(X, ratio, seed, offset=0, bias=None, residual=None, offset_d
     from (seed, offset) and the element's index.  ``offset_device``: a one-element
     int64 CUDA tensor added to ``offset`` when the kernel runs (for captured
     graphs).  Returns Y."""
+    index, code = _first("X", X)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_bias_dropout(X, ratio, seed, offset, bias, residual, offset_device, Y)
     lib = load_library()
-    _operand("X", X, X, dtype=X.dtype if isinstance(X, torch.Tensor) else None)
-    code = _dtype(X)
-    if X.dim() < 1:
-        raise ValueError("X must have a last dimension")
+    shape = X.shape
     if bias is not None:
-        _operand("bias", bias, X, X.shape[-1:])
+        _operand("bias", bias, X, shape[-1:])
     if residual is not None:
-        _operand("residual", residual, X, X.shape)
+        _operand("residual", residual, X, shape)
     od = _offset_device(offset_device, X)
-    with _on_stream(stream, X.device):
-        if Y is None:
-            Y = torch.empty_like(X)
-        else:
-            _operand("Y", Y, X, X.shape)
-        _check(lib.ep_bias_dropout(code, X.data_ptr(), _shape(X.shape), X.dim(), _addr(bias), _addr(residual),
-                                   float(ratio), _u64("seed", seed), _u64("offset", offset), od, Y.data_ptr(),
-                                   torch.cuda.current_stream(X.device).cuda_stream))
+    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, shape)
+    _check(lib.ep_bias_dropout(code, X.data_ptr(), _dims(shape), len(shape), _addr(bias), _addr(residual), float(ratio),
+                               _u64("seed", seed), _u64("offset", offset), od, Y.data_ptr(), _raw_stream(index)))
     return Y
-
-
-def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
-    """Workspace bytes of ep_bias_dropout_grad with dbias."""
-    code = _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(load_library().ep_bias_dropout_grad_workspace_size(code, _shape(shape), len(shape)))
 
 
 def ep_bias_dropout_grad(dY, ratio, seed, offset=0, offset_device=None, dX=None, dbias=None, workspace=None,
                          stream=None):
     """Gradient of ep_bias_dropout (the residual's is dY itself).  ``dbias``: a
     tensor to fill, True to allocate, or None.  Returns (dX, dbias or None)."""
+    index, code = _first("dY", dY)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_bias_dropout_grad(dY, ratio, seed, offset, offset_device, dX, dbias, workspace)
     lib = load_library()
-    _operand("dY", dY, dY, dtype=dY.dtype if isinstance(dY, torch.Tensor) else None)
-    code = _dtype(dY)
-    if dY.dim() < 1:
-        raise ValueError("dY must have a last dimension")
-    shape, rank = _shape(dY.shape), dY.dim()
+    shape = dY.shape
     od = _offset_device(offset_device, dY)
-    with _on_stream(stream, dY.device):
-        if dX is None:
-            dX = torch.empty_like(dY)
-        else:
-            _operand("dX", dX, dY, dY.shape)
-        dbias = _param_grad("dbias", dbias, dY, dY.shape[-1:])
-        need = 0 if dbias is None else lib.ep_bias_dropout_grad_workspace_size(code, shape, rank)
-        ws, wbytes, _keep = _scratch(workspace, need, dY)
-        _check(lib.ep_bias_dropout_grad(code, dY.data_ptr(), shape, rank, float(ratio), _u64("seed", seed),
-                                        _u64("offset", offset), od, dX.data_ptr(), _addr(dbias), ws, wbytes,
-                                        torch.cuda.current_stream(dY.device).cuda_stream))
+    dX = torch.empty_like(dY) if dX is None else _operand("dX", dX, dY, shape)
+    dbias = _param_grad("dbias", dbias, dY, shape[-1:])
+    need = 0 if dbias is None else _bias_dropout_grad_need(code, shape)
+    ws, wbytes, _keep = _scratch(workspace, need, dY)
+    _check(lib.ep_bias_dropout_grad(code, dY.data_ptr(), _dims(shape), len(shape), float(ratio), _u64("seed", seed),
+                                    _u64("offset", offset), od, dX.data_ptr(), _addr(dbias), ws, wbytes,
+                                    _raw_stream(index)))
     return dX, dbias

@@ -37,8 +37,13 @@ struct DropRng {
   float scale;
 };
 
+// WIDE: block numbers beyond 32 bits (more than 2^34 elements).  Else the
+// counter's second word is 0, and with the offset and the key the same in all
+// threads the first two rounds have one product per thread each, not two.
+template <bool WIDE>
 __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
-  uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32), c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
+  uint32_t c0 = uint32_t(block), c1 = WIDE ? uint32_t(block >> 32) : 0u;
+  uint32_t c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
   uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
@@ -53,28 +58,73 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_
   return make_uint4(c0, c1, c2, c3);
 }
 
-// keep(i) of the VW elements from index i0 (a multiple of 4) on, as bits.
-template <int VW>
-__device__ __forceinline__ uint32_t keep_bits(int64_t i0, uint64_t offset, const DropRng& g) {
-  uint32_t m = 0;
+// v[e] = keep(i0 + e) ? v[e] : 0 for the VW elements from index i0 (a multiple of 4) on.
+template <bool WIDE, int VW>
+__device__ __forceinline__ void drop(int64_t i0, uint64_t offset, const DropRng& g, float (&v)[VW]) {
 #pragma unroll
-  for (int b = 0; b < VW / 4; ++b) {
-    const uint4 w = philox(uint64_t(i0) / 4 + b, offset, g.seed);
-    m |= (uint32_t(w.x <= g.last_kept) | uint32_t(w.y <= g.last_kept) << 1 | uint32_t(w.z <= g.last_kept) << 2 |
-          uint32_t(w.w <= g.last_kept) << 3)
-         << (4 * b);
+  for (int b = 0; b < VW; b += 4) {
+    const uint4 w = philox<WIDE>(uint64_t(i0 + b) / 4, offset, g.seed);
+    v[b] = w.x <= g.last_kept ? v[b] : 0.f;
+    v[b + 1] = w.y <= g.last_kept ? v[b + 1] : 0.f;
+    v[b + 2] = w.z <= g.last_kept ? v[b + 2] : 0.f;
+    v[b + 3] = w.w <= g.last_kept ? v[b + 3] : 0.f;
   }
-  return m;
 }
 
 __device__ __forceinline__ uint64_t offset_of(const DropRng& g) {
   return g.offset + (g.offset_dev != nullptr ? *g.offset_dev : 0ull);
 }
 
+// A fragment as it is loaded: 16 bytes (VEC, aligned and whole), else VW values.
+template <typename T, bool VEC> struct RawFrag;
+template <typename T> struct RawFrag<T, true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p, int64_t i0, int64_t) { u = dev::ld16_stream(p + i0); }
+  __device__ __forceinline__ void get(float (&v)[dev::Vec16<T>::N]) const { dev::Conv<T>::unpack(u, v); }
+};
+template <typename T> struct RawFrag<T, false> {
+  float f[dev::Vec16<T>::N];
+  __device__ __forceinline__ void load(const T* p, int64_t i0, int64_t n) { dev::load_frag<T, false>(p, i0, n, f); }
+  __device__ __forceinline__ void get(float (&v)[dev::Vec16<T>::N]) const {
+#pragma unroll
+    for (int e = 0; e < dev::Vec16<T>::N; ++e) v[e] = f[e];
+  }
+};
+
+// One fragment of the forward pass: bias, scale and mask on `v`, the residual
+// added, stored.
+template <typename T, int BIAS, bool RES, bool VEC, bool WIDE>
+__device__ __forceinline__ void drop_frag(int64_t i0, int64_t n, int64_t col, int64_t C, const T* __restrict__ bias,
+                                          uint64_t offset, const DropRng& g, float (&v)[dev::Vec16<T>::N],
+                                          const RawFrag<T, VEC>& res, T* y) {
+  constexpr int VW = dev::Vec16<T>::N;
+  if constexpr (BIAS == 1) {
+    dev::add_raw<T>(dev::ld16_keep(bias + col), v);
+  } else if constexpr (BIAS == 2) {
+    int64_t c = col;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      v[e] = __fadd_rn(v[e], dev::ld1_keep(bias + c));
+      if (++c == C) c = 0;
+    }
+  }
+  drop<WIDE>(i0, offset, g, v);  // a dropped element is 0 from here on, whatever it was
+  if constexpr (RES) {
+    float r[VW];
+    res.get(r);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = fmaf(v[e], g.scale, r[e]);
+  } else {
+    dev::scale_pairs(v, g.scale);
+  }
+  dev::store_frag<T, VEC>(y, i0, n, v);
+}
+
 // BIAS 0: none; 1: C % VW == 0 and the bias 16-byte aligned (a fragment's bias
 // is one 16-byte read); 2: any other.  VEC: X, residual and Y 16-byte aligned.
-// Flat fragments: rows of any C, the last fragment may be partial.
-template <typename T, int BIAS, bool VEC>
+// Flat fragments, so rows of any C; the last one may be partial and is done
+// apart.  Bound by the generator's integer multiplies.
+template <typename T, int BIAS, bool RES, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, int64_t n, int64_t C,
                int64_t col_step, DropRng g) {
@@ -83,49 +133,42 @@ k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, 
   dev::pdl_wait();
   dev::pdl_trigger();
   const uint64_t offset = offset_of(g);
-  const int64_t nfrag = (n + VW - 1) / VW;
+  const int64_t nfrag = VEC ? n / VW : (n + VW - 1) / VW;
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t f00 = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   int64_t col = BIAS ? (f00 * VW) % C : 0;
   for (int64_t f0 = f00; f0 < nfrag; f0 += stride * U) {
-    float a[U][VW], r[U][VW];
+    RawFrag<T, VEC> a[U], r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t f = f0 + u * stride;
       if (f < nfrag) {
-        dev::load_frag<T, VEC>(x, f * VW, n, a[u]);
-        if (residual != nullptr) dev::load_frag<T, VEC>(residual, f * VW, n, r[u]);
+        a[u].load(x, f * VW, n);
+        if constexpr (RES) r[u].load(residual, f * VW, n);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t f = f0 + u * stride;
       if (f < nfrag) {
-        if constexpr (BIAS == 1) {
-          float b[VW];
-          dev::Conv<T>::unpack(dev::ld16_keep(bias + col), b);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) a[u][e] = __fadd_rn(a[u][e], b[e]);
-        } else if constexpr (BIAS == 2) {
-          int64_t c = col;
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            a[u][e] = __fadd_rn(a[u][e], dev::ld1_keep(bias + c));
-            if (++c == C) c = 0;
-          }
-        }
-        const uint32_t keep = keep_bits<VW>(f * VW, offset, g);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const float res = residual != nullptr ? r[u][e] : 0.f;
-          a[u][e] = (keep >> e & 1u) ? (residual != nullptr ? fmaf(a[u][e], g.scale, res) : a[u][e] * g.scale) : res;
-        }
-        dev::store_frag<T, VEC>(y, f * VW, n, a[u]);
+        float v[VW];
+        a[u].get(v);
+        drop_frag<T, BIAS, RES, VEC, WIDE>(f * VW, n, col, C, bias, offset, g, v, r[u], y);
         if constexpr (BIAS != 0) {
           col += col_step;
           if (col >= C) col -= C;
         }
       }
+    }
+  }
+  if constexpr (VEC) {  // the elements after the last whole fragment
+    if (f00 == 0 && n % VW != 0) {
+      const int64_t i0 = n - n % VW;
+      RawFrag<T, false> r;
+      float v[VW];
+      dev::load_frag<T, false>(x, i0, n, v);
+      if constexpr (RES) r.load(residual, i0, n);
+      drop_frag<T, BIAS == 1 ? 2 : BIAS, RES, false, WIDE>(i0, n, i0 % C, C, bias, offset, g, v, r, y);
     }
   }
 }
@@ -134,7 +177,7 @@ k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, 
 // adds the dX it writes, in float32 and before they are rounded, to its VW
 // sums, and leaves the sums of its chunk in `partial`: [chunk][C] where one tile covers a
 // walk row (the block adds the repeats of a channel up), else [chunk][walk row].
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kWalkThreads)
 k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRng g, float* partial) {
   constexpr int VW = dev::Vec16<T>::N;
@@ -153,21 +196,24 @@ k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRn
   if (mine) {
     const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
     for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-      float v[U][VW];
+      // the tensor's last fragment, which may be partial, is in its last walk row
+      RawFrag<T, VEC> a[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r0 + u < r1) dev::load_frag<T, VEC>(dy, ((r0 + u) * p.row_frags + j) * VW, n, v[u]);
+      for (int u = 0; u < U; ++u) {
+        const int64_t i0 = ((r0 + u) * p.row_frags + j) * VW;
+        if (r0 + u < r1 && (VEC ? i0 + VW <= n : i0 < n)) a[u].load(dy, i0, n);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t i0 = ((r0 + u) * p.row_frags + j) * VW;
         if (r0 + u < r1 && i0 < n) {
-          const uint32_t keep = keep_bits<VW>(i0, offset, g);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            v[u][e] = (keep >> e & 1u) ? v[u][e] * g.scale : 0.f;
-            acc[e] += v[u][e];
-          }
-          dev::store_frag<T, VEC>(dx, i0, n, v[u]);
+          float v[VW];
+          if (!VEC || i0 + VW <= n) a[u].get(v);
+          else dev::load_frag<T, false>(dy, i0, n, v);
+          drop<WIDE>(i0, offset, g, v);
+          dev::scale_pairs(v, g.scale);
+          dev::add_pairs(acc, v);
+          dev::store_frag<T, VEC>(dx, i0, n, v);
         }
       }
     }
@@ -210,32 +256,34 @@ inline DropRng rng_of(const BiasDropoutArgs& a) {
   return DropRng{a.seed, a.offset, a.offset_dev, a.last_kept, a.scale};
 }
 
-template <typename T, int BIAS, bool VEC>
+template <typename T, int BIAS, bool RES, bool VEC, bool WIDE>
 cudaError_t launch_fwd(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
   const int64_t nfrag = (a.n + VW - 1) / VW;
   const int64_t need = (nfrag + kThreads - 1) / kThreads;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(need, int64_t(sm_count) * 8));
   const int64_t step = BIAS ? (grid * kThreads * VW) % a.C : 0;
-  cudaError_t e = launch(k_bias_dropout<T, BIAS, VEC>, dim3(unsigned(grid)), dim3(kThreads), 0, stream,
+  cudaError_t e = launch(k_bias_dropout<T, BIAS, RES, VEC, WIDE>, dim3(unsigned(grid)), dim3(kThreads), 0, stream,
                          static_cast<const T*>(a.x), static_cast<const T*>(a.bias),
                          static_cast<const T*>(a.residual), static_cast<T*>(a.y), a.n, a.C, step, rng_of(a));
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
 
-template <typename T>
+// Block numbers of the generator fit 32 bits.
+inline bool narrow(int64_t n) { return (n + 3) / 4 <= (int64_t(1) << 32); }
+
+template <typename T, bool RES>
 cudaError_t bias_dropout_t(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
-  const bool vec = al16(a.x) && al16(a.y) && (a.residual == nullptr || al16(a.residual));
-  const int bias = a.bias == nullptr ? 0 : (a.C % VW == 0 && al16(a.bias)) ? 1 : 2;
-  if (vec) {
-    if (bias == 0) return launch_fwd<T, 0, true>(a, sm_count, stream, launches);
-    if (bias == 1) return launch_fwd<T, 1, true>(a, sm_count, stream, launches);
-    return launch_fwd<T, 2, true>(a, sm_count, stream, launches);
+  const bool vec = al16(a.x) && al16(a.y) && (!RES || al16(a.residual));
+  if (!narrow(a.n) || !vec) {  // the general form of both
+    return a.bias == nullptr ? launch_fwd<T, 0, RES, false, true>(a, sm_count, stream, launches)
+                             : launch_fwd<T, 2, RES, false, true>(a, sm_count, stream, launches);
   }
-  if (bias == 0) return launch_fwd<T, 0, false>(a, sm_count, stream, launches);
-  return launch_fwd<T, 2, false>(a, sm_count, stream, launches);
+  if (a.bias == nullptr) return launch_fwd<T, 0, RES, true, false>(a, sm_count, stream, launches);
+  if (a.C % VW == 0 && al16(a.bias)) return launch_fwd<T, 1, RES, true, false>(a, sm_count, stream, launches);
+  return launch_fwd<T, 2, RES, true, false>(a, sm_count, stream, launches);
 }
 
 WalkPlan grad_walk(DType t, int64_t n, int64_t C) {
@@ -248,11 +296,11 @@ cudaError_t bias_dropout_grad_t(const BiasDropoutArgs& a, cudaStream_t stream, i
   float* partial = static_cast<float*>(a.workspace);
   const dim3 grid(unsigned(int64_t(p.tiles) * p.chunks));
   cudaError_t e;
-  if (al16(a.x) && al16(a.y))
-    e = launch(k_bias_dropout_grad<T, true>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
+  if (al16(a.x) && al16(a.y) && narrow(a.n))
+    e = launch(k_bias_dropout_grad<T, true, false>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
                static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
   else
-    e = launch(k_bias_dropout_grad<T, false>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
+    e = launch(k_bias_dropout_grad<T, false, true>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
                static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
   if (e != cudaSuccess) return e;
   *launches += 1;
@@ -266,10 +314,17 @@ cudaError_t bias_dropout_grad_t(const BiasDropoutArgs& a, cudaStream_t stream, i
 }  // namespace
 
 cudaError_t launch_bias_dropout(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  const bool res = a.residual != nullptr;
   switch (a.t) {
-    case DType::F32: return bias_dropout_t<float>(a, sm_count, stream, launches);
-    case DType::F16: return bias_dropout_t<__half>(a, sm_count, stream, launches);
-    default: return bias_dropout_t<__nv_bfloat16>(a, sm_count, stream, launches);
+    case DType::F32:
+      return res ? bias_dropout_t<float, true>(a, sm_count, stream, launches)
+                 : bias_dropout_t<float, false>(a, sm_count, stream, launches);
+    case DType::F16:
+      return res ? bias_dropout_t<__half, true>(a, sm_count, stream, launches)
+                 : bias_dropout_t<__half, false>(a, sm_count, stream, launches);
+    default:
+      return res ? bias_dropout_t<__nv_bfloat16, true>(a, sm_count, stream, launches)
+                 : bias_dropout_t<__nv_bfloat16, false>(a, sm_count, stream, launches);
   }
 }
 
