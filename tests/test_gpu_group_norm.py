@@ -19,6 +19,8 @@ SHAPES = [
     ((1, 9, 4104), 27), ((2, 3, 2055), 5), ((1, 4, 8192), 64),   # rows wider than a block of threads
     ((1, 5000, 32), 8), ((2, 3000, 1), 1), ((1, 2777, 5), 5), ((1, 700, 3), 1),  # few channels
     ((2, 9973, 40), 4),
+    ((2, 1024, 320), 32), ((1, 2048, 96), 96), ((3, 1331, 189), 9), ((1, 4096, 64), 2),  # spread over a cluster
+    ((1, 70000, 64), 4), ((2, 30011, 33), 3), ((1, 300, 12288), 32),  # more than a cluster holds
 ]
 
 
@@ -68,6 +70,31 @@ def test_group_norm_shapes(lib, dtype, shape, groups):
 def test_group_norm_alignment(lib, dtype, shape, groups, offset):
     d = group_norm_inputs(shape, dtype, 11 + offset)
     check_forward(lib, d, groups, 1e-5, True, offset=offset)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,groups", SHAPES)
+def test_group_norm_shapes_apart(lib, dtype, shape, groups):
+    # an output at another offset than the input: the split form, for every shape
+    d = group_norm_inputs(shape, dtype, 17 + sum(shape))
+    x, dy, gamma, beta = (d[k].cuda() for k in ("X", "dY", "gamma", "beta"))
+    es = x.element_size()
+    y, dx = (Guarded(shape, x.dtype, offset_bytes=es) for _ in range(2))
+    _, mean, inv = lib.ep_group_norm(x, gamma, beta, groups, 1e-5, lib.EP_ACT_SILU, Y=y.tensor, mean=True,
+                                     inv_std_dev=True)
+    _, dg, db = lib.ep_group_norm_grad(dy, x, gamma, beta, mean, inv, groups, lib.EP_ACT_SILU, dX=dx.tensor)
+    torch.cuda.synchronize()
+    y.check()
+    dx.check()
+    n, c = shape[0], shape[-1]
+    o = tr.group_norm(d["X"], d["gamma"], d["beta"], groups, 1e-5, True)
+    stats_close(mean.cpu(), inv.cpu(), o, 1.0)
+    assert_within(y.tensor.cpu(), o["Y"].reshape(n, -1, c),
+                  norm_delta(o["mean"], o["inv_std_dev"], d["gamma"], groups, c), "gn")
+    o = tr.group_norm_grad(d["dY"], d["X"], d["gamma"], d["beta"], mean.cpu(), inv.cpu(), groups, True)
+    assert_within(dx.tensor.cpu(), o["dX"], 64 * U32 * o["dX_scale"], "gn dX")
+    assert_within(dg.cpu(), o["dgamma"], 64 * U32 * o["dgamma_scale"], "gn dgamma")
+    assert_within(db.cpu(), o["dbeta"], 64 * U32 * o["dbeta_scale"], "gn dbeta")
 
 
 def test_group_norm_different_alignments(lib):

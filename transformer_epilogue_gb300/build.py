@@ -25,7 +25,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtransformer_epilogue.so")
 
 SOURCES = ["ep_api.cpp", "skip_layer_norm.cu", "bias_softmax.cu", "elementwise.cu", "group_norm.cu",
-           "bias_dropout.cu"]
+           "group_norm_fused.cu", "bias_dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]

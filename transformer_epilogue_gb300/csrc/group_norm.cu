@@ -28,34 +28,11 @@
 #include "column_walk.cuh"
 #include "device_common.cuh"
 #include "ep_internal.h"
+#include "group_norm.cuh"
 #include "launch_util.h"
 
 namespace ep {
 namespace {
-
-// u * sigmoid(u).  float32: the library exponential and a rounded division.
-// 16-bit results: 2^x and 1/x by the hardware approximations, whose errors (a
-// few float32 ulp) are far below the result's rounding; below u = -88.7 the
-// exponential overflows and the result, above -1e-36, is -0.
-template <typename T>
-__device__ __forceinline__ float silu(float u) {
-  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(u, 1.0f + expf(-u));
-  else return u * dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
-}
-
-template <typename T>
-__device__ __forceinline__ float sigmoid(float u) {
-  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(1.0f, 1.0f + expf(-u));
-  else return dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
-}
-
-// du of the definition.
-template <typename T, bool SILU>
-__device__ __forceinline__ float act_grad(float dy, float u) {
-  if constexpr (!SILU) return dy;
-  const float s = sigmoid<T>(u);
-  return dy * (s * fmaf(u, 1.0f - s, 1.0f));
-}
 
 // One call's sizes, as every kernel of the split form gets them.
 // (C is at most kMaxGroupNormChannels, so positions in a walk row fit an int.)
@@ -698,10 +675,14 @@ size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int6
 }
 
 size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
-  return gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total;
+  return std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
+                  group_norm_grad_fused_bytes(t, N, S, C, G));
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  bool done = false;
+  const cudaError_t e = launch_group_norm_fused(a, sm_count, stream, launches, &done);
+  if (done || e != cudaSuccess) return e;
   switch (a.t) {
     case DType::F32: return group_norm_t<float>(a, sm_count, stream, launches);
     case DType::F16: return group_norm_t<__half>(a, sm_count, stream, launches);
@@ -710,6 +691,9 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
 }
 
 cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  bool done = false;
+  const cudaError_t e = launch_group_norm_grad_fused(a, sm_count, stream, launches, &done);
+  if (done || e != cudaSuccess) return e;
   switch (a.t) {
     case DType::F32: return group_norm_grad_t<float>(a, sm_count, stream, launches);
     case DType::F16: return group_norm_grad_t<__half>(a, sm_count, stream, launches);

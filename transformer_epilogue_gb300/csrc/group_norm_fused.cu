@@ -1,0 +1,824 @@
+// GroupNorm and its gradient with the sample on chip: x (and dy) are read once,
+// into registers, and the result is written from there.  One launch for the
+// forward pass, no scratch.  The definitions stand in group_norm.cu.
+//
+// A block holds walk rows of `cf` fragments, one thread to a fragment column, so
+// a thread's channels stay the same:
+//   MODE 0  C % VW == 0 and D % VW == 0: a walk row is a row of a slab of W
+//           channels (whole groups), and a fragment lies in one group;
+//   MODE 1  C % VW == 0, any D: the same slabs, sums for each channel;
+//   MODE 2  any C and alignment: a walk row is the C / gcd(C, VW) fragments after
+//           which channels repeat (column_walk.cuh), over the whole sample; the
+//           first and the last fragment of a sample may be partial.
+// `phases` walk rows lie side by side in a block, `per_sample` of them in one
+// sample; each thread has up to NV rows.  Small samples share a block; a large
+// one is spread over the CTAs of a cluster, each with its range of rows, whose
+// group sums meet in distributed shared memory.
+//
+// Statistics: values are taken relative to their group's first value, summed,
+// and the squares of their distances from the block's mean of the group summed
+// in a second pass over the registers; a cluster's blocks are joined with Chan's
+// formula.  All in float32, in an order that does not depend on timing.
+//
+// What bounds it: small samples, the latency of load, two block reductions and
+// store; large batches, DRAM.
+#include <algorithm>
+#include <climits>
+#include <numeric>
+
+#include "column_walk.cuh"
+#include "device_common.cuh"
+#include "ep_internal.h"
+#include "group_norm.cuh"
+#include "launch_util.h"
+
+namespace ep {
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxCluster = 16;
+
+struct FusedPlan {
+  int W;              // channels after which a walk row repeats: a slab's, or C
+  int cf;             // fragments of a walk row
+  int slabs;          // C / W
+  int q;              // groups in a slab
+  int phases, per_sample, samples;  // walk rows side by side, of one sample, samples in a block
+  int threads, nv, cluster;
+  int rows, rows_per_cta;           // walk rows of a sample; of one CTA
+  int64_t items;      // blocks of samples x slabs, each `cluster` CTAs
+  int64_t grid_items; // items running at a time (the gradient; forward: all)
+};
+
+struct FusedDims {
+  int64_t N, S, L;
+  int C, G, D;
+  float eps;
+  bool silu;
+  FusedPlan p;
+};
+
+// Where a thread stands in an item.
+template <typename T, int MODE>
+struct Place {
+  static constexpr int VW = dev::Vec16<T>::N;
+  int64_t n;       // its sample
+  int64_t e0;      // its first fragment's first element, from the sample's (slab's) start
+  int64_t stride;  // elements from one of its fragments to the next
+  int64_t lim;     // MODE 2: elements of the sample
+  int off;
+  int kn;          // its fragments
+  int slab;
+
+  __device__ __forceinline__ Place(const FusedDims& d, const T* x, int64_t item, int rank, int trow, int tcol) {
+    const FusedPlan& p = d.p;
+    slab = MODE == 2 ? 0 : static_cast<int>(item % p.slabs);
+    const int ns = trow / p.per_sample, ph = trow - ns * p.per_sample;
+    n = (MODE == 2 ? item : item / p.slabs) * p.samples + ns;
+    const bool live = trow < p.phases && n < d.N;
+    off = MODE == 2 && live ? dev::misalignment(x + n * d.L) : 0;
+    const int64_t row = MODE == 2 ? int64_t(p.cf) * VW : d.C;
+    const int r0 = rank * p.rows_per_cta + ph, r1 = min(p.rows, (rank + 1) * p.rows_per_cta);
+    kn = live && r0 < r1 ? (r1 - r0 + p.per_sample - 1) / p.per_sample : 0;
+    e0 = r0 * row + tcol * VW - off;
+    stride = p.per_sample * row;
+    lim = d.L;
+  }
+  __device__ __forceinline__ bool whole(int k) const {
+    return MODE != 2 || (e0 + k * stride >= 0 && e0 + k * stride + VW <= lim);
+  }
+  __device__ __forceinline__ bool inside(int k, int e) const {
+    return MODE != 2 || (e0 + k * stride + e >= 0 && e0 + k * stride + e < lim);
+  }
+  __device__ __forceinline__ uint4 load(const T* base, int k) const {
+    const int64_t at = e0 + k * stride;
+    if (whole(k)) return dev::ld16_stream(base + at);
+    float v[VW];
+    dev::load_frag<T, false>(base, at, lim, v);
+    return dev::Conv<T>::pack(v);  // exact: the values are T's
+  }
+  __device__ __forceinline__ void store(T* base, int k, const float (&v)[VW]) const {
+    const int64_t at = e0 + k * stride;
+    if (whole(k)) dev::st16_stream(base + at, dev::Conv<T>::pack(v));
+    else dev::store_frag<T, false>(base, at, lim, v);
+  }
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 16 bytes at this shared-memory address in the cluster's block `rank`.
+__device__ __forceinline__ float4 ld_rank(const float4* p, int rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// Sums over the entries of each (sample, group) of a block.  Entries are floats
+// (or pairs) by position: fragment (MODE 0) or element; the group's are at
+// off + g De + j + k Cw, j < De, modulo the np positions of a sample (the
+// positions before `off` hold the channels that the last repeat misses).  A set
+// of lanes, the smallest power of two that holds a group's entries, takes one
+// (sample, group) at a time.
+struct Gather {
+  int De, Cw, np, entries, set, q, slots;
+  __device__ __forceinline__ Gather(const FusedPlan& p, int D, int VW, bool frags) {
+    De = frags ? D / VW : D;
+    Cw = frags ? p.cf : p.W;
+    np = p.per_sample * p.cf * (frags ? 1 : VW);
+    entries = np / Cw * De;
+    set = entries >= 32 ? 32 : entries <= 1 ? 1 : 1 << (32 - __clz(entries - 1));
+    q = p.q;
+    slots = p.samples * p.q;
+  }
+  // add(position, a, b) for each entry, then done(slot, a, b) by one lane
+  template <typename OFF, typename ADD, typename DONE>
+  __device__ __forceinline__ void run(OFF off_of, ADD add, DONE done) const {
+    const int sets = blockDim.x / set, l = threadIdx.x & (set - 1);
+    for (int s0 = 0; s0 < slots; s0 += sets) {
+      const int s = s0 + threadIdx.x / set;
+      float a = 0.f, b = 0.f;
+      if (s < slots) {
+        const int ns = s / q, start = off_of(ns) + (s - ns * q) * De;
+        for (int i = l; i < entries; i += set) {
+          const int k = i / De;
+          int pos = start + (i - k * De) + k * Cw;
+          if (pos >= np) pos -= np;
+          add(ns * np + pos, a, b);
+        }
+      }
+      for (int o = set >> 1; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      if (s < slots && l == 0) done(s, a, b);
+    }
+  }
+};
+
+// Joins the cluster's values of each slot: f(slot, lane's rank value or 0).
+template <typename F>
+__device__ __forceinline__ void for_slots_by_rank(int slots, int cluster, F f) {
+  const int sets = blockDim.x / cluster;  // the cluster size is a power of two up to 16
+  for (int s0 = 0; s0 < slots; s0 += sets) f(s0 + int(threadIdx.x) / cluster, int(threadIdx.x) & (cluster - 1));
+}
+__device__ __forceinline__ float set_sum(float x, int set) {
+  for (int o = set >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <typename T, int NV, int MODE>
+__global__ void __launch_bounds__(kMaxThreads)
+k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, T* y, float* mean_out,
+           float* inv_out, FusedDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = MODE == 0 ? 1 : VW;  // entries of a thread
+  extern __shared__ __align__(16) float smem[];
+  const FusedPlan& p = d.p;
+  const int slots = p.samples * p.q, ents = p.phases * p.cf * EV;
+  float4* xch = reinterpret_cast<float4*>(smem);                 // (count, mean, M2) for the cluster
+  float* ent = smem + (p.cluster > 1 ? 4 * slots : 0);
+  float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
+  float* gk = cnt + (MODE == 2 ? ents : 0);                      // the group's first value
+  float* gm = gk + slots;
+  float* gr = gm + slots;
+  const int rank = blockIdx.x % p.cluster;
+  const int64_t item = blockIdx.x / p.cluster;
+  const int trow = threadIdx.x / p.cf, tcol = threadIdx.x - trow * p.cf;
+  const int ns = trow / p.per_sample;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+
+  const Place<T, MODE> at(d, x, item, rank, trow, tcol);
+  const T* xs = x + (at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0);
+  uint4 raw[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (k < at.kn) raw[k] = at.load(xs, k);
+
+  // this thread's channels (within the slab), groups and shifts
+  int c0 = MODE == 2 ? (tcol * VW + p.W - at.off % p.W) % p.W : tcol * VW;
+  int grp[EV];
+  float shift[EV];
+  {
+    int c = c0;
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      const int g = c / d.D;
+      grp[e] = ns * p.q + g;
+      shift[e] = at.kn > 0 ? dev::ld1_stream(xs + g * d.D) : 0.f;
+      if (++c == p.W) c = 0;
+    }
+  }
+
+  // sums relative to the shift, then squares relative to the block's mean
+  const bool mine = trow < p.phases;
+  auto pass = [&](const float (&m)[EV], bool square, float (&s)[EV]) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e) s[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k < at.kn) {
+        float v[VW];
+        dev::Conv<T>::unpack(raw[k], v);
+        const bool whole = at.whole(k);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const int i = MODE == 0 ? 0 : e;
+          v[e] = (v[e] - shift[i]) - (square ? m[i] : 0.f);
+          if (!whole && !at.inside(k, e)) v[e] = 0.f;
+          if (square) v[e] *= v[e];
+        }
+        if constexpr (MODE == 0) {
+          if constexpr (VW == 8) s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+          else s[0] += (v[0] + v[1]) + (v[2] + v[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) s[e] += v[e];
+        }
+      }
+    }
+  };
+  const Gather gather(p, d.D, VW, MODE == 0);
+  const int64_t n0 = (MODE == 2 ? item : item / p.slabs) * p.samples;
+  auto off_of = [&](int s) {
+    return MODE == 2 && n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0;
+  };
+  // values of a group in this CTA
+  const int my_rows = max(0, min(p.rows, (rank + 1) * p.rows_per_cta) - rank * p.rows_per_cta);
+  const float count = MODE == 2 ? float(d.S) * float(d.D) : float(my_rows) * float(d.D);
+
+  float m[EV], s[EV];
+#pragma unroll
+  for (int e = 0; e < EV; ++e) m[e] = 0.f;
+  pass(m, false, s);
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
+    if constexpr (MODE == 2) {
+#pragma unroll
+      for (int e = 0; e < EV; ++e) m[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (k < at.kn) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) m[e] += at.inside(k, e) ? 1.f : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EV; ++e) cnt[threadIdx.x * EV + e] = m[e];
+    }
+  }
+  __syncthreads();
+  gather.run(off_of,
+             [&](int i, float& a, float& b) {
+               a += ent[i];
+               if constexpr (MODE == 2) b += cnt[i];
+             },
+             [&](int s, float a, float b) {
+               const float n = MODE == 2 ? b : count;
+               gm[s] = n > 0.f ? a / n : 0.f;
+               const int g = s % p.q;
+               const int64_t sample = n0 + s / p.q;
+               gk[s] = sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(at.slab) * p.W + g * d.D) : 0.f;
+               if (p.cluster > 1) xch[s].x = n;
+             });
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < EV; ++e) m[e] = mine ? gm[grp[e]] : 0.f;
+  pass(m, true, s);
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
+  }
+  __syncthreads();
+  const float total = float(d.S) * float(d.D);
+  auto finish = [&](int s, float mean, float m2) {
+    const float mu = gk[s] + mean, r = 1.0f / sqrtf(m2 / total + d.eps);
+    gm[s] = mu;
+    gr[s] = r;
+    const int64_t sample = n0 + s / p.q;
+    if (rank == 0 && sample < d.N) {
+      const int64_t i = sample * d.G + int64_t(at.slab) * p.q + s % p.q;
+      if (mean_out != nullptr) mean_out[i] = mu;
+      if (inv_out != nullptr) inv_out[i] = r;
+    }
+  };
+  gather.run(off_of, [&](int i, float& a, float&) { a += ent[i]; },
+             [&](int s, float a, float) {
+               if (p.cluster == 1) finish(s, gm[s], a);
+               else xch[s] = make_float4(xch[s].x, gm[s], a, 0.f);
+             });
+  if (p.cluster > 1) {
+    cluster_sync();
+    for_slots_by_rank(slots, p.cluster, [&](int s, int r) {
+      const float4 v = s < slots ? ld_rank(xch + s, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float mean = set_sum(v.x * v.y, p.cluster) / total;
+      const float t = v.y - mean;
+      const float m2 = set_sum(v.z + v.x * t * t, p.cluster);
+      if (s < slots && r == 0) finish(s, mean, m2);
+    });
+    cluster_sync();  // no block leaves (or overwrites x) while another reads its sums
+  } else {
+    __syncthreads();
+  }
+
+  // y
+  float mu[EV], rs[EV], a[VW], b[VW];
+#pragma unroll
+  for (int e = 0; e < EV; ++e) {
+    mu[e] = mine ? gm[grp[e]] : 0.f;
+    rs[e] = mine ? gr[grp[e]] : 0.f;
+  }
+  if (at.kn > 0) {
+    const int cs = at.slab * p.W;
+    if constexpr (MODE == 2) {
+      int c = c0;
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        a[e] = dev::ld1_keep(gamma + c);
+        b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+        if (++c == p.W) c = 0;
+      }
+    } else {  // (the parameters may have any alignment)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        a[e] = dev::ld1_keep(gamma + cs + c0 + e);
+        b[e] = beta != nullptr ? dev::ld1_keep(beta + cs + c0 + e) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) a[e] *= rs[MODE == 0 ? 0 : e];
+    T* ys = y + at.n * d.L + cs;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k < at.kn) {
+        float v[VW];
+        dev::Conv<T>::unpack(raw[k], v);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) v[e] = fmaf(v[e] - mu[MODE == 0 ? 0 : e], a[e], b[e]);
+        if (d.silu) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) v[e] = silu<T>(v[e]);
+        }
+        at.store(ys, k, v);
+      }
+    }
+  }
+}
+
+// The gradient.  A CTA takes items in turn (grid_items apart), all of one slab,
+// and keeps the sums of du and du * h of its channels over them in registers;
+// they leave once, as row (item index * cluster + rank) of cpart: 2 x [row][C].
+// The groups' means m1 and m2 of an item meet as the forward's sums do.
+template <typename T, int NV, int MODE>
+__global__ void __launch_bounds__(kMaxThreads)
+k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+                const float* inv, T* dx, float* cpart, FusedDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = MODE == 0 ? 1 : VW;
+  extern __shared__ __align__(16) float smem[];
+  const FusedPlan& p = d.p;
+  const int slots = p.samples * p.q, ents = p.phases * p.cf * VW;
+  float4* xch = reinterpret_cast<float4*>(smem);
+  float* ent_a = smem + (p.cluster > 1 ? 4 * slots : 0);
+  float* ent_b = ent_a + ents;
+  float* g1 = ent_b + ents;
+  float* g2 = g1 + slots;
+  const int rank = blockIdx.x % p.cluster;
+  const int64_t first = blockIdx.x / p.cluster;
+  const int trow = threadIdx.x / p.cf, tcol = threadIdx.x - trow * p.cf;
+  const int ns = trow / p.per_sample;
+  const bool mine = trow < p.phases;
+  const float scale = 1.0f / (float(d.S) * float(d.D));
+  const Gather gather(p, d.D, VW, MODE == 0);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+
+  float tot_a[VW], tot_b[VW], ga[VW], be[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = ga[e] = be[e] = 0.f;
+  int off = 0, c0 = 0, slab = 0;
+  bool once = true;
+
+  for (int64_t item = first; item < p.items; item += p.grid_items) {
+    const Place<T, MODE> at(d, x, item, rank, trow, tcol);
+    const int64_t base = at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0;
+    uint4 raw[NV], rdy[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k < at.kn) {
+        raw[k] = at.load(x + base, k);
+        rdy[k] = at.load(dy + base, k);
+      }
+    }
+    if (once) {  // the items of a CTA share their slab, and (MODE 2) their offset
+      once = false;
+      slab = at.slab;
+      if constexpr (MODE == 2) {
+        const int64_t n0 = item * p.samples;
+        off = dev::misalignment(x + n0 * d.L);
+      }
+      c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
+      if (mine) {
+        int c = c0;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          ga[e] = dev::ld1_keep(gamma + slab * p.W + c);
+          be[e] = beta != nullptr ? dev::ld1_keep(beta + slab * p.W + c) : 0.f;
+          if (++c == p.W) c = 0;
+        }
+      }
+    }
+    float mu[EV], rs[EV];
+    int grp[EV];
+    {
+      int c = c0;
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        const int g = c / d.D;
+        grp[e] = ns * p.q + g;
+        const int64_t i = at.n * d.G + int64_t(slab) * p.q + g;
+        mu[e] = at.kn > 0 ? mean[i] : 0.f;
+        rs[e] = at.kn > 0 ? inv[i] : 0.f;
+        if (++c == p.W) c = 0;
+      }
+    }
+    float sa[VW], sb[VW];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
+    // h and du of fragment k (0 outside the sample: adds nothing)
+    auto values = [&](int k, float (&h)[VW], float (&du)[VW]) {
+      dev::Conv<T>::unpack(raw[k], h);
+      dev::Conv<T>::unpack(rdy[k], du);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) h[e] = (h[e] - mu[MODE == 0 ? 0 : e]) * rs[MODE == 0 ? 0 : e];
+      if (d.silu) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) du[e] = act_grad<T, true>(du[e], fmaf(h[e], ga[e], be[e]));
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (k < at.kn) {
+        float h[VW], du[VW];
+        values(k, h, du);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          sa[e] += du[e];
+          sb[e] = fmaf(du[e], h[e], sb[e]);
+        }
+      }
+    }
+    if (mine) {
+      if constexpr (MODE == 0) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          a = fmaf(sa[e], ga[e], a);
+          b = fmaf(sb[e], ga[e], b);
+        }
+        ent_a[threadIdx.x] = a;
+        ent_b[threadIdx.x] = b;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          ent_a[threadIdx.x * VW + e] = sa[e] * ga[e];
+          ent_b[threadIdx.x * VW + e] = sb[e] * ga[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        tot_a[e] += sa[e];
+        tot_b[e] += sb[e];
+      }
+    }
+    __syncthreads();
+    gather.run([&](int) { return off; },
+               [&](int i, float& a, float& b) {
+                 a += ent_a[i];
+                 b += ent_b[i];
+               },
+               [&](int s, float a, float b) {
+                 if (p.cluster == 1) {
+                   g1[s] = a * scale;
+                   g2[s] = b * scale;
+                 } else {
+                   xch[s] = make_float4(a, b, 0.f, 0.f);
+                 }
+               });
+    if (p.cluster > 1) {
+      cluster_sync();
+      for_slots_by_rank(slots, p.cluster, [&](int s, int r) {
+        const float4 v = s < slots ? ld_rank(xch + s, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float a = set_sum(v.x, p.cluster), b = set_sum(v.y, p.cluster);
+        if (s < slots && r == 0) {
+          g1[s] = a * scale;
+          g2[s] = b * scale;
+        }
+      });
+      cluster_sync();  // the next item's sums go to the same place
+    } else {
+      __syncthreads();
+    }
+    if (at.kn > 0) {
+      float a1[EV], a2[EV];
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        a1[e] = g1[grp[e]];
+        a2[e] = g2[grp[e]];
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (k < at.kn) {
+          float h[VW], v[VW];
+          values(k, h, v);  // again: keeping du would cost more registers than the block has
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            const int i = MODE == 0 ? 0 : e;
+            v[e] = rs[i] * (fmaf(v[e], ga[e], -a1[i]) - h[e] * a2[i]);
+          }
+          at.store(dx + base, k, v);
+        }
+      }
+    }
+    // (g1, g2 are written again only after the next item's first barrier)
+  }
+
+  if (cpart == nullptr) return;
+  __syncthreads();
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      ent_a[threadIdx.x * VW + e] = tot_a[e];
+      ent_b[threadIdx.x * VW + e] = tot_b[e];
+    }
+  }
+  __syncthreads();
+  // channel c is at off + c + k W, modulo a sample's positions, in every sample
+  const int np = p.per_sample * p.cf * VW, reps = np / p.W;
+  const int64_t rows = p.grid_items / p.slabs * p.cluster;
+  const int64_t row = (first / p.slabs) * p.cluster + rank;
+  const int many = reps * p.samples;
+  const int set = many >= 32 ? 32 : 1;  // lanes to a channel
+  for (int c = threadIdx.x / set; c < p.W; c += blockDim.x / set) {
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x & (set - 1); i < many; i += set) {
+      const int k = i % reps;
+      int pos = off + c + k * p.W;
+      if (pos >= np) pos -= np;
+      pos += i / reps * np;
+      a += ent_a[pos];
+      b += ent_b[pos];
+    }
+    if (set == 32) {  // (a warp's lanes share c)
+      a = dev::warp_sum(a);
+      b = dev::warp_sum(b);
+    }
+    if ((threadIdx.x & (set - 1)) == 0) {
+      float* out = cpart + row * d.C + slab * p.W + c;
+      out[0] = a;
+      out[rows * d.C] = b;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// plans
+// ---------------------------------------------------------------------------
+
+int pow2_at_least(int64_t v) {
+  int p = 1;
+  while (p < v) p *= 2;
+  return p;
+}
+
+// Splits the rows of a sample (cf fragments each) over threads and CTAs: false
+// if `nv_max` fragments a thread do not hold it.
+bool split_rows(FusedPlan* p, int64_t N, int64_t rows, int nv_max) {
+  if (p->cf > kMaxThreads || rows > INT_MAX / 2) return false;
+  p->rows = int(rows);
+  const int64_t frags = rows * p->cf;
+  if (frags <= 4 * kWalkThreads) {
+    // a small sample: one CTA, about 256 threads, with other samples where there
+    // are enough of them (and two fragments a thread where one sample fills it)
+    int phases = std::max(1, kWalkThreads / p->cf);
+    p->per_sample = int(std::min<int64_t>(rows, phases));
+    while ((rows + p->per_sample - 1) / p->per_sample > nv_max && p->cf * (p->per_sample + 1) <= kMaxThreads)
+      p->per_sample += 1;
+    if ((rows + p->per_sample - 1) / p->per_sample > nv_max) return false;
+    const int64_t fit = std::max(1, phases / p->per_sample);
+    p->samples = int(std::max<int64_t>(1, std::min(fit, N * p->slabs / (2 * kPlanSms))));
+    p->phases = p->samples * p->per_sample;
+    p->cluster = 1;
+    p->rows_per_cta = int(rows);
+  } else {
+    const int most = kMaxThreads / p->cf;  // rows side by side
+    int64_t per = rows;
+    int k = 1;
+    while (k < kMaxCluster && ((per = (rows + k - 1) / k) + most - 1) / most > nv_max) k *= 2;
+    while (k < kMaxCluster && N * p->slabs * k < kPlanSms && (rows + k - 1) / k > most) k *= 2;
+    per = (rows + k - 1) / k;
+    if ((per + most - 1) / most > nv_max) return false;
+    p->cluster = k;
+    p->rows_per_cta = int(per);
+    p->per_sample = p->phases = int(std::min<int64_t>(per, most));
+    p->samples = 1;
+  }
+  p->threads = (p->phases * p->cf + 31) / 32 * 32;
+  const int need = (p->rows_per_cta + p->per_sample - 1) / p->per_sample;
+  p->nv = pow2_at_least(need);
+  p->items = (N + p->samples - 1) / p->samples * p->slabs;
+  p->grid_items = p->items;
+  return p->items * p->cluster <= INT_MAX;
+}
+
+// slab: C % vw == 0 and 16-byte-aligned operands; else the walk over whole samples.
+bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, int nv_max, FusedPlan* p) {
+  const int64_t D = C / G;
+  if (!slab) {
+    p->W = int(C);
+    p->slabs = 1;
+    p->q = int(G);
+    const int64_t period = C / std::gcd(C, int64_t(vw));
+    if (period > kMaxThreads) return false;
+    p->cf = int(period);
+    const int64_t total = (S * C + 2 * (vw - 1)) / vw;  // fragments, wherever a sample starts
+    return split_rows(p, N, (total + period - 1) / period, nv_max);
+  }
+  if (C % vw != 0) return false;
+  auto with = [&](int64_t q) {
+    p->W = int(q * D);
+    p->slabs = int(G / q);
+    p->q = int(q);
+    p->cf = int(q * D / vw);
+    return split_rows(p, N, S, nv_max);
+  };
+  // a small sample stays in one piece, with contiguous rows
+  if (C / vw <= kMaxThreads && S * (C / vw) <= 4 * kWalkThreads) return with(G);
+  // else the narrowest slab of whole groups whose rows are 128 bytes or more
+  for (int64_t q = 1; q <= G; ++q) {
+    if (G % q != 0 || q * D % vw != 0) continue;
+    if (q * D / vw > kMaxThreads) break;
+    if (q * D / vw >= 8 || q == G) return with(q);
+  }
+  return false;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads, size_t smem, int cluster,
+                           cudaStream_t stream, Args... args) {
+  if (cluster > 8) {  // beyond the portable size
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = EP_PDL ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Shared memory: the cluster's exchange, the entries (MODE 2: and their counts;
+// the gradient: two sets for every channel) and the groups' values.
+size_t fused_smem(const FusedPlan& p, int mode, int vw, bool grad) {
+  const size_t slots = size_t(p.samples) * p.q, frags = size_t(p.phases) * p.cf;
+  const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
+  return 4 * (ents + (p.cluster > 1 ? 4 * slots : 0) + (grad ? 2 : 3) * slots);
+}
+constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
+
+template <typename T, int MODE>
+cudaError_t fused_fwd(const GroupNormArgs& a, const FusedDims& d, cudaStream_t stream, int* launches) {
+  const FusedPlan& p = d.p;
+  auto fn = p.nv == 1   ? k_gn_fused<T, 1, MODE>
+            : p.nv == 2 ? k_gn_fused<T, 2, MODE>
+            : p.nv == 4 ? k_gn_fused<T, 4, MODE>
+            : p.nv == 8 ? k_gn_fused<T, 8, MODE>
+                        : k_gn_fused<T, 16, MODE>;
+  const cudaError_t e = launch_cluster(
+      fn, unsigned(p.items * p.cluster), p.threads, fused_smem(p, MODE, dev::Vec16<T>::N, false), p.cluster, stream,
+      static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta),
+      static_cast<T*>(a.y), a.mean, a.inv, d);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+template <typename T, int MODE>
+cudaError_t fused_grad(const GroupNormGradArgs& a, const FusedDims& d, float* cpart, cudaStream_t stream,
+                       int* launches) {
+  const FusedPlan& p = d.p;
+  auto fn = p.nv == 1   ? k_gn_grad_fused<T, 1, MODE>
+            : p.nv == 2 ? k_gn_grad_fused<T, 2, MODE>
+                        : k_gn_grad_fused<T, 4, MODE>;
+  cudaError_t e = launch_cluster(
+      fn, unsigned(p.grid_items * p.cluster), p.threads, fused_smem(p, MODE, dev::Vec16<T>::N, true), p.cluster,
+      stream, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
+      static_cast<const T*>(a.beta), a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (cpart != nullptr) {
+    const int64_t jobs = (int64_t(d.C) + 31) / 32 * 2;
+    // the sums of du are dbeta, those of du * h are dgamma
+    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart,
+               p.grid_items / p.slabs * p.cluster, int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta),
+               static_cast<T*>(a.dgamma));
+    if (e == cudaSuccess) *launches += 1;
+  }
+  return e;
+}
+
+inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uintptr_t>(p) & 15u); }
+
+// Items of the gradient that run at a time: all CTAs resident at about four (of
+// 256 threads) an SM, a whole number of them for each slab.
+void persist(FusedPlan* p) {
+  const int64_t ctas = kPlanSms * std::max(1, 1024 / p->threads);
+  const int64_t per_slab = std::max<int64_t>(1, ctas / (int64_t(p->slabs) * p->cluster));
+  p->grid_items = std::min(p->items / p->slabs, per_slab) * p->slabs;
+}
+
+constexpr int kFwdNv = 16, kGradNv = 4;
+
+bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, FusedPlan* p) {
+  if (!fused_plan(vw, N, S, C, G, slab, kGradNv, p)) return false;
+  persist(p);
+  // a CTA's items share the offset of their channels: all samples start alike,
+  // or a CTA has one sample
+  if (!slab && S * C % vw != 0 && (p->samples > 1 || p->grid_items < p->items)) return false;
+  return fused_smem(*p, slab ? 0 : 2, vw, true) <= kSmemMost;
+}
+
+}  // namespace
+
+size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+  const int vw = t == DType::F32 ? 4 : 8;
+  size_t most = 0;
+  for (int slab = 0; slab < 2; ++slab) {
+    FusedPlan p;
+    if (grad_plan(vw, N, S, C, G, slab != 0, &p))
+      most = std::max(most, size_t(p.grid_items / p.slabs * p.cluster) * size_t(C) * 8);
+  }
+  return most;
+}
+
+cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t stream, int* launches, bool* done) {
+  const int vw = a.t == DType::F32 ? 4 : 8;
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, a.silu, {}};
+  *done = false;
+  if (misalign16(a.x) != misalign16(a.y)) return cudaSuccess;
+  const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
+  if (!fused_plan(vw, a.N, a.S, a.C, a.G, slab, kFwdNv, &d.p)) return cudaSuccess;
+  const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
+  if (fused_smem(d.p, mode, vw, false) > kSmemMost) return cudaSuccess;
+  *done = true;
+#define EP_GN_FUSED(T)                                                          \
+  (mode == 0   ? fused_fwd<T, 0>(a, d, stream, launches)                        \
+   : mode == 1 ? fused_fwd<T, 1>(a, d, stream, launches)                        \
+               : fused_fwd<T, 2>(a, d, stream, launches))
+  switch (a.t) {
+    case DType::F32: return EP_GN_FUSED(float);
+    case DType::F16: return EP_GN_FUSED(__half);
+    default: return EP_GN_FUSED(__nv_bfloat16);
+  }
+#undef EP_GN_FUSED
+}
+
+cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int, cudaStream_t stream, int* launches,
+                                         bool* done) {
+  const int vw = a.t == DType::F32 ? 4 : 8;
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, a.silu, {}};
+  *done = false;
+  if (misalign16(a.x) != misalign16(a.dy) || misalign16(a.x) != misalign16(a.dx)) return cudaSuccess;
+  const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
+  if (!grad_plan(vw, a.N, a.S, a.C, a.G, slab, &d.p)) return cudaSuccess;
+  *done = true;
+  const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
+  float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
+#define EP_GN_GRAD_FUSED(T)                                                     \
+  (mode == 0   ? fused_grad<T, 0>(a, d, cpart, stream, launches)                \
+   : mode == 1 ? fused_grad<T, 1>(a, d, cpart, stream, launches)                \
+               : fused_grad<T, 2>(a, d, cpart, stream, launches))
+  switch (a.t) {
+    case DType::F32: return EP_GN_GRAD_FUSED(float);
+    case DType::F16: return EP_GN_GRAD_FUSED(__half);
+    default: return EP_GN_GRAD_FUSED(__nv_bfloat16);
+  }
+#undef EP_GN_GRAD_FUSED
+}
+
+}  // namespace ep
