@@ -14,10 +14,9 @@
 // Split form (this file's general path, any C, S and alignment): the walk of
 // column_walk.cuh over each sample.  Pass 1 leaves (count, mean, sum of squared
 // distances) per chunk and group, a small kernel joins the chunks, pass 2 reads
-// x again (from L2 where it fits) and writes y.  Values are taken relative to
-// the group's first one, and each channel's mean and M2 are carried as Welford's
-// and joined with Chan's formula, so that neither a large mean nor a first
-// value that is far off costs the variance its digits.  The gradient has the same three steps, with per-channel sums of du
+// x again (from L2 where it fits) and writes y.  The statistics are taken
+// relative to values near their mean throughout, so that a large mean costs the
+// variance nothing.  The gradient has the same three steps, with per-channel sums of du
 // and du * h beside the groups' sums.
 //
 // All sums and statistics are float32; results are rounded once, to T.
@@ -34,8 +33,19 @@
 namespace ep {
 namespace {
 
-// One call's sizes, as every kernel of the split form gets them.
-// (C is at most kMaxGroupNormChannels, so positions in a walk row fit an int.)
+// The split kernels' forms:
+//  kAny      any C and alignment: fragments are checked against the sample's
+//            ends, and a sample may start off a 16-byte boundary (VEC: whole
+//            fragments are loaded as 16 bytes; else value by value);
+//  kChannel  C % VW == 0 and 16-byte-aligned operands: every fragment is whole
+//            (and the last walk row may have fewer than the others);
+//  kGroup    and D % VW == 0: a fragment lies in one group, so statistics and
+//            group sums are per fragment, not per channel.
+enum { kAny = 0, kChannel = 1, kGroup = 2 };
+
+// One call's sizes, as every kernel of the split form gets them (C is at most
+// kMaxGroupNormChannels, so positions in a walk row fit an int), for the
+// samples of one launch.
 struct GnDims {
   int64_t N, S, L;  // L = S * C
   int C, G, D;
@@ -44,9 +54,9 @@ struct GnDims {
 };
 
 // Where a sample's walk row starts: `off` elements before the sample.
-template <typename T, bool VEC>
+template <typename T, int FORM, bool VEC>
 __device__ __forceinline__ int walk_offset(const T* sample) {
-  return VEC ? dev::misalignment(sample) : 0;
+  return FORM == kAny && VEC ? dev::misalignment(sample) : 0;
 }
 
 // The channel of the first element of fragment column j.
@@ -66,6 +76,7 @@ __device__ __forceinline__ int first_repeat(int p0, int off, int c0, int D, int 
 // channel c of the group, by the lanes of a warp in turn: the lanes split into
 // sets of the smallest power of two that holds D channels (at most 32), each set
 // taking the repeats in turn, so that few channels still use (and sum over) all lanes.
+// (kGroup: positions are fragments, and C, D, c0 count fragments too.)
 template <typename F>
 __device__ __forceinline__ void for_group(int p0, int np, int off, int c0, int D, int C, F f) {
   const int lane = threadIdx.x & 31;
@@ -81,108 +92,152 @@ __device__ __forceinline__ bool group_in_tile(int p0, int np, int off, int c0, i
   return off + c0 + int64_t(first_repeat(p0, off, c0, D, C)) * C < p0 + np;
 }
 
-// Pass 1.  partial: [item][tile][G] x (count, mean, M2), or, where a sample has
-// one item and one tile, the statistics themselves (partial == nullptr).
-template <typename T, bool VEC>
+// A CTA's place: its tile of the walk row and its thread's fragment column.
+struct Tile {
+  int tile, frags;   // the tile's number and fragments
+  int64_t j;         // fragment column
+  int64_t rows;      // walk rows of a sample that have a fragment j (kAny: all, with checks)
+  bool mine;
+  __device__ __forceinline__ Tile(const WalkPlan& p, int64_t sample_frags) {
+    tile = p.tiles == 1 ? 0 : static_cast<int>(blockIdx.x % unsigned(p.tiles));
+    frags = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags));
+    j = int64_t(tile) * p.tile_frags + threadIdx.x;
+    mine = int(threadIdx.x) < frags;
+    rows = sample_frags < 0 ? p.rows : (sample_frags - j + p.row_frags - 1) / p.row_frags;
+  }
+};
+
+// Pass 1.  partial: [item][tile][G] x (count, mean, M2), relative to the group's
+// first value, or, where a sample has one item and one tile, the statistics
+// themselves (partial == nullptr).  A thread sums its values and their squares
+// relative to the mean of its first U rows, which is near enough to its own mean
+// that nothing cancels; the threads' (count, mean, M2) are joined by two sums,
+// the second relative to the first's mean.
+template <typename T, int FORM>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
   constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = FORM == kGroup ? 1 : VW;  // sums of a thread
   constexpr int U = 4;
-  __shared__ float s_cnt[kWalkThreads * VW], s_mean[kWalkThreads * VW], s_m2[kWalkThreads * VW];
+  __shared__ float s_cnt[kWalkThreads * EV], s_mean[kWalkThreads * EV], s_m2[kWalkThreads * EV];
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
-  const int tile = blockIdx.x % p.tiles;
-  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
-  const bool mine = int(threadIdx.x) < p.tile_frags && j < p.row_frags;
-  const int p0 = tile * p.tile_frags * VW;
-  const int np = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags)) * VW;
+  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
+  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV;
+  const int Cw = FORM == kGroup ? d.C / VW : d.C, Dw = FORM == kGroup ? d.D / VW : d.D;
   const int64_t items = d.N * p.chunks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 
-  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
-    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
+    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
     const T* xs = x + n * d.L;
-    const int off = walk_offset<T, VEC>(xs);
-    if (mine) {
-      float mean[VW], m2[VW], cnt = 0.f, extra[VW], shift[VW];
-      int c = first_channel(j, VW, off, d.C);
+    const int off = walk_offset<T, FORM, true>(xs);
+    if (t.mine) {
+      float first[EV], c[EV], s[EV], q[EV], cnt[EV];
+      for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int, int g) {
+        if (e < EV) first[e] = dev::ld1_keep(xs + int64_t(g) * d.D);
+      });
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        mean[e] = m2[e] = extra[e] = 0.f;
-        shift[e] = dev::ld1_keep(xs + c / d.D * d.D);
-        if (++c == d.C) c = 0;
-      }
-      const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
-      for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-        float v[U][VW];
-        bool whole = r0 + U <= r1;
+      for (int e = 0; e < EV; ++e) s[e] = q[e] = cnt[e] = 0.f;
+      const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
+      const int64_t pitch = p.row_frags * VW;
+      const T* px = xs + (ra * p.row_frags + t.j) * VW;
+      if constexpr (FORM != kAny) {
+        // centre: the first rows' mean
+        if (ra < rb) {
+          float m[EV];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
-          whole = whole && e0 >= 0 && e0 + VW <= d.L;
-          if (r0 + u < r1) {
-            dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+          for (int e = 0; e < EV; ++e) m[e] = 0.f;
+          const int u1 = static_cast<int>(min(int64_t(U), rb - ra));
+          for (int u = 0; u < u1; ++u) {
+            float v[VW];
+            dev::Conv<T>::unpack(dev::ld16_keep(px + u * pitch), v);
 #pragma unroll
-            for (int e = 0; e < VW; ++e) v[u][e] -= shift[e];
+            for (int e = 0; e < VW; ++e) m[EV == 1 ? 0 : e] += v[e] - first[EV == 1 ? 0 : e];
           }
+#pragma unroll
+          for (int e = 0; e < EV; ++e) c[e] = first[e] + m[e] / float(u1 * (VW / EV));
+        } else {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) c[e] = first[e];
         }
-        if (whole) {  // U values of every channel: their mean and M2, joined to the running ones
-          const float tot = cnt + float(U), w = float(U) / tot, cw = cnt * w;
+        auto add = [&](uint4 raw) {
+          float v[VW];
+          dev::Conv<T>::unpack(raw, v);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float mb = ((v[0][e] + v[1][e]) + (v[2][e] + v[3][e])) * (1.0f / U);
-            float q = 0.f;
+          for (int e = 0; e < VW; ++e) v[e] -= c[EV == 1 ? 0 : e];
+          if constexpr (EV == 1) {
+            float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const float t = v[u][e] - mb;
-              q = fmaf(t, t, q);
+            for (int e = 0; e < VW; e += 2) {
+              a += v[e] + v[e + 1];
+              b = fmaf(v[e], v[e], b);
+              q[0] = fmaf(v[e + 1], v[e + 1], q[0]);
             }
-            const float t = mb - mean[e];
-            if (extra[e] == 0.f) {
-              mean[e] = fmaf(t, w, mean[e]);
-              m2[e] += fmaf(t * t, cw, q);
-            } else {
-              const float ce = cnt + extra[e], we = float(U) / (ce + float(U));
-              mean[e] = fmaf(t, we, mean[e]);
-              m2[e] += fmaf(t * t, ce * we, q);
-            }
-          }
-          cnt = tot;
-        } else {  // the ends of a sample: one value at a time
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
+            s[0] += a;
+            q[0] += b;
+          } else {
 #pragma unroll
             for (int e = 0; e < VW; ++e) {
-              if (r0 + u < r1 && e0 + e >= 0 && e0 + e < d.L) {
-                extra[e] += 1.f;
-                const float t = v[u][e] - mean[e];
-                mean[e] += t / (cnt + extra[e]);
-                m2[e] = fmaf(t, v[u][e] - mean[e], m2[e]);
+              s[e] += v[e];
+              q[e] = fmaf(v[e], v[e], q[e]);
+            }
+          }
+        };
+        int64_t r = ra;
+        for (; r + U <= rb; r += U, px += U * pitch) {
+          uint4 raw[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) raw[u] = dev::ld16_keep(px + u * pitch);
+#pragma unroll
+          for (int u = 0; u < U; ++u) add(raw[u]);
+        }
+        for (; r < rb; ++r, px += pitch) add(dev::ld16_keep(px));
+#pragma unroll
+        for (int e = 0; e < EV; ++e) cnt[e] = ra < rb ? float(rb - ra) * (VW / EV) : 0.f;
+      } else {
+        // the centre is the first value a channel meets here
+#pragma unroll
+        for (int e = 0; e < VW; ++e) c[e] = first[e];
+        for (int64_t r0 = ra; r0 < rb; r0 += U) {
+          float v[U][VW];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (r0 + u < rb) dev::load_frag<T, true>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+              if (r0 + u < rb && e0 + e >= 0 && e0 + e < d.L) {
+                if (cnt[e] == 0.f) c[e] = v[u][e];
+                const float w = v[u][e] - c[e];
+                cnt[e] += 1.f;
+                s[e] += w;
+                q[e] = fmaf(w, w, q[e]);
               }
             }
           }
         }
       }
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        s_cnt[threadIdx.x * VW + e] = cnt + extra[e];
-        s_mean[threadIdx.x * VW + e] = mean[e];
-        s_m2[threadIdx.x * VW + e] = m2[e];
+      for (int e = 0; e < EV; ++e) {
+        const float m = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
+        s_cnt[threadIdx.x * EV + e] = cnt[e];
+        s_mean[threadIdx.x * EV + e] = (c[e] - first[e]) + m;
+        s_m2[threadIdx.x * EV + e] = not_negative(q[e] - s[e] * m);
       }
     }
     __syncthreads();
     for (int g = warp; g < d.G; g += warps) {
-      if (p.tiles > 1 && !group_in_tile(p0, np, off, g * d.D, d.D, d.C)) {
-        if (lane == 0) {
-          float* out = partial + ((item * p.tiles + tile) * d.G + g) * 3;
-          out[0] = out[1] = out[2] = 0.f;
-        }
+      float* out = partial + ((item * p.tiles + t.tile) * d.G + g) * 3;
+      if (p.tiles > 1 && !group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
+        if (lane == 0) out[0] = out[1] = out[2] = 0.f;
         continue;
       }
       float c = 0.f, s = 0.f, q = 0.f;
-      for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int) {
+      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
         c += s_cnt[i];
         s = fmaf(s_cnt[i], s_mean[i], s);
       });
@@ -190,21 +245,20 @@ k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out
       s = dev::warp_sum(s);
       const float mg = c > 0.f ? s / c : 0.f;
       float res = 0.f;  // what rounding s / c and the sum left out of the mean
-      for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int) {
-        const float t = s_mean[i] - mg;
-        res = fmaf(s_cnt[i], t, res);
-        q += fmaf(s_cnt[i] * t, t, s_m2[i]);
+      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+        const float w = s_mean[i] - mg;
+        res = fmaf(s_cnt[i], w, res);
+        q += fmaf(s_cnt[i] * w, w, s_m2[i]);
       });
       res = dev::warp_sum(res);
       q = dev::warp_sum(q);
       if (lane == 0) {
         const float fix = c > 0.f ? res / c : 0.f;
-        const float mf = mg + fix, m2g = fmaxf(0.f, q - res * fix);
+        const float mf = mg + fix, m2g = not_negative(q - res * fix);
         if (partial == nullptr) {
-          mean_out[n * d.G + g] = dev::ld1_keep(xs + g * d.D) + mf;
+          mean_out[n * d.G + g] = dev::ld1_keep(xs + int64_t(g) * d.D) + mf;
           inv_out[n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
         } else {
-          float* out = partial + ((item * p.tiles + tile) * d.G + g) * 3;
           out[0] = c;
           out[1] = mf;
           out[2] = m2g;
@@ -226,79 +280,133 @@ k_gn_join(const T* x, const float* partial, GnDims d, float* mean_out, float* in
   for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
     const float* src = partial + ((i / d.G) * parts * d.G + i % d.G) * 3;
     float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
+#pragma unroll 4
     for (int64_t k = lane; k < parts; k += 32) {
       const float* e = src + k * d.G * 3;
-      c += __ldcg(e);
-      s = fmaf(__ldcg(e), __ldcg(e + 1), s);
+      const float n = __ldcg(e);
+      c += n;
+      s = fmaf(n, __ldcg(e + 1), s);
     }
     c = dev::warp_sum(c);
     s = dev::warp_sum(s);
     const float mg = s / c;
+#pragma unroll 4
     for (int64_t k = lane; k < parts; k += 32) {
       const float* e = src + k * d.G * 3;
-      const float t = __ldcg(e + 1) - mg, n = __ldcg(e);
-      res = fmaf(n, t, res);
-      q += fmaf(n * t, t, __ldcg(e + 2));
+      const float w = __ldcg(e + 1) - mg, n = __ldcg(e);
+      res = fmaf(n, w, res);
+      q += fmaf(n * w, w, __ldcg(e + 2));
     }
     res = dev::warp_sum(res);
     q = dev::warp_sum(q);
     if (lane == 0) {
       const float fix = res / c;
       mean_out[i] = dev::ld1_keep(x + i / d.G * d.L + i % d.G * d.D) + (mg + fix);
-      inv_out[i] = 1.0f / sqrtf(fmaxf(0.f, q - res * fix) / c + d.eps);
+      inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
     }
   }
 }
 
-// Pass 2: y from x and the statistics.
-template <typename T, bool VEC, bool SILU>
+// Pass 2: y from x and the statistics.  Bound by the data where x comes from DRAM.
+template <typename T, int FORM, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean, const float* inv,
            T* y, GnDims d) {
   constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = FORM == kGroup ? 1 : VW;
   constexpr int U = 4;
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
-  const int tile = blockIdx.x % p.tiles;
-  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
-  if (int(threadIdx.x) >= p.tile_frags || j >= p.row_frags) return;
+  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
+  if (!t.mine) return;
   const int64_t items = d.N * p.chunks;
-  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
-    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
+    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
     const T* xs = x + n * d.L;
     T* ys = y + n * d.L;
-    const int off = walk_offset<T, VEC>(xs);
-    float mu[VW], a[VW], b[VW];
-    int c = first_channel(j, VW, off, d.C);
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      const int64_t g = n * d.G + c / d.D;
-      mu[e] = mean[g];
-      a[e] = inv[g] * dev::ld1_keep(gamma + c);
+    const int off = walk_offset<T, FORM, VEC>(xs);
+    float mu[EV], a[VW], b[VW];
+    for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int c, int g) {
+      if (e < EV) mu[e] = mean[n * d.G + g];
+      a[e] = inv[n * d.G + g] * dev::ld1_keep(gamma + c);
       b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-      if (++c == d.C) c = 0;
-    }
-    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
-    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-      float v[U][VW];
+    });
+    auto value = [&](float (&v)[VW]) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r0 + u < r1) dev::load_frag<T, VEC>(xs, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
+      for (int e = 0; e < VW; ++e) {
+        v[e] = fmaf(v[e] - mu[EV == 1 ? 0 : e], a[e], b[e]);
+        if constexpr (SILU) v[e] = silu<T>(v[e]);
+      }
+    };
+    const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
+    if constexpr (FORM != kAny) {
+      const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
+      const T* px = xs + at;
+      T* py = ys + at;
+      int64_t r = ra;
+      for (; r + U <= rb; r += U, px += U * pitch, py += U * pitch) {
+        uint4 raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 + u < r1) {
+        for (int u = 0; u < U; ++u) raw[u] = dev::ld16_stream(px + u * pitch);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float w = fmaf(v[u][e] - mu[e], a[e], b[e]);
-            v[u][e] = SILU ? silu<T>(w) : w;
+        for (int u = 0; u < U; ++u) {
+          float v[VW];
+          dev::Conv<T>::unpack(raw[u], v);
+          value(v);
+          dev::st16_stream(py + u * pitch, dev::Conv<T>::pack(v));
+        }
+      }
+      for (; r < rb; ++r, px += pitch, py += pitch) {
+        float v[VW];
+        dev::Conv<T>::unpack(dev::ld16_stream(px), v);
+        value(v);
+        dev::st16_stream(py, dev::Conv<T>::pack(v));
+      }
+    } else {
+      for (int64_t r0 = ra; r0 < rb; r0 += U) {
+        float v[U][VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (r0 + u < rb) dev::load_frag<T, VEC>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (r0 + u < rb) {
+            value(v[u]);
+            dev::store_frag<T, VEC>(ys, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
           }
-          dev::store_frag<T, VEC>(ys, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
         }
       }
     }
   }
 }
+
+// What the gradient's passes make of x and dy: h and du, with a thread's channel
+// values in registers.
+template <typename T, int EV, bool SILU>
+struct GradValues {
+  static constexpr int VW = dev::Vec16<T>::N;
+  float mu[EV], rs[EV], ga[VW], be[VW];
+  __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
+                                       const T* __restrict__ beta, const float* mean, const float* inv) {
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
+      if (e < EV) {
+        mu[e] = mean[ng + g];
+        rs[e] = inv[ng + g];
+      }
+      ga[e] = dev::ld1_keep(gamma + c);
+      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+    });
+  }
+  // x -> h, dy -> du
+  __device__ __forceinline__ void operator()(float (&v)[VW], float (&w)[VW]) const {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      v[e] = (v[e] - mu[EV == 1 ? 0 : e]) * rs[EV == 1 ? 0 : e];
+      if constexpr (SILU) w[e] = silu_grad<T>(w[e], fmaf(v[e], ga[e], be[e]));
+    }
+  }
+};
 
 // Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
 // groups' sums of each item.  A CTA's items share `off` (the launch sees to
@@ -306,22 +414,22 @@ k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
 //   gpart: [item][tile][G] x (sum du gamma, sum du gamma h)
 //   cpart: 2 x [CTA row][C] (one tile) or 2 x [CTA row][walk row], position 0
 //          being channel 0
-template <typename T, bool VEC, bool SILU>
+template <typename T, int FORM, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                const float* inv, GnDims d, float* gpart, float* cpart) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int U = 2;
+  constexpr int EV = FORM == kGroup ? 1 : VW;
+  constexpr int U = sizeof(T) == 4 ? 4 : 2;
   __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
-  const int tile = blockIdx.x % p.tiles;
-  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
-  const bool mine = int(threadIdx.x) < p.tile_frags && j < p.row_frags;
-  const int p0 = tile * p.tile_frags * VW;
-  const int np = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags)) * VW;
-  const int64_t items = d.N * p.chunks, cta_rows = gridDim.x / p.tiles, cta_row = blockIdx.x / p.tiles;
+  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
+  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV;
+  const int Cw = FORM == kGroup ? d.C / VW : d.C, Dw = FORM == kGroup ? d.D / VW : d.D;
+  const int64_t items = d.N * p.chunks;
+  const int cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   float tot_a[VW], tot_b[VW];
 #pragma unroll
@@ -329,51 +437,78 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
   int off = 0;
 
   for (int64_t item = cta_row; item < items; item += cta_rows) {
-    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
     const T* xs = x + n * d.L;
     const T* ds = dy + n * d.L;
-    off = walk_offset<T, VEC>(xs);
-    if (mine) {
-      float mu[VW], rs[VW], ga[VW], be[VW], sa[VW], sb[VW];
-      int c = first_channel(j, VW, off, d.C);
+    off = walk_offset<T, FORM, VEC>(xs);
+    if (t.mine) {
+      GradValues<T, EV, SILU> val;
+      val.load(first_channel(t.j, VW, off, d.C), n * d.G, d, gamma, beta, mean, inv);
+      float sa[VW], sb[VW];
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const int64_t g = n * d.G + c / d.D;
-        mu[e] = mean[g];
-        rs[e] = inv[g];
-        ga[e] = SILU ? dev::ld1_keep(gamma + c) : 1.f;
-        be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-        sa[e] = sb[e] = 0.f;
-        if (++c == d.C) c = 0;
-      }
-      const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
-      for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-        float v[U][VW], w[U][VW];
+      for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
+      auto add = [&](float (&v)[VW], float (&w)[VW]) {
+        val(v, w);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
-          if (r0 + u < r1) {
-            dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
-            dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);  // 0 outside the sample: adds nothing
+        for (int e = 0; e < VW; ++e) {
+          sa[e] += w[e];
+          sb[e] = fmaf(w[e], v[e], sb[e]);
+        }
+      };
+      const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
+      if constexpr (FORM != kAny) {
+        const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
+        const T* px = xs + at;
+        const T* pd = ds + at;
+        int64_t r = ra;
+        for (; r + U <= rb; r += U, px += U * pitch, pd += U * pitch) {
+          uint4 rx[U], rd[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            rx[u] = dev::ld16_keep(px + u * pitch);
+            rd[u] = dev::ld16_keep(pd + u * pitch);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[VW], w[VW];
+            dev::Conv<T>::unpack(rx[u], v);
+            dev::Conv<T>::unpack(rd[u], w);
+            add(v, w);
           }
         }
+        for (; r < rb; ++r, px += pitch, pd += pitch) {
+          float v[VW], w[VW];
+          dev::Conv<T>::unpack(dev::ld16_keep(px), v);
+          dev::Conv<T>::unpack(dev::ld16_keep(pd), w);
+          add(v, w);
+        }
+      } else {
+        for (int64_t r = ra; r < rb; ++r) {
+          const int64_t e0 = (r * p.row_frags + t.j) * VW - off;
+          float v[VW], w[VW];
+          dev::load_frag<T, VEC>(xs, e0, d.L, v);
+          dev::load_frag<T, VEC>(ds, e0, d.L, w);  // 0 outside the sample: adds nothing
+          add(v, w);
+        }
+      }
+      if constexpr (FORM == kGroup) {
+        float a = 0.f, b = 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (r0 + u < r1) {
+        for (int e = 0; e < VW; ++e) {
+          a = fmaf(sa[e], val.ga[e], a);
+          b = fmaf(sb[e], val.ga[e], b);
+        }
+        s_a[threadIdx.x] = a;
+        s_b[threadIdx.x] = b;
+      } else {
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              const float h = (v[u][e] - mu[e]) * rs[e];
-              const float du = act_grad<T, SILU>(w[u][e], fmaf(h, ga[e], be[e]));
-              sa[e] += du;
-              sb[e] = fmaf(du, h, sb[e]);
-            }
-          }
+        for (int e = 0; e < VW; ++e) {
+          s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
+          s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
         }
       }
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        s_a[threadIdx.x * VW + e] = sa[e];
-        s_b[threadIdx.x * VW + e] = sb[e];
         tot_a[e] += sa[e];
         tot_b[e] += sb[e];
       }
@@ -381,17 +516,16 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
     __syncthreads();
     for (int g = warp; g < d.G; g += warps) {
       float a = 0.f, b = 0.f;
-      if (p.tiles == 1 || group_in_tile(p0, np, off, g * d.D, d.D, d.C)) {
-        for_group(p0, np, off, g * d.D, d.D, d.C, [&](int i, int c) {
-          const float gm = dev::ld1_keep(gamma + c);
-          a = fmaf(gm, s_a[i], a);
-          b = fmaf(gm, s_b[i], b);
+      if (p.tiles == 1 || group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
+        for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+          a += s_a[i];
+          b += s_b[i];
         });
         a = dev::warp_sum(a);
         b = dev::warp_sum(b);
       }
       if (lane == 0) {
-        float* out = gpart + ((item * p.tiles + tile) * d.G + g) * 2;
+        float* out = gpart + ((item * p.tiles + t.tile) * d.G + g) * 2;
         out[0] = a;
         out[1] = b;
       }
@@ -400,20 +534,21 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
   }
   if (cpart == nullptr) return;
   if (p.tiles > 1) {
-    if (mine) {
+    if (t.mine) {
       const int64_t P = p.row_frags * VW;
       float* oa = cpart + cta_row * P;
       float* ob = oa + cta_rows * P;
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const int64_t q = (j * VW + e + P - off) % P;
+        int64_t q = t.j * VW + e - off;
+        if (q < 0) q += P;
         oa[q] = tot_a[e];
         ob[q] = tot_b[e];
       }
     }
     return;
   }
-  if (mine) {
+  if (t.mine) {
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
       s_a[threadIdx.x * VW + e] = tot_a[e];
@@ -421,14 +556,14 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
     }
   }
   __syncthreads();
-  const int c32 = d.C, reps = static_cast<int>(p.reps), P = np;
-  float* oa = cpart + cta_row * d.C;
-  float* ob = oa + cta_rows * d.C;
+  const int reps = static_cast<int>(p.reps), P = t.frags * VW;
+  float* oa = cpart + int64_t(cta_row) * d.C;
+  float* ob = oa + int64_t(cta_rows) * d.C;
   if (reps <= 16) {
-    for (int c = threadIdx.x; c < c32; c += blockDim.x) {
+    for (int c = threadIdx.x; c < d.C; c += blockDim.x) {
       float a = 0.f, b = 0.f;
       for (int k = 0; k < reps; ++k) {
-        int q = c + off + k * c32;
+        int q = c + off + k * d.C;
         if (q >= P) q -= P;
         a += s_a[q];
         b += s_b[q];
@@ -437,10 +572,10 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
       ob[c] = b;
     }
   } else {
-    for (int c = warp; c < c32; c += warps) {
+    for (int c = warp; c < d.C; c += warps) {
       float a = 0.f, b = 0.f;
       for (int k = lane; k < reps; k += 32) {
-        int q = c + off + k * c32;
+        int q = c + off + k * d.C;
         if (q >= P) q -= P;
         a += s_a[q];
         b += s_b[q];
@@ -464,11 +599,13 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
   const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
   const float scale = 1.0f / (float(d.S) * float(d.D));
   for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
-    const float* src = gpart + ((i / d.G) * parts * d.G + i % d.G) * 2;
+    const float2* src = reinterpret_cast<const float2*>(gpart) + (i / d.G) * parts * d.G + i % d.G;
     float a = 0.f, b = 0.f;
+#pragma unroll 4
     for (int64_t k = lane; k < parts; k += 32) {
-      a += __ldcg(src + k * d.G * 2);
-      b += __ldcg(src + k * d.G * 2 + 1);
+      const float2 v = __ldcg(src + k * d.G);
+      a += v.x;
+      b += v.y;
     }
     a = dev::warp_sum(a);
     b = dev::warp_sum(b);
@@ -480,60 +617,81 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
 }
 
 // Gradient, pass 2: dx.
-template <typename T, bool VEC, bool SILU>
+template <typename T, int FORM, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                 const float* inv, const float* m1, const float* m2, T* dx, GnDims d) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int U = 2;
+  constexpr int EV = FORM == kGroup ? 1 : VW;
+  constexpr int U = sizeof(T) == 4 ? 4 : 2;
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
-  const int tile = blockIdx.x % p.tiles;
-  const int64_t j = int64_t(tile) * p.tile_frags + threadIdx.x;
-  if (int(threadIdx.x) >= p.tile_frags || j >= p.row_frags) return;
+  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
+  if (!t.mine) return;
   const int64_t items = d.N * p.chunks;
-  for (int64_t item = blockIdx.x / p.tiles; item < items; item += gridDim.x / p.tiles) {
-    const int64_t n = item / p.chunks, chunk = item % p.chunks;
+  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
+    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
     const T* xs = x + n * d.L;
     const T* ds = dy + n * d.L;
     T* os = dx + n * d.L;
-    const int off = walk_offset<T, VEC>(xs);
-    float mu[VW], rs[VW], ga[VW], be[VW], a1[VW], a2[VW];
-    int c = first_channel(j, VW, off, d.C);
+    const int off = walk_offset<T, FORM, VEC>(xs);
+    const int c0 = first_channel(t.j, VW, off, d.C);
+    GradValues<T, EV, SILU> val;
+    val.load(c0, n * d.G, d, gamma, beta, mean, inv);
+    float a1[EV], a2[EV];
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
+      if (e < EV) {
+        a1[e] = __ldcg(m1 + n * d.G + g);
+        a2[e] = __ldcg(m2 + n * d.G + g);
+      }
+    });
+    auto value = [&](float (&v)[VW], float (&w)[VW]) {  // x, dy -> dx in v
+      val(v, w);
 #pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      const int64_t g = n * d.G + c / d.D;
-      mu[e] = mean[g];
-      rs[e] = inv[g];
-      ga[e] = dev::ld1_keep(gamma + c);
-      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-      a1[e] = __ldcg(m1 + g);
-      a2[e] = __ldcg(m2 + g);
-      if (++c == d.C) c = 0;
-    }
-    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
-    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-      float v[U][VW], w[U][VW];
+      for (int e = 0; e < VW; ++e) {
+        const int i = EV == 1 ? 0 : e;
+        v[e] = val.rs[i] * (fmaf(w[e], val.ga[e], -a1[i]) - v[e] * a2[i]);
+      }
+    };
+    const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
+    if constexpr (FORM != kAny) {
+      const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
+      const T* px = xs + at;
+      const T* pd = ds + at;
+      T* po = os + at;
+      int64_t r = ra;
+      for (; r + U <= rb; r += U, px += U * pitch, pd += U * pitch, po += U * pitch) {
+        uint4 rx[U], rd[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t e0 = ((r0 + u) * p.row_frags + j) * VW - off;
-        if (r0 + u < r1) {
-          dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
-          dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);
+        for (int u = 0; u < U; ++u) {
+          rx[u] = dev::ld16_stream(px + u * pitch);
+          rd[u] = dev::ld16_stream(pd + u * pitch);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[VW], w[VW];
+          dev::Conv<T>::unpack(rx[u], v);
+          dev::Conv<T>::unpack(rd[u], w);
+          value(v, w);
+          dev::st16_stream(po + u * pitch, dev::Conv<T>::pack(v));
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 + u < r1) {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float h = (v[u][e] - mu[e]) * rs[e];
-            const float du = act_grad<T, SILU>(w[u][e], fmaf(h, ga[e], be[e]));
-            v[u][e] = rs[e] * (fmaf(du, ga[e], -a1[e]) - h * a2[e]);
-          }
-          dev::store_frag<T, VEC>(os, ((r0 + u) * p.row_frags + j) * VW - off, d.L, v[u]);
-        }
+      for (; r < rb; ++r, px += pitch, pd += pitch, po += pitch) {
+        float v[VW], w[VW];
+        dev::Conv<T>::unpack(dev::ld16_stream(px), v);
+        dev::Conv<T>::unpack(dev::ld16_stream(pd), w);
+        value(v, w);
+        dev::st16_stream(po, dev::Conv<T>::pack(v));
+      }
+    } else {
+      for (int64_t r = ra; r < rb; ++r) {
+        const int64_t e0 = (r * p.row_frags + t.j) * VW - off;
+        float v[VW], w[VW];
+        dev::load_frag<T, VEC>(xs, e0, d.L, v);
+        dev::load_frag<T, VEC>(ds, e0, d.L, w);
+        value(v, w);
+        dev::store_frag<T, VEC>(os, e0, d.L, v);
       }
     }
   }
@@ -605,9 +763,10 @@ cudaError_t group_norm_t(const GroupNormArgs& a, int sm_count, cudaStream_t stre
   const T* beta = static_cast<const T*>(a.beta);
   T* y = static_cast<T*>(a.y);
   const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles)), block(d.p.threads);
-  const bool vec = misalign16(x) == misalign16(y);
-  // statistics need no alignment of y
-  cudaError_t e = launch(k_gn_stats<T, true>, grid, block, 0, stream, x, d, partial, mean, inv);
+  const int whole = a.C % dev::Vec16<T>::N == 0 ? (d.D % dev::Vec16<T>::N == 0 ? kGroup : kChannel) : kAny;
+  const int form1 = misalign16(x) == 0 ? whole : kAny;  // statistics need no alignment of y
+  auto f1 = form1 == kGroup ? k_gn_stats<T, kGroup> : form1 == kChannel ? k_gn_stats<T, kChannel> : k_gn_stats<T, kAny>;
+  cudaError_t e = launch(f1, grid, block, 0, stream, x, d, partial, mean, inv);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (partial != nullptr) {
@@ -615,8 +774,15 @@ cudaError_t group_norm_t(const GroupNormArgs& a, int sm_count, cudaStream_t stre
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
-  auto fn = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
-                : (a.silu ? k_gn_apply<T, false, true> : k_gn_apply<T, false, false>);
+  const bool vec = misalign16(x) == misalign16(y);
+  auto pick = [&](auto silu) {
+    constexpr bool kSilu = decltype(silu)::value;
+    if (!vec) return k_gn_apply<T, kAny, false, kSilu>;
+    return form1 == kGroup     ? k_gn_apply<T, kGroup, true, kSilu>
+           : form1 == kChannel ? k_gn_apply<T, kChannel, true, kSilu>
+                               : k_gn_apply<T, kAny, true, kSilu>;
+  };
+  auto fn = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
   e = launch(fn, grid, block, 0, stream, x, gamma, beta, mean, inv, y, d);
   if (e == cudaSuccess) *launches += 1;
   return e;
@@ -643,8 +809,15 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, int sm_count, cudaStre
   const bool one_off = d.L % VW == 0 || rows >= d.N * d.p.chunks;
   const bool vec1 = misalign16(x) == misalign16(dy) && one_off;
   const bool vec2 = misalign16(x) == misalign16(dy) && misalign16(x) == misalign16(dx);
-  auto f1 = vec1 ? (a.silu ? k_gn_grad_sums<T, true, true> : k_gn_grad_sums<T, true, false>)
-                 : (a.silu ? k_gn_grad_sums<T, false, true> : k_gn_grad_sums<T, false, false>);
+  const int whole = misalign16(x) != 0 || a.C % VW != 0 ? kAny : d.D % VW == 0 ? kGroup : kChannel;
+  auto pick1 = [&](auto silu) {
+    constexpr bool kSilu = decltype(silu)::value;
+    if (!vec1) return k_gn_grad_sums<T, kAny, false, kSilu>;
+    return whole == kGroup     ? k_gn_grad_sums<T, kGroup, true, kSilu>
+           : whole == kChannel ? k_gn_grad_sums<T, kChannel, true, kSilu>
+                               : k_gn_grad_sums<T, kAny, true, kSilu>;
+  };
+  auto f1 = a.silu ? pick1(std::true_type{}) : pick1(std::false_type{});
   cudaError_t e = launch(f1, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean,
                          a.inv, d, gpart, cpart);
   if (e != cudaSuccess) return e;
@@ -652,8 +825,14 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, int sm_count, cudaStre
   e = launch(k_gn_grad_join, dim3(join_grid(d)), dim3(256), 0, stream, gpart, d, m1, m2);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  auto f2 = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
-                 : (a.silu ? k_gn_grad_apply<T, false, true> : k_gn_grad_apply<T, false, false>);
+  auto pick2 = [&](auto silu) {
+    constexpr bool kSilu = decltype(silu)::value;
+    if (!vec2) return k_gn_grad_apply<T, kAny, false, kSilu>;
+    return whole == kGroup     ? k_gn_grad_apply<T, kGroup, true, kSilu>
+           : whole == kChannel ? k_gn_grad_apply<T, kChannel, true, kSilu>
+                               : k_gn_grad_apply<T, kAny, true, kSilu>;
+  };
+  auto f2 = a.silu ? pick2(std::true_type{}) : pick2(std::false_type{});
   const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles));
   e = launch(f2, grid, dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
   if (e != cudaSuccess) return e;

@@ -10,29 +10,61 @@
 
 namespace ep {
 
-// u * sigmoid(u).  float32: the library exponential and a rounded division.
-// 16-bit results: 2^x and 1/x by the hardware approximations, whose errors (a
-// few float32 ulp) are far below the result's rounding; below u = -88.7 the
-// exponential overflows and the result, above -1e-36, is -0.
+// sigmoid(u) = 1 / (1 + e^-u).
+//  float32: e^-u = 2^p (1 + c), p = -u log2(e) rounded and c what the rounding
+//  and log2(e)'s own left out, times ln 2; the reciprocal by the hardware's
+//  approximation and one Newton step: within 3 float32 ulp.  u is held in
+//  [-87, 100], where nothing overflows: below, sigmoid is e^-87 = 1.6e-38.
+//  16-bit results: 2^x and 1/x by the hardware approximations with p rounded,
+//  errors of a few float32 ulp and |u| 2^-24, far below the results' rounding;
+//  from u = -88.7 down 2^p overflows and sigmoid(u) is 0.
 template <typename T>
-__device__ __forceinline__ float silu(float u) {
-  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(u, 1.0f + expf(-u));
-  else return u * dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
+__device__ __forceinline__ float sigmoid(float u) {
+  if constexpr (std::is_same_v<T, float>) {
+    constexpr float kL = 1.44269502162933349609375f;  // log2(e) rounded to float32
+    constexpr float kLlo = 1.92596298909109e-08f;     // log2(e) - kL
+    constexpr float kLn2 = 0.6931471805599453f;
+    const float t = fmaxf(fminf(-u, 87.f), -100.f);
+    const float p = __fmul_rn(t, kL);
+    const float c = fmaf(t, kL, -p) + t * kLlo;
+    const float e = dev::ex2_approx(p);
+    const float d = 1.0f + fmaf(e * c, kLn2, e);
+    const float r = dev::rcp_approx(d);
+    return fmaf(r, fmaf(-d, r, 1.0f), r);
+  } else {
+    return dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ float sigmoid(float u) {
-  if constexpr (std::is_same_v<T, float>) return __fdiv_rn(1.0f, 1.0f + expf(-u));
-  else return dev::rcp_approx(1.0f + dev::ex2_approx(u * -dev::kLog2e));
+__device__ __forceinline__ float silu(float u) {
+  return u * sigmoid<T>(u);
 }
 
 // du of the definition.
-template <typename T, bool SILU>
-__device__ __forceinline__ float act_grad(float dy, float u) {
-  if constexpr (!SILU) return dy;
+template <typename T>
+__device__ __forceinline__ float silu_grad(float dy, float u) {
   const float s = sigmoid<T>(u);
   return dy * (s * fmaf(u, 1.0f - s, 1.0f));
 }
+
+// f(e, c, g) for the channels c (and their groups g) of the VW elements from c on, modulo C.
+template <int VW, typename F>
+__device__ __forceinline__ void for_channels(int c, int C, int D, F f) {
+  int g = c / D, in = c - g * D;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    f(e, c, g);
+    if (++in == D) {
+      in = 0;
+      ++g;
+    }
+    if (++c == C) c = g = in = 0;
+  }
+}
+
+// A sum of squares that rounding took below zero is 0 (and NaN stays NaN).
+__device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : q; }
 
 // The fused form (group_norm_fused.cu): a sample's slab of channels stays on
 // chip between the statistics and the result.  *done says whether the shape and

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <climits>
 #include <numeric>
+#include <type_traits>
 
 #include "column_walk.cuh"
 #include "device_common.cuh"
@@ -55,6 +56,7 @@ struct FusedDims {
   int C, G, D;
   float eps;
   bool silu;
+  bool pvec;          // gamma and beta 16-byte aligned
   FusedPlan p;
 };
 
@@ -70,11 +72,13 @@ struct Place {
   int kn;          // its fragments
   int slab;
 
-  __device__ __forceinline__ Place(const FusedDims& d, const T* x, int64_t item, int rank, int trow, int tcol) {
+  __device__ __forceinline__ Place(const FusedDims& d, const T* x, unsigned item, int rank, int trow, int tcol,
+                                   int ns) {
     const FusedPlan& p = d.p;
-    slab = MODE == 2 ? 0 : static_cast<int>(item % p.slabs);
-    const int ns = trow / p.per_sample, ph = trow - ns * p.per_sample;
-    n = (MODE == 2 ? item : item / p.slabs) * p.samples + ns;
+    const unsigned block = p.slabs == 1 ? item : item / unsigned(p.slabs);
+    slab = static_cast<int>(item - block * unsigned(p.slabs));
+    const int ph = trow - ns * p.per_sample;
+    n = int64_t(block) * p.samples + ns;
     const bool live = trow < p.phases && n < d.N;
     off = MODE == 2 && live ? dev::misalignment(x + n * d.L) : 0;
     const int64_t row = MODE == 2 ? int64_t(p.cf) * VW : d.C;
@@ -119,19 +123,21 @@ __device__ __forceinline__ float4 ld_rank(const float4* p, int rank) {
 }
 
 // Sums over the entries of each (sample, group) of a block.  Entries are floats
-// (or pairs) by position: fragment (MODE 0) or element; the group's are at
+// by position: fragment (MODE 0) or element; the group's are at
 // off + g De + j + k Cw, j < De, modulo the np positions of a sample (the
 // positions before `off` hold the channels that the last repeat misses).  A set
-// of lanes, the smallest power of two that holds a group's entries, takes one
-// (sample, group) at a time.
+// of lanes takes one (sample, group) at a time: `cols` lanes (a power of two)
+// side by side over j, and as many repeats k next to each other as fit a warp.
 struct Gather {
-  int De, Cw, np, entries, set, q, slots;
+  int De, Cw, np, reps, cols, set, q, slots;
   __device__ __forceinline__ Gather(const FusedPlan& p, int D, int VW, bool frags) {
     De = frags ? D / VW : D;
     Cw = frags ? p.cf : p.W;
     np = p.per_sample * p.cf * (frags ? 1 : VW);
-    entries = np / Cw * De;
-    set = entries >= 32 ? 32 : entries <= 1 ? 1 : 1 << (32 - __clz(entries - 1));
+    reps = np / Cw;
+    cols = De >= 32 ? 32 : De <= 1 ? 1 : 1 << (32 - __clz(De - 1));
+    const int rows = reps <= 1 ? 1 : 1 << (32 - __clz(reps - 1));
+    set = min(32, cols * rows);
     q = p.q;
     slots = p.samples * p.q;
   }
@@ -139,26 +145,50 @@ struct Gather {
   template <typename OFF, typename ADD, typename DONE>
   __device__ __forceinline__ void run(OFF off_of, ADD add, DONE done) const {
     const int sets = blockDim.x / set, l = threadIdx.x & (set - 1);
+    const int j0 = l & (cols - 1), k0 = l / cols, ks = set / cols;
     for (int s0 = 0; s0 < slots; s0 += sets) {
       const int s = s0 + threadIdx.x / set;
       float a = 0.f, b = 0.f;
       if (s < slots) {
-        const int ns = s / q, start = off_of(ns) + (s - ns * q) * De;
-        for (int i = l; i < entries; i += set) {
-          const int k = i / De;
-          int pos = start + (i - k * De) + k * Cw;
-          if (pos >= np) pos -= np;
-          add(ns * np + pos, a, b);
+        const int ns = slots == q ? 0 : s / q, start = off_of(ns) + (s - ns * q) * De;
+        for (int k = k0; k < reps; k += ks) {
+          for (int j = j0; j < De; j += cols) {
+            int pos = start + j + k * Cw;
+            if (pos >= np) pos -= np;
+            add(ns * np + pos, a, b);
+          }
         }
       }
       for (int o = set >> 1; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
         b += __shfl_xor_sync(0xffffffffu, b, o);
       }
-      if (s < slots && l == 0) done(s, a, b);
+      if (s < slots && l == 0) done(s, ns_of(s), a, b);
     }
   }
+  __device__ __forceinline__ int ns_of(int s) const { return slots == q ? 0 : s / q; }
 };
+
+// gamma and beta of VW channels from c on (modulo W), which start at `from`.
+template <typename T, bool WRAP>
+__device__ __forceinline__ void load_params(const T* __restrict__ gamma, const T* __restrict__ beta, int from, int c,
+                                            int W, bool vec, float (&a)[dev::Vec16<T>::N],
+                                            float (&b)[dev::Vec16<T>::N]) {
+  constexpr int VW = dev::Vec16<T>::N;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) b[e] = 0.f;
+  if (!WRAP && vec) {
+    dev::Conv<T>::unpack(dev::ld16_keep(gamma + from + c), a);
+    if (beta != nullptr) dev::Conv<T>::unpack(dev::ld16_keep(beta + from + c), b);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      a[e] = dev::ld1_keep(gamma + from + c);
+      if (beta != nullptr) b[e] = dev::ld1_keep(beta + from + c);
+      if (++c == W) c = 0;
+    }
+  }
+}
 
 // Joins the cluster's values of each slot: f(slot, lane's rank value or 0).
 template <typename F>
@@ -169,6 +199,38 @@ __device__ __forceinline__ void for_slots_by_rank(int slots, int cluster, F f) {
 __device__ __forceinline__ float set_sum(float x, int set) {
   for (int o = set >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+
+// A thread's sums of its values' distances from a centre, or of their squares.
+template <typename T, int NV, int MODE, bool SQUARE>
+__device__ __forceinline__ void centred_sums(const uint4 (&raw)[NV], const Place<T, MODE>& at,
+                                             const float (&c)[MODE == 0 ? 1 : dev::Vec16<T>::N],
+                                             float (&s)[MODE == 0 ? 1 : dev::Vec16<T>::N]) {
+  constexpr int VW = dev::Vec16<T>::N;
+#pragma unroll
+  for (int e = 0; e < (MODE == 0 ? 1 : VW); ++e) s[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    if (k < at.kn) {
+      float v[VW];
+      dev::Conv<T>::unpack(raw[k], v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) v[e] -= c[MODE == 0 ? 0 : e];
+      if (MODE == 2 && !at.whole(k)) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) v[e] = at.inside(k, e) ? v[e] : 0.f;
+      }
+      if constexpr (MODE == 0) {
+        float a[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < VW; ++e) a[e & 1] = SQUARE ? fmaf(v[e], v[e], a[e & 1]) : a[e & 1] + v[e];
+        s[0] += a[0] + a[1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) s[e] = SQUARE ? fmaf(v[e], v[e], s[e]) : s[e] + v[e];
+      }
+    }
+  }
 }
 
 template <typename T, int NV, int MODE>
@@ -186,14 +248,14 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float* gk = cnt + (MODE == 2 ? ents : 0);                      // the group's first value
   float* gm = gk + slots;
   float* gr = gm + slots;
-  const int rank = blockIdx.x % p.cluster;
-  const int64_t item = blockIdx.x / p.cluster;
-  const int trow = threadIdx.x / p.cf, tcol = threadIdx.x - trow * p.cf;
-  const int ns = trow / p.per_sample;
+  const int rank = blockIdx.x & (p.cluster - 1);
+  const unsigned item = blockIdx.x / unsigned(p.cluster);
+  const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
+  const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   dev::pdl_wait();
   dev::pdl_trigger();
 
-  const Place<T, MODE> at(d, x, item, rank, trow, tcol);
+  const Place<T, MODE> at(d, x, item, rank, trow, tcol, ns);
   const T* xs = x + (at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0);
   uint4 raw[NV];
 #pragma unroll
@@ -204,47 +266,16 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   int c0 = MODE == 2 ? (tcol * VW + p.W - at.off % p.W) % p.W : tcol * VW;
   int grp[EV];
   float shift[EV];
-  {
-    int c = c0;
-#pragma unroll
-    for (int e = 0; e < EV; ++e) {
-      const int g = c / d.D;
+  for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
+    if (e < EV) {
       grp[e] = ns * p.q + g;
       shift[e] = at.kn > 0 ? dev::ld1_stream(xs + g * d.D) : 0.f;
-      if (++c == p.W) c = 0;
     }
-  }
+  });
 
-  // sums relative to the shift, then squares relative to the block's mean
   const bool mine = trow < p.phases;
-  auto pass = [&](const float (&m)[EV], bool square, float (&s)[EV]) {
-#pragma unroll
-    for (int e = 0; e < EV; ++e) s[e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (k < at.kn) {
-        float v[VW];
-        dev::Conv<T>::unpack(raw[k], v);
-        const bool whole = at.whole(k);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          const int i = MODE == 0 ? 0 : e;
-          v[e] = (v[e] - shift[i]) - (square ? m[i] : 0.f);
-          if (!whole && !at.inside(k, e)) v[e] = 0.f;
-          if (square) v[e] *= v[e];
-        }
-        if constexpr (MODE == 0) {
-          if constexpr (VW == 8) s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-          else s[0] += (v[0] + v[1]) + (v[2] + v[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) s[e] += v[e];
-        }
-      }
-    }
-  };
   const Gather gather(p, d.D, VW, MODE == 0);
-  const int64_t n0 = (MODE == 2 ? item : item / p.slabs) * p.samples;
+  const int64_t n0 = int64_t(p.slabs == 1 ? item : item / unsigned(p.slabs)) * p.samples;
   auto off_of = [&](int s) {
     return MODE == 2 && n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0;
   };
@@ -253,9 +284,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   const float count = MODE == 2 ? float(d.S) * float(d.D) : float(my_rows) * float(d.D);
 
   float m[EV], s[EV];
-#pragma unroll
-  for (int e = 0; e < EV; ++e) m[e] = 0.f;
-  pass(m, false, s);
+  centred_sums<T, NV, MODE, false>(raw, at, shift, s);
   if (mine) {
 #pragma unroll
     for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
@@ -279,39 +308,46 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
                a += ent[i];
                if constexpr (MODE == 2) b += cnt[i];
              },
-             [&](int s, float a, float b) {
+             [&](int s, int ns, float a, float b) {
                const float n = MODE == 2 ? b : count;
-               gm[s] = n > 0.f ? a / n : 0.f;
-               const int g = s % p.q;
-               const int64_t sample = n0 + s / p.q;
-               gk[s] = sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(at.slab) * p.W + g * d.D) : 0.f;
-               if (p.cluster > 1) xch[s].x = n;
+               const int g = s - ns * p.q;
+               const int64_t sample = n0 + ns;
+               const float first =
+                   sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(at.slab) * p.W + g * d.D) : 0.f;
+               const float mean = n > 0.f ? a / n : 0.f;
+               const float centre = first + mean;
+               // the centre is rounded: it lies by `by` off the mean, which adds n by^2 to the squares
+               const float by = mean - (centre - first);
+               gk[s] = first;
+               gm[s] = centre;
+               gr[s] = n * by * by;
+               if (p.cluster > 1) xch[s] = make_float4(n, mean, 0.f, 0.f);
              });
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < EV; ++e) m[e] = mine ? gm[grp[e]] : 0.f;
-  pass(m, true, s);
+  centred_sums<T, NV, MODE, true>(raw, at, m, s);
   if (mine) {
 #pragma unroll
     for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
   }
   __syncthreads();
   const float total = float(d.S) * float(d.D);
-  auto finish = [&](int s, float mean, float m2) {
-    const float mu = gk[s] + mean, r = 1.0f / sqrtf(m2 / total + d.eps);
+  auto finish = [&](int s, int ns, float mu, float m2) {
+    const float r = 1.0f / sqrtf(not_negative(m2) / total + d.eps);
     gm[s] = mu;
     gr[s] = r;
-    const int64_t sample = n0 + s / p.q;
+    const int64_t sample = n0 + ns;
     if (rank == 0 && sample < d.N) {
-      const int64_t i = sample * d.G + int64_t(at.slab) * p.q + s % p.q;
+      const int64_t i = sample * d.G + int64_t(at.slab) * p.q + (s - ns * p.q);
       if (mean_out != nullptr) mean_out[i] = mu;
       if (inv_out != nullptr) inv_out[i] = r;
     }
   };
   gather.run(off_of, [&](int i, float& a, float&) { a += ent[i]; },
-             [&](int s, float a, float) {
-               if (p.cluster == 1) finish(s, gm[s], a);
-               else xch[s] = make_float4(xch[s].x, gm[s], a, 0.f);
+             [&](int s, int ns, float a, float) {
+               if (p.cluster == 1) finish(s, ns, gm[s], a - gr[s]);
+               else xch[s].z = not_negative(a - gr[s]);
              });
   if (p.cluster > 1) {
     cluster_sync();
@@ -320,7 +356,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
       const float mean = set_sum(v.x * v.y, p.cluster) / total;
       const float t = v.y - mean;
       const float m2 = set_sum(v.z + v.x * t * t, p.cluster);
-      if (s < slots && r == 0) finish(s, mean, m2);
+      if (s < slots && r == 0) finish(s, 0, gk[s] + mean, m2);
     });
     cluster_sync();  // no block leaves (or overwrites x) while another reads its sums
   } else {
@@ -336,21 +372,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   }
   if (at.kn > 0) {
     const int cs = at.slab * p.W;
-    if constexpr (MODE == 2) {
-      int c = c0;
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        a[e] = dev::ld1_keep(gamma + c);
-        b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-        if (++c == p.W) c = 0;
-      }
-    } else {  // (the parameters may have any alignment)
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        a[e] = dev::ld1_keep(gamma + cs + c0 + e);
-        b[e] = beta != nullptr ? dev::ld1_keep(beta + cs + c0 + e) : 0.f;
-      }
-    }
+    load_params<T, MODE == 2>(gamma, beta, cs, c0, p.W, d.pvec, a, b);
 #pragma unroll
     for (int e = 0; e < VW; ++e) a[e] *= rs[MODE == 0 ? 0 : e];
     T* ys = y + at.n * d.L + cs;
@@ -389,10 +411,10 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float* ent_b = ent_a + ents;
   float* g1 = ent_b + ents;
   float* g2 = g1 + slots;
-  const int rank = blockIdx.x % p.cluster;
-  const int64_t first = blockIdx.x / p.cluster;
-  const int trow = threadIdx.x / p.cf, tcol = threadIdx.x - trow * p.cf;
-  const int ns = trow / p.per_sample;
+  const int rank = blockIdx.x & (p.cluster - 1);
+  const unsigned first = blockIdx.x / unsigned(p.cluster);
+  const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
+  const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   const bool mine = trow < p.phases;
   const float scale = 1.0f / (float(d.S) * float(d.D));
   const Gather gather(p, d.D, VW, MODE == 0);
@@ -400,13 +422,14 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   dev::pdl_trigger();
 
   float tot_a[VW], tot_b[VW], ga[VW], be[VW];
+  int grp[EV];  // within the slab
 #pragma unroll
   for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = ga[e] = be[e] = 0.f;
   int off = 0, c0 = 0, slab = 0;
   bool once = true;
 
-  for (int64_t item = first; item < p.items; item += p.grid_items) {
-    const Place<T, MODE> at(d, x, item, rank, trow, tcol);
+  for (unsigned item = first; item < unsigned(p.items); item += unsigned(p.grid_items)) {
+    const Place<T, MODE> at(d, x, item, rank, trow, tcol, ns);
     const int64_t base = at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0;
     uint4 raw[NV], rdy[NV];
 #pragma unroll
@@ -420,33 +443,20 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       once = false;
       slab = at.slab;
       if constexpr (MODE == 2) {
-        const int64_t n0 = item * p.samples;
-        off = dev::misalignment(x + n0 * d.L);
+        off = dev::misalignment(x + int64_t(item) * p.samples * d.L);
       }
       c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
-      if (mine) {
-        int c = c0;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          ga[e] = dev::ld1_keep(gamma + slab * p.W + c);
-          be[e] = beta != nullptr ? dev::ld1_keep(beta + slab * p.W + c) : 0.f;
-          if (++c == p.W) c = 0;
-        }
-      }
+      if (mine) load_params<T, MODE == 2>(gamma, beta, slab * p.W, c0, p.W, d.pvec, ga, be);
+      for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
+        if (e < EV) grp[e] = g;
+      });
     }
     float mu[EV], rs[EV];
-    int grp[EV];
-    {
-      int c = c0;
+    const int64_t ng = at.n * d.G + int64_t(slab) * p.q;
 #pragma unroll
-      for (int e = 0; e < EV; ++e) {
-        const int g = c / d.D;
-        grp[e] = ns * p.q + g;
-        const int64_t i = at.n * d.G + int64_t(slab) * p.q + g;
-        mu[e] = at.kn > 0 ? mean[i] : 0.f;
-        rs[e] = at.kn > 0 ? inv[i] : 0.f;
-        if (++c == p.W) c = 0;
-      }
+    for (int e = 0; e < EV; ++e) {
+      mu[e] = at.kn > 0 ? mean[ng + grp[e]] : 0.f;
+      rs[e] = at.kn > 0 ? inv[ng + grp[e]] : 0.f;
     }
     float sa[VW], sb[VW];
 #pragma unroll
@@ -459,7 +469,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       for (int e = 0; e < VW; ++e) h[e] = (h[e] - mu[MODE == 0 ? 0 : e]) * rs[MODE == 0 ? 0 : e];
       if (d.silu) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) du[e] = act_grad<T, true>(du[e], fmaf(h[e], ga[e], be[e]));
+        for (int e = 0; e < VW; ++e) du[e] = silu_grad<T>(du[e], fmaf(h[e], ga[e], be[e]));
       }
     };
 #pragma unroll
@@ -503,7 +513,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
                  a += ent_a[i];
                  b += ent_b[i];
                },
-               [&](int s, float a, float b) {
+               [&](int s, int, float a, float b) {
                  if (p.cluster == 1) {
                    g1[s] = a * scale;
                    g2[s] = b * scale;
@@ -529,8 +539,8 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       float a1[EV], a2[EV];
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        a1[e] = g1[grp[e]];
-        a2[e] = g2[grp[e]];
+        a1[e] = g1[ns * p.q + grp[e]];
+        a2[e] = g2[ns * p.q + grp[e]];
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -584,6 +594,175 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       out[0] = a;
       out[rows * d.C] = b;
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One position a sample (S = 1), D / VW a power of two up to 32: the norm over
+// each token's groups.  A group's fragments are neighbouring lanes, so its sums
+// are shuffles and there is no shared memory and no barrier.  A block has `cols`
+// fragment columns of a tile and `rows` tokens side by side; it takes every
+// grid-th set of tokens, so its channels (and parameters) stay the same.  U
+// tokens are loaded before the first is used.
+// ---------------------------------------------------------------------------
+
+struct TokenPlan {
+  int cols, rows, tiles, ctas;  // ctas: of each tile
+};
+
+struct TokenDims {
+  int64_t N, C;
+  int G, set;                   // lanes of a group
+  float eps, scale;             // scale: 1 / D
+  bool silu, pvec;
+  TokenPlan p;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, T* y, float* mean_out,
+           float* inv_out, TokenDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int trow = threadIdx.x / unsigned(d.p.cols), tile = blockIdx.x % unsigned(d.p.tiles);
+  const int col = tile * d.p.cols + (threadIdx.x - trow * d.p.cols);  // of fragments
+  const int lead = (threadIdx.x & 31) & ~(d.set - 1);
+  const bool mine = trow < d.p.rows && col * VW < d.C;  // uniform in a set
+  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N;
+  int64_t n = int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows + trow;
+  float a[VW], b[VW];
+  if (mine) load_params<T, false>(gamma, beta, 0, col * VW, 0, d.pvec, a, b);
+  // every lane of a warp goes round as often as its first (the shuffles are whole warps')
+  const int rounds = static_cast<int>((n1 - (int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows) + step * U - 1) /
+                                      (step * U));
+  for (int i = 0; i < rounds; ++i, n += step * U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (mine && n + u * step < n1) raw[u] = dev::ld16_stream(x + (n + u * step) * d.C + col * VW);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool on = mine && n + u * step < n1;
+      float v[VW];
+      if (on) {
+        dev::Conv<T>::unpack(raw[u], v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) v[e] = 0.f;
+      }
+      const float first = __shfl_sync(0xffffffffu, v[0], lead);
+      float s = 0.f, q = 0.f;
+#pragma unroll
+      for (int e = 0; e < VW; ++e) s += v[e] - first;
+      const float m = set_sum(s, d.set) * d.scale;
+      const float mu = first + m, by = m - (mu - first);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        v[e] -= mu;
+        q = fmaf(v[e], v[e], q);
+      }
+      q = set_sum(q, d.set) * d.scale;  // relative to mu, which is rounded: `by` off the mean
+      const float r = 1.0f / sqrtf(not_negative(q - by * by) + d.eps);
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          v[e] = fmaf(v[e], a[e] * r, b[e]);
+          if (d.silu) v[e] = silu<T>(v[e]);
+        }
+        const int64_t t = n + u * step;
+        dev::st16_stream(y + t * d.C + col * VW, dev::Conv<T>::pack(v));
+        if ((threadIdx.x & 31) == lead) {
+          const int64_t g = t * d.G + col / d.set;
+          if (mean_out != nullptr) mean_out[g] = mu;
+          if (inv_out != nullptr) inv_out[g] = r;
+        }
+      }
+    }
+  }
+}
+
+// The gradient; the sums for dgamma and dbeta run on in registers and leave as
+// row blockIdx / tiles of cpart: 2 x [ctas][C].
+template <typename T>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_grad_token(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+                const float* inv, T* dx, float* cpart, TokenDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 2;
+  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int trow = threadIdx.x / unsigned(d.p.cols), tile = blockIdx.x % unsigned(d.p.tiles);
+  const int row = blockIdx.x / unsigned(d.p.tiles);
+  const int col = tile * d.p.cols + (threadIdx.x - trow * d.p.cols);
+  const bool mine = trow < d.p.rows && col * VW < d.C;
+  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N;
+  int64_t n = int64_t(row) * d.p.rows + trow;
+  float ga[VW], be[VW], tot_a[VW], tot_b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) ga[e] = be[e] = tot_a[e] = tot_b[e] = 0.f;
+  if (mine) load_params<T, false>(gamma, beta, 0, col * VW, 0, d.pvec, ga, be);
+  const int rounds = static_cast<int>((n1 - int64_t(row) * d.p.rows + step * U - 1) / (step * U));
+  for (int i = 0; i < rounds; ++i, n += step * U) {
+    uint4 rx[U], rd[U];
+    float mu[U], rs[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = n + u * step;
+      if (mine && t < n1) {
+        rx[u] = dev::ld16_stream(x + t * d.C + col * VW);
+        rd[u] = dev::ld16_stream(dy + t * d.C + col * VW);
+        mu[u] = mean[t * d.G + col / d.set];
+        rs[u] = inv[t * d.G + col / d.set];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = n + u * step;
+      const bool on = mine && t < n1;
+      float h[VW], w[VW], p = 0.f, q = 0.f;
+      if (on) {
+        dev::Conv<T>::unpack(rx[u], h);
+        dev::Conv<T>::unpack(rd[u], w);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          h[e] = (h[e] - mu[u]) * rs[u];
+          if (d.silu) w[e] = silu_grad<T>(w[e], fmaf(h[e], ga[e], be[e]));
+          tot_a[e] += w[e];
+          tot_b[e] = fmaf(w[e], h[e], tot_b[e]);
+          w[e] *= ga[e];
+          p += w[e];
+          q = fmaf(w[e], h[e], q);
+        }
+      }
+      p = set_sum(p, d.set) * d.scale;
+      q = set_sum(q, d.set) * d.scale;
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) w[e] = rs[u] * ((w[e] - p) - h[e] * q);
+        dev::st16_stream(dx + t * d.C + col * VW, dev::Conv<T>::pack(w));
+      }
+    }
+  }
+  if (cpart == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    s_a[threadIdx.x * VW + e] = tot_a[e];
+    s_b[threadIdx.x * VW + e] = tot_b[e];
+  }
+  __syncthreads();
+  const int W = d.p.cols * VW;
+  for (int c = threadIdx.x; c < W && tile * W + c < d.C; c += blockDim.x) {
+    float sa = 0.f, sb = 0.f;
+    for (int k = 0; k < d.p.rows; ++k) {
+      sa += s_a[k * W + c];
+      sb += s_b[k * W + c];
+    }
+    float* out = cpart + int64_t(row) * d.C + tile * W + c;
+    out[0] = sa;
+    out[int64_t(d.p.ctas) * d.C] = sb;
   }
 }
 
@@ -667,6 +846,54 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, i
     if (q * D / vw >= 8 || q == G) return with(q);
   }
   return false;
+}
+
+// The token form applies: S = 1, aligned, and a group is 1 to 32 (a power of two) lanes.
+bool token_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, TokenPlan* p, int* set) {
+  const int64_t D = C / G;
+  if (S != 1 || D % vw != 0 || D / vw > 32 || (D / vw & (D / vw - 1)) != 0) return false;
+  *set = int(D / vw);
+  const int64_t frags = C / vw;
+  p->tiles = int((frags + kWalkThreads - 1) / kWalkThreads);
+  p->cols = int((frags / *set + p->tiles - 1) / p->tiles) * *set;  // whole groups
+  p->rows = int(std::max<int64_t>(1, std::min<int64_t>(kWalkThreads / p->cols, (N + kPlanSms - 1) / kPlanSms)));
+  // about 1024 threads an SM
+  const int threads = (p->cols * p->rows + 31) / 32 * 32;
+  const int64_t most = std::max<int64_t>(1, int64_t(kPlanSms) * (1024 / threads) / p->tiles);
+  p->ctas = int(std::min((N + p->rows - 1) / p->rows, most));
+  return true;
+}
+
+TokenDims token_dims(int64_t N, int64_t C, int64_t G, float eps, bool silu, bool pvec, const TokenPlan& p, int set) {
+  return TokenDims{N, C, int(G), set, eps, 1.0f / float(C / G), silu, pvec, p};
+}
+
+inline int token_threads(const TokenPlan& p) { return (p.cols * p.rows + 31) / 32 * 32; }
+
+template <typename T>
+cudaError_t token_fwd(const GroupNormArgs& a, const TokenDims& d, cudaStream_t stream, int* launches) {
+  const cudaError_t e = launch(k_gn_token<T>, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
+                               static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
+                               static_cast<const T*>(a.beta), static_cast<T*>(a.y), a.mean, a.inv, d);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+template <typename T>
+cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cpart, cudaStream_t stream,
+                       int* launches) {
+  cudaError_t e = launch(k_gn_grad_token<T>, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
+                         static_cast<const T*>(a.dy), static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
+                         static_cast<const T*>(a.beta), a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (cpart != nullptr) {
+    const int64_t jobs = (d.C + 31) / 32 * 2;
+    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart, int64_t(d.p.ctas),
+               int64_t(1), d.C, 2, static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
+    if (e == cudaSuccess) *launches += 1;
+  }
+  return e;
 }
 
 template <typename... KArgs, typename... Args>
@@ -768,6 +995,9 @@ bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, Fu
 size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
   const int vw = t == DType::F32 ? 4 : 8;
   size_t most = 0;
+  TokenPlan tp;
+  int set;
+  if (token_plan(vw, N, S, C, G, &tp, &set)) most = size_t(tp.ctas) * size_t(C) * 8;
   for (int slab = 0; slab < 2; ++slab) {
     FusedPlan p;
     if (grad_plan(vw, N, S, C, G, slab != 0, &p))
@@ -778,10 +1008,22 @@ size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int
 
 cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t stream, int* launches, bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
-  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, a.silu, {}};
+  const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, a.silu, pvec, {}};
   *done = false;
   if (misalign16(a.x) != misalign16(a.y)) return cudaSuccess;
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
+  TokenPlan tp;
+  int set;
+  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, &tp, &set)) {
+    *done = true;
+    const TokenDims t = token_dims(a.N, a.C, a.G, a.eps, a.silu, pvec, tp, set);
+    switch (a.t) {
+      case DType::F32: return token_fwd<float>(a, t, stream, launches);
+      case DType::F16: return token_fwd<__half>(a, t, stream, launches);
+      default: return token_fwd<__nv_bfloat16>(a, t, stream, launches);
+    }
+  }
   if (!fused_plan(vw, a.N, a.S, a.C, a.G, slab, kFwdNv, &d.p)) return cudaSuccess;
   const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
   if (fused_smem(d.p, mode, vw, false) > kSmemMost) return cudaSuccess;
@@ -801,14 +1043,26 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t st
 cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int, cudaStream_t stream, int* launches,
                                          bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
-  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, a.silu, {}};
+  const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, a.silu, pvec, {}};
   *done = false;
   if (misalign16(a.x) != misalign16(a.dy) || misalign16(a.x) != misalign16(a.dx)) return cudaSuccess;
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
+  float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
+  TokenPlan tp;
+  int set;
+  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, &tp, &set)) {
+    *done = true;
+    const TokenDims t = token_dims(a.N, a.C, a.G, 0.f, a.silu, pvec, tp, set);
+    switch (a.t) {
+      case DType::F32: return token_grad<float>(a, t, cpart, stream, launches);
+      case DType::F16: return token_grad<__half>(a, t, cpart, stream, launches);
+      default: return token_grad<__nv_bfloat16>(a, t, cpart, stream, launches);
+    }
+  }
   if (!grad_plan(vw, a.N, a.S, a.C, a.G, slab, &d.p)) return cudaSuccess;
   *done = true;
   const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
-  float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
 #define EP_GN_GRAD_FUSED(T)                                                     \
   (mode == 0   ? fused_grad<T, 0>(a, d, cpart, stream, launches)                \
    : mode == 1 ? fused_grad<T, 1>(a, d, cpart, stream, launches)                \
