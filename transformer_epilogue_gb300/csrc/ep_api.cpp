@@ -134,11 +134,12 @@ int ep_abi_version(void) { return kAbiVersion; }
 
 namespace {
 cudaError_t sum_pipe_timeouts(unsigned int* total, bool clear) {
-  unsigned int a = 0, b = 0, c = 0;
+  unsigned int a = 0, b = 0, c = 0, g = 0;
   cudaError_t e = ep::sln_pipe_timeouts(&a, clear);
   if (e == cudaSuccess) e = ep::softmax_pipe_timeouts(&b, clear);
   if (e == cudaSuccess) e = ep::elementwise_pipe_timeouts(&c, clear);
-  *total = a + b + c;
+  if (e == cudaSuccess) e = ep::group_norm_pipe_timeouts(&g, clear);
+  *total = a + b + c + g;
   return e;
 }
 }  // namespace

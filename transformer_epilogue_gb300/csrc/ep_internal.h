@@ -150,6 +150,7 @@ cudaError_t static_softmax_scratch(void** addr);
 cudaError_t sln_pipe_timeouts(unsigned int* count, bool clear);
 cudaError_t softmax_pipe_timeouts(unsigned int* count, bool clear);
 cudaError_t elementwise_pipe_timeouts(unsigned int* count, bool clear);
+cudaError_t group_norm_pipe_timeouts(unsigned int* count, bool clear);
 
 // One-CTA kernel whose bounded wait is made to run out after timeout_ns.
 cudaError_t launch_selftest_bounded_wait(uint64_t timeout_ns, cudaStream_t stream, int* launches);

@@ -29,23 +29,13 @@
 #include "ep_internal.h"
 #include "group_norm.cuh"
 #include "launch_util.h"
+#include "tma_pipe.cuh"
 
 namespace ep {
 namespace {
 
-// The split kernels' forms:
-//  kAny      any C and alignment: fragments are checked against the sample's
-//            ends, and a sample may start off a 16-byte boundary (VEC: whole
-//            fragments are loaded as 16 bytes; else value by value);
-//  kChannel  C % VW == 0 and 16-byte-aligned operands: every fragment is whole
-//            (and the last walk row may have fewer than the others);
-//  kGroup    and D % VW == 0: a fragment lies in one group, so statistics and
-//            group sums are per fragment, not per channel.
-enum { kAny = 0, kChannel = 1, kGroup = 2 };
-
 // One call's sizes, as every kernel of the split form gets them (C is at most
-// kMaxGroupNormChannels, so positions in a walk row fit an int), for the
-// samples of one launch.
+// kMaxGroupNormChannels, so positions in a walk row fit an int).
 struct GnDims {
   int64_t N, S, L;  // L = S * C
   int C, G, D;
@@ -54,9 +44,9 @@ struct GnDims {
 };
 
 // Where a sample's walk row starts: `off` elements before the sample.
-template <typename T, int FORM, bool VEC>
+template <typename T, bool VEC>
 __device__ __forceinline__ int walk_offset(const T* sample) {
-  return FORM == kAny && VEC ? dev::misalignment(sample) : 0;
+  return VEC ? dev::misalignment(sample) : 0;
 }
 
 // The channel of the first element of fragment column j.
@@ -96,443 +86,128 @@ __device__ __forceinline__ bool group_in_tile(int p0, int np, int off, int c0, i
 struct Tile {
   int tile, frags;   // the tile's number and fragments
   int64_t j;         // fragment column
-  int64_t rows;      // walk rows of a sample that have a fragment j (kAny: all, with checks)
   bool mine;
-  __device__ __forceinline__ Tile(const WalkPlan& p, int64_t sample_frags) {
+  __device__ __forceinline__ explicit Tile(const WalkPlan& p) {
     tile = p.tiles == 1 ? 0 : static_cast<int>(blockIdx.x % unsigned(p.tiles));
     frags = static_cast<int>(min(int64_t(p.tile_frags), p.row_frags - int64_t(tile) * p.tile_frags));
     j = int64_t(tile) * p.tile_frags + threadIdx.x;
     mine = int(threadIdx.x) < frags;
-    rows = sample_frags < 0 ? p.rows : (sample_frags - j + p.row_frags - 1) / p.row_frags;
   }
 };
 
-// Pass 1.  partial: [item][tile][G] x (count, mean, M2), relative to the group's
-// first value, or, where a sample has one item and one tile, the statistics
-// themselves (partial == nullptr).  A thread sums its values and their squares
-// relative to the mean of its first U rows, which is near enough to its own mean
-// that nothing cancels; the threads' (count, mean, M2) are joined by two sums,
-// the second relative to the first's mean.
-template <typename T, int FORM>
-__global__ void __launch_bounds__(kWalkThreads)
-k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
-  constexpr int VW = dev::Vec16<T>::N;
-  constexpr int EV = FORM == kGroup ? 1 : VW;  // sums of a thread
-  constexpr int U = 4;
-  __shared__ float s_cnt[kWalkThreads * EV], s_mean[kWalkThreads * EV], s_m2[kWalkThreads * EV];
-  dev::pdl_wait();
-  dev::pdl_trigger();
-  const WalkPlan& p = d.p;
-  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
-  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV;
-  const int Cw = FORM == kGroup ? d.C / VW : d.C, Dw = FORM == kGroup ? d.D / VW : d.D;
-  const int64_t items = d.N * p.chunks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-
-  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
-    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
-    const T* xs = x + n * d.L;
-    const int off = walk_offset<T, FORM, true>(xs);
-    if (t.mine) {
-      float first[EV], c[EV], s[EV], q[EV], cnt[EV];
-      for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int, int g) {
-        if (e < EV) first[e] = dev::ld1_keep(xs + int64_t(g) * d.D);
-      });
-#pragma unroll
-      for (int e = 0; e < EV; ++e) s[e] = q[e] = cnt[e] = 0.f;
-      const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
-      const int64_t pitch = p.row_frags * VW;
-      const T* px = xs + (ra * p.row_frags + t.j) * VW;
-      if constexpr (FORM != kAny) {
-        // centre: the first rows' mean
-        if (ra < rb) {
-          float m[EV];
-#pragma unroll
-          for (int e = 0; e < EV; ++e) m[e] = 0.f;
-          const int u1 = static_cast<int>(min(int64_t(U), rb - ra));
-          for (int u = 0; u < u1; ++u) {
-            float v[VW];
-            dev::Conv<T>::unpack(dev::ld16_keep(px + u * pitch), v);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) m[EV == 1 ? 0 : e] += v[e] - first[EV == 1 ? 0 : e];
-          }
-#pragma unroll
-          for (int e = 0; e < EV; ++e) c[e] = first[e] + m[e] / float(u1 * (VW / EV));
-        } else {
-#pragma unroll
-          for (int e = 0; e < EV; ++e) c[e] = first[e];
-        }
-        auto add = [&](uint4 raw) {
-          float v[VW];
-          dev::Conv<T>::unpack(raw, v);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) v[e] -= c[EV == 1 ? 0 : e];
-          if constexpr (EV == 1) {
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int e = 0; e < VW; e += 2) {
-              a += v[e] + v[e + 1];
-              b = fmaf(v[e], v[e], b);
-              q[0] = fmaf(v[e + 1], v[e + 1], q[0]);
-            }
-            s[0] += a;
-            q[0] += b;
-          } else {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              s[e] += v[e];
-              q[e] = fmaf(v[e], v[e], q[e]);
-            }
-          }
-        };
-        int64_t r = ra;
-        for (; r + U <= rb; r += U, px += U * pitch) {
-          uint4 raw[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) raw[u] = dev::ld16_keep(px + u * pitch);
-#pragma unroll
-          for (int u = 0; u < U; ++u) add(raw[u]);
-        }
-        for (; r < rb; ++r, px += pitch) add(dev::ld16_keep(px));
-#pragma unroll
-        for (int e = 0; e < EV; ++e) cnt[e] = ra < rb ? float(rb - ra) * (VW / EV) : 0.f;
-      } else {
-        // the centre is the first value a channel meets here
-#pragma unroll
-        for (int e = 0; e < VW; ++e) c[e] = first[e];
-        for (int64_t r0 = ra; r0 < rb; r0 += U) {
-          float v[U][VW];
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (r0 + u < rb) dev::load_frag<T, true>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              if (r0 + u < rb && e0 + e >= 0 && e0 + e < d.L) {
-                if (cnt[e] == 0.f) c[e] = v[u][e];
-                const float w = v[u][e] - c[e];
-                cnt[e] += 1.f;
-                s[e] += w;
-                q[e] = fmaf(w, w, q[e]);
-              }
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < EV; ++e) {
-        const float m = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
-        s_cnt[threadIdx.x * EV + e] = cnt[e];
-        s_mean[threadIdx.x * EV + e] = (c[e] - first[e]) + m;
-        s_m2[threadIdx.x * EV + e] = not_negative(q[e] - s[e] * m);
-      }
-    }
-    __syncthreads();
-    for (int g = warp; g < d.G; g += warps) {
-      float* out = partial + ((item * p.tiles + t.tile) * d.G + g) * 3;
-      if (p.tiles > 1 && !group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
-        if (lane == 0) out[0] = out[1] = out[2] = 0.f;
-        continue;
-      }
-      float c = 0.f, s = 0.f, q = 0.f;
-      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
-        c += s_cnt[i];
-        s = fmaf(s_cnt[i], s_mean[i], s);
-      });
-      c = dev::warp_sum(c);
-      s = dev::warp_sum(s);
-      const float mg = c > 0.f ? s / c : 0.f;
-      float res = 0.f;  // what rounding s / c and the sum left out of the mean
-      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
-        const float w = s_mean[i] - mg;
-        res = fmaf(s_cnt[i], w, res);
-        q += fmaf(s_cnt[i] * w, w, s_m2[i]);
-      });
-      res = dev::warp_sum(res);
-      q = dev::warp_sum(q);
-      if (lane == 0) {
-        const float fix = c > 0.f ? res / c : 0.f;
-        const float mf = mg + fix, m2g = not_negative(q - res * fix);
-        if (partial == nullptr) {
-          mean_out[n * d.G + g] = dev::ld1_keep(xs + int64_t(g) * d.D) + mf;
-          inv_out[n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
-        } else {
-          out[0] = c;
-          out[1] = mf;
-          out[2] = m2g;
-        }
-      }
-    }
-    __syncthreads();
+// Items of a CTA, first to last or (reversed: the pass that finds in L2 what
+// the pass before read last) last to first.
+struct Items {
+  int64_t items, step, at;
+  bool reversed;
+  __device__ __forceinline__ Items(const GnDims& d, bool rev) : items(d.N * d.p.chunks), reversed(rev) {
+    at = blockIdx.x / unsigned(d.p.tiles);
+    step = gridDim.x / unsigned(d.p.tiles);
   }
-}
+  __device__ __forceinline__ bool more() const { return at < items; }
+  __device__ __forceinline__ int64_t item() const { return reversed ? items - 1 - at : at; }
+  __device__ __forceinline__ void next() { at += step; }
+};
 
-// Joins a group's chunks and tiles: one warp for each (n, g).
-template <typename T>
-__global__ void __launch_bounds__(256)
-k_gn_join(const T* x, const float* partial, GnDims d, float* mean_out, float* inv_out) {
-  dev::pdl_wait();
-  dev::pdl_trigger();
+// The walk rows [ra, rb) of an item, and its sample.  `rows`: of a sample.
+struct Range {
+  int64_t n, ra, rb;
+  __device__ __forceinline__ Range(const WalkPlan& p, int64_t item, int64_t rows) {
+    n = p.chunks == 1 ? item : item / p.chunks;
+    ra = (item - n * p.chunks) * p.rows_per_chunk;
+    rb = min(rows, ra + p.rows_per_chunk);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Block epilogues, shared by the staged and the general kernels.  `sync` is the
+// barrier of the threads that take part.  Positions are elements (EV = VW) or
+// fragments (EV = 1, where a fragment lies in one group).
+// ---------------------------------------------------------------------------
+
+// The threads' (count, mean, M2) for each position, in shared memory, to the
+// item's groups: two sums, the second relative to the first's mean.
+template <typename T, int EV>
+__device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, const Range& r, int64_t item, int off,
+                                                const T* xs, int warps, const float* s_cnt, const float* s_mean,
+                                                const float* s_m2, float* partial, float* mean_out, float* inv_out) {
+  const WalkPlan& p = d.p;
+  const int f = EV == 1 ? dev::Vec16<T>::N : 1;  // elements of a position
+  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV, Cw = d.C / f, Dw = d.D / f;
   const int lane = threadIdx.x & 31;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
-  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
-    const float* src = partial + ((i / d.G) * parts * d.G + i % d.G) * 3;
-    float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
-#pragma unroll 4
-    for (int64_t k = lane; k < parts; k += 32) {
-      const float* e = src + k * d.G * 3;
-      const float n = __ldcg(e);
-      c += n;
-      s = fmaf(n, __ldcg(e + 1), s);
+  for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
+    float* out = partial + ((item * p.tiles + t.tile) * d.G + g) * 3;
+    if (p.tiles > 1 && !group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
+      if (lane == 0) out[0] = out[1] = out[2] = 0.f;
+      continue;
     }
+    float c = 0.f, s = 0.f, q = 0.f;
+    for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+      c += s_cnt[i];
+      s = fmaf(s_cnt[i], s_mean[i], s);
+    });
     c = dev::warp_sum(c);
     s = dev::warp_sum(s);
-    const float mg = s / c;
-#pragma unroll 4
-    for (int64_t k = lane; k < parts; k += 32) {
-      const float* e = src + k * d.G * 3;
-      const float w = __ldcg(e + 1) - mg, n = __ldcg(e);
-      res = fmaf(n, w, res);
-      q += fmaf(n * w, w, __ldcg(e + 2));
-    }
+    const float mg = c > 0.f ? s / c : 0.f;
+    float res = 0.f;  // what rounding s / c and the sum left out of the mean
+    for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+      const float w = s_mean[i] - mg;
+      res = fmaf(s_cnt[i], w, res);
+      q += fmaf(s_cnt[i] * w, w, s_m2[i]);
+    });
     res = dev::warp_sum(res);
     q = dev::warp_sum(q);
     if (lane == 0) {
-      const float fix = res / c;
-      mean_out[i] = dev::ld1_keep(x + i / d.G * d.L + i % d.G * d.D) + (mg + fix);
-      inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
-    }
-  }
-}
-
-// Pass 2: y from x and the statistics.  Bound by the data where x comes from DRAM.
-template <typename T, int FORM, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kWalkThreads)
-k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean, const float* inv,
-           T* y, GnDims d) {
-  constexpr int VW = dev::Vec16<T>::N;
-  constexpr int EV = FORM == kGroup ? 1 : VW;
-  constexpr int U = 4;
-  dev::pdl_wait();
-  dev::pdl_trigger();
-  const WalkPlan& p = d.p;
-  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
-  if (!t.mine) return;
-  const int64_t items = d.N * p.chunks;
-  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
-    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
-    const T* xs = x + n * d.L;
-    T* ys = y + n * d.L;
-    const int off = walk_offset<T, FORM, VEC>(xs);
-    float mu[EV], a[VW], b[VW];
-    for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int c, int g) {
-      if (e < EV) mu[e] = mean[n * d.G + g];
-      a[e] = inv[n * d.G + g] * dev::ld1_keep(gamma + c);
-      b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-    });
-    auto value = [&](float (&v)[VW]) {
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        v[e] = fmaf(v[e] - mu[EV == 1 ? 0 : e], a[e], b[e]);
-        if constexpr (SILU) v[e] = silu<T>(v[e]);
-      }
-    };
-    const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
-    if constexpr (FORM != kAny) {
-      const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
-      const T* px = xs + at;
-      T* py = ys + at;
-      int64_t r = ra;
-      for (; r + U <= rb; r += U, px += U * pitch, py += U * pitch) {
-        uint4 raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = dev::ld16_stream(px + u * pitch);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[VW];
-          dev::Conv<T>::unpack(raw[u], v);
-          value(v);
-          dev::st16_stream(py + u * pitch, dev::Conv<T>::pack(v));
-        }
-      }
-      for (; r < rb; ++r, px += pitch, py += pitch) {
-        float v[VW];
-        dev::Conv<T>::unpack(dev::ld16_stream(px), v);
-        value(v);
-        dev::st16_stream(py, dev::Conv<T>::pack(v));
-      }
-    } else {
-      for (int64_t r0 = ra; r0 < rb; r0 += U) {
-        float v[U][VW];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (r0 + u < rb) dev::load_frag<T, VEC>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (r0 + u < rb) {
-            value(v[u]);
-            dev::store_frag<T, VEC>(ys, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
-          }
-        }
+      const float fix = c > 0.f ? res / c : 0.f;
+      const float mf = mg + fix, m2g = not_negative(q - res * fix);
+      if (partial == nullptr) {
+        mean_out[r.n * d.G + g] = dev::ld1_keep(xs + int64_t(g) * d.D) + mf;
+        inv_out[r.n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
+      } else {
+        out[0] = c;
+        out[1] = mf;
+        out[2] = m2g;
       }
     }
   }
 }
 
-// What the gradient's passes make of x and dy: h and du, with a thread's channel
-// values in registers.
-template <typename T, int EV, bool SILU>
-struct GradValues {
-  static constexpr int VW = dev::Vec16<T>::N;
-  float mu[EV], rs[EV], ga[VW], be[VW];
-  __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
-                                       const T* __restrict__ beta, const float* mean, const float* inv) {
-    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
-      if (e < EV) {
-        mu[e] = mean[ng + g];
-        rs[e] = inv[ng + g];
-      }
-      ga[e] = dev::ld1_keep(gamma + c);
-      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-    });
-  }
-  // x -> h, dy -> du
-  __device__ __forceinline__ void operator()(float (&v)[VW], float (&w)[VW]) const {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      v[e] = (v[e] - mu[EV == 1 ? 0 : e]) * rs[EV == 1 ? 0 : e];
-      if constexpr (SILU) w[e] = silu_grad<T>(w[e], fmaf(v[e], ga[e], be[e]));
-    }
-  }
-};
-
-// Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
-// groups' sums of each item.  A CTA's items share `off` (the launch sees to
-// it), so a thread's channels stay the same and its sums run on over them.
-//   gpart: [item][tile][G] x (sum du gamma, sum du gamma h)
-//   cpart: 2 x [CTA row][C] (one tile) or 2 x [CTA row][walk row], position 0
-//          being channel 0
-template <typename T, int FORM, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kWalkThreads)
-k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
-               const float* inv, GnDims d, float* gpart, float* cpart) {
-  constexpr int VW = dev::Vec16<T>::N;
-  constexpr int EV = FORM == kGroup ? 1 : VW;
-  constexpr int U = sizeof(T) == 4 ? 4 : 2;
-  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
-  dev::pdl_wait();
-  dev::pdl_trigger();
+// The positions' (sum du gamma, sum du gamma h), in shared memory, to the item's groups.
+template <typename T, int EV>
+__device__ __forceinline__ void join_group_sums(const GnDims& d, const Tile& t, int64_t item, int off, int warps,
+                                                const float* s_a, const float* s_b, float* gpart) {
   const WalkPlan& p = d.p;
-  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
-  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV;
-  const int Cw = FORM == kGroup ? d.C / VW : d.C, Dw = FORM == kGroup ? d.D / VW : d.D;
-  const int64_t items = d.N * p.chunks;
-  const int cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  float tot_a[VW], tot_b[VW];
-#pragma unroll
-  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
-  int off = 0;
-
-  for (int64_t item = cta_row; item < items; item += cta_rows) {
-    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
-    const T* xs = x + n * d.L;
-    const T* ds = dy + n * d.L;
-    off = walk_offset<T, FORM, VEC>(xs);
-    if (t.mine) {
-      GradValues<T, EV, SILU> val;
-      val.load(first_channel(t.j, VW, off, d.C), n * d.G, d, gamma, beta, mean, inv);
-      float sa[VW], sb[VW];
-#pragma unroll
-      for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
-      auto add = [&](float (&v)[VW], float (&w)[VW]) {
-        val(v, w);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          sa[e] += w[e];
-          sb[e] = fmaf(w[e], v[e], sb[e]);
-        }
-      };
-      const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
-      if constexpr (FORM != kAny) {
-        const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
-        const T* px = xs + at;
-        const T* pd = ds + at;
-        int64_t r = ra;
-        for (; r + U <= rb; r += U, px += U * pitch, pd += U * pitch) {
-          uint4 rx[U], rd[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            rx[u] = dev::ld16_keep(px + u * pitch);
-            rd[u] = dev::ld16_keep(pd + u * pitch);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float v[VW], w[VW];
-            dev::Conv<T>::unpack(rx[u], v);
-            dev::Conv<T>::unpack(rd[u], w);
-            add(v, w);
-          }
-        }
-        for (; r < rb; ++r, px += pitch, pd += pitch) {
-          float v[VW], w[VW];
-          dev::Conv<T>::unpack(dev::ld16_keep(px), v);
-          dev::Conv<T>::unpack(dev::ld16_keep(pd), w);
-          add(v, w);
-        }
-      } else {
-        for (int64_t r = ra; r < rb; ++r) {
-          const int64_t e0 = (r * p.row_frags + t.j) * VW - off;
-          float v[VW], w[VW];
-          dev::load_frag<T, VEC>(xs, e0, d.L, v);
-          dev::load_frag<T, VEC>(ds, e0, d.L, w);  // 0 outside the sample: adds nothing
-          add(v, w);
-        }
-      }
-      if constexpr (FORM == kGroup) {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          a = fmaf(sa[e], val.ga[e], a);
-          b = fmaf(sb[e], val.ga[e], b);
-        }
-        s_a[threadIdx.x] = a;
-        s_b[threadIdx.x] = b;
-      } else {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
-          s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        tot_a[e] += sa[e];
-        tot_b[e] += sb[e];
-      }
+  const int f = EV == 1 ? dev::Vec16<T>::N : 1;
+  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV, Cw = d.C / f, Dw = d.D / f;
+  const int lane = threadIdx.x & 31;
+  for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
+    float a = 0.f, b = 0.f;
+    if (p.tiles == 1 || group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
+      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+        a += s_a[i];
+        b += s_b[i];
+      });
+      a = dev::warp_sum(a);
+      b = dev::warp_sum(b);
     }
-    __syncthreads();
-    for (int g = warp; g < d.G; g += warps) {
-      float a = 0.f, b = 0.f;
-      if (p.tiles == 1 || group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
-        for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
-          a += s_a[i];
-          b += s_b[i];
-        });
-        a = dev::warp_sum(a);
-        b = dev::warp_sum(b);
-      }
-      if (lane == 0) {
-        float* out = gpart + ((item * p.tiles + t.tile) * d.G + g) * 2;
-        out[0] = a;
-        out[1] = b;
-      }
+    if (lane == 0) {
+      float* out = gpart + ((item * p.tiles + t.tile) * d.G + g) * 2;
+      out[0] = a;
+      out[1] = b;
     }
-    __syncthreads();
   }
-  if (cpart == nullptr) return;
+}
+
+// A CTA's channel sums to row cta_row of cpart: 2 x [CTA row][C] (one tile), or
+// 2 x [CTA row][walk row], position 0 being channel 0.
+template <typename T, typename SYNC>
+__device__ __forceinline__ void leave_channel_sums(const GnDims& d, const Tile& t, int off, int threads,
+                                                   const float (&tot_a)[dev::Vec16<T>::N],
+                                                   const float (&tot_b)[dev::Vec16<T>::N], float* s_a, float* s_b,
+                                                   float* cpart, SYNC sync) {
+  constexpr int VW = dev::Vec16<T>::N;
+  const WalkPlan& p = d.p;
+  const int64_t cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
   if (p.tiles > 1) {
     if (t.mine) {
       const int64_t P = p.row_frags * VW;
@@ -555,144 +230,745 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
       s_b[threadIdx.x * VW + e] = tot_b[e];
     }
   }
-  __syncthreads();
-  const int reps = static_cast<int>(p.reps), P = t.frags * VW;
-  float* oa = cpart + int64_t(cta_row) * d.C;
-  float* ob = oa + int64_t(cta_rows) * d.C;
-  if (reps <= 16) {
-    for (int c = threadIdx.x; c < d.C; c += blockDim.x) {
-      float a = 0.f, b = 0.f;
-      for (int k = 0; k < reps; ++k) {
-        int q = c + off + k * d.C;
-        if (q >= P) q -= P;
-        a += s_a[q];
-        b += s_b[q];
-      }
+  sync();
+  const int reps = static_cast<int>(p.reps), P = t.frags * VW, lane = threadIdx.x & 31;
+  float* oa = cpart + cta_row * d.C;
+  float* ob = oa + cta_rows * d.C;
+  const int lanes = reps <= 16 ? 1 : 32;  // to a channel
+  for (int c = threadIdx.x / lanes; c < d.C; c += threads / lanes) {
+    float a = 0.f, b = 0.f;
+    for (int k = lanes == 1 ? 0 : lane; k < reps; k += lanes) {
+      int q = c + off + k * d.C;
+      if (q >= P) q -= P;
+      a += s_a[q];
+      b += s_b[q];
+    }
+    if (lanes == 32) {
+      a = dev::warp_sum(a);
+      b = dev::warp_sum(b);
+    }
+    if (lanes == 1 || lane == 0) {
       oa[c] = a;
       ob[c] = b;
     }
-  } else {
-    for (int c = warp; c < d.C; c += warps) {
-      float a = 0.f, b = 0.f;
-      for (int k = lane; k < reps; k += 32) {
-        int q = c + off + k * d.C;
-        if (q >= P) q -= P;
-        a += s_a[q];
-        b += s_b[q];
-      }
-      a = dev::warp_sum(a);
-      b = dev::warp_sum(b);
-      if (lane == 0) {
-        oa[c] = a;
-        ob[c] = b;
-      }
-    }
   }
 }
 
-// Joins the groups' sums over chunks and tiles: m1, m2 of each (n, g).
-__global__ void __launch_bounds__(256)
-k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
+// ---------------------------------------------------------------------------
+// What a thread does with its fragments.
+// ---------------------------------------------------------------------------
+
+// A thread's channel values for the forward pass.
+template <typename T, int EV, bool SILU>
+struct ApplyValues {
+  static constexpr int VW = dev::Vec16<T>::N;
+  float mu[EV], a[VW], b[VW];
+  __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
+                                       const T* __restrict__ beta, const float* mean, const float* inv) {
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
+      if (e < EV) mu[e] = mean[ng + g];
+      a[e] = inv[ng + g] * dev::ld1_keep(gamma + c);
+      b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+    });
+  }
+  __device__ __forceinline__ void operator()(float (&v)[VW]) const {
+    centre_scale_add(v, mu, a, b);
+    if constexpr (SILU) activate<T>(v);
+  }
+};
+
+// The same for the gradient: x -> h, dy -> du.
+template <typename T, int EV, bool SILU>
+struct GradValues {
+  static constexpr int VW = dev::Vec16<T>::N;
+  float mu[EV], rs[EV], ga[VW], be[VW];
+  __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
+                                       const T* __restrict__ beta, const float* mean, const float* inv) {
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
+      if (e < EV) {
+        mu[e] = mean[ng + g];
+        rs[e] = inv[ng + g];
+      }
+      ga[e] = dev::ld1_keep(gamma + c);
+      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
+    });
+  }
+  __device__ __forceinline__ void operator()(float (&v)[VW], float (&w)[VW]) const {
+    centre_scale(v, mu, rs);
+    if constexpr (SILU) {
+      float u[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) u[e] = be[e];
+      fma_pairs(v, ga, u);
+      activate_grad<T>(w, u);
+    }
+  }
+};
+
+// dx from h (in v) and du (in w): v <- rs (du gamma - m1 - h m2).
+template <typename T, int EV, bool SILU>
+struct GradApplyValues : GradValues<T, EV, SILU> {
+  static constexpr int VW = dev::Vec16<T>::N;
+  using Base = GradValues<T, EV, SILU>;
+  float a1[EV], a2[EV];  // -m1, -m2
+  __device__ __forceinline__ void load_means(int c0, int64_t ng, const GnDims& d, const float* m1, const float* m2) {
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
+      if (e < EV) {
+        a1[e] = -__ldcg(m1 + ng + g);
+        a2[e] = -__ldcg(m2 + ng + g);
+      }
+    });
+  }
+  __device__ __forceinline__ void dx(float (&v)[VW], float (&w)[VW]) const {
+    (*this)(v, w);
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 t = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(Base::ga[e], Base::ga[e + 1]),
+                                  pair_of<VW>(a1, e));
+      const float2 r = __fmul2_rn(__ffma2_rn(make_float2(v[e], v[e + 1]), pair_of<VW>(a2, e), t),
+                                  pair_of<VW>(Base::rs, e));
+      v[e] = r.x;
+      v[e + 1] = r.y;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Staged walk rows (C % VW == 0, 16-byte-aligned operands: every fragment is
+// whole, and a sample's last walk row may be shorter): a producer thread bulk-copies the rows
+// of its CTA's items into a ring of shared-memory stages, the consumers (one to
+// a fragment column) read them from there.  The copies in flight cost no
+// registers: measured against loads into registers, where two CTAs an SM had
+// 32 KB in flight, the passes take less than half the time.
+// Stages are handed over by mbarriers (tma_pipe.cuh), with bounded waits; a
+// consumer whose wait ran out takes no more rows but stays in step with the
+// block's barriers.
+// ---------------------------------------------------------------------------
+
+constexpr int kStageBytes = 16384;   // of all operands together
+constexpr int kStages = 4;
+constexpr int kStageSmem = kStages * kStageBytes;
+
+struct StageBars {
+  uint64_t full[kStages], empty[kStages];
+};
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+template <typename T, int NOPS>
+struct RowStream {
+  static constexpr int VW = dev::Vec16<T>::N;
+  StageBars* bars;
+  unsigned char* smem;
+  int rows;            // walk rows in a stage
+  int row_bytes;       // of this tile
+  int64_t total;       // walk rows of a sample
+  int64_t frags, row_frags;  // fragments of a sample, of a walk row
+  dev::Ring ring;
+  bool ok = true;
+
+  __device__ __forceinline__ RowStream(StageBars* b, unsigned char* m, const GnDims& d, const Tile& t)
+      : bars(b), smem(m), row_bytes(t.frags * 16), ring(kStages) {
+    rows = kStageBytes / NOPS / row_bytes;  // >= 2: a tile has at most kWalkThreads fragments
+    frags = d.L / VW;
+    row_frags = d.p.row_frags;
+    total = (frags + row_frags - 1) / row_frags;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        dev::mbar_init(&bars->full[i], 1);
+        dev::mbar_init(&bars->empty[i], (blockDim.x - 32) / 32);
+      }
+      dev::mbar_init_fence();
+    }
+    __syncthreads();
+  }
+
+  // Walk rows of a sample that have a fragment j.
+  __device__ __forceinline__ int64_t of_column(int64_t j) const { return (frags - j + row_frags - 1) / row_frags; }
+
+  // The producer: the rows of all the CTA's items.
+  __device__ __forceinline__ void produce(const T* const (&base)[NOPS], const GnDims& d, const Tile& t, bool reversed,
+                                          uint64_t policy) {
+    const WalkPlan& p = d.p;
+    int64_t n_filled = 0;
+    for (Items it(d, reversed); it.more(); it.next()) {
+      const Range range(p, it.item(), total);
+      for (int64_t r = range.ra; r < range.rb; r += rows, ring.next(), ++n_filled) {
+        if (n_filled >= kStages && !dev::mbar_wait(&bars->empty[ring.st], ring.phase ^ 1u)) {
+          // the copies in flight land before the block ends
+          for (int64_t k = n_filled - kStages; k < n_filled; ++k)
+            dev::mbar_wait(&bars->full[k % kStages], uint32_t((k / kStages) & 1));
+          return;
+        }
+        const int64_t f0 = range.n * frags + r * p.row_frags + int64_t(t.tile) * p.tile_frags;
+        const int k = static_cast<int>(min(int64_t(rows), range.rb - r));
+        unsigned char* dst = smem + ring.st * kStageBytes;
+        if (p.tiles == 1) {  // contiguous; the sample's last walk row may be short
+          const uint32_t bytes = uint32_t(min(int64_t(k) * p.row_frags, frags - r * p.row_frags)) * 16u;
+          dev::mbar_arrive_expect_tx(&bars->full[ring.st], NOPS * bytes);
+#pragma unroll
+          for (int o = 0; o < NOPS; ++o)
+            dev::bulk_g2s(dst + o * (kStageBytes / NOPS), base[o] + f0 * VW, bytes, &bars->full[ring.st], policy);
+        } else {
+          dev::mbar_arrive_expect_tx(&bars->full[ring.st], uint32_t(NOPS * k * row_bytes));
+          for (int i = 0; i < k; ++i)
+#pragma unroll
+            for (int o = 0; o < NOPS; ++o)
+              dev::bulk_g2s(dst + o * (kStageBytes / NOPS) + i * row_bytes, base[o] + (f0 + i * p.row_frags) * VW,
+                            uint32_t(row_bytes), &bars->full[ring.st], policy);
+        }
+      }
+    }
+  }
+
+  // A consumer: f(row, raw) for the walk rows [ra, rb) of an item; `mine` and
+  // rows below `r1` for the thread's own fragment column.
+  template <typename F>
+  __device__ __forceinline__ void consume(int64_t ra, int64_t rb, int64_t r1, bool mine, F f) {
+    for (int64_t r = ra; r < rb; r += rows, ring.next()) {
+      ok = ok && dev::mbar_wait(&bars->full[ring.st], ring.phase);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        continue;
+      }
+      const unsigned char* src = smem + ring.st * kStageBytes + threadIdx.x * 16;
+      const int k = mine ? static_cast<int>(min(int64_t(rows), r1 - r)) : 0;
+      for (int i = 0; i < k; ++i) {
+        uint4 raw[NOPS];
+#pragma unroll
+        for (int o = 0; o < NOPS; ++o) raw[o] = dev::lds16(src + o * (kStageBytes / NOPS) + i * row_bytes);
+        f(r + i, raw);
+      }
+      dev::release_stage(&bars->empty[ring.st]);
+    }
+  }
+};
+
+// The barrier of a staged kernel's consumers.
+__device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blockDim.x - 32); }
+
+// Pass 1.  partial: [item][tile][G] x (count, mean, M2), relative to the group's
+// first value, or, where a sample has one item and one tile, the statistics
+// themselves (partial == nullptr).  A thread sums its values and their squares
+// relative to a centre among its own (its first value of the channel; GROUP: its
+// first fragment's mean).  Cancellation then costs at most u times the thread's
+// row count, however far off that value is: what lies that far off makes up the
+// group's variance.
+template <typename T, bool GROUP>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_stats_staged(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = GROUP ? 1 : VW;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  __shared__ float s_cnt[kWalkThreads * EV], s_mean[kWalkThreads * EV], s_m2[kWalkThreads * EV];
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 1> rows(&bars, smem, d, t);
   dev::pdl_wait();
   dev::pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
-  const float scale = 1.0f / (float(d.S) * float(d.D));
-  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < d.N * d.G; i += int64_t(gridDim.x) * 8) {
-    const float2* src = reinterpret_cast<const float2*>(gpart) + (i / d.G) * parts * d.G + i % d.G;
-    float a = 0.f, b = 0.f;
-#pragma unroll 4
-    for (int64_t k = lane; k < parts; k += 32) {
-      const float2 v = __ldcg(src + k * d.G);
-      a += v.x;
-      b += v.y;
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[1] = {x};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, policy_evict_normal());
+    return;
+  }
+  const int c0 = first_channel(t.j, VW, 0, d.C);
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    const T* xs = x + r.n * d.L;
+    float first[EV], c[EV], s[VW], q[VW];
+#pragma unroll
+    for (int e = 0; e < EV; ++e) first[e] = c[e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
+    if (t.mine)
+      for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
+        if (e < EV) first[e] = dev::ld1_keep(xs + int64_t(g) * d.D);
+      });
+    const int64_t r1 = min(r.rb, rows.of_column(t.j));
+    rows.consume(r.ra, r.rb, r1, t.mine, [&](int64_t row, const uint4 (&raw)[1]) {
+      float v[VW];
+      dev::Conv<T>::unpack(raw[0], v);
+      if (row == r.ra) {
+        if constexpr (EV == 1) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) m += v[e] - v[0];
+          c[0] = fmaf(m, 1.0f / VW, v[0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) c[e] = v[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) {
+        const float2 m = pair_of<VW>(c, e);
+        const float2 w = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m.x, -m.y));
+        v[e] = w.x;
+        v[e + 1] = w.y;
+      }
+      dev::add_pairs(s, v);
+      fma_pairs(v, v, q);
+    });
+    if (t.mine) {
+      if constexpr (EV == 1) {
+#pragma unroll
+        for (int e = 1; e < VW; ++e) {
+          s[0] += s[e];
+          q[0] += q[e];
+        }
+      }
+      const float cnt = r.ra < r1 ? float(r1 - r.ra) * (VW / EV) : 0.f;
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        const float m = cnt > 0.f ? s[e] / cnt : 0.f;
+        s_cnt[threadIdx.x * EV + e] = cnt;
+        s_mean[threadIdx.x * EV + e] = cnt > 0.f ? (c[e] - first[e]) + m : 0.f;
+        s_m2[threadIdx.x * EV + e] = not_negative(q[e] - s[e] * m);
+      }
     }
-    a = dev::warp_sum(a);
-    b = dev::warp_sum(b);
-    if (lane == 0) {
-      m1[i] = a * scale;
-      m2[i] = b * scale;
+    consumer_sync();
+    join_statistics<T, EV>(d, t, r, it.item(), 0, xs, consumers / 32, s_cnt, s_mean, s_m2, partial, mean_out, inv_out);
+    consumer_sync();
+  }
+}
+
+// Pass 2: y from x and the statistics, over the items in reverse: what pass 1
+// read last is in L2.
+template <typename T, bool GROUP, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+                  const float* inv, T* y, GnDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 1> rows(&bars, smem, d, t);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[1] = {x};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
+    return;
+  }
+  const int c0 = first_channel(t.j, VW, 0, d.C);
+  for (Items it(d, true); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    ApplyValues<T, GROUP ? 1 : VW, SILU> val;
+    if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+    T* py = y + r.n * d.L + t.j * VW;
+    const int64_t pitch = p.row_frags * VW;
+    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t row, const uint4 (&raw)[1]) {
+      float v[VW];
+      dev::Conv<T>::unpack(raw[0], v);
+      val(v);
+      dev::st16_stream(py + row * pitch, dev::Conv<T>::pack(v));
+    });
+  }
+}
+
+// Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
+// groups' sums of each item.
+//   gpart: [item][tile][G] x (sum du gamma, sum du gamma h); cpart: leave_channel_sums
+template <typename T, bool GROUP, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
+                      const float* mean, const float* inv, GnDims d, float* gpart, float* cpart) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int EV = GROUP ? 1 : VW;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 2> rows(&bars, smem, d, t);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[2] = {x, dy};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, policy_evict_normal());
+    return;
+  }
+  const int c0 = first_channel(t.j, VW, 0, d.C);
+  float tot_a[VW], tot_b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    GradValues<T, EV, SILU> val;
+    if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+    float sa[VW], sb[VW];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
+    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t, const uint4 (&raw)[2]) {
+      float v[VW], w[VW];
+      dev::Conv<T>::unpack(raw[0], v);
+      dev::Conv<T>::unpack(raw[1], w);
+      val(v, w);
+      dev::add_pairs(sa, w);
+      fma_pairs(w, v, sb);
+    });
+    if (t.mine) {
+      dev::add_pairs(tot_a, sa);
+      dev::add_pairs(tot_b, sb);
+      if constexpr (GROUP) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          a = fmaf(sa[e], val.ga[e], a);
+          b = fmaf(sb[e], val.ga[e], b);
+        }
+        s_a[threadIdx.x] = a;
+        s_b[threadIdx.x] = b;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
+          s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
+        }
+      }
+    }
+    consumer_sync();
+    join_group_sums<T, EV>(d, t, it.item(), 0, consumers / 32, s_a, s_b, gpart);
+    consumer_sync();
+  }
+  if (cpart != nullptr) leave_channel_sums<T>(d, t, 0, consumers, tot_a, tot_b, s_a, s_b, cpart, consumer_sync);
+}
+
+// Gradient, pass 2: dx, over the items in reverse.
+template <typename T, bool GROUP, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
+                       const float* mean, const float* inv, const float* m1, const float* m2, T* dx, GnDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 2> rows(&bars, smem, d, t);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[2] = {x, dy};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
+    return;
+  }
+  const int c0 = first_channel(t.j, VW, 0, d.C);
+  for (Items it(d, true); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    GradApplyValues<T, GROUP ? 1 : VW, SILU> val;
+    if (t.mine) {
+      val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+      val.load_means(c0, r.n * d.G, d, m1, m2);
+    }
+    T* po = dx + r.n * d.L + t.j * VW;
+    const int64_t pitch = p.row_frags * VW;
+    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t row, const uint4 (&raw)[2]) {
+      float v[VW], w[VW];
+      dev::Conv<T>::unpack(raw[0], v);
+      dev::Conv<T>::unpack(raw[1], w);
+      val.dx(v, w);
+      dev::st16_stream(po + row * pitch, dev::Conv<T>::pack(v));
+    });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The same four passes for any C and alignment: fragments are checked against
+// the sample's ends, and a sample may start off a 16-byte boundary (VEC: whole
+// fragments are loaded as 16 bytes; else value by value).
+// ---------------------------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  __shared__ float s_cnt[kWalkThreads * VW], s_mean[kWalkThreads * VW], s_m2[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), p.rows);
+    const T* xs = x + r.n * d.L;
+    const int off = walk_offset<T, true>(xs);
+    if (t.mine) {
+      float first[VW], c[VW], s[VW], q[VW], cnt[VW];
+      for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D,
+                       [&](int e, int, int g) { first[e] = dev::ld1_keep(xs + int64_t(g) * d.D); });
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        c[e] = first[e];  // then the first value that the channel meets here
+        s[e] = q[e] = cnt[e] = 0.f;
+      }
+      for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
+        float v[U][VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (r0 + u < r.rb) dev::load_frag<T, true>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            if (r0 + u < r.rb && e0 + e >= 0 && e0 + e < d.L) {
+              if (cnt[e] == 0.f) c[e] = v[u][e];
+              const float w = v[u][e] - c[e];
+              cnt[e] += 1.f;
+              s[e] += w;
+              q[e] = fmaf(w, w, q[e]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const float m = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
+        s_cnt[threadIdx.x * VW + e] = cnt[e];
+        s_mean[threadIdx.x * VW + e] = (c[e] - first[e]) + m;
+        s_m2[threadIdx.x * VW + e] = not_negative(q[e] - s[e] * m);
+      }
+    }
+    __syncthreads();
+    join_statistics<T, VW>(d, t, r, it.item(), off, xs, blockDim.x / 32, s_cnt, s_mean, s_m2, partial, mean_out,
+                           inv_out);
+    __syncthreads();
+  }
+}
+
+template <typename T, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean, const float* inv,
+           T* y, GnDims d) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 4;
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  if (!t.mine) return;
+  for (Items it(d, true); it.more(); it.next()) {
+    const Range r(p, it.item(), p.rows);
+    const T* xs = x + r.n * d.L;
+    T* ys = y + r.n * d.L;
+    const int off = walk_offset<T, VEC>(xs);
+    ApplyValues<T, VW, SILU> val;
+    val.load(first_channel(t.j, VW, off, d.C), r.n * d.G, d, gamma, beta, mean, inv);
+    for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
+      float v[U][VW];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (r0 + u < r.rb) dev::load_frag<T, VEC>(xs, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u < r.rb) {
+          val(v[u]);
+          dev::store_frag<T, VEC>(ys, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+        }
+      }
     }
   }
 }
 
-// Gradient, pass 2: dx.
-template <typename T, int FORM, bool VEC, bool SILU>
+// A CTA's items share `off` (the launch sees to it), so a thread's channels stay
+// the same and its sums run on over them.
+template <typename T, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads)
+k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
+               const float* inv, GnDims d, float* gpart, float* cpart) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int U = 2;
+  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  float tot_a[VW], tot_b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
+  int off = 0;
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), p.rows);
+    const T* xs = x + r.n * d.L;
+    const T* ds = dy + r.n * d.L;
+    off = walk_offset<T, VEC>(xs);
+    if (t.mine) {
+      GradValues<T, VW, SILU> val;
+      val.load(first_channel(t.j, VW, off, d.C), r.n * d.G, d, gamma, beta, mean, inv);
+      float sa[VW], sb[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
+      for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
+        float v[U][VW], w[U][VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
+          if (r0 + u < r.rb) {
+            dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+            dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);  // 0 outside the sample: adds nothing
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (r0 + u < r.rb) {
+            val(v[u], w[u]);
+            dev::add_pairs(sa, w[u]);
+            fma_pairs(w[u], v[u], sb);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
+        s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
+        tot_a[e] += sa[e];
+        tot_b[e] += sb[e];
+      }
+    }
+    __syncthreads();
+    join_group_sums<T, VW>(d, t, it.item(), off, blockDim.x / 32, s_a, s_b, gpart);
+    __syncthreads();
+  }
+  if (cpart != nullptr)
+    leave_channel_sums<T>(d, t, off, int(blockDim.x), tot_a, tot_b, s_a, s_b, cpart, [] { __syncthreads(); });
+}
+
+template <typename T, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                 const float* inv, const float* m1, const float* m2, T* dx, GnDims d) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int EV = FORM == kGroup ? 1 : VW;
-  constexpr int U = sizeof(T) == 4 ? 4 : 2;
+  constexpr int U = 2;
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
-  const Tile t(p, FORM == kAny ? -1 : d.L / VW);
+  const Tile t(p);
   if (!t.mine) return;
-  const int64_t items = d.N * p.chunks;
-  for (int64_t item = blockIdx.x / unsigned(p.tiles); item < items; item += gridDim.x / unsigned(p.tiles)) {
-    const int64_t n = item / p.chunks, chunk = item - n * p.chunks;
-    const T* xs = x + n * d.L;
-    const T* ds = dy + n * d.L;
-    T* os = dx + n * d.L;
-    const int off = walk_offset<T, FORM, VEC>(xs);
+  for (Items it(d, true); it.more(); it.next()) {
+    const Range r(p, it.item(), p.rows);
+    const T* xs = x + r.n * d.L;
+    const T* ds = dy + r.n * d.L;
+    T* os = dx + r.n * d.L;
+    const int off = walk_offset<T, VEC>(xs);
     const int c0 = first_channel(t.j, VW, off, d.C);
-    GradValues<T, EV, SILU> val;
-    val.load(c0, n * d.G, d, gamma, beta, mean, inv);
-    float a1[EV], a2[EV];
-    for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
-      if (e < EV) {
-        a1[e] = __ldcg(m1 + n * d.G + g);
-        a2[e] = __ldcg(m2 + n * d.G + g);
-      }
-    });
-    auto value = [&](float (&v)[VW], float (&w)[VW]) {  // x, dy -> dx in v
-      val(v, w);
+    GradApplyValues<T, VW, SILU> val;
+    val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+    val.load_means(c0, r.n * d.G, d, m1, m2);
+    for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
+      float v[U][VW], w[U][VW];
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        const int i = EV == 1 ? 0 : e;
-        v[e] = val.rs[i] * (fmaf(w[e], val.ga[e], -a1[i]) - v[e] * a2[i]);
-      }
-    };
-    const int64_t ra = chunk * p.rows_per_chunk, rb = min(t.rows, ra + p.rows_per_chunk);
-    if constexpr (FORM != kAny) {
-      const int64_t pitch = p.row_frags * VW, at = (ra * p.row_frags + t.j) * VW;
-      const T* px = xs + at;
-      const T* pd = ds + at;
-      T* po = os + at;
-      int64_t r = ra;
-      for (; r + U <= rb; r += U, px += U * pitch, pd += U * pitch, po += U * pitch) {
-        uint4 rx[U], rd[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          rx[u] = dev::ld16_stream(px + u * pitch);
-          rd[u] = dev::ld16_stream(pd + u * pitch);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[VW], w[VW];
-          dev::Conv<T>::unpack(rx[u], v);
-          dev::Conv<T>::unpack(rd[u], w);
-          value(v, w);
-          dev::st16_stream(po + u * pitch, dev::Conv<T>::pack(v));
+      for (int u = 0; u < U; ++u) {
+        const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
+        if (r0 + u < r.rb) {
+          dev::load_frag<T, VEC>(xs, e0, d.L, v[u]);
+          dev::load_frag<T, VEC>(ds, e0, d.L, w[u]);
         }
       }
-      for (; r < rb; ++r, px += pitch, pd += pitch, po += pitch) {
-        float v[VW], w[VW];
-        dev::Conv<T>::unpack(dev::ld16_stream(px), v);
-        dev::Conv<T>::unpack(dev::ld16_stream(pd), w);
-        value(v, w);
-        dev::st16_stream(po, dev::Conv<T>::pack(v));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u < r.rb) {
+          val.dx(v[u], w[u]);
+          dev::store_frag<T, VEC>(os, ((r0 + u) * p.row_frags + t.j) * VW - off, d.L, v[u]);
+        }
       }
-    } else {
-      for (int64_t r = ra; r < rb; ++r) {
-        const int64_t e0 = (r * p.row_frags + t.j) * VW - off;
-        float v[VW], w[VW];
-        dev::load_frag<T, VEC>(xs, e0, d.L, v);
-        dev::load_frag<T, VEC>(ds, e0, d.L, w);
-        value(v, w);
-        dev::store_frag<T, VEC>(os, e0, d.L, v);
-      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joining a group's chunks and tiles.  THREADS (a warp, or a block where there
+// are many parts) take one (n, g); bound by the latency of a few reads.
+// ---------------------------------------------------------------------------
+
+constexpr int kJoinThreads = 256;
+
+template <int THREADS>
+__device__ __forceinline__ float join_sum(float x, float* red) {
+  x = dev::warp_sum(x);
+  if constexpr (THREADS > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) x += red[w];
+  }
+  return x;
+}
+
+// (count, mean, M2) of the parts -> the group's statistics.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(kJoinThreads)
+k_gn_join(const T* x, const float* partial, GnDims d, float* mean_out, float* inv_out) {
+  __shared__ float red[kJoinThreads / 32];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int t = threadIdx.x % THREADS;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kJoinThreads / THREADS;
+  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(gridDim.x) * per) {
+    const float* src = partial + ((i / d.G) * parts * d.G + i % d.G) * 3;
+    float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
+#pragma unroll 4
+    for (int64_t k = t; k < parts; k += THREADS) {
+      const float* e = src + k * d.G * 3;
+      const float n = __ldcg(e);
+      c += n;
+      s = fmaf(n, __ldcg(e + 1), s);
+    }
+    c = join_sum<THREADS>(c, red);
+    s = join_sum<THREADS>(s, red);
+    const float mg = s / c;
+#pragma unroll 4
+    for (int64_t k = t; k < parts; k += THREADS) {
+      const float* e = src + k * d.G * 3;
+      const float w = __ldcg(e + 1) - mg, n = __ldcg(e);
+      res = fmaf(n, w, res);
+      q += fmaf(n * w, w, __ldcg(e + 2));
+    }
+    res = join_sum<THREADS>(res, red);
+    q = join_sum<THREADS>(q, red);
+    if (t == 0) {
+      const float fix = res / c;
+      mean_out[i] = dev::ld1_keep(x + i / d.G * d.L + i % d.G * d.D) + (mg + fix);
+      inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
+    }
+  }
+}
+
+// The gradient's sums of the parts -> m1, m2 of each (n, g).
+template <int THREADS>
+__global__ void __launch_bounds__(kJoinThreads)
+k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
+  __shared__ float red[kJoinThreads / 32];
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int t = threadIdx.x % THREADS;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kJoinThreads / THREADS;
+  const float scale = 1.0f / (float(d.S) * float(d.D));
+  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(gridDim.x) * per) {
+    const float2* src = reinterpret_cast<const float2*>(gpart) + (i / d.G) * parts * d.G + i % d.G;
+    float a = 0.f, b = 0.f;
+#pragma unroll 4
+    for (int64_t k = t; k < parts; k += THREADS) {
+      const float2 v = __ldcg(src + k * d.G);
+      a += v.x;
+      b += v.y;
+    }
+    a = join_sum<THREADS>(a, red);
+    b = join_sum<THREADS>(b, red);
+    if (t == 0) {
+      m1[i] = a * scale;
+      m2[i] = b * scale;
     }
   }
 }
@@ -701,7 +977,7 @@ int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
 GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
   GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, {}};
-  d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 4, 4);
+  d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
   return d;
 }
 
@@ -711,7 +987,7 @@ int64_t cta_rows_of(const GnDims& d, int64_t most_ctas) {
 }
 
 bool split_parts(const GnDims& d) { return d.p.chunks > 1 || d.p.tiles > 1; }
-int64_t grad_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 4); }
+int64_t grad_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 2); }
 
 // Offset in bytes of the next array in a workspace: each starts on 16 bytes.
 size_t pad16(size_t b) { return (b + 15) / 16 * 16; }
@@ -746,12 +1022,36 @@ GnGradWorkspace gn_grad_workspace(const GnDims& d, DType t) {
 
 inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uintptr_t>(p) & 15u); }
 
+// A warp for each (n, g), or a block where there are more parts than a warp takes at once.
+inline bool join_by_block(const GnDims& d) { return int64_t(d.p.chunks) * d.p.tiles > 64; }
 inline unsigned join_grid(const GnDims& d) {
-  return unsigned(std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms * 8));
+  const int64_t per = join_by_block(d) ? 1 : kJoinThreads / 32;
+  return unsigned(std::min<int64_t>((d.N * d.G + per - 1) / per, kPlanSms * 8));
+}
+
+// Staged kernels: CTAs of consumers and a producer warp, two an SM.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_staged(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cudaStream_t stream, int* launches,
+                          Args... args) {
+  int per_sm = 1;
+  const int threads = d.p.threads + 32;
+  cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, kStageSmem, &per_sm);
+  if (e != cudaSuccess) return e;
+  e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(threads), kStageSmem, stream, args...);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_plain(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cudaStream_t stream, int* launches,
+                         Args... args) {
+  const cudaError_t e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), 0, stream, args...);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
 }
 
 template <typename T>
-cudaError_t group_norm_t(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launches) {
+  constexpr int VW = dev::Vec16<T>::N;
   const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps);
   const GnWorkspace w = gn_workspace(d);
   char* ws = static_cast<char*>(a.workspace);
@@ -762,34 +1062,36 @@ cudaError_t group_norm_t(const GroupNormArgs& a, int sm_count, cudaStream_t stre
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* beta = static_cast<const T*>(a.beta);
   T* y = static_cast<T*>(a.y);
-  const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles)), block(d.p.threads);
-  const int whole = a.C % dev::Vec16<T>::N == 0 ? (d.D % dev::Vec16<T>::N == 0 ? kGroup : kChannel) : kAny;
-  const int form1 = misalign16(x) == 0 ? whole : kAny;  // statistics need no alignment of y
-  auto f1 = form1 == kGroup ? k_gn_stats<T, kGroup> : form1 == kChannel ? k_gn_stats<T, kChannel> : k_gn_stats<T, kAny>;
-  cudaError_t e = launch(f1, grid, block, 0, stream, x, d, partial, mean, inv);
+  const int64_t rows = cta_rows_of(d, kPlanSms * 2);
+  // the staged passes want whole fragments; the statistics need no alignment of y
+  const bool staged = a.C % VW == 0 && misalign16(x) == 0, group = d.D % VW == 0;
+  const bool vec = misalign16(x) == misalign16(y);
+  cudaError_t e;
+  if (staged) {
+    auto f = group ? k_gn_stats_staged<T, true> : k_gn_stats_staged<T, false>;
+    e = launch_staged(f, rows, d, stream, launches, x, d, partial, mean, inv);
+  } else {
+    e = launch_plain(k_gn_stats<T>, rows, d, stream, launches, x, d, partial, mean, inv);
+  }
   if (e != cudaSuccess) return e;
-  *launches += 1;
   if (partial != nullptr) {
-    e = launch(k_gn_join<T>, dim3(join_grid(d)), dim3(256), 0, stream, x, partial, d, mean, inv);
+    auto f = join_by_block(d) ? k_gn_join<T, kJoinThreads> : k_gn_join<T, 32>;
+    e = launch(f, dim3(join_grid(d)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
-  const bool vec = misalign16(x) == misalign16(y);
-  auto pick = [&](auto silu) {
-    constexpr bool kSilu = decltype(silu)::value;
-    if (!vec) return k_gn_apply<T, kAny, false, kSilu>;
-    return form1 == kGroup     ? k_gn_apply<T, kGroup, true, kSilu>
-           : form1 == kChannel ? k_gn_apply<T, kChannel, true, kSilu>
-                               : k_gn_apply<T, kAny, true, kSilu>;
-  };
-  auto fn = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
-  e = launch(fn, grid, block, 0, stream, x, gamma, beta, mean, inv, y, d);
-  if (e == cudaSuccess) *launches += 1;
-  return e;
+  if (staged && vec) {
+    auto f = group ? (a.silu ? k_gn_apply_staged<T, true, true> : k_gn_apply_staged<T, true, false>)
+                   : (a.silu ? k_gn_apply_staged<T, false, true> : k_gn_apply_staged<T, false, false>);
+    return launch_staged(f, rows, d, stream, launches, x, gamma, beta, mean, inv, y, d);
+  }
+  auto f = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
+               : (a.silu ? k_gn_apply<T, false, true> : k_gn_apply<T, false, false>);
+  return launch_plain(f, rows, d, stream, launches, x, gamma, beta, mean, inv, y, d);
 }
 
 template <typename T>
-cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
   const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f);
   const GnGradWorkspace w = gn_grad_workspace(d, a.t);
@@ -806,42 +1108,41 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, int sm_count, cudaStre
   const int64_t rows = grad_rows(d);
   // whole fragments need x and dy (and dx) at one offset within 16 bytes, and
   // one walk offset for all the samples that a CTA takes
-  const bool one_off = d.L % VW == 0 || rows >= d.N * d.p.chunks;
-  const bool vec1 = misalign16(x) == misalign16(dy) && one_off;
-  const bool vec2 = misalign16(x) == misalign16(dy) && misalign16(x) == misalign16(dx);
-  const int whole = misalign16(x) != 0 || a.C % VW != 0 ? kAny : d.D % VW == 0 ? kGroup : kChannel;
-  auto pick1 = [&](auto silu) {
-    constexpr bool kSilu = decltype(silu)::value;
-    if (!vec1) return k_gn_grad_sums<T, kAny, false, kSilu>;
-    return whole == kGroup     ? k_gn_grad_sums<T, kGroup, true, kSilu>
-           : whole == kChannel ? k_gn_grad_sums<T, kChannel, true, kSilu>
-                               : k_gn_grad_sums<T, kAny, true, kSilu>;
-  };
-  auto f1 = a.silu ? pick1(std::true_type{}) : pick1(std::false_type{});
-  cudaError_t e = launch(f1, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean,
-                         a.inv, d, gpart, cpart);
+  const bool same = misalign16(x) == misalign16(dy);
+  const bool staged = a.C % VW == 0 && misalign16(x) == 0 && same, group = d.D % VW == 0;
+  const bool vec1 = same && (d.L % VW == 0 || rows >= d.N * d.p.chunks);
+  const bool vec2 = same && misalign16(x) == misalign16(dx);
+  cudaError_t e;
+  if (staged) {
+    auto f = group ? (a.silu ? k_gn_grad_sums_staged<T, true, true> : k_gn_grad_sums_staged<T, true, false>)
+                   : (a.silu ? k_gn_grad_sums_staged<T, false, true> : k_gn_grad_sums_staged<T, false, false>);
+    e = launch_staged(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
+  } else {
+    auto f = vec1 ? (a.silu ? k_gn_grad_sums<T, true, true> : k_gn_grad_sums<T, true, false>)
+                  : (a.silu ? k_gn_grad_sums<T, false, true> : k_gn_grad_sums<T, false, false>);
+    e = launch_plain(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
+  }
+  if (e != cudaSuccess) return e;
+  auto join = join_by_block(d) ? k_gn_grad_join<kJoinThreads> : k_gn_grad_join<32>;
+  e = launch(join, dim3(join_grid(d)), dim3(kJoinThreads), 0, stream, gpart, d, m1, m2);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  e = launch(k_gn_grad_join, dim3(join_grid(d)), dim3(256), 0, stream, gpart, d, m1, m2);
+  if (staged && vec2) {
+    auto f = group ? (a.silu ? k_gn_grad_apply_staged<T, true, true> : k_gn_grad_apply_staged<T, true, false>)
+                   : (a.silu ? k_gn_grad_apply_staged<T, false, true> : k_gn_grad_apply_staged<T, false, false>);
+    e = launch_staged(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
+  } else {
+    auto f = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
+                  : (a.silu ? k_gn_grad_apply<T, false, true> : k_gn_grad_apply<T, false, false>);
+    e = launch_plain(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
+  }
   if (e != cudaSuccess) return e;
-  *launches += 1;
-  auto pick2 = [&](auto silu) {
-    constexpr bool kSilu = decltype(silu)::value;
-    if (!vec2) return k_gn_grad_apply<T, kAny, false, kSilu>;
-    return whole == kGroup     ? k_gn_grad_apply<T, kGroup, true, kSilu>
-           : whole == kChannel ? k_gn_grad_apply<T, kChannel, true, kSilu>
-                               : k_gn_grad_apply<T, kAny, true, kSilu>;
-  };
-  auto f2 = a.silu ? pick2(std::true_type{}) : pick2(std::false_type{});
-  const dim3 grid(unsigned(cta_rows_of(d, int64_t(sm_count) * 8) * d.p.tiles));
-  e = launch(f2, grid, dim3(d.p.threads), 0, stream, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
-  if (e != cudaSuccess) return e;
-  *launches += 1;
   if (cpart != nullptr) {
-    const int64_t jobs = std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, INT_MAX);
+    const int64_t jobs = (int64_t(d.C) + 31) / 32 * 2;
     // the sums of du are dbeta, those of du * h are dgamma
     e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart, rows,
-               d.p.tiles > 1 ? d.p.reps : int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
+               d.p.tiles > 1 ? d.p.reps : int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta),
+               static_cast<T*>(a.dgamma));
     if (e == cudaSuccess) *launches += 1;
   }
   return e;
@@ -863,9 +1164,9 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
   const cudaError_t e = launch_group_norm_fused(a, sm_count, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
   switch (a.t) {
-    case DType::F32: return group_norm_t<float>(a, sm_count, stream, launches);
-    case DType::F16: return group_norm_t<__half>(a, sm_count, stream, launches);
-    default: return group_norm_t<__nv_bfloat16>(a, sm_count, stream, launches);
+    case DType::F32: return group_norm_t<float>(a, stream, launches);
+    case DType::F16: return group_norm_t<__half>(a, stream, launches);
+    default: return group_norm_t<__nv_bfloat16>(a, stream, launches);
   }
 }
 
@@ -874,10 +1175,12 @@ cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cud
   const cudaError_t e = launch_group_norm_grad_fused(a, sm_count, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
   switch (a.t) {
-    case DType::F32: return group_norm_grad_t<float>(a, sm_count, stream, launches);
-    case DType::F16: return group_norm_grad_t<__half>(a, sm_count, stream, launches);
-    default: return group_norm_grad_t<__nv_bfloat16>(a, sm_count, stream, launches);
+    case DType::F32: return group_norm_grad_t<float>(a, stream, launches);
+    case DType::F16: return group_norm_grad_t<__half>(a, stream, launches);
+    default: return group_norm_grad_t<__nv_bfloat16>(a, stream, launches);
   }
 }
+
+cudaError_t group_norm_pipe_timeouts(unsigned int* count, bool clear) { return read_pipe_timeouts(count, clear); }
 
 }  // namespace ep

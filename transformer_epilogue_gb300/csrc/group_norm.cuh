@@ -48,6 +48,87 @@ __device__ __forceinline__ float silu_grad(float dy, float u) {
   return dy * (s * fmaf(u, 1.0f - s, 1.0f));
 }
 
+// The same on VW values, two to a packed float32 instruction where there is
+// one (each lane rounded as the scalar operation would).
+//   activate: v <- v * sigmoid(v);  activate_grad: w <- w * derivative at u
+template <typename T, int VW>
+__device__ __forceinline__ void activate(float (&v)[VW]) {
+  if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = silu<T>(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 u = make_float2(v[e], v[e + 1]);
+      const float2 t = __fmul2_rn(u, make_float2(-dev::kLog2e, -dev::kLog2e));
+      const float2 d = __fadd2_rn(make_float2(dev::ex2_approx(t.x), dev::ex2_approx(t.y)), make_float2(1.f, 1.f));
+      const float2 y = __fmul2_rn(u, make_float2(dev::rcp_approx(d.x), dev::rcp_approx(d.y)));
+      v[e] = y.x;
+      v[e + 1] = y.y;
+    }
+  }
+}
+template <typename T, int VW>
+__device__ __forceinline__ void activate_grad(float (&w)[VW], const float (&u)[VW]) {
+  if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) w[e] = silu_grad<T>(w[e], u[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 one = make_float2(1.f, 1.f);
+      const float2 u2 = make_float2(u[e], u[e + 1]), w2 = make_float2(w[e], w[e + 1]);
+      const float2 t = __fmul2_rn(u2, make_float2(-dev::kLog2e, -dev::kLog2e));
+      const float2 d = __fadd2_rn(make_float2(dev::ex2_approx(t.x), dev::ex2_approx(t.y)), one);
+      const float2 s = make_float2(dev::rcp_approx(d.x), dev::rcp_approx(d.y));
+      const float2 f = __ffma2_rn(u2, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one);
+      const float2 y = __fmul2_rn(__fmul2_rn(w2, s), f);
+      w[e] = y.x;
+      w[e + 1] = y.y;
+    }
+  }
+}
+
+// v <- (v - m) * k + b, and v <- (v - m) * k, each product and sum rounded once
+// (m, k: one value, or one for each element).
+template <int VW, int EV>
+__device__ __forceinline__ float2 pair_of(const float (&a)[EV], int e) {
+  return EV == 1 ? make_float2(a[0], a[0]) : make_float2(a[EV == 1 ? 0 : e], a[EV == 1 ? 0 : e + 1]);
+}
+template <int VW, int EV>
+__device__ __forceinline__ void centre_scale_add(float (&v)[VW], const float (&m)[EV], const float (&k)[VW],
+                                                 const float (&b)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; e += 2) {
+    const float2 m2 = pair_of<VW>(m, e);
+    const float2 t = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m2.x, -m2.y));
+    const float2 r = __ffma2_rn(t, make_float2(k[e], k[e + 1]), make_float2(b[e], b[e + 1]));
+    v[e] = r.x;
+    v[e + 1] = r.y;
+  }
+}
+template <int VW, int EV>
+__device__ __forceinline__ void centre_scale(float (&v)[VW], const float (&m)[EV], const float (&k)[EV]) {
+#pragma unroll
+  for (int e = 0; e < VW; e += 2) {
+    const float2 m2 = pair_of<VW>(m, e);
+    const float2 t = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m2.x, -m2.y));
+    const float2 r = __fmul2_rn(t, pair_of<VW>(k, e));
+    v[e] = r.x;
+    v[e + 1] = r.y;
+  }
+}
+// c <- a * b + c and c <- a * b, element by element.
+template <int VW>
+__device__ __forceinline__ void fma_pairs(const float (&a)[VW], const float (&b)[VW], float (&c)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; e += 2) {
+    const float2 r = __ffma2_rn(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]));
+    c[e] = r.x;
+    c[e + 1] = r.y;
+  }
+}
+
 // f(e, c, g) for the channels c (and their groups g) of the VW elements from c on, modulo C.
 template <int VW, typename F>
 __device__ __forceinline__ void for_channels(int c, int C, int D, F f) {

@@ -22,6 +22,7 @@
 //
 // What bounds it: small samples, the latency of load, two block reductions and
 // store; large batches, DRAM.
+#include <cstdlib>
 #include <algorithm>
 #include <climits>
 #include <numeric>
@@ -797,6 +798,8 @@ bool split_rows(FusedPlan* p, int64_t N, int64_t rows, int nv_max) {
     p->rows_per_cta = int(rows);
   } else {
     const int most = kMaxThreads / p->cf;  // rows side by side
+    static const int kMaxCluster = getenv("EPX_MAXK") ? atoi(getenv("EPX_MAXK")) : 16;
+    if (kMaxCluster == 0) return false;
     int64_t per = rows;
     int k = 1;
     while (k < kMaxCluster && ((per = (rows + k - 1) / k) + most - 1) / most > nv_max) k *= 2;
