@@ -95,6 +95,10 @@ __device__ __forceinline__ int misalignment(const T* p) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
 }
 
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -109,38 +113,42 @@ namespace {
 // arrays, r < terms, w < reps * C) -> out_b[c] = sum over r and over the w = c
 // mod C, in a fixed order, rounded once.  A block takes 32 channels; its warps
 // share the terms.  Bound by the latency of its reads: partials are a few per
-// cent of what the kernel before read.
-constexpr int kSumsThreads = 512;
+// cent of what the kernel before read.  Block `block` of `blocks`.
+constexpr int kSumsThreads = 1024;
+
+template <typename T>
+__device__ __forceinline__ void channel_sums(const float* partial, int64_t terms, int64_t reps, int64_t C, int buffers,
+                                             T* out0, T* out1, unsigned block, unsigned blocks) {
+  __shared__ float part[kSumsThreads / 32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned cblocks = unsigned((C + 31) / 32);
+  for (unsigned job = block; job < cblocks * buffers; job += blocks) {
+    const unsigned b = job / cblocks;
+    const int64_t c = int64_t(job - b * cblocks) * 32 + lane;
+    T* out = b == 0 ? out0 : out1;
+    const int64_t n = terms * reps;  // (r, k) with w = c + k * C: a row of C values each
+    const float* src = partial + int64_t(b) * n * C + c;
+    float acc = 0.f;
+    if (c < C && out != nullptr) {
+#pragma unroll 10
+      for (int64_t q = warp; q < n; q += kSumsThreads / 32) acc += __ldcg(src + q * C);
+    }
+    part[warp][lane] = acc;
+    __syncthreads();
+    // warp w adds up the columns of channel w
+    const float s = dev::warp_sum(part[lane][warp]);
+    const int64_t cw = int64_t(job - b * cblocks) * 32 + warp;
+    if (lane == 0 && cw < C && out != nullptr) dev::st1_stream(out + cw, s);
+    __syncthreads();
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kSumsThreads)
 k_channel_sums(const float* partial, int64_t terms, int64_t reps, int64_t C, int buffers, T* out0, T* out1) {
-  __shared__ float part[kSumsThreads / 32][33];
   dev::pdl_wait();
   dev::pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t cblocks = (C + 31) / 32;
-  for (int64_t job = blockIdx.x; job < cblocks * buffers; job += gridDim.x) {
-    const int b = static_cast<int>(job / cblocks);
-    const int64_t c = (job % cblocks) * 32 + lane;
-    T* out = b == 0 ? out0 : out1;
-    const float* src = partial + int64_t(b) * terms * reps * C;
-    float acc = 0.f;
-    if (c < C) {
-      const int64_t n = terms * reps;  // (r, k) with w = c + k * C: a row of C values each
-#pragma unroll 4
-      for (int64_t q = warp; q < n; q += kSumsThreads / 32) acc += __ldcg(src + q * C + c);
-    }
-    part[warp][lane] = acc;
-    __syncthreads();
-    if (warp == 0 && c < C && out != nullptr) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < kSumsThreads / 32; ++w) s += part[w][lane];
-      dev::st1_stream(out + c, s);
-    }
-    __syncthreads();
-  }
+  channel_sums<T>(partial, terms, reps, C, buffers, out0, out1, blockIdx.x, gridDim.x);
 }
 
 }  // namespace

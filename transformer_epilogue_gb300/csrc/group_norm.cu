@@ -40,8 +40,17 @@ struct GnDims {
   int64_t N, S, L;  // L = S * C
   int C, G, D;
   float eps;
+  // whole fragments of a sample, the walk rows that are full and the rest
+  int64_t frags, full_rows;
+  int rest;
+  bool pvec;  // gamma and beta 16-byte aligned (and every fragment's channels one after another)
   WalkPlan p;
 };
+
+// a / b where a mostly fits 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a <= int64_t(0xffffffffu) ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 
 // Where a sample's walk row starts: `off` elements before the sample.
 template <typename T, bool VEC>
@@ -51,7 +60,7 @@ __device__ __forceinline__ int walk_offset(const T* sample) {
 
 // The channel of the first element of fragment column j.
 __device__ __forceinline__ int first_channel(int64_t j, int vw, int off, int C) {
-  return static_cast<int>((j * vw + C - off % C) % C);
+  return static_cast<int>((unsigned(j) * unsigned(vw) + unsigned(C - off % C)) % unsigned(C));
 }
 
 // The first repeat k of a group whose channels [c0, c0 + D), at the positions
@@ -62,25 +71,48 @@ __device__ __forceinline__ int first_repeat(int p0, int off, int c0, int D, int 
   return (a >= 0 ? a / C : -((-a + C - 1) / C)) + 1;
 }
 
-// Calls f(i, c) for every position p0 + i of a tile of np positions that holds a
-// channel c of the group, by the lanes of a warp in turn: the lanes split into
-// sets of the smallest power of two that holds D channels (at most 32), each set
-// taking the repeats in turn, so that few channels still use (and sum over) all lanes.
-// (kGroup: positions are fragments, and C, D, c0 count fragments too.)
-template <typename F>
-__device__ __forceinline__ void for_group(int p0, int np, int off, int c0, int D, int C, F f) {
-  const int lane = threadIdx.x & 31;
-  const int set = D >= 32 ? 32 : D <= 1 ? 1 : 1 << (32 - __clz(D - 1));
-  const int64_t step = int64_t(C) * (32 / set);
-  for (int64_t a = off + c0 + int64_t(first_repeat(p0, off, c0, D, C) + lane / set) * C - p0; a < np; a += step) {
-    const int lo = static_cast<int>(max(int64_t(0), a)), hi = static_cast<int>(min(int64_t(np), a + D));
-    for (int i = lo + (lane & (set - 1)); i < hi; i += set) f(i, c0 + (i - static_cast<int>(a)));
+// The positions of a tile that hold a group's channels, by the lanes of a warp.
+// `cols` lanes (a power of two) stand side
+// by side over the group's channels, and as many of its repeats as fit a warp
+// next to each other, so that few channels still use (and sum over) all lanes.
+struct GroupWalk {
+  int np, C, D, reps, cols;
+  int p0;         // the tile's first position
+  bool whole;     // the tile is the walk row: positions wrap around
+  __device__ __forceinline__ GroupWalk(const WalkPlan& p, int tile, int frags, int C_, int D_, int vw) {
+    np = frags * vw;
+    C = C_;
+    D = D_;
+    whole = p.tiles == 1;
+    p0 = tile * p.tile_frags * vw;
+    reps = whole ? static_cast<int>(p.reps) : 0;
+    cols = D >= 32 ? 32 : D <= 1 ? 1 : 1 << (32 - __clz(D - 1));
   }
-}
-
-__device__ __forceinline__ bool group_in_tile(int p0, int np, int off, int c0, int D, int C) {
-  return off + c0 + int64_t(first_repeat(p0, off, c0, D, C)) * C < p0 + np;
-}
+  template <typename F>
+  __device__ __forceinline__ void run(int g, int off, F f) const {
+    const int lane = threadIdx.x & 31, j0 = lane & (cols - 1), ks = 32 / cols;
+    if (whole) {
+      const int start = off + g * D;
+      for (int k = lane / cols; k < reps; k += ks) {
+        for (int j = j0; j < D; j += cols) {
+          int pos = start + j + k * C;
+          if (pos >= np) pos -= np;
+          f(pos);
+        }
+      }
+    } else {
+      const int c0 = g * D;
+      for (int64_t a = off + c0 + int64_t(first_repeat(p0, off, c0, D, C) + lane / cols) * C - p0; a < np;
+           a += int64_t(C) * ks) {
+        const int lo = static_cast<int>(max(int64_t(0), a)), hi = static_cast<int>(min(int64_t(np), a + D));
+        for (int i = lo + j0; i < hi; i += cols) f(i);
+      }
+    }
+  }
+  __device__ __forceinline__ bool has(int g, int off) const {
+    return whole || off + g * D + int64_t(first_repeat(p0, off, g * D, D, C)) * C < p0 + np;
+  }
+};
 
 // A CTA's place: its tile of the walk row and its thread's fragment column.
 struct Tile {
@@ -113,36 +145,34 @@ struct Items {
 struct Range {
   int64_t n, ra, rb;
   __device__ __forceinline__ Range(const WalkPlan& p, int64_t item, int64_t rows) {
-    n = p.chunks == 1 ? item : item / p.chunks;
+    n = p.chunks == 1 ? item : quotient(item, p.chunks);
     ra = (item - n * p.chunks) * p.rows_per_chunk;
     rb = min(rows, ra + p.rows_per_chunk);
   }
 };
 
 // ---------------------------------------------------------------------------
-// Block epilogues, shared by the staged and the general kernels.  `sync` is the
-// barrier of the threads that take part.  Positions are elements (EV = VW) or
-// fragments (EV = 1, where a fragment lies in one group).
+// Block epilogues of the general kernels: a warp to a group, with the walk row's
+// offset and repeats.
 // ---------------------------------------------------------------------------
 
 // The threads' (count, mean, M2) for each position, in shared memory, to the
 // item's groups: two sums, the second relative to the first's mean.
-template <typename T, int EV>
+template <typename T>
 __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, const Range& r, int64_t item, int off,
                                                 const T* xs, int warps, const float* s_cnt, const float* s_mean,
-                                                const float* s_m2, float* partial, float* mean_out, float* inv_out) {
+                                                const float* s_m2, float4* partial, float* mean_out, float* inv_out) {
   const WalkPlan& p = d.p;
-  const int f = EV == 1 ? dev::Vec16<T>::N : 1;  // elements of a position
-  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV, Cw = d.C / f, Dw = d.D / f;
+  const GroupWalk walk(p, t.tile, t.frags, d.C, d.D, dev::Vec16<T>::N);
   const int lane = threadIdx.x & 31;
   for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
-    float* out = partial + ((item * p.tiles + t.tile) * d.G + g) * 3;
-    if (p.tiles > 1 && !group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
-      if (lane == 0) out[0] = out[1] = out[2] = 0.f;
+    float4* out = partial + (item * p.tiles + t.tile) * d.G + g;
+    if (!walk.has(g, off)) {
+      if (lane == 0) *out = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
     float c = 0.f, s = 0.f, q = 0.f;
-    for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+    walk.run(g, off, [&](int i) {
       c += s_cnt[i];
       s = fmaf(s_cnt[i], s_mean[i], s);
     });
@@ -150,7 +180,7 @@ __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, 
     s = dev::warp_sum(s);
     const float mg = c > 0.f ? s / c : 0.f;
     float res = 0.f;  // what rounding s / c and the sum left out of the mean
-    for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+    walk.run(g, off, [&](int i) {
       const float w = s_mean[i] - mg;
       res = fmaf(s_cnt[i], w, res);
       q += fmaf(s_cnt[i] * w, w, s_m2[i]);
@@ -164,26 +194,23 @@ __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, 
         mean_out[r.n * d.G + g] = dev::ld1_keep(xs + int64_t(g) * d.D) + mf;
         inv_out[r.n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
       } else {
-        out[0] = c;
-        out[1] = mf;
-        out[2] = m2g;
+        *out = make_float4(c, mf, m2g, 0.f);
       }
     }
   }
 }
 
 // The positions' (sum du gamma, sum du gamma h), in shared memory, to the item's groups.
-template <typename T, int EV>
+template <typename T>
 __device__ __forceinline__ void join_group_sums(const GnDims& d, const Tile& t, int64_t item, int off, int warps,
                                                 const float* s_a, const float* s_b, float* gpart) {
   const WalkPlan& p = d.p;
-  const int f = EV == 1 ? dev::Vec16<T>::N : 1;
-  const int p0 = t.tile * p.tile_frags * EV, np = t.frags * EV, Cw = d.C / f, Dw = d.D / f;
+  const GroupWalk walk(p, t.tile, t.frags, d.C, d.D, dev::Vec16<T>::N);
   const int lane = threadIdx.x & 31;
   for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
     float a = 0.f, b = 0.f;
-    if (p.tiles == 1 || group_in_tile(p0, np, off, g * Dw, Dw, Cw)) {
-      for_group(p0, np, off, g * Dw, Dw, Cw, [&](int i, int) {
+    if (walk.has(g, off)) {
+      walk.run(g, off, [&](int i) {
         a += s_a[i];
         b += s_b[i];
       });
@@ -198,13 +225,20 @@ __device__ __forceinline__ void join_group_sums(const GnDims& d, const Tile& t, 
   }
 }
 
-// A CTA's channel sums to row cta_row of cpart: 2 x [CTA row][C] (one tile), or
-// 2 x [CTA row][walk row], position 0 being channel 0.
+// VW floats to their places in shared memory, 16 bytes at a time.
+template <int VW>
+__device__ __forceinline__ void put(float* s, const float (&v)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; e += 4)
+    *reinterpret_cast<float4*>(s + threadIdx.x * VW + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+}
+
+// A CTA's channel sums, which its threads left at their positions in tot_a and
+// tot_b, to row cta_row of cpart: 2 x [CTA row][C] (one tile), or 2 x [CTA row]
+// [walk row], position 0 being channel 0.
 template <typename T, typename SYNC>
 __device__ __forceinline__ void leave_channel_sums(const GnDims& d, const Tile& t, int off, int threads,
-                                                   const float (&tot_a)[dev::Vec16<T>::N],
-                                                   const float (&tot_b)[dev::Vec16<T>::N], float* s_a, float* s_b,
-                                                   float* cpart, SYNC sync) {
+                                                   const float* tot_a, const float* tot_b, float* cpart, SYNC sync) {
   constexpr int VW = dev::Vec16<T>::N;
   const WalkPlan& p = d.p;
   const int64_t cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
@@ -217,18 +251,11 @@ __device__ __forceinline__ void leave_channel_sums(const GnDims& d, const Tile& 
       for (int e = 0; e < VW; ++e) {
         int64_t q = t.j * VW + e - off;
         if (q < 0) q += P;
-        oa[q] = tot_a[e];
-        ob[q] = tot_b[e];
+        oa[q] = tot_a[threadIdx.x * VW + e];
+        ob[q] = tot_b[threadIdx.x * VW + e];
       }
     }
     return;
-  }
-  if (t.mine) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      s_a[threadIdx.x * VW + e] = tot_a[e];
-      s_b[threadIdx.x * VW + e] = tot_b[e];
-    }
   }
   sync();
   const int reps = static_cast<int>(p.reps), P = t.frags * VW, lane = threadIdx.x & 31;
@@ -240,8 +267,8 @@ __device__ __forceinline__ void leave_channel_sums(const GnDims& d, const Tile& 
     for (int k = lanes == 1 ? 0 : lane; k < reps; k += lanes) {
       int q = c + off + k * d.C;
       if (q >= P) q -= P;
-      a += s_a[q];
-      b += s_b[q];
+      a += tot_a[q];
+      b += tot_b[q];
     }
     if (lanes == 32) {
       a = dev::warp_sum(a);
@@ -254,9 +281,75 @@ __device__ __forceinline__ void leave_channel_sums(const GnDims& d, const Tile& 
   }
 }
 
+// The staged kernels' block sums, in two steps with all threads in both: over the
+// repeats of each column (a channel, or a fragment of one group) in the tile, then
+// over each group's columns.  (One warp to a group took 2400 instructions a warp
+// for 2 x 4096 x 320, six times the streaming itself.)  Column i of the tile is
+// at positions i + k cols; its group is i / D, counted from the tile's first column.
+struct Columns {
+  int cols, reps, D;       // in the tile, with D columns to a group
+  int g0, n_groups, in0;   // the tile's first group, groups in it, columns of g0 before it
+  __device__ __forceinline__ Columns(const GnDims& d, const Tile& t, int ev, int per) {
+    const bool whole = d.p.tiles == 1;
+    D = d.D / per;
+    reps = whole ? static_cast<int>(d.p.reps) : 1;  // (more tiles: C % VW == 0, a walk row is C)
+    cols = whole ? d.C / per : t.frags * ev;
+    const int first = t.tile * d.p.tile_frags * ev;
+    g0 = whole ? 0 : first / D;
+    in0 = whole ? 0 : first - g0 * D;
+    n_groups = whole ? d.G : (in0 + cols + D - 1) / D;
+  }
+  // Columns [lo, hi) of the tile's group g (from g0).
+  __device__ __forceinline__ int lo(int g) const { return max(0, g * D - in0); }
+  __device__ __forceinline__ int hi(int g) const { return min(cols, (g + 1) * D - in0); }
+};
+
+// Parts of the groups that the tile does not touch.
+__device__ __forceinline__ void clear_others(const GnDims& d, const Columns& c, float* out, int width, int threads) {
+  if (d.p.tiles == 1) return;
+  for (int g = threadIdx.x; g < d.G; g += threads)
+    if (g < c.g0 || g >= c.g0 + c.n_groups)
+      for (int i = 0; i < width; ++i) out[g * width + i] = 0.f;
+}
+
 // ---------------------------------------------------------------------------
 // What a thread does with its fragments.
 // ---------------------------------------------------------------------------
+
+// The VW channels of a parameter from c on (modulo C), `vec`: 16 bytes at once.
+template <typename T>
+__device__ __forceinline__ void load_param(const T* __restrict__ param, int c, int C, bool vec,
+                                           float (&v)[dev::Vec16<T>::N]) {
+  if (vec) {
+    dev::Conv<T>::unpack(dev::ld16_keep(param + c), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < dev::Vec16<T>::N; ++e) {
+      v[e] = dev::ld1_keep(param + c);
+      if (++c == C) c = 0;
+    }
+  }
+}
+
+// mu of the thread's groups, and k scaled by their 1/sqrt(var + eps).
+template <int EV, int VW>
+__device__ __forceinline__ void scale_by_group(int c0, int64_t ng, const GnDims& d, const float* mean,
+                                               const float* inv, float (&mu)[EV], float (&k)[VW]) {
+  const float* m = mean + ng;
+  const float* r = inv + ng;
+  if constexpr (EV == 1) {
+    const int g = c0 / d.D;
+    mu[0] = m[g];
+    const float rg = r[g];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) k[e] *= rg;
+  } else {
+    for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
+      mu[e] = m[g];
+      k[e] *= r[g];
+    });
+  }
+}
 
 // A thread's channel values for the forward pass.
 template <typename T, int EV, bool SILU>
@@ -265,11 +358,11 @@ struct ApplyValues {
   float mu[EV], a[VW], b[VW];
   __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
                                        const T* __restrict__ beta, const float* mean, const float* inv) {
-    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
-      if (e < EV) mu[e] = mean[ng + g];
-      a[e] = inv[ng + g] * dev::ld1_keep(gamma + c);
-      b[e] = beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-    });
+#pragma unroll
+    for (int e = 0; e < VW; ++e) b[e] = 0.f;
+    load_param(gamma, c0, d.C, d.pvec, a);
+    if (beta != nullptr) load_param(beta, c0, d.C, d.pvec, b);
+    scale_by_group(c0, ng, d, mean, inv, mu, a);
   }
   __device__ __forceinline__ void operator()(float (&v)[VW]) const {
     centre_scale_add(v, mu, a, b);
@@ -277,45 +370,50 @@ struct ApplyValues {
   }
 };
 
-// The same for the gradient: x -> h, dy -> du.
+// The same for the gradient: x -> t = x - mu, dy -> du, with u = t (r gamma) + beta.
 template <typename T, int EV, bool SILU>
 struct GradValues {
   static constexpr int VW = dev::Vec16<T>::N;
-  float mu[EV], rs[EV], ga[VW], be[VW];
+  float mu[EV], k[VW], be[VW];  // k = r gamma
   __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
                                        const T* __restrict__ beta, const float* mean, const float* inv) {
-    for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
-      if (e < EV) {
-        mu[e] = mean[ng + g];
-        rs[e] = inv[ng + g];
-      }
-      ga[e] = dev::ld1_keep(gamma + c);
-      be[e] = SILU && beta != nullptr ? dev::ld1_keep(beta + c) : 0.f;
-    });
+#pragma unroll
+    for (int e = 0; e < VW; ++e) be[e] = 0.f;
+    load_param(gamma, c0, d.C, d.pvec, k);
+    if (SILU && beta != nullptr) load_param(beta, c0, d.C, d.pvec, be);
+    scale_by_group(c0, ng, d, mean, inv, mu, k);
   }
   __device__ __forceinline__ void operator()(float (&v)[VW], float (&w)[VW]) const {
-    centre_scale(v, mu, rs);
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 m = pair_of<VW>(mu, e);
+      const float2 t = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m.x, -m.y));
+      v[e] = t.x;
+      v[e + 1] = t.y;
+    }
     if constexpr (SILU) {
       float u[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) u[e] = be[e];
-      fma_pairs(v, ga, u);
+      fma_pairs(v, k, u);
       activate_grad<T>(w, u);
     }
   }
 };
 
-// dx from h (in v) and du (in w): v <- rs (du gamma - m1 - h m2).
+// dx = r (du gamma - m1 - h m2) = du k + (t q2 + q1), q2 = -r^2 m2, q1 = -r m1.
 template <typename T, int EV, bool SILU>
 struct GradApplyValues : GradValues<T, EV, SILU> {
   static constexpr int VW = dev::Vec16<T>::N;
   using Base = GradValues<T, EV, SILU>;
-  float a1[EV], a2[EV];  // -m1, -m2
-  __device__ __forceinline__ void load_means(int c0, int64_t ng, const GnDims& d, const float* m1, const float* m2) {
+  float q1[EV], q2[EV];
+  __device__ __forceinline__ void load_means(int c0, int64_t ng, const GnDims& d, const float* inv, const float* m1,
+                                             const float* m2) {
     for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
       if (e < EV) {
-        a1[e] = -__ldcg(m1 + ng + g);
-        a2[e] = -__ldcg(m2 + ng + g);
+        const float r = inv[ng + g];
+        q1[e] = -r * __ldcg(m1 + ng + g);
+        q2[e] = -r * (r * __ldcg(m2 + ng + g));
       }
     });
   }
@@ -323,10 +421,8 @@ struct GradApplyValues : GradValues<T, EV, SILU> {
     (*this)(v, w);
 #pragma unroll
     for (int e = 0; e < VW; e += 2) {
-      const float2 t = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(Base::ga[e], Base::ga[e + 1]),
-                                  pair_of<VW>(a1, e));
-      const float2 r = __fmul2_rn(__ffma2_rn(make_float2(v[e], v[e + 1]), pair_of<VW>(a2, e), t),
-                                  pair_of<VW>(Base::rs, e));
+      const float2 t = __ffma2_rn(make_float2(v[e], v[e + 1]), pair_of<VW>(q2, e), pair_of<VW>(q1, e));
+      const float2 r = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(Base::k[e], Base::k[e + 1]), t);
       v[e] = r.x;
       v[e + 1] = r.y;
     }
@@ -367,16 +463,18 @@ struct RowStream {
   int rows;            // walk rows in a stage
   int row_bytes;       // of this tile
   int64_t total;       // walk rows of a sample
-  int64_t frags, row_frags;  // fragments of a sample, of a walk row
+  int64_t frags, full_rows;
+  int rest;
   dev::Ring ring;
   bool ok = true;
 
   __device__ __forceinline__ RowStream(StageBars* b, unsigned char* m, const GnDims& d, const Tile& t)
       : bars(b), smem(m), row_bytes(t.frags * 16), ring(kStages) {
     rows = kStageBytes / NOPS / row_bytes;  // >= 2: a tile has at most kWalkThreads fragments
-    frags = d.L / VW;
-    row_frags = d.p.row_frags;
-    total = (frags + row_frags - 1) / row_frags;
+    frags = d.frags;
+    full_rows = d.full_rows;
+    rest = d.rest;
+    total = full_rows + (rest > 0 ? 1 : 0);
     if (threadIdx.x == 0) {
       for (int i = 0; i < kStages; ++i) {
         dev::mbar_init(&bars->full[i], 1);
@@ -388,7 +486,7 @@ struct RowStream {
   }
 
   // Walk rows of a sample that have a fragment j.
-  __device__ __forceinline__ int64_t of_column(int64_t j) const { return (frags - j + row_frags - 1) / row_frags; }
+  __device__ __forceinline__ int64_t of_column(int64_t j) const { return full_rows + (j < rest ? 1 : 0); }
 
   // The producer: the rows of all the CTA's items.
   __device__ __forceinline__ void produce(const T* const (&base)[NOPS], const GnDims& d, const Tile& t, bool reversed,
@@ -425,47 +523,76 @@ struct RowStream {
     }
   }
 
-  // A consumer: f(row, raw) for the walk rows [ra, rb) of an item; `mine` and
-  // rows below `r1` for the thread's own fragment column.
+  // A consumer: f(row, raw) for the walk rows of an item that have a fragment in
+  // the thread's column, rows counted from the item's first; two at a time, so
+  // that one row's arithmetic covers the other's latency.
   template <typename F>
-  __device__ __forceinline__ void consume(int64_t ra, int64_t rb, int64_t r1, bool mine, F f) {
-    for (int64_t r = ra; r < rb; r += rows, ring.next()) {
+  __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
+    const int n = static_cast<int>(range.rb - range.ra);
+    for (int r = 0; r < n; r += rows, ring.next()) {
       ok = ok && dev::mbar_wait(&bars->full[ring.st], ring.phase);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         continue;
       }
       const unsigned char* src = smem + ring.st * kStageBytes + threadIdx.x * 16;
-      const int k = mine ? static_cast<int>(min(int64_t(rows), r1 - r)) : 0;
-      for (int i = 0; i < k; ++i) {
-        uint4 raw[NOPS];
+      const int k = min(rows, mine - r);
+      auto load = [&](int i, uint4 (&raw)[NOPS]) {
 #pragma unroll
         for (int o = 0; o < NOPS; ++o) raw[o] = dev::lds16(src + o * (kStageBytes / NOPS) + i * row_bytes);
-        f(r + i, raw);
+      };
+      int i = 0;
+      for (; i + 1 < k; i += 2) {
+        uint4 a[NOPS], b[NOPS];
+        load(i, a);
+        load(i + 1, b);
+        f(r + i, a);
+        f(r + i + 1, b);
+      }
+      if (i < k) {
+        uint4 a[NOPS];
+        load(i, a);
+        f(r + i, a);
       }
       dev::release_stage(&bars->empty[ring.st]);
     }
+  }
+  // The next stage (an item's first), once its rows are there.
+  __device__ __forceinline__ const unsigned char* peek() {
+    ok = ok && dev::mbar_wait(&bars->full[ring.st], ring.phase);
+    return smem + ring.st * kStageBytes;
+  }
+  // Rows of an item that have a fragment in column j (0 where the thread has none).
+  __device__ __forceinline__ int mine(const Range& range, const Tile& t) const {
+    return t.mine ? static_cast<int>(max(int64_t(0), min(range.rb, of_column(t.j)) - range.ra)) : 0;
   }
 };
 
 // The barrier of a staged kernel's consumers.
 __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blockDim.x - 32); }
 
-// Pass 1.  partial: [item][tile][G] x (count, mean, M2), relative to the group's
-// first value, or, where a sample has one item and one tile, the statistics
-// themselves (partial == nullptr).  A thread sums its values and their squares
-// relative to a centre among its own (its first value of the channel; GROUP: its
-// first fragment's mean).  Cancellation then costs at most u times the thread's
-// row count, however far off that value is: what lies that far off makes up the
-// group's variance.
+// The median of three values: no single outlier moves it.
+__device__ __forceinline__ float median3(float a, float b, float c) {
+  return fmaxf(fminf(a, b), fminf(fmaxf(a, b), c));
+}
+
+// Pass 1.  partial: [item][tile][G] x (count, mean, M2, -), the mean relative to
+// the group's first value in the sample.  The block takes its values relative to
+// a centre of each group, so that its sums and sums of squares simply add up: the
+// median of three of the group's values in the item's first walk row, which lies
+// among the values unless two of the three are outliers.  Off by k standard
+// deviations it costs the variance k^2 2^-24 of its value.
 template <typename T, bool GROUP>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
-k_gn_stats_staged(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
+k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
   constexpr int VW = dev::Vec16<T>::N;
   constexpr int EV = GROUP ? 1 : VW;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) StageBars bars;
-  __shared__ float s_cnt[kWalkThreads * EV], s_mean[kWalkThreads * EV], s_m2[kWalkThreads * EV];
+  // after the stages: two sums by position, the centres of the tile's groups
+  float* s_a = reinterpret_cast<float*>(smem + kStageSmem);
+  float* s_b = s_a + kWalkThreads * EV;
+  float* centre = s_b + kWalkThreads * EV;
   const WalkPlan& p = d.p;
   const Tile t(p);
   RowStream<T, 1> rows(&bars, smem, d, t);
@@ -477,34 +604,46 @@ k_gn_stats_staged(const T* x, GnDims d, float* partial, float* mean_out, float* 
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, policy_evict_normal());
     return;
   }
-  const int c0 = first_channel(t.j, VW, 0, d.C);
+  const Columns cols(d, t, EV, GROUP ? VW : 1);
+  const int per = GROUP ? VW : 1;  // elements of a column
+  int grp[EV];
+  {
+    int g = (t.mine ? int(threadIdx.x) * EV % cols.cols : 0) + cols.in0, in = g % cols.D;
+    g /= cols.D;
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      grp[e] = g;
+      if (++in == cols.D) {
+        in = 0;
+        if (++g == cols.n_groups) g = 0;  // the next repeat of the channels
+      }
+    }
+  }
   for (Items it(d, false); it.more(); it.next()) {
     const Range r(p, it.item(), rows.total);
-    const T* xs = x + r.n * d.L;
-    float first[EV], c[EV], s[VW], q[VW];
-#pragma unroll
-    for (int e = 0; e < EV; ++e) first[e] = c[e] = 0.f;
+    float4* out = partial + (it.item() * p.tiles + t.tile) * d.G;
+    if (r.ra >= r.rb) {  // the plan's rows may be one more than there are
+      for (int g = threadIdx.x; g < d.G; g += consumers) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+      continue;
+    }
+    float c[EV], s[VW], q[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
-    if (t.mine)
-      for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
-        if (e < EV) first[e] = dev::ld1_keep(xs + int64_t(g) * d.D);
-      });
-    const int64_t r1 = min(r.rb, rows.of_column(t.j));
-    rows.consume(r.ra, r.rb, r1, t.mine, [&](int64_t row, const uint4 (&raw)[1]) {
+    // positions of the sample (repeats of the channels) in the item, and in its first walk row
+    const int64_t pos0 = r.ra * p.reps, pos1 = min(r.rb * p.reps, d.S);
+    const T* row0 = reinterpret_cast<const T*>(rows.peek());
+    const int n_rep = static_cast<int>(min(int64_t(cols.reps), pos1 - pos0));
+    for (int g = threadIdx.x; g < cols.n_groups; g += consumers) {
+      const int lo = cols.lo(g) * per, n = (cols.hi(g) - cols.lo(g)) * per, step = cols.cols * per;
+      centre[g] = median3(dev::to_float(row0[lo]), dev::to_float(row0[lo + n / 2 + n_rep / 2 * step]),
+                          dev::to_float(row0[lo + n - 1 + (n_rep - 1) * step]));
+    }
+    consumer_sync();
+#pragma unroll
+    for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
+    rows.consume(r, rows.mine(r, t), [&](int, const uint4 (&raw)[1]) {
       float v[VW];
       dev::Conv<T>::unpack(raw[0], v);
-      if (row == r.ra) {
-        if constexpr (EV == 1) {
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < VW; ++e) m += v[e] - v[0];
-          c[0] = fmaf(m, 1.0f / VW, v[0]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) c[e] = v[e];
-        }
-      }
 #pragma unroll
       for (int e = 0; e < VW; e += 2) {
         const float2 m = pair_of<VW>(c, e);
@@ -522,18 +661,43 @@ k_gn_stats_staged(const T* x, GnDims d, float* partial, float* mean_out, float* 
           s[0] += s[e];
           q[0] += q[e];
         }
-      }
-      const float cnt = r.ra < r1 ? float(r1 - r.ra) * (VW / EV) : 0.f;
-#pragma unroll
-      for (int e = 0; e < EV; ++e) {
-        const float m = cnt > 0.f ? s[e] / cnt : 0.f;
-        s_cnt[threadIdx.x * EV + e] = cnt;
-        s_mean[threadIdx.x * EV + e] = cnt > 0.f ? (c[e] - first[e]) + m : 0.f;
-        s_m2[threadIdx.x * EV + e] = not_negative(q[e] - s[e] * m);
+        s_a[threadIdx.x] = s[0];
+        s_b[threadIdx.x] = q[0];
+      } else {
+        put(s_a, s);
+        put(s_b, q);
       }
     }
     consumer_sync();
-    join_statistics<T, EV>(d, t, r, it.item(), 0, xs, consumers / 32, s_cnt, s_mean, s_m2, partial, mean_out, inv_out);
+    if (cols.reps > 1) {  // to the first repeat's place
+      sum_sets(consumers, cols.cols, cols.reps,
+               [&](int i, int k, float& a, float& b) {
+                 a += s_a[i + k * cols.cols];
+                 b += s_b[i + k * cols.cols];
+               },
+               [&](int i, float a, float b) {
+                 s_a[i] = a;
+                 s_b[i] = b;
+               });
+      consumer_sync();
+    }
+    if (p.tiles > 1)
+      for (int g = threadIdx.x; g < d.G; g += consumers)
+        if (g < cols.g0 || g >= cols.g0 + cols.n_groups) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float positions = float(pos1 - pos0);
+    sum_sets(consumers, cols.n_groups, cols.D,
+             [&](int g, int k, float& a, float& b) {
+               const int i = cols.lo(g) + k;
+               if (i < cols.hi(g)) {
+                 a += s_a[i];
+                 b += s_b[i];
+               }
+             },
+             [&](int g, float a, float b) {
+               const float n = positions * float((cols.hi(g) - cols.lo(g)) * per), m = a / n;
+               const float first = dev::ld1_keep(x + r.n * d.L + int64_t(cols.g0 + g) * d.D);
+               out[cols.g0 + g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), 0.f);
+             });
     consumer_sync();
   }
 }
@@ -563,9 +727,9 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     const Range r(p, it.item(), rows.total);
     ApplyValues<T, GROUP ? 1 : VW, SILU> val;
     if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
-    T* py = y + r.n * d.L + t.j * VW;
     const int64_t pitch = p.row_frags * VW;
-    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t row, const uint4 (&raw)[1]) {
+    T* py = y + r.n * d.L + r.ra * pitch + t.j * VW;
+    rows.consume(r, rows.mine(r, t), [&](int row, const uint4 (&raw)[1]) {
       float v[VW];
       dev::Conv<T>::unpack(raw[0], v);
       val(v);
@@ -585,7 +749,11 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
   constexpr int EV = GROUP ? 1 : VW;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) StageBars bars;
-  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  // after the stages: the sums by position, and by channel over the CTA's items
+  float* s_a = reinterpret_cast<float*>(smem + kStageSmem);
+  float* s_b = s_a + kWalkThreads * VW;
+  float* tot_a = s_b + kWalkThreads * VW;
+  float* tot_b = tot_a + kWalkThreads * VW;
   const WalkPlan& p = d.p;
   const Tile t(p);
   RowStream<T, 2> rows(&bars, smem, d, t);
@@ -598,9 +766,8 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
     return;
   }
   const int c0 = first_channel(t.j, VW, 0, d.C);
-  float tot_a[VW], tot_b[VW];
-#pragma unroll
-  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
+  const Columns cols(d, t, VW, 1);
+  bool once = true;
   for (Items it(d, false); it.more(); it.next()) {
     const Range r(p, it.item(), rows.total);
     GradValues<T, EV, SILU> val;
@@ -608,7 +775,7 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
     float sa[VW], sb[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
-    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t, const uint4 (&raw)[2]) {
+    rows.consume(r, rows.mine(r, t), [&](int, const uint4 (&raw)[2]) {
       float v[VW], w[VW];
       dev::Conv<T>::unpack(raw[0], v);
       dev::Conv<T>::unpack(raw[1], w);
@@ -617,30 +784,49 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
       fma_pairs(w, v, sb);
     });
     if (t.mine) {
-      dev::add_pairs(tot_a, sa);
-      dev::add_pairs(tot_b, sb);
-      if constexpr (GROUP) {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          a = fmaf(sa[e], val.ga[e], a);
-          b = fmaf(sb[e], val.ga[e], b);
-        }
-        s_a[threadIdx.x] = a;
-        s_b[threadIdx.x] = b;
-      } else {
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
-          s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
-        }
-      }
+      for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) { sb[e] *= inv[r.n * d.G + g]; });  // du t r = du h
+      put(s_a, sa);
+      put(s_b, sb);
     }
     consumer_sync();
-    join_group_sums<T, EV>(d, t, it.item(), 0, consumers / 32, s_a, s_b, gpart);
+    // by channel: to the totals, and times gamma back to place (a repeat's is free) for the groups
+    sum_sets(consumers, cols.cols, cols.reps,
+             [&](int i, int k, float& a, float& b) {
+               a += s_a[i + k * cols.cols];
+               b += s_b[i + k * cols.cols];
+             },
+             [&](int i, float a, float b) {
+               tot_a[i] = once ? a : tot_a[i] + a;
+               tot_b[i] = once ? b : tot_b[i] + b;
+               const float ga = dev::ld1_keep(gamma + cols.g0 * d.D + cols.in0 + i);
+               s_a[i] = a * ga;  // read by this thread's set alone
+               s_b[i] = b * ga;
+             });
+    once = false;
+    consumer_sync();
+    float* out = gpart + (it.item() * p.tiles + t.tile) * d.G * 2;
+    clear_others(d, cols, out, 2, consumers);
+    sum_sets(consumers, cols.n_groups, cols.D,
+             [&](int g, int k, float& a, float& b) {
+               const int i = cols.lo(g) + k;
+               if (i < cols.hi(g)) {
+                 a += s_a[i];
+                 b += s_b[i];
+               }
+             },
+             [&](int g, float a, float b) {
+               out[(cols.g0 + g) * 2] = a;
+               out[(cols.g0 + g) * 2 + 1] = b;
+             });
     consumer_sync();
   }
-  if (cpart != nullptr) leave_channel_sums<T>(d, t, 0, consumers, tot_a, tot_b, s_a, s_b, cpart, consumer_sync);
+  if (cpart == nullptr) return;
+  const int64_t cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
+  float* oa = cpart + cta_row * d.C + cols.g0 * d.D + cols.in0;
+  for (int i = threadIdx.x; i < cols.cols; i += consumers) {  // a thread's own or, after the barrier, any
+    oa[i] = tot_a[i];
+    oa[cta_rows * d.C + i] = tot_b[i];
+  }
 }
 
 // Gradient, pass 2: dx, over the items in reverse.
@@ -668,11 +854,11 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     GradApplyValues<T, GROUP ? 1 : VW, SILU> val;
     if (t.mine) {
       val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
-      val.load_means(c0, r.n * d.G, d, m1, m2);
+      val.load_means(c0, r.n * d.G, d, inv, m1, m2);
     }
-    T* po = dx + r.n * d.L + t.j * VW;
     const int64_t pitch = p.row_frags * VW;
-    rows.consume(r.ra, r.rb, min(r.rb, rows.of_column(t.j)), t.mine, [&](int64_t row, const uint4 (&raw)[2]) {
+    T* po = dx + r.n * d.L + r.ra * pitch + t.j * VW;
+    rows.consume(r, rows.mine(r, t), [&](int row, const uint4 (&raw)[2]) {
       float v[VW], w[VW];
       dev::Conv<T>::unpack(raw[0], v);
       dev::Conv<T>::unpack(raw[1], w);
@@ -690,7 +876,7 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
 
 template <typename T>
 __global__ void __launch_bounds__(kWalkThreads)
-k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out) {
+k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_out) {
   constexpr int VW = dev::Vec16<T>::N;
   constexpr int U = 4;
   __shared__ float s_cnt[kWalkThreads * VW], s_mean[kWalkThreads * VW], s_m2[kWalkThreads * VW];
@@ -740,7 +926,7 @@ k_gn_stats(const T* x, GnDims d, float* partial, float* mean_out, float* inv_out
       }
     }
     __syncthreads();
-    join_statistics<T, VW>(d, t, r, it.item(), off, xs, blockDim.x / 32, s_cnt, s_mean, s_m2, partial, mean_out,
+    join_statistics<T>(d, t, r, it.item(), off, xs, blockDim.x / 32, s_cnt, s_mean, s_m2, partial, mean_out,
                            inv_out);
     __syncthreads();
   }
@@ -780,6 +966,36 @@ k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   }
 }
 
+// The sums over a thread's rows, of du (sa) and of du t (sb), to those of du and
+// du h = r du t: for the parameters (added to tot) and, times gamma, for the groups.
+template <typename T>
+__device__ __forceinline__ void finish_sums(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
+                                            const float* inv, float (&sa)[dev::Vec16<T>::N],
+                                            float (&sb)[dev::Vec16<T>::N], float* tot_a, float* tot_b, float* s_a,
+                                            float* s_b, bool first) {
+  constexpr int VW = dev::Vec16<T>::N;
+  float ga[VW];
+  for_channels<VW>(c0, d.C, d.D, [&](int e, int c, int g) {
+    ga[e] = dev::ld1_keep(gamma + c);
+    sb[e] *= inv[ng + g];
+  });
+#pragma unroll
+  for (int e = 0; e < VW; e += 4) {  // a thread's own places
+    float4* a = reinterpret_cast<float4*>(tot_a + threadIdx.x * VW + e);
+    float4* b = reinterpret_cast<float4*>(tot_b + threadIdx.x * VW + e);
+    const float4 pa = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *a, pb = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *b;
+    *a = make_float4(pa.x + sa[e], pa.y + sa[e + 1], pa.z + sa[e + 2], pa.w + sa[e + 3]);
+    *b = make_float4(pb.x + sb[e], pb.y + sb[e + 1], pb.z + sb[e + 2], pb.w + sb[e + 3]);
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    sa[e] *= ga[e];
+    sb[e] *= ga[e];
+  }
+  put(s_a, sa);
+  put(s_b, sb);
+}
+
 // A CTA's items share `off` (the launch sees to it), so a thread's channels stay
 // the same and its sums run on over them.
 template <typename T, bool VEC, bool SILU>
@@ -788,23 +1004,25 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
                const float* inv, GnDims d, float* gpart, float* cpart) {
   constexpr int VW = dev::Vec16<T>::N;
   constexpr int U = 2;
-  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  __shared__ __align__(16) float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* tot_a = reinterpret_cast<float*>(smem);  // the totals over the CTA's items
+  float* tot_b = tot_a + kWalkThreads * VW;
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
   const Tile t(p);
-  float tot_a[VW], tot_b[VW];
-#pragma unroll
-  for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = 0.f;
   int off = 0;
+  bool once = true;
   for (Items it(d, false); it.more(); it.next()) {
     const Range r(p, it.item(), p.rows);
     const T* xs = x + r.n * d.L;
     const T* ds = dy + r.n * d.L;
     off = walk_offset<T, VEC>(xs);
     if (t.mine) {
+      const int c0 = first_channel(t.j, VW, off, d.C);
       GradValues<T, VW, SILU> val;
-      val.load(first_channel(t.j, VW, off, d.C), r.n * d.G, d, gamma, beta, mean, inv);
+      val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
       float sa[VW], sb[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
@@ -827,20 +1045,15 @@ k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __
           }
         }
       }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        s_a[threadIdx.x * VW + e] = sa[e] * val.ga[e];
-        s_b[threadIdx.x * VW + e] = sb[e] * val.ga[e];
-        tot_a[e] += sa[e];
-        tot_b[e] += sb[e];
-      }
+      finish_sums<T>(c0, r.n * d.G, d, gamma, inv, sa, sb, tot_a, tot_b, s_a, s_b, once);
     }
+    once = false;
     __syncthreads();
-    join_group_sums<T, VW>(d, t, it.item(), off, blockDim.x / 32, s_a, s_b, gpart);
+    join_group_sums<T>(d, t, it.item(), off, blockDim.x / 32, s_a, s_b, gpart);
     __syncthreads();
   }
   if (cpart != nullptr)
-    leave_channel_sums<T>(d, t, off, int(blockDim.x), tot_a, tot_b, s_a, s_b, cpart, [] { __syncthreads(); });
+    leave_channel_sums<T>(d, t, off, int(blockDim.x), tot_a, tot_b, cpart, [] { __syncthreads(); });
 }
 
 template <typename T, bool VEC, bool SILU>
@@ -863,7 +1076,7 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
     const int c0 = first_channel(t.j, VW, off, d.C);
     GradApplyValues<T, VW, SILU> val;
     val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
-    val.load_means(c0, r.n * d.G, d, m1, m2);
+    val.load_means(c0, r.n * d.G, d, inv, m1, m2);
     for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
       float v[U][VW], w[U][VW];
 #pragma unroll
@@ -890,7 +1103,7 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 // are many parts) take one (n, g); bound by the latency of a few reads.
 // ---------------------------------------------------------------------------
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 64;
 
 template <int THREADS>
 __device__ __forceinline__ float join_sum(float x, float* red) {
@@ -906,57 +1119,77 @@ __device__ __forceinline__ float join_sum(float x, float* red) {
   return x;
 }
 
-// (count, mean, M2) of the parts -> the group's statistics.
-template <typename T, int THREADS>
+// (count, mean, M2) of the parts -> the group's statistics: a warp for each
+// (n, g), which keeps up to kJoinKept parts a lane in registers for the second
+// sum and reads the others again.
+constexpr int kJoinKept = 10;
+
+template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
-k_gn_join(const T* x, const float* partial, GnDims d, float* mean_out, float* inv_out) {
-  __shared__ float red[kJoinThreads / 32];
+k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* inv_out) {
   dev::pdl_wait();
   dev::pdl_trigger();
-  const int t = threadIdx.x % THREADS;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kJoinThreads / THREADS;
-  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(gridDim.x) * per) {
-    const float* src = partial + ((i / d.G) * parts * d.G + i % d.G) * 3;
+  const int lane = threadIdx.x & 31;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
+  for (int64_t i = int64_t(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < d.N * d.G;
+       i += int64_t(gridDim.x) * (kJoinThreads / 32)) {
+    const int64_t n = quotient(i, d.G), g = i - n * d.G;
+    const float4* src = partial + n * parts * d.G + g;
+    const float first = dev::ld1_keep(x + n * d.L + g * d.D);
+    float4 kept[kJoinKept];
+#pragma unroll
+    for (int u = 0; u < kJoinKept; ++u)
+      kept[u] = lane + u * 32 < parts ? __ldcg(src + int64_t(lane + u * 32) * d.G) : make_float4(0.f, 0.f, 0.f, 0.f);
     float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
-#pragma unroll 4
-    for (int64_t k = t; k < parts; k += THREADS) {
-      const float* e = src + k * d.G * 3;
-      const float n = __ldcg(e);
-      c += n;
-      s = fmaf(n, __ldcg(e + 1), s);
+#pragma unroll
+    for (int u = 0; u < kJoinKept; ++u) {
+      c += kept[u].x;
+      s = fmaf(kept[u].x, kept[u].y, s);
     }
-    c = join_sum<THREADS>(c, red);
-    s = join_sum<THREADS>(s, red);
-    const float mg = s / c;
-#pragma unroll 4
-    for (int64_t k = t; k < parts; k += THREADS) {
-      const float* e = src + k * d.G * 3;
-      const float w = __ldcg(e + 1) - mg, n = __ldcg(e);
-      res = fmaf(n, w, res);
-      q += fmaf(n * w, w, __ldcg(e + 2));
+    for (int64_t k = lane + kJoinKept * 32; k < parts; k += 32) {
+      const float4 v = __ldcg(src + k * d.G);
+      c += v.x;
+      s = fmaf(v.x, v.y, s);
     }
-    res = join_sum<THREADS>(res, red);
-    q = join_sum<THREADS>(q, red);
-    if (t == 0) {
-      const float fix = res / c;
-      mean_out[i] = dev::ld1_keep(x + i / d.G * d.L + i % d.G * d.D) + (mg + fix);
+    c = dev::warp_sum(c);
+    const float mg = dev::warp_sum(s) / c;
+    auto square = [&](const float4& v) {
+      const float w = v.y - mg;
+      res = fmaf(v.x, w, res);
+      q += fmaf(v.x * w, w, v.z);
+    };
+#pragma unroll
+    for (int u = 0; u < kJoinKept; ++u) square(kept[u]);
+    for (int64_t k = lane + kJoinKept * 32; k < parts; k += 32) square(__ldcg(src + k * d.G));
+    res = dev::warp_sum(res);
+    q = dev::warp_sum(q);
+    if (lane == 0) {
+      const float fix = res / c;  // what rounding left out of the mean
+      mean_out[i] = first + (mg + fix);
       inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
     }
   }
 }
 
-// The gradient's sums of the parts -> m1, m2 of each (n, g).
-template <int THREADS>
-__global__ void __launch_bounds__(kJoinThreads)
-k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
-  __shared__ float red[kJoinThreads / 32];
+// The gradient's sums of the parts -> m1, m2 of each (n, g); and, in the blocks
+// after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(kSumsThreads)
+k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
+               int64_t reps, T* dbeta, T* dgamma) {
+  __shared__ float red[kSumsThreads / 32];
   dev::pdl_wait();
   dev::pdl_trigger();
+  if (int(blockIdx.x) >= join_blocks) {
+    channel_sums<T>(cpart, rows, reps, d.C, 2, dbeta, dgamma, blockIdx.x - join_blocks, gridDim.x - join_blocks);
+    return;
+  }
   const int t = threadIdx.x % THREADS;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kJoinThreads / THREADS;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kSumsThreads / THREADS;
   const float scale = 1.0f / (float(d.S) * float(d.D));
-  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(gridDim.x) * per) {
-    const float2* src = reinterpret_cast<const float2*>(gpart) + (i / d.G) * parts * d.G + i % d.G;
+  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(join_blocks) * per) {
+    const int64_t n = quotient(i, d.G);
+    const float2* src = reinterpret_cast<const float2*>(gpart) + n * parts * d.G + (i - n * d.G);
     float a = 0.f, b = 0.f;
 #pragma unroll 4
     for (int64_t k = t; k < parts; k += THREADS) {
@@ -976,8 +1209,11 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2) {
 int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
 GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
-  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, {}};
+  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, {}};
   d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
+  d.frags = d.L / vec_width(t);
+  d.full_rows = d.frags / d.p.row_frags;
+  d.rest = int(d.frags % d.p.row_frags);
   return d;
 }
 
@@ -999,7 +1235,7 @@ GnWorkspace gn_workspace(const GnDims& d) {
   GnWorkspace w;
   const size_t stats = pad16(size_t(d.N) * d.G * 4);
   w.partial = 0;
-  w.mean = split_parts(d) ? pad16(size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 12) : 0;
+  w.mean = size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 16;
   w.inv = w.mean + stats;
   w.total = w.inv + stats;
   return w;
@@ -1022,29 +1258,22 @@ GnGradWorkspace gn_grad_workspace(const GnDims& d, DType t) {
 
 inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uintptr_t>(p) & 15u); }
 
-// A warp for each (n, g), or a block where there are more parts than a warp takes at once.
-inline bool join_by_block(const GnDims& d) { return int64_t(d.p.chunks) * d.p.tiles > 64; }
-inline unsigned join_grid(const GnDims& d) {
-  const int64_t per = join_by_block(d) ? 1 : kJoinThreads / 32;
-  return unsigned(std::min<int64_t>((d.N * d.G + per - 1) / per, kPlanSms * 8));
-}
-
 // Staged kernels: CTAs of consumers and a producer warp, two an SM.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_staged(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cudaStream_t stream, int* launches,
-                          Args... args) {
+                          size_t extra, Args... args) {
   int per_sm = 1;
   const int threads = d.p.threads + 32;
-  cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, kStageSmem, &per_sm);
+  cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, kStageSmem + extra, &per_sm);
   if (e != cudaSuccess) return e;
-  e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(threads), kStageSmem, stream, args...);
+  e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(threads), kStageSmem + extra, stream, args...);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
 template <typename... KArgs, typename... Args>
 cudaError_t launch_plain(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cudaStream_t stream, int* launches,
-                         Args... args) {
-  const cudaError_t e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), 0, stream, args...);
+                         size_t extra, Args... args) {
+  const cudaError_t e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads), extra, stream, args...);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -1052,48 +1281,55 @@ cudaError_t launch_plain(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cu
 template <typename T>
 cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
-  const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps);
+  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps);
+  d.pvec = a.C % VW == 0 && misalign16(a.x) == 0 && misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   const GnWorkspace w = gn_workspace(d);
   char* ws = static_cast<char*>(a.workspace);
   float* mean = a.mean != nullptr ? a.mean : reinterpret_cast<float*>(ws + w.mean);
   float* inv = a.inv != nullptr ? a.inv : reinterpret_cast<float*>(ws + w.inv);
-  float* partial = split_parts(d) ? reinterpret_cast<float*>(ws + w.partial) : nullptr;
+  // (the general statistics of a single part are final at once)
+  const bool staged = a.C % VW == 0 && misalign16(a.x) == 0, group = d.D % VW == 0;
+  float4* partial = staged || split_parts(d) ? reinterpret_cast<float4*>(ws + w.partial) : nullptr;
   const T* x = static_cast<const T*>(a.x);
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* beta = static_cast<const T*>(a.beta);
   T* y = static_cast<T*>(a.y);
   const int64_t rows = cta_rows_of(d, kPlanSms * 2);
   // the staged passes want whole fragments; the statistics need no alignment of y
-  const bool staged = a.C % VW == 0 && misalign16(x) == 0, group = d.D % VW == 0;
   const bool vec = misalign16(x) == misalign16(y);
   cudaError_t e;
   if (staged) {
     auto f = group ? k_gn_stats_staged<T, true> : k_gn_stats_staged<T, false>;
-    e = launch_staged(f, rows, d, stream, launches, x, d, partial, mean, inv);
+    // two sums by position and the groups' centres
+    const size_t extra = sizeof(float) * kWalkThreads * 3 * (group ? 1 : VW);
+    e = launch_staged(f, rows, d, stream, launches, extra, x, d, partial);
   } else {
-    e = launch_plain(k_gn_stats<T>, rows, d, stream, launches, x, d, partial, mean, inv);
+    e = launch_plain(k_gn_stats<T>, rows, d, stream, launches, 0, x, d, partial, mean, inv);
   }
   if (e != cudaSuccess) return e;
   if (partial != nullptr) {
-    auto f = join_by_block(d) ? k_gn_join<T, kJoinThreads> : k_gn_join<T, 32>;
-    e = launch(f, dim3(join_grid(d)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv);
+    const int64_t joins = std::min<int64_t>((d.N * d.G + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kPlanSms * 8);
+    e = launch(k_gn_join<T>, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
   if (staged && vec) {
     auto f = group ? (a.silu ? k_gn_apply_staged<T, true, true> : k_gn_apply_staged<T, true, false>)
                    : (a.silu ? k_gn_apply_staged<T, false, true> : k_gn_apply_staged<T, false, false>);
-    return launch_staged(f, rows, d, stream, launches, x, gamma, beta, mean, inv, y, d);
+    return launch_staged(f, rows, d, stream, launches, 0, x, gamma, beta, mean, inv, y, d);
   }
   auto f = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
                : (a.silu ? k_gn_apply<T, false, true> : k_gn_apply<T, false, false>);
-  return launch_plain(f, rows, d, stream, launches, x, gamma, beta, mean, inv, y, d);
+  return launch_plain(f, rows, d, stream, launches, 0, x, gamma, beta, mean, inv, y, d);
 }
 
 template <typename T>
 cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
-  const GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f);
+  // shared memory of the sums: by position and by channel (staged), or the totals (general)
+  constexpr size_t kStagedSums = size_t(kWalkThreads) * VW * 16, kTotals = size_t(kWalkThreads) * VW * 8;
+  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f);
+  d.pvec = a.C % VW == 0 && misalign16(a.x) == 0 && misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   const GnGradWorkspace w = gn_grad_workspace(d, a.t);
   char* ws = static_cast<char*>(a.workspace);
   float* gpart = reinterpret_cast<float*>(ws + w.gpart);
@@ -1116,36 +1352,32 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   if (staged) {
     auto f = group ? (a.silu ? k_gn_grad_sums_staged<T, true, true> : k_gn_grad_sums_staged<T, true, false>)
                    : (a.silu ? k_gn_grad_sums_staged<T, false, true> : k_gn_grad_sums_staged<T, false, false>);
-    e = launch_staged(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
+    e = launch_staged(f, rows, d, stream, launches, kStagedSums, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
   } else {
     auto f = vec1 ? (a.silu ? k_gn_grad_sums<T, true, true> : k_gn_grad_sums<T, true, false>)
                   : (a.silu ? k_gn_grad_sums<T, false, true> : k_gn_grad_sums<T, false, false>);
-    e = launch_plain(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
+    e = launch_plain(f, rows, d, stream, launches, kTotals, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
   }
   if (e != cudaSuccess) return e;
-  auto join = join_by_block(d) ? k_gn_grad_join<kJoinThreads> : k_gn_grad_join<32>;
-  e = launch(join, dim3(join_grid(d)), dim3(kJoinThreads), 0, stream, gpart, d, m1, m2);
+  // joining the groups' parts and adding up the channels in one launch
+  const bool by_block = int64_t(d.p.chunks) * d.p.tiles > 64;
+  const int64_t per = by_block ? 1 : kSumsThreads / 32;
+  const int64_t joins = std::min<int64_t>((d.N * d.G + per - 1) / per, kPlanSms * 4);
+  const int64_t sums = cpart != nullptr ? std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, kPlanSms * 4) : 0;
+  auto join = by_block ? k_gn_grad_join<T, kSumsThreads> : k_gn_grad_join<T, 32>;
+  // (the sums of du are dbeta, those of du * h are dgamma)
+  e = launch(join, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, gpart, d, m1, m2, int(joins), cpart,
+             rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (staged && vec2) {
     auto f = group ? (a.silu ? k_gn_grad_apply_staged<T, true, true> : k_gn_grad_apply_staged<T, true, false>)
                    : (a.silu ? k_gn_grad_apply_staged<T, false, true> : k_gn_grad_apply_staged<T, false, false>);
-    e = launch_staged(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
-  } else {
-    auto f = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
-                  : (a.silu ? k_gn_grad_apply<T, false, true> : k_gn_grad_apply<T, false, false>);
-    e = launch_plain(f, rows, d, stream, launches, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
+    return launch_staged(f, rows, d, stream, launches, 0, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
   }
-  if (e != cudaSuccess) return e;
-  if (cpart != nullptr) {
-    const int64_t jobs = (int64_t(d.C) + 31) / 32 * 2;
-    // the sums of du are dbeta, those of du * h are dgamma
-    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart, rows,
-               d.p.tiles > 1 ? d.p.reps : int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta),
-               static_cast<T*>(a.dgamma));
-    if (e == cudaSuccess) *launches += 1;
-  }
-  return e;
+  auto f = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
+                : (a.silu ? k_gn_grad_apply<T, false, true> : k_gn_grad_apply<T, false, false>);
+  return launch_plain(f, rows, d, stream, launches, 0, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
 }
 
 }  // namespace

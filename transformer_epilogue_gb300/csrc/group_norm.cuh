@@ -144,6 +144,29 @@ __device__ __forceinline__ void for_channels(int c, int C, int D, F f) {
   }
 }
 
+// For each i < n: val(i, k, a, b) over k < terms, added up in a and b, then
+// out(i, a, b) by one thread.  `lanes` neighbouring lanes (a power of two) share
+// the terms of one i, as many as `threads` (whole warps, all calling) allow.
+template <typename VAL, typename OUT>
+__device__ __forceinline__ void sum_sets(int threads, int n, int terms, VAL val, OUT out) {
+  int log = 0;
+  while (log < 5 && (2 << log) * n <= threads && (2 << log) <= terms) ++log;
+  const int lanes = 1 << log, l = threadIdx.x & (lanes - 1);
+  for (int i0 = 0; i0 < n; i0 += threads >> log) {
+    const int i = i0 + (threadIdx.x >> log);
+    float a = 0.f, b = 0.f;
+    if (i < n) {
+#pragma unroll 4
+      for (int k = l; k < terms; k += lanes) val(i, k, a, b);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (i < n && l == 0) out(i, a, b);
+  }
+}
+
 // A sum of squares that rounding took below zero is 0 (and NaN stays NaN).
 __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : q; }
 

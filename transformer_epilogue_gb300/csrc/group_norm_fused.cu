@@ -123,51 +123,56 @@ __device__ __forceinline__ float4 ld_rank(const float4* p, int rank) {
   return v;
 }
 
-// Sums over the entries of each (sample, group) of a block.  Entries are floats
-// by position: fragment (MODE 0) or element; the group's are at
-// off + g De + j + k Cw, j < De, modulo the np positions of a sample (the
-// positions before `off` hold the channels that the last repeat misses).  A set
-// of lanes takes one (sample, group) at a time: `cols` lanes (a power of two)
-// side by side over j, and as many repeats k next to each other as fit a warp.
-struct Gather {
-  int De, Cw, np, reps, cols, set, q, slots;
-  __device__ __forceinline__ Gather(const FusedPlan& p, int D, int VW, bool frags) {
+// Sums over the entries of each (sample, group) of a block, in two steps: over
+// the repeats of each column (fragments in MODE 0, else channels), then over a
+// group's columns.  Entries are floats by position; column c of sample ns is at
+// off + c + k Cw, modulo the np positions of a sample (the positions before
+// `off` hold the channels that the last repeat misses).
+struct Entries {
+  int De, Cw, np, reps, q, slots, cols;
+  __device__ __forceinline__ Entries(const FusedPlan& p, int D, int VW, bool frags) {
     De = frags ? D / VW : D;
     Cw = frags ? p.cf : p.W;
     np = p.per_sample * p.cf * (frags ? 1 : VW);
-    reps = np / Cw;
-    cols = De >= 32 ? 32 : De <= 1 ? 1 : 1 << (32 - __clz(De - 1));
-    const int rows = reps <= 1 ? 1 : 1 << (32 - __clz(reps - 1));
-    set = min(32, cols * rows);
+    reps = static_cast<int>(unsigned(np) / unsigned(Cw));
     q = p.q;
     slots = p.samples * p.q;
+    cols = p.samples * Cw;
   }
-  // add(position, a, b) for each entry, then done(slot, a, b) by one lane
-  template <typename OFF, typename ADD, typename DONE>
-  __device__ __forceinline__ void run(OFF off_of, ADD add, DONE done) const {
-    const int sets = blockDim.x / set, l = threadIdx.x & (set - 1);
-    const int j0 = l & (cols - 1), k0 = l / cols, ks = set / cols;
-    for (int s0 = 0; s0 < slots; s0 += sets) {
-      const int s = s0 + threadIdx.x / set;
-      float a = 0.f, b = 0.f;
-      if (s < slots) {
-        const int ns = slots == q ? 0 : s / q, start = off_of(ns) + (s - ns * q) * De;
-        for (int k = k0; k < reps; k += ks) {
-          for (int j = j0; j < De; j += cols) {
-            int pos = start + j + k * Cw;
-            if (pos >= np) pos -= np;
-            add(ns * np + pos, a, b);
-          }
-        }
-      }
-      for (int o = set >> 1; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
-      if (s < slots && l == 0) done(s, ns_of(s), a, b);
+  __device__ __forceinline__ int sample_of(int slot) const {
+    return slots == q ? 0 : static_cast<int>(unsigned(slot) / unsigned(q));
+  }
+  // add(position, a, b) for each entry; col_a (and col_b): a float a column;
+  // done(slot, sample, a, b) by one lane.  `plain`: one repeat and no offset, so
+  // that entries are columns already.
+  template <bool PAIR, typename OFF, typename ADD, typename DONE>
+  __device__ __forceinline__ void run(const float* ent_a, const float* ent_b, float* col_a, float* col_b, bool plain,
+                                      OFF off_of, ADD add, DONE done) const {
+    const float* ca = ent_a;
+    const float* cb = ent_b;
+    if (!plain) {
+      sum_sets(blockDim.x, cols, reps,
+               [&](int i, int k, float& a, float& b) {
+                 const int ns = cols == Cw ? 0 : static_cast<int>(unsigned(i) / unsigned(Cw));
+                 int pos = off_of(ns) + (i - ns * Cw) + k * Cw;
+                 if (pos >= np) pos -= np;
+                 add(ns * np + pos, a, b);
+               },
+               [&](int i, float a, float b) {
+                 col_a[i] = a;
+                 if constexpr (PAIR) col_b[i] = b;
+               });
+      __syncthreads();
+      ca = col_a;
+      cb = col_b;
     }
+    sum_sets(blockDim.x, slots, De,
+             [&](int s, int k, float& a, float& b) {  // (sample ns, group g: columns ns Cw + g De + k)
+               a += ca[s * De + k];
+               if constexpr (PAIR) b += cb[s * De + k];
+             },
+             [&](int s, float a, float b) { done(s, sample_of(s), a, b); });
   }
-  __device__ __forceinline__ int ns_of(int s) const { return slots == q ? 0 : s / q; }
 };
 
 // gamma and beta of VW channels from c on (modulo W), which start at `from`.
@@ -200,6 +205,18 @@ __device__ __forceinline__ void for_slots_by_rank(int slots, int cluster, F f) {
 __device__ __forceinline__ float set_sum(float x, int set) {
   for (int o = set >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+
+// A thread's entries to their positions, 16 bytes at a time where there are several.
+template <int EV>
+__device__ __forceinline__ void put_entries(float* ent, const float (&v)[EV]) {
+  if constexpr (EV == 1) {
+    ent[threadIdx.x] = v[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < EV; e += 4)
+      *reinterpret_cast<float4*>(ent + threadIdx.x * EV + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
 }
 
 // A thread's sums of its values' distances from a centre, or of their squares.
@@ -246,7 +263,10 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float4* xch = reinterpret_cast<float4*>(smem);                 // (count, mean, M2) for the cluster
   float* ent = smem + (p.cluster > 1 ? 4 * slots : 0);
   float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
-  float* gk = cnt + (MODE == 2 ? ents : 0);                      // the group's first value
+  float* col = cnt + (MODE == 2 ? ents : 0);                     // sums by column, and their counts
+  const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
+  float* col_n = col + cols;
+  float* gk = col_n + (MODE == 2 ? cols : 0);                    // the group's first value
   float* gm = gk + slots;
   float* gr = gm + slots;
   const int rank = blockIdx.x & (p.cluster - 1);
@@ -275,7 +295,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   });
 
   const bool mine = trow < p.phases;
-  const Gather gather(p, d.D, VW, MODE == 0);
+  const Entries entries(p, d.D, VW, MODE == 0);
+  const bool plain = MODE != 2 && entries.reps == 1;
   const int64_t n0 = int64_t(p.slabs == 1 ? item : item / unsigned(p.slabs)) * p.samples;
   auto off_of = [&](int s) {
     return MODE == 2 && n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0;
@@ -287,8 +308,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float m[EV], s[EV];
   centred_sums<T, NV, MODE, false>(raw, at, shift, s);
   if (mine) {
-#pragma unroll
-    for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
+    put_entries(ent, s);
     if constexpr (MODE == 2) {
 #pragma unroll
       for (int e = 0; e < EV; ++e) m[e] = 0.f;
@@ -299,12 +319,12 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
           for (int e = 0; e < EV; ++e) m[e] += at.inside(k, e) ? 1.f : 0.f;
         }
       }
-#pragma unroll
-      for (int e = 0; e < EV; ++e) cnt[threadIdx.x * EV + e] = m[e];
+      put_entries(cnt, m);
     }
   }
   __syncthreads();
-  gather.run(off_of,
+  entries.run<MODE == 2>(
+             ent, cnt, col, col_n, plain, off_of,
              [&](int i, float& a, float& b) {
                a += ent[i];
                if constexpr (MODE == 2) b += cnt[i];
@@ -329,8 +349,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   for (int e = 0; e < EV; ++e) m[e] = mine ? gm[grp[e]] : 0.f;
   centred_sums<T, NV, MODE, true>(raw, at, m, s);
   if (mine) {
-#pragma unroll
-    for (int e = 0; e < EV; ++e) ent[threadIdx.x * EV + e] = s[e];
+    put_entries(ent, s);
   }
   __syncthreads();
   const float total = float(d.S) * float(d.D);
@@ -345,7 +364,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
       if (inv_out != nullptr) inv_out[i] = r;
     }
   };
-  gather.run(off_of, [&](int i, float& a, float&) { a += ent[i]; },
+  entries.run<false>(
+             ent, cnt, col, col_n, plain, off_of, [&](int i, float& a, float&) { a += ent[i]; },
              [&](int s, int ns, float a, float) {
                if (p.cluster == 1) finish(s, ns, gm[s], a - gr[s]);
                else xch[s].z = not_negative(a - gr[s]);
@@ -382,12 +402,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
       if (k < at.kn) {
         float v[VW];
         dev::Conv<T>::unpack(raw[k], v);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) v[e] = fmaf(v[e] - mu[MODE == 0 ? 0 : e], a[e], b[e]);
-        if (d.silu) {
-#pragma unroll
-          for (int e = 0; e < VW; ++e) v[e] = silu<T>(v[e]);
-        }
+        centre_scale_add(v, mu, a, b);
+        if (d.silu) activate<T>(v);
         at.store(ys, k, v);
       }
     }
@@ -410,7 +426,10 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float4* xch = reinterpret_cast<float4*>(smem);
   float* ent_a = smem + (p.cluster > 1 ? 4 * slots : 0);
   float* ent_b = ent_a + ents;
-  float* g1 = ent_b + ents;
+  const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
+  float* col_a = ent_b + ents;
+  float* col_b = col_a + cols;
+  float* g1 = col_b + cols;
   float* g2 = g1 + slots;
   const int rank = blockIdx.x & (p.cluster - 1);
   const unsigned first = blockIdx.x / unsigned(p.cluster);
@@ -418,7 +437,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   const bool mine = trow < p.phases;
   const float scale = 1.0f / (float(d.S) * float(d.D));
-  const Gather gather(p, d.D, VW, MODE == 0);
+  const Entries entries(p, d.D, VW, MODE == 0);
   dev::pdl_wait();
   dev::pdl_trigger();
 
@@ -466,11 +485,13 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
     auto values = [&](int k, float (&h)[VW], float (&du)[VW]) {
       dev::Conv<T>::unpack(raw[k], h);
       dev::Conv<T>::unpack(rdy[k], du);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) h[e] = (h[e] - mu[MODE == 0 ? 0 : e]) * rs[MODE == 0 ? 0 : e];
+      centre_scale(h, mu, rs);
       if (d.silu) {
+        float u[VW];
 #pragma unroll
-        for (int e = 0; e < VW; ++e) du[e] = silu_grad<T>(du[e], fmaf(h[e], ga[e], be[e]));
+        for (int e = 0; e < VW; ++e) u[e] = be[e];
+        fma_pairs(h, ga, u);
+        activate_grad<T>(du, u);
       }
     };
 #pragma unroll
@@ -478,11 +499,8 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       if (k < at.kn) {
         float h[VW], du[VW];
         values(k, h, du);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          sa[e] += du[e];
-          sb[e] = fmaf(du[e], h[e], sb[e]);
-        }
+        dev::add_pairs(sa, du);
+        fma_pairs(du, h, sb);
       }
     }
     if (mine) {
@@ -496,20 +514,21 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
         ent_a[threadIdx.x] = a;
         ent_b[threadIdx.x] = b;
       } else {
+        float a[VW], b[VW];
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
-          ent_a[threadIdx.x * VW + e] = sa[e] * ga[e];
-          ent_b[threadIdx.x * VW + e] = sb[e] * ga[e];
+          a[e] = sa[e] * ga[e];
+          b[e] = sb[e] * ga[e];
         }
+        put_entries(ent_a, a);
+        put_entries(ent_b, b);
       }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        tot_a[e] += sa[e];
-        tot_b[e] += sb[e];
-      }
+      dev::add_pairs(tot_a, sa);
+      dev::add_pairs(tot_b, sb);
     }
     __syncthreads();
-    gather.run([&](int) { return off; },
+    entries.run<true>(
+               ent_a, ent_b, col_a, col_b, MODE != 2 && entries.reps == 1, [&](int) { return off; },
                [&](int i, float& a, float& b) {
                  a += ent_a[i];
                  b += ent_b[i];
@@ -563,11 +582,8 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   if (cpart == nullptr) return;
   __syncthreads();
   if (mine) {
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      ent_a[threadIdx.x * VW + e] = tot_a[e];
-      ent_b[threadIdx.x * VW + e] = tot_b[e];
-    }
+    put_entries(ent_a, tot_a);
+    put_entries(ent_b, tot_b);
   }
   __syncthreads();
   // channel c is at off + c + k W, modulo a sample's positions, in every sample
@@ -928,7 +944,8 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads,
 size_t fused_smem(const FusedPlan& p, int mode, int vw, bool grad) {
   const size_t slots = size_t(p.samples) * p.q, frags = size_t(p.phases) * p.cf;
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
-  return 4 * (ents + (p.cluster > 1 ? 4 * slots : 0) + (grad ? 2 : 3) * slots);
+  const size_t cols = size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
+  return 4 * (ents + cols + (p.cluster > 1 ? 4 * slots : 0) + (grad ? 2 : 3) * slots);
 }
 constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
 
@@ -990,7 +1007,7 @@ bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, Fu
   // a CTA's items share the offset of their channels: all samples start alike,
   // or a CTA has one sample
   if (!slab && S * C % vw != 0 && (p->samples > 1 || p->grid_items < p->items)) return false;
-  return fused_smem(*p, slab ? 0 : 2, vw, true) <= kSmemMost;
+  return fused_smem(*p, slab ? 1 : 2, vw, true) <= kSmemMost;  // (mode 0 needs less)
 }
 
 }  // namespace
