@@ -441,8 +441,8 @@ struct GradApplyValues : GradValues<T, EV, SILU> {
 // block's barriers.
 // ---------------------------------------------------------------------------
 
-constexpr int kStageBytes = 16384;   // of all operands together
-constexpr int kStages = 4;
+constexpr int kStageBytes = 32768;   // of all operands together
+constexpr int kStages = 2;
 constexpr int kStageSmem = kStages * kStageBytes;
 
 struct StageBars {
@@ -524,7 +524,7 @@ struct RowStream {
   }
 
   // A consumer: f(row, raw) for the walk rows of an item that have a fragment in
-  // the thread's column, rows counted from the item's first; two at a time, so
+  // the thread's column, rows counted from the item's first; four or two at a time, so
   // that one row's arithmetic covers the other's latency.
   template <typename F>
   __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
@@ -542,6 +542,17 @@ struct RowStream {
         for (int o = 0; o < NOPS; ++o) raw[o] = dev::lds16(src + o * (kStageBytes / NOPS) + i * row_bytes);
       };
       int i = 0;
+      for (; i + 3 < k; i += 4) {
+        uint4 a[NOPS], b[NOPS], c[NOPS], e[NOPS];
+        load(i, a);
+        load(i + 1, b);
+        load(i + 2, c);
+        load(i + 3, e);
+        f(r + i, a);
+        f(r + i + 1, b);
+        f(r + i + 2, c);
+        f(r + i + 3, e);
+      }
       for (; i + 1 < k; i += 2) {
         uint4 a[NOPS], b[NOPS];
         load(i, a);
