@@ -20,6 +20,7 @@ SHAPES = [
     ((1, 5000, 32), 8), ((2, 3000, 1), 1), ((1, 2777, 5), 5), ((1, 700, 3), 1),  # few channels
     ((2, 9973, 40), 4),
     ((2, 1024, 320), 32), ((1, 2048, 96), 96), ((3, 1331, 189), 9), ((1, 4096, 64), 2),  # spread over a cluster
+    ((4503, 1, 1024), 8), ((1103, 1, 4352), 17), ((9001, 1, 544), 17),  # many tokens
     ((1, 70000, 64), 4), ((2, 30011, 33), 3), ((1, 300, 12288), 32),  # more than a cluster holds
 ]
 

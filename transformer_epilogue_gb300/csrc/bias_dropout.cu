@@ -26,34 +26,37 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The generator's state of one call: the key, the offset (plus *offset_dev, read
+// The generator's state of one call: the rounds' keys, the offset (plus *offset_dev, read
 // when the kernel runs, so that a captured graph draws anew on every replay)
 // and the last word that keeps an element.
+constexpr int kRounds = 10;
 struct DropRng {
-  uint64_t seed;
   uint64_t offset;
   const uint64_t* offset_dev;
+  uint32_t keys[2 * kRounds];  // the key words of each round
   uint32_t last_kept;
   float scale;
 };
 
-// WIDE: block numbers beyond 32 bits (more than 2^34 elements).  Else the
-// counter's second word is 0, and with the offset and the key the same in all
-// threads the first two rounds have one product per thread each, not two.
+// The four words of a block.  Written in 32-bit halves, with the round keys from
+// the kernel's parameters, so that a round is two wide multiplies and two
+// three-input exclusive ors (as 64-bit products and running keys it took 140 us,
+// not 108, for 2^27 float16 elements).  WIDE: block numbers beyond 32 bits (more
+// than 2^34 elements).  Else the counter's second word is 0, and with the offset
+// and the key the same in all threads the first two rounds have one product per
+// thread each, not two.
 template <bool WIDE>
-__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, const DropRng& g) {
   uint32_t c0 = uint32_t(block), c1 = WIDE ? uint32_t(block >> 32) : 0u;
   uint32_t c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
-  uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint64_t p0 = uint64_t(0xD2511F53u) * c0, p1 = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(p1 >> 32) ^ c1 ^ k0;
-    c1 = uint32_t(p1);
-    c2 = uint32_t(p0 >> 32) ^ c3 ^ k1;
-    c3 = uint32_t(p0);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+  for (int r = 0; r < kRounds; ++r) {
+    const uint32_t h0 = __umulhi(0xD2511F53u, c0), l0 = 0xD2511F53u * c0;
+    const uint32_t h1 = __umulhi(0xCD9E8D57u, c2), l1 = 0xCD9E8D57u * c2;
+    c0 = h1 ^ c1 ^ g.keys[2 * r];
+    c1 = l1;
+    c2 = h0 ^ c3 ^ g.keys[2 * r + 1];
+    c3 = l0;
   }
   return make_uint4(c0, c1, c2, c3);
 }
@@ -63,7 +66,7 @@ template <bool WIDE, int VW>
 __device__ __forceinline__ void drop(int64_t i0, uint64_t offset, const DropRng& g, float (&v)[VW]) {
 #pragma unroll
   for (int b = 0; b < VW; b += 4) {
-    const uint4 w = philox<WIDE>(uint64_t(i0 + b) / 4, offset, g.seed);
+    const uint4 w = philox<WIDE>(uint64_t(i0 + b) / 4, offset, g);
     v[b] = w.x <= g.last_kept ? v[b] : 0.f;
     v[b + 1] = w.y <= g.last_kept ? v[b + 1] : 0.f;
     v[b + 2] = w.z <= g.last_kept ? v[b + 2] : 0.f;
@@ -178,10 +181,11 @@ k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, 
 // sums, and leaves the sums of its chunk in `partial`: [chunk][C] where one tile covers a
 // walk row (the block adds the repeats of a channel up), else [chunk][walk row].
 template <typename T, bool VEC, bool WIDE>
-__global__ void __launch_bounds__(kWalkThreads)
-k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRng g, float* partial) {
+__global__ void __launch_bounds__(kWalkThreads, 4)
+k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, int64_t full_rows, int64_t rest, DropRng g,
+                    float* partial) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int U = 4;
+  constexpr int U = 3;
   __shared__ float sums[kWalkThreads * VW];
   dev::pdl_wait();
   dev::pdl_trigger();
@@ -193,29 +197,42 @@ k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRn
   float acc[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) acc[e] = 0.f;
+  auto row = [&](int64_t i0, float (&v)[VW]) {
+    drop<WIDE>(i0, offset, g, v);
+    dev::scale_pairs(v, g.scale);
+    dev::add_pairs(acc, v);
+  };
   if (mine) {
-    const int64_t r1 = min(p.rows, (chunk + 1) * p.rows_per_chunk);
-    for (int64_t r0 = chunk * p.rows_per_chunk; r0 < r1; r0 += U) {
-      // the tensor's last fragment, which may be partial, is in its last walk row
+    const int64_t ra = chunk * p.rows_per_chunk, pitch = p.row_frags * VW;
+    // rows of this chunk with a whole fragment in this column, and then perhaps the tensor's last, partial one
+    const int64_t rb = min(full_rows + (j < rest ? 1 : 0), ra + p.rows_per_chunk);
+    int64_t i0 = (ra * p.row_frags + j) * VW, r = ra;
+    for (; r + U <= rb; r += U, i0 += U * pitch) {
       RawFrag<T, VEC> a[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i0 = ((r0 + u) * p.row_frags + j) * VW;
-        if (r0 + u < r1 && (VEC ? i0 + VW <= n : i0 < n)) a[u].load(dy, i0, n);
-      }
+      for (int u = 0; u < U; ++u) a[u].load(dy, i0 + u * pitch, n);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t i0 = ((r0 + u) * p.row_frags + j) * VW;
-        if (r0 + u < r1 && i0 < n) {
-          float v[VW];
-          if (!VEC || i0 + VW <= n) a[u].get(v);
-          else dev::load_frag<T, false>(dy, i0, n, v);
-          drop<WIDE>(i0, offset, g, v);
-          dev::scale_pairs(v, g.scale);
-          dev::add_pairs(acc, v);
-          dev::store_frag<T, VEC>(dx, i0, n, v);
-        }
+        float v[VW];
+        a[u].get(v);
+        row(i0 + u * pitch, v);
+        if constexpr (VEC) dev::st16_stream(dx + i0 + u * pitch, dev::Conv<T>::pack(v));
+        else dev::store_frag<T, false>(dx, i0 + u * pitch, n, v);
       }
+    }
+    for (; r < rb; ++r, i0 += pitch) {
+      RawFrag<T, VEC> a;
+      float v[VW];
+      a.load(dy, i0, n);
+      a.get(v);
+      row(i0, v);
+      dev::store_frag<T, VEC>(dx, i0, n, v);
+    }
+    if (j == rest && n % VW != 0 && r == full_rows && r < ra + p.rows_per_chunk) {
+      float v[VW];
+      dev::load_frag<T, false>(dy, i0, n, v);
+      row(i0, v);
+      dev::store_frag<T, false>(dx, i0, n, v);
     }
   }
   if (p.tiles > 1) {
@@ -253,7 +270,15 @@ k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, DropRn
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline DropRng rng_of(const BiasDropoutArgs& a) {
-  return DropRng{a.seed, a.offset, a.offset_dev, a.last_kept, a.scale};
+  DropRng g{a.offset, a.offset_dev, {}, a.last_kept, a.scale};
+  uint32_t k0 = uint32_t(a.seed), k1 = uint32_t(a.seed >> 32);
+  for (int r = 0; r < kRounds; ++r) {
+    g.keys[2 * r] = k0;
+    g.keys[2 * r + 1] = k1;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return g;
 }
 
 template <typename T, int BIAS, bool RES, bool VEC, bool WIDE>
@@ -287,7 +312,7 @@ cudaError_t bias_dropout_t(const BiasDropoutArgs& a, int sm_count, cudaStream_t 
 }
 
 WalkPlan grad_walk(DType t, int64_t n, int64_t C) {
-  return make_walk(n, C, t == DType::F32 ? 4 : 8, 1, kPlanSms * 4, 4);
+  return make_walk(n, C, t == DType::F32 ? 4 : 8, 1, kPlanSms * 8, 4);
 }
 
 template <typename T>
@@ -295,13 +320,15 @@ cudaError_t bias_dropout_grad_t(const BiasDropoutArgs& a, cudaStream_t stream, i
   const WalkPlan p = grad_walk(a.t, a.n, a.C);
   float* partial = static_cast<float*>(a.workspace);
   const dim3 grid(unsigned(int64_t(p.tiles) * p.chunks));
+  constexpr int VW = dev::Vec16<T>::N;
+  const int64_t full_rows = a.n / VW / p.row_frags, rest = a.n / VW % p.row_frags;
   cudaError_t e;
   if (al16(a.x) && al16(a.y) && narrow(a.n))
     e = launch(k_bias_dropout_grad<T, true, false>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
-               static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
+               static_cast<T*>(a.y), a.n, a.C, p, full_rows, rest, rng_of(a), partial);
   else
     e = launch(k_bias_dropout_grad<T, false, true>, grid, dim3(p.threads), 0, stream, static_cast<const T*>(a.x),
-               static_cast<T*>(a.y), a.n, a.C, p, rng_of(a), partial);
+               static_cast<T*>(a.y), a.n, a.C, p, full_rows, rest, rng_of(a), partial);
   if (e != cudaSuccess) return e;
   *launches += 1;
   const int64_t jobs = std::min<int64_t>((a.C + 31) / 32, INT_MAX);

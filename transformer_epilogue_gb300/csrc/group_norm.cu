@@ -523,11 +523,10 @@ struct RowStream {
     }
   }
 
-  // A consumer: f(row, raw) for the walk rows of an item that have a fragment in
-  // the thread's column, rows counted from the item's first; four or two at a time, so
-  // that one row's arithmetic covers the other's latency.
+  // A consumer: f(row, src) for each stage of an item, row the stage's first,
+  // counted from the item's first, and src the thread's place in it.
   template <typename F>
-  __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
+  __device__ __forceinline__ void stages(const Range& range, F f) {
     const int n = static_cast<int>(range.rb - range.ra);
     for (int r = 0; r < n; r += rows, ring.next()) {
       ok = ok && dev::mbar_wait(&bars->full[ring.st], ring.phase);
@@ -535,38 +534,43 @@ struct RowStream {
         ok = false;
         continue;
       }
-      const unsigned char* src = smem + ring.st * kStageBytes + threadIdx.x * 16;
-      const int k = min(rows, mine - r);
-      auto load = [&](int i, uint4 (&raw)[NOPS]) {
-#pragma unroll
-        for (int o = 0; o < NOPS; ++o) raw[o] = dev::lds16(src + o * (kStageBytes / NOPS) + i * row_bytes);
-      };
-      int i = 0;
-      for (; i + 3 < k; i += 4) {
-        uint4 a[NOPS], b[NOPS], c[NOPS], e[NOPS];
-        load(i, a);
-        load(i + 1, b);
-        load(i + 2, c);
-        load(i + 3, e);
-        f(r + i, a);
-        f(r + i + 1, b);
-        f(r + i + 2, c);
-        f(r + i + 3, e);
-      }
-      for (; i + 1 < k; i += 2) {
-        uint4 a[NOPS], b[NOPS];
-        load(i, a);
-        load(i + 1, b);
-        f(r + i, a);
-        f(r + i + 1, b);
-      }
-      if (i < k) {
-        uint4 a[NOPS];
-        load(i, a);
-        f(r + i, a);
-      }
+      f(r, smem + ring.st * kStageBytes + threadIdx.x * 16);
       dev::release_stage(&bars->empty[ring.st]);
     }
+  }
+  template <int R>
+  __device__ __forceinline__ void load(const unsigned char* src, int i, uint4 (&raw)[R][NOPS]) const {
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+#pragma unroll
+      for (int o = 0; o < NOPS; ++o)
+        raw[u][o] = dev::lds16(src + o * (kStageBytes / NOPS) + (i + u) * row_bytes);
+  }
+  // f(row, raw) for the walk rows of an item that have a fragment in the thread's
+  // column; raw holds four, two or one rows, so that one row's arithmetic covers
+  // another's latency.
+  template <typename F>
+  __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
+    stages(range, [&](int r, const unsigned char* src) {
+      const int k = min(rows, mine - r);
+      int i = 0;
+      for (; i + 3 < k; i += 4) {
+        uint4 raw[4][NOPS];
+        load(src, i, raw);
+        f(r + i, raw);
+      }
+      if (i + 1 < k) {
+        uint4 raw[2][NOPS];
+        load(src, i, raw);
+        f(r + i, raw);
+        i += 2;
+      }
+      if (i < k) {
+        uint4 raw[1][NOPS];
+        load(src, i, raw);
+        f(r + i, raw);
+      }
+    });
   }
   // The next stage (an item's first), once its rows are there.
   __device__ __forceinline__ const unsigned char* peek() {
@@ -652,18 +656,21 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
     consumer_sync();
 #pragma unroll
     for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
-    rows.consume(r, rows.mine(r, t), [&](int, const uint4 (&raw)[1]) {
-      float v[VW];
-      dev::Conv<T>::unpack(raw[0], v);
+    rows.consume(r, rows.mine(r, t), [&](int, const auto& raw) {
 #pragma unroll
-      for (int e = 0; e < VW; e += 2) {
-        const float2 m = pair_of<VW>(c, e);
-        const float2 w = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m.x, -m.y));
-        v[e] = w.x;
-        v[e + 1] = w.y;
+      for (const auto& one : raw) {
+        float v[VW];
+        dev::Conv<T>::unpack(one[0], v);
+#pragma unroll
+        for (int e = 0; e < VW; e += 2) {
+          const float2 m = pair_of<VW>(c, e);
+          const float2 w = __fadd2_rn(make_float2(v[e], v[e + 1]), make_float2(-m.x, -m.y));
+          v[e] = w.x;
+          v[e + 1] = w.y;
+        }
+        dev::add_pairs(s, v);
+        fma_pairs(v, v, q);
       }
-      dev::add_pairs(s, v);
-      fma_pairs(v, v, q);
     });
     if (t.mine) {
       if constexpr (EV == 1) {
@@ -740,11 +747,14 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
     const int64_t pitch = p.row_frags * VW;
     T* py = y + r.n * d.L + r.ra * pitch + t.j * VW;
-    rows.consume(r, rows.mine(r, t), [&](int row, const uint4 (&raw)[1]) {
-      float v[VW];
-      dev::Conv<T>::unpack(raw[0], v);
-      val(v);
-      dev::st16_stream(py + row * pitch, dev::Conv<T>::pack(v));
+    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
+#pragma unroll
+      for (const auto& one : raw) {
+        float v[VW];
+        dev::Conv<T>::unpack(one[0], v);
+        val(v);
+        dev::st16_stream(py + row++ * pitch, dev::Conv<T>::pack(v));
+      }
     });
   }
 }
@@ -786,13 +796,16 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
     float sa[VW], sb[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
-    rows.consume(r, rows.mine(r, t), [&](int, const uint4 (&raw)[2]) {
-      float v[VW], w[VW];
-      dev::Conv<T>::unpack(raw[0], v);
-      dev::Conv<T>::unpack(raw[1], w);
-      val(v, w);
-      dev::add_pairs(sa, w);
-      fma_pairs(w, v, sb);
+    rows.consume(r, rows.mine(r, t), [&](int, const auto& raw) {
+#pragma unroll
+      for (const auto& one : raw) {
+        float v[VW], w[VW];
+        dev::Conv<T>::unpack(one[0], v);
+        dev::Conv<T>::unpack(one[1], w);
+        val(v, w);
+        dev::add_pairs(sa, w);
+        fma_pairs(w, v, sb);
+      }
     });
     if (t.mine) {
       for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) { sb[e] *= inv[r.n * d.G + g]; });  // du t r = du h
@@ -869,14 +882,257 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     }
     const int64_t pitch = p.row_frags * VW;
     T* po = dx + r.n * d.L + r.ra * pitch + t.j * VW;
-    rows.consume(r, rows.mine(r, t), [&](int row, const uint4 (&raw)[2]) {
-      float v[VW], w[VW];
-      dev::Conv<T>::unpack(raw[0], v);
-      dev::Conv<T>::unpack(raw[1], w);
-      val.dx(v, w);
-      dev::st16_stream(po + row * pitch, dev::Conv<T>::pack(v));
+    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
+#pragma unroll
+      for (const auto& one : raw) {
+        float v[VW], w[VW];
+        dev::Conv<T>::unpack(one[0], v);
+        dev::Conv<T>::unpack(one[1], w);
+        val.dx(v, w);
+        dev::st16_stream(po + row++ * pitch, dev::Conv<T>::pack(v));
+      }
     });
   }
+}
+
+// ---------------------------------------------------------------------------
+// One position a sample (S = 1), D / VW a power of two up to 32: the norm over
+// each token's groups.  A group's fragments are neighbouring lanes, so its sums
+// are shuffles; the tensor is one walk over all the tokens (N = 1, S = tokens in
+// `d`), in the staged rows above, and a thread's channels stay the same.  This
+// form is for many tokens; k_gn_token (group_norm_fused.cu) takes few.
+// ---------------------------------------------------------------------------
+
+struct TokenSet {
+  int lanes;       // of a group
+  unsigned mask;   // this thread's set of them
+  int64_t tokens_a_row, token0;  // tokens of a walk row, this thread's among them
+  int group;       // of the token
+  __device__ __forceinline__ TokenSet(const GnDims& d, const Tile& t, int vw, int set) : lanes(set) {
+    const int lane = threadIdx.x & 31, frags = d.C / vw;  // of a token
+    mask = set == 32 ? 0xffffffffu : ((1u << set) - 1u) << (lane & ~(set - 1));
+    tokens_a_row = d.p.row_frags / frags;
+    token0 = t.j / frags;
+    group = static_cast<int>(t.j - token0 * frags) / set;
+  }
+  template <int R>
+  __device__ __forceinline__ void sum(float (&x)[R]) const {
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      float y[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u) y[u] = __shfl_xor_sync(mask, x[u], o);
+#pragma unroll
+      for (int u = 0; u < R; ++u) x[u] += y[u];
+    }
+  }
+};
+
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, T* y, float* mean_out,
+                  float* inv_out, GnDims d, int set) {
+  constexpr int VW = dev::Vec16<T>::N;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 1> rows(&bars, smem, d, t);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[1] = {x};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, dev::policy_evict_first());
+    return;
+  }
+  const TokenSet ts(d, t, VW, set);
+  const float scale = 1.0f / float(d.D);
+  const int lead = (threadIdx.x & 31) & ~(set - 1);
+  float a[VW], b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) a[e] = b[e] = 0.f;
+  if (t.mine) {
+    const int c0 = first_channel(t.j, VW, 0, d.C);
+    load_param(gamma, c0, d.C, d.pvec, a);
+    if (beta != nullptr) load_param(beta, c0, d.C, d.pvec, b);
+  }
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    const int64_t pitch = p.row_frags * VW;
+    T* py = y + r.ra * pitch + t.j * VW;
+    const int64_t g0 = (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
+    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
+      constexpr int R = sizeof(raw) / sizeof(raw[0]);
+      float v[R][VW], s[R], q[R], mu[R], by[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u) dev::Conv<T>::unpack(raw[u][0], v[u]);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {  // sums relative to the group's first value
+        mu[u] = __shfl_sync(ts.mask, v[u][0], lead);
+        s[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) s[u] += v[u][e] - mu[u];
+      }
+      ts.sum(s);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        const float m = s[u] * scale, first = mu[u];
+        mu[u] = first + m;
+        by[u] = m - (mu[u] - first);  // mu is rounded: off the mean by this
+        q[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          v[u][e] -= mu[u];
+          q[u] = fmaf(v[u][e], v[u][e], q[u]);
+        }
+      }
+      ts.sum(q);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        const float k = 1.0f / sqrtf(not_negative(fmaf(q[u], scale, -by[u] * by[u])) + d.eps);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) v[u][e] = fmaf(v[u][e] * k, a[e], b[e]);
+        if constexpr (SILU) activate<T>(v[u]);
+        dev::st16_stream(py + (row + u) * pitch, dev::Conv<T>::pack(v[u]));
+        if ((threadIdx.x & 31) == lead) {
+          const int64_t g = g0 + (row + u) * ts.tokens_a_row * d.G;
+          if (mean_out != nullptr) mean_out[g] = mu[u];
+          if (inv_out != nullptr) inv_out[g] = k;
+        }
+      }
+    });
+  }
+}
+
+// Its gradient.  The statistics of a stage's tokens are loaded before the stage
+// before it is used; the parameters' sums run on in registers and leave as row
+// blockIdx / tiles of cpart, 2 x [row][C].
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kWalkThreads + 32, 2)
+k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
+                       const float* mean, const float* inv, T* dx, float* cpart, GnDims d, int set) {
+  constexpr int VW = dev::Vec16<T>::N;
+  constexpr int kAhead = 4;  // rows of a stage whose statistics are loaded ahead
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) StageBars bars;
+  float* s_a = reinterpret_cast<float*>(smem + kStageSmem);
+  float* s_b = s_a + kWalkThreads * VW;
+  const WalkPlan& p = d.p;
+  const Tile t(p);
+  RowStream<T, 2> rows(&bars, smem, d, t);
+  dev::pdl_wait();
+  dev::pdl_trigger();
+  const int consumers = blockDim.x - 32;
+  if (int(threadIdx.x) >= consumers) {
+    const T* const base[2] = {x, dy};
+    if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, dev::policy_evict_first());
+    return;
+  }
+  const TokenSet ts(d, t, VW, set);
+  const float scale = 1.0f / float(d.D);
+  float ga[VW], be[VW], tot_a[VW], tot_b[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) ga[e] = be[e] = tot_a[e] = tot_b[e] = 0.f;
+  if (t.mine) {
+    const int c0 = first_channel(t.j, VW, 0, d.C);
+    load_param(gamma, c0, d.C, d.pvec, ga);
+    if (SILU && beta != nullptr) load_param(beta, c0, d.C, d.pvec, be);
+  }
+  for (Items it(d, false); it.more(); it.next()) {
+    const Range r(p, it.item(), rows.total);
+    const int64_t pitch = p.row_frags * VW, gpitch = ts.tokens_a_row * d.G;
+    const int mine = rows.mine(r, t);
+    T* po = dx + r.ra * pitch + t.j * VW;
+    const float* pm = mean + (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
+    const float* pi = inv + (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
+    float mu[kAhead], rs[kAhead];
+    auto ahead = [&](int row) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const bool on = u < rows.rows && row + u < mine;
+        mu[u] = on ? pm[(row + u) * gpitch] : 0.f;
+        rs[u] = on ? pi[(row + u) * gpitch] : 0.f;
+      }
+    };
+    ahead(0);
+    rows.stages(r, [&](int row, const unsigned char* src) {
+      float m[kAhead], k[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        m[u] = mu[u];
+        k[u] = rs[u];
+      }
+      ahead(row + rows.rows);
+      const int n = min(rows.rows, mine - row);
+      auto two = [&](int i, int count, float m0, float m1, float k0, float k1) {
+        uint4 raw[2][2];
+        rows.load(src, i, raw);
+        float h[2][VW], w[2][VW], s[4];
+        const float mm[2] = {m0, m1}, kk[2] = {k0, k1};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          dev::Conv<T>::unpack(raw[u][0], h[u]);
+          dev::Conv<T>::unpack(raw[u][1], w[u]);
+          if (u >= count) {
+#pragma unroll
+            for (int e = 0; e < VW; ++e) h[u][e] = w[u][e] = 0.f;
+          }
+          const float one_m[1] = {mm[u]}, one_k[1] = {kk[u]};
+          centre_scale(h[u], one_m, one_k);
+          if constexpr (SILU) {
+            float a[VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) a[e] = be[e];
+            fma_pairs(h[u], ga, a);
+            activate_grad<T>(w[u], a);
+          }
+          dev::add_pairs(tot_a, w[u]);
+          fma_pairs(w[u], h[u], tot_b);
+          s[2 * u] = s[2 * u + 1] = 0.f;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            w[u][e] *= ga[e];
+            s[2 * u] += w[u][e];
+            s[2 * u + 1] = fmaf(w[u][e], h[u][e], s[2 * u + 1]);
+          }
+        }
+        ts.sum(s);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float p1 = s[2 * u] * scale, p2 = s[2 * u + 1] * scale;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) w[u][e] = kk[u] * (fmaf(-p2, h[u][e], w[u][e] - p1));
+          if (u < count) dev::st16_stream(po + (row + i + u) * pitch, dev::Conv<T>::pack(w[u]));
+        }
+      };
+      // (a second row beyond the last is read from within the stage, and not used)
+      if (n > 0) two(0, n, m[0], m[1], k[0], k[1]);
+      if (n > 2) two(2, n - 2, m[2], m[3], k[2], k[3]);
+      for (int i = kAhead; i < n; i += 2) {
+        const bool both = i + 1 < n;
+        two(i, n - i, pm[(row + i) * gpitch], both ? pm[(row + i + 1) * gpitch] : 0.f, pi[(row + i) * gpitch],
+            both ? pi[(row + i + 1) * gpitch] : 0.f);
+      }
+    });
+  }
+  if (cpart == nullptr) return;
+  if (t.mine) {
+    put(s_a, tot_a);
+    put(s_b, tot_b);
+  }
+  consumer_sync();
+  const Columns cols(d, t, VW, 1);
+  const int64_t cta_rows = gridDim.x / unsigned(p.tiles), cta_row = blockIdx.x / unsigned(p.tiles);
+  float* oa = cpart + cta_row * d.C + int64_t(t.tile) * p.tile_frags * VW;
+  sum_sets(consumers, cols.cols, cols.reps,
+           [&](int i, int k, float& a, float& b) {
+             a += s_a[i + k * cols.cols];
+             b += s_b[i + k * cols.cols];
+           },
+           [&](int i, float a, float b) {
+             oa[i] = a;
+             oa[cta_rows * d.C + i] = b;
+           });
 }
 
 // ---------------------------------------------------------------------------
@@ -1391,6 +1647,56 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   return launch_plain(f, rows, d, stream, launches, 0, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
 }
 
+// The token form: the tensor as one sample of N positions, tiles of whole groups.
+GnDims token_dims(DType t, int64_t N, int64_t C, int64_t G, float eps) {
+  GnDims d = dims_of(t, 1, N, C, G, eps);
+  const int set = int(d.D / vec_width(t));
+  d.p = make_walk(d.L, C, int(vec_width(t)), 1, kPlanSms * 2, 4);
+  d.p.tile_frags = (d.p.tile_frags + set - 1) / set * set;
+  d.p.threads = (d.p.tile_frags + 31) / 32 * 32;
+  return d;
+}
+int64_t token_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 2); }
+
+// At least this many bytes: below, the direct form's shorter start wins
+// (bf16, C = 4096, us: ).
+constexpr int64_t kTokenStagedBytes = int64_t(8) << 20;
+
+bool token_staged(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+  const int64_t vw = vec_width(t), D = C / G;
+  return S == 1 && D % vw == 0 && D / vw <= 32 && (D / vw & (D / vw - 1)) == 0 &&
+         N * C * (t == DType::F32 ? 4 : 2) >= kTokenStagedBytes;
+}
+
+template <typename T>
+cudaError_t token_fwd_t(const GroupNormArgs& a, cudaStream_t stream, int* launches) {
+  GnDims d = token_dims(a.t, a.N, a.C, a.G, a.eps);
+  d.pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
+  auto f = a.silu ? k_gn_token_staged<T, true> : k_gn_token_staged<T, false>;
+  return launch_staged(f, token_rows(d), d, stream, launches, 0, static_cast<const T*>(a.x),
+                       static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta), static_cast<T*>(a.y), a.mean,
+                       a.inv, d, int(d.D / dev::Vec16<T>::N));
+}
+
+template <typename T>
+cudaError_t token_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* launches) {
+  constexpr int VW = dev::Vec16<T>::N;
+  GnDims d = token_dims(a.t, a.N, a.C, a.G, 0.f);
+  d.pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
+  const int64_t rows = token_rows(d);
+  float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
+  auto f = a.silu ? k_gn_grad_token_staged<T, true> : k_gn_grad_token_staged<T, false>;
+  cudaError_t e = launch_staged(f, rows, d, stream, launches, size_t(kWalkThreads) * VW * 8,
+                                static_cast<const T*>(a.dy), static_cast<const T*>(a.x),
+                                static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta), a.mean, a.inv,
+                                static_cast<T*>(a.dx), cpart, d, int(d.D / VW));
+  if (e != cudaSuccess || cpart == nullptr) return e;
+  e = launch(k_channel_sums<T>, dim3(unsigned((int64_t(d.C) + 31) / 32 * 2)), dim3(kSumsThreads), 0, stream, cpart,
+             rows, int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
 }  // namespace
 
 size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
@@ -1398,11 +1704,21 @@ size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int6
 }
 
 size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
-  return std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
-                  group_norm_grad_fused_bytes(t, N, S, C, G));
+  size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
+                         group_norm_grad_fused_bytes(t, N, S, C, G));
+  if (token_staged(t, N, S, C, G))
+    most = std::max(most, size_t(token_rows(token_dims(t, N, C, G, 0.f))) * size_t(C) * 8);
+  return most;
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  if (token_staged(a.t, a.N, a.S, a.C, a.G) && misalign16(a.x) == 0 && misalign16(a.y) == 0) {
+    switch (a.t) {
+      case DType::F32: return token_fwd_t<float>(a, stream, launches);
+      case DType::F16: return token_fwd_t<__half>(a, stream, launches);
+      default: return token_fwd_t<__nv_bfloat16>(a, stream, launches);
+    }
+  }
   bool done = false;
   const cudaError_t e = launch_group_norm_fused(a, sm_count, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
@@ -1414,6 +1730,13 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
 }
 
 cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  if (token_staged(a.t, a.N, a.S, a.C, a.G) && misalign16(a.x) == 0 && misalign16(a.dy) == 0 && misalign16(a.dx) == 0) {
+    switch (a.t) {
+      case DType::F32: return token_grad_t<float>(a, stream, launches);
+      case DType::F16: return token_grad_t<__half>(a, stream, launches);
+      default: return token_grad_t<__nv_bfloat16>(a, stream, launches);
+    }
+  }
   bool done = false;
   const cudaError_t e = launch_group_norm_grad_fused(a, sm_count, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
