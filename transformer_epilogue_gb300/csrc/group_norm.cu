@@ -963,40 +963,42 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     const int64_t g0 = (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
       constexpr int R = sizeof(raw) / sizeof(raw[0]);
-      float v[R][VW], s[R], q[R], mu[R], by[R];
+      // sums and sums of squares relative to a centre: the median of three of the
+      // group's values.  With at most 256 values to a group it is at most 16
+      // standard deviations off the mean, whatever they are.
+      float v[R][VW], c[R], s[2 * R];
 #pragma unroll
-      for (int u = 0; u < R; ++u) dev::Conv<T>::unpack(raw[u][0], v[u]);
+      for (int u = 0; u < R; ++u) {
+        dev::Conv<T>::unpack(raw[u][0], v[u]);
+        c[u] = median3(__shfl_sync(ts.mask, v[u][0], lead), __shfl_sync(ts.mask, v[u][VW / 2], lead + set / 2),
+                       __shfl_sync(ts.mask, v[u][VW - 1], lead + set - 1));
+      }
 #pragma unroll
-      for (int u = 0; u < R; ++u) {  // sums relative to the group's first value
-        mu[u] = __shfl_sync(ts.mask, v[u][0], lead);
-        s[u] = 0.f;
+      for (int u = 0; u < R; ++u) {
+        float2 p = make_float2(0.f, 0.f), q = p;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) s[u] += v[u][e] - mu[u];
+        for (int e = 0; e < VW; e += 2) {
+          const float2 w = __fadd2_rn(make_float2(v[u][e], v[u][e + 1]), make_float2(-c[u], -c[u]));
+          p = __fadd2_rn(p, w);
+          q = __ffma2_rn(w, w, q);
+        }
+        s[2 * u] = p.x + p.y;
+        s[2 * u + 1] = q.x + q.y;
       }
       ts.sum(s);
 #pragma unroll
       for (int u = 0; u < R; ++u) {
-        const float m = s[u] * scale, first = mu[u];
-        mu[u] = first + m;
-        by[u] = m - (mu[u] - first);  // mu is rounded: off the mean by this
-        q[u] = 0.f;
+        const float m = s[2 * u] * scale, mu[1] = {c[u] + m};
+        const float k = rsqrtf(not_negative(fmaf(s[2 * u + 1], scale, -m * m)) + d.eps);
+        float f[VW];
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          v[u][e] -= mu[u];
-          q[u] = fmaf(v[u][e], v[u][e], q[u]);
-        }
-      }
-      ts.sum(q);
-#pragma unroll
-      for (int u = 0; u < R; ++u) {
-        const float k = 1.0f / sqrtf(not_negative(fmaf(q[u], scale, -by[u] * by[u])) + d.eps);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) v[u][e] = fmaf(v[u][e] * k, a[e], b[e]);
+        for (int e = 0; e < VW; ++e) f[e] = a[e] * k;
+        centre_scale_add(v[u], mu, f, b);
         if constexpr (SILU) activate<T>(v[u]);
         dev::st16_stream(py + (row + u) * pitch, dev::Conv<T>::pack(v[u]));
         if ((threadIdx.x & 31) == lead) {
           const int64_t g = g0 + (row + u) * ts.tokens_a_row * d.G;
-          if (mean_out != nullptr) mean_out[g] = mu[u];
+          if (mean_out != nullptr) mean_out[g] = mu[0];
           if (inv_out != nullptr) inv_out[g] = k;
         }
       }
