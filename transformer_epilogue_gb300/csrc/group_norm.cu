@@ -462,6 +462,7 @@ struct RowStream {
   unsigned char* smem;
   int rows;            // walk rows in a stage
   int row_bytes;       // of this tile
+  int place;           // this thread's in a row (threads beyond the tile read its first fragment)
   int64_t total;       // walk rows of a sample
   int64_t frags, full_rows;
   int rest;
@@ -469,7 +470,7 @@ struct RowStream {
   bool ok = true;
 
   __device__ __forceinline__ RowStream(StageBars* b, unsigned char* m, const GnDims& d, const Tile& t)
-      : bars(b), smem(m), row_bytes(t.frags * 16), ring(kStages) {
+      : bars(b), smem(m), row_bytes(t.frags * 16), place(t.mine ? int(threadIdx.x) * 16 : 0), ring(kStages) {
     rows = kStageBytes / NOPS / row_bytes;  // >= 2: a tile has at most kWalkThreads fragments
     frags = d.frags;
     full_rows = d.full_rows;
@@ -534,7 +535,7 @@ struct RowStream {
         ok = false;
         continue;
       }
-      f(r, smem + ring.st * kStageBytes + threadIdx.x * 16);
+      f(r, smem + ring.st * kStageBytes + place);
       dev::release_stage(&bars->empty[ring.st]);
     }
   }
@@ -547,25 +548,25 @@ struct RowStream {
         raw[u][o] = dev::lds16(src + o * (kStageBytes / NOPS) + (i + u) * row_bytes);
   }
   // f(row, raw) for the walk rows of an item that have a fragment in the thread's
-  // column; raw holds four, two or one rows, so that one row's arithmetic covers
-  // another's latency.
-  template <typename F>
+  // column; raw holds four (or at most MOST), two or one rows, so that one row's
+  // arithmetic covers another's latency.
+  template <int MOST = 4, typename F>
   __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
     stages(range, [&](int r, const unsigned char* src) {
       const int k = min(rows, mine - r);
       int i = 0;
-      for (; i + 3 < k; i += 4) {
-        uint4 raw[4][NOPS];
+      for (; i + MOST <= k; i += MOST) {
+        uint4 raw[MOST][NOPS];
         load(src, i, raw);
         f(r + i, raw);
       }
-      if (i + 1 < k) {
+      if (MOST > 2 && i + 1 < k) {
         uint4 raw[2][NOPS];
         load(src, i, raw);
         f(r + i, raw);
         i += 2;
       }
-      if (i < k) {
+      if (MOST > 1 && i < k) {
         uint4 raw[1][NOPS];
         load(src, i, raw);
         f(r + i, raw);
@@ -905,22 +906,22 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
 
 struct TokenSet {
   int lanes;       // of a group
-  unsigned mask;   // this thread's set of them
-  int64_t tokens_a_row, token0;  // tokens of a walk row, this thread's among them
+  int tokens_a_row, token0;  // tokens of a walk row, this thread's among them
   int group;       // of the token
   __device__ __forceinline__ TokenSet(const GnDims& d, const Tile& t, int vw, int set) : lanes(set) {
-    const int lane = threadIdx.x & 31, frags = d.C / vw;  // of a token
-    mask = set == 32 ? 0xffffffffu : ((1u << set) - 1u) << (lane & ~(set - 1));
-    tokens_a_row = d.p.row_frags / frags;
-    token0 = t.j / frags;
-    group = static_cast<int>(t.j - token0 * frags) / set;
+    const unsigned frags = unsigned(d.C / vw);  // of a token
+    tokens_a_row = static_cast<int>(unsigned(d.p.row_frags) / frags);
+    token0 = static_cast<int>(unsigned(t.j) / frags);
+    group = static_cast<int>(unsigned(t.j) - token0 * frags) / set;
   }
+  // Sums over the set's lanes.  Every lane of the warp takes part (the shuffles
+  // are whole warps': with a set's own mask the warp ran once for each set).
   template <int R>
   __device__ __forceinline__ void sum(float (&x)[R]) const {
     for (int o = lanes >> 1; o > 0; o >>= 1) {
       float y[R];
 #pragma unroll
-      for (int u = 0; u < R; ++u) y[u] = __shfl_xor_sync(mask, x[u], o);
+      for (int u = 0; u < R; ++u) y[u] = __shfl_xor_sync(0xffffffffu, x[u], o);
 #pragma unroll
       for (int u = 0; u < R; ++u) x[u] += y[u];
     }
@@ -947,7 +948,7 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
   }
   const TokenSet ts(d, t, VW, set);
   const float scale = 1.0f / float(d.D);
-  const int lead = (threadIdx.x & 31) & ~(set - 1);
+  const int lane = threadIdx.x & 31, lead = lane & ~(set - 1);
   float a[VW], b[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) a[e] = b[e] = 0.f;
@@ -958,10 +959,13 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
   }
   for (Items it(d, false); it.more(); it.next()) {
     const Range r(p, it.item(), rows.total);
-    const int64_t pitch = p.row_frags * VW;
+    const int64_t pitch = p.row_frags * VW, gpitch = int64_t(ts.tokens_a_row) * d.G;
+    const int mine = rows.mine(r, t);  // lanes without the last row go round with the others
     T* py = y + r.ra * pitch + t.j * VW;
     const int64_t g0 = (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
-    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
+    float* pm = mean_out != nullptr && lane == lead ? mean_out + g0 : nullptr;
+    float* pi = inv_out != nullptr && lane == lead ? inv_out + g0 : nullptr;
+    rows.consume<2>(r, static_cast<int>(r.rb - r.ra), [&](int row, const auto& raw) {
       constexpr int R = sizeof(raw) / sizeof(raw[0]);
       // sums and sums of squares relative to a centre: the median of three of the
       // group's values.  With at most 256 values to a group it is at most 16
@@ -970,8 +974,8 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         dev::Conv<T>::unpack(raw[u][0], v[u]);
-        c[u] = median3(__shfl_sync(ts.mask, v[u][0], lead), __shfl_sync(ts.mask, v[u][VW / 2], lead + set / 2),
-                       __shfl_sync(ts.mask, v[u][VW - 1], lead + set - 1));
+        c[u] = median3(__shfl_sync(0xffffffffu, v[u][0], lead), __shfl_sync(0xffffffffu, v[u][VW / 2], lead + set / 2),
+                       __shfl_sync(0xffffffffu, v[u][VW - 1], lead + set - 1));
       }
 #pragma unroll
       for (int u = 0; u < R; ++u) {
@@ -995,28 +999,31 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
         for (int e = 0; e < VW; ++e) f[e] = a[e] * k;
         centre_scale_add(v[u], mu, f, b);
         if constexpr (SILU) activate<T>(v[u]);
-        dev::st16_stream(py + (row + u) * pitch, dev::Conv<T>::pack(v[u]));
-        if ((threadIdx.x & 31) == lead) {
-          const int64_t g = g0 + (row + u) * ts.tokens_a_row * d.G;
-          if (mean_out != nullptr) mean_out[g] = mu[0];
-          if (inv_out != nullptr) inv_out[g] = k;
+        if (row + u < mine) {
+          dev::st16_stream(py, dev::Conv<T>::pack(v[u]));
+          if (pm != nullptr) *pm = mu[0];
+          if (pi != nullptr) *pi = k;
         }
+        py += pitch;
+        if (pm != nullptr) pm += gpitch;
+        if (pi != nullptr) pi += gpitch;
       }
     });
   }
 }
 
-// Its gradient.  The statistics of a stage's tokens are loaded before the stage
-// before it is used; the parameters' sums run on in registers and leave as row
-// blockIdx / tiles of cpart, 2 x [row][C].
+// Its gradient.  The statistics of an item's tokens are fetched into shared memory
+// first (the plan keeps an item that short): loaded row by row they cost 6 of 30
+// us for bf16 8192 x 2048.  The parameters' sums run on in registers and leave as
+// row blockIdx / tiles of cpart, 2 x [row][C].
 template <typename T, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
                        const float* mean, const float* inv, T* dx, float* cpart, GnDims d, int set) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int kAhead = 4;  // rows of a stage whose statistics are loaded ahead
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) StageBars bars;
+  // after the stages: an item's statistics, in the end the sums by position
   float* s_a = reinterpret_cast<float*>(smem + kStageSmem);
   float* s_b = s_a + kWalkThreads * VW;
   const WalkPlan& p = d.p;
@@ -1042,44 +1049,41 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
   }
   for (Items it(d, false); it.more(); it.next()) {
     const Range r(p, it.item(), rows.total);
-    const int64_t pitch = p.row_frags * VW, gpitch = ts.tokens_a_row * d.G;
-    const int mine = rows.mine(r, t);
+    const int64_t pitch = p.row_frags * VW;
+    const int mine = rows.mine(r, t), all = static_cast<int>(r.rb - r.ra);
     T* po = dx + r.ra * pitch + t.j * VW;
-    const float* pm = mean + (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
-    const float* pi = inv + (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
-    float mu[kAhead], rs[kAhead];
-    auto ahead = [&](int row) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const bool on = u < rows.rows && row + u < mine;
-        mu[u] = on ? pm[(row + u) * gpitch] : 0.f;
-        rs[u] = on ? pi[(row + u) * gpitch] : 0.f;
+    {
+      // groups of the tile in a walk row (they are flat over a row's tokens), and of the tensor in all
+      const int in_row = t.frags / set, count = all * in_row;
+      const int64_t row_groups = int64_t(ts.tokens_a_row) * d.G, total = d.S * d.G;
+      const int64_t g0 = r.ra * row_groups + t.tile * p.tile_frags / set;
+      for (int i = threadIdx.x; i < count; i += consumers) {
+        const int row = static_cast<int>(unsigned(i) / unsigned(in_row));
+        const int64_t g = g0 + row * row_groups + (i - row * in_row);
+        s_a[i] = g < total ? mean[g] : 0.f;
+        s_b[i] = g < total ? inv[g] : 0.f;
       }
-    };
-    ahead(0);
+    }
+    consumer_sync();
+    const int in_row = t.frags / set, own_group = min(int(threadIdx.x) / set, in_row - 1);
     rows.stages(r, [&](int row, const unsigned char* src) {
-      float m[kAhead], k[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        m[u] = mu[u];
-        k[u] = rs[u];
-      }
-      ahead(row + rows.rows);
-      const int n = min(rows.rows, mine - row);
-      auto two = [&](int i, int count, float m0, float m1, float k0, float k1) {
+      const int n = min(rows.rows, all - row);  // lanes without the last row go round too
+      const int own = min(rows.rows, mine - row);
+      auto two = [&](int i) {
         uint4 raw[2][2];
         rows.load(src, i, raw);
-        float h[2][VW], w[2][VW], s[4];
-        const float mm[2] = {m0, m1}, kk[2] = {k0, k1};
+        float h[2][VW], w[2][VW], s[4], kk[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           dev::Conv<T>::unpack(raw[u][0], h[u]);
           dev::Conv<T>::unpack(raw[u][1], w[u]);
-          if (u >= count) {
+          if (i + u >= own) {
 #pragma unroll
             for (int e = 0; e < VW; ++e) h[u][e] = w[u][e] = 0.f;
           }
-          const float one_m[1] = {mm[u]}, one_k[1] = {kk[u]};
+          const int at = min(row + i + u, all - 1) * in_row + own_group;
+          const float one_m[1] = {s_a[at]}, one_k[1] = {s_b[at]};
+          kk[u] = one_k[0];
           centre_scale(h[u], one_m, one_k);
           if constexpr (SILU) {
             float a[VW];
@@ -1104,18 +1108,13 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
           const float p1 = s[2 * u] * scale, p2 = s[2 * u + 1] * scale;
 #pragma unroll
           for (int e = 0; e < VW; ++e) w[u][e] = kk[u] * (fmaf(-p2, h[u][e], w[u][e] - p1));
-          if (u < count) dev::st16_stream(po + (row + i + u) * pitch, dev::Conv<T>::pack(w[u]));
+          if (i + u < own) dev::st16_stream(po + (row + i + u) * pitch, dev::Conv<T>::pack(w[u]));
         }
       };
-      // (a second row beyond the last is read from within the stage, and not used)
-      if (n > 0) two(0, n, m[0], m[1], k[0], k[1]);
-      if (n > 2) two(2, n - 2, m[2], m[3], k[2], k[3]);
-      for (int i = kAhead; i < n; i += 2) {
-        const bool both = i + 1 < n;
-        two(i, n - i, pm[(row + i) * gpitch], both ? pm[(row + i + 1) * gpitch] : 0.f, pi[(row + i) * gpitch],
-            both ? pi[(row + i + 1) * gpitch] : 0.f);
-      }
+      // (a second row beyond the last is read from within the block's memory, and not used)
+      for (int i = 0; i < n; i += 2) two(i);
     });
+    consumer_sync();
   }
   if (cpart == nullptr) return;
   if (t.mine) {
@@ -1660,6 +1659,16 @@ GnDims token_dims(DType t, int64_t N, int64_t C, int64_t G, float eps) {
 }
 int64_t token_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 2); }
 
+// The gradient's items are short enough for their statistics to fit shared memory
+// (a float each for kWalkThreads * vw groups).
+GnDims token_grad_dims(DType t, int64_t N, int64_t C, int64_t G) {
+  GnDims d = token_dims(t, N, C, G, 0.f);
+  const int64_t in_row = d.p.tile_frags / (d.D / vec_width(t));
+  d.p.rows_per_chunk = std::min<int64_t>(d.p.rows_per_chunk, kWalkThreads * vec_width(t) / in_row);
+  d.p.chunks = int((d.p.rows + d.p.rows_per_chunk - 1) / d.p.rows_per_chunk);
+  return d;
+}
+
 // At least this many bytes: below, the direct form's shorter start wins
 // (bf16, C = 4096, us: ).
 constexpr int64_t kTokenStagedBytes = int64_t(8) << 20;
@@ -1683,7 +1692,7 @@ cudaError_t token_fwd_t(const GroupNormArgs& a, cudaStream_t stream, int* launch
 template <typename T>
 cudaError_t token_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
-  GnDims d = token_dims(a.t, a.N, a.C, a.G, 0.f);
+  GnDims d = token_grad_dims(a.t, a.N, a.C, a.G);
   d.pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   const int64_t rows = token_rows(d);
   float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
@@ -1709,7 +1718,7 @@ size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C,
   size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
                          group_norm_grad_fused_bytes(t, N, S, C, G));
   if (token_staged(t, N, S, C, G))
-    most = std::max(most, size_t(token_rows(token_dims(t, N, C, G, 0.f))) * size_t(C) * 8);
+    most = std::max(most, size_t(token_rows(token_grad_dims(t, N, C, G))) * size_t(C) * 8);
   return most;
 }
 
