@@ -151,6 +151,26 @@ struct Range {
   }
 };
 
+// A sample as the staged kernels read it: `nf` fragments from fragment f0 of the
+// tensor on, the first `off` elements of which belong to the sample before.
+// (Off and the ends matter where C % VW != 0: ODD.)
+struct Sample {
+  int off;
+  int64_t f0, nf;
+};
+
+// An item's partial fragments, if this thread has one: the sample's first (before
+// `lo` outside) and last (from `hi` on), by their row in the item.  They are
+// read from global memory, value by value: the tensor's last one is not staged.
+struct Ends {
+  int first = -1, last = -1, lo = 0, hi = 0;
+  int64_t e0 = 0, pitch = 0;  // the thread's first element in the item, from the sample's start
+  __device__ __forceinline__ bool has(int row) const { return row == first || row == last; }
+  __device__ __forceinline__ bool inside(int row, int e) const {
+    return !(row == first && e < lo) && !(row == last && e >= hi);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Block epilogues of the general kernels: a warp to a group, with the walk row's
 // offset and repeats.
@@ -298,6 +318,16 @@ struct Columns {
     g0 = whole ? 0 : first / D;
     in0 = whole ? 0 : first - g0 * D;
     n_groups = whole ? d.G : (in0 + cols + D - 1) / D;
+  }
+  // The position of column i's repeat k (ODD: behind the first `off`, around the walk row's end).
+  template <bool ODD>
+  __device__ __forceinline__ int at(int i, int k, int off) const {
+    int pos = i + k * cols;
+    if constexpr (ODD) {
+      pos += off;
+      if (pos >= reps * cols) pos -= reps * cols;
+    }
+    return pos;
   }
   // Columns [lo, hi) of the tile's group g (from g0).
   __device__ __forceinline__ int lo(int g) const { return max(0, g * D - in0); }
@@ -455,7 +485,7 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   return pol;
 }
 
-template <typename T, int NOPS>
+template <typename T, int NOPS, bool ODD = false>
 struct RowStream {
   static constexpr int VW = dev::Vec16<T>::N;
   StageBars* bars;
@@ -463,8 +493,8 @@ struct RowStream {
   int rows;            // walk rows in a stage
   int row_bytes;       // of this tile
   int place;           // this thread's in a row (threads beyond the tile read its first fragment)
-  int64_t total;       // walk rows of a sample
-  int64_t frags, full_rows;
+  int64_t total;       // walk rows of a sample (ODD: at most)
+  int64_t frags, full_rows, row_frags, L, whole;
   int rest;
   dev::Ring ring;
   bool ok = true;
@@ -475,7 +505,10 @@ struct RowStream {
     frags = d.frags;
     full_rows = d.full_rows;
     rest = d.rest;
-    total = full_rows + (rest > 0 ? 1 : 0);
+    row_frags = d.p.row_frags;
+    L = d.L;
+    whole = d.N * d.L / VW;  // whole fragments of the tensor
+    total = ODD ? d.p.rows : full_rows + (rest > 0 ? 1 : 0);
     if (threadIdx.x == 0) {
       for (int i = 0; i < kStages; ++i) {
         dev::mbar_init(&bars->full[i], 1);
@@ -486,8 +519,40 @@ struct RowStream {
     __syncthreads();
   }
 
+  __device__ __forceinline__ Sample sample(int64_t n) const {
+    if constexpr (!ODD) return Sample{0, n * frags, frags};
+    const int64_t e = n * L;
+    const int off = static_cast<int>(e & (VW - 1));
+    return Sample{off, e / VW, (off + L + VW - 1) / VW};
+  }
+  // An item's rows (ODD: the sample's own count of them).
+  __device__ __forceinline__ Range range(const WalkPlan& p, int64_t item) const {
+    Range r(p, item, total);
+    if constexpr (ODD) r.rb = min(r.rb, quotient(sample(r.n).nf + row_frags - 1, int(row_frags)));
+    return r;
+  }
   // Walk rows of a sample that have a fragment j.
-  __device__ __forceinline__ int64_t of_column(int64_t j) const { return full_rows + (j < rest ? 1 : 0); }
+  __device__ __forceinline__ int64_t of_column(const Sample& s, int64_t j) const {
+    if constexpr (ODD) return quotient(s.nf - j + row_frags - 1, int(row_frags));
+    return full_rows + (j < rest ? 1 : 0);
+  }
+  __device__ __forceinline__ Ends ends(const Range& r, const Tile& t) const {
+    Ends en;
+    if constexpr (ODD) {
+      const Sample s = sample(r.n);
+      en.e0 = (r.ra * row_frags + t.j) * VW - s.off;
+      en.pitch = row_frags * VW;
+      if (t.mine) {
+        if (s.off > 0 && t.j == 0 && r.ra == 0) en.first = 0;
+        const int64_t last_row = quotient(s.nf - 1, int(row_frags));
+        en.lo = s.off;
+        en.hi = static_cast<int>(s.off + L - (s.nf - 1) * VW);
+        if (en.hi < VW && t.j == s.nf - 1 - last_row * row_frags && last_row >= r.ra && last_row < r.rb)
+          en.last = static_cast<int>(last_row - r.ra);
+      }
+    }
+    return en;
+  }
 
   // The producer: the rows of all the CTA's items.
   __device__ __forceinline__ void produce(const T* const (&base)[NOPS], const GnDims& d, const Tile& t, bool reversed,
@@ -495,7 +560,8 @@ struct RowStream {
     const WalkPlan& p = d.p;
     int64_t n_filled = 0;
     for (Items it(d, reversed); it.more(); it.next()) {
-      const Range range(p, it.item(), total);
+      const Range range = this->range(p, it.item());
+      const Sample s = sample(range.n);
       for (int64_t r = range.ra; r < range.rb; r += rows, ring.next(), ++n_filled) {
         if (n_filled >= kStages && !dev::mbar_wait(&bars->empty[ring.st], ring.phase ^ 1u)) {
           // the copies in flight land before the block ends
@@ -503,14 +569,15 @@ struct RowStream {
             dev::mbar_wait(&bars->full[k % kStages], uint32_t((k / kStages) & 1));
           return;
         }
-        const int64_t f0 = range.n * frags + r * p.row_frags + int64_t(t.tile) * p.tile_frags;
+        const int64_t f0 = s.f0 + r * p.row_frags + int64_t(t.tile) * p.tile_frags;
         const int k = static_cast<int>(min(int64_t(rows), range.rb - r));
         unsigned char* dst = smem + ring.st * kStageBytes;
         if (p.tiles == 1) {  // contiguous; the sample's last walk row may be short
-          const uint32_t bytes = uint32_t(min(int64_t(k) * p.row_frags, frags - r * p.row_frags)) * 16u;
+          const int64_t left = ODD ? min(s.nf - r * p.row_frags, whole - f0) : frags - r * p.row_frags;
+          const uint32_t bytes = uint32_t(min(int64_t(k) * p.row_frags, left)) * 16u;
           dev::mbar_arrive_expect_tx(&bars->full[ring.st], NOPS * bytes);
 #pragma unroll
-          for (int o = 0; o < NOPS; ++o)
+          for (int o = 0; o < NOPS && bytes > 0; ++o)
             dev::bulk_g2s(dst + o * (kStageBytes / NOPS), base[o] + f0 * VW, bytes, &bars->full[ring.st], policy);
         } else {
           dev::mbar_arrive_expect_tx(&bars->full[ring.st], uint32_t(NOPS * k * row_bytes));
@@ -580,7 +647,7 @@ struct RowStream {
   }
   // Rows of an item that have a fragment in column j (0 where the thread has none).
   __device__ __forceinline__ int mine(const Range& range, const Tile& t) const {
-    return t.mine ? static_cast<int>(max(int64_t(0), min(range.rb, of_column(t.j)) - range.ra)) : 0;
+    return t.mine ? static_cast<int>(max(int64_t(0), min(range.rb, of_column(sample(range.n), t.j)) - range.ra)) : 0;
   }
 };
 
@@ -598,7 +665,7 @@ __device__ __forceinline__ float median3(float a, float b, float c) {
 // median of three of the group's values in the item's first walk row, which lies
 // among the values unless two of the three are outliers.  Off by k standard
 // deviations it costs the variance k^2 2^-24 of its value.
-template <typename T, bool GROUP>
+template <typename T, bool GROUP, bool ODD>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
   constexpr int VW = dev::Vec16<T>::N;
@@ -611,7 +678,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
   float* centre = s_b + kWalkThreads * EV;
   const WalkPlan& p = d.p;
   const Tile t(p);
-  RowStream<T, 1> rows(&bars, smem, d, t);
+  RowStream<T, 1, ODD> rows(&bars, smem, d, t);
   dev::pdl_wait();
   dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
@@ -636,7 +703,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
     }
   }
   for (Items it(d, false); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
     float4* out = partial + (it.item() * p.tiles + t.tile) * d.G;
     if (r.ra >= r.rb) {  // the plan's rows may be one more than there are
       for (int g = threadIdx.x; g < d.G; g += consumers) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -645,8 +712,25 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
     float c[EV], s[VW], q[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
+    const int off = ODD ? rows.sample(r.n).off : 0;
+    const Ends ends = rows.ends(r, t);
+    const T* xs = x + r.n * d.L;
+    int64_t e_a = 0, e_b = 0;  // ODD: the item's elements of the sample
+    if constexpr (ODD) {
+      e_a = max(int64_t(0), r.ra * p.row_frags * VW - off);
+      e_b = min(d.L, r.rb * p.row_frags * VW - off);
+      // positions of the sample that begin in the item (or its last)
+      const int64_t s0 = min(quotient(e_a + d.C - 1, d.C), d.S - 1), s1 = max(s0, quotient(e_b, d.C) - 1);
+      for (int g = threadIdx.x; g < d.G; g += consumers) {
+        const int c = g * d.D;
+        centre[g] = median3(dev::to_float(xs[s0 * d.C + c]), dev::to_float(xs[(s0 + s1) / 2 * d.C + c + d.D / 2]),
+                            dev::to_float(xs[s1 * d.C + c + d.D - 1]));
+      }
+      if (t.mine) for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int, int g) { if (e < EV) grp[e] = g; });
+    }
     // positions of the sample (repeats of the channels) in the item, and in its first walk row
     const int64_t pos0 = r.ra * p.reps, pos1 = min(r.rb * p.reps, d.S);
+    if constexpr (!ODD) {
     const T* row0 = reinterpret_cast<const T*>(rows.peek());
     const int n_rep = static_cast<int>(min(int64_t(cols.reps), pos1 - pos0));
     for (int g = threadIdx.x; g < cols.n_groups; g += consumers) {
@@ -654,14 +738,22 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
       centre[g] = median3(dev::to_float(row0[lo]), dev::to_float(row0[lo + n / 2 + n_rep / 2 * step]),
                           dev::to_float(row0[lo + n - 1 + (n_rep - 1) * step]));
     }
+    }
     consumer_sync();
 #pragma unroll
     for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
-    rows.consume(r, rows.mine(r, t), [&](int, const auto& raw) {
+    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
 #pragma unroll
       for (const auto& one : raw) {
         float v[VW];
         dev::Conv<T>::unpack(one[0], v);
+        if (ODD && ends.has(row)) {  // what is outside counts as the centre
+          dev::load_frag<T, false>(xs, ends.e0 + row * ends.pitch, d.L, v);
+#pragma unroll
+          for (int e = 0; e < VW; ++e)
+            if (!ends.inside(row, e)) v[e] = c[EV == 1 ? 0 : e];
+        }
+        ++row;
 #pragma unroll
         for (int e = 0; e < VW; e += 2) {
           const float2 m = pair_of<VW>(c, e);
@@ -688,15 +780,23 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
       }
     }
     consumer_sync();
-    if (cols.reps > 1) {  // to the first repeat's place
+    // to the first repeat's place (ODD: to the centre's other side, after all places have been read)
+    float* t_a = s_a;
+    float* t_b = s_b;
+    if (ODD) {
+      t_a = centre + kWalkThreads * EV;
+      t_b = t_a + kWalkThreads * EV;
+    }
+    if (ODD || cols.reps > 1) {
       sum_sets(consumers, cols.cols, cols.reps,
                [&](int i, int k, float& a, float& b) {
-                 a += s_a[i + k * cols.cols];
-                 b += s_b[i + k * cols.cols];
+                 const int pos = cols.at<ODD>(i, k, off);
+                 a += s_a[pos];
+                 b += s_b[pos];
                },
                [&](int i, float a, float b) {
-                 s_a[i] = a;
-                 s_b[i] = b;
+                 t_a[i] = a;
+                 t_b[i] = b;
                });
       consumer_sync();
     }
@@ -708,13 +808,20 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
              [&](int g, int k, float& a, float& b) {
                const int i = cols.lo(g) + k;
                if (i < cols.hi(g)) {
-                 a += s_a[i];
-                 b += s_b[i];
+                 a += t_a[i];
+                 b += t_b[i];
                }
              },
              [&](int g, float a, float b) {
-               const float n = positions * float((cols.hi(g) - cols.lo(g)) * per), m = a / n;
-               const float first = dev::ld1_keep(x + r.n * d.L + int64_t(cols.g0 + g) * d.D);
+               float n = positions * float((cols.hi(g) - cols.lo(g)) * per);
+               if constexpr (ODD) {  // the group's values among the sample's first e_a, first e_b
+                 const int64_t qa = quotient(e_a, d.C), qb = quotient(e_b, d.C);
+                 const int ia = min(max(int(e_a - qa * d.C) - g * d.D, 0), d.D);
+                 const int ib = min(max(int(e_b - qb * d.C) - g * d.D, 0), d.D);
+                 n = float((qb - qa) * d.D + (ib - ia));
+               }
+               const float m = n > 0.f ? a / n : 0.f;
+               const float first = dev::ld1_keep(xs + int64_t(cols.g0 + g) * d.D);
                out[cols.g0 + g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), 0.f);
              });
     consumer_sync();
@@ -723,7 +830,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
 
 // Pass 2: y from x and the statistics, over the items in reverse: what pass 1
 // read last is in L2.
-template <typename T, bool GROUP, bool SILU>
+template <typename T, bool GROUP, bool ODD, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                   const float* inv, T* y, GnDims d) {
@@ -732,7 +839,7 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
   __shared__ __align__(8) StageBars bars;
   const WalkPlan& p = d.p;
   const Tile t(p);
-  RowStream<T, 1> rows(&bars, smem, d, t);
+  RowStream<T, 1, ODD> rows(&bars, smem, d, t);
   dev::pdl_wait();
   dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
@@ -741,20 +848,31 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
-  const int c0 = first_channel(t.j, VW, 0, d.C);
+  int c0 = first_channel(t.j, VW, 0, d.C);
   for (Items it(d, true); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
+    const int off = ODD ? rows.sample(r.n).off : 0;
+    const Ends ends = rows.ends(r, t);
+    if constexpr (ODD) c0 = first_channel(t.j, VW, off, d.C);
     ApplyValues<T, GROUP ? 1 : VW, SILU> val;
     if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
     const int64_t pitch = p.row_frags * VW;
-    T* py = y + r.n * d.L + r.ra * pitch + t.j * VW;
+    T* py = y + r.n * d.L - off + r.ra * pitch + t.j * VW;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
 #pragma unroll
       for (const auto& one : raw) {
         float v[VW];
         dev::Conv<T>::unpack(one[0], v);
-        val(v);
-        dev::st16_stream(py + row++ * pitch, dev::Conv<T>::pack(v));
+        if (ODD && ends.has(row)) {
+          const int64_t e0 = ends.e0 + row * ends.pitch;
+          dev::load_frag<T, false>(x + r.n * d.L, e0, d.L, v);
+          val(v);
+          dev::store_frag<T, false>(y + r.n * d.L, e0, d.L, v);
+        } else {
+          val(v);
+          dev::st16_stream(py + row * pitch, dev::Conv<T>::pack(v));
+        }
+        ++row;
       }
     });
   }
@@ -763,7 +881,7 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
 // Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
 // groups' sums of each item.
 //   gpart: [item][tile][G] x (sum du gamma, sum du gamma h); cpart: leave_channel_sums
-template <typename T, bool GROUP, bool SILU>
+template <typename T, bool GROUP, bool ODD, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
                       const float* mean, const float* inv, GnDims d, float* gpart, float* cpart) {
@@ -776,9 +894,11 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
   float* s_b = s_a + kWalkThreads * VW;
   float* tot_a = s_b + kWalkThreads * VW;
   float* tot_b = tot_a + kWalkThreads * VW;
+  float* t_a = ODD ? tot_b + kWalkThreads * VW : s_a;
+  float* t_b = ODD ? t_a + kWalkThreads * VW : s_b;
   const WalkPlan& p = d.p;
   const Tile t(p);
-  RowStream<T, 2> rows(&bars, smem, d, t);
+  RowStream<T, 2, ODD> rows(&bars, smem, d, t);
   dev::pdl_wait();
   dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
@@ -787,22 +907,31 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, false, policy_evict_normal());
     return;
   }
-  const int c0 = first_channel(t.j, VW, 0, d.C);
+  int c0 = first_channel(t.j, VW, 0, d.C);
   const Columns cols(d, t, VW, 1);
   bool once = true;
   for (Items it(d, false); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
+    const int off = ODD ? rows.sample(r.n).off : 0;
+    const Ends ends = rows.ends(r, t);
+    if constexpr (ODD) c0 = first_channel(t.j, VW, off, d.C);
     GradValues<T, EV, SILU> val;
     if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
     float sa[VW], sb[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) sa[e] = sb[e] = 0.f;
-    rows.consume(r, rows.mine(r, t), [&](int, const auto& raw) {
+    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
 #pragma unroll
       for (const auto& one : raw) {
         float v[VW], w[VW];
         dev::Conv<T>::unpack(one[0], v);
         dev::Conv<T>::unpack(one[1], w);
+        if (ODD && ends.has(row)) {  // 0 outside the sample: adds nothing
+          const int64_t e0 = ends.e0 + row * ends.pitch;
+          dev::load_frag<T, false>(x + r.n * d.L, e0, d.L, v);
+          dev::load_frag<T, false>(dy + r.n * d.L, e0, d.L, w);
+        }
+        ++row;
         val(v, w);
         dev::add_pairs(sa, w);
         fma_pairs(w, v, sb);
@@ -814,18 +943,20 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
       put(s_b, sb);
     }
     consumer_sync();
-    // by channel: to the totals, and times gamma back to place (a repeat's is free) for the groups
+    // by channel: to the totals, and times gamma to the first repeat's place, which only the
+    // threads of that channel read (ODD: to memory of its own)
     sum_sets(consumers, cols.cols, cols.reps,
              [&](int i, int k, float& a, float& b) {
-               a += s_a[i + k * cols.cols];
-               b += s_b[i + k * cols.cols];
+               const int pos = cols.at<ODD>(i, k, off);
+               a += s_a[pos];
+               b += s_b[pos];
              },
              [&](int i, float a, float b) {
                tot_a[i] = once ? a : tot_a[i] + a;
                tot_b[i] = once ? b : tot_b[i] + b;
                const float ga = dev::ld1_keep(gamma + cols.g0 * d.D + cols.in0 + i);
-               s_a[i] = a * ga;  // read by this thread's set alone
-               s_b[i] = b * ga;
+               t_a[i] = a * ga;
+               t_b[i] = b * ga;
              });
     once = false;
     consumer_sync();
@@ -835,8 +966,8 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
              [&](int g, int k, float& a, float& b) {
                const int i = cols.lo(g) + k;
                if (i < cols.hi(g)) {
-                 a += s_a[i];
-                 b += s_b[i];
+                 a += t_a[i];
+                 b += t_b[i];
                }
              },
              [&](int g, float a, float b) {
@@ -855,7 +986,7 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
 }
 
 // Gradient, pass 2: dx, over the items in reverse.
-template <typename T, bool GROUP, bool SILU>
+template <typename T, bool GROUP, bool ODD, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
                        const float* mean, const float* inv, const float* m1, const float* m2, T* dx, GnDims d) {
@@ -864,7 +995,7 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
   __shared__ __align__(8) StageBars bars;
   const WalkPlan& p = d.p;
   const Tile t(p);
-  RowStream<T, 2> rows(&bars, smem, d, t);
+  RowStream<T, 2, ODD> rows(&bars, smem, d, t);
   dev::pdl_wait();
   dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
@@ -873,24 +1004,36 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
-  const int c0 = first_channel(t.j, VW, 0, d.C);
+  int c0 = first_channel(t.j, VW, 0, d.C);
   for (Items it(d, true); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
+    const int off = ODD ? rows.sample(r.n).off : 0;
+    const Ends ends = rows.ends(r, t);
+    if constexpr (ODD) c0 = first_channel(t.j, VW, off, d.C);
     GradApplyValues<T, GROUP ? 1 : VW, SILU> val;
     if (t.mine) {
       val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
       val.load_means(c0, r.n * d.G, d, inv, m1, m2);
     }
     const int64_t pitch = p.row_frags * VW;
-    T* po = dx + r.n * d.L + r.ra * pitch + t.j * VW;
+    T* po = dx + r.n * d.L - off + r.ra * pitch + t.j * VW;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
 #pragma unroll
       for (const auto& one : raw) {
         float v[VW], w[VW];
         dev::Conv<T>::unpack(one[0], v);
         dev::Conv<T>::unpack(one[1], w);
-        val.dx(v, w);
-        dev::st16_stream(po + row++ * pitch, dev::Conv<T>::pack(v));
+        if (ODD && ends.has(row)) {
+          const int64_t e0 = ends.e0 + row * ends.pitch;
+          dev::load_frag<T, false>(x + r.n * d.L, e0, d.L, v);
+          dev::load_frag<T, false>(dy + r.n * d.L, e0, d.L, w);
+          val.dx(v, w);
+          dev::store_frag<T, false>(dx + r.n * d.L, e0, d.L, v);
+        } else {
+          val.dx(v, w);
+          dev::st16_stream(po + row * pitch, dev::Conv<T>::pack(v));
+        }
+        ++row;
       }
     });
   }
@@ -958,7 +1101,7 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     if (beta != nullptr) load_param(beta, c0, d.C, d.pvec, b);
   }
   for (Items it(d, false); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
     const int64_t pitch = p.row_frags * VW, gpitch = int64_t(ts.tokens_a_row) * d.G;
     const int mine = rows.mine(r, t);  // lanes without the last row go round with the others
     T* py = y + r.ra * pitch + t.j * VW;
@@ -1048,7 +1191,7 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     if (SILU && beta != nullptr) load_param(beta, c0, d.C, d.pvec, be);
   }
   for (Items it(d, false); it.more(); it.next()) {
-    const Range r(p, it.item(), rows.total);
+    const Range r = rows.range(p, it.item());
     const int64_t pitch = p.row_frags * VW;
     const int mine = rows.mine(r, t), all = static_cast<int>(r.rb - r.ra);
     T* po = dx + r.ra * pitch + t.j * VW;
@@ -1556,7 +1699,8 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   float* mean = a.mean != nullptr ? a.mean : reinterpret_cast<float*>(ws + w.mean);
   float* inv = a.inv != nullptr ? a.inv : reinterpret_cast<float*>(ws + w.inv);
   // (the general statistics of a single part are final at once)
-  const bool staged = a.C % VW == 0 && misalign16(a.x) == 0, group = d.D % VW == 0;
+  const bool odd = a.C % VW != 0, group = !odd && d.D % VW == 0;
+  const bool staged = misalign16(a.x) == 0 && (!odd || d.p.tiles == 1);
   float4* partial = staged || split_parts(d) ? reinterpret_cast<float4*>(ws + w.partial) : nullptr;
   const T* x = static_cast<const T*>(a.x);
   const T* gamma = static_cast<const T*>(a.gamma);
@@ -1567,9 +1711,11 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   const bool vec = misalign16(x) == misalign16(y);
   cudaError_t e;
   if (staged) {
-    auto f = group ? k_gn_stats_staged<T, true> : k_gn_stats_staged<T, false>;
-    // two sums by position and the groups' centres
-    const size_t extra = sizeof(float) * kWalkThreads * 3 * (group ? 1 : VW);
+    auto f = group ? k_gn_stats_staged<T, true, false>
+             : odd ? k_gn_stats_staged<T, false, true>
+                   : k_gn_stats_staged<T, false, false>;
+    // two sums by position and the groups' centres (and two sums by column)
+    const size_t extra = sizeof(float) * kWalkThreads * (odd ? 5 : 3) * (group ? 1 : VW);
     e = launch_staged(f, rows, d, stream, launches, extra, x, d, partial);
   } else {
     e = launch_plain(k_gn_stats<T>, rows, d, stream, launches, 0, x, d, partial, mean, inv);
@@ -1582,8 +1728,13 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
     *launches += 1;
   }
   if (staged && vec) {
-    auto f = group ? (a.silu ? k_gn_apply_staged<T, true, true> : k_gn_apply_staged<T, true, false>)
-                   : (a.silu ? k_gn_apply_staged<T, false, true> : k_gn_apply_staged<T, false, false>);
+    auto pick = [&](auto silu) {
+      constexpr bool kSilu = decltype(silu)::value;
+      return group ? k_gn_apply_staged<T, true, false, kSilu>
+             : odd ? k_gn_apply_staged<T, false, true, kSilu>
+                   : k_gn_apply_staged<T, false, false, kSilu>;
+    };
+    auto f = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
     return launch_staged(f, rows, d, stream, launches, 0, x, gamma, beta, mean, inv, y, d);
   }
   auto f = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
@@ -1613,14 +1764,20 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   // whole fragments need x and dy (and dx) at one offset within 16 bytes, and
   // one walk offset for all the samples that a CTA takes
   const bool same = misalign16(x) == misalign16(dy);
-  const bool staged = a.C % VW == 0 && misalign16(x) == 0 && same, group = d.D % VW == 0;
+  const bool odd = a.C % VW != 0, group = !odd && d.D % VW == 0;
+  const bool staged = misalign16(x) == 0 && same && (!odd || d.p.tiles == 1);
   const bool vec1 = same && (d.L % VW == 0 || rows >= d.N * d.p.chunks);
   const bool vec2 = same && misalign16(x) == misalign16(dx);
   cudaError_t e;
   if (staged) {
-    auto f = group ? (a.silu ? k_gn_grad_sums_staged<T, true, true> : k_gn_grad_sums_staged<T, true, false>)
-                   : (a.silu ? k_gn_grad_sums_staged<T, false, true> : k_gn_grad_sums_staged<T, false, false>);
-    e = launch_staged(f, rows, d, stream, launches, kStagedSums, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
+    auto pick = [&](auto silu) {
+      constexpr bool kSilu = decltype(silu)::value;
+      return group ? k_gn_grad_sums_staged<T, true, false, kSilu>
+             : odd ? k_gn_grad_sums_staged<T, false, true, kSilu>
+                   : k_gn_grad_sums_staged<T, false, false, kSilu>;
+    };
+    auto f = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
+    e = launch_staged(f, rows, d, stream, launches, odd ? kStagedSums / 2 * 3 : kStagedSums, dy, x, gamma, beta, a.mean, a.inv, d, gpart, cpart);
   } else {
     auto f = vec1 ? (a.silu ? k_gn_grad_sums<T, true, true> : k_gn_grad_sums<T, true, false>)
                   : (a.silu ? k_gn_grad_sums<T, false, true> : k_gn_grad_sums<T, false, false>);
@@ -1639,8 +1796,13 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (staged && vec2) {
-    auto f = group ? (a.silu ? k_gn_grad_apply_staged<T, true, true> : k_gn_grad_apply_staged<T, true, false>)
-                   : (a.silu ? k_gn_grad_apply_staged<T, false, true> : k_gn_grad_apply_staged<T, false, false>);
+    auto pick = [&](auto silu) {
+      constexpr bool kSilu = decltype(silu)::value;
+      return group ? k_gn_grad_apply_staged<T, true, false, kSilu>
+             : odd ? k_gn_grad_apply_staged<T, false, true, kSilu>
+                   : k_gn_grad_apply_staged<T, false, false, kSilu>;
+    };
+    auto f = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
     return launch_staged(f, rows, d, stream, launches, 0, dy, x, gamma, beta, a.mean, a.inv, m1, m2, dx, d);
   }
   auto f = vec2 ? (a.silu ? k_gn_grad_apply<T, true, true> : k_gn_grad_apply<T, true, false>)
