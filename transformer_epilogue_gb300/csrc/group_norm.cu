@@ -840,14 +840,14 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
   const WalkPlan& p = d.p;
   const Tile t(p);
   RowStream<T, 1, ODD> rows(&bars, smem, d, t);
-  dev::pdl_wait();
-  dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
-  if (int(threadIdx.x) >= consumers) {
+  if (int(threadIdx.x) >= consumers) {  // (the inputs: before the join's end)
     const T* const base[1] = {x};
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
+  dev::pdl_wait();
+  dev::pdl_trigger();
   int c0 = first_channel(t.j, VW, 0, d.C);
   for (Items it(d, true); it.more(); it.next()) {
     const Range r = rows.range(p, it.item());
@@ -996,14 +996,14 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
   const WalkPlan& p = d.p;
   const Tile t(p);
   RowStream<T, 2, ODD> rows(&bars, smem, d, t);
-  dev::pdl_wait();
-  dev::pdl_trigger();
   const int consumers = blockDim.x - 32;
-  if (int(threadIdx.x) >= consumers) {
+  if (int(threadIdx.x) >= consumers) {  // (the inputs: before the join's end)
     const T* const base[2] = {x, dy};
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
+  dev::pdl_wait();
+  dev::pdl_trigger();
   int c0 = first_channel(t.j, VW, 0, d.C);
   for (Items it(d, true); it.more(); it.next()) {
     const Range r = rows.range(p, it.item());
@@ -1512,6 +1512,11 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 // ---------------------------------------------------------------------------
 // Joining a group's chunks and tiles.  THREADS (a warp, or a block where there
 // are many parts) take one (n, g); bound by the latency of a few reads.
+//
+// The joins let pass 2 launch before they wait for pass 1: pass 1 has seen the
+// call's predecessors end before a join starts, so the inputs are there for pass
+// 2's producers, which fill their stages while pass 1 runs out.  Its consumers
+// wait for the join's results (and through them for pass 1).
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 64;
@@ -1538,8 +1543,8 @@ constexpr int kJoinKept = 10;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
 k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* inv_out) {
-  dev::pdl_wait();
   dev::pdl_trigger();
+  dev::pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
   for (int64_t i = int64_t(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < d.N * d.G;
@@ -1589,8 +1594,8 @@ __global__ void __launch_bounds__(kSumsThreads)
 k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
                int64_t reps, T* dbeta, T* dgamma) {
   __shared__ float red[kSumsThreads / 32];
-  dev::pdl_wait();
   dev::pdl_trigger();
+  dev::pdl_wait();
   if (int(blockIdx.x) >= join_blocks) {
     channel_sums<T>(cpart, rows, reps, d.C, 2, dbeta, dgamma, blockIdx.x - join_blocks, gridDim.x - join_blocks);
     return;
@@ -1831,14 +1836,17 @@ GnDims token_grad_dims(DType t, int64_t N, int64_t C, int64_t G) {
   return d;
 }
 
-// At least this many bytes: below, the direct form's shorter start wins
-// (bf16, C = 4096, us: ).
-constexpr int64_t kTokenStagedBytes = int64_t(8) << 20;
+// The staged token form from this many bytes of x on; below, the direct form's
+// shorter start wins.  bf16, C = 4096, staged and direct, us: 64 tokens (0.5 MB)
+// 3.75 and 3.30, 128 3.77 and 3.85, 256 3.84 and 5.97, 512 4.9 and 6.4; the
+// gradient 128 11.1 and 8.6, 256 11.5 and 14.0, 512 12.1 and 15.7.
+constexpr int64_t kTokenStagedBytes = int64_t(1) << 20;
+constexpr int64_t kTokenGradStagedBytes = int64_t(2) << 20;
 
-bool token_staged(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+bool token_staged(DType t, int64_t N, int64_t S, int64_t C, int64_t G, int64_t from) {
   const int64_t vw = vec_width(t), D = C / G;
   return S == 1 && D % vw == 0 && D / vw <= 32 && (D / vw & (D / vw - 1)) == 0 &&
-         N * C * (t == DType::F32 ? 4 : 2) >= kTokenStagedBytes;
+         N * C * (t == DType::F32 ? 4 : 2) >= from;
 }
 
 template <typename T>
@@ -1879,13 +1887,13 @@ size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int6
 size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
   size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
                          group_norm_grad_fused_bytes(t, N, S, C, G));
-  if (token_staged(t, N, S, C, G))
+  if (token_staged(t, N, S, C, G, kTokenGradStagedBytes))
     most = std::max(most, size_t(token_rows(token_grad_dims(t, N, C, G))) * size_t(C) * 8);
   return most;
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
-  if (token_staged(a.t, a.N, a.S, a.C, a.G) && misalign16(a.x) == 0 && misalign16(a.y) == 0) {
+  if (token_staged(a.t, a.N, a.S, a.C, a.G, kTokenStagedBytes) && misalign16(a.x) == 0 && misalign16(a.y) == 0) {
     switch (a.t) {
       case DType::F32: return token_fwd_t<float>(a, stream, launches);
       case DType::F16: return token_fwd_t<__half>(a, stream, launches);
@@ -1903,7 +1911,8 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
 }
 
 cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
-  if (token_staged(a.t, a.N, a.S, a.C, a.G) && misalign16(a.x) == 0 && misalign16(a.dy) == 0 && misalign16(a.dx) == 0) {
+  if (token_staged(a.t, a.N, a.S, a.C, a.G, kTokenGradStagedBytes) && misalign16(a.x) == 0 &&
+      misalign16(a.dy) == 0 && misalign16(a.dx) == 0) {
     switch (a.t) {
       case DType::F32: return token_grad_t<float>(a, stream, launches);
       case DType::F16: return token_grad_t<__half>(a, stream, launches);

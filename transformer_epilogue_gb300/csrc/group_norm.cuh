@@ -170,9 +170,9 @@ __device__ __forceinline__ void sum_sets(int threads, int n, int terms, VAL val,
 // A sum of squares that rounding took below zero is 0 (and NaN stays NaN).
 __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : q; }
 
-// The fused form (group_norm_fused.cu): a sample's slab of channels stays on
-// chip between the statistics and the result.  *done says whether the shape and
-// the alignment allow it; if not, nothing has been launched.
+// The fused form (group_norm_fused.cu): small samples, and few tokens, in one
+// launch.  *done says whether the shape and the alignment allow it; if not,
+// nothing has been launched.
 cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches,
                                     bool* done);
 cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream,

@@ -1,28 +1,29 @@
-// GroupNorm and its gradient with the sample on chip: x (and dy) are read once,
-// into registers, and the result is written from there.  One launch for the
-// forward pass, no scratch.  The definitions stand in group_norm.cu.
+// GroupNorm and its gradient for small samples: a sample is held by one block,
+// in registers, x (and dy) are read once and the result is written from there.  One
+// launch for the forward pass, no scratch.  The definitions stand in group_norm.cu.
 //
 // A block holds walk rows of `cf` fragments, one thread to a fragment column, so
 // a thread's channels stay the same:
-//   MODE 0  C % VW == 0 and D % VW == 0: a walk row is a row of a slab of W
-//           channels (whole groups), and a fragment lies in one group;
-//   MODE 1  C % VW == 0, any D: the same slabs, sums for each channel;
+//   MODE 0  C % VW == 0 and D % VW == 0: a walk row is a position's C channels, and
+//           a fragment lies in one group;
+//   MODE 1  C % VW == 0, any D: the same rows, sums for each channel;
 //   MODE 2  any C and alignment: a walk row is the C / gcd(C, VW) fragments after
-//           which channels repeat (column_walk.cuh), over the whole sample; the
-//           first and the last fragment of a sample may be partial.
+//           which channels repeat (column_walk.cuh); the first and the last
+//           fragment of a sample may be partial.
 // `phases` walk rows lie side by side in a block, `per_sample` of them in one
-// sample; each thread has up to NV rows.  Small samples share a block; a large
-// one is spread over the CTAs of a cluster, each with its range of rows, whose
-// group sums meet in distributed shared memory.
+// sample; each thread has up to NV rows.  Several samples share a block where
+// there are many.
 //
 // Statistics: values are taken relative to their group's first value, summed,
-// and the squares of their distances from the block's mean of the group summed
-// in a second pass over the registers; a cluster's blocks are joined with Chan's
-// formula.  All in float32, in an order that does not depend on timing.
+// and the squares of their distances from the group's mean summed in a second
+// pass over the registers.  All in float32, in an order that does not depend on
+// timing.
 //
-// What bounds it: small samples, the latency of load, two block reductions and
-// store; large batches, DRAM.
-#include <cstdlib>
+// What bounds it: the latency of load, two block reductions and store.  (Spreading
+// a larger sample over a cluster of up to 16 blocks, with the groups' sums in
+// distributed shared memory, was built and measured: 7.0 us against the split
+// form's 8.6 for f16 2x256x1280, but 20.7 against 11.0 for 2x4096x320 and 156
+// against 66 for bf16 8x16384x512, so larger samples take the split form.)
 #include <algorithm>
 #include <climits>
 #include <numeric>
@@ -38,17 +39,14 @@ namespace ep {
 namespace {
 
 constexpr int kMaxThreads = 512;
-constexpr int kMaxCluster = 16;
 
 struct FusedPlan {
-  int W;              // channels after which a walk row repeats: a slab's, or C
+  int W;              // channels: C
   int cf;             // fragments of a walk row
-  int slabs;          // C / W
-  int q;              // groups in a slab
   int phases, per_sample, samples;  // walk rows side by side, of one sample, samples in a block
-  int threads, nv, cluster;
-  int rows, rows_per_cta;           // walk rows of a sample; of one CTA
-  int64_t items;      // blocks of samples x slabs, each `cluster` CTAs
+  int threads, nv;
+  int rows;           // walk rows of a sample
+  int64_t items;      // blocks of samples
   int64_t grid_items; // items running at a time (the gradient; forward: all)
 };
 
@@ -66,26 +64,21 @@ template <typename T, int MODE>
 struct Place {
   static constexpr int VW = dev::Vec16<T>::N;
   int64_t n;       // its sample
-  int64_t e0;      // its first fragment's first element, from the sample's (slab's) start
+  int64_t e0;      // its first fragment's first element, from the sample's start
   int64_t stride;  // elements from one of its fragments to the next
   int64_t lim;     // MODE 2: elements of the sample
   int off;
   int kn;          // its fragments
-  int slab;
 
-  __device__ __forceinline__ Place(const FusedDims& d, const T* x, unsigned item, int rank, int trow, int tcol,
-                                   int ns) {
+  __device__ __forceinline__ Place(const FusedDims& d, const T* x, unsigned item, int trow, int tcol, int ns) {
     const FusedPlan& p = d.p;
-    const unsigned block = p.slabs == 1 ? item : item / unsigned(p.slabs);
-    slab = static_cast<int>(item - block * unsigned(p.slabs));
     const int ph = trow - ns * p.per_sample;
-    n = int64_t(block) * p.samples + ns;
+    n = int64_t(item) * p.samples + ns;
     const bool live = trow < p.phases && n < d.N;
     off = MODE == 2 && live ? dev::misalignment(x + n * d.L) : 0;
-    const int64_t row = MODE == 2 ? int64_t(p.cf) * VW : d.C;
-    const int r0 = rank * p.rows_per_cta + ph, r1 = min(p.rows, (rank + 1) * p.rows_per_cta);
-    kn = live && r0 < r1 ? (r1 - r0 + p.per_sample - 1) / p.per_sample : 0;
-    e0 = r0 * row + tcol * VW - off;
+    const int64_t row = int64_t(p.cf) * VW;  // (C where C % VW == 0)
+    kn = live && ph < p.rows ? (p.rows - ph + p.per_sample - 1) / p.per_sample : 0;
+    e0 = ph * row + tcol * VW - off;
     stride = p.per_sample * row;
     lim = d.L;
   }
@@ -109,20 +102,6 @@ struct Place {
   }
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// 16 bytes at this shared-memory address in the cluster's block `rank`.
-__device__ __forceinline__ float4 ld_rank(const float4* p, int rank) {
-  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
-
 // Sums over the entries of each (sample, group) of a block, in two steps: over
 // the repeats of each column (fragments in MODE 0, else channels), then over a
 // group's columns.  Entries are floats by position; column c of sample ns is at
@@ -135,8 +114,8 @@ struct Entries {
     Cw = frags ? p.cf : p.W;
     np = p.per_sample * p.cf * (frags ? 1 : VW);
     reps = static_cast<int>(unsigned(np) / unsigned(Cw));
-    q = p.q;
-    slots = p.samples * p.q;
+    q = p.W / D;
+    slots = p.samples * q;
     cols = p.samples * Cw;
   }
   __device__ __forceinline__ int sample_of(int slot) const {
@@ -175,33 +154,28 @@ struct Entries {
   }
 };
 
-// gamma and beta of VW channels from c on (modulo W), which start at `from`.
+// gamma and beta of VW channels from c on (modulo W).
 template <typename T, bool WRAP>
-__device__ __forceinline__ void load_params(const T* __restrict__ gamma, const T* __restrict__ beta, int from, int c,
-                                            int W, bool vec, float (&a)[dev::Vec16<T>::N],
+__device__ __forceinline__ void load_params(const T* __restrict__ gamma, const T* __restrict__ beta, int c, int W,
+                                            bool vec, float (&a)[dev::Vec16<T>::N],
                                             float (&b)[dev::Vec16<T>::N]) {
   constexpr int VW = dev::Vec16<T>::N;
 #pragma unroll
   for (int e = 0; e < VW; ++e) b[e] = 0.f;
   if (!WRAP && vec) {
-    dev::Conv<T>::unpack(dev::ld16_keep(gamma + from + c), a);
-    if (beta != nullptr) dev::Conv<T>::unpack(dev::ld16_keep(beta + from + c), b);
+    dev::Conv<T>::unpack(dev::ld16_keep(gamma + c), a);
+    if (beta != nullptr) dev::Conv<T>::unpack(dev::ld16_keep(beta + c), b);
   } else {
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      a[e] = dev::ld1_keep(gamma + from + c);
-      if (beta != nullptr) b[e] = dev::ld1_keep(beta + from + c);
+      a[e] = dev::ld1_keep(gamma + c);
+      if (beta != nullptr) b[e] = dev::ld1_keep(beta + c);
       if (++c == W) c = 0;
     }
   }
 }
 
-// Joins the cluster's values of each slot: f(slot, lane's rank value or 0).
-template <typename F>
-__device__ __forceinline__ void for_slots_by_rank(int slots, int cluster, F f) {
-  const int sets = blockDim.x / cluster;  // the cluster size is a power of two up to 16
-  for (int s0 = 0; s0 < slots; s0 += sets) f(s0 + int(threadIdx.x) / cluster, int(threadIdx.x) & (cluster - 1));
-}
+// Sums over `set` neighbouring lanes (a power of two).
 __device__ __forceinline__ float set_sum(float x, int set) {
   for (int o = set >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -259,37 +233,34 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   constexpr int EV = MODE == 0 ? 1 : VW;  // entries of a thread
   extern __shared__ __align__(16) float smem[];
   const FusedPlan& p = d.p;
-  const int slots = p.samples * p.q, ents = p.phases * p.cf * EV;
-  float4* xch = reinterpret_cast<float4*>(smem);                 // (count, mean, M2) for the cluster
-  float* ent = smem + (p.cluster > 1 ? 4 * slots : 0);
+  const int slots = p.samples * d.G, ents = p.phases * p.cf * EV;
+  float* ent = smem;
   float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
   float* col = cnt + (MODE == 2 ? ents : 0);                     // sums by column, and their counts
   const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_n = col + cols;
-  float* gk = col_n + (MODE == 2 ? cols : 0);                    // the group's first value
-  float* gm = gk + slots;
+  float* gm = col_n + (MODE == 2 ? cols : 0);
   float* gr = gm + slots;
-  const int rank = blockIdx.x & (p.cluster - 1);
-  const unsigned item = blockIdx.x / unsigned(p.cluster);
+  const unsigned item = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   dev::pdl_wait();
   dev::pdl_trigger();
 
-  const Place<T, MODE> at(d, x, item, rank, trow, tcol, ns);
-  const T* xs = x + (at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0);
+  const Place<T, MODE> at(d, x, item, trow, tcol, ns);
+  const T* xs = x + (at.kn > 0 ? at.n * d.L : 0);
   uint4 raw[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (k < at.kn) raw[k] = at.load(xs, k);
 
-  // this thread's channels (within the slab), groups and shifts
+  // this thread's channels, groups and shifts
   int c0 = MODE == 2 ? (tcol * VW + p.W - at.off % p.W) % p.W : tcol * VW;
   int grp[EV];
   float shift[EV];
   for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
     if (e < EV) {
-      grp[e] = ns * p.q + g;
+      grp[e] = ns * d.G + g;
       shift[e] = at.kn > 0 ? dev::ld1_stream(xs + g * d.D) : 0.f;
     }
   });
@@ -297,13 +268,11 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   const bool mine = trow < p.phases;
   const Entries entries(p, d.D, VW, MODE == 0);
   const bool plain = MODE != 2 && entries.reps == 1;
-  const int64_t n0 = int64_t(p.slabs == 1 ? item : item / unsigned(p.slabs)) * p.samples;
+  const int64_t n0 = int64_t(item) * p.samples;
   auto off_of = [&](int s) {
     return MODE == 2 && n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0;
   };
-  // values of a group in this CTA
-  const int my_rows = max(0, min(p.rows, (rank + 1) * p.rows_per_cta) - rank * p.rows_per_cta);
-  const float count = MODE == 2 ? float(d.S) * float(d.D) : float(my_rows) * float(d.D);
+  const float total = float(d.S) * float(d.D);
 
   float m[EV], s[EV];
   centred_sums<T, NV, MODE, false>(raw, at, shift, s);
@@ -330,19 +299,16 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
                if constexpr (MODE == 2) b += cnt[i];
              },
              [&](int s, int ns, float a, float b) {
-               const float n = MODE == 2 ? b : count;
-               const int g = s - ns * p.q;
+               const float n = MODE == 2 ? b : total;
                const int64_t sample = n0 + ns;
                const float first =
-                   sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(at.slab) * p.W + g * d.D) : 0.f;
+                   sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(s - ns * d.G) * d.D) : 0.f;
                const float mean = n > 0.f ? a / n : 0.f;
                const float centre = first + mean;
                // the centre is rounded: it lies by `by` off the mean, which adds n by^2 to the squares
                const float by = mean - (centre - first);
-               gk[s] = first;
                gm[s] = centre;
                gr[s] = n * by * by;
-               if (p.cluster > 1) xch[s] = make_float4(n, mean, 0.f, 0.f);
              });
   __syncthreads();
 #pragma unroll
@@ -352,37 +318,19 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     put_entries(ent, s);
   }
   __syncthreads();
-  const float total = float(d.S) * float(d.D);
-  auto finish = [&](int s, int ns, float mu, float m2) {
-    const float r = 1.0f / sqrtf(not_negative(m2) / total + d.eps);
-    gm[s] = mu;
-    gr[s] = r;
-    const int64_t sample = n0 + ns;
-    if (rank == 0 && sample < d.N) {
-      const int64_t i = sample * d.G + int64_t(at.slab) * p.q + (s - ns * p.q);
-      if (mean_out != nullptr) mean_out[i] = mu;
-      if (inv_out != nullptr) inv_out[i] = r;
-    }
-  };
   entries.run<false>(
              ent, cnt, col, col_n, plain, off_of, [&](int i, float& a, float&) { a += ent[i]; },
              [&](int s, int ns, float a, float) {
-               if (p.cluster == 1) finish(s, ns, gm[s], a - gr[s]);
-               else xch[s].z = not_negative(a - gr[s]);
+               const float r = 1.0f / sqrtf(not_negative(a - gr[s]) / total + d.eps);
+               gr[s] = r;
+               const int64_t sample = n0 + ns;
+               if (sample < d.N) {
+                 const int64_t i = sample * d.G + (s - ns * d.G);
+                 if (mean_out != nullptr) mean_out[i] = gm[s];
+                 if (inv_out != nullptr) inv_out[i] = r;
+               }
              });
-  if (p.cluster > 1) {
-    cluster_sync();
-    for_slots_by_rank(slots, p.cluster, [&](int s, int r) {
-      const float4 v = s < slots ? ld_rank(xch + s, r) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float mean = set_sum(v.x * v.y, p.cluster) / total;
-      const float t = v.y - mean;
-      const float m2 = set_sum(v.z + v.x * t * t, p.cluster);
-      if (s < slots && r == 0) finish(s, 0, gk[s] + mean, m2);
-    });
-    cluster_sync();  // no block leaves (or overwrites x) while another reads its sums
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
 
   // y
   float mu[EV], rs[EV], a[VW], b[VW];
@@ -392,11 +340,10 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     rs[e] = mine ? gr[grp[e]] : 0.f;
   }
   if (at.kn > 0) {
-    const int cs = at.slab * p.W;
-    load_params<T, MODE == 2>(gamma, beta, cs, c0, p.W, d.pvec, a, b);
+    load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, a, b);
 #pragma unroll
     for (int e = 0; e < VW; ++e) a[e] *= rs[MODE == 0 ? 0 : e];
-    T* ys = y + at.n * d.L + cs;
+    T* ys = y + at.n * d.L;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (k < at.kn) {
@@ -410,10 +357,9 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   }
 }
 
-// The gradient.  A CTA takes items in turn (grid_items apart), all of one slab,
-// and keeps the sums of du and du * h of its channels over them in registers;
-// they leave once, as row (item index * cluster + rank) of cpart: 2 x [row][C].
-// The groups' means m1 and m2 of an item meet as the forward's sums do.
+// The gradient.  A CTA takes items in turn (grid_items apart) and keeps the sums
+// of du and du * h of its channels over them in registers; they leave once, as row
+// blockIdx of cpart: 2 x [row][C].
 template <typename T, int NV, int MODE>
 __global__ void __launch_bounds__(kMaxThreads)
 k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
@@ -422,17 +368,15 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   constexpr int EV = MODE == 0 ? 1 : VW;
   extern __shared__ __align__(16) float smem[];
   const FusedPlan& p = d.p;
-  const int slots = p.samples * p.q, ents = p.phases * p.cf * VW;
-  float4* xch = reinterpret_cast<float4*>(smem);
-  float* ent_a = smem + (p.cluster > 1 ? 4 * slots : 0);
+  const int slots = p.samples * d.G, ents = p.phases * p.cf * VW;
+  float* ent_a = smem;
   float* ent_b = ent_a + ents;
   const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_a = ent_b + ents;
   float* col_b = col_a + cols;
   float* g1 = col_b + cols;
   float* g2 = g1 + slots;
-  const int rank = blockIdx.x & (p.cluster - 1);
-  const unsigned first = blockIdx.x / unsigned(p.cluster);
+  const unsigned first = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   const bool mine = trow < p.phases;
@@ -442,15 +386,15 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   dev::pdl_trigger();
 
   float tot_a[VW], tot_b[VW], ga[VW], be[VW];
-  int grp[EV];  // within the slab
+  int grp[EV];
 #pragma unroll
   for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = ga[e] = be[e] = 0.f;
-  int off = 0, c0 = 0, slab = 0;
+  int off = 0, c0 = 0;
   bool once = true;
 
   for (unsigned item = first; item < unsigned(p.items); item += unsigned(p.grid_items)) {
-    const Place<T, MODE> at(d, x, item, rank, trow, tcol, ns);
-    const int64_t base = at.kn > 0 ? at.n * d.L + int64_t(at.slab) * p.W : 0;
+    const Place<T, MODE> at(d, x, item, trow, tcol, ns);
+    const int64_t base = at.kn > 0 ? at.n * d.L : 0;
     uint4 raw[NV], rdy[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -459,20 +403,19 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
         rdy[k] = at.load(dy + base, k);
       }
     }
-    if (once) {  // the items of a CTA share their slab, and (MODE 2) their offset
+    if (once) {  // the items of a CTA share (MODE 2) their offset
       once = false;
-      slab = at.slab;
       if constexpr (MODE == 2) {
         off = dev::misalignment(x + int64_t(item) * p.samples * d.L);
       }
       c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
-      if (mine) load_params<T, MODE == 2>(gamma, beta, slab * p.W, c0, p.W, d.pvec, ga, be);
+      if (mine) load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, ga, be);
       for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
         if (e < EV) grp[e] = g;
       });
     }
     float mu[EV], rs[EV];
-    const int64_t ng = at.n * d.G + int64_t(slab) * p.q;
+    const int64_t ng = at.n * d.G;
 #pragma unroll
     for (int e = 0; e < EV; ++e) {
       mu[e] = at.kn > 0 ? mean[ng + grp[e]] : 0.f;
@@ -534,33 +477,16 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
                  b += ent_b[i];
                },
                [&](int s, int, float a, float b) {
-                 if (p.cluster == 1) {
-                   g1[s] = a * scale;
-                   g2[s] = b * scale;
-                 } else {
-                   xch[s] = make_float4(a, b, 0.f, 0.f);
-                 }
+                 g1[s] = a * scale;
+                 g2[s] = b * scale;
                });
-    if (p.cluster > 1) {
-      cluster_sync();
-      for_slots_by_rank(slots, p.cluster, [&](int s, int r) {
-        const float4 v = s < slots ? ld_rank(xch + s, r) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float a = set_sum(v.x, p.cluster), b = set_sum(v.y, p.cluster);
-        if (s < slots && r == 0) {
-          g1[s] = a * scale;
-          g2[s] = b * scale;
-        }
-      });
-      cluster_sync();  // the next item's sums go to the same place
-    } else {
-      __syncthreads();
-    }
+    __syncthreads();
     if (at.kn > 0) {
       float a1[EV], a2[EV];
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
-        a1[e] = g1[ns * p.q + grp[e]];
-        a2[e] = g2[ns * p.q + grp[e]];
+        a1[e] = g1[ns * d.G + grp[e]];
+        a2[e] = g2[ns * d.G + grp[e]];
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -588,8 +514,6 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   __syncthreads();
   // channel c is at off + c + k W, modulo a sample's positions, in every sample
   const int np = p.per_sample * p.cf * VW, reps = np / p.W;
-  const int64_t rows = p.grid_items / p.slabs * p.cluster;
-  const int64_t row = (first / p.slabs) * p.cluster + rank;
   const int many = reps * p.samples;
   const int set = many >= 32 ? 32 : 1;  // lanes to a channel
   for (int c = threadIdx.x / set; c < p.W; c += blockDim.x / set) {
@@ -607,9 +531,9 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       b = dev::warp_sum(b);
     }
     if ((threadIdx.x & (set - 1)) == 0) {
-      float* out = cpart + row * d.C + slab * p.W + c;
+      float* out = cpart + int64_t(first) * d.C + c;
       out[0] = a;
-      out[rows * d.C] = b;
+      out[p.grid_items * d.C] = b;
     }
   }
 }
@@ -650,7 +574,7 @@ k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N;
   int64_t n = int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows + trow;
   float a[VW], b[VW];
-  if (mine) load_params<T, false>(gamma, beta, 0, col * VW, 0, d.pvec, a, b);
+  if (mine) load_params<T, false>(gamma, beta, col * VW, 0, d.pvec, a, b);
   // every lane of a warp goes round as often as its first (the shuffles are whole warps')
   const int rounds = static_cast<int>((n1 - (int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows) + step * U - 1) /
                                       (step * U));
@@ -720,7 +644,7 @@ k_gn_grad_token(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float ga[VW], be[VW], tot_a[VW], tot_b[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) ga[e] = be[e] = tot_a[e] = tot_b[e] = 0.f;
-  if (mine) load_params<T, false>(gamma, beta, 0, col * VW, 0, d.pvec, ga, be);
+  if (mine) load_params<T, false>(gamma, beta, col * VW, 0, d.pvec, ga, be);
   const int rounds = static_cast<int>((n1 - int64_t(row) * d.p.rows + step * U - 1) / (step * U));
   for (int i = 0; i < rounds; ++i, n += step * U) {
     uint4 rx[U], rd[U];
@@ -793,78 +717,37 @@ int pow2_at_least(int64_t v) {
   return p;
 }
 
-// Splits the rows of a sample (cf fragments each) over threads and CTAs: false
-// if `nv_max` fragments a thread do not hold it.
-bool split_rows(FusedPlan* p, int64_t N, int64_t rows, int nv_max) {
-  if (p->cf > kMaxThreads || rows > INT_MAX / 2) return false;
-  p->rows = int(rows);
-  const int64_t frags = rows * p->cf;
-  if (frags <= 4 * kWalkThreads) {
-    // a small sample: one CTA, about 256 threads, with other samples where there
-    // are enough of them (and two fragments a thread where one sample fills it)
-    int phases = std::max(1, kWalkThreads / p->cf);
-    p->per_sample = int(std::min<int64_t>(rows, phases));
-    while ((rows + p->per_sample - 1) / p->per_sample > nv_max && p->cf * (p->per_sample + 1) <= kMaxThreads)
-      p->per_sample += 1;
-    if ((rows + p->per_sample - 1) / p->per_sample > nv_max) return false;
-    const int64_t fit = std::max(1, phases / p->per_sample);
-    p->samples = int(std::max<int64_t>(1, std::min(fit, N * p->slabs / (2 * kPlanSms))));
-    p->phases = p->samples * p->per_sample;
-    p->cluster = 1;
-    p->rows_per_cta = int(rows);
-  } else {
-    const int most = kMaxThreads / p->cf;  // rows side by side
-    static const int kMaxCluster = getenv("EPX_MAXK") ? atoi(getenv("EPX_MAXK")) : 16;
-    if (kMaxCluster == 0) return false;
-    int64_t per = rows;
-    int k = 1;
-    while (k < kMaxCluster && ((per = (rows + k - 1) / k) + most - 1) / most > nv_max) k *= 2;
-    while (k < kMaxCluster && N * p->slabs * k < kPlanSms && (rows + k - 1) / k > most) k *= 2;
-    per = (rows + k - 1) / k;
-    if ((per + most - 1) / most > nv_max) return false;
-    p->cluster = k;
-    p->rows_per_cta = int(per);
-    p->per_sample = p->phases = int(std::min<int64_t>(per, most));
-    p->samples = 1;
-  }
-  p->threads = (p->phases * p->cf + 31) / 32 * 32;
-  const int need = (p->rows_per_cta + p->per_sample - 1) / p->per_sample;
-  p->nv = pow2_at_least(need);
-  p->items = (N + p->samples - 1) / p->samples * p->slabs;
-  p->grid_items = p->items;
-  return p->items * p->cluster <= INT_MAX;
-}
+// Up to this many fragments a sample has a block of 256 threads, beyond that one of 512.
+constexpr int64_t kSmallFrags = 4 * kWalkThreads;
 
-// slab: C % vw == 0 and 16-byte-aligned operands; else the walk over whole samples.
-bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, int nv_max, FusedPlan* p) {
-  const int64_t D = C / G;
-  if (!slab) {
-    p->W = int(C);
-    p->slabs = 1;
-    p->q = int(G);
-    const int64_t period = C / std::gcd(C, int64_t(vw));
-    if (period > kMaxThreads) return false;
-    p->cf = int(period);
-    const int64_t total = (S * C + 2 * (vw - 1)) / vw;  // fragments, wherever a sample starts
-    return split_rows(p, N, (total + period - 1) / period, nv_max);
-  }
-  if (C % vw != 0) return false;
-  auto with = [&](int64_t q) {
-    p->W = int(q * D);
-    p->slabs = int(G / q);
-    p->q = int(q);
-    p->cf = int(q * D / vw);
-    return split_rows(p, N, S, nv_max);
-  };
-  // a small sample stays in one piece, with contiguous rows
-  if (C / vw <= kMaxThreads && S * (C / vw) <= 4 * kWalkThreads) return with(G);
-  // else the narrowest slab of whole groups whose rows are 128 bytes or more
-  for (int64_t q = 1; q <= G; ++q) {
-    if (G % q != 0 || q * D % vw != 0) continue;
-    if (q * D / vw > kMaxThreads) break;
-    if (q * D / vw >= 8 || q == G) return with(q);
-  }
-  return false;
+// slab: C % vw == 0 and 16-byte-aligned operands; else the walk over whole
+// samples.  False where a sample is too large for a block of nv_max fragments a thread.
+bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, FusedPlan* p) {
+  if (slab && C % vw != 0) return false;
+  const int64_t period = slab ? C / vw : C / std::gcd(C, int64_t(vw));
+  if (period > kMaxThreads) return false;
+  p->W = int(C);
+  p->cf = int(period);
+  // walk rows of a sample, wherever it starts
+  const int64_t rows = slab ? S : ((S * C + 2 * (vw - 1)) / vw + period - 1) / period;
+  const int64_t frags = rows * period;
+  if (frags > int64_t(kMaxThreads) * nv_max) return false;
+  p->rows = int(rows);
+  const int threads = frags > kSmallFrags ? kMaxThreads : kWalkThreads;
+  const int phases = std::max(1, threads / p->cf);
+  p->per_sample = int(std::min<int64_t>(rows, phases));
+  while ((rows + p->per_sample - 1) / p->per_sample > nv_max && p->cf * (p->per_sample + 1) <= kMaxThreads)
+    p->per_sample += 1;
+  if ((rows + p->per_sample - 1) / p->per_sample > nv_max) return false;
+  // other samples beside it, where there are enough of them
+  const int64_t fit = std::max(1, phases / p->per_sample);
+  p->samples = int(std::max<int64_t>(1, std::min(fit, N / (2 * kPlanSms))));
+  p->phases = p->samples * p->per_sample;
+  p->threads = (p->phases * p->cf + 31) / 32 * 32;
+  p->nv = pow2_at_least((rows + p->per_sample - 1) / p->per_sample);
+  p->items = (N + p->samples - 1) / p->samples;
+  p->grid_items = p->items;
+  return p->items <= INT_MAX;
 }
 
 // The token form applies: S = 1, aligned, and a group is 1 to 32 (a power of two) lanes.
@@ -915,37 +798,13 @@ cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cp
   return e;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, int threads, size_t smem, int cluster,
-                           cudaStream_t stream, Args... args) {
-  if (cluster > 8) {  // beyond the portable size
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = EP_PDL ? 1 : 0;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-// Shared memory: the cluster's exchange, the entries (MODE 2: and their counts;
-// the gradient: two sets for every channel) and the groups' values.
-size_t fused_smem(const FusedPlan& p, int mode, int vw, bool grad) {
-  const size_t slots = size_t(p.samples) * p.q, frags = size_t(p.phases) * p.cf;
+// Shared memory: the entries (MODE 2: and their counts; the gradient: two sets for
+// every channel), the columns' sums and the groups' values.
+size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
+  const size_t slots = size_t(p.samples) * G, frags = size_t(p.phases) * p.cf;
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
   const size_t cols = size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
-  return 4 * (ents + cols + (p.cluster > 1 ? 4 * slots : 0) + (grad ? 2 : 3) * slots);
+  return 4 * (ents + cols + 2 * slots);
 }
 constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
 
@@ -955,12 +814,11 @@ cudaError_t fused_fwd(const GroupNormArgs& a, const FusedDims& d, cudaStream_t s
   auto fn = p.nv == 1   ? k_gn_fused<T, 1, MODE>
             : p.nv == 2 ? k_gn_fused<T, 2, MODE>
             : p.nv == 4 ? k_gn_fused<T, 4, MODE>
-            : p.nv == 8 ? k_gn_fused<T, 8, MODE>
-                        : k_gn_fused<T, 16, MODE>;
-  const cudaError_t e = launch_cluster(
-      fn, unsigned(p.items * p.cluster), p.threads, fused_smem(p, MODE, dev::Vec16<T>::N, false), p.cluster, stream,
-      static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta),
-      static_cast<T*>(a.y), a.mean, a.inv, d);
+                        : k_gn_fused<T, 8, MODE>;
+  const cudaError_t e = launch(fn, dim3(unsigned(p.items)), dim3(p.threads),
+                               fused_smem(p, MODE, dev::Vec16<T>::N, a.G, false), stream,
+                               static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
+                               static_cast<const T*>(a.beta), static_cast<T*>(a.y), a.mean, a.inv, d);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -972,18 +830,17 @@ cudaError_t fused_grad(const GroupNormGradArgs& a, const FusedDims& d, float* cp
   auto fn = p.nv == 1   ? k_gn_grad_fused<T, 1, MODE>
             : p.nv == 2 ? k_gn_grad_fused<T, 2, MODE>
                         : k_gn_grad_fused<T, 4, MODE>;
-  cudaError_t e = launch_cluster(
-      fn, unsigned(p.grid_items * p.cluster), p.threads, fused_smem(p, MODE, dev::Vec16<T>::N, true), p.cluster,
-      stream, static_cast<const T*>(a.dy), static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
-      static_cast<const T*>(a.beta), a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
+  cudaError_t e = launch(fn, dim3(unsigned(p.grid_items)), dim3(p.threads),
+                         fused_smem(p, MODE, dev::Vec16<T>::N, a.G, true), stream, static_cast<const T*>(a.dy),
+                         static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta),
+                         a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (cpart != nullptr) {
     const int64_t jobs = (int64_t(d.C) + 31) / 32 * 2;
     // the sums of du are dbeta, those of du * h are dgamma
-    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart,
-               p.grid_items / p.slabs * p.cluster, int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta),
-               static_cast<T*>(a.dgamma));
+    e = launch(k_channel_sums<T>, dim3(unsigned(jobs)), dim3(kSumsThreads), 0, stream, cpart, p.grid_items,
+               int64_t(1), int64_t(d.C), 2, static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
     if (e == cudaSuccess) *launches += 1;
   }
   return e;
@@ -991,23 +848,16 @@ cudaError_t fused_grad(const GroupNormGradArgs& a, const FusedDims& d, float* cp
 
 inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uintptr_t>(p) & 15u); }
 
-// Items of the gradient that run at a time: all CTAs resident at about four (of
-// 256 threads) an SM, a whole number of them for each slab.
-void persist(FusedPlan* p) {
-  const int64_t ctas = kPlanSms * std::max(1, 1024 / p->threads);
-  const int64_t per_slab = std::max<int64_t>(1, ctas / (int64_t(p->slabs) * p->cluster));
-  p->grid_items = std::min(p->items / p->slabs, per_slab) * p->slabs;
-}
-
-constexpr int kFwdNv = 16, kGradNv = 4;
+constexpr int kFwdNv = 8, kGradNv = 4;
 
 bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, FusedPlan* p) {
-  if (!fused_plan(vw, N, S, C, G, slab, kGradNv, p)) return false;
-  persist(p);
+  if (!fused_plan(vw, N, S, C, slab, kGradNv, p)) return false;
+  // items that run at a time: about 1024 threads an SM
+  p->grid_items = std::min<int64_t>(p->items, kPlanSms * std::max(1, 1024 / p->threads));
   // a CTA's items share the offset of their channels: all samples start alike,
   // or a CTA has one sample
   if (!slab && S * C % vw != 0 && (p->samples > 1 || p->grid_items < p->items)) return false;
-  return fused_smem(*p, slab ? 1 : 2, vw, true) <= kSmemMost;  // (mode 0 needs less)
+  return fused_smem(*p, slab ? 1 : 2, vw, G, true) <= kSmemMost;  // (mode 0 needs less)
 }
 
 }  // namespace
@@ -1021,7 +871,7 @@ size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int
   for (int slab = 0; slab < 2; ++slab) {
     FusedPlan p;
     if (grad_plan(vw, N, S, C, G, slab != 0, &p))
-      most = std::max(most, size_t(p.grid_items / p.slabs * p.cluster) * size_t(C) * 8);
+      most = std::max(most, size_t(p.grid_items) * size_t(C) * 8);
   }
   return most;
 }
@@ -1044,9 +894,9 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t st
       default: return token_fwd<__nv_bfloat16>(a, t, stream, launches);
     }
   }
-  if (!fused_plan(vw, a.N, a.S, a.C, a.G, slab, kFwdNv, &d.p)) return cudaSuccess;
+  if (!fused_plan(vw, a.N, a.S, a.C, slab, kFwdNv, &d.p)) return cudaSuccess;
   const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
-  if (fused_smem(d.p, mode, vw, false) > kSmemMost) return cudaSuccess;
+  if (fused_smem(d.p, mode, vw, a.G, false) > kSmemMost) return cudaSuccess;
   *done = true;
 #define EP_GN_FUSED(T)                                                          \
   (mode == 0   ? fused_fwd<T, 0>(a, d, stream, launches)                        \
