@@ -336,21 +336,22 @@ def _first(name, t):
     return t.get_device(), _dtype(t)
 
 
-def _operand(name, t, like, shape=None, dtype=None):
-    """t, checked to be a contiguous CUDA tensor on like's device with the given
-    dtype (like's if None) and shape (any if None)."""
+def _operand(name, t, like, index, shape=None, dtype=None):
+    """t, checked to be a contiguous CUDA tensor on like's device (`index`) with
+    the given dtype (like's if None) and shape (any if None)."""
     dtype = like.dtype if dtype is None else dtype
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and \
+            (shape is None or t.shape == shape) and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != like.get_device():
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, not {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _elsewhere(stream, index):
@@ -363,16 +364,23 @@ def _elsewhere(stream, index):
     return None if _current_device() == index else torch.cuda.device(index)
 
 
-def _scratch(workspace, need, like):
-    """(pointer, bytes, tensor) of the caller's workspace, or of one allocated for this call."""
+# Scratch comes from PyTorch's allocator as a bare pointer: a tensor that nobody
+# sees costs 2 us more.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", torch.cuda.caching_allocator_alloc)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", torch.cuda.caching_allocator_delete)
+
+
+def _scratch(workspace, need, like, raw_stream):
+    """(pointer, bytes, owned): the caller's workspace, or memory allocated for
+    this call, which goes back to the allocator once the call is in the stream
+    (owned; the current device and stream are the call's)."""
     if workspace is None:
         if need == 0:
-            return None, 0, None
-        workspace = like.new_empty(need, dtype=torch.uint8)
-        return workspace.data_ptr(), need, workspace
+            return None, 0, False
+        return _raw_alloc(need, raw_stream), need, True
     if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the operands' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), False
 
 
 def _addr(t):
@@ -435,23 +443,23 @@ def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
     return _bias_dropout_grad_need(_code(dtype), tuple(shape))
 
 
-def _group_stats(name, t, X, n, groups):
+def _group_stats(name, t, X, index, n, groups):
     if t is None or t is False:
         return None
     if t is True:
-        return X.new_empty((n, max(0, groups)), dtype=torch.float32)
-    _operand(name, t, X, dtype=torch.float32)
+        return torch.empty((n, max(0, groups)), dtype=torch.float32, device=X.device)
+    _operand(name, t, X, index, dtype=torch.float32)
     if t.numel() != n * groups:
         raise ValueError(f"{name} must have {n * groups} elements")
     return t
 
 
-def _param_grad(name, t, X, channels):
+def _param_grad(name, t, X, index, channels):
     if t is None or t is False:
         return None
     if t is True:
-        return X.new_empty(channels)
-    return _operand(name, t, X, channels)
+        return torch.empty(channels, dtype=X.dtype, device=X.device)
+    return _operand(name, t, X, index, channels)
 
 
 def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_EPSILON, activation=EP_ACT_NONE,
@@ -471,15 +479,21 @@ def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_E
     lib = load_library()
     shape, groups = X.shape, int(groups)
     nsc, channels = _nsc(shape), shape[-1:]
-    _operand("gamma", gamma, X, channels)
+    _operand("gamma", gamma, X, index, channels)
     if beta is not None:
-        _operand("beta", beta, X, channels)
-    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, shape)
-    mean = _group_stats("mean", mean, X, shape[0], groups)
-    inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, shape[0], groups)
-    ws, wbytes, _keep = _scratch(workspace, _group_norm_need(code, shape, groups, False), X)
-    _check(lib.ep_group_norm(code, X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation),
-                             Y.data_ptr(), _addr(mean), _addr(inv_std_dev), ws, wbytes, _raw_stream(index)))
+        _operand("beta", beta, X, index, channels)
+    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, index, shape)
+    mean = _group_stats("mean", mean, X, index, shape[0], groups)
+    inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, index, shape[0], groups)
+    args = (code, X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation),
+            Y.data_ptr(), _addr(mean), _addr(inv_std_dev))
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, _group_norm_need(code, shape, groups, False), X, s)
+    try:
+        _check(lib.ep_group_norm(*args, ws, wbytes, s))
+    finally:
+        if owned:
+            _raw_delete(ws)
     return Y, mean, inv_std_dev
 
 
@@ -500,21 +514,26 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
     lib = load_library()
     shape, groups = X.shape, int(groups)
     nsc, channels = _nsc(shape), shape[-1:]
-    _operand("dY", dY, X, shape)
-    _operand("gamma", gamma, X, channels)
+    _operand("dY", dY, X, index, shape)
+    _operand("gamma", gamma, X, index, channels)
     if beta is not None:
-        _operand("beta", beta, X, channels)
+        _operand("beta", beta, X, index, channels)
     for name, t in (("mean", mean), ("inv_std_dev", inv_std_dev)):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} is required")
-        _group_stats(name, t, X, shape[0], groups)
-    dX = torch.empty_like(X) if dX is None else _operand("dX", dX, X, shape)
-    dgamma = _param_grad("dgamma", dgamma, X, channels)
-    dbeta = _param_grad("dbeta", dbeta, X, channels)
-    ws, wbytes, _keep = _scratch(workspace, _group_norm_need(code, shape, groups, True), X)
-    _check(lib.ep_group_norm_grad(code, dY.data_ptr(), X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups,
-                                  int(activation), mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(), _addr(dgamma),
-                                  _addr(dbeta), ws, wbytes, _raw_stream(index)))
+        _group_stats(name, t, X, index, shape[0], groups)
+    dX = torch.empty_like(X) if dX is None else _operand("dX", dX, X, index, shape)
+    dgamma = _param_grad("dgamma", dgamma, X, index, channels)
+    dbeta = _param_grad("dbeta", dbeta, X, index, channels)
+    args = (code, dY.data_ptr(), X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, int(activation),
+            mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(), _addr(dgamma), _addr(dbeta))
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, _group_norm_need(code, shape, groups, True), X, s)
+    try:
+        _check(lib.ep_group_norm_grad(*args, ws, wbytes, s))
+    finally:
+        if owned:
+            _raw_delete(ws)
     return dX, dgamma, dbeta
 
 
@@ -541,11 +560,11 @@ def ep_bias_dropout(X, ratio, seed, offset=0, bias=None, residual=None, offset_d
     lib = load_library()
     shape = X.shape
     if bias is not None:
-        _operand("bias", bias, X, shape[-1:])
+        _operand("bias", bias, X, index, shape[-1:])
     if residual is not None:
-        _operand("residual", residual, X, shape)
+        _operand("residual", residual, X, index, shape)
     od = _offset_device(offset_device, X)
-    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, shape)
+    Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, index, shape)
     _check(lib.ep_bias_dropout(code, X.data_ptr(), _dims(shape), len(shape), _addr(bias), _addr(residual), float(ratio),
                                _u64("seed", seed), _u64("offset", offset), od, Y.data_ptr(), _raw_stream(index)))
     return Y
@@ -563,11 +582,16 @@ def ep_bias_dropout_grad(dY, ratio, seed, offset=0, offset_device=None, dX=None,
     lib = load_library()
     shape = dY.shape
     od = _offset_device(offset_device, dY)
-    dX = torch.empty_like(dY) if dX is None else _operand("dX", dX, dY, shape)
-    dbias = _param_grad("dbias", dbias, dY, shape[-1:])
+    dX = torch.empty_like(dY) if dX is None else _operand("dX", dX, dY, index, shape)
+    dbias = _param_grad("dbias", dbias, dY, index, shape[-1:])
     need = 0 if dbias is None else _bias_dropout_grad_need(code, shape)
-    ws, wbytes, _keep = _scratch(workspace, need, dY)
-    _check(lib.ep_bias_dropout_grad(code, dY.data_ptr(), _dims(shape), len(shape), float(ratio), _u64("seed", seed),
-                                    _u64("offset", offset), od, dX.data_ptr(), _addr(dbias), ws, wbytes,
-                                    _raw_stream(index)))
+    args = (code, dY.data_ptr(), _dims(shape), len(shape), float(ratio), _u64("seed", seed), _u64("offset", offset),
+            od, dX.data_ptr(), _addr(dbias))
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, need, dY, s)
+    try:
+        _check(lib.ep_bias_dropout_grad(*args, ws, wbytes, s))
+    finally:
+        if owned:
+            _raw_delete(ws)
     return dX, dbias
