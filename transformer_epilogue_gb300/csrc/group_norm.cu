@@ -44,6 +44,7 @@ struct GnDims {
   int64_t frags, full_rows;
   int rest;
   bool pvec;  // gamma and beta 16-byte aligned (and every fragment's channels one after another)
+  bool here;  // pass 2 joins the chunks itself
   WalkPlan p;
 };
 
@@ -386,12 +387,14 @@ template <typename T, int EV, bool SILU>
 struct ApplyValues {
   static constexpr int VW = dev::Vec16<T>::N;
   float mu[EV], a[VW], b[VW];
-  __device__ __forceinline__ void load(int c0, int64_t ng, const GnDims& d, const T* __restrict__ gamma,
-                                       const T* __restrict__ beta, const float* mean, const float* inv) {
+  __device__ __forceinline__ void load_params(int c0, const GnDims& d, const T* __restrict__ gamma,
+                                              const T* __restrict__ beta) {
 #pragma unroll
     for (int e = 0; e < VW; ++e) b[e] = 0.f;
     load_param(gamma, c0, d.C, d.pvec, a);
     if (beta != nullptr) load_param(beta, c0, d.C, d.pvec, b);
+  }
+  __device__ __forceinline__ void scale(int c0, int64_t ng, const GnDims& d, const float* mean, const float* inv) {
     scale_by_group(c0, ng, d, mean, inv, mu, a);
   }
   __device__ __forceinline__ void operator()(float (&v)[VW]) const {
@@ -442,8 +445,8 @@ struct GradApplyValues : GradValues<T, EV, SILU> {
     for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
       if (e < EV) {
         const float r = inv[ng + g];
-        q1[e] = -r * __ldcg(m1 + ng + g);
-        q2[e] = -r * (r * __ldcg(m2 + ng + g));
+        q1[e] = -r * m1[ng + g];
+        q2[e] = -r * (r * m2[ng + g]);
       }
     });
   }
@@ -659,8 +662,8 @@ __device__ __forceinline__ float median3(float a, float b, float c) {
   return fmaxf(fminf(a, b), fminf(fmaxf(a, b), c));
 }
 
-// Pass 1.  partial: [item][tile][G] x (count, mean, M2, -), the mean relative to
-// the group's first value in the sample.  The block takes its values relative to
+// Pass 1.  partial: [item][tile][G] x (count, mean, M2, the group's first value in
+// the sample), the mean relative to that value.  The block takes its values relative to
 // a centre of each group, so that its sums and sums of squares simply add up: the
 // median of three of the group's values in the item's first walk row, which lies
 // among the values unless two of the three are outliers.  Off by k standard
@@ -822,21 +825,72 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                }
                const float m = n > 0.f ? a / n : 0.f;
                const float first = dev::ld1_keep(xs + int64_t(cols.g0 + g) * d.D);
-               out[cols.g0 + g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), 0.f);
+               out[cols.g0 + g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), first);
              });
     consumer_sync();
   }
+}
+
+// The statistics of sample n, joined by pass 2 itself (GnDims::here), by all
+// consumers: neighbouring threads take neighbouring groups, the rest of the block
+// the other parts.  The parts' means are taken relative to the median of three of
+// them: one centre, and no part read twice.  Off by k of the group's standard
+// deviations it costs the variance k^2 2^-24 of its value, and k^2 is less than
+// the number of parts.
+struct JoinHere {
+  float a[kWalkThreads], b[kWalkThreads];       // by thread
+  float mean[kWalkThreads], inv[kWalkThreads];  // by group
+};
+__device__ __forceinline__ void join_stats_here(const float4* partial, const GnDims& d, int64_t n, int threads,
+                                                JoinHere& js) {
+  const int slices = static_cast<int>(unsigned(threads) / unsigned(d.G));
+  const int slice = static_cast<int>(threadIdx.x / unsigned(d.G)), g = threadIdx.x - slice * d.G;
+  const float4* src = partial + n * d.p.chunks * d.G + g;
+  const float4 first = __ldcg(src), last = __ldcg(src + (d.p.chunks - 1) * d.G);
+  const float mid = __ldcg(src + (d.p.chunks - 1) / 2 * d.G).y;
+  const float centre = median3(first.y, mid, last.x > 0.f ? last.y : first.y);  // (the last may be empty)
+  float a = 0.f, b = 0.f;
+  if (slice < slices) {
+#pragma unroll 8
+    for (int k = slice; k < d.p.chunks; k += slices) {
+      const float4 v = __ldcg(src + k * d.G);
+      const float w = v.y - centre, cw = v.x * w;
+      a += cw;
+      b += fmaf(cw, w, v.z);
+    }
+  }
+  consumer_sync();  // (the sample before has been read)
+  js.a[threadIdx.x] = a;
+  js.b[threadIdx.x] = b;
+  if (slice == 0) {
+    js.mean[g] = centre;
+    js.inv[g] = first.w;
+  }
+  consumer_sync();
+  const float total = float(d.S) * float(d.D);
+  sum_sets(threads, d.G, slices,
+           [&](int i, int k, float& sa, float& sb) {
+             sa += js.a[k * d.G + i];
+             sb += js.b[k * d.G + i];
+           },
+           [&](int i, float sa, float sb) {
+             const float m = sa / total;
+             js.mean[i] = js.inv[i] + (js.mean[i] + m);  // the group's first value + (the centre + m)
+             js.inv[i] = 1.0f / sqrtf(not_negative(sb - sa * m) / total + d.eps);
+           });
+  consumer_sync();
 }
 
 // Pass 2: y from x and the statistics, over the items in reverse: what pass 1
 // read last is in L2.
 template <typename T, bool GROUP, bool ODD, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
-k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
-                  const float* inv, T* y, GnDims d) {
+k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float4* partial,
+                  float* mean, float* inv, T* y, GnDims d) {
   constexpr int VW = dev::Vec16<T>::N;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) StageBars bars;
+  __shared__ JoinHere js;
   const WalkPlan& p = d.p;
   const Tile t(p);
   RowStream<T, 1, ODD> rows(&bars, smem, d, t);
@@ -846,16 +900,30 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
-  dev::pdl_wait();
-  dev::pdl_trigger();
   int c0 = first_channel(t.j, VW, 0, d.C);
-  for (Items it(d, true); it.more(); it.next()) {
+  bool waited = false;
+  int64_t joined = -1;
+  for (Items it(d, true); it.more(); it.next()) {  // (every CTA has an item)
     const Range r = rows.range(p, it.item());
     const int off = ODD ? rows.sample(r.n).off : 0;
     const Ends ends = rows.ends(r, t);
     if constexpr (ODD) c0 = first_channel(t.j, VW, off, d.C);
     ApplyValues<T, GROUP ? 1 : VW, SILU> val;
-    if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+    if (t.mine) val.load_params(c0, d, gamma, beta);
+    if (!waited) {
+      waited = true;
+      dev::pdl_wait();
+      dev::pdl_trigger();
+    }
+    if (d.here && joined != r.n) {
+      joined = r.n;
+      join_stats_here(partial, d, r.n, consumers, js);
+    }
+    if (d.here && r.ra == 0 && int(threadIdx.x) < d.G) {
+      if (mean != nullptr) mean[r.n * d.G + threadIdx.x] = js.mean[threadIdx.x];
+      if (inv != nullptr) inv[r.n * d.G + threadIdx.x] = js.inv[threadIdx.x];
+    }
+    if (t.mine) val.scale(c0, d.here ? 0 : r.n * d.G, d, d.here ? js.mean : mean, d.here ? js.inv : inv);
     const int64_t pitch = p.row_frags * VW;
     T* py = y + r.n * d.L - off + r.ra * pitch + t.j * VW;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
@@ -1002,19 +1070,21 @@ k_gn_grad_apply_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     if (int(threadIdx.x) == consumers) rows.produce(base, d, t, true, dev::policy_evict_first());
     return;
   }
-  dev::pdl_wait();
-  dev::pdl_trigger();
   int c0 = first_channel(t.j, VW, 0, d.C);
-  for (Items it(d, true); it.more(); it.next()) {
+  bool waited = false;
+  for (Items it(d, true); it.more(); it.next()) {  // (every CTA has an item)
     const Range r = rows.range(p, it.item());
     const int off = ODD ? rows.sample(r.n).off : 0;
     const Ends ends = rows.ends(r, t);
     if constexpr (ODD) c0 = first_channel(t.j, VW, off, d.C);
     GradApplyValues<T, GROUP ? 1 : VW, SILU> val;
-    if (t.mine) {
-      val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
-      val.load_means(c0, r.n * d.G, d, inv, m1, m2);
+    if (t.mine) val.load(c0, r.n * d.G, d, gamma, beta, mean, inv);
+    if (!waited) {
+      waited = true;
+      dev::pdl_wait();
+      dev::pdl_trigger();
     }
+    if (t.mine) val.load_means(c0, r.n * d.G, d, inv, m1, m2);
     const int64_t pitch = p.row_frags * VW;
     T* po = dx + r.n * d.L - off + r.ra * pitch + t.j * VW;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
@@ -1360,7 +1430,9 @@ k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     T* ys = y + r.n * d.L;
     const int off = walk_offset<T, VEC>(xs);
     ApplyValues<T, VW, SILU> val;
-    val.load(first_channel(t.j, VW, off, d.C), r.n * d.G, d, gamma, beta, mean, inv);
+    const int c0 = first_channel(t.j, VW, off, d.C);
+    val.load_params(c0, d, gamma, beta);
+    val.scale(c0, r.n * d.G, d, mean, inv);
     for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
       float v[U][VW];
 #pragma unroll
@@ -1625,7 +1697,7 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_bloc
 int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
 GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
-  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, {}};
+  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, {}};
   d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
   d.frags = d.L / vec_width(t);
   d.full_rows = d.frags / d.p.row_frags;
@@ -1636,6 +1708,16 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
 // CTA rows (of `tiles` CTAs) of a launch over N * chunks items.
 int64_t cta_rows_of(const GnDims& d, int64_t most_ctas) {
   return std::max<int64_t>(1, std::min(d.N * d.p.chunks, most_ctas / d.p.tiles));
+}
+
+// Pass 2 joins the parts itself where a block reads them fast: 1024 of them, not
+// more than 128 chunks.  With the join in pass 2 and as a launch of its own, us: f16
+// 3x1331x189 (909 parts) 10.6 and 11.4, bf16 32x4096x320 (320) 45.8 and 47.5; but
+// f16 8x1024x640 (1216) 13.3 and 12.6, 2x4096x320 (4864) 14.6 and 10.9, and one
+// group in 304 chunks 12.2 and 11.6.  (The gradient, whose join adds up the channels
+// too, lost by it: f16 8x1024x640 22.6 and 20.0.)
+bool join_in_pass2(const GnDims& d) {
+  return d.p.tiles == 1 && d.G <= d.p.threads && d.p.chunks <= 128 && int64_t(d.p.chunks) * d.G <= 1024;
 }
 
 bool split_parts(const GnDims& d) { return d.p.chunks > 1 || d.p.tiles > 1; }
@@ -1714,6 +1796,7 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   const int64_t rows = cta_rows_of(d, kPlanSms * 2);
   // the staged passes want whole fragments; the statistics need no alignment of y
   const bool vec = misalign16(x) == misalign16(y);
+  d.here = staged && vec && join_in_pass2(d);
   cudaError_t e;
   if (staged) {
     auto f = group ? k_gn_stats_staged<T, true, false>
@@ -1726,7 +1809,7 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
     e = launch_plain(k_gn_stats<T>, rows, d, stream, launches, 0, x, d, partial, mean, inv);
   }
   if (e != cudaSuccess) return e;
-  if (partial != nullptr) {
+  if (partial != nullptr && !d.here) {
     const int64_t joins = std::min<int64_t>((d.N * d.G + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kPlanSms * 8);
     e = launch(k_gn_join<T>, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv);
     if (e != cudaSuccess) return e;
@@ -1740,7 +1823,8 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
                    : k_gn_apply_staged<T, false, false, kSilu>;
     };
     auto f = a.silu ? pick(std::true_type{}) : pick(std::false_type{});
-    return launch_staged(f, rows, d, stream, launches, 0, x, gamma, beta, mean, inv, y, d);
+    return launch_staged(f, rows, d, stream, launches, 0, x, gamma, beta, partial, d.here ? a.mean : mean,
+                         d.here ? a.inv : inv, y, d);
   }
   auto f = vec ? (a.silu ? k_gn_apply<T, true, true> : k_gn_apply<T, true, false>)
                : (a.silu ? k_gn_apply<T, false, true> : k_gn_apply<T, false, false>);
