@@ -19,9 +19,13 @@ SHAPES = [
     ((1, 9, 4104), 27), ((2, 3, 2055), 5), ((1, 4, 8192), 64),   # rows wider than a block of threads
     ((1, 5000, 32), 8), ((2, 3000, 1), 1), ((1, 2777, 5), 5), ((1, 700, 3), 1),  # few channels
     ((2, 9973, 40), 4),
-    ((2, 1024, 320), 32), ((1, 2048, 96), 96), ((3, 1331, 189), 9), ((1, 4096, 64), 2),  # spread over a cluster
+    ((2, 1024, 320), 32), ((1, 2048, 96), 96), ((3, 1331, 189), 9), ((1, 4096, 64), 2),  # more than a block holds
     ((4503, 1, 1024), 8), ((1103, 1, 4352), 17), ((9001, 1, 544), 17),  # many tokens
-    ((1, 70000, 64), 4), ((2, 30011, 33), 3), ((1, 300, 12288), 32),  # more than a cluster holds
+    # many small samples, several to a block or one block after another, that start anywhere
+    ((700, 1, 76), 4), ((650, 3, 27), 9), ((400, 2, 675), 3), ((1100, 5, 117), 9), ((333, 1, 744), 8),
+    ((900, 1, 2976), 32), ((310, 8, 4), 4), ((500, 2, 384), 64), ((2000, 2, 1), 1), ((160, 1, 4095), 5),
+    ((77, 9, 1044), 9), ((2, 401, 1530), 9), ((1, 2500, 1044), 9), ((3, 700, 747), 9),
+    ((1, 70000, 64), 4), ((2, 30011, 33), 3), ((1, 300, 12288), 32),  # large samples
 ]
 
 

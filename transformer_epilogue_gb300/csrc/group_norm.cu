@@ -45,6 +45,7 @@ struct GnDims {
   int rest;
   bool pvec;  // gamma and beta 16-byte aligned (and every fragment's channels one after another)
   bool here;  // pass 2 joins the chunks itself
+  int64_t ctas;  // CTAs that the plan is made for
   WalkPlan p;
 };
 
@@ -1178,7 +1179,7 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     const int64_t g0 = (r.ra * ts.tokens_a_row + ts.token0) * d.G + ts.group;
     float* pm = mean_out != nullptr && lane == lead ? mean_out + g0 : nullptr;
     float* pi = inv_out != nullptr && lane == lead ? inv_out + g0 : nullptr;
-    rows.consume<2>(r, static_cast<int>(r.rb - r.ra), [&](int row, const auto& raw) {
+    rows.template consume<2>(r, static_cast<int>(r.rb - r.ra), [&](int row, const auto& raw) {
       constexpr int R = sizeof(raw) / sizeof(raw[0]);
       // sums and sums of squares relative to a centre: the median of three of the
       // group's values.  With at most 256 values to a group it is at most 16
@@ -1694,11 +1695,20 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_bloc
   }
 }
 
+// CTAs an SM that the general kernels' plan is made for (us, 2, 8 and 16 of them: f16
+// 2x16070x1044 176, 127 and 146, its gradient 263, 217 and 236).
+constexpr int kGeneralCtas = 8;
+
 int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
 GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
-  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, {}};
+  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, 0, {}};
   d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
+  d.ctas = kPlanSms * 2;
+  if (d.p.tiles > 1 && C % vec_width(t) != 0) {  // the general kernels: no stages, so more blocks an SM
+    d.ctas = kPlanSms * kGeneralCtas;
+    d.p = make_walk(d.L, C, int(vec_width(t)), N, d.ctas, 4);
+  }
   d.frags = d.L / vec_width(t);
   d.full_rows = d.frags / d.p.row_frags;
   d.rest = int(d.frags % d.p.row_frags);
@@ -1706,8 +1716,8 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
 }
 
 // CTA rows (of `tiles` CTAs) of a launch over N * chunks items.
-int64_t cta_rows_of(const GnDims& d, int64_t most_ctas) {
-  return std::max<int64_t>(1, std::min(d.N * d.p.chunks, most_ctas / d.p.tiles));
+int64_t cta_rows_of(const GnDims& d) {
+  return std::max<int64_t>(1, std::min(d.N * d.p.chunks, d.ctas / d.p.tiles));
 }
 
 // Pass 2 joins the parts itself where a block reads them fast: 1024 of them, not
@@ -1721,7 +1731,7 @@ bool join_in_pass2(const GnDims& d) {
 }
 
 bool split_parts(const GnDims& d) { return d.p.chunks > 1 || d.p.tiles > 1; }
-int64_t grad_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 2); }
+int64_t grad_rows(const GnDims& d) { return cta_rows_of(d); }
 
 // Offset in bytes of the next array in a workspace: each starts on 16 bytes.
 size_t pad16(size_t b) { return (b + 15) / 16 * 16; }
@@ -1793,7 +1803,7 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* beta = static_cast<const T*>(a.beta);
   T* y = static_cast<T*>(a.y);
-  const int64_t rows = cta_rows_of(d, kPlanSms * 2);
+  const int64_t rows = cta_rows_of(d);
   // the staged passes want whole fragments; the statistics need no alignment of y
   const bool vec = misalign16(x) == misalign16(y);
   d.here = staged && vec && join_in_pass2(d);
@@ -1908,7 +1918,7 @@ GnDims token_dims(DType t, int64_t N, int64_t C, int64_t G, float eps) {
   d.p.threads = (d.p.tile_frags + 31) / 32 * 32;
   return d;
 }
-int64_t token_rows(const GnDims& d) { return cta_rows_of(d, kPlanSms * 2); }
+int64_t token_rows(const GnDims& d) { return cta_rows_of(d); }
 
 // The gradient's items are short enough for their statistics to fit shared memory
 // (a float each for kWalkThreads * vw groups).

@@ -8,11 +8,12 @@
 //           a fragment lies in one group;
 //   MODE 1  C % VW == 0, any D: the same rows, sums for each channel;
 //   MODE 2  any C and alignment: a walk row is the C / gcd(C, VW) fragments after
-//           which channels repeat (column_walk.cuh); the first and the last
-//           fragment of a sample may be partial.
+//           which channels repeat (column_walk.cuh), or the sample where that has
+//           fewer; the first and the last fragment of a sample may be partial.
 // `phases` walk rows lie side by side in a block, `per_sample` of them in one
 // sample; each thread has up to NV rows.  Several samples share a block where
-// there are many.
+// there are many.  (Blocks that take several sets of samples in turn, parameters
+// kept, lost: f16 300x48x256 7.7 us to 10.8.)
 //
 // Statistics: values are taken relative to their group's first value, summed,
 // and the squares of their distances from the group's mean summed in a second
@@ -46,8 +47,9 @@ struct FusedPlan {
   int phases, per_sample, samples;  // walk rows side by side, of one sample, samples in a block
   int threads, nv;
   int rows;           // walk rows of a sample
+  int reps;           // times each channel occurs in a thread's walk rows of a sample, side by side
   int64_t items;      // blocks of samples
-  int64_t grid_items; // items running at a time (the gradient; forward: all)
+  int64_t grid_items; // the gradient: items that run at a time
 };
 
 struct FusedDims {
@@ -88,6 +90,11 @@ struct Place {
   __device__ __forceinline__ bool inside(int k, int e) const {
     return MODE != 2 || (e0 + k * stride + e >= 0 && e0 + k * stride + e < lim);
   }
+  // Fragment k, where it lies in the sample, on its way into L2.
+  __device__ __forceinline__ void prefetch(const T* base, int k) const {
+    const int64_t at = e0 + k * stride;
+    if (MODE != 2 || (at >= 0 && at < lim)) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + at));
+  }
   __device__ __forceinline__ uint4 load(const T* base, int k) const {
     const int64_t at = e0 + k * stride;
     if (whole(k)) return dev::ld16_stream(base + at);
@@ -113,7 +120,7 @@ struct Entries {
     De = frags ? D / VW : D;
     Cw = frags ? p.cf : p.W;
     np = p.per_sample * p.cf * (frags ? 1 : VW);
-    reps = static_cast<int>(unsigned(np) / unsigned(Cw));
+    reps = p.reps;
     q = p.W / D;
     slots = p.samples * q;
     cols = p.samples * Cw;
@@ -121,36 +128,42 @@ struct Entries {
   __device__ __forceinline__ int sample_of(int slot) const {
     return slots == q ? 0 : static_cast<int>(unsigned(slot) / unsigned(q));
   }
-  // add(position, a, b) for each entry; col_a (and col_b): a float a column;
-  // done(slot, sample, a, b) by one lane.  `plain`: one repeat and no offset, so
-  // that entries are columns already.
+  // The columns' sums: add(position, a, b) for each entry, into col_a (and col_b).
+  template <bool PAIR, typename OFF, typename ADD>
+  __device__ __forceinline__ void columns(float* col_a, float* col_b, OFF off_of, ADD add) const {
+    sum_sets(blockDim.x, cols, reps,
+             [&](int i, int k, float& a, float& b) {
+               const int ns = cols == Cw ? 0 : static_cast<int>(unsigned(i) / unsigned(Cw));
+               int pos = off_of(ns) + (i - ns * Cw) + k * Cw;
+               if (pos >= np) pos -= np;
+               add(ns * np + pos, a, b);
+             },
+             [&](int i, float a, float b) {
+               col_a[i] = a;
+               if constexpr (PAIR) col_b[i] = b;
+             });
+    __syncthreads();
+  }
+  // The groups' sums: add(slot, k, column, a, b), then done(slot, sample, a, b) by one lane.
+  template <typename ADD, typename DONE>
+  __device__ __forceinline__ void groups(ADD add, DONE done) const {
+    sum_sets(blockDim.x, slots, De,
+             [&](int s, int k, float& a, float& b) { add(s, k, s * De + k, a, b); },  // (columns ns Cw + g De + k)
+             [&](int s, float a, float b) { done(s, sample_of(s), a, b); });
+  }
+  // Both.  `plain`: one repeat and no offset, so that entries are columns already.
   template <bool PAIR, typename OFF, typename ADD, typename DONE>
   __device__ __forceinline__ void run(const float* ent_a, const float* ent_b, float* col_a, float* col_b, bool plain,
                                       OFF off_of, ADD add, DONE done) const {
-    const float* ca = ent_a;
-    const float* cb = ent_b;
-    if (!plain) {
-      sum_sets(blockDim.x, cols, reps,
-               [&](int i, int k, float& a, float& b) {
-                 const int ns = cols == Cw ? 0 : static_cast<int>(unsigned(i) / unsigned(Cw));
-                 int pos = off_of(ns) + (i - ns * Cw) + k * Cw;
-                 if (pos >= np) pos -= np;
-                 add(ns * np + pos, a, b);
-               },
-               [&](int i, float a, float b) {
-                 col_a[i] = a;
-                 if constexpr (PAIR) col_b[i] = b;
-               });
-      __syncthreads();
-      ca = col_a;
-      cb = col_b;
-    }
-    sum_sets(blockDim.x, slots, De,
-             [&](int s, int k, float& a, float& b) {  // (sample ns, group g: columns ns Cw + g De + k)
-               a += ca[s * De + k];
-               if constexpr (PAIR) b += cb[s * De + k];
-             },
-             [&](int s, float a, float b) { done(s, sample_of(s), a, b); });
+    if (!plain) columns<PAIR>(col_a, col_b, off_of, add);
+    const float* ca = plain ? ent_a : col_a;
+    const float* cb = plain ? ent_b : col_b;
+    groups(
+        [&](int, int, int c, float& a, float& b) {
+          a += ca[c];
+          if constexpr (PAIR) b += cb[c];
+        },
+        done);
   }
 };
 
@@ -241,6 +254,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float* col_n = col + cols;
   float* gm = col_n + (MODE == 2 ? cols : 0);
   float* gr = gm + slots;
+  float* gf = gr + slots;                                        // the groups' first values
   const unsigned item = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
@@ -254,6 +268,11 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   for (int k = 0; k < NV; ++k)
     if (k < at.kn) raw[k] = at.load(xs, k);
 
+  for (int s = threadIdx.x; s < slots; s += blockDim.x) {
+    const int sn = p.samples == 1 ? 0 : s / unsigned(d.G);
+    const int64_t sample = int64_t(item) * p.samples + sn;
+    gf[s] = sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(s - sn * d.G) * d.D) : 0.f;
+  }
   // this thread's channels, groups and shifts
   int c0 = MODE == 2 ? (tcol * VW + p.W - at.off % p.W) % p.W : tcol * VW;
   int grp[EV];
@@ -298,11 +317,9 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
                a += ent[i];
                if constexpr (MODE == 2) b += cnt[i];
              },
-             [&](int s, int ns, float a, float b) {
+             [&](int s, int, float a, float b) {
                const float n = MODE == 2 ? b : total;
-               const int64_t sample = n0 + ns;
-               const float first =
-                   sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(s - ns * d.G) * d.D) : 0.f;
+               const float first = gf[s];
                const float mean = n > 0.f ? a / n : 0.f;
                const float centre = first + mean;
                // the centre is rounded: it lies by `by` off the mean, which adds n by^2 to the squares
@@ -358,8 +375,9 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
 }
 
 // The gradient.  A CTA takes items in turn (grid_items apart) and keeps the sums
-// of du and du * h of its channels over them in registers; they leave once, as row
-// blockIdx of cpart: 2 x [row][C].
+// of du and du * h of its channels over them, in registers or (MODE 2, where a
+// thread's channels change with the sample's start) in shared memory; they leave
+// once, as row blockIdx of cpart: 2 x [row][C].
 template <typename T, int NV, int MODE>
 __global__ void __launch_bounds__(kMaxThreads)
 k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
@@ -376,6 +394,9 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float* col_b = col_a + cols;
   float* g1 = col_b + cols;
   float* g2 = g1 + slots;
+  float* ch_a = g2 + slots;  // MODE 2: the channels' sums, and gamma
+  float* ch_b = ch_a + p.W;
+  float* ch_g = ch_b + p.W;
   const unsigned first = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
@@ -389,8 +410,14 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   int grp[EV];
 #pragma unroll
   for (int e = 0; e < VW; ++e) tot_a[e] = tot_b[e] = ga[e] = be[e] = 0.f;
-  int off = 0, c0 = 0;
-  bool once = true;
+  int off = -1;
+  const int64_t ahead = p.grid_items * p.samples;  // samples to the next item
+  if constexpr (MODE == 2) {
+    for (int c = threadIdx.x; c < p.W; c += blockDim.x) {  // (used after the first item's first barrier)
+      ch_a[c] = ch_b[c] = 0.f;
+      ch_g[c] = dev::ld1_keep(gamma + c);
+    }
+  }
 
   for (unsigned item = first; item < unsigned(p.items); item += unsigned(p.grid_items)) {
     const Place<T, MODE> at(d, x, item, trow, tcol, ns);
@@ -403,13 +430,19 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
         rdy[k] = at.load(dy + base, k);
       }
     }
-    if (once) {  // the items of a CTA share (MODE 2) their offset
-      once = false;
-      if constexpr (MODE == 2) {
-        off = dev::misalignment(x + int64_t(item) * p.samples * d.L);
+    if (at.n + ahead < d.N) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (k < at.kn) {
+          at.prefetch(x + base + ahead * d.L, k);
+          at.prefetch(dy + base + ahead * d.L, k);
+        }
       }
-      c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
-      if (mine) load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, ga, be);
+    }
+    if (off != at.off && mine) {
+      off = at.off;
+      const int c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
+      load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, ga, be);
       for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
         if (e < EV) grp[e] = g;
       });
@@ -456,7 +489,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
         }
         ent_a[threadIdx.x] = a;
         ent_b[threadIdx.x] = b;
-      } else {
+      } else if constexpr (MODE == 1) {
         float a[VW], b[VW];
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
@@ -465,21 +498,47 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
         }
         put_entries(ent_a, a);
         put_entries(ent_b, b);
+      } else {
+        put_entries(ent_a, sa);
+        put_entries(ent_b, sb);
       }
-      dev::add_pairs(tot_a, sa);
-      dev::add_pairs(tot_b, sb);
+      if constexpr (MODE != 2) {
+        dev::add_pairs(tot_a, sa);
+        dev::add_pairs(tot_b, sb);
+      }
     }
     __syncthreads();
-    entries.run<true>(
-               ent_a, ent_b, col_a, col_b, MODE != 2 && entries.reps == 1, [&](int) { return off; },
-               [&](int i, float& a, float& b) {
-                 a += ent_a[i];
-                 b += ent_b[i];
-               },
-               [&](int s, int, float a, float b) {
-                 g1[s] = a * scale;
-                 g2[s] = b * scale;
-               });
+    auto means = [&](int s, int, float a, float b) {
+      g1[s] = a * scale;
+      g2[s] = b * scale;
+    };
+    auto entry = [&](int i, float& a, float& b) {
+      a += ent_a[i];
+      b += ent_b[i];
+    };
+    if constexpr (MODE != 2) {
+      entries.template run<true>(ent_a, ent_b, col_a, col_b, entries.reps == 1, [](int) { return 0; }, entry, means);
+    } else {
+      const int64_t n0 = int64_t(item) * p.samples;
+      entries.columns<true>(
+          col_a, col_b, [&](int s) { return n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0; }, entry);
+      for (int c = threadIdx.x; c < p.W; c += blockDim.x) {
+        float a = ch_a[c], b = ch_b[c];
+        for (int s = 0; s < p.samples; ++s) {
+          a += col_a[s * p.W + c];
+          b += col_b[s * p.W + c];
+        }
+        ch_a[c] = a;
+        ch_b[c] = b;
+      }
+      entries.groups(
+          [&](int s, int, int c, float& a, float& b) {
+            const float g = ch_g[c - (entries.sample_of(s) * p.W)];
+            a = fmaf(col_a[c], g, a);
+            b = fmaf(col_b[c], g, b);
+          },
+          means);
+    }
     __syncthreads();
     if (at.kn > 0) {
       float a1[EV], a2[EV];
@@ -507,22 +566,27 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 
   if (cpart == nullptr) return;
   __syncthreads();
+  if constexpr (MODE == 2) {
+    for (int c = threadIdx.x; c < p.W; c += blockDim.x) {
+      float* out = cpart + int64_t(first) * d.C + c;
+      out[0] = ch_a[c];
+      out[p.grid_items * d.C] = ch_b[c];
+    }
+    return;
+  }
   if (mine) {
     put_entries(ent_a, tot_a);
     put_entries(ent_b, tot_b);
   }
   __syncthreads();
-  // channel c is at off + c + k W, modulo a sample's positions, in every sample
-  const int np = p.per_sample * p.cf * VW, reps = np / p.W;
+  // channel c is at c + k W in every sample
+  const int np = p.per_sample * p.cf * VW, reps = p.per_sample;
   const int many = reps * p.samples;
   const int set = many >= 32 ? 32 : 1;  // lanes to a channel
   for (int c = threadIdx.x / set; c < p.W; c += blockDim.x / set) {
     float a = 0.f, b = 0.f;
     for (int i = threadIdx.x & (set - 1); i < many; i += set) {
-      const int k = i % reps;
-      int pos = off + c + k * p.W;
-      if (pos >= np) pos -= np;
-      pos += i / reps * np;
+      const int pos = c + i % reps * p.W + i / reps * np;
       a += ent_a[pos];
       b += ent_b[pos];
     }
@@ -724,12 +788,12 @@ constexpr int64_t kSmallFrags = 4 * kWalkThreads;
 // samples.  False where a sample is too large for a block of nv_max fragments a thread.
 bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, FusedPlan* p) {
   if (slab && C % vw != 0) return false;
-  const int64_t period = slab ? C / vw : C / std::gcd(C, int64_t(vw));
+  const int64_t all = (S * C + 2 * (vw - 1)) / vw;  // of a sample, wherever it starts
+  const int64_t period = slab ? C / vw : std::min(C / std::gcd(C, int64_t(vw)), all);
   if (period > kMaxThreads) return false;
   p->W = int(C);
   p->cf = int(period);
-  // walk rows of a sample, wherever it starts
-  const int64_t rows = slab ? S : ((S * C + 2 * (vw - 1)) / vw + period - 1) / period;
+  const int64_t rows = slab ? S : (all + period - 1) / period;
   const int64_t frags = rows * period;
   if (frags > int64_t(kMaxThreads) * nv_max) return false;
   p->rows = int(rows);
@@ -743,6 +807,8 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, 
   const int64_t fit = std::max(1, phases / p->per_sample);
   p->samples = int(std::max<int64_t>(1, std::min(fit, N / (2 * kPlanSms))));
   p->phases = p->samples * p->per_sample;
+  // (a walk row that is the sample has its S positions, one that is a period as many as fit)
+  p->reps = slab ? p->per_sample : rows == 1 && period == all ? int(S) : int(p->per_sample * period * vw / C);
   p->threads = (p->phases * p->cf + 31) / 32 * 32;
   p->nv = pow2_at_least((rows + p->per_sample - 1) / p->per_sample);
   p->items = (N + p->samples - 1) / p->samples;
@@ -799,12 +865,14 @@ cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cp
 }
 
 // Shared memory: the entries (MODE 2: and their counts; the gradient: two sets for
-// every channel), the columns' sums and the groups' values.
+// every channel), the columns' sums and the groups' values (the gradient, MODE 2:
+// and the channels' sums and gamma).
 size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
   const size_t slots = size_t(p.samples) * G, frags = size_t(p.phases) * p.cf;
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
   const size_t cols = size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
-  return 4 * (ents + cols + 2 * slots);
+  const size_t channels = grad && mode == 2 ? 3 * size_t(p.W) : 0;
+  return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels);
 }
 constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
 
@@ -854,9 +922,6 @@ bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, Fu
   if (!fused_plan(vw, N, S, C, slab, kGradNv, p)) return false;
   // items that run at a time: about 1024 threads an SM
   p->grid_items = std::min<int64_t>(p->items, kPlanSms * std::max(1, 1024 / p->threads));
-  // a CTA's items share the offset of their channels: all samples start alike,
-  // or a CTA has one sample
-  if (!slab && S * C % vw != 0 && (p->samples > 1 || p->grid_items < p->items)) return false;
   return fused_smem(*p, slab ? 1 : 2, vw, G, true) <= kSmemMost;  // (mode 0 needs less)
 }
 
