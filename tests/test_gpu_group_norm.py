@@ -21,6 +21,9 @@ SHAPES = [
     ((2, 9973, 40), 4),
     ((2, 1024, 320), 32), ((1, 2048, 96), 96), ((3, 1331, 189), 9), ((1, 4096, 64), 2),  # more than a block holds
     ((4503, 1, 1024), 8), ((1103, 1, 4352), 17), ((9001, 1, 544), 17),  # many tokens
+    # tokens whose groups are 10, 5, 128, 256 and 18 fragments (fp16)
+    ((700, 1, 320), 4), ((3, 1, 1280), 32), ((300, 1, 8192), 8), ((41, 1, 4096), 2), ((5, 1, 432), 3),
+    ((1000, 1, 768), 3), ((1, 1, 544), 1),
     # many small samples, several to a block or one block after another, that start anywhere
     ((700, 1, 76), 4), ((650, 3, 27), 9), ((400, 2, 675), 3), ((1100, 5, 117), 9), ((333, 1, 744), 8),
     ((900, 1, 2976), 32), ((310, 8, 4), 4), ((500, 2, 384), 64), ((2000, 2, 1), 1), ((160, 1, 4095), 5),

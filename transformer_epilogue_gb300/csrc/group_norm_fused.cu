@@ -603,86 +603,121 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 }
 
 // ---------------------------------------------------------------------------
-// One position a sample (S = 1), D / VW a power of two up to 32: the norm over
-// each token's groups.  A group's fragments are neighbouring lanes, so its sums
-// are shuffles and there is no shared memory and no barrier.  A block has `cols`
-// fragment columns of a tile and `rows` tokens side by side; it takes every
-// grid-th set of tokens, so its channels (and parameters) stay the same.  U
-// tokens are loaded before the first is used.
+// One position a sample (S = 1), D % VW == 0: the norm over each token's groups.  A
+// group's fragments are on neighbouring lanes (`set`, a power of two up to 32, where
+// lanes beyond the group's fragments idle), NV on each, so its sums are shuffles and
+// there is no shared memory and no barrier.  A block has `cols` lanes, of whole
+// groups, and `rows` tokens side by side; it takes every grid-th set of tokens, so
+// its channels stay the same.  U tokens are loaded before the first is used.
 // ---------------------------------------------------------------------------
 
 struct TokenPlan {
   int cols, rows, tiles, ctas;  // ctas: of each tile
+  int set, log_set, nv;
 };
 
 struct TokenDims {
   int64_t N, C;
-  int G, set;                   // lanes of a group
+  int G, frags, tile_groups;    // fragments of a group, groups of a tile
   float eps, scale;             // scale: 1 / D
   bool silu, pvec;
   TokenPlan p;
 };
 
-template <typename T>
+// A thread's place: its token row, group and first fragment in the group.
+struct TokenPlace {
+  int trow, g, li, row;
+  bool mine;  // uniform in a set
+  __device__ __forceinline__ explicit TokenPlace(const TokenDims& d) {
+    trow = threadIdx.x / unsigned(d.p.cols);
+    const int lane = threadIdx.x - trow * d.p.cols, tile = blockIdx.x % unsigned(d.p.tiles);
+    row = static_cast<int>(blockIdx.x / unsigned(d.p.tiles));
+    g = tile * d.tile_groups + (lane >> d.p.log_set);
+    li = lane & (d.p.set - 1);
+    mine = trow < d.p.rows && g < d.G;
+  }
+  // Whether the thread has fragment k of its group, and its first channel.
+  __device__ __forceinline__ bool has(const TokenDims& d, int k) const { return li + k * d.p.set < d.frags; }
+  template <int VW>
+  __device__ __forceinline__ int channel(const TokenDims& d, int k) const {
+    return (g * d.frags + li + k * d.p.set) * VW;
+  }
+};
+
+template <typename T, int NV>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, T* y, float* mean_out,
            float* inv_out, TokenDims d) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int U = 4;
+  constexpr int U = NV >= 4 ? 1 : 4 / NV;
   dev::pdl_wait();
   dev::pdl_trigger();
-  const int trow = threadIdx.x / unsigned(d.p.cols), tile = blockIdx.x % unsigned(d.p.tiles);
-  const int col = tile * d.p.cols + (threadIdx.x - trow * d.p.cols);  // of fragments
-  const int lead = (threadIdx.x & 31) & ~(d.set - 1);
-  const bool mine = trow < d.p.rows && col * VW < d.C;  // uniform in a set
-  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N;
-  int64_t n = int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows + trow;
+  const TokenPlace at(d);
+  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N, first_row = int64_t(at.row) * d.p.rows;
+  int64_t n = first_row + at.trow;
+  const int lead = (threadIdx.x & 31) & ~(d.p.set - 1);
+  // one fragment: the parameters stay in registers
   float a[VW], b[VW];
-  if (mine) load_params<T, false>(gamma, beta, col * VW, 0, d.pvec, a, b);
+  if (NV == 1 && at.mine && at.has(d, 0))
+    load_params<T, false>(gamma, beta, at.channel<VW>(d, 0), 0, d.pvec, a, b);
   // every lane of a warp goes round as often as its first (the shuffles are whole warps')
-  const int rounds = static_cast<int>((n1 - (int64_t(blockIdx.x / unsigned(d.p.tiles)) * d.p.rows) + step * U - 1) /
-                                      (step * U));
+  const int rounds = static_cast<int>((n1 - first_row + step * U - 1) / (step * U));
   for (int i = 0; i < rounds; ++i, n += step * U) {
-    uint4 raw[U];
+    uint4 raw[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (mine && n + u * step < n1) raw[u] = dev::ld16_stream(x + (n + u * step) * d.C + col * VW);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (at.mine && n + u * step < n1 && at.has(d, k))
+          raw[u][k] = dev::ld16_stream(x + (n + u * step) * d.C + at.channel<VW>(d, k));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool on = mine && n + u * step < n1;
-      float v[VW];
-      if (on) {
-        dev::Conv<T>::unpack(raw[u], v);
-      } else {
+      const bool on = at.mine && n + u * step < n1;
+      float v[NV][VW];
 #pragma unroll
-        for (int e = 0; e < VW; ++e) v[e] = 0.f;
+      for (int k = 0; k < NV; ++k) {
+        if (on && at.has(d, k)) {
+          dev::Conv<T>::unpack(raw[u][k], v[k]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) v[k][e] = 0.f;
+        }
       }
-      const float first = __shfl_sync(0xffffffffu, v[0], lead);
+      const float first = __shfl_sync(0xffffffffu, v[0][0], lead);
       float s = 0.f, q = 0.f;
 #pragma unroll
-      for (int e = 0; e < VW; ++e) s += v[e] - first;
-      const float m = set_sum(s, d.set) * d.scale;
+      for (int k = 0; k < NV; ++k)
+        if (at.has(d, k))
+#pragma unroll
+          for (int e = 0; e < VW; ++e) s += v[k][e] - first;
+      const float m = set_sum(s, d.p.set) * d.scale;
       const float mu = first + m, by = m - (mu - first);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        v[e] -= mu;
-        q = fmaf(v[e], v[e], q);
-      }
-      q = set_sum(q, d.set) * d.scale;  // relative to mu, which is rounded: `by` off the mean
-      const float r = 1.0f / sqrtf(not_negative(q - by * by) + d.eps);
-      if (on) {
+      for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          v[e] = fmaf(v[e], a[e] * r, b[e]);
-          if (d.silu) v[e] = silu<T>(v[e]);
+        for (int e = 0; e < VW; ++e) v[k][e] -= mu;
+        if (at.has(d, k))
+#pragma unroll
+          for (int e = 0; e < VW; ++e) q = fmaf(v[k][e], v[k][e], q);
+      }
+      q = set_sum(q, d.p.set) * d.scale;  // relative to mu, which is rounded: `by` off the mean
+      const float r = 1.0f / sqrtf(not_negative(q - by * by) + d.eps);
+      const int64_t t = n + u * step;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (on && at.has(d, k)) {
+          if constexpr (NV > 1) load_params<T, false>(gamma, beta, at.channel<VW>(d, k), 0, d.pvec, a, b);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            v[k][e] = fmaf(v[k][e], a[e] * r, b[e]);
+            if (d.silu) v[k][e] = silu<T>(v[k][e]);
+          }
+          dev::st16_stream(y + t * d.C + at.channel<VW>(d, k), dev::Conv<T>::pack(v[k]));
         }
-        const int64_t t = n + u * step;
-        dev::st16_stream(y + t * d.C + col * VW, dev::Conv<T>::pack(v));
-        if ((threadIdx.x & 31) == lead) {
-          const int64_t g = t * d.G + col / d.set;
-          if (mean_out != nullptr) mean_out[g] = mu;
-          if (inv_out != nullptr) inv_out[g] = r;
-        }
+      }
+      if (on && at.li == 0) {
+        if (mean_out != nullptr) mean_out[t * d.G + at.g] = mu;
+        if (inv_out != nullptr) inv_out[t * d.G + at.g] = r;
       }
     }
   }
@@ -690,84 +725,101 @@ k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
 
 // The gradient; the sums for dgamma and dbeta run on in registers and leave as
 // row blockIdx / tiles of cpart: 2 x [ctas][C].
-template <typename T>
+template <typename T, int NV>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_grad_token(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                 const float* inv, T* dx, float* cpart, TokenDims d) {
   constexpr int VW = dev::Vec16<T>::N;
-  constexpr int U = 2;
-  __shared__ float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
+  constexpr int U = NV == 1 ? 2 : 1;
+  __shared__ __align__(16) float s_a[kWalkThreads * VW], s_b[kWalkThreads * VW];
   dev::pdl_wait();
   dev::pdl_trigger();
-  const int trow = threadIdx.x / unsigned(d.p.cols), tile = blockIdx.x % unsigned(d.p.tiles);
-  const int row = blockIdx.x / unsigned(d.p.tiles);
-  const int col = tile * d.p.cols + (threadIdx.x - trow * d.p.cols);
-  const bool mine = trow < d.p.rows && col * VW < d.C;
-  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N;
-  int64_t n = int64_t(row) * d.p.rows + trow;
-  float ga[VW], be[VW], tot_a[VW], tot_b[VW];
+  const TokenPlace at(d);
+  const int64_t step = int64_t(d.p.ctas) * d.p.rows, n1 = d.N, first_row = int64_t(at.row) * d.p.rows;
+  int64_t n = first_row + at.trow;
+  float ga[VW], be[VW], tot_a[NV][VW], tot_b[NV][VW];
 #pragma unroll
-  for (int e = 0; e < VW; ++e) ga[e] = be[e] = tot_a[e] = tot_b[e] = 0.f;
-  if (mine) load_params<T, false>(gamma, beta, col * VW, 0, d.pvec, ga, be);
-  const int rounds = static_cast<int>((n1 - int64_t(row) * d.p.rows + step * U - 1) / (step * U));
+  for (int e = 0; e < VW; ++e) {
+    ga[e] = be[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) tot_a[k][e] = tot_b[k][e] = 0.f;
+  }
+  if (NV == 1 && at.mine && at.has(d, 0))
+    load_params<T, false>(gamma, beta, at.channel<VW>(d, 0), 0, d.pvec, ga, be);
+  const int rounds = static_cast<int>((n1 - first_row + step * U - 1) / (step * U));
   for (int i = 0; i < rounds; ++i, n += step * U) {
-    uint4 rx[U], rd[U];
+    uint4 rx[U][NV], rd[U][NV];
     float mu[U], rs[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = n + u * step;
-      if (mine && t < n1) {
-        rx[u] = dev::ld16_stream(x + t * d.C + col * VW);
-        rd[u] = dev::ld16_stream(dy + t * d.C + col * VW);
-        mu[u] = mean[t * d.G + col / d.set];
-        rs[u] = inv[t * d.G + col / d.set];
+      if (at.mine && t < n1) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          if (at.has(d, k)) {
+            rx[u][k] = dev::ld16_stream(x + t * d.C + at.channel<VW>(d, k));
+            rd[u][k] = dev::ld16_stream(dy + t * d.C + at.channel<VW>(d, k));
+          }
+        }
+        mu[u] = mean[t * d.G + at.g];
+        rs[u] = inv[t * d.G + at.g];
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = n + u * step;
-      const bool on = mine && t < n1;
-      float h[VW], w[VW], p = 0.f, q = 0.f;
-      if (on) {
-        dev::Conv<T>::unpack(rx[u], h);
-        dev::Conv<T>::unpack(rd[u], w);
+      const bool on = at.mine && t < n1;
+      float h[NV][VW], w[NV][VW], p = 0.f, q = 0.f;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          h[e] = (h[e] - mu[u]) * rs[u];
-          if (d.silu) w[e] = silu_grad<T>(w[e], fmaf(h[e], ga[e], be[e]));
-          tot_a[e] += w[e];
-          tot_b[e] = fmaf(w[e], h[e], tot_b[e]);
-          w[e] *= ga[e];
-          p += w[e];
-          q = fmaf(w[e], h[e], q);
+      for (int k = 0; k < NV; ++k) {
+        if (on && at.has(d, k)) {
+          if constexpr (NV > 1) load_params<T, false>(gamma, beta, at.channel<VW>(d, k), 0, d.pvec, ga, be);
+          dev::Conv<T>::unpack(rx[u][k], h[k]);
+          dev::Conv<T>::unpack(rd[u][k], w[k]);
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            h[k][e] = (h[k][e] - mu[u]) * rs[u];
+            if (d.silu) w[k][e] = silu_grad<T>(w[k][e], fmaf(h[k][e], ga[e], be[e]));
+            tot_a[k][e] += w[k][e];
+            tot_b[k][e] = fmaf(w[k][e], h[k][e], tot_b[k][e]);
+            w[k][e] *= ga[e];
+            p += w[k][e];
+            q = fmaf(w[k][e], h[k][e], q);
+          }
         }
       }
-      p = set_sum(p, d.set) * d.scale;
-      q = set_sum(q, d.set) * d.scale;
-      if (on) {
+      p = set_sum(p, d.p.set) * d.scale;
+      q = set_sum(q, d.p.set) * d.scale;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) w[e] = rs[u] * ((w[e] - p) - h[e] * q);
-        dev::st16_stream(dx + t * d.C + col * VW, dev::Conv<T>::pack(w));
+      for (int k = 0; k < NV; ++k) {
+        if (on && at.has(d, k)) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e) w[k][e] = rs[u] * ((w[k][e] - p) - h[k][e] * q);
+          dev::st16_stream(dx + t * d.C + at.channel<VW>(d, k), dev::Conv<T>::pack(w[k]));
+        }
       }
     }
   }
   if (cpart == nullptr) return;
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    s_a[threadIdx.x * VW + e] = tot_a[e];
-    s_b[threadIdx.x * VW + e] = tot_b[e];
-  }
-  __syncthreads();
-  const int W = d.p.cols * VW;
-  for (int c = threadIdx.x; c < W && tile * W + c < d.C; c += blockDim.x) {
-    float sa = 0.f, sb = 0.f;
-    for (int k = 0; k < d.p.rows; ++k) {
-      sa += s_a[k * W + c];
-      sb += s_b[k * W + c];
+  for (int k = 0; k < NV; ++k) {
+    if (k > 0) __syncthreads();
+    put_entries(s_a, tot_a[k]);
+    put_entries(s_b, tot_b[k]);
+    __syncthreads();
+    const int W = d.p.cols * VW, tile0 = static_cast<int>(blockIdx.x % unsigned(d.p.tiles)) * d.tile_groups;
+    for (int i = threadIdx.x; i < W; i += blockDim.x) {
+      const int lane = i / VW, g = tile0 + (lane >> d.p.log_set), f = (lane & (d.p.set - 1)) + k * d.p.set;
+      if (g >= d.G || f >= d.frags) continue;
+      float sa = 0.f, sb = 0.f;
+      for (int r = 0; r < d.p.rows; ++r) {
+        sa += s_a[r * W + i];
+        sb += s_b[r * W + i];
+      }
+      float* out = cpart + int64_t(at.row) * d.C + (g * d.frags + f) * VW + i % VW;
+      out[0] = sa;
+      out[int64_t(d.p.ctas) * d.C] = sb;
     }
-    float* out = cpart + int64_t(row) * d.C + tile * W + c;
-    out[0] = sa;
-    out[int64_t(d.p.ctas) * d.C] = sb;
   }
 }
 
@@ -816,14 +868,16 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, 
   return p->items <= INT_MAX;
 }
 
-// The token form applies: S = 1, aligned, and a group is 1 to 32 (a power of two) lanes.
-bool token_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, TokenPlan* p, int* set) {
-  const int64_t D = C / G;
-  if (S != 1 || D % vw != 0 || D / vw > 32 || (D / vw & (D / vw - 1)) != 0) return false;
-  *set = int(D / vw);
-  const int64_t frags = C / vw;
-  p->tiles = int((frags + kWalkThreads - 1) / kWalkThreads);
-  p->cols = int((frags / *set + p->tiles - 1) / p->tiles) * *set;  // whole groups
+// The token form applies: S = 1, aligned, and a group is up to nv_max fragments on each of 32 lanes.
+bool token_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, int nv_max, TokenPlan* p) {
+  const int64_t D = C / G, frags = D / vw;
+  if (S != 1 || D % vw != 0 || frags > 32 * nv_max) return false;
+  p->set = int(std::min<int64_t>(32, pow2_at_least(frags)));
+  p->log_set = __builtin_ctz(unsigned(p->set));
+  p->nv = pow2_at_least((frags + 31) / 32);
+  const int64_t most_groups = kWalkThreads / p->set;
+  p->tiles = int((G + most_groups - 1) / most_groups);
+  p->cols = int((G + p->tiles - 1) / p->tiles) * p->set;
   p->rows = int(std::max<int64_t>(1, std::min<int64_t>(kWalkThreads / p->cols, (N + kPlanSms - 1) / kPlanSms)));
   // about 1024 threads an SM
   const int threads = (p->cols * p->rows + 31) / 32 * 32;
@@ -832,15 +886,17 @@ bool token_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, TokenPlan* p
   return true;
 }
 
-TokenDims token_dims(int64_t N, int64_t C, int64_t G, float eps, bool silu, bool pvec, const TokenPlan& p, int set) {
-  return TokenDims{N, C, int(G), set, eps, 1.0f / float(C / G), silu, pvec, p};
+TokenDims token_dims(int64_t N, int64_t C, int64_t G, float eps, bool silu, bool pvec, const TokenPlan& p, int vw) {
+  return TokenDims{N,   C,   int(G), int(C / G / vw), p.cols / p.set, eps, 1.0f / float(C / G), silu, pvec, p};
 }
 
 inline int token_threads(const TokenPlan& p) { return (p.cols * p.rows + 31) / 32 * 32; }
 
 template <typename T>
 cudaError_t token_fwd(const GroupNormArgs& a, const TokenDims& d, cudaStream_t stream, int* launches) {
-  const cudaError_t e = launch(k_gn_token<T>, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
+  auto fn = d.p.nv == 1 ? k_gn_token<T, 1> : d.p.nv == 2 ? k_gn_token<T, 2> : d.p.nv == 4 ? k_gn_token<T, 4>
+                                                                                          : k_gn_token<T, 8>;
+  const cudaError_t e = launch(fn, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
                                static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
                                static_cast<const T*>(a.beta), static_cast<T*>(a.y), a.mean, a.inv, d);
   if (e == cudaSuccess) *launches += 1;
@@ -850,7 +906,8 @@ cudaError_t token_fwd(const GroupNormArgs& a, const TokenDims& d, cudaStream_t s
 template <typename T>
 cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cpart, cudaStream_t stream,
                        int* launches) {
-  cudaError_t e = launch(k_gn_grad_token<T>, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
+  auto fn = d.p.nv == 1 ? k_gn_grad_token<T, 1> : d.p.nv == 2 ? k_gn_grad_token<T, 2> : k_gn_grad_token<T, 4>;
+  cudaError_t e = launch(fn, dim3(unsigned(d.p.tiles * d.p.ctas)), dim3(token_threads(d.p)), 0, stream,
                          static_cast<const T*>(a.dy), static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
                          static_cast<const T*>(a.beta), a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
   if (e != cudaSuccess) return e;
@@ -931,8 +988,7 @@ size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int
   const int vw = t == DType::F32 ? 4 : 8;
   size_t most = 0;
   TokenPlan tp;
-  int set;
-  if (token_plan(vw, N, S, C, G, &tp, &set)) most = size_t(tp.ctas) * size_t(C) * 8;
+  if (token_plan(vw, N, S, C, G, kGradNv, &tp)) most = size_t(tp.ctas) * size_t(C) * 8;
   for (int slab = 0; slab < 2; ++slab) {
     FusedPlan p;
     if (grad_plan(vw, N, S, C, G, slab != 0, &p))
@@ -949,10 +1005,9 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t st
   if (misalign16(a.x) != misalign16(a.y)) return cudaSuccess;
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
   TokenPlan tp;
-  int set;
-  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, &tp, &set)) {
+  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, kFwdNv, &tp)) {
     *done = true;
-    const TokenDims t = token_dims(a.N, a.C, a.G, a.eps, a.silu, pvec, tp, set);
+    const TokenDims t = token_dims(a.N, a.C, a.G, a.eps, a.silu, pvec, tp, vw);
     switch (a.t) {
       case DType::F32: return token_fwd<float>(a, t, stream, launches);
       case DType::F16: return token_fwd<__half>(a, t, stream, launches);
@@ -985,10 +1040,9 @@ cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int, cudaSt
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
   float* cpart = a.dgamma != nullptr || a.dbeta != nullptr ? static_cast<float*>(a.workspace) : nullptr;
   TokenPlan tp;
-  int set;
-  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, &tp, &set)) {
+  if (slab && token_plan(vw, a.N, a.S, a.C, a.G, kGradNv, &tp)) {
     *done = true;
-    const TokenDims t = token_dims(a.N, a.C, a.G, 0.f, a.silu, pvec, tp, set);
+    const TokenDims t = token_dims(a.N, a.C, a.G, 0.f, a.silu, pvec, tp, vw);
     switch (a.t) {
       case DType::F32: return token_grad<float>(a, t, cpart, stream, launches);
       case DType::F16: return token_grad<__half>(a, t, cpart, stream, launches);
