@@ -48,6 +48,7 @@ struct FusedPlan {
   int threads, nv;
   int rows;           // walk rows of a sample
   int reps;           // times each channel occurs in a thread's walk rows of a sample, side by side
+  bool direct;        // MODE 2, one position a sample: entries are columns, from the sample's start on
   int64_t items;      // blocks of samples
   int64_t grid_items; // the gradient: items that run at a time
 };
@@ -112,30 +113,39 @@ struct Place {
 // Sums over the entries of each (sample, group) of a block, in two steps: over
 // the repeats of each column (fragments in MODE 0, else channels), then over a
 // group's columns.  Entries are floats by position; column c of sample ns is at
-// off + c + k Cw, modulo the np positions of a sample (the positions before
-// `off` hold the channels that the last repeat misses).
+// start[ns] + c + k Cw, modulo the np positions of a sample (the positions before
+// its start hold the channels that the last repeat misses; MODE 0, 1: no starts).
+template <int MODE>
 struct Entries {
   int De, Cw, np, reps, q, slots, cols;
-  __device__ __forceinline__ Entries(const FusedPlan& p, int D, int VW, bool frags) {
-    De = frags ? D / VW : D;
-    Cw = frags ? p.cf : p.W;
-    np = p.per_sample * p.cf * (frags ? 1 : VW);
+  bool direct;
+  const int* start;
+  __device__ __forceinline__ Entries(const FusedPlan& p, int D, int VW, const int* start_) : start(start_) {
+    De = MODE == 0 ? D / VW : D;
+    Cw = MODE == 0 ? p.cf : p.W;
+    np = p.per_sample * p.cf * (MODE == 0 ? 1 : VW);
     reps = p.reps;
     q = p.W / D;
     slots = p.samples * q;
     cols = p.samples * Cw;
+    direct = MODE == 2 ? p.direct : reps == 1;
   }
   __device__ __forceinline__ int sample_of(int slot) const {
     return slots == q ? 0 : static_cast<int>(unsigned(slot) / unsigned(q));
   }
-  // The columns' sums: add(position, a, b) for each entry, into col_a (and col_b).
-  template <bool PAIR, typename OFF, typename ADD>
-  __device__ __forceinline__ void columns(float* col_a, float* col_b, OFF off_of, ADD add) const {
+  // The columns' sums, where entries are not columns already: add(position, a, b)
+  // for each entry, into col_a (and col_b).
+  template <bool PAIR, typename ADD>
+  __device__ __forceinline__ void columns(float* col_a, float* col_b, ADD add) const {
+    if (direct) return;
     sum_sets(blockDim.x, cols, reps,
              [&](int i, int k, float& a, float& b) {
                const int ns = cols == Cw ? 0 : static_cast<int>(unsigned(i) / unsigned(Cw));
-               int pos = off_of(ns) + (i - ns * Cw) + k * Cw;
-               if (pos >= np) pos -= np;
+               int pos = (i - ns * Cw) + k * Cw;
+               if constexpr (MODE == 2) {
+                 pos += start[ns];
+                 if (pos >= np) pos -= np;
+               }
                add(ns * np + pos, a, b);
              },
              [&](int i, float a, float b) {
@@ -144,28 +154,47 @@ struct Entries {
              });
     __syncthreads();
   }
-  // The groups' sums: add(slot, k, column, a, b), then done(slot, sample, a, b) by one lane.
+  // MODE 2: where sample ns's columns stand, in the entries (direct) or the columns' sums.
+  __device__ __forceinline__ int base(int ns) const { return direct ? ns * np + start[ns] : ns * Cw; }
+  // The groups' sums: add(column's place, channel (MODE 2), a, b), then done(slot,
+  // sample, a, b) by one lane.
   template <typename ADD, typename DONE>
   __device__ __forceinline__ void groups(ADD add, DONE done) const {
     sum_sets(blockDim.x, slots, De,
-             [&](int s, int k, float& a, float& b) { add(s, k, s * De + k, a, b); },  // (columns ns Cw + g De + k)
+             [&](int s, int k, float& a, float& b) {
+               if constexpr (MODE == 2) {
+                 const int ns = sample_of(s), c = (s - ns * q) * De + k;
+                 add(base(ns) + c, c, a, b);
+               } else {
+                 add(s * De + k, 0, a, b);  // (at ns Cw + g De + k, direct or not)
+               }
+             },
              [&](int s, float a, float b) { done(s, sample_of(s), a, b); });
   }
-  // Both.  `plain`: one repeat and no offset, so that entries are columns already.
-  template <bool PAIR, typename OFF, typename ADD, typename DONE>
-  __device__ __forceinline__ void run(const float* ent_a, const float* ent_b, float* col_a, float* col_b, bool plain,
-                                      OFF off_of, ADD add, DONE done) const {
-    if (!plain) columns<PAIR>(col_a, col_b, off_of, add);
-    const float* ca = plain ? ent_a : col_a;
-    const float* cb = plain ? ent_b : col_b;
+  // Both.
+  template <bool PAIR, typename ADD, typename DONE>
+  __device__ __forceinline__ void run(const float* ent_a, const float* ent_b, float* col_a, float* col_b, ADD add,
+                                      DONE done) const {
+    columns<PAIR>(col_a, col_b, add);
+    const float* ca = direct ? ent_a : col_a;
+    const float* cb = direct ? ent_b : col_b;
     groups(
-        [&](int, int, int c, float& a, float& b) {
-          a += ca[c];
-          if constexpr (PAIR) b += cb[c];
+        [&](int i, int, float& a, float& b) {
+          a += ca[i];
+          if constexpr (PAIR) b += cb[i];
         },
         done);
   }
 };
+
+// Where each sample of an item starts in its first fragment, by the first threads.
+template <typename T>
+__device__ __forceinline__ void put_starts(int* start, const FusedDims& d, const T* x, unsigned item) {
+  if (int(threadIdx.x) < d.p.samples) {
+    const int64_t n = int64_t(item) * d.p.samples + threadIdx.x;
+    start[threadIdx.x] = n < d.N ? dev::misalignment(x + n * d.L) : 0;
+  }
+}
 
 // gamma and beta of VW channels from c on (modulo W).
 template <typename T, bool WRAP>
@@ -255,6 +284,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float* gm = col_n + (MODE == 2 ? cols : 0);
   float* gr = gm + slots;
   float* gf = gr + slots;                                        // the groups' first values
+  int* start = reinterpret_cast<int*>(gf + slots);               // MODE 2: the samples' starts
   const unsigned item = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
@@ -268,6 +298,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   for (int k = 0; k < NV; ++k)
     if (k < at.kn) raw[k] = at.load(xs, k);
 
+  if constexpr (MODE == 2) put_starts(start, d, x, item);
   for (int s = threadIdx.x; s < slots; s += blockDim.x) {
     const int sn = p.samples == 1 ? 0 : s / unsigned(d.G);
     const int64_t sample = int64_t(item) * p.samples + sn;
@@ -285,12 +316,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   });
 
   const bool mine = trow < p.phases;
-  const Entries entries(p, d.D, VW, MODE == 0);
-  const bool plain = MODE != 2 && entries.reps == 1;
+  const Entries<MODE> entries(p, d.D, VW, start);
   const int64_t n0 = int64_t(item) * p.samples;
-  auto off_of = [&](int s) {
-    return MODE == 2 && n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0;
-  };
   const float total = float(d.S) * float(d.D);
 
   float m[EV], s[EV];
@@ -311,8 +338,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     }
   }
   __syncthreads();
-  entries.run<MODE == 2>(
-             ent, cnt, col, col_n, plain, off_of,
+  entries.template run<MODE == 2>(
+             ent, cnt, col, col_n,
              [&](int i, float& a, float& b) {
                a += ent[i];
                if constexpr (MODE == 2) b += cnt[i];
@@ -335,8 +362,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     put_entries(ent, s);
   }
   __syncthreads();
-  entries.run<false>(
-             ent, cnt, col, col_n, plain, off_of, [&](int i, float& a, float&) { a += ent[i]; },
+  entries.template run<false>(
+             ent, cnt, col, col_n, [&](int i, float& a, float&) { a += ent[i]; },
              [&](int s, int ns, float a, float) {
                const float r = 1.0f / sqrtf(not_negative(a - gr[s]) / total + d.eps);
                gr[s] = r;
@@ -397,12 +424,13 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float* ch_a = g2 + slots;  // MODE 2: the channels' sums, and gamma
   float* ch_b = ch_a + p.W;
   float* ch_g = ch_b + p.W;
+  int* start = reinterpret_cast<int*>(ch_g + p.W);
   const unsigned first = blockIdx.x;
   const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
   const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
   const bool mine = trow < p.phases;
   const float scale = 1.0f / (float(d.S) * float(d.D));
-  const Entries entries(p, d.D, VW, MODE == 0);
+  const Entries<MODE> entries(p, d.D, VW, start);
   dev::pdl_wait();
   dev::pdl_trigger();
 
@@ -420,6 +448,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   }
 
   for (unsigned item = first; item < unsigned(p.items); item += unsigned(p.grid_items)) {
+    if constexpr (MODE == 2) put_starts(start, d, x, item);
     const Place<T, MODE> at(d, x, item, trow, tcol, ns);
     const int64_t base = at.kn > 0 ? at.n * d.L : 0;
     uint4 raw[NV], rdy[NV];
@@ -517,25 +546,24 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       b += ent_b[i];
     };
     if constexpr (MODE != 2) {
-      entries.template run<true>(ent_a, ent_b, col_a, col_b, entries.reps == 1, [](int) { return 0; }, entry, means);
+      entries.template run<true>(ent_a, ent_b, col_a, col_b, entry, means);
     } else {
-      const int64_t n0 = int64_t(item) * p.samples;
-      entries.columns<true>(
-          col_a, col_b, [&](int s) { return n0 + s < d.N ? dev::misalignment(x + (n0 + s) * d.L) : 0; }, entry);
+      entries.template columns<true>(col_a, col_b, entry);
+      const float* ca = entries.direct ? ent_a : col_a;
+      const float* cb = entries.direct ? ent_b : col_b;
       for (int c = threadIdx.x; c < p.W; c += blockDim.x) {
         float a = ch_a[c], b = ch_b[c];
         for (int s = 0; s < p.samples; ++s) {
-          a += col_a[s * p.W + c];
-          b += col_b[s * p.W + c];
+          a += ca[entries.base(s) + c];
+          b += cb[entries.base(s) + c];
         }
         ch_a[c] = a;
         ch_b[c] = b;
       }
       entries.groups(
-          [&](int s, int, int c, float& a, float& b) {
-            const float g = ch_g[c - (entries.sample_of(s) * p.W)];
-            a = fmaf(col_a[c], g, a);
-            b = fmaf(col_b[c], g, b);
+          [&](int i, int c, float& a, float& b) {
+            a = fmaf(ca[i], ch_g[c], a);
+            b = fmaf(cb[i], ch_g[c], b);
           },
           means);
     }
@@ -859,6 +887,7 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, 
   const int64_t fit = std::max(1, phases / p->per_sample);
   p->samples = int(std::max<int64_t>(1, std::min(fit, N / (2 * kPlanSms))));
   p->phases = p->samples * p->per_sample;
+  p->direct = !slab && S == 1 && period == all;
   // (a walk row that is the sample has its S positions, one that is a period as many as fit)
   p->reps = slab ? p->per_sample : rows == 1 && period == all ? int(S) : int(p->per_sample * period * vw / C);
   p->threads = (p->phases * p->cf + 31) / 32 * 32;
@@ -929,7 +958,7 @@ size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
   const size_t cols = size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
   const size_t channels = grad && mode == 2 ? 3 * size_t(p.W) : 0;
-  return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels);
+  return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels + (mode == 2 ? p.samples : 0));
 }
 constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
 
