@@ -1701,13 +1701,25 @@ constexpr int kGeneralCtas = 8;
 
 int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
-GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps) {
+// `periods`: walk rows are whole periods of the channels, as the gradient's channel
+// sums want them; else a sample shorter than a period is a walk row by itself.
+GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, bool periods) {
   GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, 0, {}};
   d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
   d.ctas = kPlanSms * 2;
   if (d.p.tiles > 1 && C % vec_width(t) != 0) {  // the general kernels: no stages, so more blocks an SM
     d.ctas = kPlanSms * kGeneralCtas;
     d.p = make_walk(d.L, C, int(vec_width(t)), N, d.ctas, 4);
+    const int64_t all = (d.L + 2 * (vec_width(t) - 1)) / vec_width(t);
+    if (!periods && all < d.p.row_frags && all > kWalkThreads) {
+      // (f16 5000x1x5001: 3267 us to 499)
+      d.p.row_frags = all;
+      d.p.tiles = int((all + kWalkThreads - 1) / kWalkThreads);
+      d.p.tile_frags = int((all + d.p.tiles - 1) / d.p.tiles);
+      d.p.threads = (d.p.tile_frags + 31) / 32 * 32;
+      d.p.rows = d.p.rows_per_chunk = 1;
+      d.p.chunks = 1;
+    }
   }
   d.frags = d.L / vec_width(t);
   d.full_rows = d.frags / d.p.row_frags;
@@ -1789,7 +1801,7 @@ cudaError_t launch_plain(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cu
 template <typename T>
 cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launches) {
   constexpr int VW = dev::Vec16<T>::N;
-  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps);
+  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, a.eps, false);
   d.pvec = a.C % VW == 0 && misalign16(a.x) == 0 && misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   const GnWorkspace w = gn_workspace(d);
   char* ws = static_cast<char*>(a.workspace);
@@ -1846,7 +1858,7 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   constexpr int VW = dev::Vec16<T>::N;
   // shared memory of the sums: by position and by channel (staged), or the totals (general)
   constexpr size_t kStagedSums = size_t(kWalkThreads) * VW * 16, kTotals = size_t(kWalkThreads) * VW * 8;
-  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f);
+  GnDims d = dims_of(a.t, a.N, a.S, a.C, a.G, 0.f, true);
   d.pvec = a.C % VW == 0 && misalign16(a.x) == 0 && misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   const GnGradWorkspace w = gn_grad_workspace(d, a.t);
   char* ws = static_cast<char*>(a.workspace);
@@ -1911,7 +1923,7 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
 
 // The token form: the tensor as one sample of N positions, tiles of whole groups.
 GnDims token_dims(DType t, int64_t N, int64_t C, int64_t G, float eps) {
-  GnDims d = dims_of(t, 1, N, C, G, eps);
+  GnDims d = dims_of(t, 1, N, C, G, eps, true);
   const int set = int(d.D / vec_width(t));
   d.p = make_walk(d.L, C, int(vec_width(t)), 1, kPlanSms * 2, 4);
   d.p.tile_frags = (d.p.tile_frags + set - 1) / set * set;
@@ -1975,11 +1987,11 @@ cudaError_t token_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* l
 }  // namespace
 
 size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
-  return gn_workspace(dims_of(t, N, S, C, G, 0.f)).total;
+  return gn_workspace(dims_of(t, N, S, C, G, 0.f, false)).total;
 }
 
 size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
-  size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f), t).total,
+  size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f, true), t).total,
                          group_norm_grad_fused_bytes(t, N, S, C, G));
   if (token_staged(t, N, S, C, G, kTokenGradStagedBytes))
     most = std::max(most, size_t(token_rows(token_grad_dims(t, N, C, G))) * size_t(C) * 8);

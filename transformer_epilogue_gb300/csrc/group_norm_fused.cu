@@ -279,7 +279,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float* ent = smem;
   float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
   float* col = cnt + (MODE == 2 ? ents : 0);                     // sums by column, and their counts
-  const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
+  const int cols = MODE == 2 && p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_n = col + cols;
   float* gm = col_n + (MODE == 2 ? cols : 0);
   float* gr = gm + slots;
@@ -416,7 +416,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   const int slots = p.samples * d.G, ents = p.phases * p.cf * VW;
   float* ent_a = smem;
   float* ent_b = ent_a + ents;
-  const int cols = p.samples * (MODE == 0 ? p.cf : p.W);
+  const int cols = MODE == 2 && p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_a = ent_b + ents;
   float* col_b = col_a + cols;
   float* g1 = col_b + cols;
@@ -956,11 +956,24 @@ cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cp
 size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
   const size_t slots = size_t(p.samples) * G, frags = size_t(p.phases) * p.cf;
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
-  const size_t cols = size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
+  const size_t cols =
+      mode == 2 && p.direct ? 0 : size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
   const size_t channels = grad && mode == 2 ? 3 * size_t(p.W) : 0;
   return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels + (mode == 2 ? p.samples : 0));
 }
-constexpr size_t kSmemMost = 48 * 1024;  // what a launch may have without opting in
+constexpr size_t kSmemMost = 96 * 1024;  // two blocks an SM
+
+// Blocks of more than 48 KB ask for it first.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_fused(void (*fn)(KArgs...), unsigned blocks, int threads, size_t smem, cudaStream_t stream,
+                         Args... args) {
+  int per_sm = 1;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+  }
+  return launch(fn, dim3(blocks), dim3(threads), smem, stream, args...);
+}
 
 template <typename T, int MODE>
 cudaError_t fused_fwd(const GroupNormArgs& a, const FusedDims& d, cudaStream_t stream, int* launches) {
@@ -969,8 +982,8 @@ cudaError_t fused_fwd(const GroupNormArgs& a, const FusedDims& d, cudaStream_t s
             : p.nv == 2 ? k_gn_fused<T, 2, MODE>
             : p.nv == 4 ? k_gn_fused<T, 4, MODE>
                         : k_gn_fused<T, 8, MODE>;
-  const cudaError_t e = launch(fn, dim3(unsigned(p.items)), dim3(p.threads),
-                               fused_smem(p, MODE, dev::Vec16<T>::N, a.G, false), stream,
+  const cudaError_t e = launch_fused(fn, unsigned(p.items), p.threads,
+                                     fused_smem(p, MODE, dev::Vec16<T>::N, a.G, false), stream,
                                static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
                                static_cast<const T*>(a.beta), static_cast<T*>(a.y), a.mean, a.inv, d);
   if (e == cudaSuccess) *launches += 1;
@@ -984,8 +997,8 @@ cudaError_t fused_grad(const GroupNormGradArgs& a, const FusedDims& d, float* cp
   auto fn = p.nv == 1   ? k_gn_grad_fused<T, 1, MODE>
             : p.nv == 2 ? k_gn_grad_fused<T, 2, MODE>
                         : k_gn_grad_fused<T, 4, MODE>;
-  cudaError_t e = launch(fn, dim3(unsigned(p.grid_items)), dim3(p.threads),
-                         fused_smem(p, MODE, dev::Vec16<T>::N, a.G, true), stream, static_cast<const T*>(a.dy),
+  cudaError_t e = launch_fused(fn, unsigned(p.grid_items), p.threads,
+                               fused_smem(p, MODE, dev::Vec16<T>::N, a.G, true), stream, static_cast<const T*>(a.dy),
                          static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta),
                          a.mean, a.inv, static_cast<T*>(a.dx), cpart, d);
   if (e != cudaSuccess) return e;
