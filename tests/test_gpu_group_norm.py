@@ -27,7 +27,7 @@ SHAPES = [
     # many small samples, several to a block or one block after another, that start anywhere
     ((700, 1, 76), 4), ((650, 3, 27), 9), ((400, 2, 675), 3), ((1100, 5, 117), 9), ((333, 1, 744), 8),
     ((900, 1, 2976), 32), ((310, 8, 4), 4), ((500, 2, 384), 64), ((2000, 2, 1), 1), ((160, 1, 4095), 5),
-    ((77, 9, 1044), 9), ((40, 1, 5001), 3), ((400, 1, 1827), 9), ((200, 2, 3999), 3), ((3, 2, 5001), 1), ((2, 401, 1530), 9), ((1, 2500, 1044), 9), ((3, 700, 747), 9),
+    ((77, 9, 1044), 9), ((40, 1, 5001), 3), ((400, 1, 1827), 9), ((200, 2, 3999), 3), ((300, 1, 2295), 9), ((500, 1, 8160), 32), ((180, 1, 7999), 1), ((3, 2, 5001), 1), ((2, 401, 1530), 9), ((1, 2500, 1044), 9), ((3, 700, 747), 9),
     ((1, 70000, 64), 4), ((2, 30011, 33), 3), ((1, 300, 12288), 32),  # large samples
 ]
 

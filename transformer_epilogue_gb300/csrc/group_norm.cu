@@ -11,13 +11,25 @@
 //   m1 = mean(du * gamma), m2 = mean(du * gamma * h)                    per (n, g)
 //   dx = r (du * gamma - m1 - h m2)
 //
-// Split form (this file's general path, any C, S and alignment): the walk of
-// column_walk.cuh over each sample.  Pass 1 leaves (count, mean, sum of squared
-// distances) per chunk and group, a small kernel joins the chunks, pass 2 reads
-// x again (from L2 where it fits) and writes y.  The statistics are taken
-// relative to values near their mean throughout, so that a large mean costs the
-// variance nothing.  The gradient has the same three steps, with per-channel sums of du
-// and du * h beside the groups' sums.
+// Five forms, in the order in which they are tried:
+//   staged tokens (here)    S = 1, groups of 1, 2, 4 ... 32 fragments, from 1 MB (the
+//                           gradient 2 MB) on: one launch at the copy rate's 75 %
+//                           (bf16 8192x1x4096 27 us; the gradient 8192x1x2048 25.8)
+//   tokens                  group_norm_fused.cu: S = 1, groups of whole fragments
+//   fused                   group_norm_fused.cu: a sample fits a block's registers
+//   staged split (here)     any other size with 16-byte-aligned tensors whose channels
+//                           repeat within a block's 256 fragments (or C % VW == 0)
+//   general split (here)    everything else
+// The split forms walk each sample as column_walk.cuh describes.  Pass 1 leaves
+// (count, mean, sum of squared distances) per chunk and group, a small kernel (or
+// pass 2 itself) joins the chunks, pass 2 reads x again, from L2 where it fits, and
+// writes y.  The statistics are taken relative to values near their mean
+// throughout, so that a large mean costs the variance nothing.  The gradient has
+// the same three steps, with per-channel sums of du and du * h beside the groups'.
+// A split form's floor is three reads and writes, not two, where x is larger than
+// L2: bf16 8x16384x512 (134 MB) takes 64 us, 60 at the copy rate; small ones are
+// bound by the latency of their launches (f16 2x4096x320 10.1 us, of which 1.6 are
+// its bytes).
 //
 // All sums and statistics are float32; results are rounded once, to T.
 #include <algorithm>
@@ -464,12 +476,15 @@ struct GradApplyValues : GradValues<T, EV, SILU> {
 };
 
 // ---------------------------------------------------------------------------
-// Staged walk rows (C % VW == 0, 16-byte-aligned operands: every fragment is
-// whole, and a sample's last walk row may be shorter): a producer thread bulk-copies the rows
-// of its CTA's items into a ring of shared-memory stages, the consumers (one to
-// a fragment column) read them from there.  The copies in flight cost no
-// registers: measured against loads into registers, where two CTAs an SM had
-// 32 KB in flight, the passes take less than half the time.
+// Staged walk rows (16-byte-aligned operands): a producer thread bulk-copies the
+// rows of its CTA's items into a ring of shared-memory stages, the consumers (one to
+// a fragment column) read them from there.  C % VW == 0: every fragment is whole,
+// and a sample's last walk row may be shorter.  ODD, any other C whose period is one
+// tile: samples start anywhere in a fragment, and the two partial fragments of a
+// sample are read and written value by value (f16 3x13310x189 18 us; 36 with the
+// general kernels).  The copies in flight cost no registers: with loads into
+// registers two CTAs an SM had 32 KB in flight, and the passes took twice the time.
+// Two stages of 32 KB and two CTAs an SM were best; three CTAs gave nothing.
 // Stages are handed over by mbarriers (tma_pipe.cuh), with bounded waits; a
 // consumer whose wait ran out takes no more rows but stays in step with the
 // block's barriers.

@@ -20,7 +20,10 @@
 // pass over the registers.  All in float32, in an order that does not depend on
 // timing.
 //
-// What bounds it: the latency of load, two block reductions and store.  (Spreading
+// What bounds it: the latency of load, two block reductions and store (f16 1x64x256
+// 5.7 us, 76 such samples 5.9, 300 8.3; as a split form 7.7, 10.2 and 16.4).  Where
+// there are thousands of samples, the instructions of MODE 1 and 2 (bf16 9668x1x2976
+// in groups of 93 177 us, of which 18 are its bytes).  (Spreading
 // a larger sample over a cluster of up to 16 blocks, with the groups' sums in
 // distributed shared memory, was built and measured: 7.0 us against the split
 // form's 8.6 for f16 2x256x1280, but 20.7 against 11.0 for 2x4096x320 and 156
@@ -39,7 +42,7 @@
 namespace ep {
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 512, kWideThreads = 1024;  // kWideThreads: samples of one walk row
 
 struct FusedPlan {
   int W;              // channels: C
@@ -48,7 +51,7 @@ struct FusedPlan {
   int threads, nv;
   int rows;           // walk rows of a sample
   int reps;           // times each channel occurs in a thread's walk rows of a sample, side by side
-  bool direct;        // MODE 2, one position a sample: entries are columns, from the sample's start on
+  bool direct;        // entries are columns: one repeat (MODE 2: and one position a sample)
   int64_t items;      // blocks of samples
   int64_t grid_items; // the gradient: items that run at a time
 };
@@ -128,7 +131,7 @@ struct Entries {
     q = p.W / D;
     slots = p.samples * q;
     cols = p.samples * Cw;
-    direct = MODE == 2 ? p.direct : reps == 1;
+    direct = p.direct;
   }
   __device__ __forceinline__ int sample_of(int slot) const {
     return slots == q ? 0 : static_cast<int>(unsigned(slot) / unsigned(q));
@@ -267,8 +270,8 @@ __device__ __forceinline__ void centred_sums(const uint4 (&raw)[NV], const Place
   }
 }
 
-template <typename T, int NV, int MODE>
-__global__ void __launch_bounds__(kMaxThreads)
+template <typename T, int NV, int MODE, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, T* y, float* mean_out,
            float* inv_out, FusedDims d) {
   constexpr int VW = dev::Vec16<T>::N;
@@ -279,7 +282,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   float* ent = smem;
   float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
   float* col = cnt + (MODE == 2 ? ents : 0);                     // sums by column, and their counts
-  const int cols = MODE == 2 && p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
+  const int cols = p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_n = col + cols;
   float* gm = col_n + (MODE == 2 ? cols : 0);
   float* gr = gm + slots;
@@ -405,8 +408,8 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
 // of du and du * h of its channels over them, in registers or (MODE 2, where a
 // thread's channels change with the sample's start) in shared memory; they leave
 // once, as row blockIdx of cpart: 2 x [row][C].
-template <typename T, int NV, int MODE>
-__global__ void __launch_bounds__(kMaxThreads)
+template <typename T, int NV, int MODE, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                 const float* inv, T* dx, float* cpart, FusedDims d) {
   constexpr int VW = dev::Vec16<T>::N;
@@ -416,7 +419,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   const int slots = p.samples * d.G, ents = p.phases * p.cf * VW;
   float* ent_a = smem;
   float* ent_b = ent_a + ents;
-  const int cols = MODE == 2 && p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
+  const int cols = p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
   float* col_a = ent_b + ents;
   float* col_b = col_a + cols;
   float* g1 = col_b + cols;
@@ -870,10 +873,10 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, 
   if (slab && C % vw != 0) return false;
   const int64_t all = (S * C + 2 * (vw - 1)) / vw;  // of a sample, wherever it starts
   const int64_t period = slab ? C / vw : std::min(C / std::gcd(C, int64_t(vw)), all);
-  if (period > kMaxThreads) return false;
+  const int64_t rows = slab ? S : (all + period - 1) / period;
+  if (period > (rows == 1 ? kWideThreads : kMaxThreads)) return false;
   p->W = int(C);
   p->cf = int(period);
-  const int64_t rows = slab ? S : (all + period - 1) / period;
   const int64_t frags = rows * period;
   if (frags > int64_t(kMaxThreads) * nv_max) return false;
   p->rows = int(rows);
@@ -887,7 +890,7 @@ bool fused_plan(int vw, int64_t N, int64_t S, int64_t C, bool slab, int nv_max, 
   const int64_t fit = std::max(1, phases / p->per_sample);
   p->samples = int(std::max<int64_t>(1, std::min(fit, N / (2 * kPlanSms))));
   p->phases = p->samples * p->per_sample;
-  p->direct = !slab && S == 1 && period == all;
+  p->direct = slab ? p->per_sample == 1 : S == 1 && period == all;
   // (a walk row that is the sample has its S positions, one that is a period as many as fit)
   p->reps = slab ? p->per_sample : rows == 1 && period == all ? int(S) : int(p->per_sample * period * vw / C);
   p->threads = (p->phases * p->cf + 31) / 32 * 32;
@@ -957,11 +960,12 @@ size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
   const size_t slots = size_t(p.samples) * G, frags = size_t(p.phases) * p.cf;
   const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
   const size_t cols =
-      mode == 2 && p.direct ? 0 : size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
+      p.direct ? 0 : size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
   const size_t channels = grad && mode == 2 ? 3 * size_t(p.W) : 0;
   return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels + (mode == 2 ? p.samples : 0));
 }
-constexpr size_t kSmemMost = 96 * 1024;  // two blocks an SM
+// Two blocks an SM, or one where a block has more threads.
+constexpr size_t smem_most(const FusedPlan& p) { return (p.threads > kMaxThreads ? 200 : 96) * 1024; }
 
 // Blocks of more than 48 KB ask for it first.
 template <typename... KArgs, typename... Args>
@@ -978,10 +982,11 @@ cudaError_t launch_fused(void (*fn)(KArgs...), unsigned blocks, int threads, siz
 template <typename T, int MODE>
 cudaError_t fused_fwd(const GroupNormArgs& a, const FusedDims& d, cudaStream_t stream, int* launches) {
   const FusedPlan& p = d.p;
-  auto fn = p.nv == 1   ? k_gn_fused<T, 1, MODE>
-            : p.nv == 2 ? k_gn_fused<T, 2, MODE>
-            : p.nv == 4 ? k_gn_fused<T, 4, MODE>
-                        : k_gn_fused<T, 8, MODE>;
+  auto fn = p.threads > kMaxThreads ? k_gn_fused<T, 1, MODE, kWideThreads>
+            : p.nv == 1             ? k_gn_fused<T, 1, MODE, kMaxThreads>
+            : p.nv == 2             ? k_gn_fused<T, 2, MODE, kMaxThreads>
+            : p.nv == 4             ? k_gn_fused<T, 4, MODE, kMaxThreads>
+                                    : k_gn_fused<T, 8, MODE, kMaxThreads>;
   const cudaError_t e = launch_fused(fn, unsigned(p.items), p.threads,
                                      fused_smem(p, MODE, dev::Vec16<T>::N, a.G, false), stream,
                                static_cast<const T*>(a.x), static_cast<const T*>(a.gamma),
@@ -994,9 +999,11 @@ template <typename T, int MODE>
 cudaError_t fused_grad(const GroupNormGradArgs& a, const FusedDims& d, float* cpart, cudaStream_t stream,
                        int* launches) {
   const FusedPlan& p = d.p;
-  auto fn = p.nv == 1   ? k_gn_grad_fused<T, 1, MODE>
-            : p.nv == 2 ? k_gn_grad_fused<T, 2, MODE>
-                        : k_gn_grad_fused<T, 4, MODE>;
+  auto fn = p.nv == 1   ? k_gn_grad_fused<T, 1, MODE, kMaxThreads>
+            : p.nv == 2 ? k_gn_grad_fused<T, 2, MODE, kMaxThreads>
+                        : k_gn_grad_fused<T, 4, MODE, kMaxThreads>;
+  if constexpr (sizeof(T) == 4)
+    if (p.threads > kMaxThreads) fn = k_gn_grad_fused<T, 1, MODE, kWideThreads>;
   cudaError_t e = launch_fused(fn, unsigned(p.grid_items), p.threads,
                                fused_smem(p, MODE, dev::Vec16<T>::N, a.G, true), stream, static_cast<const T*>(a.dy),
                          static_cast<const T*>(a.x), static_cast<const T*>(a.gamma), static_cast<const T*>(a.beta),
@@ -1019,9 +1026,12 @@ constexpr int kFwdNv = 8, kGradNv = 4;
 
 bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, FusedPlan* p) {
   if (!fused_plan(vw, N, S, C, slab, kGradNv, p)) return false;
+  // (8 values a thread do not fit the 64 registers of a wide block's threads: f16 3000x1x8160
+  // 531 us, and 339 in the split form; f32 3000x1x2295 82, and 338)
+  if (p->threads > kMaxThreads && vw != 4) return false;
   // items that run at a time: about 1024 threads an SM
   p->grid_items = std::min<int64_t>(p->items, kPlanSms * std::max(1, 1024 / p->threads));
-  return fused_smem(*p, slab ? 1 : 2, vw, G, true) <= kSmemMost;  // (mode 0 needs less)
+  return fused_smem(*p, slab ? 1 : 2, vw, G, true) <= smem_most(*p);  // (mode 0 needs less)
 }
 
 }  // namespace
@@ -1058,7 +1068,7 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t st
   }
   if (!fused_plan(vw, a.N, a.S, a.C, slab, kFwdNv, &d.p)) return cudaSuccess;
   const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
-  if (fused_smem(d.p, mode, vw, a.G, false) > kSmemMost) return cudaSuccess;
+  if (fused_smem(d.p, mode, vw, a.G, false) > smem_most(d.p)) return cudaSuccess;
   *done = true;
 #define EP_GN_FUSED(T)                                                          \
   (mode == 0   ? fused_fwd<T, 0>(a, d, stream, launches)                        \
