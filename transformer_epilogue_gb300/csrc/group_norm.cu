@@ -1598,8 +1598,8 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 }
 
 // ---------------------------------------------------------------------------
-// Joining a group's chunks and tiles.  THREADS (a warp, or a block where there
-// are many parts) take one (n, g); bound by the latency of a few reads.
+// Joining a group's chunks and tiles: a warp takes one (n, g); bound by the latency
+// of a few reads.
 //
 // The joins let pass 2 launch before they wait for pass 1: pass 1 has seen the
 // call's predecessors end before a join starts, so the inputs are there for pass
@@ -1608,20 +1608,6 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 64;
-
-template <int THREADS>
-__device__ __forceinline__ float join_sum(float x, float* red) {
-  x = dev::warp_sum(x);
-  if constexpr (THREADS > 32) {
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.f;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) x += red[w];
-  }
-  return x;
-}
 
 // (count, mean, M2) of the parts -> the group's statistics: a warp for each
 // (n, g), which keeps up to kJoinKept parts a lane in registers for the second
@@ -1677,33 +1663,32 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
 
 // The gradient's sums of the parts -> m1, m2 of each (n, g); and, in the blocks
 // after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
-template <typename T, int THREADS>
+template <typename T>
 __global__ void __launch_bounds__(kSumsThreads)
 k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
                int64_t reps, T* dbeta, T* dgamma) {
-  __shared__ float red[kSumsThreads / 32];
   dev::pdl_trigger();
   dev::pdl_wait();
   if (int(blockIdx.x) >= join_blocks) {
     channel_sums<T>(cpart, rows, reps, d.C, 2, dbeta, dgamma, blockIdx.x - join_blocks, gridDim.x - join_blocks);
     return;
   }
-  const int t = threadIdx.x % THREADS;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kSumsThreads / THREADS;
+  const int lane = threadIdx.x & 31;
+  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kSumsThreads / 32;
   const float scale = 1.0f / (float(d.S) * float(d.D));
-  for (int64_t i = int64_t(blockIdx.x) * per + threadIdx.x / THREADS; i < d.N * d.G; i += int64_t(join_blocks) * per) {
+  for (int64_t i = int64_t(threadIdx.x / 32) * join_blocks + blockIdx.x; i < d.N * d.G; i += join_blocks * per) {
     const int64_t n = quotient(i, d.G);
     const float2* src = reinterpret_cast<const float2*>(gpart) + n * parts * d.G + (i - n * d.G);
     float a = 0.f, b = 0.f;
-#pragma unroll 4
-    for (int64_t k = t; k < parts; k += THREADS) {
+#pragma unroll 8
+    for (int64_t k = lane; k < parts; k += 32) {
       const float2 v = __ldcg(src + k * d.G);
       a += v.x;
       b += v.y;
     }
-    a = join_sum<THREADS>(a, red);
-    b = join_sum<THREADS>(b, red);
-    if (t == 0) {
+    a = dev::warp_sum(a);
+    b = dev::warp_sum(b);
+    if (lane == 0) {
       m1[i] = a * scale;
       m2[i] = b * scale;
     }
@@ -1911,13 +1896,10 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   }
   if (e != cudaSuccess) return e;
   // joining the groups' parts and adding up the channels in one launch
-  const bool by_block = int64_t(d.p.chunks) * d.p.tiles > 64;
-  const int64_t per = by_block ? 1 : kSumsThreads / 32;
-  const int64_t joins = std::min<int64_t>((d.N * d.G + per - 1) / per, kPlanSms * 4);
+  const int64_t joins = std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms);
   const int64_t sums = cpart != nullptr ? std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, kPlanSms * 4) : 0;
-  auto join = by_block ? k_gn_grad_join<T, kSumsThreads> : k_gn_grad_join<T, 32>;
   // (the sums of du are dbeta, those of du * h are dgamma)
-  e = launch(join, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, gpart, d, m1, m2, int(joins), cpart,
+  e = launch(k_gn_grad_join<T>, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, gpart, d, m1, m2, int(joins), cpart,
              rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
   if (e != cudaSuccess) return e;
   *launches += 1;
