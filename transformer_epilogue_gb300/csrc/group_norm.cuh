@@ -167,6 +167,11 @@ __device__ __forceinline__ void sum_sets(int threads, int n, int terms, VAL val,
   }
 }
 
+// The median of three values: no single outlier moves it.
+__device__ __forceinline__ float median3(float a, float b, float c) {
+  return fmaxf(fminf(a, b), fminf(fmaxf(a, b), c));
+}
+
 // A sum of squares that rounding took below zero is 0 (and NaN stays NaN).
 __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : q; }
 

@@ -15,15 +15,17 @@
 // there are many.  (Blocks that take several sets of samples in turn, parameters
 // kept, lost: f16 300x48x256 7.7 us to 10.8.)
 //
-// Statistics: values are taken relative to their group's first value, summed,
-// and the squares of their distances from the group's mean summed in a second
-// pass over the registers.  All in float32, in an order that does not depend on
-// timing.
+// Statistics: sums and sums of squares of the distances from a centre of the group,
+// the median of three of its values (the first, a middle, the last), so that no
+// single outlier moves it: k standard deviations off the mean it costs the variance
+// k^2 2^-24 of its value.  All in float32, in an order that does not depend on
+// timing.  (The squares about the mean, as a second pass over the registers, took two
+// more block sums: f16 1x64x256 5.7 us and 4.7, f32 9651x2x459 122 and 68.)
 //
 // What bounds it: the latency of load, two block reductions and store (f16 1x64x256
-// 5.7 us, 76 such samples 5.9, 300 8.3; as a split form 7.7, 10.2 and 16.4).  Where
+// 4.7 us, 76 such samples 4.7, 300 6.6; as a split form 7.7, 10.2 and 16.4).  Where
 // there are thousands of samples, the instructions of MODE 1 and 2 (bf16 9668x1x2976
-// in groups of 93 177 us, of which 18 are its bytes).  (Spreading
+// in groups of 93 118 us, of which 18 are its bytes).  (Spreading
 // a larger sample over a cluster of up to 16 blocks, with the groups' sums in
 // distributed shared memory, was built and measured: 7.0 us against the split
 // form's 8.6 for f16 2x256x1280, but 20.7 against 11.0 for 2x4096x320 and 156
@@ -57,9 +59,9 @@ struct FusedPlan {
 };
 
 struct FusedDims {
-  int64_t N, S, L;
+  int64_t N, S, L;  // (a sample that fits a block has less than 2^31 elements)
   int C, G, D;
-  float eps;
+  float eps, scale;   // scale: 1 / (S D)
   bool silu;
   bool pvec;          // gamma and beta 16-byte aligned
   FusedPlan p;
@@ -69,12 +71,12 @@ struct FusedDims {
 template <typename T, int MODE>
 struct Place {
   static constexpr int VW = dev::Vec16<T>::N;
-  int64_t n;       // its sample
-  int64_t e0;      // its first fragment's first element, from the sample's start
-  int64_t stride;  // elements from one of its fragments to the next
-  int64_t lim;     // MODE 2: elements of the sample
+  int64_t n;   // its sample
+  int e0;      // its first fragment's first element, from the sample's start
+  int stride;  // elements from one of its fragments to the next
+  int lim;     // MODE 2: elements of the sample
   int off;
-  int kn;          // its fragments
+  int kn;      // its fragments
 
   __device__ __forceinline__ Place(const FusedDims& d, const T* x, unsigned item, int trow, int tcol, int ns) {
     const FusedPlan& p = d.p;
@@ -82,36 +84,50 @@ struct Place {
     n = int64_t(item) * p.samples + ns;
     const bool live = trow < p.phases && n < d.N;
     off = MODE == 2 && live ? dev::misalignment(x + n * d.L) : 0;
-    const int64_t row = int64_t(p.cf) * VW;  // (C where C % VW == 0)
-    kn = live && ph < p.rows ? (p.rows - ph + p.per_sample - 1) / p.per_sample : 0;
+    const int row = p.cf * VW;  // (C where C % VW == 0)
+    kn = !live || ph >= p.rows          ? 0
+         : p.rows <= p.per_sample       ? 1
+                                        : static_cast<int>(unsigned(p.rows - ph + p.per_sample - 1) / unsigned(p.per_sample));
     e0 = ph * row + tcol * VW - off;
     stride = p.per_sample * row;
-    lim = d.L;
+    lim = static_cast<int>(d.L);
   }
   __device__ __forceinline__ bool whole(int k) const {
     return MODE != 2 || (e0 + k * stride >= 0 && e0 + k * stride + VW <= lim);
   }
   __device__ __forceinline__ bool inside(int k, int e) const {
-    return MODE != 2 || (e0 + k * stride + e >= 0 && e0 + k * stride + e < lim);
+    return MODE != 2 || unsigned(e0 + k * stride + e) < unsigned(lim);
   }
   // Fragment k, where it lies in the sample, on its way into L2.
   __device__ __forceinline__ void prefetch(const T* base, int k) const {
-    const int64_t at = e0 + k * stride;
-    if (MODE != 2 || (at >= 0 && at < lim)) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + at));
+    const int at = e0 + k * stride;
+    if (MODE != 2 || unsigned(at) < unsigned(lim)) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + at));
   }
   __device__ __forceinline__ uint4 load(const T* base, int k) const {
-    const int64_t at = e0 + k * stride;
-    if (whole(k)) return dev::ld16_stream(base + at);
+    const T* at = base + (e0 + k * stride);
+    if (whole(k)) return dev::ld16_stream(at);
     float v[VW];
-    dev::load_frag<T, false>(base, at, lim, v);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) v[e] = inside(k, e) ? dev::ld1_stream(at + e) : 0.f;
     return dev::Conv<T>::pack(v);  // exact: the values are T's
   }
   __device__ __forceinline__ void store(T* base, int k, const float (&v)[VW]) const {
-    const int64_t at = e0 + k * stride;
-    if (whole(k)) dev::st16_stream(base + at, dev::Conv<T>::pack(v));
-    else dev::store_frag<T, false>(base, at, lim, v);
+    T* at = base + (e0 + k * stride);
+    if (whole(k)) {
+      dev::st16_stream(at, dev::Conv<T>::pack(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        if (inside(k, e)) dev::st1_stream(at + e, v[e]);
+    }
   }
 };
+
+// The channel of the first element of a thread's fragments.
+__device__ __forceinline__ int fused_channel(int tcol, int vw, int off, int W) {
+  const unsigned c = unsigned(tcol * vw + W - (off < W ? off : off % W));
+  return static_cast<int>(c < unsigned(W) ? c : c < 2u * unsigned(W) ? c - unsigned(W) : c % unsigned(W));
+}
 
 // Sums over the entries of each (sample, group) of a block, in two steps: over
 // the repeats of each column (fragments in MODE 0, else channels), then over a
@@ -138,7 +154,7 @@ struct Entries {
   }
   // The columns' sums, where entries are not columns already: add(position, a, b)
   // for each entry, into col_a (and col_b).
-  template <bool PAIR, typename ADD>
+  template <typename ADD>
   __device__ __forceinline__ void columns(float* col_a, float* col_b, ADD add) const {
     if (direct) return;
     sum_sets(blockDim.x, cols, reps,
@@ -153,7 +169,7 @@ struct Entries {
              },
              [&](int i, float a, float b) {
                col_a[i] = a;
-               if constexpr (PAIR) col_b[i] = b;
+               col_b[i] = b;
              });
     __syncthreads();
   }
@@ -175,16 +191,16 @@ struct Entries {
              [&](int s, float a, float b) { done(s, sample_of(s), a, b); });
   }
   // Both.
-  template <bool PAIR, typename ADD, typename DONE>
+  template <typename ADD, typename DONE>
   __device__ __forceinline__ void run(const float* ent_a, const float* ent_b, float* col_a, float* col_b, ADD add,
                                       DONE done) const {
-    columns<PAIR>(col_a, col_b, add);
+    columns(col_a, col_b, add);
     const float* ca = direct ? ent_a : col_a;
     const float* cb = direct ? ent_b : col_b;
     groups(
         [&](int i, int, float& a, float& b) {
           a += ca[i];
-          if constexpr (PAIR) b += cb[i];
+          b += cb[i];
         },
         done);
   }
@@ -238,14 +254,16 @@ __device__ __forceinline__ void put_entries(float* ent, const float (&v)[EV]) {
   }
 }
 
-// A thread's sums of its values' distances from a centre, or of their squares.
-template <typename T, int NV, int MODE, bool SQUARE>
+// A thread's sums of its values' distances from a centre, and of their squares.
+template <typename T, int NV, int MODE>
 __device__ __forceinline__ void centred_sums(const uint4 (&raw)[NV], const Place<T, MODE>& at,
                                              const float (&c)[MODE == 0 ? 1 : dev::Vec16<T>::N],
-                                             float (&s)[MODE == 0 ? 1 : dev::Vec16<T>::N]) {
+                                             float (&s)[MODE == 0 ? 1 : dev::Vec16<T>::N],
+                                             float (&q)[MODE == 0 ? 1 : dev::Vec16<T>::N]) {
   constexpr int VW = dev::Vec16<T>::N;
+  float ts[VW], tq[VW];
 #pragma unroll
-  for (int e = 0; e < (MODE == 0 ? 1 : VW); ++e) s[e] = 0.f;
+  for (int e = 0; e < VW; ++e) ts[e] = tq[e] = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     if (k < at.kn) {
@@ -257,15 +275,22 @@ __device__ __forceinline__ void centred_sums(const uint4 (&raw)[NV], const Place
 #pragma unroll
         for (int e = 0; e < VW; ++e) v[e] = at.inside(k, e) ? v[e] : 0.f;
       }
-      if constexpr (MODE == 0) {
-        float a[2] = {0.f, 0.f};
+      dev::add_pairs(ts, v);
+      fma_pairs(v, v, tq);
+    }
+  }
+  if constexpr (MODE == 0) {
+    s[0] = q[0] = 0.f;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) a[e & 1] = SQUARE ? fmaf(v[e], v[e], a[e & 1]) : a[e & 1] + v[e];
-        s[0] += a[0] + a[1];
-      } else {
+    for (int e = 0; e < VW; ++e) {
+      s[0] += ts[e];
+      q[0] += tq[e];
+    }
+  } else {
 #pragma unroll
-        for (int e = 0; e < VW; ++e) s[e] = SQUARE ? fmaf(v[e], v[e], s[e]) : s[e] + v[e];
-      }
+    for (int e = 0; e < VW; ++e) {
+      s[e] = ts[e];
+      q[e] = tq[e];
     }
   }
 }
@@ -279,18 +304,18 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   extern __shared__ __align__(16) float smem[];
   const FusedPlan& p = d.p;
   const int slots = p.samples * d.G, ents = p.phases * p.cf * EV;
-  float* ent = smem;
-  float* cnt = ent + ents;                                       // MODE 2: valid values behind each entry
-  float* col = cnt + (MODE == 2 ? ents : 0);                     // sums by column, and their counts
+  float* ent_a = smem;             // sums and sums of squares by position
+  float* ent_b = ent_a + ents;
   const int cols = p.direct ? 0 : p.samples * (MODE == 0 ? p.cf : p.W);
-  float* col_n = col + cols;
-  float* gm = col_n + (MODE == 2 ? cols : 0);
+  float* col_a = ent_b + ents;     // by column
+  float* col_b = col_a + cols;
+  float* gm = col_b + cols;        // the groups' centres, then means
   float* gr = gm + slots;
-  float* gf = gr + slots;                                        // the groups' first values
-  int* start = reinterpret_cast<int*>(gf + slots);               // MODE 2: the samples' starts
+  int* start = reinterpret_cast<int*>(gr + slots);  // MODE 2: the samples' starts
   const unsigned item = blockIdx.x;
-  const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
-  const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
+  const int trow = p.phases == 1 ? (int(threadIdx.x) < p.cf ? 0 : 1) : int(threadIdx.x / unsigned(p.cf));
+  const int tcol = threadIdx.x - trow * p.cf;
+  const int ns = p.samples == 1 ? 0 : int(unsigned(trow) / unsigned(p.per_sample));
   dev::pdl_wait();
   dev::pdl_trigger();
 
@@ -302,94 +327,61 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     if (k < at.kn) raw[k] = at.load(xs, k);
 
   if constexpr (MODE == 2) put_starts(start, d, x, item);
+  const int64_t n0 = int64_t(item) * p.samples;
+  const int mid = static_cast<int>(d.S / 2) * d.C + d.D / 2, end = static_cast<int>(d.L) - d.C + d.D - 1;
   for (int s = threadIdx.x; s < slots; s += blockDim.x) {
-    const int sn = p.samples == 1 ? 0 : s / unsigned(d.G);
-    const int64_t sample = int64_t(item) * p.samples + sn;
-    gf[s] = sample < d.N ? dev::ld1_stream(x + sample * d.L + int64_t(s - sn * d.G) * d.D) : 0.f;
-  }
-  // this thread's channels, groups and shifts
-  int c0 = MODE == 2 ? (tcol * VW + p.W - at.off % p.W) % p.W : tcol * VW;
-  int grp[EV];
-  float shift[EV];
-  for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
-    if (e < EV) {
-      grp[e] = ns * d.G + g;
-      shift[e] = at.kn > 0 ? dev::ld1_stream(xs + g * d.D) : 0.f;
+    const int sn = p.samples == 1 ? 0 : int(unsigned(s) / unsigned(d.G));
+    if (n0 + sn < d.N) {
+      const T* first = x + (n0 + sn) * d.L + (s - sn * d.G) * d.D;
+      gm[s] = median3(dev::ld1_stream(first), dev::ld1_stream(first + mid), dev::ld1_stream(first + end));
     }
+  }
+  // this thread's channels and groups
+  const int c0 = fused_channel(tcol, VW, at.off, p.W);
+  int grp[EV];
+  for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
+    if (e < EV) grp[e] = ns * d.G + g;
   });
-
   const bool mine = trow < p.phases;
   const Entries<MODE> entries(p, d.D, VW, start);
-  const int64_t n0 = int64_t(item) * p.samples;
-  const float total = float(d.S) * float(d.D);
+  __syncthreads();
 
-  float m[EV], s[EV];
-  centred_sums<T, NV, MODE, false>(raw, at, shift, s);
+  float m[EV], s[EV], q[EV];
+#pragma unroll
+  for (int e = 0; e < EV; ++e) m[e] = at.kn > 0 ? gm[grp[e]] : 0.f;
+  centred_sums<T, NV, MODE>(raw, at, m, s, q);
   if (mine) {
-    put_entries(ent, s);
-    if constexpr (MODE == 2) {
-#pragma unroll
-      for (int e = 0; e < EV; ++e) m[e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (k < at.kn) {
-#pragma unroll
-          for (int e = 0; e < EV; ++e) m[e] += at.inside(k, e) ? 1.f : 0.f;
+    put_entries(ent_a, s);
+    put_entries(ent_b, q);
+  }
+  __syncthreads();
+  entries.run(
+      ent_a, ent_b, col_a, col_b,
+      [&](int i, float& a, float& b) {
+        a += ent_a[i];
+        b += ent_b[i];
+      },
+      [&](int s, int ns, float a, float b) {
+        const float m = a * d.scale;  // from the centre
+        const float mean = gm[s] + m, r = 1.0f / sqrtf(not_negative(b - a * m) * d.scale + d.eps);
+        gm[s] = mean;
+        gr[s] = r;
+        if (n0 + ns < d.N) {
+          const int64_t i = n0 * d.G + s;  // (slots are samples' groups in order)
+          if (mean_out != nullptr) mean_out[i] = mean;
+          if (inv_out != nullptr) inv_out[i] = r;
         }
-      }
-      put_entries(cnt, m);
-    }
-  }
-  __syncthreads();
-  entries.template run<MODE == 2>(
-             ent, cnt, col, col_n,
-             [&](int i, float& a, float& b) {
-               a += ent[i];
-               if constexpr (MODE == 2) b += cnt[i];
-             },
-             [&](int s, int, float a, float b) {
-               const float n = MODE == 2 ? b : total;
-               const float first = gf[s];
-               const float mean = n > 0.f ? a / n : 0.f;
-               const float centre = first + mean;
-               // the centre is rounded: it lies by `by` off the mean, which adds n by^2 to the squares
-               const float by = mean - (centre - first);
-               gm[s] = centre;
-               gr[s] = n * by * by;
-             });
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < EV; ++e) m[e] = mine ? gm[grp[e]] : 0.f;
-  centred_sums<T, NV, MODE, true>(raw, at, m, s);
-  if (mine) {
-    put_entries(ent, s);
-  }
-  __syncthreads();
-  entries.template run<false>(
-             ent, cnt, col, col_n, [&](int i, float& a, float&) { a += ent[i]; },
-             [&](int s, int ns, float a, float) {
-               const float r = 1.0f / sqrtf(not_negative(a - gr[s]) / total + d.eps);
-               gr[s] = r;
-               const int64_t sample = n0 + ns;
-               if (sample < d.N) {
-                 const int64_t i = sample * d.G + (s - ns * d.G);
-                 if (mean_out != nullptr) mean_out[i] = gm[s];
-                 if (inv_out != nullptr) inv_out[i] = r;
-               }
-             });
+      });
   __syncthreads();
 
   // y
-  float mu[EV], rs[EV], a[VW], b[VW];
-#pragma unroll
-  for (int e = 0; e < EV; ++e) {
-    mu[e] = mine ? gm[grp[e]] : 0.f;
-    rs[e] = mine ? gr[grp[e]] : 0.f;
-  }
   if (at.kn > 0) {
+    float mu[EV], a[VW], b[VW];
     load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, a, b);
 #pragma unroll
-    for (int e = 0; e < VW; ++e) a[e] *= rs[MODE == 0 ? 0 : e];
+    for (int e = 0; e < EV; ++e) mu[e] = gm[grp[e]];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) a[e] *= gr[grp[MODE == 0 ? 0 : e]];
     T* ys = y + at.n * d.L;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -429,10 +421,11 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
   float* ch_g = ch_b + p.W;
   int* start = reinterpret_cast<int*>(ch_g + p.W);
   const unsigned first = blockIdx.x;
-  const int trow = threadIdx.x / unsigned(p.cf), tcol = threadIdx.x - trow * p.cf;
-  const int ns = p.samples == 1 ? 0 : trow / unsigned(p.per_sample);
+  const int trow = p.phases == 1 ? (int(threadIdx.x) < p.cf ? 0 : 1) : int(threadIdx.x / unsigned(p.cf));
+  const int tcol = threadIdx.x - trow * p.cf;
+  const int ns = p.samples == 1 ? 0 : int(unsigned(trow) / unsigned(p.per_sample));
   const bool mine = trow < p.phases;
-  const float scale = 1.0f / (float(d.S) * float(d.D));
+  const float scale = d.scale;
   const Entries<MODE> entries(p, d.D, VW, start);
   dev::pdl_wait();
   dev::pdl_trigger();
@@ -473,7 +466,7 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
     }
     if (off != at.off && mine) {
       off = at.off;
-      const int c0 = MODE == 2 ? (tcol * VW + p.W - off % p.W) % p.W : tcol * VW;
+      const int c0 = fused_channel(tcol, VW, off, p.W);
       load_params<T, MODE == 2>(gamma, beta, c0, p.W, d.pvec, ga, be);
       for_channels<VW>(c0, p.W, d.D, [&](int e, int, int g) {
         if (e < EV) grp[e] = g;
@@ -549,9 +542,9 @@ k_gn_grad_fused(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
       b += ent_b[i];
     };
     if constexpr (MODE != 2) {
-      entries.template run<true>(ent_a, ent_b, col_a, col_b, entry, means);
+      entries.run(ent_a, ent_b, col_a, col_b, entry, means);
     } else {
-      entries.template columns<true>(col_a, col_b, entry);
+      entries.columns(col_a, col_b, entry);
       const float* ca = entries.direct ? ent_a : col_a;
       const float* cb = entries.direct ? ent_b : col_b;
       for (int c = threadIdx.x; c < p.W; c += blockDim.x) {
@@ -953,16 +946,15 @@ cudaError_t token_grad(const GroupNormGradArgs& a, const TokenDims& d, float* cp
   return e;
 }
 
-// Shared memory: the entries (MODE 2: and their counts; the gradient: two sets for
-// every channel), the columns' sums and the groups' values (the gradient, MODE 2:
-// and the channels' sums and gamma).
+// Shared memory: two sums for each entry, each column and each group (the gradient:
+// an entry for every channel; MODE 2: and the channels' sums and gamma).
 size_t fused_smem(const FusedPlan& p, int mode, int vw, int64_t G, bool grad) {
   const size_t slots = size_t(p.samples) * G, frags = size_t(p.phases) * p.cf;
-  const size_t ents = grad ? 2 * frags * vw : mode == 0 ? frags : frags * vw * (mode == 2 ? 2 : 1);
+  const size_t ents = 2 * frags * (grad || mode != 0 ? vw : 1);
   const size_t cols =
-      p.direct ? 0 : size_t(p.samples) * (mode == 0 ? p.cf : p.W) * (grad || mode == 2 ? 2 : 1);
+      p.direct ? 0 : 2 * size_t(p.samples) * (mode == 0 ? p.cf : p.W);
   const size_t channels = grad && mode == 2 ? 3 * size_t(p.W) : 0;
-  return 4 * (ents + cols + (grad ? 2 : 3) * slots + channels + (mode == 2 ? p.samples : 0));
+  return 4 * (ents + cols + 2 * slots + channels + (mode == 2 ? p.samples : 0));
 }
 // Two blocks an SM, or one where a block has more threads.
 constexpr size_t smem_most(const FusedPlan& p) { return (p.threads > kMaxThreads ? 200 : 96) * 1024; }
@@ -1052,7 +1044,7 @@ size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int
 cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t stream, int* launches, bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
   const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
-  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, a.silu, pvec, {}};
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, float(1.0 / (double(a.S) * double(a.C / a.G))), a.silu, pvec, {}};
   *done = false;
   if (misalign16(a.x) != misalign16(a.y)) return cudaSuccess;
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
@@ -1086,7 +1078,7 @@ cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int, cudaSt
                                          bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
   const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
-  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, a.silu, pvec, {}};
+  FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, float(1.0 / (double(a.S) * double(a.C / a.G))), a.silu, pvec, {}};
   *done = false;
   if (misalign16(a.x) != misalign16(a.dy) || misalign16(a.x) != misalign16(a.dx)) return cudaSuccess;
   const bool slab = a.C % vw == 0 && misalign16(a.x) == 0;
