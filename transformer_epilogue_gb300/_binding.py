@@ -366,7 +366,8 @@ def _elsewhere(stream, index):
 
 # Scratch comes from PyTorch's allocator as a bare pointer: a tensor that nobody
 # sees costs 2 us more.
-_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", torch.cuda.caching_allocator_alloc)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc",
+                     lambda size, stream: torch.cuda.caching_allocator_alloc(size, stream=stream))
 _raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", torch.cuda.caching_allocator_delete)
 
 

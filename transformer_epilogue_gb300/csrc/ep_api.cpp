@@ -525,7 +525,7 @@ ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape, const v
   ep::GroupNormArgs a{to_dtype(t), X, gamma, beta, Y, mean, inv_std_dev, g.N, g.S, g.C, groups, epsilon,
                       activation == EP_ACT_SILU, workspace};
   int launches = 0;
-  cudaError_t e = ep::launch_group_norm(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  cudaError_t e = ep::launch_group_norm(a, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches, "group_norm");
 }
 
@@ -577,7 +577,7 @@ ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const in
   ep::GroupNormGradArgs a{to_dtype(t), dY, X, gamma, beta, mean, inv_std_dev, dX, dgamma, dbeta,
                           g.N, g.S, g.C, groups, activation == EP_ACT_SILU, workspace};
   int launches = 0;
-  cudaError_t e = ep::launch_group_norm_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  cudaError_t e = ep::launch_group_norm_grad(a, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches, "group_norm_grad");
 }
 

@@ -125,8 +125,8 @@ cudaError_t launch_bias_softmax(const SoftmaxArgs& a, int sm_count, int l2_bytes
 cudaError_t launch_bias_add(const BiasAddArgs& a, int sm_count, cudaStream_t stream, int* launches);
 cudaError_t launch_quick_gelu(const QuickGeluArgs& a, int sm_count, cudaStream_t stream, int* launches);
 
-cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches);
-cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches);
+cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream, int* launches);
+cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, cudaStream_t stream, int* launches);
 cudaError_t launch_bias_dropout(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches);
 cudaError_t launch_bias_dropout_grad(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches);
 

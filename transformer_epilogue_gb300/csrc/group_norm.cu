@@ -1990,7 +1990,7 @@ size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C,
   return most;
 }
 
-cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream, int* launches) {
   if (token_staged(a.t, a.N, a.S, a.C, a.G, kTokenStagedBytes) && misalign16(a.x) == 0 && misalign16(a.y) == 0) {
     switch (a.t) {
       case DType::F32: return token_fwd_t<float>(a, stream, launches);
@@ -1999,7 +1999,7 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
     }
   }
   bool done = false;
-  const cudaError_t e = launch_group_norm_fused(a, sm_count, stream, launches, &done);
+  const cudaError_t e = launch_group_norm_fused(a, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
   switch (a.t) {
     case DType::F32: return group_norm_t<float>(a, stream, launches);
@@ -2008,7 +2008,7 @@ cudaError_t launch_group_norm(const GroupNormArgs& a, int sm_count, cudaStream_t
   }
 }
 
-cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, cudaStream_t stream, int* launches) {
   if (token_staged(a.t, a.N, a.S, a.C, a.G, kTokenGradStagedBytes) && misalign16(a.x) == 0 &&
       misalign16(a.dy) == 0 && misalign16(a.dx) == 0) {
     switch (a.t) {
@@ -2018,7 +2018,7 @@ cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, int sm_count, cud
     }
   }
   bool done = false;
-  const cudaError_t e = launch_group_norm_grad_fused(a, sm_count, stream, launches, &done);
+  const cudaError_t e = launch_group_norm_grad_fused(a, stream, launches, &done);
   if (done || e != cudaSuccess) return e;
   switch (a.t) {
     case DType::F32: return group_norm_grad_t<float>(a, stream, launches);

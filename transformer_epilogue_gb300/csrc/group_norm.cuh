@@ -178,10 +178,8 @@ __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : 
 // The fused form (group_norm_fused.cu): small samples, and few tokens, in one
 // launch.  *done says whether the shape and the alignment allow it; if not,
 // nothing has been launched.
-cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int sm_count, cudaStream_t stream, int* launches,
-                                    bool* done);
-cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int sm_count, cudaStream_t stream,
-                                         int* launches, bool* done);
+cudaError_t launch_group_norm_fused(const GroupNormArgs& a, cudaStream_t stream, int* launches, bool* done);
+cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, cudaStream_t stream, int* launches, bool* done);
 // Workspace bytes of the fused gradient (0 where it does not apply).
 size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G);
 

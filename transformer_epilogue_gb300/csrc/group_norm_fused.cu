@@ -1041,7 +1041,7 @@ size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int
   return most;
 }
 
-cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t stream, int* launches, bool* done) {
+cudaError_t launch_group_norm_fused(const GroupNormArgs& a, cudaStream_t stream, int* launches, bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
   const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), a.eps, float(1.0 / (double(a.S) * double(a.C / a.G))), a.silu, pvec, {}};
@@ -1074,8 +1074,7 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, int, cudaStream_t st
 #undef EP_GN_FUSED
 }
 
-cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, int, cudaStream_t stream, int* launches,
-                                         bool* done) {
+cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, cudaStream_t stream, int* launches, bool* done) {
   const int vw = a.t == DType::F32 ? 4 : 8;
   const bool pvec = misalign16(a.gamma) == 0 && misalign16(a.beta) == 0;
   FusedDims d{a.N, a.S, a.S * a.C, int(a.C), int(a.G), int(a.C / a.G), 0.f, float(1.0 / (double(a.S) * double(a.C / a.G))), a.silu, pvec, {}};
