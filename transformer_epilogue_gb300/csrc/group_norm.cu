@@ -375,22 +375,31 @@ __device__ __forceinline__ void load_param(const T* __restrict__ param, int c, i
   }
 }
 
-// mu of the thread's groups, and k scaled by their 1/sqrt(var + eps).
-template <int EV, int VW>
+// mu of the thread's groups, and k scaled by their 1/sqrt(var + eps).  ld: how they
+// are read.  What a join writes while this kernel may already have been launched is
+// read by plain cached loads (__ldca, or through a generic pointer), never as
+// read-only data.
+struct PlainLoad {
+  __device__ __forceinline__ float operator()(const float* p) const { return *p; }
+};
+struct CachedLoad {
+  __device__ __forceinline__ float operator()(const float* p) const { return __ldca(p); }
+};
+template <int EV, int VW, typename LD>
 __device__ __forceinline__ void scale_by_group(int c0, int64_t ng, const GnDims& d, const float* mean,
-                                               const float* inv, float (&mu)[EV], float (&k)[VW]) {
+                                               const float* inv, float (&mu)[EV], float (&k)[VW], LD ld) {
   const float* m = mean + ng;
   const float* r = inv + ng;
   if constexpr (EV == 1) {
     const int g = c0 / d.D;
-    mu[0] = m[g];
-    const float rg = r[g];
+    mu[0] = ld(m + g);
+    const float rg = ld(r + g);
 #pragma unroll
     for (int e = 0; e < VW; ++e) k[e] *= rg;
   } else {
     for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
-      mu[e] = m[g];
-      k[e] *= r[g];
+      mu[e] = ld(m + g);
+      k[e] *= ld(r + g);
     });
   }
 }
@@ -407,8 +416,10 @@ struct ApplyValues {
     load_param(gamma, c0, d.C, d.pvec, a);
     if (beta != nullptr) load_param(beta, c0, d.C, d.pvec, b);
   }
-  __device__ __forceinline__ void scale(int c0, int64_t ng, const GnDims& d, const float* mean, const float* inv) {
-    scale_by_group(c0, ng, d, mean, inv, mu, a);
+  template <typename LD>
+  __device__ __forceinline__ void scale(int c0, int64_t ng, const GnDims& d, const float* mean, const float* inv,
+                                        LD ld) {
+    scale_by_group(c0, ng, d, mean, inv, mu, a, ld);
   }
   __device__ __forceinline__ void operator()(float (&v)[VW]) const {
     centre_scale_add(v, mu, a, b);
@@ -427,7 +438,7 @@ struct GradValues {
     for (int e = 0; e < VW; ++e) be[e] = 0.f;
     load_param(gamma, c0, d.C, d.pvec, k);
     if (SILU && beta != nullptr) load_param(beta, c0, d.C, d.pvec, be);
-    scale_by_group(c0, ng, d, mean, inv, mu, k);
+    scale_by_group(c0, ng, d, mean, inv, mu, k, PlainLoad{});
   }
   __device__ __forceinline__ void operator()(float (&v)[VW], float (&w)[VW]) const {
 #pragma unroll
@@ -458,8 +469,8 @@ struct GradApplyValues : GradValues<T, EV, SILU> {
     for_channels<VW>(c0, d.C, d.D, [&](int e, int, int g) {
       if (e < EV) {
         const float r = inv[ng + g];
-        q1[e] = -r * m1[ng + g];
-        q2[e] = -r * (r * m2[ng + g]);
+        q1[e] = -r * __ldca(m1 + ng + g);
+        q2[e] = -r * (r * __ldca(m2 + ng + g));
       }
     });
   }
@@ -934,7 +945,7 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
       if (mean != nullptr) mean[r.n * d.G + threadIdx.x] = js.mean[threadIdx.x];
       if (inv != nullptr) inv[r.n * d.G + threadIdx.x] = js.inv[threadIdx.x];
     }
-    if (t.mine) val.scale(c0, d.here ? 0 : r.n * d.G, d, d.here ? js.mean : mean, d.here ? js.inv : inv);
+    if (t.mine) val.scale(c0, d.here ? 0 : r.n * d.G, d, d.here ? js.mean : mean, d.here ? js.inv : inv, PlainLoad{});
     const int64_t pitch = p.row_frags * VW;
     T* py = y + r.n * d.L - off + r.ra * pitch + t.j * VW;
     rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
@@ -1443,7 +1454,7 @@ k_gn_apply(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     ApplyValues<T, VW, SILU> val;
     const int c0 = first_channel(t.j, VW, off, d.C);
     val.load_params(c0, d, gamma, beta);
-    val.scale(c0, r.n * d.G, d, mean, inv);
+    val.scale(c0, r.n * d.G, d, mean, inv, CachedLoad{});
     for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
       float v[U][VW];
 #pragma unroll
