@@ -1304,6 +1304,7 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
     rows.stages(r, [&](int row, const unsigned char* src) {
       const int n = min(rows.rows, all - row);  // lanes without the last row go round too
       const int own = min(rows.rows, mine - row);
+      const int warp_own = __reduce_min_sync(0xffffffffu, own);  // rows that all lanes have
       auto two = [&](int i) {
         uint4 raw[2][2];
         rows.load(src, i, raw);
@@ -1312,7 +1313,7 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
         for (int u = 0; u < 2; ++u) {
           dev::Conv<T>::unpack(raw[u][0], h[u]);
           dev::Conv<T>::unpack(raw[u][1], w[u]);
-          if (i + u >= own) {
+          if (i + u >= warp_own && i + u >= own) {
 #pragma unroll
             for (int e = 0; e < VW; ++e) h[u][e] = w[u][e] = 0.f;
           }
@@ -1329,20 +1330,30 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
           }
           dev::add_pairs(tot_a, w[u]);
           fma_pairs(w[u], h[u], tot_b);
-          s[2 * u] = s[2 * u + 1] = 0.f;
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
 #pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            w[u][e] *= ga[e];
-            s[2 * u] += w[u][e];
-            s[2 * u + 1] = fmaf(w[u][e], h[u][e], s[2 * u + 1]);
+          for (int e = 0; e < VW; e += 2) {
+            const float2 g = __fmul2_rn(make_float2(w[u][e], w[u][e + 1]), make_float2(ga[e], ga[e + 1]));
+            sa = __fadd2_rn(sa, g);
+            sb = __ffma2_rn(g, make_float2(h[u][e], h[u][e + 1]), sb);
+            w[u][e] = g.x;
+            w[u][e + 1] = g.y;
           }
+          s[2 * u] = sa.x + sa.y;
+          s[2 * u + 1] = sb.x + sb.y;
         }
         ts.sum(s);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float p1 = s[2 * u] * scale, p2 = s[2 * u + 1] * scale;
+          // r (w - m1 - h m2) = w r + (h (-r m2) - r m1)
+          const float p1 = -kk[u] * (s[2 * u] * scale), p2 = -kk[u] * (s[2 * u + 1] * scale);
 #pragma unroll
-          for (int e = 0; e < VW; ++e) w[u][e] = kk[u] * (fmaf(-p2, h[u][e], w[u][e] - p1));
+          for (int e = 0; e < VW; e += 2) {
+            const float2 q = __ffma2_rn(make_float2(h[u][e], h[u][e + 1]), make_float2(p2, p2), make_float2(p1, p1));
+            const float2 z = __ffma2_rn(make_float2(w[u][e], w[u][e + 1]), make_float2(kk[u], kk[u]), q);
+            w[u][e] = z.x;
+            w[u][e + 1] = z.y;
+          }
           if (i + u < own) dev::st16_stream(po + (row + i + u) * pitch, dev::Conv<T>::pack(w[u]));
         }
       };
