@@ -324,7 +324,7 @@ def ep_quick_gelu(X, alpha=DEFAULT_ALPHA, Y=None, stream=None):
 # the current stream's handle without a Stream object (2 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _first(name, t):
@@ -401,7 +401,6 @@ def _dims(shape):
     return _shape(shape)
 
 
-@functools.lru_cache(maxsize=4096)
 def _nsc(shape):
     """(N, S, C) of a channels-last shape: the dimensions between the first and
     the last are positions."""
@@ -414,10 +413,12 @@ def _nsc(shape):
 
 
 @functools.lru_cache(maxsize=4096)
-def _group_norm_need(code, shape, groups, grad):
+def _group_norm_plan(code, shape, groups, grad):
+    """(N, S, C) as the library reads it, the channels' shape and the workspace's bytes."""
     lib = load_library()
     fn = lib.ep_group_norm_grad_workspace_size if grad else lib.ep_group_norm_workspace_size
-    return int(fn(code, _nsc(shape), groups))
+    nsc = _nsc(shape)
+    return nsc, torch.Size(shape[-1:]), int(fn(code, nsc, groups))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -431,12 +432,12 @@ def _code(dtype):
 
 def ep_group_norm_workspace_size(dtype, shape, groups) -> int:
     """Workspace bytes of ep_group_norm for a channels-last shape."""
-    return _group_norm_need(_code(dtype), tuple(shape), int(groups), False)
+    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), False)[2]
 
 
 def ep_group_norm_grad_workspace_size(dtype, shape, groups) -> int:
     """Workspace bytes of ep_group_norm_grad for a channels-last shape."""
-    return _group_norm_need(_code(dtype), tuple(shape), int(groups), True)
+    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), True)[2]
 
 
 def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
@@ -479,7 +480,7 @@ def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_E
             return ep_group_norm(X, gamma, beta, groups, epsilon, activation, Y, mean, inv_std_dev, workspace)
     lib = load_library()
     shape, groups = X.shape, int(groups)
-    nsc, channels = _nsc(shape), shape[-1:]
+    nsc, channels, need = _group_norm_plan(code, shape, groups, False)
     _operand("gamma", gamma, X, index, channels)
     if beta is not None:
         _operand("beta", beta, X, index, channels)
@@ -489,7 +490,7 @@ def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_E
     args = (code, X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation),
             Y.data_ptr(), _addr(mean), _addr(inv_std_dev))
     s = _raw_stream(index)
-    ws, wbytes, owned = _scratch(workspace, _group_norm_need(code, shape, groups, False), X, s)
+    ws, wbytes, owned = _scratch(workspace, need, X, s)
     try:
         _check(lib.ep_group_norm(*args, ws, wbytes, s))
     finally:
@@ -514,7 +515,7 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
                                       workspace)
     lib = load_library()
     shape, groups = X.shape, int(groups)
-    nsc, channels = _nsc(shape), shape[-1:]
+    nsc, channels, need = _group_norm_plan(code, shape, groups, True)
     _operand("dY", dY, X, index, shape)
     _operand("gamma", gamma, X, index, channels)
     if beta is not None:
@@ -529,7 +530,7 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
     args = (code, dY.data_ptr(), X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, int(activation),
             mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(), _addr(dgamma), _addr(dbeta))
     s = _raw_stream(index)
-    ws, wbytes, owned = _scratch(workspace, _group_norm_need(code, shape, groups, True), X, s)
+    ws, wbytes, owned = _scratch(workspace, need, X, s)
     try:
         _check(lib.ep_group_norm_grad(*args, ws, wbytes, s))
     finally:
