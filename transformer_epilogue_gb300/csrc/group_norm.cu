@@ -57,6 +57,8 @@ struct GnDims {
   int rest;
   bool pvec;  // gamma and beta 16-byte aligned (and every fragment's channels one after another)
   bool here;  // pass 2 joins the chunks itself
+  int slots;  // groups that a tile of the walk row can meet: its parts of an item
+  bool staged, shifted;  // how the parts lie: see Slots; shifted: walks start before their sample
   int64_t ctas;  // CTAs that the plan is made for
   WalkPlan p;
 };
@@ -173,6 +175,85 @@ struct Sample {
   int64_t f0, nf;
 };
 
+// An item's parts: `slots` for each tile of the walk row, from the tile's first group
+// on (modulo G), so that scratch grows with the groups and not with groups x tiles
+// (f16 1x64x65536 in 65536 groups: 303 MB to 11).
+//  staged: channels do not wrap around in a tile, so group g is in the tiles t0 ...
+//  that its channels reach, in all but the first of them as the first group;
+//  general: a tile's channels may wrap around and start off the sample; the join looks
+//  at every tile.  Where a tile has a slot for every group, slot g is group g.
+struct Slots {
+  int slots, G, first;
+  __device__ __forceinline__ Slots(const GnDims& d, int tile, int off, int vw) : slots(d.slots), G(d.G), first(0) {
+    if (slots < G || (d.staged && d.p.tiles > 1))
+      first = first_channel(int64_t(tile) * d.p.tile_frags, vw, off, d.C) / d.D;
+  }
+  __device__ __forceinline__ int group(int s) const { return first + s < G ? first + s : first + s - G; }
+  __device__ __forceinline__ int slot(int g) const { return g >= first ? g - first : g - first + G; }
+};
+
+// The parts of group g of a sample on staged rows of several tiles, by index: where part
+// k stands, counted in slots from the sample's first.  No branches: the join's loads go
+// out together.
+struct GroupParts {
+  unsigned count, of_chunk, magic;  // magic: 2^32 / of_chunk, rounded up (k of_chunk < 2^32)
+  int tiles, slots, base0, base1;   // the first and the other parts of a chunk
+  __device__ __forceinline__ GroupParts(const GnDims& d, int g, int vw) : tiles(d.p.tiles), slots(d.slots) {
+    const int e0 = g * d.D, tile = d.p.tile_frags * vw, t0 = e0 / tile;
+    of_chunk = (e0 + d.D - 1) / tile - t0 + 1;
+    base1 = t0 * slots;
+    base0 = base1 + g - t0 * tile / d.D;
+    count = unsigned(d.p.chunks) * of_chunk;
+    magic = of_chunk > 1 ? 0xffffffffu / of_chunk + 1u : 0u;
+  }
+  template <typename F>
+  __device__ __forceinline__ F load(const F* src, unsigned k) const {
+    const unsigned chunk = of_chunk > 1 ? __umulhi(k, magic) : k, i = k - chunk * of_chunk;
+    return k < count ? __ldcg(src + int64_t(chunk * unsigned(tiles) + i) * slots + (i == 0 ? base0 : base1)) : F{};
+  }
+};
+
+// The same where a tile meets some of the groups and channels wrap around in it:
+// every tile is looked at.
+struct ScannedParts {
+  const GnDims& d;
+  int g, vw, off;
+  unsigned count;
+  __device__ __forceinline__ ScannedParts(const GnDims& d_, int g_, int vw_, int off_)
+      : d(d_), g(g_), vw(vw_), off(off_), count(unsigned(d_.p.chunks) * d_.p.tiles) {}
+  template <typename F>
+  __device__ __forceinline__ F load(const F* src, unsigned k) const {
+    if (k >= count) return F{};
+    const int s = Slots(d, static_cast<int>(k % unsigned(d.p.tiles)), off, vw).slot(g);
+    return s < d.slots ? __ldcg(src + int64_t(k) * d.slots + s) : F{};
+  }
+};
+
+// The same where slot g is group g in every tile.
+struct LinearParts {
+  unsigned count;
+  int slots, g;
+  __device__ __forceinline__ LinearParts(const GnDims& d, int g_)
+      : count(unsigned(d.p.chunks) * d.p.tiles), slots(d.slots), g(g_) {}
+  template <typename F>
+  __device__ __forceinline__ F load(const F* src, unsigned k) const {
+    return k < count ? __ldcg(src + int64_t(k) * slots + g) : F{};
+  }
+};
+
+// f(parts) for those of group g of the sample that starts at xs.
+template <typename T, typename F>
+__device__ __forceinline__ void with_parts(const GnDims& d, int g, const T* xs, F f) {
+  constexpr int VW = dev::Vec16<T>::N;
+  if (d.p.tiles == 1 || (!d.staged && d.slots == d.G)) {
+    f(LinearParts(d, g));
+  } else if (d.staged) {
+    f(GroupParts(d, g, VW));
+  } else {
+    f(ScannedParts(d, g, VW, d.shifted ? dev::misalignment(xs) : 0));
+  }
+}
+
 // An item's partial fragments, if this thread has one: the sample's first (before
 // `lo` outside) and last (from `hi` on), by their row in the item.  They are
 // read from global memory, value by value: the tensor's last one is not staged.
@@ -199,8 +280,10 @@ __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, 
   const WalkPlan& p = d.p;
   const GroupWalk walk(p, t.tile, t.frags, d.C, d.D, dev::Vec16<T>::N);
   const int lane = threadIdx.x & 31;
-  for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
-    float4* out = partial + (item * p.tiles + t.tile) * d.G + g;
+  const Slots slots(d, t.tile, off, dev::Vec16<T>::N);
+  for (int i = threadIdx.x >> 5; i < d.slots; i += warps) {
+    const int g = slots.group(i);
+    float4* out = partial + (item * p.tiles + t.tile) * d.slots + i;
     if (!walk.has(g, off)) {
       if (lane == 0) *out = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
@@ -241,7 +324,9 @@ __device__ __forceinline__ void join_group_sums(const GnDims& d, const Tile& t, 
   const WalkPlan& p = d.p;
   const GroupWalk walk(p, t.tile, t.frags, d.C, d.D, dev::Vec16<T>::N);
   const int lane = threadIdx.x & 31;
-  for (int g = threadIdx.x >> 5; g < d.G; g += warps) {
+  const Slots slots(d, t.tile, off, dev::Vec16<T>::N);
+  for (int i = threadIdx.x >> 5; i < d.slots; i += warps) {
+    const int g = slots.group(i);
     float a = 0.f, b = 0.f;
     if (walk.has(g, off)) {
       walk.run(g, off, [&](int i) {
@@ -252,7 +337,7 @@ __device__ __forceinline__ void join_group_sums(const GnDims& d, const Tile& t, 
       b = dev::warp_sum(b);
     }
     if (lane == 0) {
-      float* out = gpart + ((item * p.tiles + t.tile) * d.G + g) * 2;
+      float* out = gpart + ((item * p.tiles + t.tile) * d.slots + i) * 2;
       out[0] = a;
       out[1] = b;
     }
@@ -347,14 +432,6 @@ struct Columns {
   __device__ __forceinline__ int lo(int g) const { return max(0, g * D - in0); }
   __device__ __forceinline__ int hi(int g) const { return min(cols, (g + 1) * D - in0); }
 };
-
-// Parts of the groups that the tile does not touch.
-__device__ __forceinline__ void clear_others(const GnDims& d, const Columns& c, float* out, int width, int threads) {
-  if (d.p.tiles == 1) return;
-  for (int g = threadIdx.x; g < d.G; g += threads)
-    if (g < c.g0 || g >= c.g0 + c.n_groups)
-      for (int i = 0; i < width; ++i) out[g * width + i] = 0.f;
-}
 
 // ---------------------------------------------------------------------------
 // What a thread does with its fragments.
@@ -684,7 +761,7 @@ struct RowStream {
 // The barrier of a staged kernel's consumers.
 __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blockDim.x - 32); }
 
-// Pass 1.  partial: [item][tile][G] x (count, mean, M2, the group's first value in
+// Pass 1.  partial: [item][tile][slot] x (count, mean, M2, the group's first value in
 // the sample), the mean relative to that value.  The block takes its values relative to
 // a centre of each group, so that its sums and sums of squares simply add up: the
 // median of three of the group's values in the item's first walk row, which lies
@@ -729,9 +806,9 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
   }
   for (Items it(d, false); it.more(); it.next()) {
     const Range r = rows.range(p, it.item());
-    float4* out = partial + (it.item() * p.tiles + t.tile) * d.G;
+    float4* out = partial + (it.item() * p.tiles + t.tile) * d.slots;
     if (r.ra >= r.rb) {  // the plan's rows may be one more than there are
-      for (int g = threadIdx.x; g < d.G; g += consumers) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = threadIdx.x; g < d.slots; g += consumers) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
     float c[EV], s[VW], q[VW];
@@ -825,9 +902,6 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                });
       consumer_sync();
     }
-    if (p.tiles > 1)
-      for (int g = threadIdx.x; g < d.G; g += consumers)
-        if (g < cols.g0 || g >= cols.g0 + cols.n_groups) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
     const float positions = float(pos1 - pos0);
     sum_sets(consumers, cols.n_groups, cols.D,
              [&](int g, int k, float& a, float& b) {
@@ -847,7 +921,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                }
                const float m = n > 0.f ? a / n : 0.f;
                const float first = dev::ld1_keep(xs + int64_t(cols.g0 + g) * d.D);
-               out[cols.g0 + g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), first);
+               out[g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), first);
              });
     consumer_sync();
   }
@@ -970,7 +1044,7 @@ k_gn_apply_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
 
 // Gradient, pass 1: per-channel sums of du and du * h of a CTA's items, and the
 // groups' sums of each item.
-//   gpart: [item][tile][G] x (sum du gamma, sum du gamma h); cpart: leave_channel_sums
+//   gpart: [item][tile][slot] x (sum du gamma, sum du gamma h); cpart: leave_channel_sums
 template <typename T, bool GROUP, bool ODD, bool SILU>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta,
@@ -1050,8 +1124,7 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
              });
     once = false;
     consumer_sync();
-    float* out = gpart + (it.item() * p.tiles + t.tile) * d.G * 2;
-    clear_others(d, cols, out, 2, consumers);
+    float* out = gpart + (it.item() * p.tiles + t.tile) * d.slots * 2;
     sum_sets(consumers, cols.n_groups, cols.D,
              [&](int g, int k, float& a, float& b) {
                const int i = cols.lo(g) + k;
@@ -1061,8 +1134,8 @@ k_gn_grad_sums_staged(const T* dy, const T* x, const T* __restrict__ gamma, cons
                }
              },
              [&](int g, float a, float b) {
-               out[(cols.g0 + g) * 2] = a;
-               out[(cols.g0 + g) * 2 + 1] = b;
+               out[g * 2] = a;
+               out[g * 2 + 1] = b;
              });
     consumer_sync();
   }
@@ -1626,54 +1699,85 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 
 constexpr int kJoinThreads = 64;
 
-// (count, mean, M2) of the parts -> the group's statistics: a warp for each
-// (n, g), which keeps up to kJoinKept parts a lane in registers for the second
-// sum and reads the others again.
+// (count, mean, M2) of the parts -> the group's statistics.  `lanes` of a warp (a power
+// of two) take one (n, g), each keeping up to KEPT parts in registers for the second
+// sum and reading others again.  How a group's parts are found (WAY) is a kernel of
+// its own: the code runs once, so what it does not need costs it instruction fetches
+// (f16 2x4096x320 in one kernel with the other ways 10.5 us, 10.1 as it is).
+//   0  part k is slot g of tile k of the sample (one tile, or a slot for every group): kJoinKept
+//   1  staged rows of many tiles; KEPT 1 where a warp's lanes hold all parts of a group: a warp for
+//      each group takes 282 us, not 203, for f16 40x100x16384 in 4096 groups
+//   2  every tile is looked at
 constexpr int kJoinKept = 10;
 
-template <typename T>
+template <typename T, int WAY, int KEPT>
 __global__ void __launch_bounds__(kJoinThreads)
-k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* inv_out) {
+k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* inv_out, int log_lanes) {
+  constexpr int VW = dev::Vec16<T>::N;
   dev::pdl_trigger();
-  dev::pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles;
-  for (int64_t i = int64_t(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < d.N * d.G;
-       i += int64_t(gridDim.x) * (kJoinThreads / 32)) {
-    const int64_t n = quotient(i, d.G), g = i - n * d.G;
-    const float4* src = partial + n * parts * d.G + g;
-    const float first = dev::ld1_keep(x + n * d.L + g * d.D);
-    float4 kept[kJoinKept];
+  bool waited = false;  // where the first group's parts lie, and x: before pass 1 ends
+  const int lanes = KEPT == 1 ? 1 << log_lanes : 32, lane = threadIdx.x & (lanes - 1);
+  const int64_t of_sample = int64_t(d.p.chunks) * d.p.tiles * d.slots, all = d.N * d.G;
+  auto sum = [&](float v) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  // (a warp's lanes go round together: lanes beyond the last group take part in its shuffles)
+  const int per_warp = 32 / lanes, in_warp = (threadIdx.x & 31) / lanes;
+  for (int64_t i0 = (int64_t(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5)) * per_warp; i0 < all;
+       i0 += int64_t(gridDim.x) * (kJoinThreads / 32) * per_warp) {
+    const int64_t i = i0 + in_warp;
+    const bool live = KEPT > 1 || i < all;
+    const int64_t n = live ? quotient(i, d.G) : 0;
+    const int g = live ? static_cast<int>(i - n * d.G) : 0;
+    const T* xs = x + n * d.L;
+    const float4* src = partial + n * of_sample;
+    const float first = dev::ld1_keep(xs + int64_t(g) * d.D);
+    auto join = [&](const auto& parts) {
+      if (!waited) dev::pdl_wait();
+      waited = true;
+      auto part = [&](unsigned k) { return live ? parts.load(src, k) : float4{}; };
+      float4 kept[KEPT];
 #pragma unroll
-    for (int u = 0; u < kJoinKept; ++u)
-      kept[u] = lane + u * 32 < parts ? __ldcg(src + int64_t(lane + u * 32) * d.G) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
+      for (int u = 0; u < KEPT; ++u) kept[u] = part(lane + u * 32);
+      float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
 #pragma unroll
-    for (int u = 0; u < kJoinKept; ++u) {
-      c += kept[u].x;
-      s = fmaf(kept[u].x, kept[u].y, s);
-    }
-    for (int64_t k = lane + kJoinKept * 32; k < parts; k += 32) {
-      const float4 v = __ldcg(src + k * d.G);
-      c += v.x;
-      s = fmaf(v.x, v.y, s);
-    }
-    c = dev::warp_sum(c);
-    const float mg = dev::warp_sum(s) / c;
-    auto square = [&](const float4& v) {
-      const float w = v.y - mg;
-      res = fmaf(v.x, w, res);
-      q += fmaf(v.x * w, w, v.z);
+      for (int u = 0; u < KEPT; ++u) {
+        c += kept[u].x;
+        s = fmaf(kept[u].x, kept[u].y, s);
+      }
+      if constexpr (KEPT > 1) {
+        for (unsigned k = lane + KEPT * 32; k < parts.count; k += 32) {
+          const float4 v = part(k);
+          c += v.x;
+          s = fmaf(v.x, v.y, s);
+        }
+      }
+      c = sum(c);
+      const float mg = sum(s) / c;
+      auto square = [&](const float4& v) {
+        const float w = v.y - mg;
+        res = fmaf(v.x, w, res);
+        q += fmaf(v.x * w, w, v.z);
+      };
+#pragma unroll
+      for (int u = 0; u < KEPT; ++u) square(kept[u]);
+      if constexpr (KEPT > 1)
+        for (unsigned k = lane + KEPT * 32; k < parts.count; k += 32) square(part(k));
+      res = sum(res);
+      q = sum(q);
+      if (live && lane == 0) {
+        const float fix = res / c;  // what rounding left out of the mean
+        mean_out[i] = first + (mg + fix);
+        inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
+      }
     };
-#pragma unroll
-    for (int u = 0; u < kJoinKept; ++u) square(kept[u]);
-    for (int64_t k = lane + kJoinKept * 32; k < parts; k += 32) square(__ldcg(src + k * d.G));
-    res = dev::warp_sum(res);
-    q = dev::warp_sum(q);
-    if (lane == 0) {
-      const float fix = res / c;  // what rounding left out of the mean
-      mean_out[i] = first + (mg + fix);
-      inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
+    if constexpr (WAY == 0) {
+      join(LinearParts(d, g));
+    } else if constexpr (WAY == 1) {
+      join(GroupParts(d, g, VW));
+    } else {
+      join(ScannedParts(d, g, VW, d.shifted ? dev::misalignment(xs) : 0));
     }
   }
 }
@@ -1682,7 +1786,7 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
 // after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
 template <typename T>
 __global__ void __launch_bounds__(kSumsThreads)
-k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
+k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
                int64_t reps, T* dbeta, T* dgamma) {
   dev::pdl_trigger();
   dev::pdl_wait();
@@ -1691,18 +1795,20 @@ k_gn_grad_join(const float* gpart, GnDims d, float* m1, float* m2, int join_bloc
     return;
   }
   const int lane = threadIdx.x & 31;
-  const int64_t parts = int64_t(d.p.chunks) * d.p.tiles, per = kSumsThreads / 32;
+  const int64_t of_sample = int64_t(d.p.chunks) * d.p.tiles * d.slots, per = kSumsThreads / 32;
   const float scale = 1.0f / (float(d.S) * float(d.D));
   for (int64_t i = int64_t(threadIdx.x / 32) * join_blocks + blockIdx.x; i < d.N * d.G; i += join_blocks * per) {
     const int64_t n = quotient(i, d.G);
-    const float2* src = reinterpret_cast<const float2*>(gpart) + n * parts * d.G + (i - n * d.G);
+    const float2* src = reinterpret_cast<const float2*>(gpart) + n * of_sample;
     float a = 0.f, b = 0.f;
+    with_parts(d, static_cast<int>(i - n * d.G), x + n * d.L, [&](const auto& parts) {
 #pragma unroll 8
-    for (int64_t k = lane; k < parts; k += 32) {
-      const float2 v = __ldcg(src + k * d.G);
-      a += v.x;
-      b += v.y;
-    }
+      for (unsigned k = lane; k < parts.count; k += 32) {
+        const float2 v = parts.load(src, k);
+        a += v.x;
+        b += v.y;
+      }
+    });
     a = dev::warp_sum(a);
     b = dev::warp_sum(b);
     if (lane == 0) {
@@ -1718,10 +1824,15 @@ constexpr int kGeneralCtas = 8;
 
 int64_t vec_width(DType t) { return t == DType::F32 ? 4 : 8; }
 
+// The most groups of D channels that a tile's run of channels can meet.
+int slots_of(const WalkPlan& p, int64_t vw, int64_t G, int64_t D) {
+  return p.tiles == 1 ? int(G) : int(std::min(G, (p.tile_frags * vw + D - 2) / D + 1));
+}
+
 // `periods`: walk rows are whole periods of the channels, as the gradient's channel
 // sums want them; else a sample shorter than a period is a walk row by itself.
 GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, bool periods) {
-  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, 0, {}};
+  GnDims d{N, S, S * C, int(C), int(G), int(C / G), eps, 0, 0, 0, false, false, 0, false, false, 0, {}};
   d.p = make_walk(d.L, C, int(vec_width(t)), N, kPlanSms * 2, 4);
   d.ctas = kPlanSms * 2;
   if (d.p.tiles > 1 && C % vec_width(t) != 0) {  // the general kernels: no stages, so more blocks an SM
@@ -1738,6 +1849,7 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, b
       d.p.chunks = 1;
     }
   }
+  d.slots = slots_of(d.p, vec_width(t), G, d.D);
   d.frags = d.L / vec_width(t);
   d.full_rows = d.frags / d.p.row_frags;
   d.rest = int(d.frags % d.p.row_frags);
@@ -1772,7 +1884,7 @@ GnWorkspace gn_workspace(const GnDims& d) {
   GnWorkspace w;
   const size_t stats = pad16(size_t(d.N) * d.G * 4);
   w.partial = 0;
-  w.mean = size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 16;
+  w.mean = size_t(d.N) * d.p.chunks * d.p.tiles * d.slots * 16;
   w.inv = w.mean + stats;
   w.total = w.inv + stats;
   return w;
@@ -1786,7 +1898,7 @@ GnGradWorkspace gn_grad_workspace(const GnDims& d, DType t) {
   const size_t stats = pad16(size_t(d.N) * d.G * 4);
   const int64_t width = d.p.tiles > 1 ? d.p.row_frags * vec_width(t) : d.C;
   w.gpart = 0;
-  w.m1 = pad16(size_t(d.N) * d.p.chunks * d.p.tiles * d.G * 8);
+  w.m1 = pad16(size_t(d.N) * d.p.chunks * d.p.tiles * d.slots * 8);
   w.m2 = w.m1 + stats;
   w.cpart = w.m2 + stats;
   w.total = w.cpart + size_t(grad_rows(d)) * width * 8;
@@ -1836,6 +1948,8 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   // the staged passes want whole fragments; the statistics need no alignment of y
   const bool vec = misalign16(x) == misalign16(y);
   d.here = staged && vec && join_in_pass2(d);
+  d.staged = staged;
+  d.shifted = !staged;
   cudaError_t e;
   if (staged) {
     auto f = group ? k_gn_stats_staged<T, true, false>
@@ -1849,8 +1963,18 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   }
   if (e != cudaSuccess) return e;
   if (partial != nullptr && !d.here) {
-    const int64_t joins = std::min<int64_t>((d.N * d.G + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kPlanSms * 8);
-    e = launch(k_gn_join<T>, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv);
+    // parts of a group at most, and the lanes that take them
+    const int64_t tile = d.p.tile_frags * VW, of_group = std::min<int64_t>(d.p.tiles, (d.D + tile - 2) / tile + 1);
+    const bool many = !staged || d.p.tiles == 1 || d.p.chunks * of_group > 32;
+    int log_lanes = 0;
+    while (!many && (1 << log_lanes) < d.p.chunks * of_group) ++log_lanes;
+    auto f = d.p.tiles == 1 || (!staged && d.slots == d.G) ? k_gn_join<T, 0, kJoinKept>
+             : !staged                                     ? k_gn_join<T, 2, kJoinKept>
+             : many                                        ? k_gn_join<T, 1, 4>
+                                                           : k_gn_join<T, 1, 1>;
+    const int64_t groups = kJoinThreads >> (many ? 5 : log_lanes);  // of a block
+    const int64_t joins = std::min<int64_t>((d.N * d.G + groups - 1) / groups, kPlanSms * 8);
+    e = launch(f, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv, log_lanes);
     if (e != cudaSuccess) return e;
     *launches += 1;
   }
@@ -1896,6 +2020,8 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   const bool staged = misalign16(x) == 0 && same && (!odd || d.p.tiles == 1);
   const bool vec1 = same && (d.L % VW == 0 || rows >= d.N * d.p.chunks);
   const bool vec2 = same && misalign16(x) == misalign16(dx);
+  d.staged = staged;
+  d.shifted = !staged && vec1;
   cudaError_t e;
   if (staged) {
     auto pick = [&](auto silu) {
@@ -1916,7 +2042,7 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   const int64_t joins = std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms);
   const int64_t sums = cpart != nullptr ? std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, kPlanSms * 4) : 0;
   // (the sums of du are dbeta, those of du * h are dgamma)
-  e = launch(k_gn_grad_join<T>, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, gpart, d, m1, m2, int(joins), cpart,
+  e = launch(k_gn_grad_join<T>, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, x, gpart, d, m1, m2, int(joins), cpart,
              rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
   if (e != cudaSuccess) return e;
   *launches += 1;
