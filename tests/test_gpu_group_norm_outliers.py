@@ -1,0 +1,67 @@
+"""GroupNorm's statistics where the values that a kernel might centre its sums on
+are outliers: the variance must keep its digits all the same.
+
+Ordinary values are +-(0.75 .. 1.25).  An outlying centre is told from the sums
+(far off the mean in standard deviations) and replaced, so what is left is a
+centre among the ordinary values or at the mean: at most 1.25 + |mean| off, k^2 <
+2.5 variances.  A sum of squares about it is (1 + k^2) times the variance's, its
+terms positive, so with sums of depth d the variance is off by (1 + k^2) (d + 8) u
+at most, relatively, and 1/sqrt by half of that.  The mean is off by (d + 8) u
+times the mean distance from the centre, and by two roundings of its own.
+
+Depth: a thread adds at most 256 rows under one centre, then come the block's
+sums, at most 8 + 16; a fused block's threads add 8 rows, and a lane up to 128
+columns; a token's lanes 8 values and 5 steps.
+"""
+import pytest
+import torch
+
+from tests._helpers import U32
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def ordinary(shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    size = torch.rand(shape, device="cuda", generator=g).mul_(0.5).add_(0.75)
+    sign = torch.randint(0, 2, shape, device="cuda", generator=g, dtype=torch.int8).mul_(2).sub_(1)
+    return size.mul_(sign).to(DT[dtype])
+
+
+def definition(x, groups):
+    """mean, 1/sqrt(var + eps) and the mean distance from the mean, in float64, (N, groups)."""
+    mean, inv, dist = [], [], []
+    for s in x:
+        v = s.double().view(s.shape[0], groups, -1)
+        m = v.mean((0, 2), keepdim=True)
+        mean.append(m.flatten())
+        inv.append(1.0 / torch.sqrt(((v - m) ** 2).mean((0, 2)) + EPS))
+        dist.append((v - m).abs().mean((0, 2)))
+    return torch.stack(mean), torch.stack(inv), torch.stack(dist)
+
+
+def check(lib, x, groups, depth):
+    c = x.shape[-1]
+    gamma, beta = torch.ones(c, dtype=x.dtype, device="cuda"), torch.zeros(c, dtype=x.dtype, device="cuda")
+    y, mean, inv = lib.ep_group_norm(x, gamma, beta, groups, EPS, mean=True, inv_std_dev=True)
+    m, r, dist = definition(x, groups)
+    off_mean = ((mean.double() - m).abs() / (U32 * ((depth + 8) * (dist + 1.5) + 2 * m.abs()))).max()
+    off_inv = ((inv.double() - r).abs() / (U32 * 1.75 * (depth + 8) * r)).max()
+    assert float(off_mean) <= 1 and float(off_inv) <= 1, (float(off_mean), float(off_inv))
+    return y, mean, inv
+
+
+# (N, S, C), groups, dtype.  So many samples that a chunk has many rows: one position a walk
+# row, two tiles of one, whole samples that start anywhere, and the kernels for any C.
+SPLIT = [((160, 1024, 516), 4, "f32"), ((160, 1024, 1032), 3, "f16"), ((160, 600, 2052), 9, "f32"),
+         ((310, 2048, 255), 5, "f32"), ((310, 2048, 255), 1, "bf16"), ((2, 3000, 64), 4, "f32")]
+
+
+@pytest.mark.parametrize("shape,groups,dtype", SPLIT)
+def test_outlying_first_value(lib, shape, groups, dtype):
+    x = ordinary(shape, dtype, 1 + sum(shape))
+    x.view(shape[0], shape[1], groups, -1)[:, 0, :, 0] = 30000.0
+    check(lib, x, groups, 256 + 24)

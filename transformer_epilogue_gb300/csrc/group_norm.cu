@@ -21,10 +21,11 @@
 //                           repeat within a block's 256 fragments (or C % VW == 0)
 //   general split (here)    everything else
 // The split forms walk each sample as column_walk.cuh describes.  Pass 1 leaves
-// (count, mean, sum of squared distances) per chunk and group, a small kernel (or
-// pass 2 itself) joins the chunks, pass 2 reads x again, from L2 where it fits, and
-// writes y.  The statistics are taken relative to values near their mean
-// throughout, so that a large mean costs the variance nothing.  The gradient has
+// (count, centre, mean - centre, sum of squared distances from the mean) per chunk
+// and group, a small kernel (or pass 2 itself) joins the chunks, pass 2 reads x again,
+// from L2 where it fits, and writes y.  The statistics are taken relative to values
+// near their mean throughout, and a part keeps its own centre beside the distance
+// from it, so that neither a large mean nor an outlying value costs them digits.  The gradient has
 // the same three steps, with per-channel sums of du and du * h beside the groups'.
 // A split form's floor is three reads and writes, not two, where x is larger than
 // L2: bf16 8x16384x512 (134 MB) takes 64 us, 60 at the copy rate; small ones are
@@ -177,7 +178,7 @@ struct Sample {
 
 // An item's parts: `slots` for each tile of the walk row, from the tile's first group
 // on (modulo G), so that scratch grows with the groups and not with groups x tiles
-// (f16 1x64x65536 in 65536 groups: 303 MB to 11).
+// (f16 1x64x65536 in 65536 groups: 303 MB to 10).
 //  staged: channels do not wrap around in a tile, so group g is in the tiles t0 ...
 //  that its channels reach, in all but the first of them as the first group;
 //  general: a tile's channels may wrap around and start off the sample; the join looks
@@ -271,11 +272,12 @@ struct Ends {
 // offset and repeats.
 // ---------------------------------------------------------------------------
 
-// The threads' (count, mean, M2) for each position, in shared memory, to the
-// item's groups: two sums, the second relative to the first's mean.
+// The threads' (count, centre, mean - centre, M2) for each position, in shared memory,
+// to the item's groups: two sums, of the means' distances from one of them and then
+// relative to the first's mean.
 template <typename T>
 __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, const Range& r, int64_t item, int off,
-                                                const T* xs, int warps, const float* s_cnt, const float* s_mean,
+                                                int warps, const float* s_cnt, const float* s_ref, const float* s_mean,
                                                 const float* s_m2, float4* partial, float* mean_out, float* inv_out) {
   const WalkPlan& p = d.p;
   const GroupWalk walk(p, t.tile, t.frags, d.C, d.D, dev::Vec16<T>::N);
@@ -288,17 +290,21 @@ __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, 
       if (lane == 0) *out = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
-    float c = 0.f, s = 0.f, q = 0.f;
-    walk.run(g, off, [&](int i) {
-      c += s_cnt[i];
-      s = fmaf(s_cnt[i], s_mean[i], s);
+    float c = 0.f, s = 0.f, q = 0.f, ref = 0.f;
+    walk.run(g, off, [&](int i) {  // relative to the lane's first mean
+      const float n = s_cnt[i], z = s_ref[i], m = s_mean[i];
+      if (c == 0.f) ref = z + m;
+      c += n;
+      s = fmaf(n, (z - ref) + m, s);
     });
+    const float own = ref;
+    ref = __shfl_sync(0xffffffffu, own, max(0, __ffs(__ballot_sync(0xffffffffu, c > 0.f)) - 1));
+    s = dev::warp_sum(c > 0.f ? fmaf(c, own - ref, s) : 0.f);
     c = dev::warp_sum(c);
-    s = dev::warp_sum(s);
     const float mg = c > 0.f ? s / c : 0.f;
     float res = 0.f;  // what rounding s / c and the sum left out of the mean
     walk.run(g, off, [&](int i) {
-      const float w = s_mean[i] - mg;
+      const float w = ((s_ref[i] - ref) + s_mean[i]) - mg;
       res = fmaf(s_cnt[i], w, res);
       q += fmaf(s_cnt[i] * w, w, s_m2[i]);
     });
@@ -308,10 +314,10 @@ __device__ __forceinline__ void join_statistics(const GnDims& d, const Tile& t, 
       const float fix = c > 0.f ? res / c : 0.f;
       const float mf = mg + fix, m2g = not_negative(q - res * fix);
       if (partial == nullptr) {
-        mean_out[r.n * d.G + g] = dev::ld1_keep(xs + int64_t(g) * d.D) + mf;
+        mean_out[r.n * d.G + g] = ref + mf;
         inv_out[r.n * d.G + g] = 1.0f / sqrtf(m2g / c + d.eps);
       } else {
-        *out = make_float4(c, mf, m2g, 0.f);
+        *out = make_float4(c, ref, mf, m2g);
       }
     }
   }
@@ -761,8 +767,7 @@ struct RowStream {
 // The barrier of a staged kernel's consumers.
 __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blockDim.x - 32); }
 
-// Pass 1.  partial: [item][tile][slot] x (count, mean, M2, the group's first value in
-// the sample), the mean relative to that value.  The block takes its values relative to
+// Pass 1.  partial: [item][tile][slot] x (count, centre, mean - centre, M2).  The block takes its values relative to
 // a centre of each group, so that its sums and sums of squares simply add up: the
 // median of three of the group's values in the item's first walk row, which lies
 // among the values unless two of the three are outliers.  Off by k standard
@@ -920,8 +925,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                  n = float((qb - qa) * d.D + (ib - ia));
                }
                const float m = n > 0.f ? a / n : 0.f;
-               const float first = dev::ld1_keep(xs + int64_t(cols.g0 + g) * d.D);
-               out[g] = make_float4(n, (centre[g] - first) + m, not_negative(b - a * m), first);
+               out[g] = make_float4(n, centre[g], m, not_negative(b - a * m));
              });
     consumer_sync();
   }
@@ -943,25 +947,23 @@ __device__ __forceinline__ void join_stats_here(const float4* partial, const GnD
   const int slice = static_cast<int>(threadIdx.x / unsigned(d.G)), g = threadIdx.x - slice * d.G;
   const float4* src = partial + n * d.p.chunks * d.G + g;
   const float4 first = __ldcg(src), last = __ldcg(src + (d.p.chunks - 1) * d.G);
-  const float mid = __ldcg(src + (d.p.chunks - 1) / 2 * d.G).y;
-  const float centre = median3(first.y, mid, last.x > 0.f ? last.y : first.y);  // (the last may be empty)
+  const float4 mid = __ldcg(src + (d.p.chunks - 1) / 2 * d.G);
+  const float mean0 = first.y + first.z;
+  const float centre = median3(mean0, mid.y + mid.z, last.x > 0.f ? last.y + last.z : mean0);  // (the last may be empty)
   float a = 0.f, b = 0.f;
   if (slice < slices) {
 #pragma unroll 8
     for (int k = slice; k < d.p.chunks; k += slices) {
       const float4 v = __ldcg(src + k * d.G);
-      const float w = v.y - centre, cw = v.x * w;
+      const float w = (v.y - centre) + v.z, cw = v.x * w;
       a += cw;
-      b += fmaf(cw, w, v.z);
+      b += fmaf(cw, w, v.w);
     }
   }
   consumer_sync();  // (the sample before has been read)
   js.a[threadIdx.x] = a;
   js.b[threadIdx.x] = b;
-  if (slice == 0) {
-    js.mean[g] = centre;
-    js.inv[g] = first.w;
-  }
+  if (slice == 0) js.mean[g] = centre;
   consumer_sync();
   const float total = float(d.S) * float(d.D);
   sum_sets(threads, d.G, slices,
@@ -971,7 +973,7 @@ __device__ __forceinline__ void join_stats_here(const float4* partial, const GnD
            },
            [&](int i, float sa, float sb) {
              const float m = sa / total;
-             js.mean[i] = js.inv[i] + (js.mean[i] + m);  // the group's first value + (the centre + m)
+             js.mean[i] += m;
              js.inv[i] = 1.0f / sqrtf(not_negative(sb - sa * m) / total + d.eps);
            });
   consumer_sync();
@@ -1466,7 +1468,8 @@ __global__ void __launch_bounds__(kWalkThreads)
 k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_out) {
   constexpr int VW = dev::Vec16<T>::N;
   constexpr int U = 4;
-  __shared__ float s_cnt[kWalkThreads * VW], s_mean[kWalkThreads * VW], s_m2[kWalkThreads * VW];
+  __shared__ float s_cnt[kWalkThreads * VW], s_ref[kWalkThreads * VW], s_mean[kWalkThreads * VW],
+      s_m2[kWalkThreads * VW];
   dev::pdl_wait();
   dev::pdl_trigger();
   const WalkPlan& p = d.p;
@@ -1476,14 +1479,9 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
     const T* xs = x + r.n * d.L;
     const int off = walk_offset<T, true>(xs);
     if (t.mine) {
-      float first[VW], c[VW], s[VW], q[VW], cnt[VW];
-      for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D,
-                       [&](int e, int, int g) { first[e] = dev::ld1_keep(xs + int64_t(g) * d.D); });
+      float c[VW], s[VW], q[VW], cnt[VW];  // c: the first value that the channel meets here
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        c[e] = first[e];  // then the first value that the channel meets here
-        s[e] = q[e] = cnt[e] = 0.f;
-      }
+      for (int e = 0; e < VW; ++e) c[e] = s[e] = q[e] = cnt[e] = 0.f;
       for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
         float v[U][VW];
 #pragma unroll
@@ -1508,13 +1506,14 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
       for (int e = 0; e < VW; ++e) {
         const float m = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
         s_cnt[threadIdx.x * VW + e] = cnt[e];
-        s_mean[threadIdx.x * VW + e] = (c[e] - first[e]) + m;
+        s_ref[threadIdx.x * VW + e] = c[e];
+        s_mean[threadIdx.x * VW + e] = m;
         s_m2[threadIdx.x * VW + e] = not_negative(q[e] - s[e] * m);
       }
     }
     __syncthreads();
-    join_statistics<T>(d, t, r, it.item(), off, xs, blockDim.x / 32, s_cnt, s_mean, s_m2, partial, mean_out,
-                           inv_out);
+    join_statistics<T>(d, t, r, it.item(), off, blockDim.x / 32, s_cnt, s_ref, s_mean, s_m2, partial, mean_out,
+                       inv_out);
     __syncthreads();
   }
 }
@@ -1699,7 +1698,9 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 
 constexpr int kJoinThreads = 64;
 
-// (count, mean, M2) of the parts -> the group's statistics.  `lanes` of a warp (a power
+// (count, centre, mean - centre, M2) of the parts -> the group's statistics, the means
+// relative to that of the first lane's first part (of a group's parts only ScannedParts
+// can be empty there: to the group's first value).  `lanes` of a warp (a power
 // of two) take one (n, g), each keeping up to KEPT parts in registers for the second
 // sum and reading others again.  How a group's parts are found (WAY) is a kernel of
 // its own: the code runs once, so what it does not need costs it instruction fetches
@@ -1740,17 +1741,21 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
       float4 kept[KEPT];
 #pragma unroll
       for (int u = 0; u < KEPT; ++u) kept[u] = part(lane + u * 32);
+      const int lead = (threadIdx.x & 31) - lane;
+      const float mean0 = __shfl_sync(0xffffffffu, kept[0].y + kept[0].z, lead);
+      const float ref = __shfl_sync(0xffffffffu, kept[0].x, lead) > 0.f ? mean0 : first;
       float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
+      auto add = [&](float4& v) {
+        v.y = (v.y - ref) + v.z;
+        c += v.x;
+        s = fmaf(v.x, v.y, s);
+      };
 #pragma unroll
-      for (int u = 0; u < KEPT; ++u) {
-        c += kept[u].x;
-        s = fmaf(kept[u].x, kept[u].y, s);
-      }
+      for (int u = 0; u < KEPT; ++u) add(kept[u]);
       if constexpr (KEPT > 1) {
         for (unsigned k = lane + KEPT * 32; k < parts.count; k += 32) {
-          const float4 v = part(k);
-          c += v.x;
-          s = fmaf(v.x, v.y, s);
+          float4 v = part(k);
+          add(v);
         }
       }
       c = sum(c);
@@ -1758,17 +1763,22 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
       auto square = [&](const float4& v) {
         const float w = v.y - mg;
         res = fmaf(v.x, w, res);
-        q += fmaf(v.x * w, w, v.z);
+        q += fmaf(v.x * w, w, v.w);
       };
 #pragma unroll
       for (int u = 0; u < KEPT; ++u) square(kept[u]);
-      if constexpr (KEPT > 1)
-        for (unsigned k = lane + KEPT * 32; k < parts.count; k += 32) square(part(k));
+      if constexpr (KEPT > 1) {
+        for (unsigned k = lane + KEPT * 32; k < parts.count; k += 32) {
+          float4 v = part(k);
+          v.y = (v.y - ref) + v.z;
+          square(v);
+        }
+      }
       res = sum(res);
       q = sum(q);
       if (live && lane == 0) {
         const float fix = res / c;  // what rounding left out of the mean
-        mean_out[i] = first + (mg + fix);
+        mean_out[i] = ref + (mg + fix);
         inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
       }
     };
