@@ -61,7 +61,29 @@ SPLIT = [((160, 1024, 516), 4, "f32"), ((160, 1024, 1032), 3, "f16"), ((160, 600
 
 
 @pytest.mark.parametrize("shape,groups,dtype", SPLIT)
+@pytest.mark.parametrize("where", ["first", "first and last", "middle and last"])
+def test_outlying_positions(lib, shape, groups, dtype, where):
+    x = ordinary(shape, dtype, sum(shape))
+    s = shape[1]
+    for name, at in (("first", 0), ("middle", s // 2), ("last", s - 1)):
+        if name in where:
+            x[:, at] = 300.0
+    check(lib, x, groups, 256 + 24)
+
+
+@pytest.mark.parametrize("shape,groups,dtype", SPLIT)
 def test_outlying_first_value(lib, shape, groups, dtype):
     x = ordinary(shape, dtype, 1 + sum(shape))
     x.view(shape[0], shape[1], groups, -1)[:, 0, :, 0] = 30000.0
+    check(lib, x, groups, 256 + 24)
+
+
+@pytest.mark.parametrize("shape,groups,dtype", [((2, 3000, 64), 4, "f32"), ((2, 4096, 320), 32, "f16"),
+                                                ((3, 1331, 189), 9, "f32"), ((1, 9000, 40), 1, "f32")])
+def test_outlying_chunks(lib, shape, groups, dtype):
+    # whole chunks (a share of the positions at both ends) away from the others
+    x = ordinary(shape, dtype, 2 + sum(shape))
+    s = shape[1]
+    for a, b in ((0, s // 60), (s - s // 60, s)):
+        x[:, a:b] += 300.0
     check(lib, x, groups, 256 + 24)

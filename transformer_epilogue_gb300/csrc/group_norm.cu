@@ -753,11 +753,6 @@ struct RowStream {
       }
     });
   }
-  // The next stage (an item's first), once its rows are there.
-  __device__ __forceinline__ const unsigned char* peek() {
-    ok = ok && dev::mbar_wait(&bars->full[ring.st], ring.phase);
-    return smem + ring.st * kStageBytes;
-  }
   // Rows of an item that have a fragment in column j (0 where the thread has none).
   __device__ __forceinline__ int mine(const Range& range, const Tile& t) const {
     return t.mine ? static_cast<int>(max(int64_t(0), min(range.rb, of_column(sample(range.n), t.j)) - range.ra)) : 0;
@@ -767,11 +762,13 @@ struct RowStream {
 // The barrier of a staged kernel's consumers.
 __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blockDim.x - 32); }
 
-// Pass 1.  partial: [item][tile][slot] x (count, centre, mean - centre, M2).  The block takes its values relative to
-// a centre of each group, so that its sums and sums of squares simply add up: the
-// median of three of the group's values in the item's first walk row, which lies
-// among the values unless two of the three are outliers.  Off by k standard
-// deviations it costs the variance k^2 2^-24 of its value.
+// Pass 1.  partial: [item][tile][slot] x (count, centre, mean - centre, M2).  The block
+// takes its values relative to a centre of each group, so that its sums and sums of
+// squares simply add up: the median of three of the group's values in the item's first,
+// middle and last position.  Off by k standard deviations it multiplies the rounding of
+// the sums by 1 + k^2; where far_off() shows k > 4 (two of the three are outliers) the
+// item is gone over again about the mean so found, from L2, and the groups whose
+// centre stays get the same sums again.  An item has at most kCentreRows walk rows.
 template <typename T, bool GROUP, bool ODD>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
@@ -816,51 +813,38 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
       for (int g = threadIdx.x; g < d.slots; g += consumers) out[g] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
-    float c[EV], s[VW], q[VW];
-#pragma unroll
-    for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
     const int off = ODD ? rows.sample(r.n).off : 0;
     const Ends ends = rows.ends(r, t);
     const T* xs = x + r.n * d.L;
-    int64_t e_a = 0, e_b = 0;  // ODD: the item's elements of the sample
-    if constexpr (ODD) {
-      e_a = max(int64_t(0), r.ra * p.row_frags * VW - off);
-      e_b = min(d.L, r.rb * p.row_frags * VW - off);
-      // positions of the sample that begin in the item (or its last)
-      const int64_t s0 = min(quotient(e_a + d.C - 1, d.C), d.S - 1), s1 = max(s0, quotient(e_b, d.C) - 1);
-      for (int g = threadIdx.x; g < d.G; g += consumers) {
-        const int c = g * d.D;
-        centre[g] = median3(dev::to_float(xs[s0 * d.C + c]), dev::to_float(xs[(s0 + s1) / 2 * d.C + c + d.D / 2]),
-                            dev::to_float(xs[s1 * d.C + c + d.D - 1]));
+    // ODD: the item's elements of the sample
+    auto from = [&] { return max(int64_t(0), r.ra * p.row_frags * VW - off); };
+    auto to = [&] { return min(d.L, r.rb * p.row_frags * VW - off); };
+    {
+      // positions of the sample (repeats of the channels) in the item (ODD: that begin in it)
+      int64_t pos0 = r.ra * p.reps, pos1 = min(r.rb * p.reps, d.S);
+      if constexpr (ODD) {
+        pos0 = min(quotient(from() + d.C - 1, d.C), d.S - 1);
+        pos1 = max(pos0 + 1, quotient(to(), d.C));
+        if (t.mine) for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int, int g) { if (e < EV) grp[e] = g; });
       }
-      if (t.mine) for_channels<VW>(first_channel(t.j, VW, off, d.C), d.C, d.D, [&](int e, int, int g) { if (e < EV) grp[e] = g; });
-    }
-    // positions of the sample (repeats of the channels) in the item, and in its first walk row
-    const int64_t pos0 = r.ra * p.reps, pos1 = min(r.rb * p.reps, d.S);
-    if constexpr (!ODD) {
-    const T* row0 = reinterpret_cast<const T*>(rows.peek());
-    const int n_rep = static_cast<int>(min(int64_t(cols.reps), pos1 - pos0));
-    for (int g = threadIdx.x; g < cols.n_groups; g += consumers) {
-      const int lo = cols.lo(g) * per, n = (cols.hi(g) - cols.lo(g)) * per, step = cols.cols * per;
-      centre[g] = median3(dev::to_float(row0[lo]), dev::to_float(row0[lo + n / 2 + n_rep / 2 * step]),
-                          dev::to_float(row0[lo + n - 1 + (n_rep - 1) * step]));
-    }
+      const T* first = xs + pos0 * d.C + int64_t(t.tile) * p.tile_frags * VW;
+      const int64_t mid = (pos1 - 1 - pos0) / 2 * d.C, last = (pos1 - 1 - pos0) * d.C;
+      for (int g = threadIdx.x; g < cols.n_groups; g += consumers) {
+        const int lo = cols.lo(g) * per, n = (cols.hi(g) - cols.lo(g)) * per;
+        centre[g] = median3(dev::to_float(first[lo]), dev::to_float(first[mid + lo + n / 2]),
+                            dev::to_float(first[last + lo + n - 1]));
+      }
     }
     consumer_sync();
+    const int mine = rows.mine(r, t);
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+      float c[EV], s[VW], q[VW];
 #pragma unroll
-    for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
-    rows.consume(r, rows.mine(r, t), [&](int row, const auto& raw) {
+      for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
 #pragma unroll
-      for (const auto& one : raw) {
-        float v[VW];
-        dev::Conv<T>::unpack(one[0], v);
-        if (ODD && ends.has(row)) {  // what is outside counts as the centre
-          dev::load_frag<T, false>(xs, ends.e0 + row * ends.pitch, d.L, v);
-#pragma unroll
-          for (int e = 0; e < VW; ++e)
-            if (!ends.inside(row, e)) v[e] = c[EV == 1 ? 0 : e];
-        }
-        ++row;
+      for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
+      auto add = [&](float (&v)[VW]) {
 #pragma unroll
         for (int e = 0; e < VW; e += 2) {
           const float2 m = pair_of<VW>(c, e);
@@ -870,64 +854,99 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
         }
         dev::add_pairs(s, v);
         fma_pairs(v, v, q);
-      }
-    });
-    if (t.mine) {
-      if constexpr (EV == 1) {
+      };
+      auto centre_outside = [&](int row, float (&v)[VW]) {  // what is outside counts as the centre
 #pragma unroll
-        for (int e = 1; e < VW; ++e) {
-          s[0] += s[e];
-          q[0] += q[e];
-        }
-        s_a[threadIdx.x] = s[0];
-        s_b[threadIdx.x] = q[0];
+        for (int e = 0; e < VW; ++e)
+          if (!ends.inside(row, e)) v[e] = c[EV == 1 ? 0 : e];
+      };
+      if (!again) {
+        rows.consume(r, mine, [&](int row, const auto& raw) {
+#pragma unroll
+          for (const auto& one : raw) {
+            float v[VW];
+            dev::Conv<T>::unpack(one[0], v);
+            if (ODD && ends.has(row)) {
+              dev::load_frag<T, false>(xs, ends.e0 + row * ends.pitch, d.L, v);
+              centre_outside(row, v);
+            }
+            ++row;
+            add(v);
+          }
+        });
       } else {
-        put(s_a, s);
-        put(s_b, q);
+        const int64_t pitch = p.row_frags * VW, e0 = (r.ra * p.row_frags + t.j) * VW - off;
+#pragma unroll 2
+        for (int row = 0; row < mine; ++row) {
+          float v[VW];
+          dev::load_frag<T, true>(xs, e0 + row * pitch, d.L, v);
+          if (ODD && ends.has(row)) centre_outside(row, v);
+          add(v);
+        }
       }
-    }
-    consumer_sync();
-    // to the first repeat's place (ODD: to the centre's other side, after all places have been read)
-    float* t_a = s_a;
-    float* t_b = s_b;
-    if (ODD) {
-      t_a = centre + kWalkThreads * EV;
-      t_b = t_a + kWalkThreads * EV;
-    }
-    if (ODD || cols.reps > 1) {
-      sum_sets(consumers, cols.cols, cols.reps,
-               [&](int i, int k, float& a, float& b) {
-                 const int pos = cols.at<ODD>(i, k, off);
-                 a += s_a[pos];
-                 b += s_b[pos];
-               },
-               [&](int i, float a, float b) {
-                 t_a[i] = a;
-                 t_b[i] = b;
-               });
+      if (t.mine) {
+        if constexpr (EV == 1) {
+#pragma unroll
+          for (int e = 1; e < VW; ++e) {
+            s[0] += s[e];
+            q[0] += q[e];
+          }
+          s_a[threadIdx.x] = s[0];
+          s_b[threadIdx.x] = q[0];
+        } else {
+          put(s_a, s);
+          put(s_b, q);
+        }
+      }
       consumer_sync();
+      // to the first repeat's place (ODD: to the centre's other side, after all places have been read)
+      float* t_a = s_a;
+      float* t_b = s_b;
+      if (ODD) {
+        t_a = centre + kWalkThreads * EV;
+        t_b = t_a + kWalkThreads * EV;
+      }
+      if (ODD || cols.reps > 1) {
+        sum_sets(consumers, cols.cols, cols.reps,
+                 [&](int i, int k, float& a, float& b) {
+                   const int pos = cols.at<ODD>(i, k, off);
+                   a += s_a[pos];
+                   b += s_b[pos];
+                 },
+                 [&](int i, float a, float b) {
+                   t_a[i] = a;
+                   t_b[i] = b;
+                 });
+        consumer_sync();
+      }
+      bool far = false;
+      sum_sets(consumers, cols.n_groups, cols.D,
+               [&](int g, int k, float& a, float& b) {
+                 const int i = cols.lo(g) + k;
+                 if (i < cols.hi(g)) {
+                   a += t_a[i];
+                   b += t_b[i];
+                 }
+               },
+               [&](int g, float a, float b) {
+                 float n;
+                 if constexpr (ODD) {  // the group's values among the sample's first from(), first to()
+                   const int64_t ea = from(), eb = to(), qa = quotient(ea, d.C), qb = quotient(eb, d.C);
+                   const int ia = min(max(int(ea - qa * d.C) - g * d.D, 0), d.D);
+                   const int ib = min(max(int(eb - qb * d.C) - g * d.D, 0), d.D);
+                   n = float((qb - qa) * d.D + (ib - ia));
+                 } else {
+                   n = float(min(r.rb * p.reps, d.S) - r.ra * p.reps) * float((cols.hi(g) - cols.lo(g)) * per);
+                 }
+                 const float m = n > 0.f ? a / n : 0.f, m2 = not_negative(b - a * m);
+                 out[g] = make_float4(n, centre[g], m, m2);
+                 if (!again && far_off(a * m, m2)) {
+                   centre[g] += m;
+                   far = true;
+                 }
+               });
+      if (dev::named_barrier_and(1, consumers, !far)) break;
     }
-    const float positions = float(pos1 - pos0);
-    sum_sets(consumers, cols.n_groups, cols.D,
-             [&](int g, int k, float& a, float& b) {
-               const int i = cols.lo(g) + k;
-               if (i < cols.hi(g)) {
-                 a += t_a[i];
-                 b += t_b[i];
-               }
-             },
-             [&](int g, float a, float b) {
-               float n = positions * float((cols.hi(g) - cols.lo(g)) * per);
-               if constexpr (ODD) {  // the group's values among the sample's first e_a, first e_b
-                 const int64_t qa = quotient(e_a, d.C), qb = quotient(e_b, d.C);
-                 const int ia = min(max(int(e_a - qa * d.C) - g * d.D, 0), d.D);
-                 const int ib = min(max(int(e_b - qb * d.C) - g * d.D, 0), d.D);
-                 n = float((qb - qa) * d.D + (ib - ia));
-               }
-               const float m = n > 0.f ? a / n : 0.f;
-               out[g] = make_float4(n, centre[g], m, not_negative(b - a * m));
-             });
-    consumer_sync();
   }
 }
 
@@ -1828,6 +1847,10 @@ k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, i
   }
 }
 
+// Walk rows of a chunk at most, in pass 1: a thread adds them one after another under one
+// centre, and one outlying row of them costs no more than its share (see far_off).
+constexpr int64_t kCentreRows = 256;
+
 // CTAs an SM that the general kernels' plan is made for (us, 2, 8 and 16 of them: f16
 // 2x16070x1044 176, 127 and 146, its gradient 263, 217 and 236).
 constexpr int kGeneralCtas = 8;
@@ -1858,6 +1881,10 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, b
       d.p.rows = d.p.rows_per_chunk = 1;
       d.p.chunks = 1;
     }
+  }
+  if (!periods && d.p.rows_per_chunk > kCentreRows) {
+    d.p.rows_per_chunk = kCentreRows;
+    d.p.chunks = int((d.p.rows + kCentreRows - 1) / kCentreRows);
   }
   d.slots = slots_of(d.p, vec_width(t), G, d.D);
   d.frags = d.L / vec_width(t);

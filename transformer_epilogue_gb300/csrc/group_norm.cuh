@@ -172,6 +172,13 @@ __device__ __forceinline__ float median3(float a, float b, float c) {
   return fmaxf(fminf(a, b), fminf(fmaxf(a, b), c));
 }
 
+// Whether sums were taken about a centre more than 4 standard deviations off the mean:
+// `cut` = n (mean - centre)^2 against m2, what is left of the squares.  Up to there the
+// rounding of the squares reaches the variance 17 times at most; beyond (two of three
+// values outlying, 6e-9 of normal ones) it is worth summing again about the mean.
+// False for infinities and NaN, where nothing is to be gained.
+__device__ __forceinline__ bool far_off(float cut, float m2) { return cut > 16.f * m2 && cut < INFINITY; }
+
 // A sum of squares that rounding took below zero is 0 (and NaN stays NaN).
 __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : q; }
 
