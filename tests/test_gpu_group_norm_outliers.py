@@ -57,7 +57,7 @@ def check(lib, x, groups, depth):
 # (N, S, C), groups, dtype.  So many samples that a chunk has many rows: one position a walk
 # row, two tiles of one, whole samples that start anywhere, and the kernels for any C.
 SPLIT = [((160, 1024, 516), 4, "f32"), ((160, 1024, 1032), 3, "f16"), ((160, 600, 2052), 9, "f32"),
-         ((310, 2048, 255), 5, "f32"), ((310, 2048, 255), 1, "bf16"), ((2, 3000, 64), 4, "f32")]
+         ((310, 2048, 255), 5, "f32"), ((310, 2048, 255), 1, "bf16"), ((210, 1024, 513), 9, "f32"), ((2, 3000, 64), 4, "f32")]
 
 
 @pytest.mark.parametrize("shape,groups,dtype", SPLIT)

@@ -1482,6 +1482,13 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
 // fragments are loaded as 16 bytes; else value by value).
 // ---------------------------------------------------------------------------
 
+// Pass 1.  A thread takes its channels' values relative to their first in the item
+// (`ref`), and sums their distances from a running mean `c` of those: after 4 rows,
+// 8, 16 ... and then every kFoldRows the mean moves on by s / n, and the squares to it
+// (q - s (s / n), at most half of q where no more rows are new than are old: nothing
+// cancels, whatever the values).
+constexpr int kFoldRows = 64;
+
 template <typename T>
 __global__ void __launch_bounds__(kWalkThreads)
 k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_out) {
@@ -1498,9 +1505,20 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
     const T* xs = x + r.n * d.L;
     const int off = walk_offset<T, true>(xs);
     if (t.mine) {
-      float c[VW], s[VW], q[VW], cnt[VW];  // c: the first value that the channel meets here
+      float ref[VW], c[VW], m2[VW], s[VW], q[VW], cnt[VW];
 #pragma unroll
-      for (int e = 0; e < VW; ++e) c[e] = s[e] = q[e] = cnt[e] = 0.f;
+      for (int e = 0; e < VW; ++e) ref[e] = c[e] = m2[e] = s[e] = q[e] = cnt[e] = 0.f;
+      auto fold = [&] {
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const float by = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
+          m2[e] += not_negative(q[e] - s[e] * by);
+          c[e] += by;
+          s[e] = q[e] = 0.f;
+        }
+      };
+      int64_t folded = r.ra;
+      int step = U;
       for (int64_t r0 = r.ra; r0 < r.rb; r0 += U) {
         float v[U][VW];
 #pragma unroll
@@ -1512,22 +1530,27 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
 #pragma unroll
           for (int e = 0; e < VW; ++e) {
             if (r0 + u < r.rb && e0 + e >= 0 && e0 + e < d.L) {
-              if (cnt[e] == 0.f) c[e] = v[u][e];
-              const float w = v[u][e] - c[e];
+              if (cnt[e] == 0.f) ref[e] = v[u][e];
+              const float w = (v[u][e] - ref[e]) - c[e];
               cnt[e] += 1.f;
               s[e] += w;
               q[e] = fmaf(w, w, q[e]);
             }
           }
         }
+        if (r0 + U - folded >= step && r0 + U < r.rb) {
+          step = folded == r.ra ? step : min(2 * step, kFoldRows);  // 4, 4, 8, 16 ...: no more than there were
+          folded = r0 + U;
+          fold();
+        }
       }
+      fold();
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const float m = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
         s_cnt[threadIdx.x * VW + e] = cnt[e];
-        s_ref[threadIdx.x * VW + e] = c[e];
-        s_mean[threadIdx.x * VW + e] = m;
-        s_m2[threadIdx.x * VW + e] = not_negative(q[e] - s[e] * m);
+        s_ref[threadIdx.x * VW + e] = ref[e];
+        s_mean[threadIdx.x * VW + e] = c[e];
+        s_m2[threadIdx.x * VW + e] = m2[e];
       }
     }
     __syncthreads();
