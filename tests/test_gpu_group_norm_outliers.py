@@ -87,3 +87,18 @@ def test_outlying_chunks(lib, shape, groups, dtype):
     for a, b in ((0, s // 60), (s - s // 60, s)):
         x[:, a:b] += 300.0
     check(lib, x, groups, 256 + 24)
+
+
+@pytest.mark.parametrize("shape,groups,dtype", [
+    ((4, 16, 1024), 1, "f32"), ((4, 32, 1024), 1, "f16"), ((40, 16, 1000), 1, "f32"), ((4, 16, 1020), 3, "f32"),
+    ((4, 30, 1007), 1, "f16"), ((500, 3, 333), 1, "f32"), ((500, 1, 2295), 1, "f32"), ((3, 40, 189), 9, "bf16")])
+def test_outliers_in_a_small_sample(lib, shape, groups, dtype):
+    x = ordinary(shape, dtype, 3 + sum(shape))
+    g = x.view(shape[0], shape[1], groups, -1)
+    for s, d in ((0, 0), (shape[1] // 2, g.shape[-1] // 2)):
+        g[::2, s, :, d] = 1000.0   # (every second sample: the others' results must not depend on it)
+    y, mean, inv = check(lib, x, groups, 8 + 8 + 128 + 16)
+    clean = ordinary(shape, dtype, 3 + sum(shape))
+    y0, mean0, inv0 = check(lib, clean, groups, 8 + 8 + 128 + 16)
+    for a, b in ((y, y0), (mean, mean0), (inv, inv0)):
+        assert torch.equal(a[1::2], b[1::2])

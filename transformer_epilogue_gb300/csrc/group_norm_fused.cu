@@ -17,9 +17,11 @@
 //
 // Statistics: sums and sums of squares of the distances from a centre of the group,
 // the median of three of its values (the first, a middle, the last), so that no
-// single outlier moves it: k standard deviations off the mean it costs the variance
-// k^2 2^-24 of its value.  All in float32, in an order that does not depend on
-// timing.  (The squares about the mean, as a second pass over the registers, took two
+// single outlier moves it: k standard deviations off the mean it multiplies the
+// rounding of the sums by 1 + k^2.  Where far_off() shows k > 4 (two outliers of the
+// three) the block sums again, from its registers, about the means so found, and the
+// groups concerned take those sums.  All in float32, in an order that does not depend
+// on timing.  (The squares about the mean in every block, as a second pass, took two
 // more block sums: f16 1x64x256 5.7 us and 4.7, f32 9651x2x459 122 and 68.)
 //
 // What bounds it: the latency of load, two block reductions and store (f16 1x64x256
@@ -346,33 +348,45 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
   const Entries<MODE> entries(p, d.D, VW, start);
   __syncthreads();
 
-  float m[EV], s[EV], q[EV];
+  bool far = false;
+  auto statistics = [&](auto second) {
+    constexpr bool again = decltype(second)::value;
+    float m[EV], s[EV], q[EV];
 #pragma unroll
-  for (int e = 0; e < EV; ++e) m[e] = at.kn > 0 ? gm[grp[e]] : 0.f;
-  centred_sums<T, NV, MODE>(raw, at, m, s, q);
-  if (mine) {
-    put_entries(ent_a, s);
-    put_entries(ent_b, q);
+    for (int e = 0; e < EV; ++e) m[e] = at.kn > 0 ? gm[grp[e]] : 0.f;
+    centred_sums<T, NV, MODE>(raw, at, m, s, q);
+    if (mine) {
+      put_entries(ent_a, s);
+      put_entries(ent_b, q);
+    }
+    __syncthreads();
+    entries.run(
+        ent_a, ent_b, col_a, col_b,
+        [&](int i, float& a, float& b) {
+          a += ent_a[i];
+          b += ent_b[i];
+        },
+        [&](int s, int ns, float a, float b) {
+          if (again && !(gr[s] < 0.f)) return;  // this group's centre was near
+          const float m = a * d.scale;  // from the centre
+          const float m2 = not_negative(b - a * m);
+          const float mean = gm[s] + m, r = 1.0f / sqrtf(m2 * d.scale + d.eps);
+          const bool redo = !again && far_off(a * m, m2);
+          far |= redo;
+          gm[s] = mean;
+          gr[s] = redo ? -r : r;
+          if (n0 + ns < d.N) {
+            const int64_t i = n0 * d.G + s;  // (slots are samples' groups in order)
+            if (mean_out != nullptr) mean_out[i] = mean;
+            if (inv_out != nullptr) inv_out[i] = r;
+          }
+        });
+  };
+  statistics(std::false_type{});
+  if (__syncthreads_or(far)) {
+    statistics(std::true_type{});
+    __syncthreads();
   }
-  __syncthreads();
-  entries.run(
-      ent_a, ent_b, col_a, col_b,
-      [&](int i, float& a, float& b) {
-        a += ent_a[i];
-        b += ent_b[i];
-      },
-      [&](int s, int ns, float a, float b) {
-        const float m = a * d.scale;  // from the centre
-        const float mean = gm[s] + m, r = 1.0f / sqrtf(not_negative(b - a * m) * d.scale + d.eps);
-        gm[s] = mean;
-        gr[s] = r;
-        if (n0 + ns < d.N) {
-          const int64_t i = n0 * d.G + s;  // (slots are samples' groups in order)
-          if (mean_out != nullptr) mean_out[i] = mean;
-          if (inv_out != nullptr) inv_out[i] = r;
-        }
-      });
-  __syncthreads();
 
   // y
   if (at.kn > 0) {
