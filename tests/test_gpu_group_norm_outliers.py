@@ -102,3 +102,19 @@ def test_outliers_in_a_small_sample(lib, shape, groups, dtype):
     y0, mean0, inv0 = check(lib, clean, groups, 8 + 8 + 128 + 16)
     for a, b in ((y, y0), (mean, mean0), (inv, inv0)):
         assert torch.equal(a[1::2], b[1::2])
+
+
+@pytest.mark.parametrize("shape,groups,dtype", [((2100, 1, 128), 1, "f32"), ((2100, 1, 256), 1, "bf16"),
+                                                ((1500, 1, 1024), 4, "f16")])
+def test_outliers_in_a_token(lib, shape, groups, dtype):
+    x = ordinary(shape, dtype, 4 + sum(shape))
+    vw = 4 if dtype == "f32" else 8
+    g = x.view(shape[0], shape[1], groups, -1)
+    d = g.shape[-1]
+    g[::2, :, :, 0] = 1000.0
+    g[::2, :, :, d // 2 + vw // 2] = 1000.0
+    y, mean, inv = check(lib, x, groups, 8 * max(1, d // 256) + 5)
+    clean = ordinary(shape, dtype, 4 + sum(shape))
+    y0, mean0, inv0 = check(lib, clean, groups, 8 * max(1, d // 256) + 5)
+    for a, b in ((y, y0), (mean, mean0), (inv, inv0)):
+        assert torch.equal(a[1::2], b[1::2])

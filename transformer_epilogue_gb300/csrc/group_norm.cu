@@ -1296,33 +1296,49 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
     float* pi = inv_out != nullptr && lane == lead ? inv_out + g0 : nullptr;
     rows.template consume<2>(r, static_cast<int>(r.rb - r.ra), [&](int row, const auto& raw) {
       constexpr int R = sizeof(raw) / sizeof(raw[0]);
-      // sums and sums of squares relative to a centre: the median of three of the
-      // group's values.  With at most 256 values to a group it is at most 16
-      // standard deviations off the mean, whatever they are.
-      float v[R][VW], c[R], s[2 * R];
+      // sums and sums of squares relative to a centre, the median of three of the
+      // group's values; where that is more than 4 standard deviations off the mean of one
+      // of the warp's groups (see far_off), again, with that group's mean as its centre
+      float v[R][VW], c[R], s[2 * R], m[R], var[R];
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         dev::Conv<T>::unpack(raw[u][0], v[u]);
         c[u] = median3(__shfl_sync(0xffffffffu, v[u][0], lead), __shfl_sync(0xffffffffu, v[u][VW / 2], lead + set / 2),
                        __shfl_sync(0xffffffffu, v[u][VW - 1], lead + set - 1));
       }
+      auto sums = [&] {
 #pragma unroll
-      for (int u = 0; u < R; ++u) {
-        float2 p = make_float2(0.f, 0.f), q = p;
+        for (int u = 0; u < R; ++u) {
+          float2 p = make_float2(0.f, 0.f), q = p;
 #pragma unroll
-        for (int e = 0; e < VW; e += 2) {
-          const float2 w = __fadd2_rn(make_float2(v[u][e], v[u][e + 1]), make_float2(-c[u], -c[u]));
-          p = __fadd2_rn(p, w);
-          q = __ffma2_rn(w, w, q);
+          for (int e = 0; e < VW; e += 2) {
+            const float2 w = __fadd2_rn(make_float2(v[u][e], v[u][e + 1]), make_float2(-c[u], -c[u]));
+            p = __fadd2_rn(p, w);
+            q = __ffma2_rn(w, w, q);
+          }
+          s[2 * u] = p.x + p.y;
+          s[2 * u + 1] = q.x + q.y;
         }
-        s[2 * u] = p.x + p.y;
-        s[2 * u + 1] = q.x + q.y;
+        ts.sum(s);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          m[u] = s[2 * u] * scale;
+          var[u] = not_negative(fmaf(s[2 * u + 1], scale, -m[u] * m[u]));
+        }
+      };
+      sums();
+      bool far = false;
+#pragma unroll
+      for (int u = 0; u < R; ++u) far |= m[u] * m[u] > 16.f * var[u];
+      if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+          if (far_off(m[u] * m[u], var[u])) c[u] += m[u];
+        sums();
       }
-      ts.sum(s);
 #pragma unroll
       for (int u = 0; u < R; ++u) {
-        const float m = s[2 * u] * scale, mu[1] = {c[u] + m};
-        const float k = rsqrtf(not_negative(fmaf(s[2 * u + 1], scale, -m * m)) + d.eps);
+        const float mu[1] = {c[u] + m[u]}, k = rsqrtf(var[u] + d.eps);
         float f[VW];
 #pragma unroll
         for (int e = 0; e < VW; ++e) f[e] = a[e] * k;
