@@ -105,7 +105,7 @@ def test_outliers_in_a_small_sample(lib, shape, groups, dtype):
 
 
 @pytest.mark.parametrize("shape,groups,dtype", [((2100, 1, 128), 1, "f32"), ((2100, 1, 256), 1, "bf16"),
-                                                ((1500, 1, 1024), 4, "f16")])
+                                                ((1500, 1, 1024), 4, "f16"), ((9, 1, 4096), 2, "f16")])
 def test_outliers_in_a_token(lib, shape, groups, dtype):
     x = ordinary(shape, dtype, 4 + sum(shape))
     vw = 4 if dtype == "f32" else 8

@@ -729,7 +729,7 @@ k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
 #pragma unroll
           for (int e = 0; e < VW; ++e) s += v[k][e] - first;
       const float m = set_sum(s, d.p.set) * d.scale;
-      const float mu = first + m, by = m - (mu - first);
+      float mu = first + m, by = m - (mu - first);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -739,7 +739,26 @@ k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
           for (int e = 0; e < VW; ++e) q = fmaf(v[k][e], v[k][e], q);
       }
       q = set_sum(q, d.p.set) * d.scale;  // relative to mu, which is rounded: `by` off the mean
-      const float r = 1.0f / sqrtf(not_negative(q - by * by) + d.eps);
+      float var = not_negative(q - by * by);
+      // `first` far off the mean: so is mu, by the rounding of so distant a sum
+      if (__any_sync(0xffffffffu, m * m > 16.f * var)) {
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (at.has(d, k))
+#pragma unroll
+            for (int e = 0; e < VW; ++e) s += v[k][e];
+        const float res = set_sum(s, d.p.set) * d.scale;
+        if (far_off(m * m, var)) {
+          mu += res;
+          var = not_negative(q - res * res);
+#pragma unroll
+          for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) v[k][e] -= res;
+        }
+      }
+      const float r = 1.0f / sqrtf(var + d.eps);
       const int64_t t = n + u * step;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
