@@ -13,8 +13,8 @@ namespace ep {
 // sigmoid(u) = 1 / (1 + e^-u).
 //  float32: e^-u = 2^p (1 + c), p = -u log2(e) rounded and c what the rounding
 //  and log2(e)'s own left out, times ln 2; the reciprocal by the hardware's
-//  approximation and one Newton step: within 3 float32 ulp.  u is held in
-//  [-87, 100], where nothing overflows: below, sigmoid is e^-87 = 1.6e-38.
+//  approximation and one Newton step: within 3 float32 ulp.  u comes from -87 on
+//  (from_87), and from 100 on e^-u counts as e^-100: nothing overflows.
 //  16-bit results: 2^x and 1/x by the hardware approximations with p rounded,
 //  errors of a few float32 ulp and |u| 2^-24, far below the results' rounding;
 //  from u = -88.7 down 2^p overflows and sigmoid(u) is 0.
@@ -24,7 +24,7 @@ __device__ __forceinline__ float sigmoid(float u) {
     constexpr float kL = 1.44269502162933349609375f;  // log2(e) rounded to float32
     constexpr float kLlo = 1.92596298909109e-08f;     // log2(e) - kL
     constexpr float kLn2 = 0.6931471805599453f;
-    const float t = fmaxf(fminf(-u, 87.f), -100.f);
+    const float t = fmaxf(-u, -100.f);
     const float p = __fmul_rn(t, kL);
     const float c = fmaf(t, kL, -p) + t * kLlo;
     const float e = dev::ex2_approx(p);
@@ -36,14 +36,24 @@ __device__ __forceinline__ float sigmoid(float u) {
   }
 }
 
+// float32: u, or -87 below that (NaN stays NaN), where u sigmoid(u) is above -1.5e-36 and
+// goes to 0: with u itself beside a sigmoid held at e^-87 it grew again, to -4.9 at -3e38.
+template <typename T>
+__device__ __forceinline__ float from_87(float u) {
+  if constexpr (std::is_same_v<T, float>) asm("max.NaN.f32 %0, %0, %1;" : "+f"(u) : "f"(-87.f));
+  return u;
+}
+
 template <typename T>
 __device__ __forceinline__ float silu(float u) {
+  u = from_87<T>(u);
   return u * sigmoid<T>(u);
 }
 
 // du of the definition.
 template <typename T>
 __device__ __forceinline__ float silu_grad(float dy, float u) {
+  u = from_87<T>(u);
   const float s = sigmoid<T>(u);
   return dy * (s * fmaf(u, 1.0f - s, 1.0f));
 }
