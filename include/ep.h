@@ -289,9 +289,11 @@ typedef enum { EP_ACT_NONE = 0, EP_ACT_SILU = 1 } ep_activation;
  * epsilon      >= 0 (the op's default is 1e-5).
  * mean, inv_std_dev   NULL, or N * groups float32 values: mu and
  *              1/sqrt(var + epsilon), which ep_group_norm_grad takes.
- * workspace    device scratch of ep_group_norm_workspace_size() bytes (may be
- *              NULL when that is 0), 16-byte aligned; its contents on entry do
- *              not matter.  Calls that may overlap on the GPU (other streams,
+ * workspace    device scratch of ep_group_norm_workspace_size() bytes, or where X
+ *              and Y start on 16-byte boundaries of
+ *              ep_group_norm_workspace_size_aligned() (may be NULL when that is 0:
+ *              small samples and tokens), 16-byte aligned; its contents on entry
+ *              do not matter.  Calls that may overlap on the GPU (other streams,
  *              concurrently replayed graphs) need one each.
  * Y may be X.  Of an empty tensor nothing is written, mean and inv_std_dev
  * included.
@@ -306,9 +308,11 @@ ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape,
                         void* Y, float* mean, float* inv_std_dev,
                         void* workspace, size_t workspace_bytes, ep_stream_t stream);
 
-/* Workspace bytes ep_group_norm needs; 0 as well for arguments it rejects.
- * They depend on the arguments alone. */
+/* Workspace bytes ep_group_norm needs, for operands at any address or on 16-byte
+ * boundaries (never more); 0 as well for arguments it rejects.  They depend on
+ * the arguments alone. */
 size_t ep_group_norm_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups);
+size_t ep_group_norm_workspace_size_aligned(ep_dtype t, const int64_t* shape, int64_t groups);
 
 /*
  * Gradient of ep_group_norm.
@@ -325,7 +329,8 @@ size_t ep_group_norm_workspace_size(ep_dtype t, const int64_t* shape, int64_t gr
  * dgamma, dbeta   C elements of T each, or NULL where not wanted.  The sums
  *              are float32 in a fixed order (the same call gives the same
  *              bits), rounded once.  Of an empty tensor they are set to 0.
- * workspace    ep_group_norm_grad_workspace_size() bytes, as for ep_group_norm.
+ * workspace    ep_group_norm_grad_workspace_size() bytes, or where dY, X and dX start
+ *              on 16-byte boundaries ..._aligned(), as for ep_group_norm.
  *
  * Errors: as ep_group_norm.
  */
@@ -335,8 +340,9 @@ ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const in
                              void* dX, void* dgamma, void* dbeta,
                              void* workspace, size_t workspace_bytes, ep_stream_t stream);
 
-/* Workspace bytes ep_group_norm_grad needs; 0 as well for arguments it rejects. */
+/* Workspace bytes ep_group_norm_grad needs, as for ep_group_norm. */
 size_t ep_group_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups);
+size_t ep_group_norm_grad_workspace_size_aligned(ep_dtype t, const int64_t* shape, int64_t groups);
 
 /*
  * BiasDropout

@@ -60,9 +60,11 @@ _SIGNATURES = {
     "ep_group_norm": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, _vp, _vp, ctypes.c_int64, ctypes.c_float,
                                      ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "ep_group_norm_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
+    "ep_group_norm_workspace_size_aligned": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
     "ep_group_norm_grad": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _i64p, _vp, _vp, ctypes.c_int64, ctypes.c_int,
                                           _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "ep_group_norm_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
+    "ep_group_norm_grad_workspace_size_aligned": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int64]),
     "ep_bias_dropout": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, _vp, _vp, ctypes.c_double,
                                        ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _vp]),
     "ep_bias_dropout_grad": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, ctypes.c_double,
@@ -414,11 +416,13 @@ def _nsc(shape):
 
 @functools.lru_cache(maxsize=4096)
 def _group_norm_plan(code, shape, groups, grad):
-    """(N, S, C) as the library reads it, the channels' shape and the workspace's bytes."""
+    """(N, S, C) as the library reads it, the channels' shape, and the workspace's
+    bytes for tensors anywhere and on 16-byte boundaries."""
     lib = load_library()
-    fn = lib.ep_group_norm_grad_workspace_size if grad else lib.ep_group_norm_workspace_size
+    name = "ep_group_norm_grad_workspace_size" if grad else "ep_group_norm_workspace_size"
     nsc = _nsc(shape)
-    return nsc, torch.Size(shape[-1:]), int(fn(code, nsc, groups))
+    return (nsc, torch.Size(shape[-1:]), int(getattr(lib, name)(code, nsc, groups)),
+            int(getattr(lib, name + "_aligned")(code, nsc, groups)))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -430,14 +434,16 @@ def _code(dtype):
     return _TORCH_TO_EP[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
 
 
-def ep_group_norm_workspace_size(dtype, shape, groups) -> int:
-    """Workspace bytes of ep_group_norm for a channels-last shape."""
-    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), False)[2]
+def ep_group_norm_workspace_size(dtype, shape, groups, aligned=False) -> int:
+    """Workspace bytes of ep_group_norm for a channels-last shape.  ``aligned``: X
+    and Y start on 16-byte boundaries (0 for small samples and tokens)."""
+    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), False)[3 if aligned else 2]
 
 
-def ep_group_norm_grad_workspace_size(dtype, shape, groups) -> int:
-    """Workspace bytes of ep_group_norm_grad for a channels-last shape."""
-    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), True)[2]
+def ep_group_norm_grad_workspace_size(dtype, shape, groups, aligned=False) -> int:
+    """Workspace bytes of ep_group_norm_grad for a channels-last shape.  ``aligned``:
+    dY, X and dX start on 16-byte boundaries."""
+    return _group_norm_plan(_code(dtype), tuple(shape), int(groups), True)[3 if aligned else 2]
 
 
 def ep_bias_dropout_grad_workspace_size(dtype, shape) -> int:
@@ -480,15 +486,18 @@ def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_E
             return ep_group_norm(X, gamma, beta, groups, epsilon, activation, Y, mean, inv_std_dev, workspace)
     lib = load_library()
     shape, groups = X.shape, int(groups)
-    nsc, channels, need = _group_norm_plan(code, shape, groups, False)
+    nsc, channels, need, need_aligned = _group_norm_plan(code, shape, groups, False)
     _operand("gamma", gamma, X, index, channels)
     if beta is not None:
         _operand("beta", beta, X, index, channels)
     Y = torch.empty_like(X) if Y is None else _operand("Y", Y, X, index, shape)
     mean = _group_stats("mean", mean, X, index, shape[0], groups)
     inv_std_dev = _group_stats("inv_std_dev", inv_std_dev, X, index, shape[0], groups)
-    args = (code, X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation),
-            Y.data_ptr(), _addr(mean), _addr(inv_std_dev))
+    px, py = X.data_ptr(), Y.data_ptr()
+    if (px | py) & 15 == 0:
+        need = need_aligned
+    args = (code, px, nsc, gamma.data_ptr(), _addr(beta), groups, float(epsilon), int(activation), py, _addr(mean),
+            _addr(inv_std_dev))
     s = _raw_stream(index)
     ws, wbytes, owned = _scratch(workspace, need, X, s)
     try:
@@ -515,7 +524,7 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
                                       workspace)
     lib = load_library()
     shape, groups = X.shape, int(groups)
-    nsc, channels, need = _group_norm_plan(code, shape, groups, True)
+    nsc, channels, need, need_aligned = _group_norm_plan(code, shape, groups, True)
     _operand("dY", dY, X, index, shape)
     _operand("gamma", gamma, X, index, channels)
     if beta is not None:
@@ -527,8 +536,11 @@ def ep_group_norm_grad(dY, X, gamma, beta, mean, inv_std_dev, groups=None, activ
     dX = torch.empty_like(X) if dX is None else _operand("dX", dX, X, index, shape)
     dgamma = _param_grad("dgamma", dgamma, X, index, channels)
     dbeta = _param_grad("dbeta", dbeta, X, index, channels)
-    args = (code, dY.data_ptr(), X.data_ptr(), nsc, gamma.data_ptr(), _addr(beta), groups, int(activation),
-            mean.data_ptr(), inv_std_dev.data_ptr(), dX.data_ptr(), _addr(dgamma), _addr(dbeta))
+    pdy, px, pdx = dY.data_ptr(), X.data_ptr(), dX.data_ptr()
+    if (pdy | px | pdx) & 15 == 0:
+        need = need_aligned
+    args = (code, pdy, px, nsc, gamma.data_ptr(), _addr(beta), groups, int(activation), mean.data_ptr(),
+            inv_std_dev.data_ptr(), pdx, _addr(dgamma), _addr(dbeta))
     s = _raw_stream(index)
     ws, wbytes, owned = _scratch(workspace, need, X, s)
     try:

@@ -441,6 +441,17 @@ ep_status gn_shape(const char* op, ep_dtype t, const int64_t* shape, int64_t gro
   return EP_OK;
 }
 
+size_t gn_workspace_size(const char* op, ep_dtype t, const int64_t* shape, int64_t groups, bool aligned,
+                         size_t (*bytes)(ep::DType, int64_t, int64_t, int64_t, int64_t, bool)) {
+  GnShape g;
+  char saved[sizeof(g_err)];
+  std::memcpy(saved, g_err, sizeof(g_err));
+  const ep_status s = gn_shape(op, t, shape, groups, &g);
+  std::memcpy(g_err, saved, sizeof(g_err));
+  if (s != EP_OK || g.n == 0) return 0;
+  return bytes(to_dtype(t), g.N, g.S, g.C, groups, aligned);
+}
+
 ep_status check_activation(const char* op, int activation) {
   if (activation != EP_ACT_NONE && activation != EP_ACT_SILU)
     return fail(EP_ERR_INVALID_ARG, "%s: activation %d is neither EP_ACT_NONE nor EP_ACT_SILU", op, activation);
@@ -482,13 +493,12 @@ ep_status check_workspace(const char* op, const void* workspace, size_t bytes, s
 }  // namespace
 
 size_t ep_group_norm_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups) {
-  GnShape g;
-  char saved[sizeof(g_err)];
-  std::memcpy(saved, g_err, sizeof(g_err));
-  const ep_status s = gn_shape("group_norm_workspace_size", t, shape, groups, &g);
-  std::memcpy(g_err, saved, sizeof(g_err));
-  if (s != EP_OK || g.n == 0) return 0;
-  return ep::group_norm_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  return gn_workspace_size("group_norm_workspace_size", t, shape, groups, false, ep::group_norm_workspace_bytes);
+}
+
+size_t ep_group_norm_workspace_size_aligned(ep_dtype t, const int64_t* shape, int64_t groups) {
+  return gn_workspace_size("group_norm_workspace_size_aligned", t, shape, groups, true,
+                           ep::group_norm_workspace_bytes);
 }
 
 ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape, const void* gamma, const void* beta,
@@ -517,7 +527,8 @@ ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape, const v
     if (overlap(mn, o) || overlap(iv, o))
       return fail(EP_ERR_INVALID_ARG, "group_norm: mean / inv_std_dev overlap another operand");
   if (overlap(mn, iv)) return fail(EP_ERR_INVALID_ARG, "group_norm: mean and inv_std_dev overlap");
-  const size_t need = ep::group_norm_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  const bool all16 = aligned(X, 16) && aligned(Y, 16);
+  const size_t need = ep::group_norm_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups, all16);
   const Span all[] = {x, y, ga, be, mn, iv};
   if (ep_status s = check_workspace("group_norm", workspace, workspace_bytes, need, all, 6); s != EP_OK) return s;
   DevInfo dv;
@@ -530,13 +541,12 @@ ep_status ep_group_norm(ep_dtype t, const void* X, const int64_t* shape, const v
 }
 
 size_t ep_group_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int64_t groups) {
-  GnShape g;
-  char saved[sizeof(g_err)];
-  std::memcpy(saved, g_err, sizeof(g_err));
-  const ep_status s = gn_shape("group_norm_grad_workspace_size", t, shape, groups, &g);
-  std::memcpy(g_err, saved, sizeof(g_err));
-  if (s != EP_OK || g.n == 0) return 0;
-  return ep::group_norm_grad_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  return gn_workspace_size("group_norm_grad_workspace_size", t, shape, groups, false, ep::group_norm_grad_workspace_bytes);
+}
+
+size_t ep_group_norm_grad_workspace_size_aligned(ep_dtype t, const int64_t* shape, int64_t groups) {
+  return gn_workspace_size("group_norm_grad_workspace_size_aligned", t, shape, groups, true,
+                           ep::group_norm_grad_workspace_bytes);
 }
 
 ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const int64_t* shape, const void* gamma,
@@ -570,7 +580,8 @@ ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const in
   if (bad_overlap_inplace_ok(dx, dy) || bad_overlap_inplace_ok(dx, x) || overlap(dx, ga) || overlap(dx, be) ||
       overlap(dx, mn) || overlap(dx, iv))
     return fail(EP_ERR_INVALID_ARG, "group_norm_grad: dX overlaps an input other than as an exact alias of dY or X");
-  const size_t need = ep::group_norm_grad_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups);
+  const bool all16 = aligned(dY, 16) && aligned(X, 16) && aligned(dX, 16);
+  const size_t need = ep::group_norm_grad_workspace_bytes(to_dtype(t), g.N, g.S, g.C, groups, all16);
   if (ep_status s = check_workspace("group_norm_grad", workspace, workspace_bytes, need, all, 9); s != EP_OK) return s;
   DevInfo dv;
   if (ep_status s = device_info(&dv); s != EP_OK) return s;

@@ -79,7 +79,7 @@ struct GroupNormArgs {
   int64_t N, S, C, G;   // > 0, G divides C
   float eps;
   bool silu;
-  void* workspace;      // group_norm_workspace_bytes (nullable when 0)
+  void* workspace;      // group_norm_workspace_bytes (nullable where 0)
 };
 
 struct GroupNormGradArgs {
@@ -130,9 +130,10 @@ cudaError_t launch_group_norm_grad(const GroupNormGradArgs& a, cudaStream_t stre
 cudaError_t launch_bias_dropout(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches);
 cudaError_t launch_bias_dropout_grad(const BiasDropoutArgs& a, int sm_count, cudaStream_t stream, int* launches);
 
-// Workspace bytes of those launches; they depend on the shape and type alone.
-size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G);
-size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G);
+// Workspace bytes of those launches, by shape and type.  `aligned`: of the forms that
+// take x, y (dy, x, dx) which start on 16-byte boundaries; else of any.
+size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned);
+size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned);
 size_t bias_dropout_grad_workspace_bytes(DType t, int64_t n, int64_t C);
 
 // Bytes of split-row workspace BiasSoftmax needs for (rows, cols) of type t;

@@ -2202,16 +2202,19 @@ cudaError_t token_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, int* l
 
 }  // namespace
 
-size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+size_t group_norm_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned) {
+  if (aligned && (token_staged(t, N, S, C, G, kTokenStagedBytes) || group_norm_fused_applies(t, N, S, C, G))) return 0;
   return gn_workspace(dims_of(t, N, S, C, G, 0.f, false)).total;
 }
 
-size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
-  size_t most = std::max(gn_grad_workspace(dims_of(t, N, S, C, G, 0.f, true), t).total,
-                         group_norm_grad_fused_bytes(t, N, S, C, G));
-  if (token_staged(t, N, S, C, G, kTokenGradStagedBytes))
-    most = std::max(most, size_t(token_rows(token_grad_dims(t, N, C, G))) * size_t(C) * 8);
-  return most;
+size_t group_norm_grad_workspace_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned) {
+  const bool token = token_staged(t, N, S, C, G, kTokenGradStagedBytes);
+  const size_t of_token = token ? size_t(token_rows(token_grad_dims(t, N, C, G))) * size_t(C) * 8 : 0;
+  if (aligned && token) return of_token;
+  bool fused = false;
+  const size_t of_fused = group_norm_grad_fused_bytes(t, N, S, C, G, aligned, &fused);
+  if (aligned && fused) return of_fused;
+  return std::max({of_token, of_fused, gn_grad_workspace(dims_of(t, N, S, C, G, 0.f, true), t).total});
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream, int* launches) {

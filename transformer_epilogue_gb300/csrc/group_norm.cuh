@@ -197,7 +197,10 @@ __device__ __forceinline__ float not_negative(float q) { return q < 0.f ? 0.f : 
 // nothing has been launched.
 cudaError_t launch_group_norm_fused(const GroupNormArgs& a, cudaStream_t stream, int* launches, bool* done);
 cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, cudaStream_t stream, int* launches, bool* done);
-// Workspace bytes of the fused gradient (0 where it does not apply).
-size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G);
+// Whether the fused form takes a shape whose x and y are 16-byte aligned.
+bool group_norm_fused_applies(DType t, int64_t N, int64_t S, int64_t C, int64_t G);
+// Workspace bytes of the fused gradient: for 16-byte-aligned operands, or the most for any.
+// *applies: whether it takes the aligned shape.
+size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned, bool* applies);
 
 }  // namespace ep

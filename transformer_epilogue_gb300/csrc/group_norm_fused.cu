@@ -1049,6 +1049,14 @@ inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uin
 
 constexpr int kFwdNv = 8, kGradNv = 4;
 
+// How fragments, channels and groups meet: see MODE above.
+int mode_of(int vw, int64_t C, int64_t G, bool slab) { return !slab ? 2 : C / G % vw == 0 ? 0 : 1; }
+
+bool fwd_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, FusedPlan* p) {
+  return fused_plan(vw, N, S, C, slab, kFwdNv, p) &&
+         fused_smem(*p, mode_of(vw, C, G, slab), vw, G, false) <= smem_most(*p);
+}
+
 bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, FusedPlan* p) {
   if (!fused_plan(vw, N, S, C, slab, kGradNv, p)) return false;
   // (8 values a thread do not fit the 64 registers of a wide block's threads: f16 3000x1x8160
@@ -1061,15 +1069,31 @@ bool grad_plan(int vw, int64_t N, int64_t S, int64_t C, int64_t G, bool slab, Fu
 
 }  // namespace
 
-size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
+bool group_norm_fused_applies(DType t, int64_t N, int64_t S, int64_t C, int64_t G) {
   const int vw = t == DType::F32 ? 4 : 8;
-  size_t most = 0;
+  const bool slab = C % vw == 0;
   TokenPlan tp;
-  if (token_plan(vw, N, S, C, G, kGradNv, &tp)) most = size_t(tp.ctas) * size_t(C) * 8;
+  FusedPlan p;
+  return (slab && token_plan(vw, N, S, C, G, kFwdNv, &tp)) || fwd_plan(vw, N, S, C, G, slab, &p);
+}
+
+size_t group_norm_grad_fused_bytes(DType t, int64_t N, int64_t S, int64_t C, int64_t G, bool aligned, bool* applies) {
+  const int vw = t == DType::F32 ? 4 : 8;
+  const bool whole = C % vw == 0;
+  size_t most = 0;
+  *applies = false;
+  TokenPlan tp;
+  if (whole && token_plan(vw, N, S, C, G, kGradNv, &tp)) {
+    *applies = true;
+    most = size_t(tp.ctas) * size_t(C) * 8;
+    if (aligned) return most;
+  }
   for (int slab = 0; slab < 2; ++slab) {
     FusedPlan p;
-    if (grad_plan(vw, N, S, C, G, slab != 0, &p))
+    if ((!aligned || (slab != 0) == whole) && grad_plan(vw, N, S, C, G, slab != 0, &p)) {
+      *applies = *applies || (slab != 0) == whole;
       most = std::max(most, size_t(p.grid_items) * size_t(C) * 8);
+    }
   }
   return most;
 }
@@ -1091,9 +1115,8 @@ cudaError_t launch_group_norm_fused(const GroupNormArgs& a, cudaStream_t stream,
       default: return token_fwd<__nv_bfloat16>(a, t, stream, launches);
     }
   }
-  if (!fused_plan(vw, a.N, a.S, a.C, slab, kFwdNv, &d.p)) return cudaSuccess;
-  const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
-  if (fused_smem(d.p, mode, vw, a.G, false) > smem_most(d.p)) return cudaSuccess;
+  if (!fwd_plan(vw, a.N, a.S, a.C, a.G, slab, &d.p)) return cudaSuccess;
+  const int mode = mode_of(vw, a.C, a.G, slab);
   *done = true;
 #define EP_GN_FUSED(T)                                                          \
   (mode == 0   ? fused_fwd<T, 0>(a, d, stream, launches)                        \
@@ -1127,7 +1150,7 @@ cudaError_t launch_group_norm_grad_fused(const GroupNormGradArgs& a, cudaStream_
   }
   if (!grad_plan(vw, a.N, a.S, a.C, a.G, slab, &d.p)) return cudaSuccess;
   *done = true;
-  const int mode = !slab ? 2 : d.D % vw == 0 ? 0 : 1;
+  const int mode = mode_of(vw, a.C, a.G, slab);
 #define EP_GN_GRAD_FUSED(T)                                                     \
   (mode == 0   ? fused_grad<T, 0>(a, d, cpart, stream, launches)                \
    : mode == 1 ? fused_grad<T, 1>(a, d, cpart, stream, launches)                \
