@@ -42,6 +42,7 @@
 #include "ep_internal.h"
 #include "group_norm.cuh"
 #include "launch_util.h"
+#include "smem_limit.h"
 #include "tma_pipe.cuh"
 
 namespace ep {
@@ -1987,11 +1988,9 @@ inline unsigned misalign16(const void* p) { return unsigned(reinterpret_cast<uin
 template <typename... KArgs, typename... Args>
 cudaError_t launch_staged(void (*fn)(KArgs...), int64_t rows, const GnDims& d, cudaStream_t stream, int* launches,
                           size_t extra, Args... args) {
-  int per_sm = 1;
-  const int threads = d.p.threads + 32;
-  cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, kStageSmem + extra, &per_sm);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn));
   if (e != cudaSuccess) return e;
-  e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(threads), kStageSmem + extra, stream, args...);
+  e = launch(fn, dim3(unsigned(rows * d.p.tiles)), dim3(d.p.threads + 32), kStageSmem + extra, stream, args...);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }

@@ -42,6 +42,7 @@
 #include "ep_internal.h"
 #include "group_norm.cuh"
 #include "launch_util.h"
+#include "smem_limit.h"
 
 namespace ep {
 namespace {
@@ -996,9 +997,8 @@ constexpr size_t smem_most(const FusedPlan& p) { return (p.threads > kMaxThreads
 template <typename... KArgs, typename... Args>
 cudaError_t launch_fused(void (*fn)(KArgs...), unsigned blocks, int threads, size_t smem, cudaStream_t stream,
                          Args... args) {
-  int per_sm = 1;
   if (smem > 48 * 1024) {
-    const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(fn), threads, smem, &per_sm);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn));
     if (e != cudaSuccess) return e;
   }
   return launch(fn, dim3(blocks), dim3(threads), smem, stream, args...);
