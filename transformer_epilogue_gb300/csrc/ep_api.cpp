@@ -561,7 +561,8 @@ ep_status ep_group_norm_grad(ep_dtype t, const void* dY, const void* X, const in
   for (const void* p : ptrs)
     if (p != nullptr && !aligned(p, es))
       return fail(EP_ERR_INVALID_ARG, "group_norm_grad: pointer %p is not aligned to the element size", p);
-  const int64_t nb = g.n * es, cb = g.C * es, sb = g.N * groups * 4;
+  const int64_t nb = g.n * es, cb = g.C * es;
+  const int64_t sb = g.n > 0 ? g.N * groups * 4 : 0;  // (not read of an empty tensor, whose N can be any)
   const Span dy{dY, nb}, x{X, nb}, ga{gamma, cb}, be{beta, cb}, mn{mean, sb}, iv{inv_std_dev, sb}, dx{dX, nb},
       dg{dgamma, cb}, db{dbeta, cb};
   const Span all[] = {dy, x, ga, be, mn, iv, dx, dg, db};
