@@ -35,6 +35,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -87,7 +88,7 @@ NCU_TRAFFIC = {
     "sln_f32_2x128x768": 1608960,
     "sln_f32_32x2048x1024_bcast_skip": 488529664,
 }
-NCU_TRAFFIC_SOURCE_HASH = "133050c074c06ab7"
+NCU_TRAFFIC_SOURCE_HASH = "24458216a37a2366"
 
 
 def _code_only(text: str) -> str:
@@ -114,17 +115,29 @@ def _code_only(text: str) -> str:
     return "\n".join(line.rstrip() for line in "".join(out).splitlines() if line.strip())
 
 
-# what the captured kernels are compiled from
-TRAFFIC_SOURCES = ("bias_softmax.cu", "device_common.cuh", "elementwise.cu", "launch_util.h", "skip_layer_norm.cu",
-                   "tma_pipe.cuh", "tuning.h")
+CSRC = os.path.join(ROOT, "transformer_epilogue_gb300", "csrc")
+TRAFFIC_KERNELS = ("bias_softmax.cu", "elementwise.cu", "skip_layer_norm.cu")   # the captured kernels' files
+
+
+def traffic_sources() -> list:
+    """What the captured kernels are compiled from: their files and, followed from
+    file to file, the headers of the same folder that these include."""
+    todo, seen = list(TRAFFIC_KERNELS), set()
+    while todo:
+        f = todo.pop()
+        if f in seen or not os.path.exists(os.path.join(CSRC, f)):
+            continue
+        seen.add(f)
+        with open(os.path.join(CSRC, f), encoding="utf-8") as src:
+            todo += re.findall(r'^\s*#\s*include\s*"([^"]+)"', src.read(), re.M)
+    return sorted(seen)
 
 
 def kernel_source_hash() -> str:
     """Hash of the timed kernels' code (comments excluded)."""
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "transformer_epilogue_gb300", "csrc")
-    for f in TRAFFIC_SOURCES:
-        with open(os.path.join(csrc, f), encoding="utf-8") as src:
+    for f in traffic_sources():
+        with open(os.path.join(CSRC, f), encoding="utf-8") as src:
             h.update(_code_only(src.read()).encode())
     return h.hexdigest()[:16]
 

@@ -18,8 +18,8 @@
 
 #include "column_walk.cuh"
 #include "device_common.cuh"
-#include "ep_internal.h"
 #include "launch_util.h"
+#include "training_internal.h"
 
 namespace ep {
 namespace {

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "ep_internal.h"
+#include "training_internal.h"
 
 namespace {
 

@@ -6,7 +6,7 @@
 #include <type_traits>
 
 #include "device_common.cuh"
-#include "ep_internal.h"
+#include "training_internal.h"
 
 namespace ep {
 

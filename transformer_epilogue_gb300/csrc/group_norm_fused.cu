@@ -39,10 +39,10 @@
 
 #include "column_walk.cuh"
 #include "device_common.cuh"
-#include "ep_internal.h"
 #include "group_norm.cuh"
 #include "launch_util.h"
 #include "smem_limit.h"
+#include "training_internal.h"
 
 namespace ep {
 namespace {
