@@ -198,7 +198,7 @@ struct Slots {
 // k stands, counted in slots from the sample's first.  No branches: the join's loads go
 // out together.
 struct GroupParts {
-  unsigned count, of_chunk, magic;  // magic: 2^32 / of_chunk, rounded up (k of_chunk < 2^32)
+  unsigned count, of_chunk, magic;  // magic: 2^32 / of_chunk, rounded up
   int tiles, slots, base0, base1;   // the first and the other parts of a chunk
   __device__ __forceinline__ GroupParts(const GnDims& d, int g, int vw) : tiles(d.p.tiles), slots(d.slots) {
     const int e0 = g * d.D, tile = d.p.tile_frags * vw, t0 = e0 / tile;
@@ -210,7 +210,9 @@ struct GroupParts {
   }
   template <typename F>
   __device__ __forceinline__ F load(const F* src, unsigned k) const {
-    const unsigned chunk = of_chunk > 1 ? __umulhi(k, magic) : k, i = k - chunk * of_chunk;
+    unsigned chunk = of_chunk > 1 ? __umulhi(k, magic) : k;
+    if (chunk * of_chunk > k) --chunk;  // (k of_chunk from 2^32 on: one too many at most)
+    const unsigned i = k - chunk * of_chunk;
     return k < count ? __ldcg(src + int64_t(chunk * unsigned(tiles) + i) * slots + (i == 0 ? base0 : base1)) : F{};
   }
 };
