@@ -245,18 +245,21 @@ struct LinearParts {
   }
 };
 
-// f(parts) for those of group g of the sample that starts at xs.
-template <typename T, typename F>
+// f(parts) for those of group g of the sample that starts at xs.  How they are found is
+// the kernel's own (WAY): a join runs once, and code that it does not need costs it
+// instruction fetches (f16 2x4096x320 with all ways in one kernel 10.5 us, 10.1 apart).
+template <typename T, int WAY, typename F>
 __device__ __forceinline__ void with_parts(const GnDims& d, int g, const T* xs, F f) {
   constexpr int VW = dev::Vec16<T>::N;
-  if (d.p.tiles == 1 || (!d.staged && d.slots == d.G)) {
+  if constexpr (WAY == 0) {
     f(LinearParts(d, g));
-  } else if (d.staged) {
+  } else if constexpr (WAY == 1) {
     f(GroupParts(d, g, VW));
   } else {
     f(ScannedParts(d, g, VW, d.shifted ? dev::misalignment(xs) : 0));
   }
 }
+inline int way_of(const GnDims& d) { return d.p.tiles == 1 || (!d.staged && d.slots == d.G) ? 0 : d.staged ? 1 : 2; }
 
 // An item's partial fragments, if this thread has one: the sample's first (before
 // `lo` outside) and last (from `hi` on), by their row in the item.  They are
@@ -840,8 +843,9 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
     }
     consumer_sync();
     const int mine = rows.mine(r, t);
-#pragma unroll 1
-    for (bool again = false;; again = true) {
+    bool far = false;
+    auto statistics = [&](auto second) {
+      constexpr bool again = decltype(second)::value;
       float c[EV], s[VW], q[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
@@ -863,7 +867,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
         for (int e = 0; e < VW; ++e)
           if (!ends.inside(row, e)) v[e] = c[EV == 1 ? 0 : e];
       };
-      if (!again) {
+      if constexpr (!again) {
         rows.consume(r, mine, [&](int row, const auto& raw) {
 #pragma unroll
           for (const auto& one : raw) {
@@ -922,7 +926,6 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                  });
         consumer_sync();
       }
-      bool far = false;
       sum_sets(consumers, cols.n_groups, cols.D,
                [&](int g, int k, float& a, float& b) {
                  const int i = cols.lo(g) + k;
@@ -948,7 +951,11 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
                    far = true;
                  }
                });
-      if (dev::named_barrier_and(1, consumers, !far)) break;
+    };
+    statistics(std::false_type{});
+    if (!dev::named_barrier_and(1, consumers, !far)) {
+      statistics(std::true_type{});
+      consumer_sync();
     }
   }
 }
@@ -1763,19 +1770,13 @@ constexpr int kJoinThreads = 64;
 // relative to that of the first lane's first part (of a group's parts only ScannedParts
 // can be empty there: to the group's first value).  `lanes` of a warp (a power
 // of two) take one (n, g), each keeping up to KEPT parts in registers for the second
-// sum and reading others again.  How a group's parts are found (WAY) is a kernel of
-// its own: the code runs once, so what it does not need costs it instruction fetches
-// (f16 2x4096x320 in one kernel with the other ways 10.5 us, 10.1 as it is).
-//   0  part k is slot g of tile k of the sample (one tile, or a slot for every group): kJoinKept
-//   1  staged rows of many tiles; KEPT 1 where a warp's lanes hold all parts of a group: a warp for
-//      each group takes 282 us, not 203, for f16 40x100x16384 in 4096 groups
-//   2  every tile is looked at
+// sum and reading others again; KEPT 1 where a warp's lanes hold all parts of a group (a
+// warp for each group: f16 40x100x16384 in 4096 groups 271 us in all, 97 so).
 constexpr int kJoinKept = 10;
 
 template <typename T, int WAY, int KEPT>
 __global__ void __launch_bounds__(kJoinThreads)
 k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* inv_out, int log_lanes) {
-  constexpr int VW = dev::Vec16<T>::N;
   dev::pdl_trigger();
   bool waited = false;  // where the first group's parts lie, and x: before pass 1 ends
   const int lanes = KEPT == 1 ? 1 << log_lanes : 32, lane = threadIdx.x & (lanes - 1);
@@ -1843,19 +1844,13 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
         inv_out[i] = 1.0f / sqrtf(not_negative(q - res * fix) / c + d.eps);
       }
     };
-    if constexpr (WAY == 0) {
-      join(LinearParts(d, g));
-    } else if constexpr (WAY == 1) {
-      join(GroupParts(d, g, VW));
-    } else {
-      join(ScannedParts(d, g, VW, d.shifted ? dev::misalignment(xs) : 0));
-    }
+    with_parts<T, WAY>(d, g, xs, join);
   }
 }
 
 // The gradient's sums of the parts -> m1, m2 of each (n, g); and, in the blocks
 // after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
-template <typename T>
+template <typename T, int WAY>
 __global__ void __launch_bounds__(kSumsThreads)
 k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
                int64_t reps, T* dbeta, T* dgamma) {
@@ -1872,7 +1867,7 @@ k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, i
     const int64_t n = quotient(i, d.G);
     const float2* src = reinterpret_cast<const float2*>(gpart) + n * of_sample;
     float a = 0.f, b = 0.f;
-    with_parts(d, static_cast<int>(i - n * d.G), x + n * d.L, [&](const auto& parts) {
+    with_parts<T, WAY>(d, static_cast<int>(i - n * d.G), x + n * d.L, [&](const auto& parts) {
 #pragma unroll 8
       for (unsigned k = lane; k < parts.count; k += 32) {
         const float2 v = parts.load(src, k);
@@ -2045,10 +2040,11 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
     const bool many = !staged || d.p.tiles == 1 || d.p.chunks * of_group > 32;
     int log_lanes = 0;
     while (!many && (1 << log_lanes) < d.p.chunks * of_group) ++log_lanes;
-    auto f = d.p.tiles == 1 || (!staged && d.slots == d.G) ? k_gn_join<T, 0, kJoinKept>
-             : !staged                                     ? k_gn_join<T, 2, kJoinKept>
-             : many                                        ? k_gn_join<T, 1, 4>
-                                                           : k_gn_join<T, 1, 1>;
+    const int way = way_of(d);
+    auto f = way == 0   ? k_gn_join<T, 0, kJoinKept>
+             : way == 2 ? k_gn_join<T, 2, kJoinKept>
+             : many     ? k_gn_join<T, 1, 4>
+                        : k_gn_join<T, 1, 1>;
     const int64_t groups = kJoinThreads >> (many ? 5 : log_lanes);  // of a block
     const int64_t joins = std::min<int64_t>((d.N * d.G + groups - 1) / groups, kPlanSms * 8);
     e = launch(f, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv, log_lanes);
@@ -2119,7 +2115,9 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   const int64_t joins = std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms);
   const int64_t sums = cpart != nullptr ? std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, kPlanSms * 4) : 0;
   // (the sums of du are dbeta, those of du * h are dgamma)
-  e = launch(k_gn_grad_join<T>, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, x, gpart, d, m1, m2, int(joins), cpart,
+  const int way = way_of(d);
+  auto join = way == 0 ? k_gn_grad_join<T, 0> : way == 1 ? k_gn_grad_join<T, 1> : k_gn_grad_join<T, 2>;
+  e = launch(join, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, x, gpart, d, m1, m2, int(joins), cpart,
              rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
   if (e != cudaSuccess) return e;
   *launches += 1;
