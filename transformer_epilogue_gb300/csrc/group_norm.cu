@@ -1508,6 +1508,10 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
 // fragments are loaded as 16 bytes; else value by value).
 // ---------------------------------------------------------------------------
 
+// Blocks an SM of the general kernels' first passes, for the compiler (two, not three, of
+// float32: f32 2x1000x1001 16.5 us, not 15.8, its gradient 22.3, not 19.1).
+template <typename T> constexpr int kGeneralBlocks = sizeof(T) == 4 ? 3 : 2;
+
 // Pass 1.  A thread takes its channels' values relative to their first in the item
 // (`ref`), and sums their distances from a running mean `c` of those: after 4 rows,
 // 8, 16 ... and then every kFoldRows the mean moves on by s / n, and the squares to it
@@ -1516,7 +1520,7 @@ k_gn_grad_token_staged(const T* dy, const T* x, const T* __restrict__ gamma, con
 constexpr int kFoldRows = 64;
 
 template <typename T>
-__global__ void __launch_bounds__(kWalkThreads)
+__global__ void __launch_bounds__(kWalkThreads, kGeneralBlocks<T>)
 k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_out) {
   constexpr int VW = dev::Vec16<T>::N;
   constexpr int U = 4;
@@ -1655,7 +1659,7 @@ __device__ __forceinline__ void finish_sums(int c0, int64_t ng, const GnDims& d,
 // A CTA's items share `off` (the launch sees to it), so a thread's channels stay
 // the same and its sums run on over them.
 template <typename T, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kWalkThreads)
+__global__ void __launch_bounds__(kWalkThreads, kGeneralBlocks<T>)
 k_gn_grad_sums(const T* dy, const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, const float* mean,
                const float* inv, GnDims d, float* gpart, float* cpart) {
   constexpr int VW = dev::Vec16<T>::N;
@@ -1848,36 +1852,45 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
   }
 }
 
-// The gradient's sums of the parts -> m1, m2 of each (n, g); and, in the blocks
-// after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
+// The gradient's sums of the parts -> m1, m2 of each (n, g), 2^log_lanes lanes to one;
+// and, in the blocks after the first `join_blocks`, the channels' sums -> dbeta, dgamma.
 template <typename T, int WAY>
 __global__ void __launch_bounds__(kSumsThreads)
 k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, int join_blocks, const float* cpart, int64_t rows,
-               int64_t reps, T* dbeta, T* dgamma) {
+               int64_t reps, T* dbeta, T* dgamma, int log_lanes) {
   dev::pdl_trigger();
   dev::pdl_wait();
   if (int(blockIdx.x) >= join_blocks) {
     channel_sums<T>(cpart, rows, reps, d.C, 2, dbeta, dgamma, blockIdx.x - join_blocks, gridDim.x - join_blocks);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t of_sample = int64_t(d.p.chunks) * d.p.tiles * d.slots, per = kSumsThreads / 32;
+  const int lanes = WAY == 1 ? 1 << log_lanes : 32, lane = threadIdx.x & (lanes - 1);
+  const int per_warp = 32 / lanes, in_warp = (threadIdx.x & 31) / lanes;
+  const int64_t of_sample = int64_t(d.p.chunks) * d.p.tiles * d.slots, all = d.N * d.G;
   const float scale = 1.0f / (float(d.S) * float(d.D));
-  for (int64_t i = int64_t(threadIdx.x / 32) * join_blocks + blockIdx.x; i < d.N * d.G; i += join_blocks * per) {
-    const int64_t n = quotient(i, d.G);
-    const float2* src = reinterpret_cast<const float2*>(gpart) + n * of_sample;
+  // (a warp's lanes go round together, as in k_gn_join)
+  for (int64_t i0 = (int64_t(threadIdx.x / 32) * join_blocks + blockIdx.x) * per_warp; i0 < all;
+       i0 += int64_t(join_blocks) * (kSumsThreads / 32) * per_warp) {
+    const int64_t i = i0 + in_warp;
+    const bool live = WAY != 1 || i < all;
     float a = 0.f, b = 0.f;
-    with_parts<T, WAY>(d, static_cast<int>(i - n * d.G), x + n * d.L, [&](const auto& parts) {
+    if (live) {
+      const int64_t n = quotient(i, d.G);
+      const float2* src = reinterpret_cast<const float2*>(gpart) + n * of_sample;
+      with_parts<T, WAY>(d, static_cast<int>(i - n * d.G), x + n * d.L, [&](const auto& parts) {
 #pragma unroll 8
-      for (unsigned k = lane; k < parts.count; k += 32) {
-        const float2 v = parts.load(src, k);
-        a += v.x;
-        b += v.y;
-      }
-    });
-    a = dev::warp_sum(a);
-    b = dev::warp_sum(b);
-    if (lane == 0) {
+        for (unsigned k = lane; k < parts.count; k += lanes) {
+          const float2 v = parts.load(src, k);
+          a += v.x;
+          b += v.y;
+        }
+      });
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (live && lane == 0) {
       m1[i] = a * scale;
       m2[i] = b * scale;
     }
@@ -1928,6 +1941,17 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, b
   d.full_rows = d.frags / d.p.row_frags;
   d.rest = int(d.frags % d.p.row_frags);
   return d;
+}
+
+// Parts of a group at most (staged rows), and the lanes that join them: a power of two.
+int64_t most_parts(const GnDims& d, int64_t vw) {
+  const int64_t tile = d.p.tile_frags * vw;
+  return d.p.chunks * std::min<int64_t>(d.p.tiles, (d.D + tile - 2) / tile + 1);
+}
+int log_lanes_of(const GnDims& d, int64_t vw) {
+  int log = 0;
+  while (log < 5 && (1 << log) < most_parts(d, vw)) ++log;
+  return log;
 }
 
 // CTA rows (of `tiles` CTAs) of a launch over N * chunks items.
@@ -2035,17 +2059,14 @@ cudaError_t group_norm_t(const GroupNormArgs& a, cudaStream_t stream, int* launc
   }
   if (e != cudaSuccess) return e;
   if (partial != nullptr && !d.here) {
-    // parts of a group at most, and the lanes that take them
-    const int64_t tile = d.p.tile_frags * VW, of_group = std::min<int64_t>(d.p.tiles, (d.D + tile - 2) / tile + 1);
-    const bool many = !staged || d.p.tiles == 1 || d.p.chunks * of_group > 32;
-    int log_lanes = 0;
-    while (!many && (1 << log_lanes) < d.p.chunks * of_group) ++log_lanes;
     const int way = way_of(d);
+    const bool many = way != 1 || most_parts(d, VW) > 32;
+    const int log_lanes = many ? 5 : log_lanes_of(d, VW);
     auto f = way == 0   ? k_gn_join<T, 0, kJoinKept>
              : way == 2 ? k_gn_join<T, 2, kJoinKept>
              : many     ? k_gn_join<T, 1, 4>
                         : k_gn_join<T, 1, 1>;
-    const int64_t groups = kJoinThreads >> (many ? 5 : log_lanes);  // of a block
+    const int64_t groups = kJoinThreads >> log_lanes;  // of a block
     const int64_t joins = std::min<int64_t>((d.N * d.G + groups - 1) / groups, kPlanSms * 8);
     e = launch(f, dim3(unsigned(joins)), dim3(kJoinThreads), 0, stream, x, partial, d, mean, inv, log_lanes);
     if (e != cudaSuccess) return e;
@@ -2112,13 +2133,14 @@ cudaError_t group_norm_grad_t(const GroupNormGradArgs& a, cudaStream_t stream, i
   }
   if (e != cudaSuccess) return e;
   // joining the groups' parts and adding up the channels in one launch
-  const int64_t joins = std::min<int64_t>((d.N * d.G + 7) / 8, kPlanSms);
+  const int way = way_of(d), log_lanes = way == 1 ? log_lanes_of(d, VW) : 5;
+  const int64_t groups = int64_t(8) << (5 - log_lanes);  // of a block, where there are few
+  const int64_t joins = std::min<int64_t>((d.N * d.G + groups - 1) / groups, kPlanSms);
   const int64_t sums = cpart != nullptr ? std::min<int64_t>((int64_t(d.C) + 31) / 32 * 2, kPlanSms * 4) : 0;
   // (the sums of du are dbeta, those of du * h are dgamma)
-  const int way = way_of(d);
   auto join = way == 0 ? k_gn_grad_join<T, 0> : way == 1 ? k_gn_grad_join<T, 1> : k_gn_grad_join<T, 2>;
   e = launch(join, dim3(unsigned(joins + sums)), dim3(kSumsThreads), 0, stream, x, gpart, d, m1, m2, int(joins), cpart,
-             rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma));
+             rows, d.p.tiles > 1 && !staged ? d.p.reps : int64_t(1), static_cast<T*>(a.dbeta), static_cast<T*>(a.dgamma), log_lanes);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (staged && vec2) {
