@@ -328,7 +328,8 @@ size_t ep_group_norm_workspace_size_aligned(ep_dtype t, const int64_t* shape, in
  * mean, inv_std_dev   N * groups float32 values, as ep_group_norm wrote them.
  * dgamma, dbeta   C elements of T each, or NULL where not wanted.  The sums
  *              are float32 in a fixed order (the same call gives the same
- *              bits), rounded once.  Of an empty tensor they are set to 0.
+ *              bits), rounded once: a float16 sum beyond 65504 is infinite.  Of an
+ *              empty tensor they are set to 0.
  * workspace    ep_group_norm_grad_workspace_size() bytes, or where dY, X and dX start
  *              on 16-byte boundaries ..._aligned(), as for ep_group_norm.
  *
@@ -350,7 +351,8 @@ size_t ep_group_norm_grad_workspace_size_aligned(ep_dtype t, const int64_t* shap
  *   function of the element's index instead of an output:
  *
  *   Y[i] = residual[i] + keep(i) * (X[i] + bias[i mod C]) / (1 - ratio)
- *   keep(i) = word(i) < K,  K = round((1 - ratio) * 2^32)
+ *   keep(i) = word(i) < K,  K = round((1 - ratio) * 2^32), but 1 at least
+ *             (a ratio within 2^-33 of 1 keeps the word 0)
  *   word(i) = 32-bit word number i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror
  *             and Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011)
  *             with the counter words (i/4 low, i/4 high, offset low, offset
@@ -388,7 +390,8 @@ ep_status ep_bias_dropout(ep_dtype t, const void* X, const int64_t* shape, int r
  *              too must still hold the forward call's number).
  * dX           the shape of dY; may be dY.
  * dbias        C elements of T, or NULL.  The sum is float32, over the values
- *              before they are rounded to T, in a fixed order, rounded once.
+ *              before they are rounded to T, in a fixed order, rounded once (beyond
+ *              65504 a float16 sum is infinite).
  *              Of an empty tensor it is set to 0.
  * workspace    with dbias: ep_bias_dropout_grad_workspace_size() bytes, 16-byte
  *              aligned; its contents on entry do not matter.  Calls that may

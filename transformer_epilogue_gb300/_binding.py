@@ -4,7 +4,9 @@ Argument marshalling only: every function here checks that its tensors are
 contiguous CUDA tensors, allocates outputs the caller did not pass (PyTorch is
 the allocator), and calls the C entry point of the same name on the current
 CUDA stream.  All computation happens in the library's CUDA kernels; there is
-no CPU or PyTorch fallback.  A non-OK status raises ``EpError``.
+no CPU or PyTorch fallback.  A non-OK status raises ``EpError``.  Nothing here is
+recorded for autograd: outputs are detached whatever the inputs require, and the
+``_grad`` functions are called by hand (or from a ``torch.autograd.Function``).
 """
 from __future__ import annotations
 
@@ -473,7 +475,8 @@ def _param_grad(name, t, X, index, channels):
 def ep_group_norm(X, gamma, beta=None, groups=None, epsilon=DEFAULT_GROUP_NORM_EPSILON, activation=EP_ACT_NONE,
                   Y=None, mean=None, inv_std_dev=None, workspace=None, stream=None):
     """GroupNorm of a channels-last X (N, positions..., C), optionally followed
-    by a SiLU (``EP_ACT_SILU``).  ``groups`` is required (the op definition has
+    by a SiLU (``EP_ACT_SILU``).  Tokens (N, C) are passed as ``X[:, None]``.  Not
+    recorded for autograd: see ``ep_group_norm_grad``.  ``groups`` is required (the op definition has
     no default for it).  ``mean`` / ``inv_std_dev``: float32 tensors of
     N * groups elements to fill, True to allocate (N, groups), or None.
     Returns (Y, mean, inv_std_dev), the last two None when not requested."""
@@ -563,7 +566,8 @@ def _offset_device(t, like):
 
 def ep_bias_dropout(X, ratio, seed, offset=0, bias=None, residual=None, offset_device=None, Y=None, stream=None):
     """BiasDropout: residual + keep * (X + bias) / (1 - ratio), the mask made
-    from (seed, offset) and the element's index.  ``offset_device``: a one-element
+    from (seed, offset) and the element's index.  Not recorded for autograd: see
+    ``ep_bias_dropout_grad``.  ``offset_device``: a one-element
     int64 CUDA tensor added to ``offset`` when the kernel runs (for captured
     graphs).  Returns Y."""
     index, code = _first("X", X)

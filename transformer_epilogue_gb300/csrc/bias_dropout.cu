@@ -4,7 +4,7 @@
 // with the mask given by a counter instead of stored):
 //   Y[i]  = residual[i] + keep(i) * (X[i] + bias[i mod C]) / (1 - ratio)
 //   dX[i] = keep(i) * dY[i] / (1 - ratio),  dbias[c] = sum over rows of dX
-//   keep(i) = word(i) < K,  K = round((1 - ratio) 2^32)
+//   keep(i) = word(i) < K,  K = round((1 - ratio) 2^32), at least 1
 //   word(i) = word i mod 4 of Philox4x32-10 at counter (i / 4, offset), key seed
 // (J. Salmon, M. Moraes, R. Dror, D. Shaw, "Parallel random numbers: as easy as
 // 1, 2, 3", SC 2011: ten rounds of two 32x32 -> 64-bit products each).  The mask
@@ -126,9 +126,11 @@ __device__ __forceinline__ void drop_frag(int64_t i0, int64_t n, int64_t col, in
 // BIAS 0: none; 1: C % VW == 0 and the bias 16-byte aligned (a fragment's bias
 // is one 16-byte read); 2: any other.  VEC: X, residual and Y 16-byte aligned.
 // Flat fragments, so rows of any C; the last one may be partial and is done
-// apart.  Bound by the generator's integer multiplies: f16 32x8192x512 without bias
-// and residual 106 us (537 MB, 76 % of the copy rate), bf16 16x1024x4096 with both 71
-// (403 MB, 84 %).
+// apart.  f16 32x8192x512 without bias and residual 106 us (537 MB, 76 % of the copy
+// rate), bf16 16x1024x4096 with both 71 (403 MB, 84 %).  No unit is full (an instruction
+// issued in 0.6 of the cycles, DRAM at 56 and 63 %, 42 to 51 % of the warps): a thread
+// loads its fragments, makes their words and stores before it loads the next, so the
+// loads and the generator's chains of wide multiplies take turns.
 template <typename T, int BIAS, bool RES, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, int64_t n, int64_t C,
@@ -182,7 +184,7 @@ k_bias_dropout(const T* x, const T* __restrict__ bias, const T* residual, T* y, 
 // adds the dX it writes, in float32 and before they are rounded, to its VW
 // sums, and leaves the sums of its chunk in `partial`: [chunk][C] where one tile covers a
 // walk row (the block adds the repeats of a channel up), else [chunk][walk row].
-// bf16 16x1024x4096: 58 us (268 MB, 69 % of the copy rate), bound as above.
+// bf16 16x1024x4096: 58 us (268 MB, 69 % of the copy rate), with DRAM at 50 %, as above.
 template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kWalkThreads, 4)
 k_bias_dropout_grad(const T* dy, T* dx, int64_t n, int64_t C, WalkPlan p, int64_t full_rows, int64_t rest, DropRng g,

@@ -14,7 +14,7 @@
 // Five forms, in the order in which they are tried:
 //   staged tokens (here)    S = 1, groups of 1, 2, 4 ... 32 fragments, from 1 MB (the
 //                           gradient 2 MB) on: one launch at the copy rate's 75 %
-//                           (bf16 8192x1x4096 27 us; the gradient 8192x1x2048 25.8)
+//                           (bf16 8192x1x4096 27 us; the gradient 8192x1x2048 25)
 //   tokens                  group_norm_fused.cu: S = 1, groups of whole fragments
 //   fused                   group_norm_fused.cu: a sample fits a block's registers
 //   staged split (here)     any other size with 16-byte-aligned tensors whose channels
@@ -28,9 +28,9 @@
 // from it, so that neither a large mean nor an outlying value costs them digits.  The gradient has
 // the same three steps, with per-channel sums of du and du * h beside the groups'.
 // A split form's floor is three reads and writes, not two, where x is larger than
-// L2: bf16 8x16384x512 (134 MB) takes 64 us, 60 at the copy rate; small ones are
-// bound by the latency of their launches (f16 2x4096x320 10.1 us, of which 1.6 are
-// its bytes).
+// L2: bf16 8x16384x512 (134 MB) takes 65 us, 60 at the copy rate; small ones are
+// bound by the latency of their launches (f16 2x4096x320 9.4 us, of which 1.6 are
+// its bytes).  Scratch: a part for each chunk and each group that a tile of it meets.
 //
 // All sums and statistics are float32; results are rounded once, to T.
 #include <algorithm>
@@ -774,7 +774,8 @@ __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blo
 // middle and last position.  Off by k standard deviations it multiplies the rounding of
 // the sums by 1 + k^2; where far_off() shows k > 4 (two of the three are outliers) the
 // item is gone over again about the mean so found, from L2, and the groups whose
-// centre stays get the same sums again.  An item has at most kCentreRows walk rows.
+// centre stays get the same sums again (where every item has to: f32 160x1024x516 in 4
+// groups 197 us to 437, bf16 8x16384x512 80 to 124).  An item has at most kCentreRows rows.
 template <typename T, bool GROUP, bool ODD>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
@@ -1348,6 +1349,7 @@ k_gn_token_staged(const T* x, const T* __restrict__ gamma, const T* __restrict__
       }
 #pragma unroll
       for (int u = 0; u < R; ++u) {
+        // (rsqrtf, within 2 ulp: the other forms divide and take a root)
         const float mu[1] = {c[u] + m[u]}, k = rsqrtf(var[u] + d.eps);
         float f[VW];
 #pragma unroll
@@ -2180,9 +2182,12 @@ GnDims token_grad_dims(DType t, int64_t N, int64_t C, int64_t G) {
 }
 
 // The staged token form from this many bytes of x on; below, the direct form's
-// shorter start wins.  bf16, C = 4096, staged and direct, us: 64 tokens (0.5 MB)
-// 3.75 and 3.30, 128 3.77 and 3.85, 256 3.84 and 5.97, 512 4.9 and 6.4; the
-// gradient 128 11.1 and 8.6, 256 11.5 and 14.0, 512 12.1 and 15.7.
+// shorter start wins.  Staged and direct, us, at 0.5, 1 and 2 MB:
+//   bf16 C = 256   3.4 3.3, 3.4 3.8, 3.5 5.8   gradient  6.2 5.7, 6.5 6.5, 7.0 9.1
+//   bf16 C = 4096  3.5 3.5, 3.5 4.0, 3.6 6.1             8.8 7.5, 9.7 8.0, 10.2 12.8
+//   f32  C = 256   3.0 3.1, 3.0 3.4, 3.1 6.2             5.6 4.8, 5.8 5.9, 6.3 7.6
+//   f32  C = 4096  3.3 3.3, 3.3 3.6, 3.3 6.6             6.9 7.6, 9.1 7.8, 9.3 8.3
+// (f32's wide gradients are the same either way up to 4 MB: 9.9 and 9.4.)
 constexpr int64_t kTokenStagedBytes = int64_t(1) << 20;
 constexpr int64_t kTokenGradStagedBytes = int64_t(2) << 20;
 

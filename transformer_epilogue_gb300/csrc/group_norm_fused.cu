@@ -25,9 +25,9 @@
 // more block sums: f16 1x64x256 5.7 us and 4.7, f32 9651x2x459 122 and 68.)
 //
 // What bounds it: the latency of load, two block reductions and store (f16 1x64x256
-// 4.7 us, 76 such samples 4.7, 300 6.6; as a split form 7.7, 10.2 and 16.4).  Where
-// there are thousands of samples, the instructions of MODE 1 and 2 (bf16 9668x1x2976
-// in groups of 93 118 us, of which 18 are its bytes).  (Spreading
+// 4.3 us, 76 such samples 4.5; as a split form 7.7 and 10.2).  Where there are
+// thousands of samples, the instructions of MODE 1 and 2 (bf16 9668x1x2976
+// in groups of 93 110 us, of which 18 are its bytes).  (Spreading
 // a larger sample over a cluster of up to 16 blocks, with the groups' sums in
 // distributed shared memory, was built and measured: 7.0 us against the split
 // form's 8.6 for f16 2x256x1280, but 20.7 against 11.0 for 2x4096x320 and 156
