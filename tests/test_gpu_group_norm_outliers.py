@@ -118,3 +118,12 @@ def test_outliers_in_a_token(lib, shape, groups, dtype):
     y0, mean0, inv0 = check(lib, clean, groups, 8 * max(1, d // 256) + 5)
     for a, b in ((y, y0), (mean, mean0), (inv, inv0)):
         assert torch.equal(a[1::2], b[1::2])
+
+
+@pytest.mark.parametrize("shape,groups,dtype", [((210, 40, 4098), 2, "f32"), ((210, 40, 4098), 3, "f32"), ((3, 700, 6006), 6, "f16"),
+                                                ((40, 90, 12288), 4, "f32")])
+def test_outlying_first_value_where_the_first_tile_lacks_the_group(lib, shape, groups, dtype):
+    # (the parts of the walk row's first tile are empty for the later groups)
+    x = ordinary(shape, dtype, 5 + sum(shape))
+    x.view(shape[0], shape[1], groups, -1)[:, 0, :, 0] = 30000.0
+    check(lib, x, groups, 256 + 24)

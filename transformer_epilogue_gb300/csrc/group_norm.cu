@@ -1773,8 +1773,8 @@ k_gn_grad_apply(const T* dy, const T* x, const T* __restrict__ gamma, const T* _
 constexpr int kJoinThreads = 64;
 
 // (count, centre, mean - centre, M2) of the parts -> the group's statistics, the means
-// relative to that of the first lane's first part (of a group's parts only ScannedParts
-// can be empty there: to the group's first value).  `lanes` of a warp (a power
+// relative to that of the first lane whose first part is not empty (tiles of a walk row
+// can lack the group; if all do, to the group's first value).  `lanes` of a warp (a power
 // of two) take one (n, g), each keeping up to KEPT parts in registers for the second
 // sum and reading others again; KEPT 1 where a warp's lanes hold all parts of a group (a
 // warp for each group: f16 40x100x16384 in 4096 groups 271 us in all, 97 so).
@@ -1810,8 +1810,9 @@ k_gn_join(const T* x, const float4* partial, GnDims d, float* mean_out, float* i
 #pragma unroll
       for (int u = 0; u < KEPT; ++u) kept[u] = part(lane + u * 32);
       const int lead = (threadIdx.x & 31) - lane;
-      const float mean0 = __shfl_sync(0xffffffffu, kept[0].y + kept[0].z, lead);
-      const float ref = __shfl_sync(0xffffffffu, kept[0].x, lead) > 0.f ? mean0 : first;
+      const unsigned filled = __ballot_sync(0xffffffffu, kept[0].x > 0.f) >> lead & (0xffffffffu >> (32 - lanes));
+      const float mean0 = __shfl_sync(0xffffffffu, kept[0].y + kept[0].z, lead + max(0, __ffs(filled) - 1));
+      const float ref = filled != 0 ? mean0 : first;
       float c = 0.f, s = 0.f, q = 0.f, res = 0.f;
       auto add = [&](float4& v) {
         v.y = (v.y - ref) + v.z;
