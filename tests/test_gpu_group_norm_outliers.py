@@ -9,8 +9,8 @@ terms positive, so with sums of depth d the variance is off by (1 + k^2) (d + 8)
 at most, relatively, and 1/sqrt by half of that.  The mean is off by (d + 8) u
 times the mean distance from the centre, and by two roundings of its own.
 
-Depth: a thread adds at most 256 rows under one centre, then come the block's
-sums, at most 8 + 16; a fused block's threads add 8 rows, and a lane up to 128
+Depth: a thread adds 256 rows one after another, then come those sums and the
+block's, at most 8 + 16 here; a fused block's threads add 8 rows, and a lane up to 128
 columns; a token's lanes 8 values and 5 steps.
 """
 import pytest

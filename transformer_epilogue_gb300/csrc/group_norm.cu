@@ -364,6 +364,19 @@ __device__ __forceinline__ void put(float* s, const float (&v)[VW]) {
     *reinterpret_cast<float4*>(s + threadIdx.x * VW + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
 }
 
+// v += a thread's places, as put left them.
+template <int VW>
+__device__ __forceinline__ void get_more(const float* s, float (&v)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; e += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(s + threadIdx.x * VW + e);
+    v[e] += t.x;
+    v[e + 1] += t.y;
+    v[e + 2] += t.z;
+    v[e + 3] += t.w;
+  }
+}
+
 // A CTA's channel sums, which its threads left at their positions in tot_a and
 // tot_b, to row cta_row of cpart: 2 x [CTA row][C] (one tile), or 2 x [CTA row]
 // [walk row], position 0 being channel 0.
@@ -735,10 +748,14 @@ struct RowStream {
   }
   // f(row, raw) for the walk rows of an item that have a fragment in the thread's
   // column; raw holds four (or at most MOST), two or one rows, so that one row's
-  // arithmetic covers another's latency.
-  template <int MOST = 4, typename F>
-  __device__ __forceinline__ void consume(const Range& range, int mine, F f) {
+  // arithmetic covers another's latency.  start(row): before each stage.
+  struct Nothing {
+    __device__ __forceinline__ void operator()(int) const {}
+  };
+  template <int MOST = 4, typename F, typename S = Nothing>
+  __device__ __forceinline__ void consume(const Range& range, int mine, F f, S start = S{}) {
     stages(range, [&](int r, const unsigned char* src) {
+      start(r);
       const int k = min(rows, mine - r);
       int i = 0;
       for (; i + MOST <= k; i += MOST) {
@@ -775,7 +792,11 @@ __device__ __forceinline__ void consumer_sync() { dev::named_barrier_sync(1, blo
 // the sums by 1 + k^2; where far_off() shows k > 4 (two of the three are outliers) the
 // item is gone over again about the mean so found, from L2, and the groups whose
 // centre stays get the same sums again (where every item has to: f32 160x1024x516 in 4
-// groups 197 us to 437, bf16 8x16384x512 80 to 124).  An item has at most kCentreRows rows.
+// groups 197 us to 437, bf16 8x16384x512 80 to 124).  A thread adds kSumRows rows one after
+// another, then those sums.  (Items of so many rows at most instead: f16 1x8388608x256
+// 2023 us, not 1915.)
+constexpr int kSumRows = 256;
+
 template <typename T, bool GROUP, bool ODD>
 __global__ void __launch_bounds__(kWalkThreads + 32, 2)
 k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
@@ -852,6 +873,28 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
       for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
 #pragma unroll
       for (int e = 0; e < EV; ++e) c[e] = centre[grp[e]];
+      int begun = 0;  // the first row of these sums: earlier ones are in the thread's places
+      auto leave = [&](int row) {
+        if constexpr (EV == 1) {
+#pragma unroll
+          for (int e = 1; e < VW; ++e) {
+            s[0] += s[e];
+            q[0] += q[e];
+          }
+          s_a[threadIdx.x] = begun > 0 ? s_a[threadIdx.x] + s[0] : s[0];
+          s_b[threadIdx.x] = begun > 0 ? s_b[threadIdx.x] + q[0] : q[0];
+        } else {
+          if (begun > 0) {
+            get_more(s_a, s);
+            get_more(s_b, q);
+          }
+          put(s_a, s);
+          put(s_b, q);
+        }
+#pragma unroll
+        for (int e = 0; e < VW; ++e) s[e] = q[e] = 0.f;
+        begun = row;
+      };
       auto add = [&](float (&v)[VW]) {
 #pragma unroll
         for (int e = 0; e < VW; e += 2) {
@@ -869,7 +912,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
           if (!ends.inside(row, e)) v[e] = c[EV == 1 ? 0 : e];
       };
       if constexpr (!again) {
-        rows.consume(r, mine, [&](int row, const auto& raw) {
+        auto take = [&](int row, const auto& raw) {
 #pragma unroll
           for (const auto& one : raw) {
             float v[VW];
@@ -881,31 +924,22 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
             ++row;
             add(v);
           }
+        };
+        rows.consume(r, mine, take, [&](int row) {
+          if (row - begun >= kSumRows && t.mine) leave(row);
         });
       } else {
         const int64_t pitch = p.row_frags * VW, e0 = (r.ra * p.row_frags + t.j) * VW - off;
 #pragma unroll 2
         for (int row = 0; row < mine; ++row) {
+          if (row - begun >= kSumRows) leave(row);
           float v[VW];
           dev::load_frag<T, true>(xs, e0 + row * pitch, d.L, v);
           if (ODD && ends.has(row)) centre_outside(row, v);
           add(v);
         }
       }
-      if (t.mine) {
-        if constexpr (EV == 1) {
-#pragma unroll
-          for (int e = 1; e < VW; ++e) {
-            s[0] += s[e];
-            q[0] += q[e];
-          }
-          s_a[threadIdx.x] = s[0];
-          s_b[threadIdx.x] = q[0];
-        } else {
-          put(s_a, s);
-          put(s_b, q);
-        }
-      }
+      if (t.mine) leave(0);
       consumer_sync();
       // to the first repeat's place (ODD: to the centre's other side, after all places have been read)
       float* t_a = s_a;
@@ -1900,10 +1934,6 @@ k_gn_grad_join(const T* x, const float* gpart, GnDims d, float* m1, float* m2, i
   }
 }
 
-// Walk rows of a chunk at most, in pass 1: a thread adds them one after another under one
-// centre, and one outlying row of them costs no more than its share (see far_off).
-constexpr int64_t kCentreRows = 256;
-
 // CTAs an SM that the general kernels' plan is made for (us, 2, 8 and 16 of them: f16
 // 2x16070x1044 176, 127 and 146, its gradient 263, 217 and 236).
 constexpr int kGeneralCtas = 8;
@@ -1934,10 +1964,6 @@ GnDims dims_of(DType t, int64_t N, int64_t S, int64_t C, int64_t G, float eps, b
       d.p.rows = d.p.rows_per_chunk = 1;
       d.p.chunks = 1;
     }
-  }
-  if (!periods && d.p.rows_per_chunk > kCentreRows) {
-    d.p.rows_per_chunk = kCentreRows;
-    d.p.chunks = int((d.p.rows + kCentreRows - 1) / kCentreRows);
   }
   d.slots = slots_of(d.p, vec_width(t), G, d.D);
   d.frags = d.L / vec_width(t);
