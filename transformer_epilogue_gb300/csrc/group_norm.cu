@@ -1574,14 +1574,17 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
       float ref[VW], c[VW], m2[VW], s[VW], q[VW], cnt[VW];
 #pragma unroll
       for (int e = 0; e < VW; ++e) ref[e] = c[e] = m2[e] = s[e] = q[e] = cnt[e] = 0.f;
+      float whole = 0.f;  // rows since the last fold that count for every element
       auto fold = [&] {
 #pragma unroll
         for (int e = 0; e < VW; ++e) {
+          cnt[e] += whole;
           const float by = cnt[e] > 0.f ? s[e] / cnt[e] : 0.f;
           m2[e] += not_negative(q[e] - s[e] * by);
           c[e] += by;
           s[e] = q[e] = 0.f;
         }
+        whole = 0.f;
       };
       int64_t folded = r.ra;
       int step = U;
@@ -1593,10 +1596,20 @@ k_gn_stats(const T* x, GnDims d, float4* partial, float* mean_out, float* inv_ou
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int64_t e0 = ((r0 + u) * p.row_frags + t.j) * VW - off;
+          if (r0 > r.ra && r0 + u < r.rb && e0 >= 0 && e0 + VW <= d.L) {
 #pragma unroll
-          for (int e = 0; e < VW; ++e) {
+            for (int e = 0; e < VW; ++e) {
+              const float w = (v[u][e] - ref[e]) - c[e];
+              s[e] += w;
+              q[e] = fmaf(w, w, q[e]);
+            }
+            whole += 1.f;
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {  // the item's first rows, and partial fragments
             if (r0 + u < r.rb && e0 + e >= 0 && e0 + e < d.L) {
-              if (cnt[e] == 0.f) ref[e] = v[u][e];
+              if (cnt[e] + whole == 0.f) ref[e] = v[u][e];
               const float w = (v[u][e] - ref[e]) - c[e];
               cnt[e] += 1.f;
               s[e] += w;
