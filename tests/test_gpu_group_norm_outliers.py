@@ -127,3 +127,28 @@ def test_outlying_first_value_where_the_first_tile_lacks_the_group(lib, shape, g
     x = ordinary(shape, dtype, 5 + sum(shape))
     x.view(shape[0], shape[1], groups, -1)[:, 0, :, 0] = 30000.0
     check(lib, x, groups, 256 + 24)
+
+
+@pytest.mark.parametrize("shape,groups,dtype", [((160, 600, 516), 4, "f32"), ((310, 1200, 255), 5, "bf16"), ((210, 300, 513), 9, "f32"),
+                                                ((40, 16, 1000), 1, "f16"), ((2100, 1, 256), 1, "bf16"), ((9, 1, 4096), 2, "f16")])
+def test_second_sums_in_place_and_from_a_graph(lib, shape, groups, dtype):
+    # what goes over its values again must not find its own results there
+    x = ordinary(shape, dtype, 6 + sum(shape))
+    for s in {0, shape[1] // 2, shape[1] - 1}:
+        x[:, s].view(shape[0], groups, -1)[:, :, ::max(1, x.shape[-1] // groups // 2)] = 1000.0
+    gamma, beta = torch.ones_like(x[0, 0]), torch.zeros_like(x[0, 0])
+    want = lib.ep_group_norm(x, gamma, beta, groups, EPS, lib.EP_ACT_SILU, mean=True, inv_std_dev=True)
+    own = x.clone()
+    got = lib.ep_group_norm(own, gamma, beta, groups, EPS, lib.EP_ACT_SILU, Y=own, mean=True, inv_std_dev=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = lib.ep_group_norm(x, gamma, beta, groups, EPS, lib.EP_ACT_SILU, mean=True, inv_std_dev=True)
+    for t in got:
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert lib.ep_pipeline_timeouts() == 0
