@@ -859,7 +859,7 @@ k_gn_stats_staged(const T* x, GnDims d, float4* partial) {
       const int64_t mid = (pos1 - 1 - pos0) / 2 * d.C, last = (pos1 - 1 - pos0) * d.C;
       for (int g = threadIdx.x; g < cols.n_groups; g += consumers) {
         const int lo = cols.lo(g) * per, n = (cols.hi(g) - cols.lo(g)) * per;
-        centre[g] = median3(dev::to_float(first[lo]), dev::to_float(first[mid + lo + n / 2]),
+        centre[g] = centre3(dev::to_float(first[lo]), dev::to_float(first[mid + lo + n / 2]),
                             dev::to_float(first[last + lo + n - 1]));
       }
     }

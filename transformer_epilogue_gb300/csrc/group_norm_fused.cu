@@ -16,8 +16,8 @@
 // kept, lost: f16 300x48x256 7.7 us to 10.8.)
 //
 // Statistics: sums and sums of squares of the distances from a centre of the group,
-// the median of three of its values (the first, a middle, the last), so that no
-// single outlier moves it: k standard deviations off the mean it multiplies the
+// the median of three of its values (the first, a middle, the last; or 0, see centre3),
+// so that no single outlier moves it: k standard deviations off the mean it multiplies the
 // rounding of the sums by 1 + k^2.  Where far_off() shows k > 4 (two outliers of the
 // three) the block sums again, from its registers, about the means so found, and the
 // groups concerned take those sums.  All in float32, in an order that does not depend
@@ -336,7 +336,7 @@ k_gn_fused(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
     const int sn = p.samples == 1 ? 0 : int(unsigned(s) / unsigned(d.G));
     if (n0 + sn < d.N) {
       const T* first = x + (n0 + sn) * d.L + (s - sn * d.G) * d.D;
-      gm[s] = median3(dev::ld1_stream(first), dev::ld1_stream(first + mid), dev::ld1_stream(first + end));
+      gm[s] = centre3(dev::ld1_stream(first), dev::ld1_stream(first + mid), dev::ld1_stream(first + end));
     }
   }
   // this thread's channels and groups
@@ -722,7 +722,9 @@ k_gn_token(const T* x, const T* __restrict__ gamma, const T* __restrict__ beta, 
           for (int e = 0; e < VW; ++e) v[k][e] = 0.f;
         }
       }
-      const float first = __shfl_sync(0xffffffffu, v[0][0], lead);
+      // the first value, or 0 where the first fragment's ends are farther apart (see centre3)
+      const float v0 = __shfl_sync(0xffffffffu, v[0][0], lead), v1 = __shfl_sync(0xffffffffu, v[0][VW - 1], lead);
+      const float first = fabsf(v0) <= fabsf(v1 - v0) ? 0.f : v0;
       float s = 0.f, q = 0.f;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
