@@ -1,7 +1,8 @@
 /*
  * transformer_epilogue_gb300 — C ABI of the fused transformer-block epilogue ops
  * (SkipLayerNormalization, BiasSoftmax, BiasAdd, QuickGelu, GroupNorm and
- * BiasDropout, the last two with their gradients) for one NVIDIA GB300
+ * BiasDropout, the last two with their gradients; an RMS norm to 8 bits and a
+ * matrix product with its epilogue, with their gradients) for one NVIDIA GB300
  * (sm_103a) GPU.
  *
  * The ops are the com.microsoft ONNX Runtime contrib ops whose definitions are
@@ -269,7 +270,15 @@ ep_status ep_quick_gelu(ep_dtype t, const void* X, int64_t numel, float alpha,
                         void* Y, ep_stream_t stream);
 
 /* Activation of GroupNorm (the contrib op's `activation` attribute). */
-typedef enum { EP_ACT_NONE = 0, EP_ACT_SILU = 1 } ep_activation;
+typedef enum {
+  EP_ACT_NONE = 0,
+  EP_ACT_SILU = 1,
+  /* of the matrix product alone */
+  EP_ACT_RELU = 2,
+  EP_ACT_QUICK_GELU = 3,
+  EP_ACT_GELU = 4,
+  EP_ACT_FAST_GELU = 5
+} ep_activation;
 
 /*
  * GroupNorm
@@ -407,6 +416,156 @@ ep_status ep_bias_dropout_grad(ep_dtype t, const void* dY, const int64_t* shape,
 /* Workspace bytes ep_bias_dropout_grad needs for dbias; 0 as well for
  * arguments it rejects. */
 size_t ep_bias_dropout_grad_workspace_size(ep_dtype t, const int64_t* shape, int rank);
+
+/*
+ * MX8: rows held in 8 bits (the OCP microscaling format MXFP8 with E4M3 elements)
+ *
+ *   32 consecutive elements of a row (its last group may be shorter) share one
+ *   E8M0 scale: a byte b that stands for 2^(b - 127), 255 for NaN.
+ *     b = max(1, ceil(log2(amax / 448)) + 127),  amax = the group's largest magnitude
+ *     q = E4M3(x * 2^(127 - b)), rounded to nearest even;  value = q * 2^(b - 127)
+ *   Nothing saturates (|x| 2^(127 - b) <= 448).  A NaN becomes a NaN element; an
+ *   infinity, which E4M3 lacks, makes its group's scale NaN.
+ *   (rows, H) values are rows * H bytes of elements and rows * ceil(H / 32) bytes of
+ *   scales, both dense.  The format comes from the OCP Microscaling Formats
+ *   specification; no op definition covers these entry points.
+ *
+ * ep_quantize_mx8     X (`rank` dims, rows along the last) of T -> Q, scales.
+ * ep_dequantize_mx8   Q, scales -> Y of T: exact, but where a value lies beyond T's
+ *                     range (float16: infinite from 65520 on; subnormals rounded).
+ *
+ * Errors: EP_ERR_UNSUPPORTED for another dtype, rank > 16, a last dimension over
+ * 2^31 - 512 or 2^39 elements; EP_ERR_INVALID_ARG for negative dims, rank 0,
+ * NULL/misaligned pointers or any overlap.
+ */
+ep_status ep_quantize_mx8(ep_dtype t, const void* X, const int64_t* shape, int rank,
+                          void* Q, uint8_t* scales, ep_stream_t stream);
+ep_status ep_dequantize_mx8(ep_dtype t, const void* Q, const uint8_t* scales, const int64_t* shape, int rank,
+                            void* Y, ep_stream_t stream);
+
+/*
+ * RMS norm with the residual's addition and an output in MX8: what
+ * ep_skip_layer_norm_ex computes in its simplified form, ready for an 8-bit
+ * product (the contrib op family's SkipSimplifiedLayerNormalization).
+ *
+ *   s = (input + skip) + bias           (float32, in this order; skip and bias optional)
+ *   input_skip_bias_sum = T(s)          (optional output)
+ *   inv = 1 / sqrt(mean(s^2) + epsilon) over the last axis
+ *   Q, scales = MX8(s * inv * gamma)    (of the float32 values: not rounded to T before)
+ *
+ * input, skip   `rank` dims (1 <= rank <= 16); skip has input's shape, or is NULL.
+ * gamma         H elements (required), H > 0 the last dimension; bias: H elements or NULL.
+ * inv_std_dev   NULL, or one float32 a row.
+ * input_skip_bias_sum   NULL, or the shape of input; may be input or skip.
+ *
+ * Errors: as ep_quantize_mx8; EP_ERR_INVALID_ARG also for H = 0, a negative or NaN
+ * epsilon or an overlap other than the above.
+ */
+ep_status ep_skip_rms_norm_mx8(ep_dtype t, const void* input, const int64_t* shape, int rank,
+                               const void* skip, const void* gamma, const void* bias, float epsilon,
+                               void* Q, uint8_t* scales, void* input_skip_bias_sum, float* inv_std_dev,
+                               ep_stream_t stream);
+
+/*
+ * Gradient of the RMS norm (of ep_skip_rms_norm_mx8, the rounding to 8 bits taken
+ * as the identity, and of ep_skip_layer_norm_ex in its simplified form).
+ *
+ *   u = dY * gamma,  h = s * inv
+ *   dX = inv * (u - h * mean(u * h)) + dsum    (the gradient of input and of skip)
+ *   dgamma = sum over rows of dY * h,  dbias = sum over rows of dX
+ *
+ * s             input_skip_bias_sum as the forward call left it; inv_std_dev its float32 statistic.
+ * dsum          the gradient that reaches input_skip_bias_sum by other ways (the residual stream), or NULL.
+ * dX            the shape of dY; may be dY, s or dsum.
+ * dgamma, dbias H elements of T, or NULL: float32 sums of the unrounded values in a fixed
+ *               order, rounded once.  Of no rows they are set to 0.
+ * workspace     ep_skip_rms_norm_grad_workspace_size() bytes, 16-byte aligned; its contents
+ *               on entry do not matter.  Calls that may overlap on the GPU need one each.
+ *
+ * Errors: as ep_skip_rms_norm_mx8; EP_ERR_WORKSPACE.
+ */
+ep_status ep_skip_rms_norm_grad(ep_dtype t, const void* dY, const void* input_skip_bias_sum, const int64_t* shape,
+                                int rank, const void* gamma, const float* inv_std_dev, const void* dsum,
+                                void* dX, void* dgamma, void* dbias,
+                                void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Workspace bytes ep_skip_rms_norm_grad needs; 0 as well for arguments it rejects. */
+size_t ep_skip_rms_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int rank);
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue
+ *
+ *   z = A W^T + bias,  Y = act(z) + residual
+ *
+ * A             (M, K) row-major; W (N, K) row-major (a row for each output channel).
+ *               ep_matmul_bias_act: of T; ep_matmul_bias_act_mx8: E4M3 elements with
+ *               A_scales (M, ceil(K / 32)) and W_scales (N, ceil(K / 32)), see MX8 above.
+ * t             T, EP_F16 or EP_BF16: bias, residual, Y and Z (and A and W of the first form).
+ * bias          N elements, or NULL.  residual: (M, N), or NULL.
+ * activation    EP_ACT_NONE; EP_ACT_SILU z s(z); EP_ACT_RELU; EP_ACT_QUICK_GELU z s(alpha z);
+ *               EP_ACT_GELU z Phi(z) (the error function); EP_ACT_FAST_GELU its tanh form
+ *               z s(2 sqrt(2/pi) (z + 0.044715 z^3)).  s(x) = 1 / (1 + e^-x); all are 0 at
+ *               z = -infinity.  alpha: of EP_ACT_QUICK_GELU alone (the QuickGelu op's default
+ *               is 1.702), finite.
+ * Y             (M, N); may be residual.
+ * Z             NULL, or the pre-activation as the gradient wants it: (M, N) of T, or with
+ *               Z_scales (M, ceil(N / 32)) in MX8.
+ * Products are exact, sums float32 (in an order that depends on the shape alone),
+ * each result rounded once.
+ * workspace     ep_matmul_bias_act_workspace_size() bytes, 16-byte aligned: rows of K
+ *               elements that are no multiple of 16 bytes, or operands that do not start on
+ *               16-byte boundaries, are copied to where they are.  Calls that may overlap on
+ *               the GPU need one each.
+ * K = 0 gives z = bias.
+ *
+ * Errors: EP_ERR_UNSUPPORTED for another dtype, M, N or K over 2^31 - 512 or operands
+ * over 2^40 elements; EP_ERR_INVALID_ARG for negative sizes, an unknown activation, an infinite or NaN
+ * alpha, missing or misaligned pointers, Z_scales without Z, or an overlap of an output
+ * other than Y exactly residual; EP_ERR_WORKSPACE.
+ */
+ep_status ep_matmul_bias_act(ep_dtype t, const void* A, const void* W, int64_t M, int64_t N, int64_t K,
+                             const void* bias, const void* residual, int activation, float alpha,
+                             void* Y, void* Z, uint8_t* Z_scales,
+                             void* workspace, size_t workspace_bytes, ep_stream_t stream);
+ep_status ep_matmul_bias_act_mx8(ep_dtype t, const void* A, const uint8_t* A_scales,
+                                 const void* W, const uint8_t* W_scales, int64_t M, int64_t N, int64_t K,
+                                 const void* bias, const void* residual, int activation, float alpha,
+                                 void* Y, void* Z, uint8_t* Z_scales,
+                                 void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Workspace bytes of the two (mx8 != 0: of the second).  aligned16 != 0: A and W
+ * start on 16-byte boundaries (0 bytes where K elements are a multiple of 16 bytes).  0 as well for
+ * arguments they reject. */
+size_t ep_matmul_bias_act_workspace_size(int mx8, int64_t M, int64_t N, int64_t K, int aligned16);
+
+/*
+ * Gradient of ep_matmul_bias_act (that of the residual is dY itself), from what
+ * the forward pass kept in T or in MX8.
+ *
+ *   dz = dY * act'(Z),  dA = dz W,  dW = dz^T A,  dbias = sum over rows of dz
+ *
+ * A             (M, K) of T, or with A_scales in MX8 (its values are taken in T for dW).
+ * W             (N, K) of T.
+ * Z             as the forward call left it: (M, N) of T, or with Z_scales in MX8.
+ *               Not read (and may be NULL) with EP_ACT_NONE.
+ * dA, dW, dbias (M, K), (N, K) and N elements of T, or NULL where not wanted.  dz is rounded
+ *               to T in front of the products of dA and dW (not of dbias); sums are float32.
+ *               Sums over no rows (M = 0, or N = 0 for dA) are set to 0.
+ * workspace     ep_matmul_bias_act_grad_workspace_size() bytes, 16-byte aligned (dz and the
+ *               operands that are copied).  Calls that may overlap on the GPU need one each.
+ *
+ * Errors: as ep_matmul_bias_act; no output may overlap another operand.
+ */
+ep_status ep_matmul_bias_act_grad(ep_dtype t, const void* dY, const void* A, const uint8_t* A_scales,
+                                  const void* W, const void* Z, const uint8_t* Z_scales,
+                                  int64_t M, int64_t N, int64_t K, int activation, float alpha,
+                                  void* dA, void* dW, void* dbias,
+                                  void* workspace, size_t workspace_bytes, ep_stream_t stream);
+
+/* Its workspace bytes.  a_mx8: A comes with A_scales; aligned16: dY, W and a
+ * 16-bit A start on 16-byte boundaries.  0 as well for arguments it rejects. */
+size_t ep_matmul_bias_act_grad_workspace_size(int64_t M, int64_t N, int64_t K, int activation, int a_mx8,
+                                              int aligned16);
 
 #ifdef __cplusplus
 }  /* extern "C" */

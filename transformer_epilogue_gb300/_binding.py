@@ -24,7 +24,7 @@ EP_OK, EP_ERR_INVALID_ARG, EP_ERR_UNSUPPORTED, EP_ERR_WORKSPACE, EP_ERR_CUDA = 0
 STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_UNSUPPORTED", 3: "EP_ERR_WORKSPACE",
                 4: "EP_ERR_CUDA"}
 
-EP_ACT_NONE, EP_ACT_SILU = 0, 1
+EP_ACT_NONE, EP_ACT_SILU, EP_ACT_RELU, EP_ACT_QUICK_GELU, EP_ACT_GELU, EP_ACT_FAST_GELU = 0, 1, 2, 3, 4, 5
 
 # Attribute defaults of the op definitions (manifest `attributes` sections).
 DEFAULT_EPSILON = 9.999999960041972e-13   # SkipLayerNormalization
@@ -38,6 +38,7 @@ _lib = None
 
 _i64p = ctypes.POINTER(ctypes.c_int64)
 _vp = ctypes.c_void_p
+_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes)
 _SIGNATURES = {
@@ -73,6 +74,22 @@ _SIGNATURES = {
                                             ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                                             _vp]),
     "ep_bias_dropout_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int]),
+    "ep_quantize_mx8": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, _vp, _vp, _vp]),
+    "ep_dequantize_mx8": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _i64p, ctypes.c_int, _vp, _vp]),
+    "ep_skip_rms_norm_mx8": (ctypes.c_int, [ctypes.c_int, _vp, _i64p, ctypes.c_int, _vp, _vp, _vp, ctypes.c_float,
+                                            _vp, _vp, _vp, _vp, _vp]),
+    "ep_skip_rms_norm_grad": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _i64p, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                             _vp, ctypes.c_size_t, _vp]),
+    "ep_skip_rms_norm_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64p, ctypes.c_int]),
+    "ep_matmul_bias_act": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _i64, _i64, _i64, _vp, _vp, ctypes.c_int,
+                                          ctypes.c_float, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ep_matmul_bias_act_mx8": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                                              ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ep_matmul_bias_act_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int]),
+    "ep_matmul_bias_act_grad": (ctypes.c_int, [ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                               ctypes.c_int, ctypes.c_float, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "ep_matmul_bias_act_grad_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
+                                                                 ctypes.c_int]),
 }
 
 
@@ -613,3 +630,325 @@ def ep_bias_dropout_grad(dY, ratio, seed, offset=0, offset_device=None, dX=None,
         if owned:
             _raw_delete(ws)
     return dX, dbias
+
+
+# ---------------------------------------------------------------------------
+# MX8 (rows in 8 bits: torch.float8_e4m3fn elements, a torch.float8_e8m0fnu scale
+# for each 32 of a row), the RMS norm and the matrix product.  Checks, streams and
+# allocations as above.
+# ---------------------------------------------------------------------------
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+@functools.lru_cache(maxsize=4096)
+def _scale_shape(shape):
+    """The shape of the scales of rows of that shape."""
+    if len(shape) == 0:
+        raise ValueError("rows need a dimension")
+    return torch.Size(shape[:-1] + ((shape[-1] + 31) // 32,))
+
+
+def _mx8_out(name, Q, scales, like, index, shape):
+    """Elements and scales to fill, made where they are not given."""
+    if (Q is None) != (scales is None):
+        raise ValueError(f"{name} and its scales are given together")
+    if Q is None:
+        return (torch.empty(shape, dtype=_E4M3, device=like.device),
+                torch.empty(_scale_shape(shape), dtype=_E8M0, device=like.device))
+    return (_operand(name, Q, like, index, shape, _E4M3),
+            _operand(f"{name}'s scales", scales, like, index, _scale_shape(shape), _E8M0))
+
+
+def ep_quantize_mx8(X, Q=None, scales=None, stream=None):
+    """X's rows (along its last dimension) in MX8.  Returns (Q, scales):
+    float8_e4m3fn of X's shape, and a float8_e8m0fnu scale for each 32 of a row."""
+    index, code = _first("X", X)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_quantize_mx8(X, Q, scales)
+    shape = X.shape
+    Q, scales = _mx8_out("Q", Q, scales, X, index, shape)
+    _check(load_library().ep_quantize_mx8(code, X.data_ptr(), _dims(shape), len(shape), Q.data_ptr(),
+                                          scales.data_ptr(), _raw_stream(index)))
+    return Q, scales
+
+
+def _mx8_in(name, Q, scales):
+    if not isinstance(Q, torch.Tensor) or not Q.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    index = Q.get_device()
+    _operand(name, Q, Q, index, dtype=_E4M3)
+    _operand(f"{name}'s scales", scales, Q, index, _scale_shape(Q.shape), _E8M0)
+    return index
+
+
+def ep_dequantize_mx8(Q, scales, dtype=None, Y=None, stream=None):
+    """The values of MX8 rows as ``dtype`` (or Y's).  Returns Y."""
+    index = _mx8_in("Q", Q, scales)
+    if Y is None and dtype is None:
+        raise ValueError("dtype or Y is required")
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_dequantize_mx8(Q, scales, dtype, Y)
+    shape = Q.shape
+    if Y is None:
+        Y = torch.empty(shape, dtype=dtype, device=Q.device)
+    else:
+        _operand("Y", Y, Q, index, shape, Y.dtype if dtype is None else dtype)
+    _check(load_library().ep_dequantize_mx8(_dtype(Y), Q.data_ptr(), scales.data_ptr(), _dims(shape), len(shape),
+                                            Y.data_ptr(), _raw_stream(index)))
+    return Y
+
+
+def _row_stats(name, t, X, index):
+    if t is None or t is False:
+        return None
+    rows = X.shape[:-1] + (1,)
+    if t is True:
+        return torch.empty(rows, dtype=torch.float32, device=X.device)
+    _operand(name, t, X, index, dtype=torch.float32)
+    if t.numel() != rows.numel():
+        raise ValueError(f"{name} must have {rows.numel()} elements")
+    return t
+
+
+def ep_skip_rms_norm_mx8(input, skip, gamma, bias=None, epsilon=DEFAULT_EPSILON, Q=None, scales=None,
+                         input_skip_bias_sum=None, inv_std_dev=None, stream=None):
+    """RMS norm of (input + skip) + bias to MX8 rows; ``skip`` has input's shape or
+    is None.  ``input_skip_bias_sum`` / ``inv_std_dev``: a tensor to fill (the sum may
+    be input or skip), True to allocate one, or None.  Returns (Q, scales,
+    input_skip_bias_sum, inv_std_dev), the last two None when not requested."""
+    index, code = _first("input", input)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_skip_rms_norm_mx8(input, skip, gamma, bias, epsilon, Q, scales, input_skip_bias_sum, inv_std_dev)
+    shape = input.shape
+    channels = shape[-1:]
+    if skip is not None:
+        _operand("skip", skip, input, index, shape)
+    _operand("gamma", gamma, input, index, channels)
+    if bias is not None:
+        _operand("bias", bias, input, index, channels)
+    Q, scales = _mx8_out("Q", Q, scales, input, index, shape)
+    if input_skip_bias_sum is True:
+        input_skip_bias_sum = torch.empty_like(input)
+    elif input_skip_bias_sum is False:
+        input_skip_bias_sum = None
+    if input_skip_bias_sum is not None:
+        _operand("input_skip_bias_sum", input_skip_bias_sum, input, index, shape)
+    inv_std_dev = _row_stats("inv_std_dev", inv_std_dev, input, index)
+    _check(load_library().ep_skip_rms_norm_mx8(
+        code, input.data_ptr(), _dims(shape), len(shape), _addr(skip), gamma.data_ptr(), _addr(bias), float(epsilon),
+        Q.data_ptr(), scales.data_ptr(), _addr(input_skip_bias_sum), _addr(inv_std_dev), _raw_stream(index)))
+    return Q, scales, input_skip_bias_sum, inv_std_dev
+
+
+@functools.lru_cache(maxsize=4096)
+def _rms_norm_grad_need(code, shape):
+    return int(load_library().ep_skip_rms_norm_grad_workspace_size(code, _dims(shape), len(shape)))
+
+
+def ep_skip_rms_norm_grad_workspace_size(dtype, shape) -> int:
+    """Workspace bytes of ep_skip_rms_norm_grad."""
+    return _rms_norm_grad_need(_code(dtype), tuple(shape))
+
+
+def ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum=None, dX=None, dgamma=True, dbias=None,
+                          workspace=None, stream=None):
+    """Gradient of the RMS norm, from the sum and the statistic that the forward
+    call left (ep_skip_rms_norm_mx8, or ep_skip_layer_norm_ex in its simplified
+    form).  ``dsum``: the gradient that reaches the sum along the residual stream.
+    ``dgamma`` / ``dbias``: tensors to fill, True to allocate, or None.  Returns
+    (dX, dgamma, dbias); dX is the gradient of input and of skip."""
+    index, code = _first("dY", dY)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum, dX, dgamma, dbias, workspace)
+    shape = dY.shape
+    channels = shape[-1:]
+    _operand("input_skip_bias_sum", input_skip_bias_sum, dY, index, shape)
+    _operand("gamma", gamma, dY, index, channels)
+    if not isinstance(inv_std_dev, torch.Tensor):
+        raise ValueError("inv_std_dev is required")
+    _row_stats("inv_std_dev", inv_std_dev, dY, index)
+    if dsum is not None:
+        _operand("dsum", dsum, dY, index, shape)
+    dX = torch.empty_like(dY) if dX is None else _operand("dX", dX, dY, index, shape)
+    dgamma = _param_grad("dgamma", dgamma, dY, index, channels)
+    dbias = _param_grad("dbias", dbias, dY, index, channels)
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, _rms_norm_grad_need(code, shape), dY, s)
+    try:
+        _check(load_library().ep_skip_rms_norm_grad(
+            code, dY.data_ptr(), input_skip_bias_sum.data_ptr(), _dims(shape), len(shape), gamma.data_ptr(),
+            inv_std_dev.data_ptr(), _addr(dsum), dX.data_ptr(), _addr(dgamma), _addr(dbias), ws, wbytes, s))
+    finally:
+        if owned:
+            _raw_delete(ws)
+    return dX, dgamma, dbias
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_sizes(a_shape, w_shape):
+    """(M, N, K) and the result's shape of A (..., K) times W (N, K)."""
+    if len(a_shape) < 1 or len(w_shape) != 2 or a_shape[-1] != w_shape[1]:
+        raise ValueError(f"A (..., K) and W (N, K) do not fit: {tuple(a_shape)} and {tuple(w_shape)}")
+    shape = torch.Size(a_shape[:-1] + w_shape[:1])
+    return torch.Size(a_shape[:-1]).numel(), w_shape[0], w_shape[1], shape
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_need(mx8, m, n, k, aligned):
+    return int(load_library().ep_matmul_bias_act_workspace_size(int(mx8), m, n, k, int(aligned)))
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_grad_need(m, n, k, activation, a_mx8, aligned):
+    return int(load_library().ep_matmul_bias_act_grad_workspace_size(m, n, k, activation, int(a_mx8), int(aligned)))
+
+
+def ep_matmul_bias_act_workspace_size(a_shape, w_shape, mx8=False, aligned=False) -> int:
+    """Workspace bytes of ep_matmul_bias_act for A (..., K) and W (N, K), of 16 bits
+    or (``mx8``) 8.  ``aligned``: both start on 16-byte boundaries."""
+    m, n, k, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
+    return _matmul_need(bool(mx8), m, n, k, bool(aligned))
+
+
+def ep_matmul_bias_act_grad_workspace_size(a_shape, w_shape, activation=EP_ACT_NONE, a_mx8=False, aligned=False) -> int:
+    """Workspace bytes of ep_matmul_bias_act_grad.  ``a_mx8``: A is in MX8;
+    ``aligned``: dY, W and a 16-bit A start on 16-byte boundaries."""
+    m, n, k, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
+    return _matmul_grad_need(m, n, k, int(activation), bool(a_mx8), bool(aligned))
+
+
+def ep_matmul_bias_act(A, W, bias=None, residual=None, activation=EP_ACT_NONE, alpha=DEFAULT_ALPHA, A_scales=None,
+                       W_scales=None, dtype=None, Y=None, Z=None, Z_scales=None, workspace=None, stream=None):
+    """Y = act(A W^T + bias) + residual for A (..., K) and W (N, K), both float16 or
+    bfloat16, or both MX8 (float8_e4m3fn with ``A_scales`` and ``W_scales``; then
+    ``dtype``, or the dtype of Y, residual or bias, is the result's).  ``Z``: the
+    pre-activation, kept for the gradient: None, True (in the result's dtype),
+    torch.float8_e4m3fn (in MX8), or a tensor to fill (with ``Z_scales`` if it is
+    float8_e4m3fn).  Returns (Y, Z, Z_scales), the last two None when not requested."""
+    if not isinstance(A, torch.Tensor) or not A.is_cuda:
+        raise ValueError("A must be a CUDA tensor")
+    index = A.get_device()
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_matmul_bias_act(A, W, bias, residual, activation, alpha, A_scales, W_scales, dtype, Y, Z,
+                                      Z_scales, workspace)
+    mx8 = A.dtype is _E4M3
+    _operand("A", A, A, index)
+    _operand("W", W, A, index)
+    m, n, k, shape = _matmul_sizes(A.shape, W.shape)
+    if mx8:
+        _operand("A_scales", A_scales, A, index, _scale_shape(A.shape), _E8M0)
+        _operand("W_scales", W_scales, A, index, _scale_shape(W.shape), _E8M0)
+        if dtype is None:
+            like = Y if Y is not None else residual if residual is not None else bias
+            if like is None:
+                raise ValueError("dtype is required for 8-bit operands")
+            dtype = like.dtype
+    else:
+        if A_scales is not None or W_scales is not None:
+            raise ValueError("scales belong to float8_e4m3fn operands")
+        if dtype is not None and dtype is not A.dtype:
+            raise TypeError(f"dtype must be the operands' {A.dtype}, not {dtype}")
+        dtype = A.dtype
+    code = _TORCH_TO_EP.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if bias is not None:
+        _operand("bias", bias, A, index, W.shape[:1], dtype)
+    if residual is not None:
+        _operand("residual", residual, A, index, shape, dtype)
+    Y = torch.empty(shape, dtype=dtype, device=A.device) if Y is None else _operand("Y", Y, A, index, shape, dtype)
+    if isinstance(Z, torch.dtype):
+        if Z is not _E4M3 or Z_scales is not None:
+            raise ValueError("Z: None, True, torch.float8_e4m3fn, or a tensor")
+        Z, Z_scales = _mx8_out("Z", None, None, A, index, shape)
+    elif isinstance(Z, torch.Tensor) and Z.dtype is _E4M3:
+        if Z_scales is None:
+            raise ValueError("Z_scales is required for a float8_e4m3fn Z")
+        Z, Z_scales = _mx8_out("Z", Z, Z_scales, A, index, shape)
+    else:
+        if Z_scales is not None:
+            raise ValueError("Z_scales belongs to a float8_e4m3fn Z")
+        if Z is True:
+            Z = torch.empty(shape, dtype=dtype, device=A.device)
+        elif Z is False:
+            Z = None
+        elif Z is not None:
+            _operand("Z", Z, A, index, shape, dtype)
+    lib = load_library()
+    pa, pw = A.data_ptr(), W.data_ptr()
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, _matmul_need(mx8, m, n, k, (pa | pw) & 15 == 0), A, s)
+    rest = (m, n, k, _addr(bias), _addr(residual), int(activation), float(alpha), Y.data_ptr(), _addr(Z),
+            _addr(Z_scales), ws, wbytes, s)
+    try:
+        if mx8:
+            _check(lib.ep_matmul_bias_act_mx8(code, pa, A_scales.data_ptr(), pw, W_scales.data_ptr(), *rest))
+        else:
+            _check(lib.ep_matmul_bias_act(code, pa, pw, *rest))
+    finally:
+        if owned:
+            _raw_delete(ws)
+    return Y, Z, Z_scales
+
+
+def _grad_out(name, t, like, index, shape):
+    if t is None or t is False:
+        return None
+    if t is True:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    return _operand(name, t, like, index, shape)
+
+
+def ep_matmul_bias_act_grad(dY, A, W, Z=None, activation=EP_ACT_NONE, alpha=DEFAULT_ALPHA, A_scales=None,
+                            Z_scales=None, dA=True, dW=True, dbias=None, workspace=None, stream=None):
+    """Gradient of ep_matmul_bias_act (the residual's is dY itself).  ``A`` and ``Z``
+    (needed with an activation) are what the forward pass kept, each in dY's
+    dtype or in MX8 (float8_e4m3fn with ``A_scales``, ``Z_scales``); ``W`` has dY's
+    dtype.  ``dA`` / ``dW`` / ``dbias``: tensors to fill, True to allocate, or None.
+    Returns (dA, dW, dbias), None where not requested."""
+    index, code = _first("dY", dY)
+    other = _elsewhere(stream, index)
+    if other is not None:
+        with other:
+            return ep_matmul_bias_act_grad(dY, A, W, Z, activation, alpha, A_scales, Z_scales, dA, dW, dbias, workspace)
+    _operand("W", W, dY, index)
+    a_mx8 = A_scales is not None
+    _operand("A", A, dY, index, dtype=_E4M3 if a_mx8 else None)
+    m, n, k, shape = _matmul_sizes(A.shape, W.shape)
+    if a_mx8:
+        _operand("A_scales", A_scales, dY, index, _scale_shape(A.shape), _E8M0)
+    if dY.shape != shape:
+        raise ValueError(f"dY must have shape {tuple(shape)}, not {tuple(dY.shape)}")
+    activation = int(activation)
+    if activation != EP_ACT_NONE:
+        if Z is None:
+            raise ValueError("Z is required with an activation")
+        _operand("Z", Z, dY, index, shape, _E4M3 if Z_scales is not None else None)
+        if Z_scales is not None:
+            _operand("Z_scales", Z_scales, dY, index, _scale_shape(shape), _E8M0)
+    dA = _grad_out("dA", dA, dY, index, A.shape)
+    dW = _grad_out("dW", dW, dY, index, W.shape)
+    dbias = _param_grad("dbias", dbias, dY, index, W.shape[:1])
+    py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
+    aligned = (py | pw | (0 if a_mx8 else pa)) & 15 == 0
+    s = _raw_stream(index)
+    ws, wbytes, owned = _scratch(workspace, _matmul_grad_need(m, n, k, activation, a_mx8, aligned), dY, s)
+    try:
+        _check(load_library().ep_matmul_bias_act_grad(
+            code, py, pa, _addr(A_scales), pw, _addr(Z), _addr(Z_scales), m, n, k, activation, float(alpha), _addr(dA),
+            _addr(dW), _addr(dbias), ws, wbytes, s))
+    finally:
+        if owned:
+            _raw_delete(ws)
+    return dA, dW, dbias

@@ -25,7 +25,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtransformer_epilogue.so")
 
 SOURCES = ["ep_api.cpp", "skip_layer_norm.cu", "bias_softmax.cu", "elementwise.cu", "group_norm.cu",
-           "group_norm_fused.cu", "bias_dropout.cu"]
+           "group_norm_fused.cu", "bias_dropout.cu", "rms_norm_mx8.cu", "matmul.cu"]
 # Compiled in one piece: split, a kernel's code depends on what else the file holds and on the number of
 # cores (the same k_gn_token_staged ran f32 4096x1x1024 in 8.3 or 10.5 us from one build to the next).
 WHOLE = ("group_norm.cu", "group_norm_fused.cu")

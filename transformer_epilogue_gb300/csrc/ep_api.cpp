@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "ep_internal.h"
+#include "mx8_internal.h"
 #include "training_internal.h"
 
 namespace {
@@ -135,12 +136,13 @@ int ep_abi_version(void) { return kAbiVersion; }
 
 namespace {
 cudaError_t sum_pipe_timeouts(unsigned int* total, bool clear) {
-  unsigned int a = 0, b = 0, c = 0, g = 0;
+  unsigned int a = 0, b = 0, c = 0, g = 0, m = 0;
   cudaError_t e = ep::sln_pipe_timeouts(&a, clear);
   if (e == cudaSuccess) e = ep::softmax_pipe_timeouts(&b, clear);
   if (e == cudaSuccess) e = ep::elementwise_pipe_timeouts(&c, clear);
   if (e == cudaSuccess) e = ep::group_norm_pipe_timeouts(&g, clear);
-  *total = a + b + c + g;
+  if (e == cudaSuccess) e = ep::matmul_pipe_timeouts(&m, clear);
+  *total = a + b + c + g + m;
   return e;
 }
 }  // namespace
@@ -683,6 +685,284 @@ ep_status ep_bias_dropout_grad(ep_dtype t, const void* dY, const int64_t* shape,
   int launches = 0;
   cudaError_t e = ep::launch_bias_dropout_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
   return finish(e, launches, "bias_dropout_grad");
+}
+
+namespace {
+
+constexpr int64_t kMostDim = (int64_t(1) << 31) - 512;  // coordinates of tiles are 32-bit
+
+ep_status mx8_shape(const char* op, ep_dtype t, const int64_t* shape, int rank, int64_t* rows, int64_t* H) {
+  if (!valid_dtype(t)) return fail(EP_ERR_UNSUPPORTED, "%s: dtype %d is not float32/float16/bfloat16", op, int(t));
+  if (rank < 1) return fail(EP_ERR_INVALID_ARG, "%s: rank must be >= 1", op);
+  if (rank > kMaxRank) return fail(EP_ERR_UNSUPPORTED, "%s: rank %d > %d", op, rank, kMaxRank);
+  if (shape == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: NULL shape array", op);
+  int64_t n = 0;
+  if (!dims_product(shape, 0, rank, &n) || !dims_product(shape, 0, rank - 1, rows))
+    return fail(EP_ERR_INVALID_ARG, "%s: negative or overflowing dims", op);
+  *H = shape[rank - 1];
+  if (*H > kMostDim || (n + 255) / 256 > kMostDim)
+    return fail(EP_ERR_UNSUPPORTED, "%s: rows of %lld elements, %lld elements in all (at most 2^31 - 512 and 2^39)", op,
+                (long long)*H, (long long)n);
+  return EP_OK;
+}
+
+int64_t mx8_scales(int64_t rows, int64_t H) { return rows * ((H + 31) / 32); }
+
+// No two of `outs` overlap, nor an output an input unless exactly and `inplace` says so for that pair.
+ep_status check_outputs(const char* op, const Span* outs, int n_outs, const Span* ins, int n_ins, int in_place_out = -1,
+                        unsigned in_place_ins = 0) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return fail(EP_ERR_INVALID_ARG, "%s: two outputs overlap", op);
+    for (int j = 0; j < n_ins; ++j) {
+      const bool may = i == in_place_out && (in_place_ins >> j & 1u) != 0;
+      if (may ? bad_overlap_inplace_ok(outs[i], ins[j]) : overlap(outs[i], ins[j]))
+        return fail(EP_ERR_INVALID_ARG, "%s: an output overlaps an input%s", op,
+                    may ? " other than as an exact alias" : "");
+    }
+  }
+  return EP_OK;
+}
+
+ep_status check_pointers(const char* op, const void* const* ptrs, int n, int a) {
+  for (int i = 0; i < n; ++i)
+    if (ptrs[i] != nullptr && !aligned(ptrs[i], a))
+      return fail(EP_ERR_INVALID_ARG, "%s: pointer %p is not aligned to %d bytes", op, ptrs[i], a);
+  return EP_OK;
+}
+
+ep_status check_matmul_activation(const char* op, int activation, float alpha) {
+  if (activation < EP_ACT_NONE || activation > EP_ACT_FAST_GELU)
+    return fail(EP_ERR_INVALID_ARG, "%s: activation %d is none of EP_ACT_*", op, activation);
+  if (!std::isfinite(alpha)) return fail(EP_ERR_INVALID_ARG, "%s: alpha must be finite", op);
+  return EP_OK;
+}
+
+bool matmul_sizes_fit(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMost = int64_t(1) << 40;  // elements of an operand: more than the device holds
+  return M >= 0 && N >= 0 && K >= 0 && M <= kMostDim && N <= kMostDim && K <= kMostDim && M * N <= kMost &&
+         M * K <= kMost && N * K <= kMost;
+}
+
+ep_status check_matmul_shape(const char* op, ep_dtype t, int64_t M, int64_t N, int64_t K) {
+  if (t != EP_F16 && t != EP_BF16)
+    return fail(EP_ERR_UNSUPPORTED, "%s: dtype %d is not float16/bfloat16", op, int(t));
+  if (M < 0 || N < 0 || K < 0) return fail(EP_ERR_INVALID_ARG, "%s: negative M, N or K", op);
+  if (!matmul_sizes_fit(M, N, K))
+    return fail(EP_ERR_UNSUPPORTED, "%s: M, N and K are at most 2^31 - 512, an operand 2^40 elements", op);
+  return EP_OK;
+}
+
+ep_status matmul_call(const char* op, ep_dtype t, bool mx8, const void* A, const uint8_t* a_scales, const void* W,
+                      const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, const void* bias, const void* residual,
+                      int activation, float alpha, void* Y, void* Z, uint8_t* z_scales, void* workspace,
+                      size_t workspace_bytes, ep_stream_t stream) {
+  if (ep_status s = check_matmul_shape(op, t, M, N, K); s != EP_OK) return s;
+  if (ep_status s = check_matmul_activation(op, activation, alpha); s != EP_OK) return s;
+  if (M == 0 || N == 0) return ok();
+  if ((K > 0 && (A == nullptr || W == nullptr)) || Y == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: A, W and Y are required", op);
+  if (mx8 && K > 0 && (a_scales == nullptr || w_scales == nullptr))
+    return fail(EP_ERR_INVALID_ARG, "%s: the scales of A and W are required", op);
+  if (z_scales != nullptr && Z == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: the scales of Z without Z", op);
+  const void* ptrs[] = {bias, residual, Y, z_scales == nullptr ? Z : nullptr, mx8 ? nullptr : A, mx8 ? nullptr : W};
+  if (ep_status s = check_pointers(op, ptrs, 6, 2); s != EP_OK) return s;
+  const int es = mx8 ? 1 : 2;
+  const Span ins[] = {{A, M * K * es},       {W, N * K * es}, {a_scales, mx8_scales(M, K)}, {w_scales, mx8_scales(N, K)},
+                      {bias, N * 2}, {residual, M * N * 2}};
+  const Span outs[] = {{Y, M * N * 2}, {Z, M * N * (z_scales != nullptr ? 1 : 2)}, {z_scales, mx8_scales(M, N)}};
+  if (ep_status s = check_outputs(op, outs, 3, ins, 6, 0, 1u << 5); s != EP_OK) return s;
+  const size_t need = ep::matmul_workspace_bytes(mx8, M, N, K, aligned(A, 16) && aligned(W, 16));
+  const Span all[] = {ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], outs[0], outs[1], outs[2]};
+  if (ep_status s = check_workspace(op, workspace, workspace_bytes, need, all, 9); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::MatmulArgs a{to_dtype(t), mx8, A, a_scales, W, w_scales, bias, residual, Y, Z, z_scales, M, N, K,
+                         activation, alpha, workspace};
+  int launches = 0;
+  const cudaError_t e = ep::launch_matmul(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
+}
+
+}  // namespace
+
+ep_status ep_quantize_mx8(ep_dtype t, const void* X, const int64_t* shape, int rank, void* Q, uint8_t* scales,
+                          ep_stream_t stream) {
+  const char* op = "quantize_mx8";
+  int64_t rows = 0, H = 0;
+  if (ep_status s = mx8_shape(op, t, shape, rank, &rows, &H); s != EP_OK) return s;
+  if (rows == 0 || H == 0) return ok();
+  if (X == nullptr || Q == nullptr || scales == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: X, Q and scales are required", op);
+  if (ep_status s = check_pointers(op, &X, 1, esize(t)); s != EP_OK) return s;
+  const Span ins[] = {{X, rows * H * esize(t)}}, outs[] = {{Q, rows * H}, {scales, mx8_scales(rows, H)}};
+  if (ep_status s = check_outputs(op, outs, 2, ins, 1); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::QuantizeArgs a{to_dtype(t), X, static_cast<uint8_t*>(Q), scales, rows, H};
+  int launches = 0;
+  const cudaError_t e = ep::launch_quantize_mx8(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
+}
+
+ep_status ep_dequantize_mx8(ep_dtype t, const void* Q, const uint8_t* scales, const int64_t* shape, int rank, void* Y,
+                            ep_stream_t stream) {
+  const char* op = "dequantize_mx8";
+  int64_t rows = 0, H = 0;
+  if (ep_status s = mx8_shape(op, t, shape, rank, &rows, &H); s != EP_OK) return s;
+  if (rows == 0 || H == 0) return ok();
+  if (Y == nullptr || Q == nullptr || scales == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: Q, scales and Y are required", op);
+  const void* y = Y;
+  if (ep_status s = check_pointers(op, &y, 1, esize(t)); s != EP_OK) return s;
+  const Span outs[] = {{Y, rows * H * esize(t)}}, ins[] = {{Q, rows * H}, {scales, mx8_scales(rows, H)}};
+  if (ep_status s = check_outputs(op, outs, 1, ins, 2); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::QuantizeArgs a{to_dtype(t), Y, static_cast<uint8_t*>(const_cast<void*>(Q)), const_cast<uint8_t*>(scales),
+                           rows, H};
+  int launches = 0;
+  const cudaError_t e = ep::launch_dequantize_mx8(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
+}
+
+ep_status ep_skip_rms_norm_mx8(ep_dtype t, const void* input, const int64_t* shape, int rank, const void* skip,
+                               const void* gamma, const void* bias, float epsilon, void* Q, uint8_t* scales,
+                               void* input_skip_bias_sum, float* inv_std_dev, ep_stream_t stream) {
+  const char* op = "skip_rms_norm_mx8";
+  int64_t rows = 0, H = 0;
+  if (ep_status s = mx8_shape(op, t, shape, rank, &rows, &H); s != EP_OK) return s;
+  if (!(epsilon >= 0.0f)) return fail(EP_ERR_INVALID_ARG, "%s: epsilon must be >= 0", op);
+  if (H == 0) return fail(EP_ERR_INVALID_ARG, "%s: rows of no elements", op);
+  if (rows == 0) return ok();
+  if (input == nullptr || gamma == nullptr || Q == nullptr || scales == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: input, gamma, Q and scales are required", op);
+  const int es = esize(t);
+  const void* ptrs[] = {input, skip, gamma, bias, input_skip_bias_sum};
+  if (ep_status s = check_pointers(op, ptrs, 5, es); s != EP_OK) return s;
+  const void* inv = inv_std_dev;
+  if (ep_status s = check_pointers(op, &inv, 1, 4); s != EP_OK) return s;
+  const int64_t nb = rows * H * es;
+  const Span ins[] = {{input, nb}, {skip, nb}, {gamma, H * es}, {bias, H * es}};
+  const Span outs[] = {{input_skip_bias_sum, nb}, {Q, rows * H}, {scales, mx8_scales(rows, H)}, {inv_std_dev, rows * 4}};
+  if (ep_status s = check_outputs(op, outs, 4, ins, 4, 0, 3u); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::RmsNormArgs a{to_dtype(t), input, skip, bias, gamma, static_cast<uint8_t*>(Q), scales, input_skip_bias_sum,
+                          inv_std_dev, rows, H, epsilon};
+  int launches = 0;
+  const cudaError_t e = ep::launch_rms_norm_mx8(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
+}
+
+size_t ep_skip_rms_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, int rank) {
+  int64_t rows = 0, H = 0;
+  char saved[sizeof(g_err)];
+  std::memcpy(saved, g_err, sizeof(g_err));
+  const ep_status s = mx8_shape("skip_rms_norm_grad_workspace_size", t, shape, rank, &rows, &H);
+  std::memcpy(g_err, saved, sizeof(g_err));
+  return s != EP_OK || rows == 0 || H == 0 ? 0 : ep::rms_norm_grad_workspace_bytes(to_dtype(t), rows, H);
+}
+
+ep_status ep_skip_rms_norm_grad(ep_dtype t, const void* dY, const void* input_skip_bias_sum, const int64_t* shape,
+                                int rank, const void* gamma, const float* inv_std_dev, const void* dsum, void* dX,
+                                void* dgamma, void* dbias, void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+  const char* op = "skip_rms_norm_grad";
+  int64_t rows = 0, H = 0;
+  if (ep_status s = mx8_shape(op, t, shape, rank, &rows, &H); s != EP_OK) return s;
+  if (H == 0) return fail(EP_ERR_INVALID_ARG, "%s: rows of no elements", op);
+  const int es = esize(t);
+  const void* ptrs[] = {dY, input_skip_bias_sum, gamma, dsum, dX, dgamma, dbias};
+  if (ep_status s = check_pointers(op, ptrs, 7, es); s != EP_OK) return s;
+  const void* inv = inv_std_dev;
+  if (ep_status s = check_pointers(op, &inv, 1, 4); s != EP_OK) return s;
+  const int64_t nb = rows * H * es;
+  const Span ins[] = {{dY, nb}, {input_skip_bias_sum, nb}, {dsum, nb}, {gamma, H * es}, {inv_std_dev, rows * 4}};
+  const Span outs[] = {{dX, nb}, {dgamma, H * es}, {dbias, H * es}};
+  if (ep_status s = check_outputs(op, outs, 3, ins, 5, 0, 7u); s != EP_OK) return s;
+  if (rows == 0) {
+    if (ep_status s = zero_fill(op, dgamma, H * es, stream); s != EP_OK) return s;
+    if (ep_status s = zero_fill(op, dbias, H * es, stream); s != EP_OK) return s;
+    return ok();
+  }
+  if (dY == nullptr || input_skip_bias_sum == nullptr || gamma == nullptr || inv_std_dev == nullptr || dX == nullptr)
+    return fail(EP_ERR_INVALID_ARG, "%s: dY, input_skip_bias_sum, gamma, inv_std_dev and dX are required", op);
+  const Span all[] = {ins[0], ins[1], ins[2], ins[3], ins[4], outs[0], outs[1], outs[2]};
+  const size_t need = ep::rms_norm_grad_workspace_bytes(to_dtype(t), rows, H);
+  if (ep_status s = check_workspace(op, workspace, workspace_bytes, need, all, 8); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::RmsNormGradArgs a{to_dtype(t), dY, input_skip_bias_sum, gamma, inv_std_dev, dsum, dX, dgamma, dbias,
+                              rows, H, workspace};
+  int launches = 0;
+  const cudaError_t e = ep::launch_rms_norm_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
+}
+
+ep_status ep_matmul_bias_act(ep_dtype t, const void* A, const void* W, int64_t M, int64_t N, int64_t K,
+                             const void* bias, const void* residual, int activation, float alpha, void* Y, void* Z,
+                             uint8_t* Z_scales, void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+  return matmul_call("matmul_bias_act", t, false, A, nullptr, W, nullptr, M, N, K, bias, residual, activation, alpha, Y,
+                     Z, Z_scales, workspace, workspace_bytes, stream);
+}
+
+ep_status ep_matmul_bias_act_mx8(ep_dtype t, const void* A, const uint8_t* A_scales, const void* W,
+                                 const uint8_t* W_scales, int64_t M, int64_t N, int64_t K, const void* bias,
+                                 const void* residual, int activation, float alpha, void* Y, void* Z,
+                                 uint8_t* Z_scales, void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+  return matmul_call("matmul_bias_act_mx8", t, true, A, A_scales, W, W_scales, M, N, K, bias, residual, activation,
+                     alpha, Y, Z, Z_scales, workspace, workspace_bytes, stream);
+}
+
+size_t ep_matmul_bias_act_workspace_size(int mx8, int64_t M, int64_t N, int64_t K, int aligned16) {
+  if (!matmul_sizes_fit(M, N, K) || M == 0 || N == 0) return 0;
+  return ep::matmul_workspace_bytes(mx8 != 0, M, N, K, aligned16 != 0);
+}
+
+size_t ep_matmul_bias_act_grad_workspace_size(int64_t M, int64_t N, int64_t K, int activation, int a_mx8,
+                                              int aligned16) {
+  if (!matmul_sizes_fit(M, N, K)) return 0;
+  return ep::matmul_grad_workspace_bytes(M, N, K, activation != EP_ACT_NONE, a_mx8 != 0, aligned16 != 0);
+}
+
+ep_status ep_matmul_bias_act_grad(ep_dtype t, const void* dY, const void* A, const uint8_t* A_scales, const void* W,
+                                  const void* Z, const uint8_t* Z_scales, int64_t M, int64_t N, int64_t K,
+                                  int activation, float alpha, void* dA, void* dW, void* dbias, void* workspace,
+                                  size_t workspace_bytes, ep_stream_t stream) {
+  const char* op = "matmul_bias_act_grad";
+  if (ep_status s = check_matmul_shape(op, t, M, N, K); s != EP_OK) return s;
+  if (ep_status s = check_matmul_activation(op, activation, alpha); s != EP_OK) return s;
+  const bool act = activation != EP_ACT_NONE;
+  const void* ptrs[] = {dY, A_scales == nullptr ? A : nullptr, W, Z_scales == nullptr ? Z : nullptr, dA, dW, dbias};
+  if (ep_status s = check_pointers(op, ptrs, 7, 2); s != EP_OK) return s;
+  const Span ins[] = {{dY, M * N * 2},
+                      {A, M * K * (A_scales != nullptr ? 1 : 2)},
+                      {A_scales, mx8_scales(M, K)},
+                      {W, N * K * 2},
+                      {Z, M * N * (Z_scales != nullptr ? 1 : 2)},
+                      {Z_scales, mx8_scales(M, N)}};
+  const Span outs[] = {{dA, M * K * 2}, {dW, N * K * 2}, {dbias, N * 2}};
+  if (ep_status s = check_outputs(op, outs, 3, ins, 6); s != EP_OK) return s;
+  if (M > 0 && N > 0) {
+    if (dY == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: dY is required", op);
+    if (act && Z == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: Z is required with an activation", op);
+    if (K > 0 && dA != nullptr && W == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: dA needs W", op);
+    if (K > 0 && dW != nullptr && A == nullptr) return fail(EP_ERR_INVALID_ARG, "%s: dW needs A", op);
+  }
+  const bool all16 = aligned(dY, 16) && aligned(W, 16) && (A_scales != nullptr || aligned(A, 16));
+  const size_t need = ep::matmul_grad_workspace_bytes(M, N, K, act, A_scales != nullptr, all16);
+  const Span all[] = {ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], outs[0], outs[1], outs[2]};
+  if (ep_status s = check_workspace(op, workspace, workspace_bytes, need, all, 9); s != EP_OK) return s;
+  if (M == 0)
+    if (ep_status s = zero_fill(op, dbias, N * 2, stream); s != EP_OK) return s;
+  DevInfo dv;
+  if (ep_status s = device_info(&dv); s != EP_OK) return s;
+  const ep::MatmulGradArgs a{to_dtype(t), dY, A, A_scales, W, act ? Z : nullptr, act ? Z_scales : nullptr, dA, dW,
+                             dbias, M, N, K, activation, alpha, workspace};
+  int launches = 0;
+  const cudaError_t e = ep::launch_matmul_grad(a, dv.sm_count, reinterpret_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches, op);
 }
 
 }  // extern "C"

@@ -1,0 +1,1177 @@
+// Matrix product with bias, activation and residual in its epilogue, on the
+// tcgen05 tensor cores, and what its gradient needs beside the products.
+//
+//   forward   z = A W^T + bias, y = act(z) + residual          A (M, K), W (N, K)
+//   gradient  dz = dY act'(z), dA = dz W, dW = dz^T A, dbias = sum of dz's rows
+//
+// All three products are C(i, j) = sum_k R(i, k) Q(j, k), i the rows and j the
+// columns of a row-major result, with R and Q either K-major (k contiguous:
+// A, W, and dz in dA) or MN-major (i or j contiguous: W in dA, dz and A in dW);
+// the tensor core reads both (umma.cuh), so nothing is transposed in memory.
+// Sums are float32 in tensor memory; E4M3 operands bring a scale for each 32 of
+// K, which the tensor core applies (kind::mxf8f6f4), so an 8-bit product has no
+// rounding but its sums'.
+//
+// Two kernels:
+//   k_mm_pair   large results: pairs of CTAs on tiles of 256 x 256 (8-bit: 256 x 192,
+//     the scales need the tensor memory of the rest), one pair to two SMs, walking over
+//     the tiles.  A pair reads each operand byte once for two SMs, which halves what
+//     shared memory and L2 deliver per product.  Two accumulators: a tile is written
+//     while the next is computed.
+//   k_mm_split  few rows, or few tiles: 128 columns of the result (the weights' rows,
+//     on the tensor core's 128 lanes) x 16 to 128 rows, K cut among the CTAs of a
+//     cluster, whose partial sums meet in distributed shared memory in the order of
+//     their ranks: one launch, no scratch, the same result every time.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "activation.cuh"
+#include "column_walk.cuh"
+#include "device_common.cuh"
+#include "launch_util.h"
+#include "mx8.cuh"
+#include "mx8_internal.h"
+#include "smem_limit.h"
+#include "umma.cuh"
+
+namespace ep {
+namespace {
+
+using namespace dev;
+
+// ---------------------------------------------------------------------------
+// epilogue
+// ---------------------------------------------------------------------------
+
+struct Epilogue {
+  const void* bias;      // nullable
+  const void* residual;  // nullable
+  void* y;
+  void* z;               // nullable: T, or (z_scales) E4M3
+  uint8_t* z_scales;
+  int64_t rows, cols;
+  int act;
+  float alpha;
+  bool vec;              // rows of y, z and residual start on 16-byte boundaries (E4M3: of cols % 16 == 0 too)
+  bool vec_bias;
+};
+
+// ---------------------------------------------------------------------------
+// the scales of 8-bit operands
+//
+// A K tile of 128 has 4 scales a row.  The tensor core wants the scales of rows
+// l, l + 32, l + 64, l + 96 (4 bytes each) in lane l of tensor memory, so the
+// shared-memory block that is copied there has 16 bytes for each l: one lane
+// brings them together.  In global memory they are rows of `groups` bytes.
+// ---------------------------------------------------------------------------
+
+struct ScaleRows {
+  const uint8_t* p;
+  int64_t rows, groups;
+  bool words;  // groups and p are multiples of 4
+};
+
+// 4 bytes from group g on of a row; 127 (the scale 1) outside, where the values are 0.
+__device__ __forceinline__ uint32_t scale_word(const ScaleRows& s, int64_t row, int64_t g) {
+  if (row >= s.rows || g >= s.groups) return 0x7F7F7F7Fu;
+  const uint8_t* p = s.p + row * s.groups + g;
+  if (s.words) return __ldg(reinterpret_cast<const uint32_t*>(p));
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= (g + i < s.groups ? uint32_t(__ldg(p + i)) : 127u) << (8 * i);
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// large results: a pair of CTAs
+// ---------------------------------------------------------------------------
+
+constexpr int kLine = 128;                 // bytes of K (or of MN) in an operand line
+constexpr int kTileM = 256;                // rows of a pair's tile
+constexpr int kHalfM = kTileM / 2;
+constexpr int kOperandM = kHalfM * kLine;  // bytes of a CTA's half of R
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = (4 + kEpiWarps) * 32;
+constexpr int kStaging = 4096;             // bytes an epilogue warp has to turn rows around
+constexpr int kRaster = 8;                 // tiles of rows that are walked together
+
+template <bool MX> struct PairShape {
+  static constexpr int kTileN = MX ? 192 : 256;
+  static constexpr int kHalfN = kTileN / 2;
+  static constexpr int kOperandN = kHalfN * kLine;
+  static constexpr int kStageBytes = kOperandM + kOperandN;
+  static constexpr int kScaleBytes = MX ? 512 + 1024 : 0;  // R's 128 rows, Q's 192 in two blocks
+  static constexpr int kStages = 5;
+  static constexpr int kChunk = MX ? 32 : 64;              // columns that a warp turns around at once
+  static constexpr int kBarriers = 2 * kStages + 5;
+  static constexpr int kSmem = 1024 + kStages * (kStageBytes + kScaleBytes) + kEpiWarps * (kStaging + 64 * 4) +
+                               kBarriers * 8 + 16;
+};
+
+struct PairArgs {
+  CUtensorMap r, q;
+  ScaleRows rs, qs;
+  Epilogue epi;
+  int64_t tiles_m, tiles_n;
+  int k_tiles;
+  int k_tile;            // elements
+  bool r_mn, q_mn;
+  uint32_t idesc;
+};
+
+// A staging row of NC 16-byte words; words are exchanged within a row so that
+// neither one word of 32 rows nor NC words of 32 / NC rows meet in a bank.
+template <int NC>
+__device__ __forceinline__ uint8_t* staged(uint8_t* buf, int r, int c) {
+  return buf + (r * NC + (c ^ ((r / (8 / NC)) & (NC - 1)))) * 16;
+}
+
+// A warp's 32 rows x NC words between shared and global memory, in whole words
+// along a row (`vec`) or element by element.
+template <int NC, typename E, bool LOAD>
+__device__ __forceinline__ void turn_rows(uint8_t* buf, E* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                          bool vec, int lane) {
+  constexpr int PER = 16 / sizeof(E);
+  if (vec) {
+    uint4 w[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int idx = i * 32 + lane, r = idx / NC, c = idx % NC;
+      const int64_t row = row0 + r, col = col0 + c * PER;
+      const bool in = row < rows && col < cols;
+      uint4* p = reinterpret_cast<uint4*>(g + row * cols + col);
+      if constexpr (LOAD) {
+        w[i] = in ? __ldcs(p) : make_uint4(0, 0, 0, 0);
+      } else if (in) {
+        __stcs(p, *reinterpret_cast<const uint4*>(staged<NC>(buf, r, c)));
+      }
+    }
+    if constexpr (LOAD) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int idx = i * 32 + lane;
+        *reinterpret_cast<uint4*>(staged<NC>(buf, idx / NC, idx % NC)) = w[i];
+      }
+    }
+  } else {
+    for (int r = 0; r < 32 && row0 + r < rows; ++r)
+#pragma unroll
+      for (int l = lane; l < NC * PER; l += 32) {
+        if (col0 + l >= cols) continue;
+        E* p = g + (row0 + r) * cols + col0 + l;
+        E* s = reinterpret_cast<E*>(staged<NC>(buf, r, l / PER)) + l % PER;
+        if constexpr (LOAD) *s = *p;
+        else *p = *s;
+      }
+  }
+}
+
+// CW columns of a warp's 32 rows, from tensor memory to the outputs.
+template <typename T, int CW>
+__device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, float* bs, uint32_t tmem, int64_t row0,
+                                           int64_t col0, int lane) {
+  if (row0 >= e.rows || col0 >= e.cols) return;
+  const T* bias = static_cast<const T*>(e.bias);
+#pragma unroll
+  for (int i = 0; i < CW / 32; ++i) {
+    const int64_t c = col0 + lane + 32 * i;
+    bs[lane + 32 * i] = bias != nullptr && c < e.cols ? to_float(__ldg(bias + c)) : 0.f;
+  }
+  __syncwarp();
+  auto load = [&](int h, float (&z)[32]) {
+    uint32_t r[32];
+    tmem_ld32(tmem + 32 * h, r);
+    tmem_wait_ld(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = *reinterpret_cast<const float4*>(bs + 32 * h + 4 * i);
+      z[4 * i] = __uint_as_float(r[4 * i]) + b.x;
+      z[4 * i + 1] = __uint_as_float(r[4 * i + 1]) + b.y;
+      z[4 * i + 2] = __uint_as_float(r[4 * i + 2]) + b.z;
+      z[4 * i + 3] = __uint_as_float(r[4 * i + 3]) + b.w;
+    }
+  };
+  constexpr int NC = CW / 8, NC8 = CW / 16;
+  auto put = [&](int h, const float (&z)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f[8] = {z[8 * i], z[8 * i + 1], z[8 * i + 2], z[8 * i + 3],
+                          z[8 * i + 4], z[8 * i + 5], z[8 * i + 6], z[8 * i + 7]};
+      *reinterpret_cast<uint4*>(staged<NC>(buf, lane, 4 * h + i)) = Conv<T>::pack(f);
+    }
+  };
+  if (e.z != nullptr) {
+    const int64_t groups = (e.cols + kMxGroup - 1) / kMxGroup;
+#pragma unroll
+    for (int h = 0; h < CW / 32; ++h) {
+      float z[32];
+      load(h, z);
+      if (e.z_scales == nullptr) {
+        put(h, z);
+      } else {  // a lane has the whole group (columns behind the last are 0)
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(z[i]));
+        const uint32_t b = mx_scale(amax);
+        const float k = mx_factor(b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = e4m3x4(z[16 * i + 4 * j] * k, z[16 * i + 4 * j + 1] * k, z[16 * i + 4 * j + 2] * k,
+                          z[16 * i + 4 * j + 3] * k);
+          *reinterpret_cast<uint4*>(staged<NC8>(buf, lane, 2 * h + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (row0 + lane < e.rows && col0 + 32 * h < e.cols)
+          e.z_scales[(row0 + lane) * groups + (col0 / 32 + h)] = uint8_t(b);
+      }
+    }
+    __syncwarp();
+    if (e.z_scales == nullptr)
+      turn_rows<NC, T, false>(buf, static_cast<T*>(e.z), row0, col0, e.rows, e.cols, e.vec, lane);
+    else
+      turn_rows<NC8, uint8_t, false>(buf, static_cast<uint8_t*>(e.z), row0, col0, e.rows, e.cols,
+                                     e.vec && e.cols % 16 == 0, lane);
+    __syncwarp();
+  }
+  if (e.residual != nullptr) {
+    turn_rows<NC, T, true>(buf, static_cast<T*>(const_cast<void*>(e.residual)), row0, col0, e.rows, e.cols, e.vec, lane);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int h = 0; h < CW / 32; ++h) {
+    float z[32];
+    load(h, z);
+    by_act(e.act, [&](auto tag) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = act_value<decltype(tag)::value>(z[i], e.alpha);
+    });
+    if (e.residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[8];
+        Conv<T>::unpack(*reinterpret_cast<const uint4*>(staged<NC>(buf, lane, 4 * h + i)), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[8 * i + j] += f[j];
+      }
+    }
+    put(h, z);
+  }
+  __syncwarp();
+  turn_rows<NC, T, false>(buf, static_cast<T*>(e.y), row0, col0, e.rows, e.cols, e.vec, lane);
+  __syncwarp();
+}
+
+// Where tile `t` of the walk lies: kRaster tiles of rows together, column by column.
+__device__ __forceinline__ void tile_place(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t* m, int64_t* n) {
+  const int64_t band = t / (kRaster * tiles_n), first = band * kRaster;
+  const int64_t high = min(tiles_m - first, int64_t(kRaster)), in = t - band * kRaster * tiles_n;
+  *n = in / high;
+  *m = first + in - *n * high;
+}
+
+// Warps: 0 loads, 1 issues the products (of the pair's first CTA alone), 2 brings
+// the scales, 3 has the tensor memory, 4.. write.  Barriers of a stage: `full`
+// (the first CTA's: both CTAs' bytes, and their scales' warps), `empty` (each
+// CTA's: the products that read it are done); of an accumulator: `ready` (each
+// CTA's), `taken` (the first CTA's: all epilogue warps of both).  A wait that
+// runs out ends its role; the others run out in turn, copies in flight are waited
+// for, and the CTAs leave together.
+template <typename T, bool MX>
+__global__ void __launch_bounds__(kPairThreads, 1)
+k_mm_pair(const __grid_constant__ PairArgs a) {
+  using S = PairShape<MX>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* scales = smem + S::kStages * S::kStageBytes;
+  uint8_t* staging = scales + S::kStages * S::kScaleBytes;
+  float* bias = reinterpret_cast<float*>(staging + kEpiWarps * kStaging);
+  uint64_t* full = reinterpret_cast<uint64_t*>(bias + kEpiWarps * 64);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* ready = empty + S::kStages;
+  uint64_t* taken = ready + 2;
+  uint64_t* drained = taken + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full + s, MX ? 3 : 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(ready + i, 1);
+      mbar_init(taken + i, 2 * kEpiWarps);
+    }
+    mbar_init(drained, 1);
+    mbar_init_fence();
+    prefetch_map(&a.r);
+    prefetch_map(&a.q);
+  }
+  if (warp == 3) tmem_alloc<true>(tmem_at, 512);
+  __syncwarp();
+  tmem_fence_before();
+  cluster_sync();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_at;
+  pdl_wait();
+  pdl_trigger();
+
+  const int64_t tiles = a.tiles_m * a.tiles_n, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring ring(S::kStages);
+      int issued = 0;
+      bool ok = true;
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        int64_t tm, tn;
+        tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+        const int m = int(tm * kTileM) + int(rank) * kHalfM, n = int(tn * S::kTileN) + int(rank) * S::kHalfN;
+        for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
+          if (issued >= S::kStages && !mbar_wait_cluster(empty + ring.st, ring.phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = cluster_addr(smem_addr(full + ring.st), 0);
+          const uint32_t dst = smem_addr(smem + ring.st * S::kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full + ring.st, 2 * S::kStageBytes);
+          const int kk = k * a.k_tile;
+          if (!MX && a.r_mn) {
+            for (int c = 0; c < kHalfM / 64; ++c) tma_load<true>(dst + c * 8192, &a.r, bar, m + 64 * c, kk);
+          } else {
+            tma_load<true>(dst, &a.r, bar, kk, m);
+          }
+          if (!MX && a.q_mn) {
+            for (int c = 0; c < S::kHalfN / 64; ++c)
+              tma_load<true>(dst + kOperandM + c * 8192, &a.q, bar, n + 64 * c, kk);
+          } else {
+            tma_load<true>(dst + kOperandM, &a.q, bar, kk, n);
+          }
+          issued = min(issued + 1, S::kStages);
+        }
+      }
+      // the last loads (of both CTAs) have landed before anyone leaves
+      if (rank == 0)
+        for (int i = 0; i < issued; ++i) {
+          ring.st = ring.st == 0 ? S::kStages - 1 : ring.st - 1;
+          if (ring.st == S::kStages - 1) ring.phase ^= 1;
+          if (!mbar_wait_cluster(full + ring.st, ring.phase)) break;
+        }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      Ring ring(S::kStages);
+      bool ok = true;
+      int64_t i = 0;
+      const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
+      for (int64_t t = pair; t < tiles && ok; t += pairs, ++i) {
+        const int acc = int(i & 1);
+        if (i >= 2 && !mbar_wait_cluster(taken + acc, uint32_t((i >> 1) - 1) & 1)) break;
+        tmem_fence_after();
+        const uint32_t d = tmem + acc * S::kTileN;
+        for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
+          if (!mbar_wait_cluster(full + ring.st, ring.phase)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t at = smem_addr(smem + ring.st * S::kStageBytes);
+          uint64_t rd = operand_desc(at, a.r_mn), qd = operand_desc(at + kOperandM, a.q_mn);
+          if constexpr (MX) {
+            const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
+            const uint32_t sfr = tmem + 2 * S::kTileN, sfq = sfr + 4;
+            copy_scales<true>(sfr, scales_desc(sf));
+            copy_scales<true>(sfq, scales_desc(sf + 512));
+            copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
+#pragma unroll
+            for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
+              mma_mx8<true>(d, rd, qd, a.idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<true>(d, rd, qd, a.idesc, (k | j) != 0);
+          }
+          mma_commit<true>(empty + ring.st);
+        }
+        if (ok) mma_commit<true>(ready + acc);
+      }
+      if (!ok) {  // products in flight end before the tensor memory is given back
+        mma_commit<true>(drained);
+        mbar_wait_cluster(drained, 0);
+      }
+    }
+  } else if (warp == 2) {
+    if constexpr (MX) {
+      Ring ring(S::kStages);
+      int64_t i = 0;
+      bool ok = true;
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        int64_t tm, tn;
+        tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+        const int64_t m = tm * kTileM + rank * kHalfM + lane, n = tn * S::kTileN + lane;
+        uint32_t w[10], next[10];
+        auto fetch = [&](int k, uint32_t (&v)[10]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = scale_word(a.rs, m + 32 * j, int64_t(k) * 4);
+#pragma unroll
+          for (int j = 0; j < 6; ++j) v[4 + j] = scale_word(a.qs, n + 32 * j, int64_t(k) * 4);
+        };
+        fetch(0, next);
+        for (int k = 0; k < a.k_tiles && ok; ++k, ++i, ring.next()) {
+#pragma unroll
+          for (int j = 0; j < 10; ++j) w[j] = next[j];
+          if (k + 1 < a.k_tiles) fetch(k + 1, next);
+          if (i >= S::kStages && !mbar_wait_cluster(empty + ring.st, ring.phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint4* sf = reinterpret_cast<uint4*>(scales + ring.st * S::kScaleBytes);
+          sf[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+          sf[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+          sf[64 + lane] = make_uint4(w[8], w[9], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(full + ring.st), 0));
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    const int w = warp - 4;
+    uint8_t* buf = staging + w * kStaging;
+    int64_t i = 0;
+    for (int64_t t = pair; t < tiles; t += pairs, ++i) {
+      const int acc = int(i & 1);
+      if (!mbar_wait_cluster(ready + acc, uint32_t(i >> 1) & 1)) break;
+      tmem_fence_after();
+      int64_t tm, tn;
+      tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+      const int64_t row0 = tm * kTileM + rank * kHalfM + 32 * (w & 3);
+      const uint32_t at = tmem + acc * S::kTileN + (uint32_t(32 * (w & 3)) << 16);
+      for (int c = (w >> 2) * S::kHalfN; c < ((w >> 2) + 1) * S::kHalfN; c += S::kChunk)
+        pair_chunk<T, S::kChunk>(a.epi, buf, bias + w * 64, at + c, row0, tn * S::kTileN + c, lane);
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(taken + acc), 0));
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  cluster_sync();
+  tmem_fence_after();
+  if (warp == 3) tmem_free<true>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// few rows or few tiles: K cut among the CTAs of a cluster
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitThreads = 256;
+constexpr int kSplitN = 128;                  // columns of the result
+constexpr int kOperandQ = kSplitN * kLine;
+constexpr int kSplitMostRows = 128;
+constexpr int kSplitBudget = 110 * 1024;      // two CTAs an SM
+constexpr int kSplitMostStages = 6;
+
+struct SplitArgs {
+  CUtensorMap r, q;
+  ScaleRows rs, qs;
+  Epilogue epi;
+  int64_t tiles_m;
+  int tile_m;            // rows: 16, 32, 64 or 128
+  int k_tiles, k_tile;
+  int stages;
+  bool r_mn, q_mn;
+  uint32_t idesc;
+};
+
+// The outputs of 8 neighbouring columns of a row.  All lanes of a warp call it
+// (four of them have a group of 32 together); `in`: the row and the columns are there.
+template <typename T>
+__device__ __forceinline__ void finish8(const Epilogue& e, float (&z)[8], int64_t row, int64_t col, bool in) {
+  const T* bias = static_cast<const T*>(e.bias);
+  const int here = in ? int(min(int64_t(8), e.cols - col)) : 0;
+  const int64_t at = row * e.cols + col;
+  if (bias != nullptr) {
+    if (e.vec_bias && here == 8) {
+      float b[8];
+      Conv<T>::unpack(ld16_keep(bias + col), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] += b[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < here) z[i] += to_float(__ldg(bias + col + i));
+    }
+  }
+  if (e.z != nullptr) {
+    if (e.z_scales == nullptr) {
+      T* p = static_cast<T*>(e.z) + at;
+      if (e.vec && here == 8) {
+        st16_stream(p, Conv<T>::pack(z));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < here) st1_stream(p + i, z[i]);
+      }
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < here) amax = fmaxf(amax, fabsf(z[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const uint32_t b = mx_scale(amax);
+      const float k = mx_factor(b);
+      const uint32_t lo = e4m3x4(z[0] * k, z[1] * k, z[2] * k, z[3] * k),
+                     hi = e4m3x4(z[4] * k, z[5] * k, z[6] * k, z[7] * k);
+      uint8_t* p = static_cast<uint8_t*>(e.z) + at;
+      if (e.vec && here == 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < here) p[i] = uint8_t((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      }
+      if (here > 0 && col % kMxGroup == 0)
+        e.z_scales[row * ((e.cols + kMxGroup - 1) / kMxGroup) + col / kMxGroup] = uint8_t(b);
+    }
+  }
+  by_act(e.act, [&](auto tag) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<decltype(tag)::value>(z[i], e.alpha);
+  });
+  T* y = static_cast<T*>(e.y) + at;
+  const T* res = static_cast<const T*>(e.residual) + (e.residual != nullptr ? at : 0);
+  if (e.vec && here == 8) {
+    if (e.residual != nullptr) {
+      float f[8];
+      Conv<T>::unpack(ld16_stream(res), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] += f[i];
+    }
+    st16_stream(y, Conv<T>::pack(z));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < here) st1_stream(y + i, e.residual != nullptr ? z[i] + ld1_stream(res + i) : z[i]);
+  }
+}
+
+// Warps: 0 loads, 1 issues the products, 2 brings the scales, 3 has the tensor
+// memory; then all of them write.
+template <typename T, bool MX>
+__global__ void __launch_bounds__(kSplitThreads)
+k_mm_split(const __grid_constant__ SplitArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kSplitMostStages], empty[kSplitMostStages], done;
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed;
+  const int stage_bytes = kOperandQ + a.tile_m * kLine;
+  uint8_t* scales = smem + a.stages * stage_bytes;  // 1024 bytes a stage
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t splits;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+  const uint32_t rank = cluster_rank();
+  const int64_t tile = blockIdx.x / splits;
+  const int64_t m0 = tile % a.tiles_m * a.tile_m, n0 = tile / a.tiles_m * kSplitN;
+  const int k0 = int(int64_t(a.k_tiles) * rank / splits), k1 = int(int64_t(a.k_tiles) * (rank + 1) / splits);
+  const uint32_t columns = MX ? 256 : a.tile_m < 32 ? 32 : a.tile_m;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(full + s, MX ? 2 : 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(&done, 1);
+    mbar_init_fence();
+    if (k0 < k1) {
+      prefetch_map(&a.r);
+      prefetch_map(&a.q);
+    }
+  }
+  if (warp == 3) tmem_alloc<false>(&tmem_at, columns);
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0 && lane == 0) {
+    Ring ring(a.stages);
+    int issued = 0;
+    for (int k = k0; k < k1; ++k, ring.next()) {
+      if (issued >= a.stages && !mbar_wait(empty + ring.st, ring.phase ^ 1)) break;
+      const uint32_t bar = smem_addr(full + ring.st), dst = smem_addr(smem + ring.st * stage_bytes);
+      mbar_arrive_expect_tx(full + ring.st, stage_bytes);
+      const int kk = k * a.k_tile, m = int(m0), n = int(n0);
+      if (!MX && a.q_mn) {
+        for (int c = 0; c < kSplitN / 64; ++c) tma_load<false>(dst + c * 8192, &a.q, bar, n + 64 * c, kk);
+      } else {
+        tma_load<false>(dst, &a.q, bar, kk, n);
+      }
+      if (!MX && a.r_mn) {
+        for (int c = 0; c < a.tile_m / 64; ++c) tma_load<false>(dst + kOperandQ + c * 8192, &a.r, bar, m + 64 * c, kk);
+      } else {
+        tma_load<false>(dst + kOperandQ, &a.r, bar, kk, m);
+      }
+      issued = min(issued + 1, a.stages);
+    }
+    for (int i = 0; i < issued; ++i) {  // the last loads have landed before the stages serve for anything else
+      ring.st = ring.st == 0 ? a.stages - 1 : ring.st - 1;
+      if (ring.st == a.stages - 1) ring.phase ^= 1;
+      if (!mbar_wait(full + ring.st, ring.phase)) break;
+    }
+  } else if (warp == 1 && lane == 0) {
+    Ring ring(a.stages);
+    const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
+    bool ok = true;
+    for (int k = k0; k < k1; ++k, ring.next()) {
+      if (!mbar_wait(full + ring.st, ring.phase)) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+      const uint32_t at = smem_addr(smem + ring.st * stage_bytes);
+      uint64_t qd = operand_desc(at, a.q_mn), rd = operand_desc(at + kOperandQ, a.r_mn);
+      if constexpr (MX) {
+        const uint32_t sf = smem_addr(scales + ring.st * 1024);
+        const uint32_t sfq = tmem + 128, sfr = tmem + 132;
+        copy_scales<false>(sfq, scales_desc(sf));
+        copy_scales<false>(sfr, scales_desc(sf + 512));
+#pragma unroll
+        for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
+          mma_mx8<false>(tmem, qd, rd, a.idesc | mma_scale_byte(j), sfq, sfr, k > k0 || j > 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<false>(tmem, qd, rd, a.idesc, k > k0 || j > 0);
+      }
+      mma_commit<false>(empty + ring.st);
+    }
+    mma_commit<false>(&done);
+    if (!mbar_wait(&done, 0) || !ok) failed = 1;
+  } else if (MX && warp == 2) {
+    Ring ring(a.stages);
+    uint32_t w[8], next[8];
+    auto fetch = [&](int k, uint32_t (&v)[8]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = scale_word(a.qs, n0 + lane + 32 * j, int64_t(k) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[4 + j] = 32 * j + lane < a.tile_m ? scale_word(a.rs, m0 + lane + 32 * j, int64_t(k) * 4) : 0x7F7F7F7Fu;
+    };
+    if (k0 < k1) fetch(k0, next);
+    for (int k = k0; k < k1; ++k, ring.next()) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = next[j];
+      if (k + 1 < k1) fetch(k + 1, next);
+      if (k - k0 >= a.stages && !mbar_wait(empty + ring.st, ring.phase ^ 1)) break;
+      uint4* sf = reinterpret_cast<uint4*>(scales + ring.st * 1024);
+      sf[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+      sf[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + ring.st);
+    }
+  }
+  __syncwarp();
+  __syncthreads();  // the products are done, the stages free
+  tmem_fence_after();
+
+  // this CTA's sums, (row, column) in float32
+  float* sums = reinterpret_cast<float*>(smem);
+  const int half = a.tile_m / 2;
+  for (int c = (warp >> 2) * half; c < ((warp >> 2) + 1) * half; c += 8) {
+    uint32_t v[8];
+    tmem_ld8(tmem + c + (uint32_t(32 * (warp & 3)) << 16), v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sums[(c + i) * kSplitN + 32 * (warp & 3) + lane] = k0 < k1 ? __uint_as_float(v[i]) : 0.f;
+  }
+  tmem_fence_before();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+  tmem_fence_after();
+  if (warp == 3) tmem_free<false>(tmem, columns);
+
+  // each CTA finishes its share of the rows
+  bool bad = false;
+  for (uint32_t s = 0; s < splits; ++s) bad |= ld_cluster_word(cluster_addr(smem_addr(&failed), s)) != 0;
+  const int share = a.tile_m / int(splits);
+  const uint32_t base = smem_addr(sums);
+  for (int idx = threadIdx.x; idx < share * (kSplitN / 8); idx += kSplitThreads) {
+    const int r = int(rank) * share + idx / (kSplitN / 8), c = idx % (kSplitN / 8) * 8;
+    float z[8] = {};
+    const uint32_t at = base + (r * kSplitN + c) * 4;
+    for (uint32_t s = 0; s < splits; ++s) {
+      const uint32_t p = cluster_addr(at, s);
+      const float4 lo = ld_cluster(p), hi = ld_cluster(p + 16);
+      const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] += f[i];
+    }
+    const int64_t row = m0 + r, col = n0 + c;
+    finish8<T>(a.epi, z, row, col, row < a.epi.rows && col < a.epi.cols && !bad);
+  }
+  if (splits > 1) {  // the others have read this CTA's sums
+    __syncwarp();
+    cluster_sync();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// beside the products
+// ---------------------------------------------------------------------------
+
+// Rows of n elements to rows `ld` apart (the tail set to 0): operands whose rows do not start on 16-byte boundaries.
+template <typename E>
+__global__ void __launch_bounds__(256)
+k_pitch(const E* __restrict__ x, E* __restrict__ y, int64_t rows, uint32_t n, uint32_t ld) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = int64_t(gridDim.x) * 8, segs = (ld + 255) / 256;
+  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows * segs; i += warps) {
+    const int64_t r = i / segs;
+    const uint32_t c0 = uint32_t(i - r * segs) * 256 + lane;
+    E v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c0 + 32 * u < n ? x[r * n + c0 + 32 * u] : E(0);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (c0 + 32 * u < ld) y[r * ld + c0 + 32 * u] = v[u];
+  }
+}
+
+// dz = dY act'(z) (rounded to T for the tensor cores, as dY itself was: a
+// relative 2^-9 of bf16 that averages out over the sums), rows `ld` apart, and
+// the column sums of dz before that rounding.  A lane has VW columns, the 8
+// warps share a chunk of rows; bound by memory.  ZM: z is absent, T, or MX8.
+constexpr int kSlopeThreads = 256;
+template <typename T, int VW, int ZM>
+__global__ void __launch_bounds__(kSlopeThreads)
+k_act_slope(const T* __restrict__ dy, const void* __restrict__ zp, const uint8_t* __restrict__ z_scales,
+            T* __restrict__ dz, int64_t rows, int64_t cols, int64_t ld, int64_t rows_per_chunk, int act, float alpha,
+            float* __restrict__ partial) {
+  constexpr int U = 4;  // rows whose loads are in flight together
+  __shared__ float part[8][32][VW + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t(blockIdx.x) * 32 + lane) * VW, groups = (cols + kMxGroup - 1) / kMxGroup;
+  const int64_t r0 = int64_t(blockIdx.y) * rows_per_chunk, r1 = min(r0 + rows_per_chunk, rows);
+  float sum[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) sum[e] = 0.f;
+  by_act(act, [&](auto tag) {
+    if (c >= ld) return;
+    for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
+      float d[U][VW], z[U][VW];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = r + 8 * u;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) d[u][e] = z[u][e] = 0.f;
+        if (row >= r1 || c >= cols) continue;
+        const int64_t at = row * cols + c;
+        if constexpr (VW == 8) Conv<T>::unpack(ld16_stream(dy + at), d[u]);
+        else d[u][0] = ld1_stream(dy + at);
+        if constexpr (ZM == 1) {
+          const T* p = static_cast<const T*>(zp) + at;
+          if constexpr (VW == 8) Conv<T>::unpack(ld16_stream(p), z[u]);
+          else z[u][0] = ld1_stream(p);
+        } else if constexpr (ZM == 2) {
+          const uint8_t* p = static_cast<const uint8_t*>(zp) + at;
+          const float k = mx_value(z_scales[row * groups + c / kMxGroup]);
+          if constexpr (VW == 8) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
+            const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = e4m3_floats(w[e]);
+              z[u][2 * e] = t.x * k;
+              z[u][2 * e + 1] = t.y * k;
+            }
+          } else {
+            z[u][0] = e4m3_floats(*p).x * k;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = r + 8 * u;
+        if (row >= r1) continue;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          if constexpr (ZM != 0) d[u][e] *= act_slope<decltype(tag)::value>(z[u][e], alpha);
+          sum[e] += d[u][e];
+        }
+        if (dz != nullptr) {
+          if constexpr (VW == 8) *reinterpret_cast<uint4*>(dz + row * ld + c) = Conv<T>::pack(d[u]);
+          else dz[row * ld + c] = from_float(d[u][0], T());
+        }
+      }
+    }
+  });
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) part[warp][lane][e] = sum[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * VW; i += kSlopeThreads) {
+    const int64_t col = int64_t(blockIdx.x) * 32 * VW + i;
+    if (col >= cols) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += part[w][i / VW][i % VW];
+    partial[int64_t(blockIdx.y) * cols + col] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+bool on(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, found once (the library does not link the driver).
+cudaError_t encoder(EncodeFn* fn) {
+  static std::mutex mu;
+  static EncodeFn found = nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (found == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &how);
+    if (e != cudaSuccess) return e;
+    if (how != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorNotSupported;
+    found = reinterpret_cast<EncodeFn>(p);
+  }
+  *fn = found;
+  return cudaSuccess;
+}
+
+// One operand of a product: `rows` rows (or columns of the result) by `depth`,
+// rows (mn: depths) `ld` elements apart.
+struct Operand {
+  const void* p;
+  const uint8_t* scales;
+  int64_t rows, depth, ld;
+  bool mn;
+};
+
+cudaError_t make_map(CUtensorMap* map, DType t, bool mx8, const Operand& o, int box_rows) {
+  EncodeFn encode = nullptr;
+  const cudaError_t e = encoder(&encode);
+  if (e != cudaSuccess) return e;
+  const int es = mx8 ? 1 : 2;
+  const cuuint64_t dims[2] = {cuuint64_t(o.mn ? o.rows : o.depth), cuuint64_t(o.mn ? o.depth : o.rows)};
+  const cuuint64_t pitch[1] = {cuuint64_t(o.ld) * es};
+  const cuuint32_t box[2] = {cuuint32_t(kLine / es), cuuint32_t(o.mn ? 64 : box_rows)};
+  const cuuint32_t ones[2] = {1, 1};
+  const CUresult r = encode(map, mx8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : t == DType::F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                            2, const_cast<void*>(o.p), dims, pitch, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+ScaleRows scale_rows(const Operand& o) {
+  const int64_t g = mx_groups(o.depth);
+  return ScaleRows{o.scales, o.rows, g, g % 4 == 0 && on(o.scales, 4)};
+}
+
+template <typename Args>
+cudaError_t launch_cluster(void (*kernel)(Args), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                           cudaStream_t stream, const Args& args) {
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = EP_PDL ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+// Pairs of CTAs that fit on the device at once.
+template <typename Args>
+cudaError_t resident_pairs(void (*kernel)(Args), unsigned threads, size_t smem, int sm_count, int* pairs) {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 64 && known[dev] != 0) {
+    *pairs = known[dev];
+    return cudaSuccess;
+  }
+  e = allow_smem(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(sm_count) / 2 * 2);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  *pairs = std::max(1, n);
+  if (dev < 64) known[dev] = *pairs;
+  return cudaSuccess;
+}
+
+struct SplitPlan {
+  int tile_m, splits;
+};
+
+// Rows: the smallest tile that holds them, up to 128 (an MN-major operand comes
+// 64 rows at a time).  K is cut until the CTAs fill the device twice over, each
+// with two K tiles at least.
+SplitPlan plan_split(int64_t rows, int64_t cols, int64_t k_tiles, bool r_mn, int sm_count) {
+  SplitPlan p{r_mn ? 64 : 16, 1};
+  while (p.tile_m < rows && p.tile_m < kSplitMostRows) p.tile_m *= 2;
+  const int64_t tiles = (rows + p.tile_m - 1) / p.tile_m * ((cols + kSplitN - 1) / kSplitN);
+  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sm_count && k_tiles >= 4 * p.splits) p.splits *= 2;
+  return p;
+}
+
+// The pair kernel where its tiles keep the SMs busy; the other where they would leave many idle.
+bool take_pair(int64_t rows, int64_t cols, int tile_n, int sm_count) {
+  const int64_t tiles = (rows + kTileM - 1) / kTileM * ((cols + tile_n - 1) / tile_n);
+  return rows > 128 && tiles * 2 >= sm_count / 2;
+}
+
+template <typename T, bool MX>
+cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue& epi, int sm_count,
+                    cudaStream_t stream, int* launches) {
+  const int k_tile = MX ? 128 : 64;
+  const int64_t k_tiles = (r.depth + k_tile - 1) / k_tile;
+  cudaError_t e;
+  if (take_pair(r.rows, q.rows, PairShape<MX>::kTileN, sm_count) && k_tiles > 0) {
+    using S = PairShape<MX>;
+    PairArgs a = {};
+    if ((e = make_map(&a.r, t, MX, r, kHalfM)) != cudaSuccess) return e;
+    if ((e = make_map(&a.q, t, MX, q, S::kHalfN)) != cudaSuccess) return e;
+    if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
+    a.epi = epi;
+    a.tiles_m = (r.rows + kTileM - 1) / kTileM;
+    a.tiles_n = (q.rows + S::kTileN - 1) / S::kTileN;
+    a.k_tiles = int(k_tiles);
+    a.k_tile = k_tile;
+    a.r_mn = r.mn;
+    a.q_mn = q.mn;
+    a.idesc = MX ? mma_desc_mx8(kTileM, S::kTileN)
+                 : mma_desc_f16(t == DType::BF16, r.mn, q.mn, kTileM, S::kTileN);
+    int pairs = 1;
+    if ((e = resident_pairs(k_mm_pair<T, MX>, kPairThreads, S::kSmem, sm_count, &pairs)) != cudaSuccess) return e;
+    const int64_t tiles = a.tiles_m * a.tiles_n;
+    e = launch_cluster(k_mm_pair<T, MX>, unsigned(2 * std::min<int64_t>(tiles, pairs)), kPairThreads, S::kSmem, 2,
+                       stream, a);
+  } else {
+    const SplitPlan p = plan_split(r.rows, q.rows, k_tiles, r.mn, sm_count);
+    SplitArgs a = {};
+    if (k_tiles > 0) {
+      if ((e = make_map(&a.r, t, MX, r, p.tile_m)) != cudaSuccess) return e;
+      if ((e = make_map(&a.q, t, MX, q, kSplitN)) != cudaSuccess) return e;
+    }
+    if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
+    a.epi = epi;
+    a.tiles_m = (r.rows + p.tile_m - 1) / p.tile_m;
+    a.tile_m = p.tile_m;
+    a.k_tiles = int(k_tiles);
+    a.k_tile = k_tile;
+    a.r_mn = r.mn;
+    a.q_mn = q.mn;
+    const int stage = kOperandQ + p.tile_m * kLine + (MX ? 1024 : 0);
+    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024) / stage);
+    a.idesc = MX ? mma_desc_mx8(kSplitN, p.tile_m) : mma_desc_f16(t == DType::BF16, q.mn, r.mn, kSplitN, p.tile_m);
+    const int64_t grid = a.tiles_m * ((q.rows + kSplitN - 1) / kSplitN) * p.splits;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage,
+                       unsigned(p.splits), stream, a);
+  }
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t product(DType t, bool mx8, const Operand& r, const Operand& q, const Epilogue& epi, int sm_count,
+                    cudaStream_t stream, int* launches) {
+  if (t == DType::F16)
+    return mx8 ? product<__half, true>(t, r, q, epi, sm_count, stream, launches)
+               : product<__half, false>(t, r, q, epi, sm_count, stream, launches);
+  return mx8 ? product<__nv_bfloat16, true>(t, r, q, epi, sm_count, stream, launches)
+             : product<__nv_bfloat16, false>(t, r, q, epi, sm_count, stream, launches);
+}
+
+// Whether rows of n elements of `es` bytes from p on can be read by TMA as they lie.
+bool in_place(const void* p, int64_t n, int es) { return n * es % 16 == 0 && on(p, 16); }
+int64_t pitched_bytes(int64_t rows, int64_t n, int es) { return round_up(rows * round_up(n, 16 / es) * es, 256); }
+
+template <typename E>
+cudaError_t pitch_rows(const void* x, void* y, int64_t rows, int64_t n, int64_t ld, int sm_count, cudaStream_t stream,
+                       int* launches) {
+  const int64_t work = (rows * ((ld + 255) / 256) + 7) / 8;
+  const cudaError_t e = launch(k_pitch<E>, dim3(unsigned(std::min<int64_t>(work, int64_t(sm_count) * 32))), dim3(256),
+                               0, stream, static_cast<const E*>(x), static_cast<E*>(y), rows, uint32_t(n), uint32_t(ld));
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+// An operand as it lies, or copied to `*ws` (which moves on) with rows on 16-byte boundaries.
+cudaError_t readable(Operand* o, int es, uint8_t** ws, int sm_count, cudaStream_t stream, int* launches) {
+  const int64_t n = o->mn ? o->rows : o->depth, rows = o->mn ? o->depth : o->rows;
+  o->ld = n;
+  if (n == 0 || rows == 0 || in_place(o->p, n, es)) return cudaSuccess;
+  o->ld = round_up(n, 16 / es);
+  void* y = *ws;
+  *ws += pitched_bytes(rows, n, es);
+  const cudaError_t e = es == 1 ? pitch_rows<uint8_t>(o->p, y, rows, n, o->ld, sm_count, stream, launches)
+                                : pitch_rows<uint16_t>(o->p, y, rows, n, o->ld, sm_count, stream, launches);
+  o->p = y;
+  return e;
+}
+
+// Row chunks of k_act_slope: blocks enough for the device, 32 rows at least.
+int64_t slope_chunks(int64_t M, int64_t N) {
+  const int64_t tiles = (N + 255) / 256;
+  return std::max<int64_t>(1, std::min({(8 * kPlanSms + tiles - 1) / tiles, (M + 31) / 32, int64_t(65535)}));
+}
+
+template <typename T>
+cudaError_t act_slope_rows(const MatmulGradArgs& a, T* dz, int64_t ld, float* partial, cudaStream_t stream,
+                           int* launches) {
+  const int zm = a.act == kActNone ? 0 : a.z_scales != nullptr ? 2 : 1;
+  const bool vec = a.N % 8 == 0 && on(a.dy, 16) && (zm != 1 || on(a.z, 16)) && (zm != 2 || on(a.z, 8));
+  const int64_t chunks = slope_chunks(a.M, a.N), per = (a.M + chunks - 1) / chunks, used = (a.M + per - 1) / per;
+  const int64_t width = dz != nullptr ? ld : a.N;
+  auto run = [&](auto kernel, int vw) {
+    return launch(kernel, dim3(unsigned((width + 32 * vw - 1) / (32 * vw)), unsigned(used)), dim3(kSlopeThreads), 0,
+                  stream, static_cast<const T*>(a.dy), a.z, a.z_scales, dz, a.M, a.N, width, per, a.act, a.alpha,
+                  partial);
+  };
+  cudaError_t e;
+  if (vec) e = zm == 0 ? run(k_act_slope<T, 8, 0>, 8) : zm == 1 ? run(k_act_slope<T, 8, 1>, 8) : run(k_act_slope<T, 8, 2>, 8);
+  else e = zm == 0 ? run(k_act_slope<T, 1, 0>, 1) : zm == 1 ? run(k_act_slope<T, 1, 1>, 1) : run(k_act_slope<T, 1, 2>, 1);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (partial == nullptr) return cudaSuccess;
+  e = launch(k_channel_sums<T>, dim3(unsigned(std::min<int64_t>((a.N + 31) / 32, 65535))), dim3(kSumsThreads), 0,
+             stream, static_cast<const float*>(partial), used, int64_t(1), a.N, 1, static_cast<T*>(a.dbias),
+             static_cast<T*>(nullptr));
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace
+
+size_t matmul_workspace_bytes(bool mx8, int64_t M, int64_t N, int64_t K, bool aligned) {
+  const int es = mx8 ? 1 : 2;
+  if (K == 0 || (aligned && K * es % 16 == 0)) return 0;
+  return size_t(pitched_bytes(M, K, es) + pitched_bytes(N, K, es));
+}
+
+cudaError_t launch_matmul(const MatmulArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  const int es = a.mx8 ? 1 : 2;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Operand r{a.a, a.a_scales, a.M, a.K, a.K, false}, q{a.w, a.w_scales, a.N, a.K, a.K, false};
+  cudaError_t e = readable(&r, es, &ws, sm_count, stream, launches);
+  if (e == cudaSuccess) e = readable(&q, es, &ws, sm_count, stream, launches);
+  if (e != cudaSuccess) return e;
+  Epilogue epi{a.bias, a.residual, a.y, a.z, a.z_scales, a.M, a.N, a.act, a.alpha, false, on(a.bias, 16)};
+  epi.vec = a.N % 8 == 0 && on(a.y, 16) && on(a.residual, 16) && on(a.z, 16);
+  return product(a.t, a.mx8, r, q, epi, sm_count, stream, launches);
+}
+
+size_t matmul_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, bool act, bool a_mx8, bool aligned) {
+  size_t b = size_t(round_up(slope_chunks(M, N) * N * 4, 256));
+  if (act || !aligned || N % 8 != 0) b += size_t(pitched_bytes(M, N, 2));
+  if (a_mx8 || !aligned || K % 8 != 0) b += size_t(pitched_bytes(M, K, 2));
+  if (!aligned || K % 8 != 0) b += size_t(pitched_bytes(N, K, 2));
+  return b;
+}
+
+cudaError_t launch_matmul_grad(const MatmulGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  cudaError_t e = cudaSuccess;
+  float* partial = nullptr;
+  if (a.dbias != nullptr && a.M > 0 && a.N > 0) {
+    partial = reinterpret_cast<float*>(ws);
+    ws += round_up(slope_chunks(a.M, a.N) * a.N * 4, 256);
+  }
+  // dz, as it lies or made
+  const void* dz = a.dy;
+  int64_t ld = a.N;
+  const bool make = a.M > 0 && a.N > 0 && (a.act != kActNone || !in_place(a.dy, a.N, 2));
+  if (make) {
+    ld = round_up(a.N, 8);
+    dz = ws;
+    ws += pitched_bytes(a.M, a.N, 2);
+  }
+  if (make || partial != nullptr) {
+    void* out = make ? const_cast<void*>(dz) : nullptr;
+    e = a.t == DType::F16 ? act_slope_rows(a, static_cast<__half*>(out), ld, partial, stream, launches)
+                          : act_slope_rows(a, static_cast<__nv_bfloat16*>(out), ld, partial, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
+  auto plain = [&](void* y, int64_t rows, int64_t cols) {
+    Epilogue epi{nullptr, nullptr, y, nullptr, nullptr, rows, cols, kActNone, 0.f, false, false};
+    epi.vec = cols % 8 == 0 && on(y, 16);
+    return epi;
+  };
+  if (a.da != nullptr && a.M > 0 && a.K > 0) {  // dA (M, K) = dz (M, N) W: W's rows are the depth
+    const Operand r{dz, nullptr, a.M, a.N, ld, false};
+    Operand q{a.w, nullptr, a.K, a.N, a.K, true};
+    if ((e = readable(&q, 2, &ws, sm_count, stream, launches)) != cudaSuccess) return e;
+    e = product(a.t, false, r, q, plain(a.da, a.M, a.K), sm_count, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dw != nullptr && a.N > 0 && a.K > 0) {  // dW (N, K) = dz^T A: both have the depth as rows
+    const Operand r{dz, nullptr, a.N, a.M, ld, true};
+    Operand q{a.a, nullptr, a.K, a.M, a.K, true};
+    if (a.a_scales != nullptr && a.M > 0) {
+      q.ld = round_up(a.K, 8);
+      q.p = ws;
+      e = launch_dequantize_pitched(a.t, static_cast<const uint8_t*>(a.a), a.a_scales, ws, a.M, a.K, q.ld, sm_count,
+                                    stream, launches);
+    } else {
+      e = readable(&q, 2, &ws, sm_count, stream, launches);
+    }
+    if (e != cudaSuccess) return e;
+    e = product(a.t, false, r, q, plain(a.dw, a.N, a.K), sm_count, stream, launches);
+  }
+  return e;
+}
+
+cudaError_t matmul_pipe_timeouts(unsigned int* count, bool clear) { return read_pipe_timeouts(count, clear); }
+
+}  // namespace ep
