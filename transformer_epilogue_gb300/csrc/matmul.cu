@@ -66,25 +66,74 @@ struct Epilogue {
 // A K tile of 128 has 4 scales a row.  The tensor core wants the scales of rows
 // l, l + 32, l + 64, l + 96 (4 bytes each) in lane l of tensor memory, so the
 // shared-memory block that is copied there has 16 bytes for each l: one lane
-// brings them together.  In global memory they are rows of `groups` bytes.
+// brings them together.  In global memory they are rows of `groups` bytes, of
+// which a lane takes 16 (4 K tiles) at a time, two such quads ahead of the one
+// in use: a quad's products take 0.8 us, a load that misses L2 as long.
 // ---------------------------------------------------------------------------
 
 struct ScaleRows {
   const uint8_t* p;
   int64_t rows, groups;
-  bool words;  // groups and p are multiples of 4
+  int unit;  // bytes that can be loaded together: p and groups are multiples of it (16, 4 or 1)
 };
 
-// 4 bytes from group g on of a row; 127 (the scale 1) outside, where the values are 0.
-__device__ __forceinline__ uint32_t scale_word(const ScaleRows& s, int64_t row, int64_t g) {
-  if (row >= s.rows || g >= s.groups) return 0x7F7F7F7Fu;
-  const uint8_t* p = s.p + row * s.groups + g;
-  if (s.words) return __ldg(reinterpret_cast<const uint32_t*>(p));
-  uint32_t w = 0;
+// The quads have a ring of their own in shared memory, with barriers of their own:
+// one proxy fence and one arrival for 4 K tiles (a fence for each K tile held the
+// products back to 0.46 us a tile, of 0.2).
+constexpr int kScaleQuads = 3;
+struct QuadRing : Ring {
+  uint32_t buf = 0;  // which of two sets of tensor-memory columns
+  __device__ __forceinline__ QuadRing() : Ring(kScaleQuads) {}
+};
+
+// 16 bytes from group g on of a row; 127 (the scale 1) outside, where the values are 0.
+__device__ __forceinline__ void scale_quad(const ScaleRows& s, int64_t row, int64_t g, uint32_t (&w)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (g + i < s.groups ? uint32_t(__ldg(p + i)) : 127u) << (8 * i);
-  return w;
+  for (int i = 0; i < 4; ++i) w[i] = 0x7F7F7F7Fu;
+  if (row >= s.rows || g >= s.groups) return;
+  const uint8_t* p = s.p + row * s.groups + g;
+  if (s.unit == 16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if (s.unit == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (g + 4 * i < s.groups) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (g + i < s.groups) w[i / 4] = (w[i / 4] & ~(255u << (8 * (i % 4)))) | uint32_t(__ldg(p + i)) << (8 * (i % 4));
+  }
 }
+
+// A lane's quads of N rows 32 apart: the one in use and the next two.
+template <int N>
+struct ScaleAhead {
+  uint32_t w[3][N][4];
+  __device__ __forceinline__ void fetch(int at, const ScaleRows& s, int64_t row, int64_t g) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) scale_quad(s, row + 32 * j, g, w[at][j]);
+  }
+  __device__ __forceinline__ void shift() {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[0][j][i] = w[1][j][i];
+        w[1][j][i] = w[2][j][i];
+      }
+  }
+  // K tile i of the quad in use, to the blocks of 512 bytes at `sf`.
+  __device__ __forceinline__ void store(int i, uint4* sf, int lane) const {
+#pragma unroll
+    for (int b = 0; b < (N + 3) / 4; ++b) {
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = 4 * b + j < N ? w[0][4 * b + j < N ? 4 * b + j : 0][i] : 0x7F7F7F7Fu;
+      sf[32 * b + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // large results: a pair of CTAs
@@ -105,7 +154,9 @@ template <bool MX> struct PairShape {
   static constexpr int kOperandN = kHalfN * kLine;
   static constexpr int kStageBytes = kOperandM + kOperandN;
   static constexpr int kScaleBytes = MX ? 512 + 1024 : 0;  // R's 128 rows, Q's 192 in two blocks
-  static constexpr int kStages = 5;
+  static constexpr int kScaleColumns = 12;                 // of tensor memory
+  static constexpr int kScaleSets = 8;                     // K tiles whose scales are there
+  static constexpr int kStages = MX ? 6 : 5;
   static constexpr int kChunk = MX ? 32 : 64;              // columns that a warp turns around at once
   static constexpr int kBarriers = 2 * kStages + 5;
   static constexpr int kSmem = 1024 + kStages * (kStageBytes + kScaleBytes) + kEpiWarps * (kStaging + 64 * 4) +
@@ -114,7 +165,7 @@ template <bool MX> struct PairShape {
 
 struct PairArgs {
   CUtensorMap r, q;
-  ScaleRows rs, qs;
+  CUtensorMap rs, qs;    // 8-bit: blocks of scales as k_arrange left them, by tile and K tile
   Epilogue epi;
   int64_t tiles_m, tiles_n;
   int k_tiles;
@@ -122,6 +173,43 @@ struct PairArgs {
   bool r_mn, q_mn;
   uint32_t idesc;
 };
+
+// Row-major scales to the blocks of 512 bytes that tensor memory takes, for the pair
+// kernel's loads: block (tile, K tile) of `blocks` x 128 rows each, tiles `rows`
+// rows apart.  A thread takes a quad of four rows.  (Warps of the pair kernel that did
+// this held its products back to 0.41 us a K tile, where 0.2 is their time.)
+struct ArrangeArgs {
+  ScaleRows s[2];
+  uint4* out[2];
+  int64_t tiles[2];
+  int rows[2], blocks[2];
+  int k_tiles;
+};
+__global__ void __launch_bounds__(256) k_arrange(const __grid_constant__ ArrangeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t quads = (a.k_tiles + 3) / 4, step = int64_t(gridDim.x) * 8;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int64_t work = a.tiles[o] * a.blocks[o] * quads;
+    for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < work; i += step) {
+      const int64_t q = i % quads, tb = i / quads, t = tb / a.blocks[o];
+      const int b = int(tb - t * a.blocks[o]);
+      uint32_t w[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int in = 128 * b + 32 * j + lane;  // behind the tile's rows: never read by a product
+        scale_quad(a.s[o], in < a.rows[o] ? t * a.rows[o] + in : a.s[o].rows, q * 16, w[j]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (4 * q + k < a.k_tiles)
+          a.out[o][((t * a.k_tiles + 4 * q + k) * a.blocks[o] + b) * 32 + lane] =
+              make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+    }
+  }
+}
 
 // A staging row of NC 16-byte words; words are exchanged within a row so that
 // neither one word of 32 rows nor NC words of 32 / NC rows meet in a bank.
@@ -275,10 +363,10 @@ __device__ __forceinline__ void tile_place(int64_t t, int64_t tiles_m, int64_t t
   *m = first + in - *n * high;
 }
 
-// Warps: 0 loads, 1 issues the products (of the pair's first CTA alone), 2 brings
-// the scales, 3 has the tensor memory, 4.. write.  Barriers of a stage: `full`
-// (the first CTA's: both CTAs' bytes, and their scales' warps), `empty` (each
-// CTA's: the products that read it are done); of an accumulator: `ready` (each
+// Warps: 0 loads, 1 issues the products (of the pair's first CTA alone), 3 has the
+// tensor memory, 4.. write.  Barriers of a stage: `full`
+// (the first CTA's: both CTAs' bytes), `empty` (each CTA's: the products that read
+// it are done); of an accumulator: `ready` (each
 // CTA's), `taken` (the first CTA's: all epilogue warps of both).  A wait that
 // runs out ends its role; the others run out in turn, copies in flight are waited
 // for, and the CTAs leave together.
@@ -298,11 +386,11 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
   uint64_t* drained = taken + 2;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full + s, MX ? 3 : 1);
+      mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -325,23 +413,25 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
 
   const int64_t tiles = a.tiles_m * a.tiles_n, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   if (warp == 0) {
-    if (lane == 0) {
-      Ring ring(S::kStages);
-      int issued = 0;
-      bool ok = true;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        int64_t tm, tn;
-        tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
-        const int m = int(tm * kTileM) + int(rank) * kHalfM, n = int(tn * S::kTileN) + int(rank) * S::kHalfN;
-        for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
-          if (issued >= S::kStages && !mbar_wait_cluster(empty + ring.st, ring.phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = cluster_addr(smem_addr(full + ring.st), 0);
-          const uint32_t dst = smem_addr(smem + ring.st * S::kStageBytes);
-          if (rank == 0) mbar_arrive_expect_tx(full + ring.st, 2 * S::kStageBytes);
-          const int kk = k * a.k_tile;
+    Ring ring(S::kStages);
+    int issued = 0;
+    bool ok = true;
+    for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      int64_t tm, tn;
+      tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+      const int m = int(tm * kTileM) + int(rank) * kHalfM, n = int(tn * S::kTileN) + int(rank) * S::kHalfN;
+      const int rs = int((tm * 2 + rank) * a.k_tiles), qs = int(tn * a.k_tiles);
+      for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
+        if (issued >= S::kStages && !warp_wait(empty + ring.st, ring.phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = cluster_addr(smem_addr(full + ring.st), 0);
+        const uint32_t dst = smem_addr(smem + ring.st * S::kStageBytes);
+        const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
+        const int kk = k * a.k_tile;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + ring.st, 2 * (S::kStageBytes + S::kScaleBytes));
           if (!MX && a.r_mn) {
             for (int c = 0; c < kHalfM / 64; ++c) tma_load<true>(dst + c * 8192, &a.r, bar, m + 64 * c, kk);
           } else {
@@ -353,91 +443,71 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
           } else {
             tma_load<true>(dst + kOperandM, &a.q, bar, kk, n);
           }
-          issued = min(issued + 1, S::kStages);
+          if constexpr (MX) {
+            tma_load<true>(sf, &a.rs, bar, 0, rs + k);
+            tma_load<true>(sf + 512, &a.qs, bar, 0, qs + k);
+          }
         }
+        __syncwarp();
+        issued = min(issued + 1, S::kStages);
       }
-      // the last loads (of both CTAs) have landed before anyone leaves
-      if (rank == 0)
-        for (int i = 0; i < issued; ++i) {
-          ring.st = ring.st == 0 ? S::kStages - 1 : ring.st - 1;
-          if (ring.st == S::kStages - 1) ring.phase ^= 1;
-          if (!mbar_wait_cluster(full + ring.st, ring.phase)) break;
-        }
     }
+    // the last loads (of both CTAs) have landed before anyone leaves
+    if (rank == 0)
+      for (int i = 0; i < issued; ++i) {
+        ring.st = ring.st == 0 ? S::kStages - 1 : ring.st - 1;
+        if (ring.st == S::kStages - 1) ring.phase ^= 1;
+        if (!warp_wait(full + ring.st, ring.phase)) break;
+      }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       Ring ring(S::kStages);
+      uint32_t set = 0;
       bool ok = true;
       int64_t i = 0;
       const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
       for (int64_t t = pair; t < tiles && ok; t += pairs, ++i) {
         const int acc = int(i & 1);
-        if (i >= 2 && !mbar_wait_cluster(taken + acc, uint32_t((i >> 1) - 1) & 1)) break;
+        if (i >= 2 && !warp_wait(taken + acc, uint32_t((i >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
         tmem_fence_after();
         const uint32_t d = tmem + acc * S::kTileN;
         for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
-          if (!mbar_wait_cluster(full + ring.st, ring.phase)) {
+          if (!warp_wait(full + ring.st, ring.phase)) {
             ok = false;
             break;
           }
           tmem_fence_after();
           const uint32_t at = smem_addr(smem + ring.st * S::kStageBytes);
           uint64_t rd = operand_desc(at, a.r_mn), qd = operand_desc(at + kOperandM, a.q_mn);
-          if constexpr (MX) {
-            const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
-            const uint32_t sfr = tmem + 2 * S::kTileN, sfq = sfr + 4;
-            copy_scales<true>(sfr, scales_desc(sf));
-            copy_scales<true>(sfq, scales_desc(sf + 512));
-            copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
+          if (elect_one()) {
+            if constexpr (MX) {
+              // in turn to the columns of kScaleSets sets, so that the copies need not wait for products in flight
+              const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
+              const uint32_t sfr = tmem + 2 * S::kTileN + set * S::kScaleColumns, sfq = sfr + 4;
+              copy_scales<true>(sfr, scales_desc(sf));
+              copy_scales<true>(sfq, scales_desc(sf + 512));
+              copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
 #pragma unroll
-            for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
-              mma_mx8<true>(d, rd, qd, a.idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
-          } else {
+              for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
+                mma_mx8<true>(d, rd, qd, a.idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<true>(d, rd, qd, a.idesc, (k | j) != 0);
+              for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<true>(d, rd, qd, a.idesc, (k | j) != 0);
+            }
+            mma_commit<true>(empty + ring.st);
+            if (k + 1 == a.k_tiles) mma_commit<true>(ready + acc);
           }
-          mma_commit<true>(empty + ring.st);
+          __syncwarp();
+          set = (set + 1) % S::kScaleSets;
         }
-        if (ok) mma_commit<true>(ready + acc);
       }
       if (!ok) {  // products in flight end before the tensor memory is given back
-        mma_commit<true>(drained);
-        mbar_wait_cluster(drained, 0);
-      }
-    }
-  } else if (warp == 2) {
-    if constexpr (MX) {
-      Ring ring(S::kStages);
-      int64_t i = 0;
-      bool ok = true;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        int64_t tm, tn;
-        tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
-        const int64_t m = tm * kTileM + rank * kHalfM + lane, n = tn * S::kTileN + lane;
-        uint32_t w[10], next[10];
-        auto fetch = [&](int k, uint32_t (&v)[10]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = scale_word(a.rs, m + 32 * j, int64_t(k) * 4);
-#pragma unroll
-          for (int j = 0; j < 6; ++j) v[4 + j] = scale_word(a.qs, n + 32 * j, int64_t(k) * 4);
-        };
-        fetch(0, next);
-        for (int k = 0; k < a.k_tiles && ok; ++k, ++i, ring.next()) {
-#pragma unroll
-          for (int j = 0; j < 10; ++j) w[j] = next[j];
-          if (k + 1 < a.k_tiles) fetch(k + 1, next);
-          if (i >= S::kStages && !mbar_wait_cluster(empty + ring.st, ring.phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint4* sf = reinterpret_cast<uint4*>(scales + ring.st * S::kScaleBytes);
-          sf[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-          sf[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
-          sf[64 + lane] = make_uint4(w[8], w[9], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(full + ring.st), 0));
-        }
+        if (elect_one()) mma_commit<true>(drained);
+        __syncwarp();
+        warp_wait(drained, 0);
       }
     }
   } else if (warp >= 4) {
@@ -446,7 +516,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
     int64_t i = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int acc = int(i & 1);
-      if (!mbar_wait_cluster(ready + acc, uint32_t(i >> 1) & 1)) break;
+      if (!mbar_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
       tmem_fence_after();
       int64_t tm, tn;
       tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
@@ -476,6 +546,7 @@ constexpr int kOperandQ = kSplitN * kLine;
 constexpr int kSplitMostRows = 128;
 constexpr int kSplitBudget = 110 * 1024;      // two CTAs an SM
 constexpr int kSplitMostStages = 6;
+constexpr int kSplitQuadBytes = 4 * 1024;     // scales of 4 K tiles: Q's 128 rows and R's, 512 bytes each
 
 struct SplitArgs {
   CUtensorMap r, q;
@@ -562,32 +633,39 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&z)[8], int64_
   }
 }
 
-// Warps: 0 loads, 1 issues the products, 2 brings the scales, 3 has the tensor
-// memory; then all of them write.
+// Warps: 0 loads, 1 issues the products, 2 and 3 bring the scales (3 has the tensor
+// memory too); then all of them write.
 template <typename T, bool MX>
 __global__ void __launch_bounds__(kSplitThreads)
 k_mm_split(const __grid_constant__ SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kSplitMostStages], empty[kSplitMostStages], done;
+  __shared__ uint64_t full[kSplitMostStages], empty[kSplitMostStages], sfull[kScaleQuads], sempty[kScaleQuads], done;
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
   const int stage_bytes = kOperandQ + a.tile_m * kLine;
-  uint8_t* scales = smem + a.stages * stage_bytes;  // 1024 bytes a stage
+  uint8_t* scales = smem + a.stages * stage_bytes;  // kScaleQuads x kSplitQuadBytes
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   uint32_t splits;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
   const uint32_t rank = cluster_rank();
   const int64_t tile = blockIdx.x / splits;
   const int64_t m0 = tile % a.tiles_m * a.tile_m, n0 = tile / a.tiles_m * kSplitN;
-  const int k0 = int(int64_t(a.k_tiles) * rank / splits), k1 = int(int64_t(a.k_tiles) * (rank + 1) / splits);
+  // K tiles of this CTA: whole quads of them, as the scales come
+  const int unit = MX ? 4 : 1, units = (a.k_tiles + unit - 1) / unit;
+  const int k0 = int(int64_t(units) * rank / splits) * unit,
+            k1 = min(int(int64_t(units) * (rank + 1) / splits) * unit, a.k_tiles);
   const uint32_t columns = MX ? 256 : a.tile_m < 32 ? 32 : a.tile_m;
   if (threadIdx.x == 0) {
     failed = 0;
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full + s, MX ? 2 : 1);
+      mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < kScaleQuads; ++i) {
+      mbar_init(sfull + i, 2);
+      mbar_init(sempty + i, 1);
     }
     mbar_init(&done, 1);
     mbar_init_fence();
@@ -605,81 +683,98 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     Ring ring(a.stages);
     int issued = 0;
+    const int m = int(m0), n = int(n0);
     for (int k = k0; k < k1; ++k, ring.next()) {
-      if (issued >= a.stages && !mbar_wait(empty + ring.st, ring.phase ^ 1)) break;
+      if (issued >= a.stages && !warp_wait(empty + ring.st, ring.phase ^ 1)) break;
       const uint32_t bar = smem_addr(full + ring.st), dst = smem_addr(smem + ring.st * stage_bytes);
-      mbar_arrive_expect_tx(full + ring.st, stage_bytes);
-      const int kk = k * a.k_tile, m = int(m0), n = int(n0);
-      if (!MX && a.q_mn) {
-        for (int c = 0; c < kSplitN / 64; ++c) tma_load<false>(dst + c * 8192, &a.q, bar, n + 64 * c, kk);
-      } else {
-        tma_load<false>(dst, &a.q, bar, kk, n);
+      const int kk = k * a.k_tile;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full + ring.st, stage_bytes);
+        if (!MX && a.q_mn) {
+          for (int c = 0; c < kSplitN / 64; ++c) tma_load<false>(dst + c * 8192, &a.q, bar, n + 64 * c, kk);
+        } else {
+          tma_load<false>(dst, &a.q, bar, kk, n);
+        }
+        if (!MX && a.r_mn) {
+          for (int c = 0; c < a.tile_m / 64; ++c) tma_load<false>(dst + kOperandQ + c * 8192, &a.r, bar, m + 64 * c, kk);
+        } else {
+          tma_load<false>(dst + kOperandQ, &a.r, bar, kk, m);
+        }
       }
-      if (!MX && a.r_mn) {
-        for (int c = 0; c < a.tile_m / 64; ++c) tma_load<false>(dst + kOperandQ + c * 8192, &a.r, bar, m + 64 * c, kk);
-      } else {
-        tma_load<false>(dst + kOperandQ, &a.r, bar, kk, m);
-      }
+      __syncwarp();
       issued = min(issued + 1, a.stages);
     }
     for (int i = 0; i < issued; ++i) {  // the last loads have landed before the stages serve for anything else
       ring.st = ring.st == 0 ? a.stages - 1 : ring.st - 1;
       if (ring.st == a.stages - 1) ring.phase ^= 1;
-      if (!mbar_wait(full + ring.st, ring.phase)) break;
+      if (!warp_wait(full + ring.st, ring.phase)) break;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     Ring ring(a.stages);
+    QuadRing quad;
     const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
     bool ok = true;
     for (int k = k0; k < k1; ++k, ring.next()) {
-      if (!mbar_wait(full + ring.st, ring.phase)) {
+      if ((MX && k % 4 == 0 && !warp_wait(sfull + quad.st, quad.phase)) || !warp_wait(full + ring.st, ring.phase)) {
         ok = false;
         break;
       }
       tmem_fence_after();
       const uint32_t at = smem_addr(smem + ring.st * stage_bytes);
       uint64_t qd = operand_desc(at, a.q_mn), rd = operand_desc(at + kOperandQ, a.r_mn);
-      if constexpr (MX) {
-        const uint32_t sf = smem_addr(scales + ring.st * 1024);
-        const uint32_t sfq = tmem + 128, sfr = tmem + 132;
-        copy_scales<false>(sfq, scales_desc(sf));
-        copy_scales<false>(sfr, scales_desc(sf + 512));
+      if (elect_one()) {
+        if constexpr (MX) {  // a quad's scales at once, 8 columns a K tile behind the 128 of the sums, two sets in turn
+          const uint32_t sft = tmem + kSplitMostRows + quad.buf * 32;
+          if (k % 4 == 0) {
+            for (int i = 0; i < 4 && k + i < k1; ++i) {
+              const uint32_t sf = smem_addr(scales + quad.st * kSplitQuadBytes + i * 1024);
+              copy_scales<false>(sft + i * 8, scales_desc(sf));
+              copy_scales<false>(sft + i * 8 + 4, scales_desc(sf + 512));
+            }
+            mma_commit<false>(sempty + quad.st);
+          }
+          const uint32_t sfq = sft + k % 4 * 8, sfr = sfq + 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
-          mma_mx8<false>(tmem, qd, rd, a.idesc | mma_scale_byte(j), sfq, sfr, k > k0 || j > 0);
-      } else {
+          for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
+            mma_mx8<false>(tmem, qd, rd, a.idesc | mma_scale_byte(j), sfq, sfr, k > k0 || j > 0);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<false>(tmem, qd, rd, a.idesc, k > k0 || j > 0);
+          for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<false>(tmem, qd, rd, a.idesc, k > k0 || j > 0);
+        }
+        mma_commit<false>(empty + ring.st);
       }
-      mma_commit<false>(empty + ring.st);
+      __syncwarp();
+      if (MX && k % 4 == 3) {
+        quad.next();
+        quad.buf ^= 1;
+      }
     }
-    mma_commit<false>(&done);
-    if (!mbar_wait(&done, 0) || !ok) failed = 1;
-  } else if (MX && warp == 2) {
-    Ring ring(a.stages);
-    uint32_t w[8], next[8];
-    auto fetch = [&](int k, uint32_t (&v)[8]) {
+    if (elect_one()) mma_commit<false>(&done);
+    __syncwarp();
+    ok = warp_wait(&done, 0) && ok;
+    if (!ok && lane == 0) failed = 1;
+  } else if (MX && (warp == 2 || warp == 3)) {  // Q's scales and R's
+    const ScaleRows& sr = warp == 2 ? a.qs : a.rs;
+    const int64_t row = (warp == 2 ? n0 : m0) + lane;
+    ScaleAhead<4> ahead;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = scale_word(a.qs, n0 + lane + 32 * j, int64_t(k) * 4);
+    for (int i = 0; i < 3; ++i)
+      if (k0 + 4 * i < k1) ahead.fetch(i, sr, row, int64_t(k0 / 4 + i) * 16);
+    Ring ring(kScaleQuads);
+    for (int k = k0; k < k1; k += 4, ring.next()) {
+      if (k - k0 >= 4 * kScaleQuads && !mbar_wait(sempty + ring.st, ring.phase ^ 1)) break;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[4 + j] = 32 * j + lane < a.tile_m ? scale_word(a.rs, m0 + lane + 32 * j, int64_t(k) * 4) : 0x7F7F7F7Fu;
-    };
-    if (k0 < k1) fetch(k0, next);
-    for (int k = k0; k < k1; ++k, ring.next()) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = next[j];
-      if (k + 1 < k1) fetch(k + 1, next);
-      if (k - k0 >= a.stages && !mbar_wait(empty + ring.st, ring.phase ^ 1)) break;
-      uint4* sf = reinterpret_cast<uint4*>(scales + ring.st * 1024);
-      sf[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-      sf[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int i = 0; i < 4; ++i)
+        ahead.store(i, reinterpret_cast<uint4*>(scales + ring.st * kSplitQuadBytes + 1024 * i + (warp == 2 ? 0 : 512)),
+                    lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + ring.st);
+      if (lane == 0) mbar_arrive(sfull + ring.st);
+      ahead.shift();
+      if (k + 12 < k1) ahead.fetch(2, sr, row, int64_t(k / 4 + 3) * 16);
     }
   }
   __syncwarp();
@@ -893,7 +988,21 @@ cudaError_t make_map(CUtensorMap* map, DType t, bool mx8, const Operand& o, int 
 
 ScaleRows scale_rows(const Operand& o) {
   const int64_t g = mx_groups(o.depth);
-  return ScaleRows{o.scales, o.rows, g, g % 4 == 0 && on(o.scales, 4)};
+  return ScaleRows{o.scales, o.rows, g,
+                   g % 16 == 0 && on(o.scales, 16) ? 16 : g % 4 == 0 && on(o.scales, 4) ? 4 : 1};
+}
+
+// Blocks of `words` 32-bit words of scales, one after the other.
+cudaError_t make_scale_map(CUtensorMap* map, const void* p, int64_t blocks, int words) {
+  EncodeFn encode = nullptr;
+  const cudaError_t e = encoder(&encode);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[2] = {cuuint64_t(words), cuuint64_t(blocks)}, pitch[1] = {cuuint64_t(words) * 4};
+  const cuuint32_t box[2] = {cuuint32_t(words), 1}, ones[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(p), dims, pitch, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <typename Args>
@@ -957,35 +1066,59 @@ struct SplitPlan {
 // Rows: the smallest tile that holds them, up to 128 (an MN-major operand comes
 // 64 rows at a time).  K is cut until the CTAs fill the device twice over, each
 // with two K tiles at least.
-SplitPlan plan_split(int64_t rows, int64_t cols, int64_t k_tiles, bool r_mn, int sm_count) {
+SplitPlan plan_split(int64_t rows, int64_t cols, int64_t k_tiles, bool mx, bool r_mn, int sm_count) {
   SplitPlan p{r_mn ? 64 : 16, 1};
   while (p.tile_m < rows && p.tile_m < kSplitMostRows) p.tile_m *= 2;
   const int64_t tiles = (rows + p.tile_m - 1) / p.tile_m * ((cols + kSplitN - 1) / kSplitN);
-  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sm_count && k_tiles >= 4 * p.splits) p.splits *= 2;
+  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sm_count && k_tiles >= (mx ? 8 : 4) * p.splits) p.splits *= 2;
   return p;
 }
 
+int64_t tiles_of(int64_t rows, int tile) { return (rows + tile - 1) / tile; }
+
 // The pair kernel where its tiles keep the SMs busy; the other where they would leave many idle.
-bool take_pair(int64_t rows, int64_t cols, int tile_n, int sm_count) {
-  const int64_t tiles = (rows + kTileM - 1) / kTileM * ((cols + tile_n - 1) / tile_n);
-  return rows > 128 && tiles * 2 >= sm_count / 2;
+template <bool MX>
+bool take_pair(int64_t rows, int64_t cols, int64_t depth) {
+  const int64_t tiles = tiles_of(rows, kTileM) * tiles_of(cols, PairShape<MX>::kTileN);
+  return depth > 0 && rows > 128 && tiles * 2 >= kPlanSms / 2;
+}
+
+// Bytes of the arranged scales of a product that takes the pair kernel.
+int64_t arranged_bytes(int64_t rows, int64_t cols, int64_t k_tiles) {
+  return tiles_of(rows, kHalfM) * k_tiles * 512 + tiles_of(cols, PairShape<true>::kTileN) * k_tiles * 1024 +
+         k_tiles * 512;
 }
 
 template <typename T, bool MX>
-cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue& epi, int sm_count,
+cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue& epi, uint8_t* ws, int sm_count,
                     cudaStream_t stream, int* launches) {
   const int k_tile = MX ? 128 : 64;
   const int64_t k_tiles = (r.depth + k_tile - 1) / k_tile;
   cudaError_t e;
-  if (take_pair(r.rows, q.rows, PairShape<MX>::kTileN, sm_count) && k_tiles > 0) {
+  if (take_pair<MX>(r.rows, q.rows, r.depth)) {
     using S = PairShape<MX>;
     PairArgs a = {};
     if ((e = make_map(&a.r, t, MX, r, kHalfM)) != cudaSuccess) return e;
     if ((e = make_map(&a.q, t, MX, q, S::kHalfN)) != cudaSuccess) return e;
-    if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
+    a.tiles_m = tiles_of(r.rows, kTileM);
+    a.tiles_n = tiles_of(q.rows, S::kTileN);
+    if constexpr (MX) {
+      ArrangeArgs g = {};
+      g.s[0] = scale_rows(r), g.s[1] = scale_rows(q);
+      g.tiles[0] = 2 * a.tiles_m, g.tiles[1] = a.tiles_n;
+      g.rows[0] = kHalfM, g.rows[1] = S::kTileN;
+      g.blocks[0] = 1, g.blocks[1] = 2;
+      g.k_tiles = int(k_tiles);
+      g.out[0] = reinterpret_cast<uint4*>(ws);
+      g.out[1] = g.out[0] + g.tiles[0] * k_tiles * 32;
+      const int64_t warps = (g.tiles[0] + 2 * g.tiles[1]) * ((k_tiles + 3) / 4);
+      e = launch(k_arrange, dim3(unsigned(std::min<int64_t>((warps + 7) / 8, 8 * sm_count))), dim3(256), 0, stream, g);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+      if ((e = make_scale_map(&a.rs, g.out[0], g.tiles[0] * k_tiles, 128)) != cudaSuccess) return e;
+      if ((e = make_scale_map(&a.qs, g.out[1], g.tiles[1] * k_tiles, 256)) != cudaSuccess) return e;
+    }
     a.epi = epi;
-    a.tiles_m = (r.rows + kTileM - 1) / kTileM;
-    a.tiles_n = (q.rows + S::kTileN - 1) / S::kTileN;
     a.k_tiles = int(k_tiles);
     a.k_tile = k_tile;
     a.r_mn = r.mn;
@@ -998,7 +1131,7 @@ cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue&
     e = launch_cluster(k_mm_pair<T, MX>, unsigned(2 * std::min<int64_t>(tiles, pairs)), kPairThreads, S::kSmem, 2,
                        stream, a);
   } else {
-    const SplitPlan p = plan_split(r.rows, q.rows, k_tiles, r.mn, sm_count);
+    const SplitPlan p = plan_split(r.rows, q.rows, k_tiles, MX, r.mn, kPlanSms);
     SplitArgs a = {};
     if (k_tiles > 0) {
       if ((e = make_map(&a.r, t, MX, r, p.tile_m)) != cudaSuccess) return e;
@@ -1012,25 +1145,25 @@ cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue&
     a.k_tile = k_tile;
     a.r_mn = r.mn;
     a.q_mn = q.mn;
-    const int stage = kOperandQ + p.tile_m * kLine + (MX ? 1024 : 0);
-    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024) / stage);
+    const int stage = kOperandQ + p.tile_m * kLine, quads = MX ? kScaleQuads * kSplitQuadBytes : 0;
+    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024 - quads) / stage);
     a.idesc = MX ? mma_desc_mx8(kSplitN, p.tile_m) : mma_desc_f16(t == DType::BF16, q.mn, r.mn, kSplitN, p.tile_m);
     const int64_t grid = a.tiles_m * ((q.rows + kSplitN - 1) / kSplitN) * p.splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage,
+    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage + quads,
                        unsigned(p.splits), stream, a);
   }
   if (e == cudaSuccess) ++*launches;
   return e;
 }
 
-cudaError_t product(DType t, bool mx8, const Operand& r, const Operand& q, const Epilogue& epi, int sm_count,
+cudaError_t product(DType t, bool mx8, const Operand& r, const Operand& q, const Epilogue& epi, uint8_t* ws, int sm_count,
                     cudaStream_t stream, int* launches) {
   if (t == DType::F16)
-    return mx8 ? product<__half, true>(t, r, q, epi, sm_count, stream, launches)
-               : product<__half, false>(t, r, q, epi, sm_count, stream, launches);
-  return mx8 ? product<__nv_bfloat16, true>(t, r, q, epi, sm_count, stream, launches)
-             : product<__nv_bfloat16, false>(t, r, q, epi, sm_count, stream, launches);
+    return mx8 ? product<__half, true>(t, r, q, epi, ws, sm_count, stream, launches)
+               : product<__half, false>(t, r, q, epi, ws, sm_count, stream, launches);
+  return mx8 ? product<__nv_bfloat16, true>(t, r, q, epi, ws, sm_count, stream, launches)
+             : product<__nv_bfloat16, false>(t, r, q, epi, ws, sm_count, stream, launches);
 }
 
 // Whether rows of n elements of `es` bytes from p on can be read by TMA as they lie.
@@ -1096,8 +1229,10 @@ cudaError_t act_slope_rows(const MatmulGradArgs& a, T* dz, int64_t ld, float* pa
 
 size_t matmul_workspace_bytes(bool mx8, int64_t M, int64_t N, int64_t K, bool aligned) {
   const int es = mx8 ? 1 : 2;
-  if (K == 0 || (aligned && K * es % 16 == 0)) return 0;
-  return size_t(pitched_bytes(M, K, es) + pitched_bytes(N, K, es));
+  size_t b = 0;
+  if (K > 0 && !(aligned && K * es % 16 == 0)) b += size_t(pitched_bytes(M, K, es) + pitched_bytes(N, K, es));
+  if (mx8 && take_pair<true>(M, N, K)) b += size_t(arranged_bytes(M, N, tiles_of(K, 128)));
+  return b;
 }
 
 cudaError_t launch_matmul(const MatmulArgs& a, int sm_count, cudaStream_t stream, int* launches) {
@@ -1109,7 +1244,7 @@ cudaError_t launch_matmul(const MatmulArgs& a, int sm_count, cudaStream_t stream
   if (e != cudaSuccess) return e;
   Epilogue epi{a.bias, a.residual, a.y, a.z, a.z_scales, a.M, a.N, a.act, a.alpha, false, on(a.bias, 16)};
   epi.vec = a.N % 8 == 0 && on(a.y, 16) && on(a.residual, 16) && on(a.z, 16);
-  return product(a.t, a.mx8, r, q, epi, sm_count, stream, launches);
+  return product(a.t, a.mx8, r, q, epi, ws, sm_count, stream, launches);
 }
 
 size_t matmul_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, bool act, bool a_mx8, bool aligned) {
@@ -1152,7 +1287,7 @@ cudaError_t launch_matmul_grad(const MatmulGradArgs& a, int sm_count, cudaStream
     const Operand r{dz, nullptr, a.M, a.N, ld, false};
     Operand q{a.w, nullptr, a.K, a.N, a.K, true};
     if ((e = readable(&q, 2, &ws, sm_count, stream, launches)) != cudaSuccess) return e;
-    e = product(a.t, false, r, q, plain(a.da, a.M, a.K), sm_count, stream, launches);
+    e = product(a.t, false, r, q, plain(a.da, a.M, a.K), nullptr, sm_count, stream, launches);
     if (e != cudaSuccess) return e;
   }
   if (a.dw != nullptr && a.N > 0 && a.K > 0) {  // dW (N, K) = dz^T A: both have the depth as rows
@@ -1167,7 +1302,7 @@ cudaError_t launch_matmul_grad(const MatmulGradArgs& a, int sm_count, cudaStream
       e = readable(&q, 2, &ws, sm_count, stream, launches);
     }
     if (e != cudaSuccess) return e;
-    e = product(a.t, false, r, q, plain(a.dw, a.N, a.K), sm_count, stream, launches);
+    e = product(a.t, false, r, q, plain(a.dw, a.N, a.K), nullptr, sm_count, stream, launches);
   }
   return e;
 }

@@ -23,6 +23,32 @@ namespace ep {
 namespace dev {
 
 // ---------------------------------------------------------------------------
+// one thread of a warp
+//
+// Loads and products are issued by one elected lane inside control flow that the
+// whole warp follows: their operands can then live in uniform registers.  (Issued
+// under a comparison of the lane's number, each cost some 70 cycles.)
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The warp's number, known to be the same in all its lanes.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0); }
+
+// mbar_wait by a whole warp: all lanes have the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// ---------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------
 
@@ -58,35 +84,12 @@ __device__ __forceinline__ uint32_t ld_cluster_word(uint32_t addr) {
   return v;
 }
 
-// Arrives on a barrier anywhere in the cluster.
+// Arrives on a barrier anywhere in the cluster.  What it announces is read by the
+// asynchronous proxy (the tensor cores read shared memory that the arriving thread
+// has fenced) or is tensor memory, so the default scope does: at cluster scope each
+// arrival waited for all of the thread's memory operations, 0.5 us.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// As mbar_wait, for barriers on which other CTAs of the cluster arrive.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-      atomicAdd(&g_pipe_timeouts, 1u);
-      return false;
-    }
-  }
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // ---------------------------------------------------------------------------
