@@ -14,8 +14,8 @@
 //
 // Two kernels:
 //   k_mm_pair   large results: pairs of CTAs on tiles of 256 x 256 (8-bit: 256 x 192,
-//     the scales need the tensor memory of the rest), one pair to two SMs, walking over
-//     the tiles.  A pair reads each operand byte once for two SMs, which halves what
+//     the scales need the tensor memory of the rest; 256 x 128 where those leave SMs
+//     idle), one pair to two SMs, walking over the tiles.  A pair reads each operand byte once for two SMs, which halves what
 //     shared memory and L2 deliver per product.  Two accumulators: a tile is written
 //     while the next is computed.
 //   k_mm_split  few rows, or few tiles: 128 columns of the result (the weights' rows,
@@ -57,6 +57,7 @@ struct Epilogue {
   int act;
   float alpha;
   bool vec;              // rows of y, z and residual start on 16-byte boundaries (E4M3: of cols % 16 == 0 too)
+  bool pairs;            // on 4-byte boundaries (E4M3: on 2-byte boundaries)
   bool vec_bias;
 };
 
@@ -148,16 +149,17 @@ constexpr int kPairThreads = (4 + kEpiWarps) * 32;
 constexpr int kStaging = 4096;             // bytes an epilogue warp has to turn rows around
 constexpr int kRaster = 8;                 // tiles of rows that are walked together
 
-template <bool MX> struct PairShape {
-  static constexpr int kTileN = MX ? 192 : 256;
+template <bool MX, int TN> struct PairShape {
+  static constexpr int kTileN = TN;
   static constexpr int kHalfN = kTileN / 2;
   static constexpr int kOperandN = kHalfN * kLine;
   static constexpr int kStageBytes = kOperandM + kOperandN;
-  static constexpr int kScaleBytes = MX ? 512 + 1024 : 0;  // R's 128 rows, Q's 192 in two blocks
-  static constexpr int kScaleColumns = 12;                 // of tensor memory
-  static constexpr int kScaleSets = 8;                     // K tiles whose scales are there
-  static constexpr int kStages = MX ? 6 : 5;
-  static constexpr int kChunk = MX ? 32 : 64;              // columns that a warp turns around at once
+  static constexpr int kQBlocks = (TN + 127) / 128;
+  static constexpr int kScaleBytes = MX ? 512 * (1 + kQBlocks) : 0;  // R's 128 rows and Q's
+  [[maybe_unused]] static constexpr int kScaleColumns = 12;                // of tensor memory
+  [[maybe_unused]] static constexpr int kScaleSets = 8;                    // K tiles whose scales are there
+  static constexpr int kStages = TN == 128 ? 7 : MX ? 6 : 5;
+  static constexpr int kChunk = TN == 192 ? 32 : 64;              // columns that a warp turns around at once
   static constexpr int kBarriers = 2 * kStages + 5;
   static constexpr int kSmem = 1024 + kStages * (kStageBytes + kScaleBytes) + kEpiWarps * (kStaging + 64 * 4) +
                                kBarriers * 8 + 16;
@@ -218,44 +220,61 @@ __device__ __forceinline__ uint8_t* staged(uint8_t* buf, int r, int c) {
   return buf + (r * NC + (c ^ ((r / (8 / NC)) & (NC - 1)))) * 16;
 }
 
-// A warp's 32 rows x NC words between shared and global memory, in whole words
-// along a row (`vec`) or element by element.
+// A warp's 32 rows x NC words between shared and global memory.
 template <int NC, typename E, bool LOAD>
-__device__ __forceinline__ void turn_rows(uint8_t* buf, E* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
-                                          bool vec, int lane) {
+__device__ __forceinline__ void turn_words(uint8_t* buf, E* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                           int lane) {
   constexpr int PER = 16 / sizeof(E);
-  if (vec) {
-    uint4 w[NC];
+  uint4 w[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int idx = i * 32 + lane, r = idx / NC, c = idx % NC;
+    const int64_t row = row0 + r, col = col0 + c * PER;
+    const bool in = row < rows && col < cols;
+    uint4* p = reinterpret_cast<uint4*>(g + row * cols + col);
+    if constexpr (LOAD) {
+      w[i] = in ? __ldcs(p) : make_uint4(0, 0, 0, 0);
+    } else if (in) {
+      __stcs(p, *reinterpret_cast<const uint4*>(staged<NC>(buf, r, c)));
+    }
+  }
+  if constexpr (LOAD) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int idx = i * 32 + lane, r = idx / NC, c = idx % NC;
-      const int64_t row = row0 + r, col = col0 + c * PER;
-      const bool in = row < rows && col < cols;
-      uint4* p = reinterpret_cast<uint4*>(g + row * cols + col);
-      if constexpr (LOAD) {
-        w[i] = in ? __ldcs(p) : make_uint4(0, 0, 0, 0);
-      } else if (in) {
-        __stcs(p, *reinterpret_cast<const uint4*>(staged<NC>(buf, r, c)));
-      }
+      const int idx = i * 32 + lane;
+      *reinterpret_cast<uint4*>(staged<NC>(buf, idx / NC, idx % NC)) = w[i];
     }
-    if constexpr (LOAD) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int idx = i * 32 + lane;
-        *reinterpret_cast<uint4*>(staged<NC>(buf, idx / NC, idx % NC)) = w[i];
-      }
-    }
-  } else {
-    for (int r = 0; r < 32 && row0 + r < rows; ++r)
-#pragma unroll
-      for (int l = lane; l < NC * PER; l += 32) {
-        if (col0 + l >= cols) continue;
-        E* p = g + (row0 + r) * cols + col0 + l;
-        E* s = reinterpret_cast<E*>(staged<NC>(buf, r, l / PER)) + l % PER;
-        if constexpr (LOAD) *s = *p;
-        else *p = *s;
-      }
   }
+}
+
+// The same by smaller units U (an element, or two neighbours), a row's units to
+// neighbouring lanes, for rows that start on no 16-byte boundary.
+template <int NC, typename U, bool LOAD>
+__device__ __forceinline__ void turn_units(uint8_t* buf, U* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                           int lane) {
+  constexpr int PER = 16 / sizeof(U), N = NC * PER;
+  const int high = int(min(rows - row0, int64_t(32)));
+#pragma unroll
+  for (int l0 = 0; l0 < N; l0 += 32) {
+    const int l = l0 + lane;
+    const bool in = l < N && col0 + l < cols;
+    U* p = g + row0 * cols + col0 + l;
+#pragma unroll 8
+    for (int r = 0; r < high; ++r) {
+      if (!in) continue;
+      U* s = reinterpret_cast<U*>(staged<NC>(buf, r, l / PER)) + l % PER;
+      if constexpr (LOAD) *s = p[r * cols];
+      else p[r * cols] = *s;
+    }
+  }
+}
+
+template <int NC, typename E, typename E2, bool LOAD>
+__device__ __forceinline__ void turn_rows(uint8_t* buf, void* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                          bool vec, bool pairs, int lane) {
+  if (vec) turn_words<NC, E, LOAD>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
+  else if (pairs) turn_units<NC, E2, LOAD>(buf, static_cast<E2*>(g), row0, col0 / 2, rows, cols / 2, lane);
+  else turn_units<NC, E, LOAD>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
 }
 
 // CW columns of a warp's 32 rows, from tensor memory to the outputs.
@@ -321,14 +340,15 @@ __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, floa
     }
     __syncwarp();
     if (e.z_scales == nullptr)
-      turn_rows<NC, T, false>(buf, static_cast<T*>(e.z), row0, col0, e.rows, e.cols, e.vec, lane);
+      turn_rows<NC, uint16_t, uint32_t, false>(buf, e.z, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
     else
-      turn_rows<NC8, uint8_t, false>(buf, static_cast<uint8_t*>(e.z), row0, col0, e.rows, e.cols,
-                                     e.vec && e.cols % 16 == 0, lane);
+      turn_rows<NC8, uint8_t, uint16_t, false>(buf, e.z, row0, col0, e.rows, e.cols, e.vec && e.cols % 16 == 0, e.pairs,
+                                               lane);
     __syncwarp();
   }
   if (e.residual != nullptr) {
-    turn_rows<NC, T, true>(buf, static_cast<T*>(const_cast<void*>(e.residual)), row0, col0, e.rows, e.cols, e.vec, lane);
+    turn_rows<NC, uint16_t, uint32_t, true>(buf, const_cast<void*>(e.residual), row0, col0, e.rows, e.cols, e.vec,
+                                            e.pairs, lane);
     __syncwarp();
   }
 #pragma unroll
@@ -351,7 +371,7 @@ __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, floa
     put(h, z);
   }
   __syncwarp();
-  turn_rows<NC, T, false>(buf, static_cast<T*>(e.y), row0, col0, e.rows, e.cols, e.vec, lane);
+  turn_rows<NC, uint16_t, uint32_t, false>(buf, e.y, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
   __syncwarp();
 }
 
@@ -370,10 +390,10 @@ __device__ __forceinline__ void tile_place(int64_t t, int64_t tiles_m, int64_t t
 // CTA's), `taken` (the first CTA's: all epilogue warps of both).  A wait that
 // runs out ends its role; the others run out in turn, copies in flight are waited
 // for, and the CTAs leave together.
-template <typename T, bool MX>
+template <typename T, bool MX, int TN>
 __global__ void __launch_bounds__(kPairThreads, 1)
 k_mm_pair(const __grid_constant__ PairArgs a) {
-  using S = PairShape<MX>;
+  using S = PairShape<MX, TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* scales = smem + S::kStages * S::kStageBytes;
@@ -412,6 +432,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
   pdl_trigger();
 
   const int64_t tiles = a.tiles_m * a.tiles_n, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const bool r_mn = !MX && a.r_mn, q_mn = !MX && a.q_mn;
   if (warp == 0) {
     Ring ring(S::kStages);
     int issued = 0;
@@ -432,14 +453,14 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
         const int kk = k * a.k_tile;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full + ring.st, 2 * (S::kStageBytes + S::kScaleBytes));
-          if (!MX && a.r_mn) {
-            for (int c = 0; c < kHalfM / 64; ++c) tma_load<true>(dst + c * 8192, &a.r, bar, m + 64 * c, kk);
-          } else {
-            tma_load<true>(dst, &a.r, bar, kk, m);
-          }
-          if (!MX && a.q_mn) {
+          // an MN-major operand comes 64 rows at a time, a K-major one in as many boxes of 64 rows
+#pragma unroll
+          for (int c = 0; c < kHalfM / 64; ++c)
+            tma_load<true>(dst + c * 8192, &a.r, bar, r_mn ? m + 64 * c : kk, r_mn ? kk : m + 64 * c);
+          if constexpr (S::kHalfN % 64 == 0) {
+#pragma unroll
             for (int c = 0; c < S::kHalfN / 64; ++c)
-              tma_load<true>(dst + kOperandM + c * 8192, &a.q, bar, n + 64 * c, kk);
+              tma_load<true>(dst + kOperandM + c * 8192, &a.q, bar, q_mn ? n + 64 * c : kk, q_mn ? kk : n + 64 * c);
           } else {
             tma_load<true>(dst + kOperandM, &a.q, bar, kk, n);
           }
@@ -465,7 +486,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
       uint32_t set = 0;
       bool ok = true;
       int64_t i = 0;
-      const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
+      const uint64_t rstep = operand_step(r_mn), qstep = operand_step(q_mn);
       for (int64_t t = pair; t < tiles && ok; t += pairs, ++i) {
         const int acc = int(i & 1);
         if (i >= 2 && !warp_wait(taken + acc, uint32_t((i >> 1) - 1) & 1)) {
@@ -481,7 +502,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
           }
           tmem_fence_after();
           const uint32_t at = smem_addr(smem + ring.st * S::kStageBytes);
-          uint64_t rd = operand_desc(at, a.r_mn), qd = operand_desc(at + kOperandM, a.q_mn);
+          uint64_t rd = operand_desc(at, r_mn), qd = operand_desc(at + kOperandM, q_mn);
           if (elect_one()) {
             if constexpr (MX) {
               // in turn to the columns of kScaleSets sets, so that the copies need not wait for products in flight
@@ -489,7 +510,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
               const uint32_t sfr = tmem + 2 * S::kTileN + set * S::kScaleColumns, sfq = sfr + 4;
               copy_scales<true>(sfr, scales_desc(sf));
               copy_scales<true>(sfq, scales_desc(sf + 512));
-              copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
+              if constexpr (S::kQBlocks == 2) copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
 #pragma unroll
               for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
                 mma_mx8<true>(d, rd, qd, a.idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
@@ -556,95 +577,137 @@ struct SplitArgs {
   int tile_m;            // rows: 16, 32, 64 or 128
   int k_tiles, k_tile;
   int stages;
+  bool sums_apart;
   bool r_mn, q_mn;
   uint32_t idesc;
 };
 
-// The outputs of 8 neighbouring columns of a row.  All lanes of a warp call it
-// (four of them have a group of 32 together); `in`: the row and the columns are there.
-template <typename T>
-__device__ __forceinline__ void finish8(const Epilogue& e, float (&z)[8], int64_t row, int64_t col, bool in) {
-  const T* bias = static_cast<const T*>(e.bias);
-  const int here = in ? int(min(int64_t(8), e.cols - col)) : 0;
-  const int64_t at = row * e.cols + col;
-  if (bias != nullptr) {
-    if (e.vec_bias && here == 8) {
-      float b[8];
-      Conv<T>::unpack(ld16_keep(bias + col), b);
+// VW neighbouring elements of T as float32: one 16-byte access, or one element.
+template <typename T, int VW>
+__device__ __forceinline__ void put_out(T* p, const float (&z)[VW]) {
+  if constexpr (VW == 8) st16_stream(p, Conv<T>::pack(z));
+  else st1_stream(p, z[0]);
+}
+
+// The sums of a CTA's share of the rows, over the cluster's ranks in their order, and
+// its outputs.  A thread has VW columns (8 where rows start on 16-byte boundaries,
+// else 1: then a warp writes 32 neighbours) of U rows at a time, whose loads are
+// issued together; the columns of a group of 32 belong to 32 / VW neighbouring lanes.
+template <typename T, int VW, int U>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const float* sums, int splits, int share, int64_t first,
+                                            int64_t n0, bool bad) {
+  constexpr int PER_ROW = kSplitN / VW, ROWS = kSplitThreads / PER_ROW;
+  const int c = int(threadIdx.x) % PER_ROW * VW;
+  const int64_t col = n0 + c, groups = (e.cols + kMxGroup - 1) / kMxGroup;
+  const bool col_in = col < e.cols && !bad;
+  const T* residual = static_cast<const T*>(e.residual);
+  float bias[VW] = {};
+  if (e.bias != nullptr && col_in) {
+    const T* b = static_cast<const T*>(e.bias) + col;
+    if (VW == 8 && e.vec_bias) {
+      Frag<T, VW> f;
+      f.load_keep(b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += b[i];
+      for (int i = 0; i < VW; ++i) bias[i] = f.v[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < here) z[i] += to_float(__ldg(bias + col + i));
+      for (int i = 0; i < VW; ++i) bias[i] = to_float(__ldg(b + i));
     }
   }
-  if (e.z != nullptr) {
-    if (e.z_scales == nullptr) {
-      T* p = static_cast<T*>(e.z) + at;
-      if (e.vec && here == 8) {
-        st16_stream(p, Conv<T>::pack(z));
-      } else {
+  // (all lanes of a warp go through the same number of turns: a shuffle takes them all)
+  for (int r0 = int(threadIdx.x) / 32 * 32 / PER_ROW; r0 < share; r0 += ROWS * U) {
+    const int rt = r0 + int(threadIdx.x) % 32 / PER_ROW;
+    bool in[U];
+    Frag<T, VW> res[U];
+    float z[U][VW];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < here) st1_stream(p + i, z[i]);
-      }
-    } else {
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < here) amax = fmaxf(amax, fabsf(z[i]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const uint32_t b = mx_scale(amax);
-      const float k = mx_factor(b);
-      const uint32_t lo = e4m3x4(z[0] * k, z[1] * k, z[2] * k, z[3] * k),
-                     hi = e4m3x4(z[4] * k, z[5] * k, z[6] * k, z[7] * k);
-      uint8_t* p = static_cast<uint8_t*>(e.z) + at;
-      if (e.vec && here == 8) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < here) p[i] = uint8_t((i < 4 ? lo : hi) >> (8 * (i & 3)));
-      }
-      if (here > 0 && col % kMxGroup == 0)
-        e.z_scales[row * ((e.cols + kMxGroup - 1) / kMxGroup) + col / kMxGroup] = uint8_t(b);
+    for (int u = 0; u < U; ++u) {
+      const int r = rt + u * ROWS;
+      const int64_t row = first + r;
+      in[u] = col_in && r < share && row < e.rows;
+      if (in[u] && residual != nullptr) res[u].load_stream(residual + row * e.cols + col);
     }
-  }
-  by_act(e.act, [&](auto tag) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_value<decltype(tag)::value>(z[i], e.alpha);
-  });
-  T* y = static_cast<T*>(e.y) + at;
-  const T* res = static_cast<const T*>(e.residual) + (e.residual != nullptr ? at : 0);
-  if (e.vec && here == 8) {
-    if (e.residual != nullptr) {
-      float f[8];
-      Conv<T>::unpack(ld16_stream(res), f);
+    for (int u = 0; u < U; ++u) {
+      const int r = rt + u * ROWS;
+      const float* at = sums + r * kSplitN + c;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += f[i];
+      for (int i = 0; i < VW; ++i) z[u][i] = 0.f;
+      if (r >= share) continue;
+      for (int s = 0; s < splits; ++s, at += share * kSplitN) {
+        if constexpr (VW == 8) {
+          const float4 lo = *reinterpret_cast<const float4*>(at), hi = *reinterpret_cast<const float4*>(at + 4);
+          const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[u][i] += f[i];
+        } else {
+          z[u][0] += *at;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) z[u][i] += bias[i];
     }
-    st16_stream(y, Conv<T>::pack(z));
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < here) st1_stream(y + i, e.residual != nullptr ? z[i] + ld1_stream(res + i) : z[i]);
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = first + rt + u * ROWS, at = row * e.cols + col;
+      if (e.z != nullptr) {
+        if (e.z_scales == nullptr) {
+          if (in[u]) put_out<T, VW>(static_cast<T*>(e.z) + at, z[u]);
+        } else {
+          float amax = 0.f;
+          if (in[u]) {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) amax = fmaxf(amax, fabsf(z[u][i]));
+          }
+#pragma unroll
+          for (int o = 16 / VW; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const uint32_t b = mx_scale(amax);
+          const float k = mx_factor(b);
+          if (in[u]) {
+            uint8_t* p = static_cast<uint8_t*>(e.z) + at;
+            if constexpr (VW == 8)
+              *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(z[u][0] * k, z[u][1] * k, z[u][2] * k, z[u][3] * k),
+                                                        e4m3x4(z[u][4] * k, z[u][5] * k, z[u][6] * k, z[u][7] * k));
+            else
+              *p = uint8_t(e4m3x2(z[u][0] * k, 0.f));
+            if (c % kMxGroup == 0) e.z_scales[row * groups + col / kMxGroup] = uint8_t(b);
+          }
+        }
+      }
+    }
+    by_act(e.act, [&](auto tag) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < VW; ++i) z[u][i] = act_value<decltype(tag)::value>(z[u][i], e.alpha);
+    });
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!in[u]) continue;
+      if (residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) z[u][i] += res[u].v[i];
+      }
+      put_out<T, VW>(static_cast<T*>(e.y) + (first + rt + u * ROWS) * e.cols + col, z[u]);
+    }
   }
 }
 
 // Warps: 0 loads, 1 issues the products, 2 and 3 bring the scales (3 has the tensor
 // memory too); then all of them write.
 template <typename T, bool MX>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitThreads, 2)
 k_mm_split(const __grid_constant__ SplitArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kSplitMostStages], empty[kSplitMostStages], sfull[kScaleQuads], sempty[kScaleQuads], done;
   __shared__ uint32_t tmem_at;
-  __shared__ int failed;
+  __shared__ uint32_t failed[8], failed_here;  // by rank; this CTA's
   const int stage_bytes = kOperandQ + a.tile_m * kLine;
   uint8_t* scales = smem + a.stages * stage_bytes;  // kScaleQuads x kSplitQuadBytes
+  // (rank, row, column) sums in float32, of the rows that this CTA finishes: in memory of their own, so that the
+  // others need not wait for this CTA's products before they send theirs; of 128 rows where the stages were
+  float* sums = reinterpret_cast<float*>(a.sums_apart ? scales + (MX ? kScaleQuads * kSplitQuadBytes : 0) : smem);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
   uint32_t splits;
@@ -657,8 +720,10 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   const int k0 = int(int64_t(units) * rank / splits) * unit,
             k1 = min(int(int64_t(units) * (rank + 1) / splits) * unit, a.k_tiles);
   const uint32_t columns = MX ? 256 : a.tile_m < 32 ? 32 : a.tile_m;
+  const bool r_mn = !MX && a.r_mn, q_mn = !MX && a.q_mn;
   if (threadIdx.x == 0) {
-    failed = 0;
+    for (int s = 0; s < 8; ++s) failed[s] = 0;
+    failed_here = 0;
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
@@ -678,6 +743,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  if (splits > 1) cluster_arrive();  // waited for in front of the first store to another CTA: it is there
   tmem_fence_after();
   const uint32_t tmem = tmem_at;
   pdl_wait();
@@ -693,16 +759,11 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
       const int kk = k * a.k_tile;
       if (elect_one()) {
         mbar_arrive_expect_tx(full + ring.st, stage_bytes);
-        if (!MX && a.q_mn) {
-          for (int c = 0; c < kSplitN / 64; ++c) tma_load<false>(dst + c * 8192, &a.q, bar, n + 64 * c, kk);
-        } else {
-          tma_load<false>(dst, &a.q, bar, kk, n);
-        }
-        if (!MX && a.r_mn) {
-          for (int c = 0; c < a.tile_m / 64; ++c) tma_load<false>(dst + kOperandQ + c * 8192, &a.r, bar, m + 64 * c, kk);
-        } else {
-          tma_load<false>(dst + kOperandQ, &a.r, bar, kk, m);
-        }
+#pragma unroll
+        for (int c = 0; c < kSplitN / 64; ++c)
+          tma_load<false>(dst + c * 8192, &a.q, bar, q_mn ? n + 64 * c : kk, q_mn ? kk : n + 64 * c);
+        tma_load<false>(dst + kOperandQ, &a.r, bar, r_mn ? m : kk, r_mn ? kk : m);
+        if (a.tile_m > 64) tma_load<false>(dst + kOperandQ + 8192, &a.r, bar, r_mn ? m + 64 : kk, r_mn ? kk : m + 64);
       }
       __syncwarp();
       issued = min(issued + 1, a.stages);
@@ -715,7 +776,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   } else if (warp == 1) {
     Ring ring(a.stages);
     QuadRing quad;
-    const uint64_t rstep = operand_step(a.r_mn), qstep = operand_step(a.q_mn);
+    const uint64_t rstep = operand_step(r_mn), qstep = operand_step(q_mn);
     bool ok = true;
     for (int k = k0; k < k1; ++k, ring.next()) {
       if ((MX && k % 4 == 0 && !warp_wait(sfull + quad.st, quad.phase)) || !warp_wait(full + ring.st, ring.phase)) {
@@ -724,7 +785,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
       }
       tmem_fence_after();
       const uint32_t at = smem_addr(smem + ring.st * stage_bytes);
-      uint64_t qd = operand_desc(at, a.q_mn), rd = operand_desc(at + kOperandQ, a.r_mn);
+      uint64_t qd = operand_desc(at, q_mn), rd = operand_desc(at + kOperandQ, r_mn);
       if (elect_one()) {
         if constexpr (MX) {  // a quad's scales at once, 8 columns a K tile behind the 128 of the sums, two sets in turn
           const uint32_t sft = tmem + kSplitMostRows + quad.buf * 32;
@@ -755,7 +816,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
     if (elect_one()) mma_commit<false>(&done);
     __syncwarp();
     ok = warp_wait(&done, 0) && ok;
-    if (!ok && lane == 0) failed = 1;
+    if (!ok && lane == 0) failed_here = 1;
   } else if (MX && (warp == 2 || warp == 3)) {  // Q's scales and R's
     const ScaleRows& sr = warp == 2 ? a.qs : a.rs;
     const int64_t row = (warp == 2 ? n0 : m0) + lane;
@@ -781,138 +842,174 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   __syncthreads();  // the products are done, the stages free
   tmem_fence_after();
 
-  // this CTA's sums, (row, column) in float32
-  float* sums = reinterpret_cast<float*>(smem);
-  const int half = a.tile_m / 2;
+  // each row's sums to the CTA that finishes it
+  const int half = a.tile_m / 2, share = a.tile_m / int(splits);
+  if (splits > 1) {
+    cluster_wait();
+    if (!a.sums_apart) cluster_sync();  // everyone's products are done
+    if (failed_here != 0 && threadIdx.x < splits) st_cluster(cluster_addr(smem_addr(&failed[rank]), threadIdx.x), 1u);
+  }
   for (int c = (warp >> 2) * half; c < ((warp >> 2) + 1) * half; c += 8) {
     uint32_t v[8];
     tmem_ld8(tmem + c + (uint32_t(32 * (warp & 3)) << 16), v);
     tmem_wait_ld(v);
+    const int col = 32 * (warp & 3) + lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      sums[(c + i) * kSplitN + 32 * (warp & 3) + lane] = k0 < k1 ? __uint_as_float(v[i]) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t f = k0 < k1 ? v[i] : 0u;
+      if (splits == 1) {
+        sums[(c + i) * kSplitN + col] = __uint_as_float(f);
+      } else {
+        const int to = (c + i) / share, r = (c + i) - to * share;
+        st_cluster(cluster_addr(smem_addr(sums + (int(rank) * share + r) * kSplitN + col), to), f);
+      }
+    }
   }
   tmem_fence_before();
   if (splits > 1) cluster_sync();
   else __syncthreads();
   tmem_fence_after();
   if (warp == 3) tmem_free<false>(tmem, columns);
-
-  // each CTA finishes its share of the rows
   bool bad = false;
-  for (uint32_t s = 0; s < splits; ++s) bad |= ld_cluster_word(cluster_addr(smem_addr(&failed), s)) != 0;
-  const int share = a.tile_m / int(splits);
-  const uint32_t base = smem_addr(sums);
-  for (int idx = threadIdx.x; idx < share * (kSplitN / 8); idx += kSplitThreads) {
-    const int r = int(rank) * share + idx / (kSplitN / 8), c = idx % (kSplitN / 8) * 8;
-    float z[8] = {};
-    const uint32_t at = base + (r * kSplitN + c) * 4;
-    for (uint32_t s = 0; s < splits; ++s) {
-      const uint32_t p = cluster_addr(at, s);
-      const float4 lo = ld_cluster(p), hi = ld_cluster(p + 16);
-      const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += f[i];
-    }
-    const int64_t row = m0 + r, col = n0 + c;
-    finish8<T>(a.epi, z, row, col, row < a.epi.rows && col < a.epi.cols && !bad);
-  }
-  if (splits > 1) {  // the others have read this CTA's sums
-    __syncwarp();
-    cluster_sync();
-  }
+  for (uint32_t s = 0; s < splits; ++s) bad |= (splits > 1 ? failed[s] : failed_here) != 0;
+  const int64_t first = m0 + int64_t(rank) * share;
+  if (a.epi.vec) finish_rows<T, 8, 2>(a.epi, sums, int(splits), share, first, n0, bad);
+  else finish_rows<T, 1, 8>(a.epi, sums, int(splits), share, first, n0, bad);
 }
 
 // ---------------------------------------------------------------------------
 // beside the products
 // ---------------------------------------------------------------------------
 
-// Rows of n elements to rows `ld` apart (the tail set to 0): operands whose rows do not start on 16-byte boundaries.
+// Rows of n elements to rows `ld` apart (the tail set to 0): operands whose rows do
+// not start on 16-byte boundaries, up to two in one launch.  A warp copies 256
+// elements of a row, neighbours to neighbouring lanes.
+struct PitchArgs {
+  const void* x[2];
+  void* y[2];
+  int64_t rows[2];
+  uint32_t n[2], ld[2];
+};
 template <typename E>
-__global__ void __launch_bounds__(256)
-k_pitch(const E* __restrict__ x, E* __restrict__ y, int64_t rows, uint32_t n, uint32_t ld) {
+__global__ void __launch_bounds__(256) k_pitch(const __grid_constant__ PitchArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t warps = int64_t(gridDim.x) * 8, segs = (ld + 255) / 256;
-  for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows * segs; i += warps) {
-    const int64_t r = i / segs;
-    const uint32_t c0 = uint32_t(i - r * segs) * 256 + lane;
-    E v[8];
+  const int64_t warps = int64_t(gridDim.x) * 8;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = c0 + 32 * u < n ? x[r * n + c0 + 32 * u] : E(0);
+  for (int o = 0; o < 2; ++o) {
+    const E* x = static_cast<const E*>(a.x[o]);
+    E* y = static_cast<E*>(a.y[o]);
+    const uint32_t n = a.n[o], ld = a.ld[o];
+    const int64_t segs = (ld + 255) / 256;
+    for (int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); i < a.rows[o] * segs; i += warps) {
+      const int64_t r = i / segs;
+      const uint32_t c0 = uint32_t(i - r * segs) * 256 + lane;
+      E v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (c0 + 32 * u < ld) y[r * ld + c0 + 32 * u] = v[u];
+      for (int u = 0; u < 8; ++u) v[u] = c0 + 32 * u < n ? __ldcs(x + r * n + c0 + 32 * u) : E(0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c0 + 32 * u < ld) y[r * ld + c0 + 32 * u] = v[u];
+    }
   }
 }
 
 // dz = dY act'(z) (rounded to T for the tensor cores, as dY itself was: a
 // relative 2^-9 of bf16 that averages out over the sums), rows `ld` apart, and
-// the column sums of dz before that rounding.  A lane has VW columns, the 8
-// warps share a chunk of rows; bound by memory.  ZM: z is absent, T, or MX8.
+// the column sums of dz before that rounding.  A lane has VW columns, the 8 warps
+// share a chunk of rows, U rows at a time with the next U rows' loads in flight;
+// bound by memory, and nearly by the slopes' 25 instructions an element.  ZM: z is
+// absent, T, or MX8.
 constexpr int kSlopeThreads = 256;
 template <typename T, int VW, int ZM>
-__global__ void __launch_bounds__(kSlopeThreads)
+__global__ void __launch_bounds__(kSlopeThreads, 3)
 k_act_slope(const T* __restrict__ dy, const void* __restrict__ zp, const uint8_t* __restrict__ z_scales,
             T* __restrict__ dz, int64_t rows, int64_t cols, int64_t ld, int64_t rows_per_chunk, int act, float alpha,
             float* __restrict__ partial) {
-  constexpr int U = 4;  // rows whose loads are in flight together
+  constexpr int U = 2;
   __shared__ float part[8][32][VW + 1];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t(blockIdx.x) * 32 + lane) * VW, groups = (cols + kMxGroup - 1) / kMxGroup;
   const int64_t r0 = int64_t(blockIdx.y) * rows_per_chunk, r1 = min(r0 + rows_per_chunk, rows);
+  struct Row {  // as loaded
+    uint4 d, z;
+    uint32_t scale;
+  };
+  Row next[U];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = r + 8 * u;
+      next[u].d = next[u].z = make_uint4(0, 0, 0, 0);
+      next[u].scale = 127;
+      if (row >= r1 || c >= cols) continue;
+      const int64_t at = row * cols + c;
+      if constexpr (VW == 8) {
+        next[u].d = ld16_stream(dy + at);
+        if constexpr (ZM == 1) next[u].z = ld16_stream(static_cast<const T*>(zp) + at);
+        if constexpr (ZM == 2) {
+          const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(zp) + at));
+          next[u].z.x = q.x;
+          next[u].z.y = q.y;
+        }
+      } else {
+        next[u].d.x = __ldcs(reinterpret_cast<const uint16_t*>(dy) + at);
+        if constexpr (ZM == 1) next[u].z.x = __ldcs(static_cast<const uint16_t*>(zp) + at);
+        if constexpr (ZM == 2) next[u].z.x = __ldcs(static_cast<const uint8_t*>(zp) + at);
+      }
+      if constexpr (ZM == 2) next[u].scale = __ldg(z_scales + row * groups + c / kMxGroup);
+    }
+  };
+  auto floats = [](uint4 v, float (&f)[VW]) {
+    if constexpr (VW == 8) {
+      Conv<T>::unpack(v, f);
+    } else {
+      const uint16_t h = uint16_t(v.x);
+      f[0] = to_float(*reinterpret_cast<const T*>(&h));
+    }
+  };
   float sum[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) sum[e] = 0.f;
   by_act(act, [&](auto tag) {
     if (c >= ld) return;
+    load(r0 + warp);
     for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
-      float d[U][VW], z[U][VW];
+      Row now[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t row = r + 8 * u;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) d[u][e] = z[u][e] = 0.f;
-        if (row >= r1 || c >= cols) continue;
-        const int64_t at = row * cols + c;
-        if constexpr (VW == 8) Conv<T>::unpack(ld16_stream(dy + at), d[u]);
-        else d[u][0] = ld1_stream(dy + at);
-        if constexpr (ZM == 1) {
-          const T* p = static_cast<const T*>(zp) + at;
-          if constexpr (VW == 8) Conv<T>::unpack(ld16_stream(p), z[u]);
-          else z[u][0] = ld1_stream(p);
-        } else if constexpr (ZM == 2) {
-          const uint8_t* p = static_cast<const uint8_t*>(zp) + at;
-          const float k = mx_value(z_scales[row * groups + c / kMxGroup]);
-          if constexpr (VW == 8) {
-            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
-            const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 t = e4m3_floats(w[e]);
-              z[u][2 * e] = t.x * k;
-              z[u][2 * e + 1] = t.y * k;
-            }
-          } else {
-            z[u][0] = e4m3_floats(*p).x * k;
-          }
-        }
-      }
+      for (int u = 0; u < U; ++u) now[u] = next[u];
+      if (r + 8 * U < r1) load(r + 8 * U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t row = r + 8 * u;
         if (row >= r1) continue;
+        float d[VW];
+        floats(now[u].d, d);
+        if constexpr (ZM != 0) {
+          float z[VW];
+          if constexpr (ZM == 1) {
+            floats(now[u].z, z);
+          } else {
+            const float k = mx_value(now[u].scale);
+            const uint32_t w[4] = {now[u].z.x, now[u].z.x >> 16, now[u].z.y, now[u].z.y >> 16};
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          if constexpr (ZM != 0) d[u][e] *= act_slope<decltype(tag)::value>(z[u][e], alpha);
-          sum[e] += d[u][e];
+            for (int e = 0; e < VW; e += 2) {
+              const float2 t = e4m3_floats(w[e / 2]);
+              z[e] = t.x * k;
+              if constexpr (VW == 8) z[e + 1] = t.y * k;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < VW; ++e) d[e] *= act_slope<decltype(tag)::value>(z[e], alpha);
         }
+#pragma unroll
+        for (int e = 0; e < VW; ++e) sum[e] += d[e];
         if (dz != nullptr) {
-          if constexpr (VW == 8) *reinterpret_cast<uint4*>(dz + row * ld + c) = Conv<T>::pack(d[u]);
-          else dz[row * ld + c] = from_float(d[u][0], T());
+          if constexpr (VW == 8) *reinterpret_cast<uint4*>(dz + row * ld + c) = Conv<T>::pack(d);
+          else dz[row * ld + c] = from_float(d[0], T());
         }
       }
     }
@@ -1059,98 +1156,131 @@ cudaError_t resident_pairs(void (*kernel)(Args), unsigned threads, size_t smem, 
   return cudaSuccess;
 }
 
-struct SplitPlan {
-  int tile_m, splits;
-};
-
-// Rows: the smallest tile that holds them, up to 128 (an MN-major operand comes
-// 64 rows at a time).  K is cut until the CTAs fill the device twice over, each
-// with two K tiles at least.
-SplitPlan plan_split(int64_t rows, int64_t cols, int64_t k_tiles, bool mx, bool r_mn, int sm_count) {
-  SplitPlan p{r_mn ? 64 : 16, 1};
-  while (p.tile_m < rows && p.tile_m < kSplitMostRows) p.tile_m *= 2;
-  const int64_t tiles = (rows + p.tile_m - 1) / p.tile_m * ((cols + kSplitN - 1) / kSplitN);
-  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * sm_count && k_tiles >= (mx ? 8 : 4) * p.splits) p.splits *= 2;
-  return p;
-}
-
 int64_t tiles_of(int64_t rows, int tile) { return (rows + tile - 1) / tile; }
 
-// The pair kernel where its tiles keep the SMs busy; the other where they would leave many idle.
-template <bool MX>
-bool take_pair(int64_t rows, int64_t cols, int64_t depth) {
-  const int64_t tiles = tiles_of(rows, kTileM) * tiles_of(cols, PairShape<MX>::kTileN);
-  return depth > 0 && rows > 128 && tiles * 2 >= kPlanSms / 2;
+// Which kernel, tile and cut of K: the least of these estimates, in cycles, which
+// follow from the shape alone (as workspace sizes do).  A K tile costs its
+// products, 2 cycles a column (of the pair kernel, whose tile is 256 rows on two
+// SMs) or a row (of the other, 128 columns on one), or its loads at 64 bytes a
+// cycle and SM, whichever is more; of a CTA by itself at least 570 cycles, the
+// time from one issue to the next.  Then there is what does not overlap: the
+// start, the first loads' latency, the epilogue.
+struct Plan {
+  int tile_n;   // of the pair kernel, else 0
+  int tile_m;   // of the other
+  int splits;
+};
+
+Plan plan_product(bool mx, int64_t rows, int64_t cols, int64_t k_tiles, bool r_mn) {
+  Plan best{0, 0, 1};
+  double least = 0;
+  // cycles of an epilogue for each row of a tile of 128 columns; rows that start on no 16-byte boundary are
+  // written element by element
+  const double row_cost = cols % 8 == 0 ? 60.0 : 120.0;
+  // the operands from memory, at 3.6 KB a cycle (6.8 TB/s)
+  const double memory = double(rows + cols) * double(k_tiles) * kLine / 3600.0;
+  auto offer = [&](double cost, const Plan& p) {
+    if (best.tile_m == 0 || cost < least) least = cost, best = p;
+  };
+  for (int tm = r_mn ? 64 : 16; tm <= kSplitMostRows; tm *= 2) {
+    const int64_t tiles = tiles_of(rows, tm) * tiles_of(cols, kSplitN);
+    const double k_cost = std::max(2.0 * tm, (kOperandQ + tm * kLine) / 64.0);
+    for (int s = 1; s <= 8 && (s == 1 || k_tiles >= (mx ? 4 : 2) * s); s *= 2) {
+      const double turns = double(tiles_of(tiles * s, kPlanSms)), k_each = double(tiles_of(k_tiles, s));
+      const double ends = 3000.0 + (s > 1 ? 2500.0 + (80.0 + row_cost) * tm : row_cost * tm);  // (stores to other CTAs: 4 bytes a cycle)
+      // two CTAs share an SM
+      const double alone = double(int64_t(turns + 1) / 2) * (ends + k_each * std::max(570.0, k_cost));
+      offer(2500.0 + std::max({alone, ends + turns * (k_each * k_cost + row_cost / 2 * tm / s), ends + memory}),
+            Plan{0, tm, s});
+    }
+    if (tm >= rows) break;
+  }
+  if (rows > 128 && k_tiles > 0)
+    for (const int tn : {mx ? 192 : 256, 128}) {
+      const int64_t turns = tiles_of(tiles_of(rows, kTileM) * tiles_of(cols, tn), kPlanSms / 2);
+      const double k_cost = std::max(2.0 * tn, (kOperandM + tn / 2 * kLine) / 64.0);
+      offer(std::max(double(turns) * std::max(double(k_tiles) * k_cost, row_cost / 2 * tn), memory) + 7000.0 + row_cost / 2 * tn + (mx ? 4000.0 : 0.0),
+            Plan{tn, 128, 1});
+    }
+  return best;
 }
 
-// Bytes of the arranged scales of a product that takes the pair kernel.
-int64_t arranged_bytes(int64_t rows, int64_t cols, int64_t k_tiles) {
-  return tiles_of(rows, kHalfM) * k_tiles * 512 + tiles_of(cols, PairShape<true>::kTileN) * k_tiles * 1024 +
-         k_tiles * 512;
+// Bytes of the arranged scales of a product on the pair kernel.
+int64_t arranged_bytes(int64_t rows, int64_t cols, int64_t k_tiles, int tile_n) {
+  return (2 * tiles_of(rows, kTileM) + tiles_of(cols, tile_n) * ((tile_n + 127) / 128)) * k_tiles * 512;
+}
+
+template <typename T, bool MX, int TN>
+cudaError_t product_pair(DType t, const Operand& r, const Operand& q, const Epilogue& epi, int64_t k_tiles, int k_tile,
+                         uint8_t* ws, int sm_count, cudaStream_t stream, int* launches) {
+  using S = PairShape<MX, TN>;
+  PairArgs a = {};
+  cudaError_t e;
+  if ((e = make_map(&a.r, t, MX, r, 64)) != cudaSuccess) return e;
+  if ((e = make_map(&a.q, t, MX, q, S::kHalfN % 64 == 0 ? 64 : S::kHalfN)) != cudaSuccess) return e;
+  a.tiles_m = tiles_of(r.rows, kTileM);
+  a.tiles_n = tiles_of(q.rows, TN);
+  if constexpr (MX) {
+    ArrangeArgs g = {};
+    g.s[0] = scale_rows(r), g.s[1] = scale_rows(q);
+    g.tiles[0] = 2 * a.tiles_m, g.tiles[1] = a.tiles_n;
+    g.rows[0] = kHalfM, g.rows[1] = TN;
+    g.blocks[0] = 1, g.blocks[1] = S::kQBlocks;
+    g.k_tiles = int(k_tiles);
+    g.out[0] = reinterpret_cast<uint4*>(ws);
+    g.out[1] = g.out[0] + g.tiles[0] * k_tiles * 32;
+    const int64_t warps = (g.tiles[0] + S::kQBlocks * g.tiles[1]) * ((k_tiles + 3) / 4);
+    e = launch(k_arrange, dim3(unsigned(std::min<int64_t>((warps + 7) / 8, 8 * sm_count))), dim3(256), 0, stream, g);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if ((e = make_scale_map(&a.rs, g.out[0], g.tiles[0] * k_tiles, 128)) != cudaSuccess) return e;
+    if ((e = make_scale_map(&a.qs, g.out[1], g.tiles[1] * k_tiles, 128 * S::kQBlocks)) != cudaSuccess) return e;
+  }
+  a.epi = epi;
+  a.k_tiles = int(k_tiles);
+  a.k_tile = k_tile;
+  a.r_mn = r.mn;
+  a.q_mn = q.mn;
+  a.idesc = MX ? mma_desc_mx8(kTileM, TN) : mma_desc_f16(t == DType::BF16, r.mn, q.mn, kTileM, TN);
+  int pairs = 1;
+  if ((e = resident_pairs(k_mm_pair<T, MX, TN>, kPairThreads, S::kSmem, sm_count, &pairs)) != cudaSuccess) return e;
+  return launch_cluster(k_mm_pair<T, MX, TN>, unsigned(2 * std::min<int64_t>(a.tiles_m * a.tiles_n, pairs)),
+                        kPairThreads, S::kSmem, 2, stream, a);
 }
 
 template <typename T, bool MX>
 cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue& epi, uint8_t* ws, int sm_count,
                     cudaStream_t stream, int* launches) {
+  constexpr int kWide = MX ? 192 : 256;
   const int k_tile = MX ? 128 : 64;
-  const int64_t k_tiles = (r.depth + k_tile - 1) / k_tile;
+  const int64_t k_tiles = tiles_of(r.depth, k_tile);
+  const Plan p = plan_product(MX, r.rows, q.rows, k_tiles, r.mn);
   cudaError_t e;
-  if (take_pair<MX>(r.rows, q.rows, r.depth)) {
-    using S = PairShape<MX>;
-    PairArgs a = {};
-    if ((e = make_map(&a.r, t, MX, r, kHalfM)) != cudaSuccess) return e;
-    if ((e = make_map(&a.q, t, MX, q, S::kHalfN)) != cudaSuccess) return e;
-    a.tiles_m = tiles_of(r.rows, kTileM);
-    a.tiles_n = tiles_of(q.rows, S::kTileN);
-    if constexpr (MX) {
-      ArrangeArgs g = {};
-      g.s[0] = scale_rows(r), g.s[1] = scale_rows(q);
-      g.tiles[0] = 2 * a.tiles_m, g.tiles[1] = a.tiles_n;
-      g.rows[0] = kHalfM, g.rows[1] = S::kTileN;
-      g.blocks[0] = 1, g.blocks[1] = 2;
-      g.k_tiles = int(k_tiles);
-      g.out[0] = reinterpret_cast<uint4*>(ws);
-      g.out[1] = g.out[0] + g.tiles[0] * k_tiles * 32;
-      const int64_t warps = (g.tiles[0] + 2 * g.tiles[1]) * ((k_tiles + 3) / 4);
-      e = launch(k_arrange, dim3(unsigned(std::min<int64_t>((warps + 7) / 8, 8 * sm_count))), dim3(256), 0, stream, g);
-      if (e != cudaSuccess) return e;
-      ++*launches;
-      if ((e = make_scale_map(&a.rs, g.out[0], g.tiles[0] * k_tiles, 128)) != cudaSuccess) return e;
-      if ((e = make_scale_map(&a.qs, g.out[1], g.tiles[1] * k_tiles, 256)) != cudaSuccess) return e;
-    }
-    a.epi = epi;
-    a.k_tiles = int(k_tiles);
-    a.k_tile = k_tile;
-    a.r_mn = r.mn;
-    a.q_mn = q.mn;
-    a.idesc = MX ? mma_desc_mx8(kTileM, S::kTileN)
-                 : mma_desc_f16(t == DType::BF16, r.mn, q.mn, kTileM, S::kTileN);
-    int pairs = 1;
-    if ((e = resident_pairs(k_mm_pair<T, MX>, kPairThreads, S::kSmem, sm_count, &pairs)) != cudaSuccess) return e;
-    const int64_t tiles = a.tiles_m * a.tiles_n;
-    e = launch_cluster(k_mm_pair<T, MX>, unsigned(2 * std::min<int64_t>(tiles, pairs)), kPairThreads, S::kSmem, 2,
-                       stream, a);
+  if (p.tile_n != 0) {
+    e = p.tile_n == kWide ? product_pair<T, MX, kWide>(t, r, q, epi, k_tiles, k_tile, ws, sm_count, stream, launches)
+                          : product_pair<T, MX, 128>(t, r, q, epi, k_tiles, k_tile, ws, sm_count, stream, launches);
   } else {
-    const SplitPlan p = plan_split(r.rows, q.rows, k_tiles, MX, r.mn, kPlanSms);
     SplitArgs a = {};
     if (k_tiles > 0) {
-      if ((e = make_map(&a.r, t, MX, r, p.tile_m)) != cudaSuccess) return e;
-      if ((e = make_map(&a.q, t, MX, q, kSplitN)) != cudaSuccess) return e;
+      if ((e = make_map(&a.r, t, MX, r, std::min(p.tile_m, 64))) != cudaSuccess) return e;
+      if ((e = make_map(&a.q, t, MX, q, 64)) != cudaSuccess) return e;
     }
     if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
     a.epi = epi;
-    a.tiles_m = (r.rows + p.tile_m - 1) / p.tile_m;
+    a.tiles_m = tiles_of(r.rows, p.tile_m);
     a.tile_m = p.tile_m;
     a.k_tiles = int(k_tiles);
     a.k_tile = k_tile;
     a.r_mn = r.mn;
     a.q_mn = q.mn;
     const int stage = kOperandQ + p.tile_m * kLine, quads = MX ? kScaleQuads * kSplitQuadBytes : 0;
-    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024 - quads) / stage);
+    const int sums = p.splits > 1 && p.tile_m <= 64 ? p.tile_m * kSplitN * 4 : 0;
+    a.sums_apart = sums > 0;
+    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024 - quads - sums) / stage);
     a.idesc = MX ? mma_desc_mx8(kSplitN, p.tile_m) : mma_desc_f16(t == DType::BF16, q.mn, r.mn, kSplitN, p.tile_m);
-    const int64_t grid = a.tiles_m * ((q.rows + kSplitN - 1) / kSplitN) * p.splits;
+    const int64_t grid = a.tiles_m * tiles_of(q.rows, kSplitN) * p.splits;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage + quads,
+    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage + quads + sums,
                        unsigned(p.splits), stream, a);
   }
   if (e == cudaSuccess) ++*launches;
@@ -1170,34 +1300,43 @@ cudaError_t product(DType t, bool mx8, const Operand& r, const Operand& q, const
 bool in_place(const void* p, int64_t n, int es) { return n * es % 16 == 0 && on(p, 16); }
 int64_t pitched_bytes(int64_t rows, int64_t n, int es) { return round_up(rows * round_up(n, 16 / es) * es, 256); }
 
-template <typename E>
-cudaError_t pitch_rows(const void* x, void* y, int64_t rows, int64_t n, int64_t ld, int sm_count, cudaStream_t stream,
-                       int* launches) {
-  const int64_t work = (rows * ((ld + 255) / 256) + 7) / 8;
-  const cudaError_t e = launch(k_pitch<E>, dim3(unsigned(std::min<int64_t>(work, int64_t(sm_count) * 32))), dim3(256),
-                               0, stream, static_cast<const E*>(x), static_cast<E*>(y), rows, uint32_t(n), uint32_t(ld));
-  if (e == cudaSuccess) ++*launches;
-  return e;
-}
+// Copies for operands that cannot be read as they lie, collected for one launch.
+struct Pitcher {
+  int es;
+  uint8_t* ws;
+  PitchArgs a = {};
+  int used = 0;
+  // o as it lies, or as its copy will.
+  void add(Operand* o) {
+    const int64_t n = o->mn ? o->rows : o->depth, rows = o->mn ? o->depth : o->rows;
+    o->ld = n;
+    if (n == 0 || rows == 0 || in_place(o->p, n, es)) return;
+    o->ld = round_up(n, 16 / es);
+    a.x[used] = o->p;
+    a.y[used] = ws;
+    a.rows[used] = rows;
+    a.n[used] = uint32_t(n);
+    a.ld[used++] = uint32_t(o->ld);
+    o->p = ws;
+    ws += pitched_bytes(rows, n, es);
+  }
+  cudaError_t run(int sm_count, cudaStream_t stream, int* launches) const {
+    if (used == 0) return cudaSuccess;
+    int64_t warps = 0;
+    for (int i = 0; i < used; ++i) warps += a.rows[i] * ((a.ld[i] + 255) / 256);
+    const dim3 grid(unsigned(std::min<int64_t>((warps + 7) / 8, int64_t(sm_count) * 16)));
+    const cudaError_t e = es == 1 ? launch(k_pitch<uint8_t>, grid, dim3(256), 0, stream, a)
+                                  : launch(k_pitch<uint16_t>, grid, dim3(256), 0, stream, a);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
+};
 
-// An operand as it lies, or copied to `*ws` (which moves on) with rows on 16-byte boundaries.
-cudaError_t readable(Operand* o, int es, uint8_t** ws, int sm_count, cudaStream_t stream, int* launches) {
-  const int64_t n = o->mn ? o->rows : o->depth, rows = o->mn ? o->depth : o->rows;
-  o->ld = n;
-  if (n == 0 || rows == 0 || in_place(o->p, n, es)) return cudaSuccess;
-  o->ld = round_up(n, 16 / es);
-  void* y = *ws;
-  *ws += pitched_bytes(rows, n, es);
-  const cudaError_t e = es == 1 ? pitch_rows<uint8_t>(o->p, y, rows, n, o->ld, sm_count, stream, launches)
-                                : pitch_rows<uint16_t>(o->p, y, rows, n, o->ld, sm_count, stream, launches);
-  o->p = y;
-  return e;
-}
-
-// Row chunks of k_act_slope: blocks enough for the device, 32 rows at least.
+// Row chunks of k_act_slope: as many blocks as the device holds (three an SM) at once,
+// 32 rows at least.
 int64_t slope_chunks(int64_t M, int64_t N) {
   const int64_t tiles = (N + 255) / 256;
-  return std::max<int64_t>(1, std::min({(8 * kPlanSms + tiles - 1) / tiles, (M + 31) / 32, int64_t(65535)}));
+  return std::max<int64_t>(1, std::min({3 * kPlanSms / tiles, (M + 31) / 32, int64_t(65535)}));
 }
 
 template <typename T>
@@ -1231,20 +1370,29 @@ size_t matmul_workspace_bytes(bool mx8, int64_t M, int64_t N, int64_t K, bool al
   const int es = mx8 ? 1 : 2;
   size_t b = 0;
   if (K > 0 && !(aligned && K * es % 16 == 0)) b += size_t(pitched_bytes(M, K, es) + pitched_bytes(N, K, es));
-  if (mx8 && take_pair<true>(M, N, K)) b += size_t(arranged_bytes(M, N, tiles_of(K, 128)));
+  if (mx8) {
+    const Plan p = plan_product(true, M, N, tiles_of(K, 128), false);
+    if (p.tile_n != 0) b += size_t(arranged_bytes(M, N, tiles_of(K, 128), p.tile_n));
+  }
   return b;
 }
 
+void set_access(Epilogue* e) {
+  e->vec = e->cols % 8 == 0 && on(e->y, 16) && on(e->residual, 16) && on(e->z, 16);
+  e->pairs = e->cols % 2 == 0 && on(e->y, 4) && on(e->residual, 4) && on(e->z, e->z_scales != nullptr ? 2 : 4);
+  e->vec_bias = on(e->bias, 16);
+}
+
 cudaError_t launch_matmul(const MatmulArgs& a, int sm_count, cudaStream_t stream, int* launches) {
-  const int es = a.mx8 ? 1 : 2;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Pitcher pitch{a.mx8 ? 1 : 2, static_cast<uint8_t*>(a.workspace)};
   Operand r{a.a, a.a_scales, a.M, a.K, a.K, false}, q{a.w, a.w_scales, a.N, a.K, a.K, false};
-  cudaError_t e = readable(&r, es, &ws, sm_count, stream, launches);
-  if (e == cudaSuccess) e = readable(&q, es, &ws, sm_count, stream, launches);
+  pitch.add(&r);
+  pitch.add(&q);
+  const cudaError_t e = pitch.run(sm_count, stream, launches);
   if (e != cudaSuccess) return e;
-  Epilogue epi{a.bias, a.residual, a.y, a.z, a.z_scales, a.M, a.N, a.act, a.alpha, false, on(a.bias, 16)};
-  epi.vec = a.N % 8 == 0 && on(a.y, 16) && on(a.residual, 16) && on(a.z, 16);
-  return product(a.t, a.mx8, r, q, epi, ws, sm_count, stream, launches);
+  Epilogue epi{a.bias, a.residual, a.y, a.z, a.z_scales, a.M, a.N, a.act, a.alpha, false, false, false};
+  set_access(&epi);
+  return product(a.t, a.mx8, r, q, epi, pitch.ws, sm_count, stream, launches);
 }
 
 size_t matmul_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, bool act, bool a_mx8, bool aligned) {
@@ -1278,32 +1426,32 @@ cudaError_t launch_matmul_grad(const MatmulGradArgs& a, int sm_count, cudaStream
                           : act_slope_rows(a, static_cast<__nv_bfloat16*>(out), ld, partial, stream, launches);
     if (e != cudaSuccess) return e;
   }
-  auto plain = [&](void* y, int64_t rows, int64_t cols) {
-    Epilogue epi{nullptr, nullptr, y, nullptr, nullptr, rows, cols, kActNone, 0.f, false, false};
-    epi.vec = cols % 8 == 0 && on(y, 16);
-    return epi;
-  };
-  if (a.da != nullptr && a.M > 0 && a.K > 0) {  // dA (M, K) = dz (M, N) W: W's rows are the depth
-    const Operand r{dz, nullptr, a.M, a.N, ld, false};
-    Operand q{a.w, nullptr, a.K, a.N, a.K, true};
-    if ((e = readable(&q, 2, &ws, sm_count, stream, launches)) != cudaSuccess) return e;
-    e = product(a.t, false, r, q, plain(a.da, a.M, a.K), nullptr, sm_count, stream, launches);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.dw != nullptr && a.N > 0 && a.K > 0) {  // dW (N, K) = dz^T A: both have the depth as rows
-    const Operand r{dz, nullptr, a.N, a.M, ld, true};
-    Operand q{a.a, nullptr, a.K, a.M, a.K, true};
+  // dA (M, K) = dz (M, N) W: W's rows are the depth.  dW (N, K) = dz^T A: both have the depth as rows.
+  Operand ra{dz, nullptr, a.M, a.N, ld, false}, qa{a.w, nullptr, a.K, a.N, a.K, true};
+  Operand rw{dz, nullptr, a.N, a.M, ld, true}, qw{a.a, nullptr, a.K, a.M, a.K, true};
+  const bool da = a.da != nullptr && a.M > 0 && a.K > 0, dw = a.dw != nullptr && a.N > 0 && a.K > 0;
+  Pitcher pitch{2, ws};
+  if (da) pitch.add(&qa);
+  if (dw) {
     if (a.a_scales != nullptr && a.M > 0) {
-      q.ld = round_up(a.K, 8);
-      q.p = ws;
-      e = launch_dequantize_pitched(a.t, static_cast<const uint8_t*>(a.a), a.a_scales, ws, a.M, a.K, q.ld, sm_count,
-                                    stream, launches);
+      qw.ld = round_up(a.K, 8);
+      qw.p = pitch.ws;
+      pitch.ws += pitched_bytes(a.M, a.K, 2);
+      e = launch_dequantize_pitched(a.t, static_cast<const uint8_t*>(a.a), a.a_scales, const_cast<void*>(qw.p), a.M, a.K,
+                                    qw.ld, sm_count, stream, launches);
+      if (e != cudaSuccess) return e;
     } else {
-      e = readable(&q, 2, &ws, sm_count, stream, launches);
+      pitch.add(&qw);
     }
-    if (e != cudaSuccess) return e;
-    e = product(a.t, false, r, q, plain(a.dw, a.N, a.K), nullptr, sm_count, stream, launches);
   }
+  if ((e = pitch.run(sm_count, stream, launches)) != cudaSuccess) return e;
+  auto plain = [&](const Operand& r, const Operand& q, void* y) {
+    Epilogue epi{nullptr, nullptr, y, nullptr, nullptr, r.rows, q.rows, kActNone, 0.f, false, false, false};
+    set_access(&epi);
+    return product(a.t, false, r, q, epi, nullptr, sm_count, stream, launches);
+  };
+  if (da) e = plain(ra, qa, a.da);
+  if (dw && e == cudaSuccess) e = plain(rw, qw, a.dw);
   return e;
 }
 

@@ -5,17 +5,20 @@
 //   u = dY gamma, x^ = s inv:  ds = inv (u - x^ mean(u x^)) + dsum,  dgamma = sum dY x^,  dbias = sum ds
 //
 // All of it is bound by memory: a row is read once, held in registers across its
-// reduction and written once.  A row belongs to TPR threads (whole warps), each
-// with NF fragments of VW consecutive elements, TPR fragments apart: 8 elements
-// where rows start on 16-byte boundaries, so that a group of 32 is four
-// neighbouring lanes and its maximum two shuffles; else one element, so that a
-// group is a warp.  Blocks keep gamma (and the bias, and the gradient's column
-// sums) in registers and walk over rows, with the next row's loads issued
-// before the present row's reduction: at 2 x 256 threads and 48 bytes each an SM
-// has the 45 KB in flight that the memory's latency takes.  Rows too long for
-// that are read twice by a block of 512 threads.
+// reduction and written once.  A row belongs to TPR threads, each with NF fragments of
+// VW consecutive elements, TPR fragments apart: 8 elements where rows start on 16-byte
+// boundaries, so that a group of 32 is four neighbouring lanes and its maximum two
+// shuffles; else one element, so that a group is a warp.  Blocks walk over rows, with
+// the next row's loads issued before the present row's reduction; what hides a row's
+// latency (loads, reduction, stores: some 3000 cycles) is also the other rows of the
+// SM's blocks.  Beside the memory it is the instructions that bind (38 an element at
+// first, 70 % of the issue slots: bf16 16384 x 4096 in 88 us): products and sums go two
+// to an instruction, indexes are 32-bit within a row (73 us, 94 % of the copy rate).
+// Rows that came through a ring of bulk copies took 104 us, blocks of one row each 91.
+// Rows too long for the registers are read twice by a block of 512 threads.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -41,6 +44,7 @@ template <typename T> struct Raw<T, 1> {
   __device__ __forceinline__ void stream(const T* p) { v = __ldcs(p); }
   __device__ __forceinline__ void keep(const T* p) { v = __ldg(p); }
   __device__ __forceinline__ void floats(float (&f)[1]) const { f[0] = to_float(v); }
+  __device__ __forceinline__ void add_to(float (&f)[1]) const { f[0] += to_float(v); }
 };
 template <typename T> struct Raw<T, 8> {
   static constexpr int W = sizeof(T) / 2;  // 16-byte words
@@ -56,6 +60,15 @@ template <typename T> struct Raw<T, 8> {
   __device__ __forceinline__ void keep(const T* p) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = ld16_keep(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void add_to(float (&f)[8]) const {
+    if constexpr (W == 1) {
+      add_raw<T, 8>(v[0], f);
+    } else {
+      float g[8];
+      floats(g);
+      add_pairs(f, g);
+    }
   }
   __device__ __forceinline__ void floats(float (&f)[8]) const {
     if constexpr (W == 1) {
@@ -87,39 +100,89 @@ __device__ __forceinline__ void store_row(T* p, const float (&f)[VW]) {
   }
 }
 
-// MX8 of a fragment whose group is held by 32 / VW neighbouring lanes (all of
-// them here; `in`: the fragment lies in the row).
+// f *= k, f *= g, two to an instruction where there are two.
 template <int VW>
-__device__ __forceinline__ void store_mx8(const float (&y)[VW], bool in, bool first, uint8_t* q, uint8_t* scale) {
-  float amax = 0.f;
-#pragma unroll
-  for (int e = 0; e < VW; ++e) amax = fmaxf(amax, fabsf(y[e]));
-#pragma unroll
-  for (int o = 16 / VW; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const uint32_t b = mx_scale(amax);
-  const float k = mx_factor(b);
-  if (!in) return;
-  if constexpr (VW == 8) {
-    const uint2 w = make_uint2(e4m3x4(y[0] * k, y[1] * k, y[2] * k, y[3] * k),
-                               e4m3x4(y[4] * k, y[5] * k, y[6] * k, y[7] * k));
-    __stcs(reinterpret_cast<uint2*>(q), w);
+__device__ __forceinline__ void scale_all(float (&f)[VW], float k) {
+  if constexpr (VW == 1) f[0] *= k;
+  else scale_pairs(f, k);
+}
+template <int VW>
+__device__ __forceinline__ void mul_all(float (&f)[VW], const float (&g)[VW]) {
+  if constexpr (VW == 1) {
+    f[0] *= g[0];
   } else {
-    *q = uint8_t(e4m3x2(y[0] * k, 0.f));
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 t = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(g[e], g[e + 1]));
+      f[e] = t.x;
+      f[e + 1] = t.y;
+    }
   }
+}
+// a + b c
+template <int VW>
+__device__ __forceinline__ void fma_all(float (&a)[VW], const float (&b)[VW], const float (&c)[VW]) {
+  if constexpr (VW == 1) {
+    a[0] = fmaf(b[0], c[0], a[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; e += 2) {
+      const float2 t =
+          __ffma2_rn(make_float2(b[e], b[e + 1]), make_float2(c[e], c[e + 1]), make_float2(a[e], a[e + 1]));
+      a[e] = t.x;
+      a[e + 1] = t.y;
+    }
+  }
+}
+template <int VW>
+__device__ __forceinline__ float sum_all(const float (&f)[VW]) {
+  float t = f[0];
+#pragma unroll
+  for (int e = 1; e < VW; ++e) t += f[e];
+  return t;
+}
+
+// MX8 of m * r for a fragment m whose group is held by 32 / VW neighbouring lanes (all
+// of them here; `in`: the fragment lies in the row).  r and the scale's power of two
+// make one factor: the power scales exactly, so (m r) 2^e and m (r 2^e) round alike.
+template <int VW>
+__device__ __forceinline__ void store_mx8(float (&m)[VW], float r, bool in, bool first, uint8_t* q, uint8_t* scale) {
+  float amax;
+  if constexpr (VW == 1) {  // magnitudes compare as their bits do; NaN is left out
+    const float f = fabsf(m[0]);
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, f == f ? __float_as_uint(f) : 0u));
+  } else {
+    amax = max3(fabsf(m[0]), fabsf(m[1]), fabsf(m[2]));
+    amax = max3(amax, fabsf(m[3]), fabsf(m[4]));
+    amax = max3(amax, fabsf(m[5]), fabsf(m[6]));
+    amax = fmaxf(amax, fabsf(m[7]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    amax = fmaxf(amax, 0.f);  // (eight NaN leave a NaN)
+  }
+  const uint32_t b = mx_scale(amax * r);
+  scale_all(m, r * mx_factor(b));
+  if (!in) return;
+  if constexpr (VW == 8)
+    __stcs(reinterpret_cast<uint2*>(q), make_uint2(e4m3x4(m[0], m[1], m[2], m[3]), e4m3x4(m[4], m[5], m[6], m[7])));
+  else
+    *q = uint8_t(e4m3x2(m[0], 0.f));
   if (first) *scale = uint8_t(b);
 }
 
-// Sum over the TPR threads of a row.  `red`: 2 x the row's warps, taken in turn
-// (`turn`), so that one barrier a row is enough.
-__device__ __forceinline__ float row_sum(float v, float* red, int turn, int tpr, int slot) {
-  v = warp_sum(v);
-  if (tpr == 32) return v;
+// Sum over the blockDim.x threads of a row (a power of two below 32, or whole warps);
+// the block's rows (blockDim.y) do it together.  `red`: 2 x the block's warps, taken
+// in turn (`turn`), so that one barrier is enough.
+__device__ __forceinline__ float row_sum(float v, float* red, int turn) {
+  const int tpr = int(blockDim.x);
+  for (int o = min(tpr, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tpr <= 32) return v;
   const int warps = tpr >> 5;
-  float* r = red + turn * warps;
+  float* r = red + (turn * int(blockDim.y) + int(threadIdx.y)) * warps;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-  float t = 0.f;
-  for (int i = 0; i < warps; ++i) t += r[i];
+  __syncthreads();
+  float t = r[0];
+  for (int i = 1; i < warps; ++i) t += r[i];
   return t;
 }
 
@@ -177,7 +240,7 @@ k_quantize(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict
   for (int u = 0; u < U; ++u) {
     float f[VW];
     raw[u].floats(f);
-    store_mx8<VW>(f, in[u], lane == 0, q + off[u], scales + i0 + u * (kRowThreads / L));
+    store_mx8<VW>(f, 1.0f, in[u], lane == 0, q + off[u], scales + i0 + u * (kRowThreads / L));
   }
 }
 
@@ -233,10 +296,15 @@ k_dequantize(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, 
 // RMS norm to MX8
 // ---------------------------------------------------------------------------
 
-// Block (TPR, R): R rows at a time, rows blockIdx.x * R + y, then gridDim.x * R further on.
-template <typename T, int VW, int NF>
-__global__ void __launch_bounds__(kLongThreads)
-k_norm(RmsNormArgs a) {
+// Blocks that an SM holds at once, by the registers of a thread's elements (the
+// present row's in float32, the next row's as loaded).
+constexpr int norm_blocks(int elements, bool wide) { return wide ? 1 : elements <= 16 ? 4 : elements <= 24 ? 3 : 2; }
+
+// Block (TPR, R): R rows at a time, the next R rows' loads issued before the present
+// rows' reduction.
+template <typename T, int VW, int NF, bool LONG>
+__global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, norm_blocks(NF * VW, LONG))
+k_norm(const __grid_constant__ RmsNormArgs a, float inv_h) {
   __shared__ float red[2 * kLongThreads / 32];
   pdl_wait();
   pdl_trigger();
@@ -245,81 +313,63 @@ k_norm(RmsNormArgs a) {
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* bias = static_cast<const T*>(a.bias);
   T* sum_out = static_cast<T*>(a.sum_out);
-  const int tpr = blockDim.x, slot = threadIdx.y;
-  const int64_t step = int64_t(gridDim.x) * blockDim.y, groups = (a.H + kMxGroup - 1) / kMxGroup;
-  constexpr bool kAhead = NF * VW <= 16;  // registers for a second row
-  int64_t row = int64_t(blockIdx.x) * blockDim.y + slot;
-  float* rred = red + slot * (2 * tpr / 32);
-  const float inv_h = 1.0f / float(a.H);
-
-  Raw<T, VW> gm[NF], bs[NF], rx[NF], rs[NF];
-  int col[NF];
-#pragma unroll
-  for (int j = 0; j < NF; ++j) {
-    col[j] = (j * tpr + int(threadIdx.x)) * VW;
-    gm[j].zero();
-    bs[j].zero();
-    rx[j].zero();
-    rs[j].zero();
-    if (col[j] < a.H) {
-      gm[j].keep(gamma + col[j]);
-      if (bias != nullptr) bs[j].keep(bias + col[j]);
-      if (kAhead && row < a.rows) {
-        rx[j].stream(x + row * a.H + col[j]);
-        if (skip != nullptr) rs[j].stream(skip + row * a.H + col[j]);
-      }
-    }
-  }
-  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-    if constexpr (!kAhead) {
-#pragma unroll
-      for (int j = 0; j < NF; ++j)
-        if (col[j] < a.H) {
-          rx[j].stream(x + row * a.H + col[j]);
-          if (skip != nullptr) rs[j].stream(skip + row * a.H + col[j]);
-        }
-    }
-    float s[NF][VW];
-    float sq = 0.f;
+  const int H = int(a.H), groups = (H + kMxGroup - 1) / kMxGroup, step = int(blockDim.x) * VW;
+  const int c0 = int(threadIdx.x) * VW;
+  const int64_t rows_step = int64_t(gridDim.x) * blockDim.y;
+  Raw<T, VW> rx[NF], rs[NF];
+  auto load = [&](int64_t row) {
+    const int cols = row < a.rows ? H : 0;
+    const int64_t at = row * H;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      float t[VW];
-      rx[j].floats(s[j]);
-      rs[j].floats(t);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) s[j][e] += t[e];
-      if (bias != nullptr) {
-        bs[j].floats(t);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) s[j][e] += t[e];
+      const int c = c0 + j * step;
+      if (c < cols) {
+        rx[j].stream(x + at + c);
+        if (skip != nullptr) rs[j].stream(skip + at + c);
       }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) sq += s[j][e] * s[j][e];
     }
-    const int64_t next = row + step;
-    if (kAhead && next < a.rows) {
+  };
 #pragma unroll
-      for (int j = 0; j < NF; ++j)
-        if (col[j] < a.H) {
-          rx[j].stream(x + next * a.H + col[j]);
-          if (skip != nullptr) rs[j].stream(skip + next * a.H + col[j]);
-        }
+  for (int j = 0; j < NF; ++j) {
+    rx[j].zero();
+    rs[j].zero();
+  }
+  int64_t r0 = int64_t(blockIdx.x) * blockDim.y;
+  load(r0 + threadIdx.y);
+  for (int turn = 0; r0 < a.rows; r0 += rows_step, turn ^= 1) {
+    const int64_t row = r0 + threadIdx.y, at = row * H;
+    const int cols = row < a.rows ? H : 0;  // (rows behind the last take part in the barriers)
+    float s[NF][VW], sq[VW] = {};
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int c = c0 + j * step;
+      rx[j].floats(s[j]);
+      rs[j].add_to(s[j]);
+      if (bias != nullptr && c < cols) {
+        Raw<T, VW> b;
+        b.keep(bias + c);
+        b.add_to(s[j]);
+      }
+      fma_all(sq, s[j], s[j]);
     }
+    if (r0 + rows_step < a.rows) load(row + rows_step);
     if (sum_out != nullptr) {
 #pragma unroll
       for (int j = 0; j < NF; ++j)
-        if (col[j] < a.H) store_row<T, VW>(sum_out + row * a.H + col[j], s[j]);
+        if (c0 + j * step < cols) store_row<T, VW>(sum_out + at + c0 + j * step, s[j]);
     }
-    const float inv = 1.0f / sqrtf(row_sum(sq, rred, turn, tpr, slot) * inv_h + a.eps);
-    if (a.inv_out != nullptr && threadIdx.x == 0) a.inv_out[row] = inv;
+    const float inv = rsqrtf(row_sum(sum_all(sq), red, turn) * inv_h + a.eps);
+    if (a.inv_out != nullptr && cols != 0 && threadIdx.x == 0) a.inv_out[row] = inv;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
+      const int c = c0 + j * step;
+      Raw<T, VW> gm;
       float g[VW];
-      gm[j].floats(g);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) s[j][e] *= inv * g[e];
-      store_mx8<VW>(s[j], col[j] < a.H, col[j] % kMxGroup == 0, a.q + row * a.H + col[j],
-                    a.scales + row * groups + col[j] / kMxGroup);
+      gm.zero();
+      if (c < H) gm.keep(gamma + c);
+      gm.floats(g);
+      mul_all(s[j], g);
+      store_mx8<VW>(s[j], inv, c < cols, c % kMxGroup == 0, a.q + at + c, a.scales + row * groups + c / kMxGroup);
     }
   }
 }
@@ -353,7 +403,7 @@ k_norm_long(RmsNormArgs a) {
       const float s = sum_at(x, skip, bias, row, a.H, c);
       sq += s * s;
     }
-    const float inv = 1.0f / sqrtf(row_sum(sq, red, turn, kLongThreads, 0) / float(a.H) + a.eps);
+    const float inv = rsqrtf(row_sum(sq, red, turn) / float(a.H) + a.eps);
     if (a.inv_out != nullptr && threadIdx.x == 0) a.inv_out[row] = inv;
     // whole warps: a group's lanes stay together.  (sum_out may be x or skip: an element is read by the thread
     // that writes it, before it does.)
@@ -365,7 +415,7 @@ k_norm_long(RmsNormArgs a) {
         if (sum_out != nullptr) st1_stream(sum_out + row * a.H + c, s);
         y[0] = s * (inv * to_float(gamma[c]));
       }
-      store_mx8<1>(y, c < a.H, c % kMxGroup == 0, a.q + row * a.H + c, a.scales + row * groups + c / kMxGroup);
+      store_mx8<1>(y, 1.0f, c < a.H, c % kMxGroup == 0, a.q + row * a.H + c, a.scales + row * groups + c / kMxGroup);
     }
   }
 }
@@ -374,123 +424,111 @@ k_norm_long(RmsNormArgs a) {
 // its gradient
 // ---------------------------------------------------------------------------
 
-// As k_norm; each thread also adds up its columns over the block's rows, and the
-// block's sums go to `partial` (gridDim.x, H), dbias's behind dgamma's.
-template <typename T, int VW, int NF, bool DB>
-__global__ void __launch_bounds__(kLongThreads)
-k_norm_grad(RmsNormGradArgs a) {
-  extern __shared__ float cols[];  // R > 1: threads x NF x VW
+// As k_norm; each thread adds up its columns, and the block's sums go to `partial`
+// (gridDim.x, H), dbias's behind dgamma's.  AHEAD: the next rows' loads are issued
+// before the present rows' reduction (where registers allow).
+template <typename T, int VW, int NF, bool LONG, bool DB>
+__global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, LONG ? 1 : 2)
+k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
+  extern __shared__ float cols_sum[];  // blockDim.y > 1: threads x NF x VW
   __shared__ float red[2 * kLongThreads / 32];
   pdl_wait();
   pdl_trigger();
+  constexpr bool AHEAD = NF * VW <= 16;
   const T* dy = static_cast<const T*>(a.dy);
   const T* sp = static_cast<const T*>(a.s);
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* dsum = static_cast<const T*>(a.dsum);
   T* dx = static_cast<T*>(a.dx);
-  const int tpr = blockDim.x, slot = threadIdx.y, slots = blockDim.y;
-  const int64_t step = int64_t(gridDim.x) * slots;
-  constexpr bool kAhead = NF * VW <= 16;  // registers for a second row
-  int64_t row = int64_t(blockIdx.x) * slots + slot;
-  float* rred = red + slot * (2 * tpr / 32);
-  const float inv_h = 1.0f / float(a.H);
+  const int H = int(a.H), step = int(blockDim.x) * VW, c0 = int(threadIdx.x) * VW;
+  const int64_t rows_step = int64_t(gridDim.x) * blockDim.y;
 
   Raw<T, VW> gm[NF], ry[NF], rs[NF], rd[NF];
-  float dg[NF][VW], db[NF][DB ? VW : 1];
+  float dg[NF][VW], db[DB ? NF : 1][VW];
   float inv = 0.f;
-  int col[NF];
+  auto load = [&](int64_t row) {
+    const int cols = row < a.rows ? H : 0;
+    inv = cols != 0 ? __ldg(a.inv + row) : 0.f;
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int c = c0 + j * step;
+      ry[j].zero();
+      rs[j].zero();
+      rd[j].zero();
+      if (c < cols) {
+        ry[j].stream(dy + row * H + c);
+        rs[j].stream(sp + row * H + c);
+        if (dsum != nullptr) rd[j].stream(dsum + row * H + c);
+      }
+    }
+  };
 #pragma unroll
   for (int j = 0; j < NF; ++j) {
-    col[j] = (j * tpr + int(threadIdx.x)) * VW;
     gm[j].zero();
-    ry[j].zero();
-    rs[j].zero();
-    rd[j].zero();
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
       dg[j][e] = 0.f;
       if constexpr (DB) db[j][e] = 0.f;
     }
-    if (col[j] < a.H) {
-      gm[j].keep(gamma + col[j]);
-      if (kAhead && row < a.rows) {
-        ry[j].stream(dy + row * a.H + col[j]);
-        rs[j].stream(sp + row * a.H + col[j]);
-        if (dsum != nullptr) rd[j].stream(dsum + row * a.H + col[j]);
-      }
-    }
+    if (c0 + j * step < H) gm[j].keep(gamma + c0 + j * step);
   }
-  if (row < a.rows) inv = a.inv[row];
-  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-    if constexpr (!kAhead) {
-#pragma unroll
-      for (int j = 0; j < NF; ++j)
-        if (col[j] < a.H) {
-          ry[j].stream(dy + row * a.H + col[j]);
-          rs[j].stream(sp + row * a.H + col[j]);
-          if (dsum != nullptr) rd[j].stream(dsum + row * a.H + col[j]);
-        }
-    }
-    float u[NF][VW], xh[NF][VW];
-    float dot = 0.f;
+  int turn = 0;
+  int64_t r0 = int64_t(blockIdx.x) * blockDim.y;
+  if (AHEAD) load(r0 + threadIdx.y);
+  for (; r0 < a.rows; r0 += rows_step, turn ^= 1) {
+    const int64_t row = r0 + threadIdx.y;
+    const int cols = row < a.rows ? H : 0;
+    if (!AHEAD) load(row);
+    const float now = inv;
+    float u[NF][VW], xh[NF][VW], dot[VW] = {};
+    auto terms = [&](int j) {  // u = dY gamma, x^ = s inv; returns dY in u first
+      ry[j].floats(u[j]);
+      rs[j].floats(xh[j]);
+      scale_all(xh[j], now);
+    };
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       float g[VW];
-      ry[j].floats(u[j]);
-      rs[j].floats(xh[j]);
+      terms(j);
+      fma_all(dg[j], u[j], xh[j]);
       gm[j].floats(g);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        xh[j][e] *= inv;
-        dg[j][e] += u[j][e] * xh[j][e];
-        u[j][e] *= g[e];
-        dot += u[j][e] * xh[j][e];
-      }
+      mul_all(u[j], g);
+      fma_all(dot, u[j], xh[j]);
     }
     Raw<T, VW> rc[NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) rc[j] = rd[j];
-    const float here = inv;
-    const int64_t next = row + step;
-    if (!kAhead && next < a.rows) inv = a.inv[next];
-    if (kAhead && next < a.rows) {
-#pragma unroll
-      for (int j = 0; j < NF; ++j)
-        if (col[j] < a.H) {
-          ry[j].stream(dy + next * a.H + col[j]);
-          rs[j].stream(sp + next * a.H + col[j]);
-          if (dsum != nullptr) rd[j].stream(dsum + next * a.H + col[j]);
-        }
-      inv = a.inv[next];
-    }
-    const float c = row_sum(dot, rred, turn, tpr, slot) * inv_h;
+    if (AHEAD && r0 + rows_step < a.rows) load(row + rows_step);
+    const float c = -row_sum(sum_all(dot), red, turn) * inv_h;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      float d[VW];
-      rc[j].floats(d);
-      if constexpr (!kAhead) {  // made again from what was loaded, in place of registers that hold it
+      if constexpr (!AHEAD) {  // made again from what was loaded, in place of registers that hold it
         float g[VW];
-        ry[j].floats(u[j]);
-        rs[j].floats(xh[j]);
+        terms(j);
         gm[j].floats(g);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-          xh[j][e] *= here;
-          u[j][e] *= g[e];
-        }
+        mul_all(u[j], g);
       }
+      float d[VW], k[VW];
+      rc[j].floats(d);
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        d[e] += here * (u[j][e] - xh[j][e] * c);
-        if constexpr (DB) db[j][e] += d[e];
+      for (int e = 0; e < VW; ++e) k[e] = c;
+      fma_all(u[j], xh[j], k);  // u - x^ mean
+#pragma unroll
+      for (int e = 0; e < VW; ++e) k[e] = now;
+      fma_all(d, u[j], k);
+      if constexpr (DB) {
+        if constexpr (VW == 1) db[j][0] += d[0];
+        else add_pairs(db[j], d);
       }
-      if (col[j] < a.H) store_row<T, VW>(dx + row * a.H + col[j], d);
+      if (c0 + j * step < cols) store_row<T, VW>(dx + row * H + c0 + j * step, d);
     }
   }
+  if (a.dgamma == nullptr && !DB) return;
   float* partial = static_cast<float*>(a.workspace);
+  const int tpr = int(blockDim.x), slots = int(blockDim.y), lane = int(threadIdx.x);
 #pragma unroll
   for (int b = 0; b < (DB ? 2 : 1); ++b) {
-    if (slots > 1) {  // the block's rows, added in the order of their slots
+    if (slots > 1) {  // the block's rows, added in their order
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < NF; ++j)
@@ -498,20 +536,21 @@ k_norm_grad(RmsNormGradArgs a) {
         for (int e = 0; e < VW; ++e) {
           float v = dg[j][e];
           if constexpr (DB) v = b == 0 ? v : db[j][e];
-          cols[((slot * NF + j) * tpr + threadIdx.x) * VW + e] = v;
+          cols_sum[((int(threadIdx.y) * NF + j) * VW + e) * tpr + lane] = v;
         }
       __syncthreads();
     }
-    if (slot != 0) continue;
+    if (threadIdx.y != 0) continue;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      if (col[j] >= a.H) continue;
-      float* out = partial + (int64_t(b) * gridDim.x + blockIdx.x) * a.H + col[j];
+      const int c = c0 + j * step;
+      if (c >= H) continue;
+      float* out = partial + (int64_t(b) * gridDim.x + blockIdx.x) * H + c;
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
         float v = dg[j][e];
         if constexpr (DB) v = b == 0 ? v : db[j][e];
-        for (int r = 1; r < slots; ++r) v += cols[((r * NF + j) * tpr + threadIdx.x) * VW + e];
+        for (int r = 1; r < slots; ++r) v += cols_sum[((r * NF + j) * VW + e) * tpr + lane];
         out[e] = v;
       }
     }
@@ -535,7 +574,7 @@ k_norm_grad_long(RmsNormGradArgs a, float* means) {
 #pragma unroll 4
     for (int64_t c = threadIdx.x; c < a.H; c += kLongThreads)
       dot += to_float(dy[row * a.H + c]) * to_float(gamma[c]) * (to_float(sp[row * a.H + c]) * inv);
-    const float m = row_sum(dot, red, turn, kLongThreads, 0) / float(a.H);
+    const float m = row_sum(dot, red, turn) / float(a.H);
     if (threadIdx.x == 0) means[row] = m;
   }
 }
@@ -588,32 +627,46 @@ bool on(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) 
 
 struct RowPlan {
   int vw, nf, tpr, slots;  // nf 0: the long form
+  bool wide;               // more than kRowThreads threads
 };
 
 // Fragments to threads: whole warps, of which as few lanes idle as the fragments a
-// thread (1, 2, 4 .. most_nf) allow; among those within an eighth of the best, the
-// most fragments, which leaves the fewest warps to join.
-RowPlan plan_rows(int64_t H, bool vec, int most_nf) {
-  RowPlan p{vec ? 8 : 1, 0, 0, 1};
-  const int64_t frags = (H + p.vw - 1) / p.vw;
+// thread (1 to most_nf) allow; among those within an eighth of the best, `best_nf`
+// fragments a thread, or else the most (which leaves the fewest warps to join).  Over
+// 256 threads only with the most fragments.
+void plan_threads(RowPlan* p, int64_t frags, int most_nf, int best_nf) {
   int64_t best = INT64_MAX;
   for (int pass = 0; pass < 2; ++pass)
-    for (int nf = 1; nf <= most_nf; nf *= 2) {
+    for (int nf = 1; nf <= most_nf; nf += nf < 4 ? 1 : 4) {
       const int64_t tpr = (frags + 32 * nf - 1) / (32 * nf) * 32;
-      if (tpr > kLongThreads) continue;
+      if (tpr > (nf == most_nf ? kLongThreads : kRowThreads)) continue;
       if (pass == 0) best = std::min(best, tpr * nf);
-      else if (tpr * nf * 8 <= best * 9) p.nf = nf, p.tpr = int(tpr);
+      else if (tpr * nf * 8 <= best * 9 && p->nf != best_nf) p->nf = nf, p->tpr = int(tpr);
     }
-  if (p.nf != 0) p.slots = std::max(1, kRowThreads / p.tpr);
-  return p;
 }
 
-// 8 elements a fragment: two fragments a thread leave registers for the next row; four (rows of 8193 to 16384
-// elements) are taken where two do not hold the row.
-RowPlan plan_rows(int64_t H, bool vec) {
-  if (!vec) return plan_rows(H, false, 8);
-  const RowPlan p = plan_rows(H, true, 2);
-  return p.nf != 0 ? p : plan_rows(H, true, 4);
+// 8 elements a fragment: rows of up to 128 elements share a warp (4, 8 or 16 threads
+// each); else two fragments a thread and four blocks an SM where that wastes no lanes
+// (bf16 16384 x 4096: 73 us; four fragments and two blocks 76), up to four where it
+// does or does not hold the row (f16 65536 x 768: 58 us with three, 68 with two; bf16
+// 8192 x 8192: 76 with four, 104 with two).  The gradient has its column sums in
+// registers too: two, and four where two do not hold the row.
+RowPlan plan_rows(int64_t H, bool vec, bool grad) {
+  RowPlan p{vec ? 8 : 1, 0, 0, 1, false};
+  const int64_t frags = (H + p.vw - 1) / p.vw;
+  if (vec && frags <= 16) {
+    p.nf = 1;
+    for (p.tpr = 4; p.tpr < frags; p.tpr *= 2) {}
+  } else if (!vec) {
+    plan_threads(&p, frags, 8, 8);
+  } else {
+    plan_threads(&p, frags, grad ? 2 : 4, 2);
+    if (p.nf == 0) plan_threads(&p, frags, 4, 4);
+  }
+  if (p.nf == 0) return p;
+  p.slots = std::max(1, kRowThreads / p.tpr);
+  p.wide = p.tpr > kRowThreads;
+  return p;
 }
 
 template <typename F>
@@ -625,21 +678,15 @@ cudaError_t by_type(DType t, F f) {
   }
 }
 
-// How many blocks of a kernel that walks over rows: what fits on the device, no more than there are rows.
-template <typename K>
-cudaError_t walk_grid(K kernel, int threads, size_t smem, int sm_count, int64_t blocks, unsigned* grid) {
-  int per_sm = 1;
-  const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
-  *grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(sm_count) * per_sm)));
-  return e;
+// Blocks of a kernel that walks over rows: `per_sm` that its registers let an SM hold, no more than there are.
+unsigned walk_grid(int64_t blocks, int sm_count, int per_sm) {
+  return unsigned(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(sm_count) * per_sm)));
 }
 
-template <typename T, int VW, int NF>
+template <typename T, int VW, int NF, bool LONG>
 cudaError_t norm_form(const RmsNormArgs& a, const RowPlan& p, int sm_count, cudaStream_t stream) {
-  unsigned grid;
-  cudaError_t e = walk_grid(k_norm<T, VW, NF>, p.tpr * p.slots, 0, sm_count, (a.rows + p.slots - 1) / p.slots, &grid);
-  if (e != cudaSuccess) return e;
-  return launch(k_norm<T, VW, NF>, dim3(grid), dim3(p.tpr, p.slots), 0, stream, a);
+  const unsigned grid = walk_grid((a.rows + p.slots - 1) / p.slots, sm_count, norm_blocks(NF * VW, LONG));
+  return launch(k_norm<T, VW, NF, LONG>, dim3(grid), dim3(p.tpr, p.slots), 0, stream, a, 1.0f / float(a.H));
 }
 
 // The gradient's blocks: two to an SM (the sums that they leave are read again),
@@ -650,16 +697,41 @@ int64_t grad_chunks(int64_t rows, int64_t H) {
   return std::max<int64_t>(1, std::min({want, (rows + 31) / 32, int64_t(65535)}));
 }
 
-template <typename T, int VW, int NF, bool DB>
+template <typename T, int VW, int NF, bool LONG, bool DB>
 cudaError_t grad_form(const RmsNormGradArgs& a, const RowPlan& p, cudaStream_t stream) {
   const size_t smem = p.slots > 1 ? size_t(p.tpr) * p.slots * NF * VW * sizeof(float) : 0;
-  return launch(k_norm_grad<T, VW, NF, DB>, dim3(unsigned(grad_blocks(a.rows, p.slots))), dim3(p.tpr, p.slots), smem,
-                stream, a);
+  return launch(k_norm_grad<T, VW, NF, LONG, DB>, dim3(unsigned(grad_blocks(a.rows, p.slots))), dim3(p.tpr, p.slots),
+                smem, stream, a, 1.0f / float(a.H));
 }
 
-template <typename T, int VW, int NF>
+template <typename T, int VW, int NF, bool LONG>
 cudaError_t grad_form(const RmsNormGradArgs& a, const RowPlan& p, cudaStream_t stream) {
-  return a.dbias != nullptr ? grad_form<T, VW, NF, true>(a, p, stream) : grad_form<T, VW, NF, false>(a, p, stream);
+  return a.dbias != nullptr ? grad_form<T, VW, NF, LONG, true>(a, p, stream)
+                            : grad_form<T, VW, NF, LONG, false>(a, p, stream);
+}
+
+// f(VW, NF, LONG) of the plan, as constants.
+template <int V> using Int = std::integral_constant<int, V>;
+template <bool GRAD, typename F>
+cudaError_t by_plan(const RowPlan& p, F f) {
+  using std::false_type;
+  using std::true_type;
+  if (p.vw == 8) {
+    if (p.nf == 1) return f(Int<8>(), Int<1>(), false_type());
+    if constexpr (GRAD) {
+      if (p.nf == 2) return p.wide ? f(Int<8>(), Int<2>(), true_type()) : f(Int<8>(), Int<2>(), false_type());
+      return f(Int<8>(), Int<4>(), true_type());
+    } else {
+      if (p.nf == 2) return f(Int<8>(), Int<2>(), false_type());
+      if (p.nf == 3) return f(Int<8>(), Int<3>(), false_type());
+      return p.wide ? f(Int<8>(), Int<4>(), true_type()) : f(Int<8>(), Int<4>(), false_type());
+    }
+  }
+  if (p.nf == 1) return f(Int<1>(), Int<1>(), false_type());
+  if (p.nf == 2) return f(Int<1>(), Int<2>(), false_type());
+  if (p.nf == 3) return f(Int<1>(), Int<3>(), false_type());
+  if (p.nf == 4) return f(Int<1>(), Int<4>(), false_type());
+  return p.wide ? f(Int<1>(), Int<8>(), true_type()) : f(Int<1>(), Int<8>(), false_type());
 }
 
 }  // namespace
@@ -703,25 +775,16 @@ cudaError_t launch_dequantize_mx8(const QuantizeArgs& a, int sm_count, cudaStrea
 cudaError_t launch_rms_norm_mx8(const RmsNormArgs& a, int sm_count, cudaStream_t stream, int* launches) {
   const bool vec = a.H % 8 == 0 && on(a.x, 16) && on(a.skip, 16) && on(a.gamma, 16) && on(a.bias, 16) && on(a.q, 8) &&
                    on(a.sum_out, 16);
-  const RowPlan p = plan_rows(a.H, vec);
+  const RowPlan p = plan_rows(a.H, vec, false);
   ++*launches;
   return by_type(a.t, [&](auto tag) {
     using T = decltype(tag);
     if (p.nf == 0) {
-      unsigned grid;
-      cudaError_t e = walk_grid(k_norm_long<T>, kLongThreads, 0, sm_count, a.rows, &grid);
-      if (e != cudaSuccess) return e;
-      return launch(k_norm_long<T>, dim3(grid), dim3(kLongThreads), 0, stream, a);
+      return launch(k_norm_long<T>, dim3(walk_grid(a.rows, sm_count, 3)), dim3(kLongThreads), 0, stream, a);
     }
-    if (vec) {
-      if (p.nf == 1) return norm_form<T, 8, 1>(a, p, sm_count, stream);
-      if (p.nf == 2) return norm_form<T, 8, 2>(a, p, sm_count, stream);
-      return norm_form<T, 8, 4>(a, p, sm_count, stream);
-    }
-    if (p.nf == 1) return norm_form<T, 1, 1>(a, p, sm_count, stream);
-    if (p.nf == 2) return norm_form<T, 1, 2>(a, p, sm_count, stream);
-    if (p.nf == 4) return norm_form<T, 1, 4>(a, p, sm_count, stream);
-    return norm_form<T, 1, 8>(a, p, sm_count, stream);
+    return by_plan<false>(p, [&](auto vw, auto nf, auto wide) {
+      return norm_form<T, vw.value, nf.value, wide.value>(a, p, sm_count, stream);
+    });
   });
 }
 
@@ -729,7 +792,7 @@ size_t rms_norm_grad_workspace_bytes(DType, int64_t rows, int64_t H) {
   size_t most = 0;
   for (const bool vec : {false, true}) {
     if (vec && H % 8 != 0) continue;
-    const RowPlan p = plan_rows(H, vec);
+    const RowPlan p = plan_rows(H, vec, true);
     const size_t sums = p.nf == 0 ? size_t(grad_chunks(rows, H)) : size_t(grad_blocks(rows, p.slots));
     most = std::max(most, 2 * sums * size_t(H) * 4 + (p.nf == 0 ? (size_t(rows) * 4 + 15) / 16 * 16 : 0));
   }
@@ -738,7 +801,7 @@ size_t rms_norm_grad_workspace_bytes(DType, int64_t rows, int64_t H) {
 
 cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
   const bool vec = a.H % 8 == 0 && on(a.dy, 16) && on(a.s, 16) && on(a.gamma, 16) && on(a.dsum, 16) && on(a.dx, 16);
-  const RowPlan p = plan_rows(a.H, vec);
+  const RowPlan p = plan_rows(a.H, vec, true);
   return by_type(a.t, [&](auto tag) {
     using T = decltype(tag);
     float* partial = static_cast<float*>(a.workspace);
@@ -748,25 +811,16 @@ cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int sm_count, cudaStr
       const int64_t chunks = grad_chunks(a.rows, a.H), per = (a.rows + chunks - 1) / chunks;
       terms = (a.rows + per - 1) / per;
       float* means = partial + 2 * chunks * a.H;
-      unsigned grid;
-      e = walk_grid(k_norm_grad_long<T>, kLongThreads, 0, sm_count, a.rows, &grid);
-      if (e != cudaSuccess) return e;
-      e = launch(k_norm_grad_long<T>, dim3(grid), dim3(kLongThreads), 0, stream, a, means);
+      e = launch(k_norm_grad_long<T>, dim3(walk_grid(a.rows, sm_count, 4)), dim3(kLongThreads), 0, stream, a, means);
       if (e != cudaSuccess) return e;
       ++*launches;
       e = launch(k_norm_grad_columns<T>, dim3(unsigned((a.H + 31) / 32), unsigned(terms)), dim3(256), 0, stream, a,
                  static_cast<const float*>(means), per, partial);
     } else {
       terms = grad_blocks(a.rows, p.slots);
-      if (vec) {
-        e = p.nf == 1 ? grad_form<T, 8, 1>(a, p, stream)
-                      : p.nf == 2 ? grad_form<T, 8, 2>(a, p, stream) : grad_form<T, 8, 4>(a, p, stream);
-      } else {
-        e = p.nf == 1   ? grad_form<T, 1, 1>(a, p, stream)
-            : p.nf == 2 ? grad_form<T, 1, 2>(a, p, stream)
-            : p.nf == 4 ? grad_form<T, 1, 4>(a, p, stream)
-                        : grad_form<T, 1, 8>(a, p, stream);
-      }
+      e = by_plan<true>(p, [&](auto vw, auto nf, auto wide) {
+        return grad_form<T, vw.value, nf.value, wide.value>(a, p, stream);
+      });
     }
     if (e != cudaSuccess) return e;
     ++*launches;
