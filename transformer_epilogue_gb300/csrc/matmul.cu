@@ -874,7 +874,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   for (uint32_t s = 0; s < splits; ++s) bad |= (splits > 1 ? failed[s] : failed_here) != 0;
   const int64_t first = m0 + int64_t(rank) * share;
   if (a.epi.vec) finish_rows<T, 8, 2>(a.epi, sums, int(splits), share, first, n0, bad);
-  else finish_rows<T, 1, 8>(a.epi, sums, int(splits), share, first, n0, bad);
+  else finish_rows<T, 1, 16>(a.epi, sums, int(splits), share, first, n0, bad);
 }
 
 // ---------------------------------------------------------------------------

@@ -428,7 +428,7 @@ k_norm_long(RmsNormArgs a) {
 // (gridDim.x, H), dbias's behind dgamma's.  AHEAD: the next rows' loads are issued
 // before the present rows' reduction (where registers allow).
 template <typename T, int VW, int NF, bool LONG, bool DB>
-__global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, LONG ? 1 : 2)
+__global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, LONG ? 1 : NF * VW <= 4 ? 4 : 2)
 k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
   extern __shared__ float cols_sum[];  // blockDim.y > 1: threads x NF x VW
   __shared__ float red[2 * kLongThreads / 32];
@@ -658,7 +658,7 @@ RowPlan plan_rows(int64_t H, bool vec, bool grad) {
     p.nf = 1;
     for (p.tpr = 4; p.tpr < frags; p.tpr *= 2) {}
   } else if (!vec) {
-    plan_threads(&p, frags, 8, 8);
+    plan_threads(&p, frags, 8, grad ? 4 : 8);
   } else {
     plan_threads(&p, frags, grad ? 2 : 4, 2);
     if (p.nf == 0) plan_threads(&p, frags, 4, 4);
@@ -689,9 +689,16 @@ cudaError_t norm_form(const RmsNormArgs& a, const RowPlan& p, int sm_count, cuda
   return launch(k_norm<T, VW, NF, LONG>, dim3(grid), dim3(p.tpr, p.slots), 0, stream, a, 1.0f / float(a.H));
 }
 
-// The gradient's blocks: two to an SM (the sums that they leave are read again),
-// a number that follows from the shape alone, as the workspace does.
-int64_t grad_blocks(int64_t rows, int slots) { return std::min<int64_t>((rows + slots - 1) / slots, 2 * kPlanSms); }
+// The gradient's blocks: as many as an SM's registers hold (up to 64, 112 and 128 a
+// thread), but no more than leave sums of a fourth of what is read (their sums are
+// written and read again); a number that follows from the shape alone, as the
+// workspace does.  (f16 65536 x 768: 76 us with three blocks of 192 threads an SM, 108 with two.)
+int64_t grad_blocks(int64_t rows, const RowPlan& p, int es) {
+  const int elements = p.nf * p.vw, regs = elements <= 4 ? 64 : elements <= 8 ? 112 : 128;
+  const int64_t per_sm = p.wide ? 1 : std::max(1, 65536 / (regs * p.tpr * p.slots));
+  const int64_t most = std::max<int64_t>(kPlanSms / 2, rows * es / 16);
+  return std::min({(rows + p.slots - 1) / p.slots, per_sm * kPlanSms, most});
+}
 int64_t grad_chunks(int64_t rows, int64_t H) {
   const int64_t want = std::max<int64_t>(1, 8 * kPlanSms / ((H + 31) / 32));
   return std::max<int64_t>(1, std::min({want, (rows + 31) / 32, int64_t(65535)}));
@@ -700,7 +707,7 @@ int64_t grad_chunks(int64_t rows, int64_t H) {
 template <typename T, int VW, int NF, bool LONG, bool DB>
 cudaError_t grad_form(const RmsNormGradArgs& a, const RowPlan& p, cudaStream_t stream) {
   const size_t smem = p.slots > 1 ? size_t(p.tpr) * p.slots * NF * VW * sizeof(float) : 0;
-  return launch(k_norm_grad<T, VW, NF, LONG, DB>, dim3(unsigned(grad_blocks(a.rows, p.slots))), dim3(p.tpr, p.slots),
+  return launch(k_norm_grad<T, VW, NF, LONG, DB>, dim3(unsigned(grad_blocks(a.rows, p, dtype_size(a.t)))), dim3(p.tpr, p.slots),
                 smem, stream, a, 1.0f / float(a.H));
 }
 
@@ -788,12 +795,12 @@ cudaError_t launch_rms_norm_mx8(const RmsNormArgs& a, int sm_count, cudaStream_t
   });
 }
 
-size_t rms_norm_grad_workspace_bytes(DType, int64_t rows, int64_t H) {
+size_t rms_norm_grad_workspace_bytes(DType t, int64_t rows, int64_t H) {
   size_t most = 0;
   for (const bool vec : {false, true}) {
     if (vec && H % 8 != 0) continue;
     const RowPlan p = plan_rows(H, vec, true);
-    const size_t sums = p.nf == 0 ? size_t(grad_chunks(rows, H)) : size_t(grad_blocks(rows, p.slots));
+    const size_t sums = p.nf == 0 ? size_t(grad_chunks(rows, H)) : size_t(grad_blocks(rows, p, dtype_size(t)));
     most = std::max(most, 2 * sums * size_t(H) * 4 + (p.nf == 0 ? (size_t(rows) * 4 + 15) / 16 * 16 : 0));
   }
   return most;
@@ -817,7 +824,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int sm_count, cudaStr
       e = launch(k_norm_grad_columns<T>, dim3(unsigned((a.H + 31) / 32), unsigned(terms)), dim3(256), 0, stream, a,
                  static_cast<const float*>(means), per, partial);
     } else {
-      terms = grad_blocks(a.rows, p.slots);
+      terms = grad_blocks(a.rows, p, dtype_size(a.t));
       e = by_plan<true>(p, [&](auto vw, auto nf, auto wide) {
         return grad_form<T, vw.value, nf.value, wide.value>(a, p, stream);
       });
