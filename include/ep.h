@@ -425,18 +425,19 @@ size_t ep_bias_dropout_grad_workspace_size(ep_dtype t, const int64_t* shape, int
  *     b = max(1, ceil(log2(amax / 448)) + 127),  amax = the group's largest magnitude
  *     q = E4M3(x * 2^(127 - b)), rounded to nearest even;  value = q * 2^(b - 127)
  *   Nothing saturates (|x| 2^(127 - b) <= 448).  A NaN becomes a NaN element; an
- *   infinity, which E4M3 lacks, makes its group's scale NaN.
+ *   infinity, which E4M3 lacks, makes its group's scale NaN (all its values read NaN).
  *   (rows, H) values are rows * H bytes of elements and rows * ceil(H / 32) bytes of
  *   scales, both dense.  The format comes from the OCP Microscaling Formats
  *   specification; no op definition covers these entry points.
  *
  * ep_quantize_mx8     X (`rank` dims, rows along the last) of T -> Q, scales.
  * ep_dequantize_mx8   Q, scales -> Y of T: exact, but where a value lies beyond T's
- *                     range (float16: infinite from 65520 on; subnormals rounded).
+ *                     range (float16: infinite from 65520 on; float32 and bfloat16 from
+ *                     2^128 on) or is subnormal in it (rounded).
  *
- * Errors: EP_ERR_UNSUPPORTED for another dtype, rank > 16, a last dimension over
- * 2^31 - 512 or 2^39 elements; EP_ERR_INVALID_ARG for negative dims, rank 0,
- * NULL/misaligned pointers or any overlap.
+ * Errors: EP_ERR_UNSUPPORTED for another dtype, rank > 16, a last dimension H over
+ * 2^31 - 512 or rows * ceil(H / 256) over 2^33; EP_ERR_INVALID_ARG for negative dims,
+ * rank 0, NULL/misaligned pointers or any overlap.
  */
 ep_status ep_quantize_mx8(ep_dtype t, const void* X, const int64_t* shape, int rank,
                           void* Q, uint8_t* scales, ep_stream_t stream);
@@ -514,8 +515,8 @@ size_t ep_skip_rms_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, in
  * each result rounded once.
  * workspace     ep_matmul_bias_act_workspace_size() bytes, 16-byte aligned: rows of K
  *               elements that are no multiple of 16 bytes, or operands that do not start on
- *               16-byte boundaries, are copied to where they are.  Calls that may overlap on
- *               the GPU need one each.
+ *               16-byte boundaries, are copied to where they are; large 8-bit products
+ *               arrange their scales in it.  Calls that may overlap on the GPU need one each.
  * K = 0 gives z = bias.
  *
  * Errors: EP_ERR_UNSUPPORTED for another dtype, M, N or K over 2^31 - 512 or operands
@@ -534,8 +535,7 @@ ep_status ep_matmul_bias_act_mx8(ep_dtype t, const void* A, const uint8_t* A_sca
                                  void* workspace, size_t workspace_bytes, ep_stream_t stream);
 
 /* Workspace bytes of the two (mx8 != 0: of the second).  aligned16 != 0: A and W
- * start on 16-byte boundaries (0 bytes where K elements are a multiple of 16 bytes).  0 as well for
- * arguments they reject. */
+ * start on 16-byte boundaries.  0 where none is needed, and for arguments they reject. */
 size_t ep_matmul_bias_act_workspace_size(int mx8, int64_t M, int64_t N, int64_t K, int aligned16);
 
 /*

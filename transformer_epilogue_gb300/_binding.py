@@ -640,24 +640,37 @@ def ep_bias_dropout_grad(dY, ratio, seed, offset=0, offset_device=None, dX=None,
 
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
+# What follows from a shape, a device index or the sizes of a product is kept by value.
+
+
+@functools.lru_cache(maxsize=64)
+def _cuda_device(index):
+    return torch.device("cuda", index)
+
 
 @functools.lru_cache(maxsize=4096)
-def _scale_shape(shape):
-    """The shape of the scales of rows of that shape."""
+def _rows_plan(shape):
+    """Rows along the last dimension: the C array, the rank, the shapes of a parameter, of MX8 scales and of a
+    statistic for each row."""
     if len(shape) == 0:
         raise ValueError("rows need a dimension")
-    return torch.Size(shape[:-1] + ((shape[-1] + 31) // 32,))
+    return (_shape(shape), len(shape), torch.Size(shape[-1:]), torch.Size(shape[:-1] + ((shape[-1] + 31) // 32,)),
+            torch.Size(shape[:-1] + (1,)))
 
 
-def _mx8_out(name, Q, scales, like, index, shape):
+def _scale_shape(shape):
+    return _rows_plan(shape)[3]
+
+
+def _mx8_out(name, Q, scales, like, index, shape, scale_shape):
     """Elements and scales to fill, made where they are not given."""
-    if (Q is None) != (scales is None):
+    if Q is None and scales is None:
+        device = _cuda_device(index)
+        return (torch.empty(shape, dtype=_E4M3, device=device), torch.empty(scale_shape, dtype=_E8M0, device=device))
+    if Q is None or scales is None:
         raise ValueError(f"{name} and its scales are given together")
-    if Q is None:
-        return (torch.empty(shape, dtype=_E4M3, device=like.device),
-                torch.empty(_scale_shape(shape), dtype=_E8M0, device=like.device))
     return (_operand(name, Q, like, index, shape, _E4M3),
-            _operand(f"{name}'s scales", scales, like, index, _scale_shape(shape), _E8M0))
+            _operand(f"{name}'s scales", scales, like, index, scale_shape, _E8M0))
 
 
 def ep_quantize_mx8(X, Q=None, scales=None, stream=None):
@@ -669,9 +682,10 @@ def ep_quantize_mx8(X, Q=None, scales=None, stream=None):
         with other:
             return ep_quantize_mx8(X, Q, scales)
     shape = X.shape
-    Q, scales = _mx8_out("Q", Q, scales, X, index, shape)
-    _check(load_library().ep_quantize_mx8(code, X.data_ptr(), _dims(shape), len(shape), Q.data_ptr(),
-                                          scales.data_ptr(), _raw_stream(index)))
+    dims, rank, _, scale_shape, _ = _rows_plan(shape)
+    Q, scales = _mx8_out("Q", Q, scales, X, index, shape, scale_shape)
+    _check(load_library().ep_quantize_mx8(code, X.data_ptr(), dims, rank, Q.data_ptr(), scales.data_ptr(),
+                                          _raw_stream(index)))
     return Q, scales
 
 
@@ -695,7 +709,7 @@ def ep_dequantize_mx8(Q, scales, dtype=None, Y=None, stream=None):
             return ep_dequantize_mx8(Q, scales, dtype, Y)
     shape = Q.shape
     if Y is None:
-        Y = torch.empty(shape, dtype=dtype, device=Q.device)
+        Y = torch.empty(shape, dtype=dtype, device=_cuda_device(index))
     else:
         _operand("Y", Y, Q, index, shape, Y.dtype if dtype is None else dtype)
     _check(load_library().ep_dequantize_mx8(_dtype(Y), Q.data_ptr(), scales.data_ptr(), _dims(shape), len(shape),
@@ -703,15 +717,14 @@ def ep_dequantize_mx8(Q, scales, dtype=None, Y=None, stream=None):
     return Y
 
 
-def _row_stats(name, t, X, index):
+def _row_stats(name, t, X, index, stat_shape):
+    if t is True:
+        return torch.empty(stat_shape, dtype=torch.float32, device=_cuda_device(index))
     if t is None or t is False:
         return None
-    rows = X.shape[:-1] + (1,)
-    if t is True:
-        return torch.empty(rows, dtype=torch.float32, device=X.device)
     _operand(name, t, X, index, dtype=torch.float32)
-    if t.numel() != rows.numel():
-        raise ValueError(f"{name} must have {rows.numel()} elements")
+    if t.numel() != stat_shape.numel():
+        raise ValueError(f"{name} must have {stat_shape.numel()} elements")
     return t
 
 
@@ -727,22 +740,22 @@ def ep_skip_rms_norm_mx8(input, skip, gamma, bias=None, epsilon=DEFAULT_EPSILON,
         with other:
             return ep_skip_rms_norm_mx8(input, skip, gamma, bias, epsilon, Q, scales, input_skip_bias_sum, inv_std_dev)
     shape = input.shape
-    channels = shape[-1:]
+    dims, rank, channels, scale_shape, stat_shape = _rows_plan(shape)
     if skip is not None:
         _operand("skip", skip, input, index, shape)
     _operand("gamma", gamma, input, index, channels)
     if bias is not None:
         _operand("bias", bias, input, index, channels)
-    Q, scales = _mx8_out("Q", Q, scales, input, index, shape)
+    Q, scales = _mx8_out("Q", Q, scales, input, index, shape, scale_shape)
     if input_skip_bias_sum is True:
         input_skip_bias_sum = torch.empty_like(input)
     elif input_skip_bias_sum is False:
         input_skip_bias_sum = None
     if input_skip_bias_sum is not None:
         _operand("input_skip_bias_sum", input_skip_bias_sum, input, index, shape)
-    inv_std_dev = _row_stats("inv_std_dev", inv_std_dev, input, index)
+    inv_std_dev = _row_stats("inv_std_dev", inv_std_dev, input, index, stat_shape)
     _check(load_library().ep_skip_rms_norm_mx8(
-        code, input.data_ptr(), _dims(shape), len(shape), _addr(skip), gamma.data_ptr(), _addr(bias), float(epsilon),
+        code, input.data_ptr(), dims, rank, _addr(skip), gamma.data_ptr(), _addr(bias), float(epsilon),
         Q.data_ptr(), scales.data_ptr(), _addr(input_skip_bias_sum), _addr(inv_std_dev), _raw_stream(index)))
     return Q, scales, input_skip_bias_sum, inv_std_dev
 
@@ -770,12 +783,12 @@ def ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum=None
         with other:
             return ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum, dX, dgamma, dbias, workspace)
     shape = dY.shape
-    channels = shape[-1:]
+    dims, rank, channels, _, stat_shape = _rows_plan(shape)
     _operand("input_skip_bias_sum", input_skip_bias_sum, dY, index, shape)
     _operand("gamma", gamma, dY, index, channels)
     if not isinstance(inv_std_dev, torch.Tensor):
         raise ValueError("inv_std_dev is required")
-    _row_stats("inv_std_dev", inv_std_dev, dY, index)
+    _row_stats("inv_std_dev", inv_std_dev, dY, index, stat_shape)
     if dsum is not None:
         _operand("dsum", dsum, dY, index, shape)
     dX = torch.empty_like(dY) if dX is None else _operand("dX", dX, dY, index, shape)
@@ -785,7 +798,7 @@ def ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum=None
     ws, wbytes, owned = _scratch(workspace, _rms_norm_grad_need(code, shape), dY, s)
     try:
         _check(load_library().ep_skip_rms_norm_grad(
-            code, dY.data_ptr(), input_skip_bias_sum.data_ptr(), _dims(shape), len(shape), gamma.data_ptr(),
+            code, dY.data_ptr(), input_skip_bias_sum.data_ptr(), dims, rank, gamma.data_ptr(),
             inv_std_dev.data_ptr(), _addr(dsum), dX.data_ptr(), _addr(dgamma), _addr(dbias), ws, wbytes, s))
     finally:
         if owned:
@@ -795,11 +808,11 @@ def ep_skip_rms_norm_grad(dY, input_skip_bias_sum, gamma, inv_std_dev, dsum=None
 
 @functools.lru_cache(maxsize=4096)
 def _matmul_sizes(a_shape, w_shape):
-    """(M, N, K) and the result's shape of A (..., K) times W (N, K)."""
+    """(M, N, K), and the shapes of the result and of the bias, of A (..., K) times W (N, K)."""
     if len(a_shape) < 1 or len(w_shape) != 2 or a_shape[-1] != w_shape[1]:
         raise ValueError(f"A (..., K) and W (N, K) do not fit: {tuple(a_shape)} and {tuple(w_shape)}")
-    shape = torch.Size(a_shape[:-1] + w_shape[:1])
-    return torch.Size(a_shape[:-1]).numel(), w_shape[0], w_shape[1], shape
+    shape, channels = torch.Size(a_shape[:-1] + w_shape[:1]), torch.Size(w_shape[:1])
+    return torch.Size(a_shape[:-1]).numel(), w_shape[0], w_shape[1], shape, channels
 
 
 @functools.lru_cache(maxsize=4096)
@@ -815,14 +828,14 @@ def _matmul_grad_need(m, n, k, activation, a_mx8, aligned):
 def ep_matmul_bias_act_workspace_size(a_shape, w_shape, mx8=False, aligned=False) -> int:
     """Workspace bytes of ep_matmul_bias_act for A (..., K) and W (N, K), of 16 bits
     or (``mx8``) 8.  ``aligned``: both start on 16-byte boundaries."""
-    m, n, k, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
+    m, n, k, _, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
     return _matmul_need(bool(mx8), m, n, k, bool(aligned))
 
 
 def ep_matmul_bias_act_grad_workspace_size(a_shape, w_shape, activation=EP_ACT_NONE, a_mx8=False, aligned=False) -> int:
     """Workspace bytes of ep_matmul_bias_act_grad.  ``a_mx8``: A is in MX8;
     ``aligned``: dY, W and a 16-bit A start on 16-byte boundaries."""
-    m, n, k, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
+    m, n, k, _, _ = _matmul_sizes(torch.Size(a_shape), torch.Size(w_shape))
     return _matmul_grad_need(m, n, k, int(activation), bool(a_mx8), bool(aligned))
 
 
@@ -843,9 +856,10 @@ def ep_matmul_bias_act(A, W, bias=None, residual=None, activation=EP_ACT_NONE, a
             return ep_matmul_bias_act(A, W, bias, residual, activation, alpha, A_scales, W_scales, dtype, Y, Z,
                                       Z_scales, workspace)
     mx8 = A.dtype is _E4M3
-    _operand("A", A, A, index)
+    if not A.is_contiguous():
+        raise ValueError("A must be contiguous")
     _operand("W", W, A, index)
-    m, n, k, shape = _matmul_sizes(A.shape, W.shape)
+    m, n, k, shape, channels = _matmul_sizes(A.shape, W.shape)
     if mx8:
         _operand("A_scales", A_scales, A, index, _scale_shape(A.shape), _E8M0)
         _operand("W_scales", W_scales, A, index, _scale_shape(W.shape), _E8M0)
@@ -864,23 +878,26 @@ def ep_matmul_bias_act(A, W, bias=None, residual=None, activation=EP_ACT_NONE, a
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
     if bias is not None:
-        _operand("bias", bias, A, index, W.shape[:1], dtype)
+        _operand("bias", bias, A, index, channels, dtype)
     if residual is not None:
         _operand("residual", residual, A, index, shape, dtype)
-    Y = torch.empty(shape, dtype=dtype, device=A.device) if Y is None else _operand("Y", Y, A, index, shape, dtype)
-    if isinstance(Z, torch.dtype):
+    Y = torch.empty(shape, dtype=dtype, device=_cuda_device(index)) if Y is None else \
+        _operand("Y", Y, A, index, shape, dtype)
+    if Z is None and Z_scales is None:
+        pass
+    elif isinstance(Z, torch.dtype):
         if Z is not _E4M3 or Z_scales is not None:
             raise ValueError("Z: None, True, torch.float8_e4m3fn, or a tensor")
-        Z, Z_scales = _mx8_out("Z", None, None, A, index, shape)
+        Z, Z_scales = _mx8_out("Z", None, None, A, index, shape, _scale_shape(shape))
     elif isinstance(Z, torch.Tensor) and Z.dtype is _E4M3:
         if Z_scales is None:
             raise ValueError("Z_scales is required for a float8_e4m3fn Z")
-        Z, Z_scales = _mx8_out("Z", Z, Z_scales, A, index, shape)
+        Z, Z_scales = _mx8_out("Z", Z, Z_scales, A, index, shape, _scale_shape(shape))
     else:
         if Z_scales is not None:
             raise ValueError("Z_scales belongs to a float8_e4m3fn Z")
         if Z is True:
-            Z = torch.empty(shape, dtype=dtype, device=A.device)
+            Z = torch.empty(shape, dtype=dtype, device=_cuda_device(index))
         elif Z is False:
             Z = None
         elif Z is not None:
@@ -906,7 +923,7 @@ def _grad_out(name, t, like, index, shape):
     if t is None or t is False:
         return None
     if t is True:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty(shape, dtype=like.dtype, device=_cuda_device(index))
     return _operand(name, t, like, index, shape)
 
 
@@ -925,7 +942,7 @@ def ep_matmul_bias_act_grad(dY, A, W, Z=None, activation=EP_ACT_NONE, alpha=DEFA
     _operand("W", W, dY, index)
     a_mx8 = A_scales is not None
     _operand("A", A, dY, index, dtype=_E4M3 if a_mx8 else None)
-    m, n, k, shape = _matmul_sizes(A.shape, W.shape)
+    m, n, k, shape, channels = _matmul_sizes(A.shape, W.shape)
     if a_mx8:
         _operand("A_scales", A_scales, dY, index, _scale_shape(A.shape), _E8M0)
     if dY.shape != shape:
@@ -939,7 +956,7 @@ def ep_matmul_bias_act_grad(dY, A, W, Z=None, activation=EP_ACT_NONE, alpha=DEFA
             _operand("Z_scales", Z_scales, dY, index, _scale_shape(shape), _E8M0)
     dA = _grad_out("dA", dA, dY, index, A.shape)
     dW = _grad_out("dW", dW, dY, index, W.shape)
-    dbias = _param_grad("dbias", dbias, dY, index, W.shape[:1])
+    dbias = _param_grad("dbias", dbias, dY, index, channels)
     py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
     aligned = (py | pw | (0 if a_mx8 else pa)) & 15 == 0
     s = _raw_stream(index)

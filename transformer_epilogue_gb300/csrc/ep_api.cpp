@@ -700,9 +700,10 @@ ep_status mx8_shape(const char* op, ep_dtype t, const int64_t* shape, int rank, 
   if (!dims_product(shape, 0, rank, &n) || !dims_product(shape, 0, rank - 1, rows))
     return fail(EP_ERR_INVALID_ARG, "%s: negative or overflowing dims", op);
   *H = shape[rank - 1];
-  if (*H > kMostDim || (n + 255) / 256 > kMostDim)
-    return fail(EP_ERR_UNSUPPORTED, "%s: rows of %lld elements, %lld elements in all (at most 2^31 - 512 and 2^39)", op,
-                (long long)*H, (long long)n);
+  // (pieces of 256 elements, of which a block takes eight: what a grid can count)
+  if (*H > kMostDim || (*H > 0 && *rows > (int64_t(1) << 33) / ((*H + 255) / 256)))
+    return fail(EP_ERR_UNSUPPORTED, "%s: %lld rows of %lld elements (at most 2^31 - 512 elements, rows * ceil(H / 256) 2^33)",
+                op, (long long)*rows, (long long)*H);
   return EP_OK;
 }
 

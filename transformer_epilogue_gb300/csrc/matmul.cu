@@ -75,7 +75,7 @@ struct Epilogue {
 struct ScaleRows {
   const uint8_t* p;
   int64_t rows, groups;
-  int unit;  // bytes that can be loaded together: p and groups are multiples of it (16, 4 or 1)
+  int unit;  // bytes that can be loaded together: p and groups are multiples of it (16, 4, 2 or 1)
 };
 
 // The quads have a ring of their own in shared memory, with barriers of their own:
@@ -100,6 +100,12 @@ __device__ __forceinline__ void scale_quad(const ScaleRows& s, int64_t row, int6
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (g + 4 * i < s.groups) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else if (s.unit == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (g + 2 * i < s.groups)
+        w[i / 2] = (w[i / 2] & ~(65535u << (16 * (i % 2)))) |
+                   uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -220,35 +226,40 @@ __device__ __forceinline__ uint8_t* staged(uint8_t* buf, int r, int c) {
   return buf + (r * NC + (c ^ ((r / (8 / NC)) & (NC - 1)))) * 16;
 }
 
-// A warp's 32 rows x NC words between shared and global memory.
-template <int NC, typename E, bool LOAD>
-__device__ __forceinline__ void turn_words(uint8_t* buf, E* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
-                                           int lane) {
+// A warp's 32 rows x NC words of 16 bytes, a row's words in neighbouring lanes, from
+// global to shared memory and back.
+template <int NC, typename E>
+__device__ __forceinline__ void read_words(uint8_t* buf, const E* g, int64_t row0, int64_t col0, int64_t rows,
+                                           int64_t cols, int lane) {
   constexpr int PER = 16 / sizeof(E);
   uint4 w[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int idx = i * 32 + lane, r = idx / NC, c = idx % NC;
-    const int64_t row = row0 + r, col = col0 + c * PER;
-    const bool in = row < rows && col < cols;
-    uint4* p = reinterpret_cast<uint4*>(g + row * cols + col);
-    if constexpr (LOAD) {
-      w[i] = in ? __ldcs(p) : make_uint4(0, 0, 0, 0);
-    } else if (in) {
-      __stcs(p, *reinterpret_cast<const uint4*>(staged<NC>(buf, r, c)));
-    }
+    const int64_t row = row0 + (i * 32 + lane) / NC, col = col0 + (i * 32 + lane) % NC * PER;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows && col < cols) w[i] = __ldcs(reinterpret_cast<const uint4*>(g + row * cols + col));
   }
-  if constexpr (LOAD) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int idx = i * 32 + lane;
-      *reinterpret_cast<uint4*>(staged<NC>(buf, idx / NC, idx % NC)) = w[i];
-    }
+  for (int i = 0; i < NC; ++i)
+    *reinterpret_cast<uint4*>(staged<NC>(buf, (i * 32 + lane) / NC, (i * 32 + lane) % NC)) = w[i];
+}
+template <int NC, typename E>
+__device__ __forceinline__ void write_words(uint8_t* buf, E* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                            int lane) {
+  constexpr int PER = 16 / sizeof(E);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int r = (i * 32 + lane) / NC, c = (i * 32 + lane) % NC;
+    const int64_t row = row0 + r, col = col0 + c * PER;
+    if (row < rows && col < cols)
+      __stcs(reinterpret_cast<uint4*>(g + row * cols + col), *reinterpret_cast<const uint4*>(staged<NC>(buf, r, c)));
   }
 }
 
 // The same by smaller units U (an element, or two neighbours), a row's units to
-// neighbouring lanes, for rows that start on no 16-byte boundary.
+// neighbouring lanes, for rows that start on no 16-byte boundary.  16 rows' loads
+// are in flight together (with 8 in a loop that stored each, f16 1331 x 1001 x 771
+// with a residual took 10 us longer).
 template <int NC, typename U, bool LOAD>
 __device__ __forceinline__ void turn_units(uint8_t* buf, U* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
                                            int lane) {
@@ -259,25 +270,36 @@ __device__ __forceinline__ void turn_units(uint8_t* buf, U* g, int64_t row0, int
     const int l = l0 + lane;
     const bool in = l < N && col0 + l < cols;
     U* p = g + row0 * cols + col0 + l;
+    auto at = [&](int r) { return reinterpret_cast<U*>(staged<NC>(buf, r, l / PER)) + l % PER; };
+#pragma unroll 1
+    for (int r0 = 0; r0 < high; r0 += 16) {
+      if constexpr (LOAD) {
+        U v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = in && r0 + r < high ? p[(r0 + r) * cols] : U(0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (l < N) *at(r0 + r) = v[r];
+      } else {
 #pragma unroll 8
-    for (int r = 0; r < high; ++r) {
-      if (!in) continue;
-      U* s = reinterpret_cast<U*>(staged<NC>(buf, r, l / PER)) + l % PER;
-      if constexpr (LOAD) *s = p[r * cols];
-      else p[r * cols] = *s;
+        for (int r = r0; r < min(r0 + 16, high); ++r)
+          if (in) p[r * cols] = *at(r);
+      }
     }
   }
 }
 
-template <int NC, typename E, typename E2, bool LOAD>
-__device__ __forceinline__ void turn_rows(uint8_t* buf, void* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
-                                          bool vec, bool pairs, int lane) {
-  if (vec) turn_words<NC, E, LOAD>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
-  else if (pairs) turn_units<NC, E2, LOAD>(buf, static_cast<E2*>(g), row0, col0 / 2, rows, cols / 2, lane);
-  else turn_units<NC, E, LOAD>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
+template <int NC, typename E, typename E2>
+__device__ __forceinline__ void write_rows(uint8_t* buf, void* g, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                           bool vec, bool pairs, int lane) {
+  if (vec) write_words<NC, E>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
+  else if (pairs) turn_units<NC, E2, false>(buf, static_cast<E2*>(g), row0, col0 / 2, rows, cols / 2, lane);
+  else turn_units<NC, E, false>(buf, static_cast<E*>(g), row0, col0, rows, cols, lane);
 }
 
-// CW columns of a warp's 32 rows, from tensor memory to the outputs.
+// CW columns of a warp's 32 rows, from tensor memory to the outputs.  (A residual
+// fetched a chunk ahead, into 32 more registers, took longer: bf16 8192 x 8192 x 256 in
+// 100 us for 89.)
 template <typename T, int CW>
 __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, float* bs, uint32_t tmem, int64_t row0,
                                            int64_t col0, int lane) {
@@ -340,15 +362,16 @@ __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, floa
     }
     __syncwarp();
     if (e.z_scales == nullptr)
-      turn_rows<NC, uint16_t, uint32_t, false>(buf, e.z, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
+      write_rows<NC, uint16_t, uint32_t>(buf, e.z, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
     else
-      turn_rows<NC8, uint8_t, uint16_t, false>(buf, e.z, row0, col0, e.rows, e.cols, e.vec && e.cols % 16 == 0, e.pairs,
-                                               lane);
+      write_rows<NC8, uint8_t, uint16_t>(buf, e.z, row0, col0, e.rows, e.cols, e.vec && e.cols % 16 == 0, e.pairs, lane);
     __syncwarp();
   }
   if (e.residual != nullptr) {
-    turn_rows<NC, uint16_t, uint32_t, true>(buf, const_cast<void*>(e.residual), row0, col0, e.rows, e.cols, e.vec,
-                                            e.pairs, lane);
+    void* r = const_cast<void*>(e.residual);
+    if (e.vec) read_words<NC>(buf, static_cast<const T*>(e.residual), row0, col0, e.rows, e.cols, lane);
+    else if (e.pairs) turn_units<NC, uint32_t, true>(buf, static_cast<uint32_t*>(r), row0, col0 / 2, e.rows, e.cols / 2, lane);
+    else turn_units<NC, uint16_t, true>(buf, static_cast<uint16_t*>(r), row0, col0, e.rows, e.cols, lane);
     __syncwarp();
   }
 #pragma unroll
@@ -371,7 +394,7 @@ __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, floa
     put(h, z);
   }
   __syncwarp();
-  turn_rows<NC, uint16_t, uint32_t, false>(buf, e.y, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
+  write_rows<NC, uint16_t, uint32_t>(buf, e.y, row0, col0, e.rows, e.cols, e.vec, e.pairs, lane);
   __syncwarp();
 }
 
@@ -1086,7 +1109,8 @@ cudaError_t make_map(CUtensorMap* map, DType t, bool mx8, const Operand& o, int 
 ScaleRows scale_rows(const Operand& o) {
   const int64_t g = mx_groups(o.depth);
   return ScaleRows{o.scales, o.rows, g,
-                   g % 16 == 0 && on(o.scales, 16) ? 16 : g % 4 == 0 && on(o.scales, 4) ? 4 : 1};
+                   g % 16 == 0 && on(o.scales, 16) ? 16
+                   : g % 4 == 0 && on(o.scales, 4) ? 4 : g % 2 == 0 && on(o.scales, 2) ? 2 : 1};
 }
 
 // Blocks of `words` 32-bit words of scales, one after the other.
@@ -1335,7 +1359,7 @@ struct Pitcher {
 // Row chunks of k_act_slope: as many blocks as the device holds (three an SM) at once,
 // 32 rows at least.
 int64_t slope_chunks(int64_t M, int64_t N) {
-  const int64_t tiles = (N + 255) / 256;
+  const int64_t tiles = std::max<int64_t>(1, (N + 255) / 256);
   return std::max<int64_t>(1, std::min({3 * kPlanSms / tiles, (M + 31) / 32, int64_t(65535)}));
 }
 

@@ -145,8 +145,9 @@ __device__ __forceinline__ float sum_all(const float (&f)[VW]) {
 // MX8 of m * r for a fragment m whose group is held by 32 / VW neighbouring lanes (all
 // of them here; `in`: the fragment lies in the row).  r and the scale's power of two
 // make one factor: the power scales exactly, so (m r) 2^e and m (r 2^e) round alike.
+// Returns the scale's byte.
 template <int VW>
-__device__ __forceinline__ void store_mx8(float (&m)[VW], float r, bool in, bool first, uint8_t* q, uint8_t* scale) {
+__device__ __forceinline__ uint32_t store_elements(float (&m)[VW], float r, bool in, uint8_t* q) {
   float amax;
   if constexpr (VW == 1) {  // magnitudes compare as their bits do; NaN is left out
     const float f = fabsf(m[0]);
@@ -162,12 +163,18 @@ __device__ __forceinline__ void store_mx8(float (&m)[VW], float r, bool in, bool
   }
   const uint32_t b = mx_scale(amax * r);
   scale_all(m, r * mx_factor(b));
-  if (!in) return;
-  if constexpr (VW == 8)
-    __stcs(reinterpret_cast<uint2*>(q), make_uint2(e4m3x4(m[0], m[1], m[2], m[3]), e4m3x4(m[4], m[5], m[6], m[7])));
-  else
-    *q = uint8_t(e4m3x2(m[0], 0.f));
-  if (first) *scale = uint8_t(b);
+  if (in) {
+    if constexpr (VW == 8)
+      __stcs(reinterpret_cast<uint2*>(q), make_uint2(e4m3x4(m[0], m[1], m[2], m[3]), e4m3x4(m[4], m[5], m[6], m[7])));
+    else
+      __stcs(q, uint8_t(e4m3x2(m[0], 0.f)));
+  }
+  return b;
+}
+template <int VW>
+__device__ __forceinline__ void store_mx8(float (&m)[VW], float r, bool in, bool first, uint8_t* q, uint8_t* scale) {
+  const uint32_t b = store_elements<VW>(m, r, in, q);
+  if (in && first) *scale = uint8_t(b);
 }
 
 // Sum over the blockDim.x threads of a row (a power of two below 32, or whole warps);
@@ -202,7 +209,9 @@ __device__ __forceinline__ void split_index(uint64_t i, uint32_t d, uint64_t* ro
   }
 }
 
-// A group of 32 to 32 / VW lanes, U groups each before the first is used.
+// A group of 32 to 32 / VW lanes, U groups each before the first is used.  VW 1: rows of
+// a few groups, which would leave most of k_quantize_ragged's 256 elements empty (f16
+// 60710 x 3: 8 us for 19).
 template <typename T, int VW, int U>
 __global__ void __launch_bounds__(kRowThreads)
 k_quantize(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict__ scales, int64_t items, uint32_t H,
@@ -244,13 +253,76 @@ k_quantize(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict
   }
 }
 
-// Fragments of VW elements of rows `ld` apart (a multiple of VW); what lies behind a row's H elements is set to 0.
-template <typename T, int VW, int U>
+// Rows that start on no 16-byte boundary: a warp takes 256 elements of a row, a group
+// at a time, one lane an element (one division for all of them).
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+k_quantize_ragged(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict__ scales, int64_t items,
+                  uint32_t H, uint32_t G) {
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t segs = (G + 7) / 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (i >= items) return;
+  uint64_t row;
+  uint32_t seg;
+  split_index(uint64_t(i), segs, &row, &seg);
+  const uint32_t left = H - seg * 256;  // elements from here on
+  const T* xs = x + row * H + seg * 256 + lane;
+  uint8_t* qs = q + row * H + seg * 256 + lane;
+  Raw<T, 1> raw[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (32u * u + lane < left) raw[u].stream(xs + 32 * u);
+    else raw[u].zero();
+  }
+  uint32_t mine = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float f[1];
+    raw[u].floats(f);
+    const uint32_t b = store_elements<1>(f, 1.0f, 32u * u + lane < left, qs + 32 * u);
+    mine = lane == u ? b : mine;
+  }
+  if (lane < 8 && 32u * lane < left) scales[row * G + seg * 8 + lane] = uint8_t(mine);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+k_dequantize_ragged(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, T* __restrict__ y, int64_t items,
+                    uint32_t H, uint32_t G, uint32_t ld) {
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t segs = (ld + 255) / 256;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (i >= items) return;
+  uint64_t row;
+  uint32_t seg;
+  split_index(uint64_t(i), segs, &row, &seg);
+  const uint32_t c0 = seg * 256 + lane, g0 = seg * 8;
+  const uint8_t* qs = q + row * H + c0;
+  T* ys = y + row * ld + c0;
+  const uint32_t mine = lane < 8 && g0 + lane < G ? __ldg(scales + row * G + g0 + lane) : 127u;
+  uint32_t e[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) e[u] = c0 + 32 * u < H ? __ldcs(qs + 32 * u) : 0u;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float k = mx_value(__shfl_sync(0xffffffffu, mine, u));
+    if (c0 + 32 * u < ld) st1_stream(ys + 32 * u, e4m3_floats(e[u]).x * k);
+  }
+}
+
+// Fragments of 8 elements of rows `ld` apart (a multiple of 8); what lies behind a row's H elements is set to 0.
+template <typename T, int U>
 __global__ void __launch_bounds__(kRowThreads)
 k_dequantize(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, T* __restrict__ y, int64_t items,
              uint32_t H, uint32_t G, uint32_t ld) {
   pdl_wait();
   pdl_trigger();
+  constexpr int VW = 8;
   const uint32_t frags = ld / VW;
   const int64_t i0 = int64_t(blockIdx.x) * (kRowThreads * U) + threadIdx.x;
   uint2 raw[U];
@@ -267,8 +339,7 @@ k_dequantize(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, 
     col *= VW;
     if (col >= H) continue;
     const uint8_t* p = q + row * H + col;
-    if constexpr (VW == 8) raw[u] = __ldcs(reinterpret_cast<const uint2*>(p));
-    else raw[u].x = *p;
+    raw[u] = __ldcs(reinterpret_cast<const uint2*>(p));
     b[u] = scales[row * G + col / kMxGroup];
   }
 #pragma unroll
@@ -277,16 +348,12 @@ k_dequantize(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales, 
     if (i >= items) continue;
     const float k = mx_value(b[u]);
     float f[VW];
-    if constexpr (VW == 8) {
-      const uint32_t w[4] = {raw[u].x, raw[u].x >> 16, raw[u].y, raw[u].y >> 16};
+    const uint32_t w[4] = {raw[u].x, raw[u].x >> 16, raw[u].y, raw[u].y >> 16};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 t = e4m3_floats(w[e]);
-        f[2 * e] = t.x * k;
-        f[2 * e + 1] = t.y * k;
-      }
-    } else {
-      f[0] = e4m3_floats(raw[u].x).x * k;
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = e4m3_floats(w[e]);
+      f[2 * e] = v.x * k;
+      f[2 * e + 1] = v.y * k;
     }
     store_row<T, VW>(y + i * VW, f);
   }
@@ -360,6 +427,9 @@ k_norm(const __grid_constant__ RmsNormArgs a, float inv_h) {
     }
     const float inv = rsqrtf(row_sum(sum_all(sq), red, turn) * inv_h + a.eps);
     if (a.inv_out != nullptr && cols != 0 && threadIdx.x == 0) a.inv_out[row] = inv;
+    uint8_t* qr = a.q + at;
+    uint8_t* scale = a.scales + row * groups;
+    uint32_t mine = 0;  // one element a fragment: lane j stores the warp's j-th group's scale
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       const int c = c0 + j * step;
@@ -369,7 +439,16 @@ k_norm(const __grid_constant__ RmsNormArgs a, float inv_h) {
       if (c < H) gm.keep(gamma + c);
       gm.floats(g);
       mul_all(s[j], g);
-      store_mx8<VW>(s[j], inv, c < cols, c % kMxGroup == 0, a.q + at + c, a.scales + row * groups + c / kMxGroup);
+      if constexpr (VW == 8) {
+        store_mx8<VW>(s[j], inv, c < cols, c % kMxGroup == 0, qr + c, scale + c / kMxGroup);
+      } else {
+        const uint32_t b = store_elements<VW>(s[j], inv, c < cols, qr + c);
+        mine = (c0 & 31) == j ? b : mine;
+      }
+    }
+    if constexpr (VW == 1) {
+      const int lane = c0 & 31, c = (c0 & ~31) + lane * step;
+      if (lane < NF && c < cols) scale[c / kMxGroup] = uint8_t(mine);
     }
   }
 }
@@ -744,33 +823,33 @@ cudaError_t by_plan(const RowPlan& p, F f) {
 }  // namespace
 
 cudaError_t launch_quantize_mx8(const QuantizeArgs& a, int, cudaStream_t stream, int* launches) {
-  const int64_t G = mx_groups(a.H), items = a.rows * G;
+  const int64_t G = mx_groups(a.H);
   const bool vec = a.H % 8 == 0 && on(a.x, 16) && on(a.q, 8);
   ++*launches;
   return by_type(a.t, [&](auto tag) {
     using T = decltype(tag);
-    const T* x = static_cast<const T*>(a.x);
-    auto run = [&](auto kernel, int per_block) {
-      return launch(kernel, dim3(unsigned((items + per_block - 1) / per_block)), dim3(kRowThreads), 0, stream, x, a.q,
-                    a.scales, items, uint32_t(a.H), uint32_t(G));
+    auto run = [&](auto kernel, int64_t items, int per_block) {
+      return launch(kernel, dim3(unsigned((items + per_block - 1) / per_block)), dim3(kRowThreads), 0, stream,
+                    static_cast<const T*>(a.x), a.q, a.scales, items, uint32_t(a.H), uint32_t(G));
     };
-    return vec ? run(k_quantize<T, 8, 4>, kRowThreads / 4 * 4) : run(k_quantize<T, 1, 8>, kRowThreads / 32 * 8);
+    if (!vec && G < 4) return run(k_quantize<T, 1, 8>, a.rows * G, kRowThreads / 4);
+    return vec ? run(k_quantize<T, 8, 4>, a.rows * G, kRowThreads)
+               : run(k_quantize_ragged<T>, a.rows * ((G + 7) / 8), kRowThreads / 32);
   });
 }
 
 cudaError_t launch_dequantize_pitched(DType t, const uint8_t* q, const uint8_t* scales, void* y, int64_t rows,
                                       int64_t n, int64_t ld, int, cudaStream_t stream, int* launches) {
   const bool vec = n % 8 == 0 && ld % 8 == 0 && on(q, 8) && on(y, 16);
-  const int64_t items = rows * (vec ? ld / 8 : ld);
-  const int per_block = kRowThreads * 4;
   ++*launches;
   return by_type(t, [&](auto tag) {
     using T = decltype(tag);
-    auto run = [&](auto kernel) {
+    auto run = [&](auto kernel, int64_t items, int per_block) {
       return launch(kernel, dim3(unsigned((items + per_block - 1) / per_block)), dim3(kRowThreads), 0, stream, q,
                     scales, static_cast<T*>(y), items, uint32_t(n), uint32_t(mx_groups(n)), uint32_t(ld));
     };
-    return vec ? run(k_dequantize<T, 8, 4>) : run(k_dequantize<T, 1, 4>);
+    return vec ? run(k_dequantize<T, 4>, rows * (ld / 8), kRowThreads * 4)
+               : run(k_dequantize_ragged<T>, rows * ((ld + 255) / 256), kRowThreads / 32);
   });
 }
 
