@@ -265,7 +265,7 @@ __device__ __forceinline__ void turn_units(uint8_t* buf, U* g, int64_t row0, int
                                            int lane) {
   constexpr int PER = 16 / sizeof(U), N = NC * PER;
   const int high = int(min(rows - row0, int64_t(32)));
-#pragma unroll
+#pragma unroll 1
   for (int l0 = 0; l0 < N; l0 += 32) {
     const int l = l0 + lane;
     const bool in = l < N && col0 + l < cols;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void pair_chunk(const Epilogue& e, uint8_t* buf, floa
   for (int h = 0; h < CW / 32; ++h) {
     float z[32];
     load(h, z);
-    by_act(e.act, [&](auto tag) {
+    if (e.act != kActNone) by_act(e.act, [&](auto tag) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) z[i] = act_value<decltype(tag)::value>(z[i], e.alpha);
     });
@@ -614,18 +614,22 @@ __device__ __forceinline__ void put_out(T* p, const float (&z)[VW]) {
 
 // The sums of a CTA's share of the rows, over the cluster's ranks in their order, and
 // its outputs.  A thread has VW columns (8 where rows start on 16-byte boundaries,
-// else 1: then a warp writes 32 neighbours) of U rows at a time, whose loads are
-// issued together; the columns of a group of 32 belong to 32 / VW neighbouring lanes.
+// else 1: then a warp writes 32 neighbours) of U rows at a time, with the next U rows'
+// residuals in flight; the columns of a group of 32 belong to 32 / VW neighbouring
+// lanes.  A small loop on purpose: run once and unrolled (16 rows a turn), the
+// instructions' own way from memory took 20 to 30 us.
 template <typename T, int VW, int U>
 __device__ __forceinline__ void finish_rows(const Epilogue& e, const float* sums, int splits, int share, int64_t first,
                                             int64_t n0, bool bad) {
   constexpr int PER_ROW = kSplitN / VW, ROWS = kSplitThreads / PER_ROW;
   const int c = int(threadIdx.x) % PER_ROW * VW;
   const int64_t col = n0 + c, groups = (e.cols + kMxGroup - 1) / kMxGroup;
-  const bool col_in = col < e.cols && !bad;
-  const T* residual = static_cast<const T*>(e.residual);
+  const int left = int(min(int64_t(share), e.rows - first));  // rows that are there
+  const int high = col < e.cols && !bad ? left : 0;           // .. of this thread's columns
+  const T* residual = e.residual != nullptr ? static_cast<const T*>(e.residual) + first * e.cols + col : nullptr;
+  T* y = static_cast<T*>(e.y) + first * e.cols + col;
   float bias[VW] = {};
-  if (e.bias != nullptr && col_in) {
+  if (e.bias != nullptr && col < e.cols) {
     const T* b = static_cast<const T*>(e.bias) + col;
     if (VW == 8 && e.vec_bias) {
       Frag<T, VW> f;
@@ -637,48 +641,58 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const float* sums
       for (int i = 0; i < VW; ++i) bias[i] = to_float(__ldg(b + i));
     }
   }
-  // (all lanes of a warp go through the same number of turns: a shuffle takes them all)
-  for (int r0 = int(threadIdx.x) / 32 * 32 / PER_ROW; r0 < share; r0 += ROWS * U) {
-    const int rt = r0 + int(threadIdx.x) % 32 / PER_ROW;
-    bool in[U];
-    Frag<T, VW> res[U];
-    float z[U][VW];
+  Frag<T, VW> next[U];
+  auto fetch = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = rt + u * ROWS;
-      const int64_t row = first + r;
-      in[u] = col_in && r < share && row < e.rows;
-      if (in[u] && residual != nullptr) res[u].load_stream(residual + row * e.cols + col);
+#pragma unroll
+      for (int i = 0; i < VW; ++i) next[u].v[i] = 0.f;
+      if (residual != nullptr && r0 + u * ROWS < high) next[u].load_stream(residual + int64_t(r0 + u * ROWS) * e.cols);
     }
+  };
+  // (all lanes of a warp go through the same number of turns: a shuffle takes them all)
+  const int mine = int(threadIdx.x) / PER_ROW;
+  fetch(mine);
+#pragma unroll 1
+  for (int t = 0; t < left; t += ROWS * U) {
+    float z[U][VW], res[U][VW];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < VW; ++i) res[u][i] = next[u].v[i];
+    fetch(t + mine + ROWS * U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = rt + u * ROWS;
+      const int r = t + mine + u * ROWS;
       const float* at = sums + r * kSplitN + c;
 #pragma unroll
-      for (int i = 0; i < VW; ++i) z[u][i] = 0.f;
+      for (int i = 0; i < VW; ++i) z[u][i] = bias[i];
       if (r >= share) continue;
+      float f[VW] = {};
+#pragma unroll 1
       for (int s = 0; s < splits; ++s, at += share * kSplitN) {
         if constexpr (VW == 8) {
           const float4 lo = *reinterpret_cast<const float4*>(at), hi = *reinterpret_cast<const float4*>(at + 4);
-          const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[u][i] += f[i];
+          const float g[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          add_pairs(f, g);
         } else {
-          z[u][0] += *at;
+          f[0] += *at;
         }
       }
 #pragma unroll
-      for (int i = 0; i < VW; ++i) z[u][i] += bias[i];
+      for (int i = 0; i < VW; ++i) z[u][i] += f[i];
     }
+    if (e.z != nullptr) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = first + rt + u * ROWS, at = row * e.cols + col;
-      if (e.z != nullptr) {
+      for (int u = 0; u < U; ++u) {
+        const int r = t + mine + u * ROWS;
+        const bool in = r < high;
+        const int64_t row = first + r, at = row * e.cols + col;
         if (e.z_scales == nullptr) {
-          if (in[u]) put_out<T, VW>(static_cast<T*>(e.z) + at, z[u]);
+          if (in) put_out<T, VW>(static_cast<T*>(e.z) + at, z[u]);
         } else {
           float amax = 0.f;
-          if (in[u]) {
+          if (in) {
 #pragma unroll
             for (int i = 0; i < VW; ++i) amax = fmaxf(amax, fabsf(z[u][i]));
           }
@@ -686,7 +700,7 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const float* sums
           for (int o = 16 / VW; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           const uint32_t b = mx_scale(amax);
           const float k = mx_factor(b);
-          if (in[u]) {
+          if (in) {
             uint8_t* p = static_cast<uint8_t*>(e.z) + at;
             if constexpr (VW == 8)
               *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(z[u][0] * k, z[u][1] * k, z[u][2] * k, z[u][3] * k),
@@ -698,20 +712,19 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const float* sums
         }
       }
     }
-    by_act(e.act, [&](auto tag) {
+    if (e.act != kActNone)
+      by_act(e.act, [&](auto tag) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < VW; ++i) z[u][i] = act_value<decltype(tag)::value>(z[u][i], e.alpha);
-    });
+          for (int i = 0; i < VW; ++i) z[u][i] = act_value<decltype(tag)::value>(z[u][i], e.alpha);
+      });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!in[u]) continue;
-      if (residual != nullptr) {
+      const int r = t + mine + u * ROWS;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) z[u][i] += res[u].v[i];
-      }
-      put_out<T, VW>(static_cast<T*>(e.y) + (first + rt + u * ROWS) * e.cols + col, z[u]);
+      for (int i = 0; i < VW; ++i) z[u][i] += res[u][i];
+      if (r < high) put_out<T, VW>(y + int64_t(r) * e.cols, z[u]);
     }
   }
 }
@@ -896,8 +909,8 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
   bool bad = false;
   for (uint32_t s = 0; s < splits; ++s) bad |= (splits > 1 ? failed[s] : failed_here) != 0;
   const int64_t first = m0 + int64_t(rank) * share;
-  if (a.epi.vec) finish_rows<T, 8, 2>(a.epi, sums, int(splits), share, first, n0, bad);
-  else finish_rows<T, 1, 16>(a.epi, sums, int(splits), share, first, n0, bad);
+  if (a.epi.vec) finish_rows<T, 8, 1>(a.epi, sums, int(splits), share, first, n0, bad);
+  else finish_rows<T, 1, 4>(a.epi, sums, int(splits), share, first, n0, bad);
 }
 
 // ---------------------------------------------------------------------------
