@@ -155,6 +155,9 @@ constexpr int kPairThreads = (4 + kEpiWarps) * 32;
 constexpr int kStaging = 4096;             // bytes an epilogue warp has to turn rows around
 constexpr int kRaster = 8;                 // tiles of rows that are walked together
 
+constexpr int kScaleColumns = 12;          // of tensor memory, for a K tile's scales
+constexpr int kScaleSets = 8;              // K tiles whose scales are there
+
 template <bool MX, int TN> struct PairShape {
   static constexpr int kTileN = TN;
   static constexpr int kHalfN = kTileN / 2;
@@ -162,8 +165,6 @@ template <bool MX, int TN> struct PairShape {
   static constexpr int kStageBytes = kOperandM + kOperandN;
   static constexpr int kQBlocks = (TN + 127) / 128;
   static constexpr int kScaleBytes = MX ? 512 * (1 + kQBlocks) : 0;  // R's 128 rows and Q's
-  [[maybe_unused]] static constexpr int kScaleColumns = 12;                // of tensor memory
-  [[maybe_unused]] static constexpr int kScaleSets = 8;                    // K tiles whose scales are there
   static constexpr int kStages = TN == 128 ? 7 : MX ? 6 : 5;
   static constexpr int kChunk = TN == 192 ? 32 : 64;              // columns that a warp turns around at once
   static constexpr int kBarriers = 2 * kStages + 5;
@@ -171,7 +172,7 @@ template <bool MX, int TN> struct PairShape {
                                kBarriers * 8 + 16;
 };
 
-struct PairArgs {
+struct PairProduct {
   CUtensorMap r, q;
   CUtensorMap rs, qs;    // 8-bit: blocks of scales as k_arrange left them, by tile and K tile
   Epilogue epi;
@@ -180,6 +181,15 @@ struct PairArgs {
   int k_tile;            // elements
   bool r_mn, q_mn;
   uint32_t idesc;
+};
+
+// One product, or (TWO) two of the same kind whose tiles are walked one after the other:
+// the two of a gradient, whose last tiles then leave SMs idle once, not twice (bf16
+// 4096 x 1024 x 4096: 44 us for 50).  A kernel of its own: the choice of a tile's
+// product costs one product alone (mx8 8192 x 4096 x 8192 182 us for 174).
+struct PairArgs {
+  PairProduct p[2];
+  int64_t first, tiles;  // tiles of p[0], and of both
 };
 
 // Row-major scales to the blocks of 512 bytes that tensor memory takes, for the pair
@@ -413,7 +423,7 @@ __device__ __forceinline__ void tile_place(int64_t t, int64_t tiles_m, int64_t t
 // CTA's), `taken` (the first CTA's: all epilogue warps of both).  A wait that
 // runs out ends its role; the others run out in turn, copies in flight are waited
 // for, and the CTAs leave together.
-template <typename T, bool MX, int TN>
+template <typename T, bool MX, int TN, bool TWO>
 __global__ void __launch_bounds__(kPairThreads, 1)
 k_mm_pair(const __grid_constant__ PairArgs a) {
   using S = PairShape<MX, TN>;
@@ -442,8 +452,8 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
     }
     mbar_init(drained, 1);
     mbar_init_fence();
-    prefetch_map(&a.r);
-    prefetch_map(&a.q);
+    prefetch_map(&a.p[0].r);
+    prefetch_map(&a.p[0].q);
   }
   if (warp == 3) tmem_alloc<true>(tmem_at, 512);
   __syncwarp();
@@ -454,18 +464,19 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
   pdl_wait();
   pdl_trigger();
 
-  const int64_t tiles = a.tiles_m * a.tiles_n, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-  const bool r_mn = !MX && a.r_mn, q_mn = !MX && a.q_mn;
+  const int64_t tiles = a.tiles, pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   if (warp == 0) {
     Ring ring(S::kStages);
     int issued = 0;
     bool ok = true;
     for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
+      const bool r_mn = !MX && p.r_mn, q_mn = !MX && p.q_mn;
       int64_t tm, tn;
-      tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+      tile_place(TWO && t >= a.first ? t - a.first : t, p.tiles_m, p.tiles_n, &tm, &tn);
       const int m = int(tm * kTileM) + int(rank) * kHalfM, n = int(tn * S::kTileN) + int(rank) * S::kHalfN;
-      const int rs = int((tm * 2 + rank) * a.k_tiles), qs = int(tn * a.k_tiles);
-      for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
+      const int rs = int((tm * 2 + rank) * p.k_tiles), qs = int(tn * p.k_tiles);
+      for (int k = 0; k < p.k_tiles; ++k, ring.next()) {
         if (issued >= S::kStages && !warp_wait(empty + ring.st, ring.phase ^ 1)) {
           ok = false;
           break;
@@ -473,23 +484,23 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
         const uint32_t bar = cluster_addr(smem_addr(full + ring.st), 0);
         const uint32_t dst = smem_addr(smem + ring.st * S::kStageBytes);
         const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
-        const int kk = k * a.k_tile;
+        const int kk = k * p.k_tile;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full + ring.st, 2 * (S::kStageBytes + S::kScaleBytes));
           // an MN-major operand comes 64 rows at a time, a K-major one in as many boxes of 64 rows
 #pragma unroll
           for (int c = 0; c < kHalfM / 64; ++c)
-            tma_load<true>(dst + c * 8192, &a.r, bar, r_mn ? m + 64 * c : kk, r_mn ? kk : m + 64 * c);
+            tma_load<true>(dst + c * 8192, &p.r, bar, r_mn ? m + 64 * c : kk, r_mn ? kk : m + 64 * c);
           if constexpr (S::kHalfN % 64 == 0) {
 #pragma unroll
             for (int c = 0; c < S::kHalfN / 64; ++c)
-              tma_load<true>(dst + kOperandM + c * 8192, &a.q, bar, q_mn ? n + 64 * c : kk, q_mn ? kk : n + 64 * c);
+              tma_load<true>(dst + kOperandM + c * 8192, &p.q, bar, q_mn ? n + 64 * c : kk, q_mn ? kk : n + 64 * c);
           } else {
-            tma_load<true>(dst + kOperandM, &a.q, bar, kk, n);
+            tma_load<true>(dst + kOperandM, &p.q, bar, kk, n);
           }
           if constexpr (MX) {
-            tma_load<true>(sf, &a.rs, bar, 0, rs + k);
-            tma_load<true>(sf + 512, &a.qs, bar, 0, qs + k);
+            tma_load<true>(sf, &p.rs, bar, 0, rs + k);
+            tma_load<true>(sf + 512, &p.qs, bar, 0, qs + k);
           }
         }
         __syncwarp();
@@ -509,8 +520,12 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
       uint32_t set = 0;
       bool ok = true;
       int64_t i = 0;
-      const uint64_t rstep = operand_step(r_mn), qstep = operand_step(q_mn);
       for (int64_t t = pair; t < tiles && ok; t += pairs, ++i) {
+        const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
+        const bool r_mn = !MX && p.r_mn, q_mn = !MX && p.q_mn;
+        const uint64_t rstep = operand_step(r_mn), qstep = operand_step(q_mn);
+        const uint32_t idesc = p.idesc;
+        const int k_tiles = p.k_tiles;
         const int acc = int(i & 1);
         if (i >= 2 && !warp_wait(taken + acc, uint32_t((i >> 1) - 1) & 1)) {
           ok = false;
@@ -518,7 +533,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
         }
         tmem_fence_after();
         const uint32_t d = tmem + acc * S::kTileN;
-        for (int k = 0; k < a.k_tiles; ++k, ring.next()) {
+        for (int k = 0; k < k_tiles; ++k, ring.next()) {
           if (!warp_wait(full + ring.st, ring.phase)) {
             ok = false;
             break;
@@ -530,22 +545,22 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
             if constexpr (MX) {
               // in turn to the columns of kScaleSets sets, so that the copies need not wait for products in flight
               const uint32_t sf = smem_addr(scales + ring.st * S::kScaleBytes);
-              const uint32_t sfr = tmem + 2 * S::kTileN + set * S::kScaleColumns, sfq = sfr + 4;
+              const uint32_t sfr = tmem + 2 * S::kTileN + set * kScaleColumns, sfq = sfr + 4;
               copy_scales<true>(sfr, scales_desc(sf));
               copy_scales<true>(sfq, scales_desc(sf + 512));
               if constexpr (S::kQBlocks == 2) copy_scales<true>(sfq + 4, scales_desc(sf + 1024));
 #pragma unroll
               for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep)
-                mma_mx8<true>(d, rd, qd, a.idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
+                mma_mx8<true>(d, rd, qd, idesc | mma_scale_byte(j), sfr, sfq, (k | j) != 0);
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<true>(d, rd, qd, a.idesc, (k | j) != 0);
+              for (int j = 0; j < 4; ++j, rd += rstep, qd += qstep) mma_f16<true>(d, rd, qd, idesc, (k | j) != 0);
             }
             mma_commit<true>(empty + ring.st);
-            if (k + 1 == a.k_tiles) mma_commit<true>(ready + acc);
+            if (k + 1 == k_tiles) mma_commit<true>(ready + acc);
           }
           __syncwarp();
-          set = (set + 1) % S::kScaleSets;
+          set = (set + 1) % kScaleSets;
         }
       }
       if (!ok) {  // products in flight end before the tensor memory is given back
@@ -562,12 +577,13 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
       const int acc = int(i & 1);
       if (!mbar_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
       tmem_fence_after();
+      const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
       int64_t tm, tn;
-      tile_place(t, a.tiles_m, a.tiles_n, &tm, &tn);
+      tile_place(TWO && t >= a.first ? t - a.first : t, p.tiles_m, p.tiles_n, &tm, &tn);
       const int64_t row0 = tm * kTileM + rank * kHalfM + 32 * (w & 3);
       const uint32_t at = tmem + acc * S::kTileN + (uint32_t(32 * (w & 3)) << 16);
       for (int c = (w >> 2) * S::kHalfN; c < ((w >> 2) + 1) * S::kHalfN; c += S::kChunk)
-        pair_chunk<T, S::kChunk>(a.epi, buf, bias + w * 64, at + c, row0, tn * S::kTileN + c, lane);
+        pair_chunk<T, S::kChunk>(p.epi, buf, bias + w * 64, at + c, row0, tn * S::kTileN + c, lane);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(taken + acc), 0));
@@ -962,7 +978,7 @@ template <typename T, int VW, int ZM>
 __global__ void __launch_bounds__(kSlopeThreads, 3)
 k_act_slope(const T* __restrict__ dy, const void* __restrict__ zp, const uint8_t* __restrict__ z_scales,
             T* __restrict__ dz, int64_t rows, int64_t cols, int64_t ld, int64_t rows_per_chunk, int act, float alpha,
-            float* __restrict__ partial) {
+            float* __restrict__ partial, T* __restrict__ dbias) {
   constexpr int U = 2;
   __shared__ float part[8][32][VW + 1];
   pdl_wait();
@@ -1050,7 +1066,7 @@ k_act_slope(const T* __restrict__ dy, const void* __restrict__ zp, const uint8_t
       }
     }
   });
-  if (partial == nullptr) return;
+  if (partial == nullptr && dbias == nullptr) return;
 #pragma unroll
   for (int e = 0; e < VW; ++e) part[warp][lane][e] = sum[e];
   __syncthreads();
@@ -1060,7 +1076,8 @@ k_act_slope(const T* __restrict__ dy, const void* __restrict__ zp, const uint8_t
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += part[w][i / VW][i % VW];
-    partial[int64_t(blockIdx.y) * cols + col] = v;
+    if (dbias != nullptr) st1_stream(dbias + col, v);  // one chunk: these are the sums
+    else partial[int64_t(blockIdx.y) * cols + col] = v;
   }
 }
 
@@ -1247,20 +1264,19 @@ int64_t arranged_bytes(int64_t rows, int64_t cols, int64_t k_tiles, int tile_n) 
   return (2 * tiles_of(rows, kTileM) + tiles_of(cols, tile_n) * ((tile_n + 127) / 128)) * k_tiles * 512;
 }
 
-template <typename T, bool MX, int TN>
-cudaError_t product_pair(DType t, const Operand& r, const Operand& q, const Epilogue& epi, int64_t k_tiles, int k_tile,
-                         uint8_t* ws, int sm_count, cudaStream_t stream, int* launches) {
+template <bool MX, int TN>
+cudaError_t fill_pair(PairProduct* a, DType t, const Operand& r, const Operand& q, const Epilogue& epi, int64_t k_tiles,
+                      uint8_t* ws, int sm_count, cudaStream_t stream, int* launches) {
   using S = PairShape<MX, TN>;
-  PairArgs a = {};
   cudaError_t e;
-  if ((e = make_map(&a.r, t, MX, r, 64)) != cudaSuccess) return e;
-  if ((e = make_map(&a.q, t, MX, q, S::kHalfN % 64 == 0 ? 64 : S::kHalfN)) != cudaSuccess) return e;
-  a.tiles_m = tiles_of(r.rows, kTileM);
-  a.tiles_n = tiles_of(q.rows, TN);
+  if ((e = make_map(&a->r, t, MX, r, 64)) != cudaSuccess) return e;
+  if ((e = make_map(&a->q, t, MX, q, S::kHalfN % 64 == 0 ? 64 : S::kHalfN)) != cudaSuccess) return e;
+  a->tiles_m = tiles_of(r.rows, kTileM);
+  a->tiles_n = tiles_of(q.rows, TN);
   if constexpr (MX) {
     ArrangeArgs g = {};
     g.s[0] = scale_rows(r), g.s[1] = scale_rows(q);
-    g.tiles[0] = 2 * a.tiles_m, g.tiles[1] = a.tiles_n;
+    g.tiles[0] = 2 * a->tiles_m, g.tiles[1] = a->tiles_n;
     g.rows[0] = kHalfM, g.rows[1] = TN;
     g.blocks[0] = 1, g.blocks[1] = S::kQBlocks;
     g.k_tiles = int(k_tiles);
@@ -1270,19 +1286,38 @@ cudaError_t product_pair(DType t, const Operand& r, const Operand& q, const Epil
     e = launch(k_arrange, dim3(unsigned(std::min<int64_t>((warps + 7) / 8, 8 * sm_count))), dim3(256), 0, stream, g);
     if (e != cudaSuccess) return e;
     ++*launches;
-    if ((e = make_scale_map(&a.rs, g.out[0], g.tiles[0] * k_tiles, 128)) != cudaSuccess) return e;
-    if ((e = make_scale_map(&a.qs, g.out[1], g.tiles[1] * k_tiles, 128 * S::kQBlocks)) != cudaSuccess) return e;
+    if ((e = make_scale_map(&a->rs, g.out[0], g.tiles[0] * k_tiles, 128)) != cudaSuccess) return e;
+    if ((e = make_scale_map(&a->qs, g.out[1], g.tiles[1] * k_tiles, 128 * S::kQBlocks)) != cudaSuccess) return e;
   }
-  a.epi = epi;
-  a.k_tiles = int(k_tiles);
-  a.k_tile = k_tile;
-  a.r_mn = r.mn;
-  a.q_mn = q.mn;
-  a.idesc = MX ? mma_desc_mx8(kTileM, TN) : mma_desc_f16(t == DType::BF16, r.mn, q.mn, kTileM, TN);
+  a->epi = epi;
+  a->k_tiles = int(k_tiles);
+  a->k_tile = MX ? 128 : 64;
+  a->r_mn = r.mn;
+  a->q_mn = q.mn;
+  a->idesc = MX ? mma_desc_mx8(kTileM, TN) : mma_desc_f16(t == DType::BF16, r.mn, q.mn, kTileM, TN);
+  return cudaSuccess;
+}
+
+template <typename T, bool MX, int TN, bool TWO>
+cudaError_t launch_pair(PairArgs* a, int sm_count, cudaStream_t stream, int* launches) {
+  using S = PairShape<MX, TN>;
+  constexpr auto kernel = k_mm_pair<T, MX, TN, TWO>;
+  a->first = a->p[0].tiles_m * a->p[0].tiles_n;
+  a->tiles = a->first + (TWO ? a->p[1].tiles_m * a->p[1].tiles_n : 0);
   int pairs = 1;
-  if ((e = resident_pairs(k_mm_pair<T, MX, TN>, kPairThreads, S::kSmem, sm_count, &pairs)) != cudaSuccess) return e;
-  return launch_cluster(k_mm_pair<T, MX, TN>, unsigned(2 * std::min<int64_t>(a.tiles_m * a.tiles_n, pairs)),
-                        kPairThreads, S::kSmem, 2, stream, a);
+  cudaError_t e = resident_pairs(kernel, kPairThreads, S::kSmem, sm_count, &pairs);
+  if (e != cudaSuccess) return e;
+  e = launch_cluster(kernel, unsigned(2 * std::min<int64_t>(a->tiles, pairs)), kPairThreads, S::kSmem, 2, stream, *a);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+template <typename T, bool MX, int TN>
+cudaError_t product_pair(DType t, const Operand& r, const Operand& q, const Epilogue& epi, int64_t k_tiles, uint8_t* ws,
+                         int sm_count, cudaStream_t stream, int* launches) {
+  PairArgs a = {};
+  const cudaError_t e = fill_pair<MX, TN>(&a.p[0], t, r, q, epi, k_tiles, ws, sm_count, stream, launches);
+  return e != cudaSuccess ? e : launch_pair<T, MX, TN, false>(&a, sm_count, stream, launches);
 }
 
 template <typename T, bool MX>
@@ -1292,36 +1327,50 @@ cudaError_t product(DType t, const Operand& r, const Operand& q, const Epilogue&
   const int k_tile = MX ? 128 : 64;
   const int64_t k_tiles = tiles_of(r.depth, k_tile);
   const Plan p = plan_product(MX, r.rows, q.rows, k_tiles, r.mn);
+  if (p.tile_n != 0)
+    return p.tile_n == kWide ? product_pair<T, MX, kWide>(t, r, q, epi, k_tiles, ws, sm_count, stream, launches)
+                             : product_pair<T, MX, 128>(t, r, q, epi, k_tiles, ws, sm_count, stream, launches);
   cudaError_t e;
-  if (p.tile_n != 0) {
-    e = p.tile_n == kWide ? product_pair<T, MX, kWide>(t, r, q, epi, k_tiles, k_tile, ws, sm_count, stream, launches)
-                          : product_pair<T, MX, 128>(t, r, q, epi, k_tiles, k_tile, ws, sm_count, stream, launches);
-  } else {
-    SplitArgs a = {};
-    if (k_tiles > 0) {
-      if ((e = make_map(&a.r, t, MX, r, std::min(p.tile_m, 64))) != cudaSuccess) return e;
-      if ((e = make_map(&a.q, t, MX, q, 64)) != cudaSuccess) return e;
-    }
-    if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
-    a.epi = epi;
-    a.tiles_m = tiles_of(r.rows, p.tile_m);
-    a.tile_m = p.tile_m;
-    a.k_tiles = int(k_tiles);
-    a.k_tile = k_tile;
-    a.r_mn = r.mn;
-    a.q_mn = q.mn;
-    const int stage = kOperandQ + p.tile_m * kLine, quads = MX ? kScaleQuads * kSplitQuadBytes : 0;
-    const int sums = p.splits > 1 && p.tile_m <= 64 ? p.tile_m * kSplitN * 4 : 0;
-    a.sums_apart = sums > 0;
-    a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024 - quads - sums) / stage);
-    a.idesc = MX ? mma_desc_mx8(kSplitN, p.tile_m) : mma_desc_f16(t == DType::BF16, q.mn, r.mn, kSplitN, p.tile_m);
-    const int64_t grid = a.tiles_m * tiles_of(q.rows, kSplitN) * p.splits;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads, size_t(1024) + size_t(a.stages) * stage + quads + sums,
-                       unsigned(p.splits), stream, a);
+  SplitArgs a = {};
+  if (k_tiles > 0) {
+    if ((e = make_map(&a.r, t, MX, r, std::min(p.tile_m, 64))) != cudaSuccess) return e;
+    if ((e = make_map(&a.q, t, MX, q, 64)) != cudaSuccess) return e;
   }
+  if (MX) a.rs = scale_rows(r), a.qs = scale_rows(q);
+  a.epi = epi;
+  a.tiles_m = tiles_of(r.rows, p.tile_m);
+  a.tile_m = p.tile_m;
+  a.k_tiles = int(k_tiles);
+  a.k_tile = k_tile;
+  a.r_mn = r.mn;
+  a.q_mn = q.mn;
+  const int stage = kOperandQ + p.tile_m * kLine, quads = MX ? kScaleQuads * kSplitQuadBytes : 0;
+  const int sums = p.splits > 1 && p.tile_m <= 64 ? p.tile_m * kSplitN * 4 : 0;
+  a.sums_apart = sums > 0;
+  a.stages = std::min(kSplitMostStages, (kSplitBudget - 1024 - quads - sums) / stage);
+  a.idesc = MX ? mma_desc_mx8(kSplitN, p.tile_m) : mma_desc_f16(t == DType::BF16, q.mn, r.mn, kSplitN, p.tile_m);
+  const int64_t grid = a.tiles_m * tiles_of(q.rows, kSplitN) * p.splits;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  e = launch_cluster(k_mm_split<T, MX>, unsigned(grid), kSplitThreads,
+                     size_t(1024) + size_t(a.stages) * stage + quads + sums, unsigned(p.splits), stream, a);
   if (e == cudaSuccess) ++*launches;
   return e;
+}
+
+// A gradient's two products in one launch, where both take the pair kernel with tiles
+// of one width; the deeper one's tiles first.
+template <typename T, int TN>
+cudaError_t pair_of_products(DType t, const Operand* const (&o)[2][2], const Epilogue (&epi)[2], int sm_count,
+                             cudaStream_t stream, int* launches) {
+  PairArgs a = {};
+  const int deep = o[1][0]->depth > o[0][0]->depth ? 1 : 0;
+  for (int i = 0; i < 2; ++i) {
+    const int j = i == 0 ? deep : 1 - deep;
+    const cudaError_t e = fill_pair<false, TN>(&a.p[i], t, *o[j][0], *o[j][1], epi[j], tiles_of(o[j][0]->depth, 64), nullptr,
+                                               sm_count, stream, launches);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pair<T, false, TN, true>(&a, sm_count, stream, launches);
 }
 
 cudaError_t product(DType t, bool mx8, const Operand& r, const Operand& q, const Epilogue& epi, uint8_t* ws, int sm_count,
@@ -1370,10 +1419,10 @@ struct Pitcher {
 };
 
 // Row chunks of k_act_slope: as many blocks as the device holds (three an SM) at once,
-// 32 rows at least.
+// 64 rows at least (so that few rows have one chunk, whose sums are dbias).
 int64_t slope_chunks(int64_t M, int64_t N) {
   const int64_t tiles = std::max<int64_t>(1, (N + 255) / 256);
-  return std::max<int64_t>(1, std::min({3 * kPlanSms / tiles, (M + 31) / 32, int64_t(65535)}));
+  return std::max<int64_t>(1, std::min({3 * kPlanSms / tiles, (M + 63) / 64, int64_t(65535)}));
 }
 
 template <typename T>
@@ -1386,14 +1435,14 @@ cudaError_t act_slope_rows(const MatmulGradArgs& a, T* dz, int64_t ld, float* pa
   auto run = [&](auto kernel, int vw) {
     return launch(kernel, dim3(unsigned((width + 32 * vw - 1) / (32 * vw)), unsigned(used)), dim3(kSlopeThreads), 0,
                   stream, static_cast<const T*>(a.dy), a.z, a.z_scales, dz, a.M, a.N, width, per, a.act, a.alpha,
-                  partial);
+                  used > 1 ? partial : nullptr, used == 1 ? static_cast<T*>(a.dbias) : nullptr);
   };
   cudaError_t e;
   if (vec) e = zm == 0 ? run(k_act_slope<T, 8, 0>, 8) : zm == 1 ? run(k_act_slope<T, 8, 1>, 8) : run(k_act_slope<T, 8, 2>, 8);
   else e = zm == 0 ? run(k_act_slope<T, 1, 0>, 1) : zm == 1 ? run(k_act_slope<T, 1, 1>, 1) : run(k_act_slope<T, 1, 2>, 1);
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (partial == nullptr) return cudaSuccess;
+  if (partial == nullptr || used == 1) return cudaSuccess;
   e = launch(k_channel_sums<T>, dim3(unsigned(std::min<int64_t>((a.N + 31) / 32, 65535))), dim3(kSumsThreads), 0,
              stream, static_cast<const float*>(partial), used, int64_t(1), a.N, 1, static_cast<T*>(a.dbias),
              static_cast<T*>(nullptr));
@@ -1482,13 +1531,25 @@ cudaError_t launch_matmul_grad(const MatmulGradArgs& a, int sm_count, cudaStream
     }
   }
   if ((e = pitch.run(sm_count, stream, launches)) != cudaSuccess) return e;
-  auto plain = [&](const Operand& r, const Operand& q, void* y) {
+  auto plain = [](const Operand& r, const Operand& q, void* y) {
     Epilogue epi{nullptr, nullptr, y, nullptr, nullptr, r.rows, q.rows, kActNone, 0.f, false, false, false};
     set_access(&epi);
-    return product(a.t, false, r, q, epi, nullptr, sm_count, stream, launches);
+    return epi;
   };
-  if (da) e = plain(ra, qa, a.da);
-  if (dw && e == cudaSuccess) e = plain(rw, qw, a.dw);
+  const Epilogue epi[2] = {plain(ra, qa, a.da), plain(rw, qw, a.dw)};
+  if (da && dw) {
+    const int width = plan_product(false, ra.rows, qa.rows, tiles_of(ra.depth, 64), false).tile_n;
+    if (width != 0 && width == plan_product(false, rw.rows, qw.rows, tiles_of(rw.depth, 64), true).tile_n) {
+      const Operand* const o[2][2] = {{&ra, &qa}, {&rw, &qw}};
+      if (a.t == DType::F16)
+        return width == 256 ? pair_of_products<__half, 256>(a.t, o, epi, sm_count, stream, launches)
+                            : pair_of_products<__half, 128>(a.t, o, epi, sm_count, stream, launches);
+      return width == 256 ? pair_of_products<__nv_bfloat16, 256>(a.t, o, epi, sm_count, stream, launches)
+                          : pair_of_products<__nv_bfloat16, 128>(a.t, o, epi, sm_count, stream, launches);
+    }
+  }
+  if (da) e = product(a.t, false, ra, qa, epi[0], nullptr, sm_count, stream, launches);
+  if (dw && e == cudaSuccess) e = product(a.t, false, rw, qw, epi[1], nullptr, sm_count, stream, launches);
   return e;
 }
 
