@@ -1,4 +1,6 @@
 """The matrix product with its epilogue, and its gradient, against the float64 oracle."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -215,3 +217,45 @@ def test_grad_parts_and_empty_sums(lib):
     assert da.shape == (0, 24) and not dw.any() and not db.any()
     da, dw, db = lib.ep_matmul_bias_act_grad(dy[:, :0].contiguous(), a, w[:0], dA=torch.full_like(a, float("nan")), dbias=True)
     assert not da.any() and dw.shape == (0, 24) and db.shape == (0,)
+
+
+# dW's sums run over M, dA's over N: few tiles of long sums beside many of short ones
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("mnk", [(16384, 384, 384), (8200, 768, 768), (10000, 520, 264), (600, 9000, 640), (9001, 301, 299),
+                                 (4096, 4096, 256)], ids=str)
+def test_grad_long_sums(lib, mnk, dtype):
+    backward(lib, *mnk, dtype)
+
+
+@pytest.mark.parametrize("mnk", [(768, 768, 4096), (300, 301, 9992), (1034, 640, 2504)], ids=str)
+def test_long_sums(lib, mnk):
+    forward(lib, *mnk, "f16", "silu")
+
+
+@pytest.mark.parametrize("act", ["none", "quick_gelu"])
+@pytest.mark.parametrize("mnk", [(16384, 768, 768), (2048, 2048, 1024), (600, 9000, 640)], ids=str)
+def test_grad_many_calls(lib, mnk, act):
+    """Calls queued one behind another, from a slow and from a fast host, and replayed: the first's bits."""
+    m, n, k = mnk
+    a, w, b, r = cuda(*product_inputs(m, n, k, "bf16", 9))
+    args = r, a, w, (r if act != "none" else None), act_code(lib, act)
+    first = lib.ep_matmul_bias_act_grad(*args)[:2]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for pause in (0, 20e-6, 60e-6):
+            for _ in range(100):
+                out = lib.ep_matmul_bias_act_grad(*args)[:2]
+                t = time.perf_counter()
+                while time.perf_counter() - t < pause:
+                    pass
+            assert all(torch.equal(x, y) for x, y in zip(out, first))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = [lib.ep_matmul_bias_act_grad(*args)[:2] for _ in range(4)]
+        for _ in range(20):
+            g.replay()
+        s.synchronize()
+        for out in outs:
+            assert all(torch.equal(x, y) for x, y in zip(out, first))
+    assert lib.ep_pipeline_timeouts() == 0
