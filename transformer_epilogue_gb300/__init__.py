@@ -1,6 +1,7 @@
 """GB300-native fused transformer-block epilogue ops (SkipLayerNormalization,
-BiasSoftmax, BiasAdd, QuickGelu, GroupNorm and BiasDropout, the last two with
-their gradients): hand-written sm_103a CUDA kernels behind a C
+BiasSoftmax, BiasAdd, QuickGelu, GroupNorm and BiasDropout, an RMS norm to MX8
+rows and a matrix product with its epilogue, the last four with their
+gradients): hand-written sm_103a CUDA kernels behind a C
 ABI (``include/ep.h``), with a thin ctypes binding."""
 from ._binding import (  # noqa: F401
     DEFAULT_ALPHA, DEFAULT_AXIS, DEFAULT_EPSILON, DEFAULT_GROUP_NORM_EPSILON, EP_ACT_NONE, EP_ACT_SILU,
