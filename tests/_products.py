@@ -11,7 +11,8 @@ plus ``delta``, as in ``_training.py``; u = 2**-24.  The deltas:
   * an activation carries that on with its largest slope, below 1.2, and adds its
     own arithmetic: t is off by four roundings, 4 u |t|, which reaches y = z s(t)
     relatively (weight below 1); 2^x, the sum, 1/x and the product a few ulp, 16 u:
-    (4 |t| + 16) u |y|; gelu: 1 + erf is off by 4 u absolutely: 4 u |z| (+ 16 u |y|).
+    (4 |t| + 16) u |y|; gelu: 1 + erf is off by 4 u absolutely: 4 u |z| (+ 16 u |y|)
+    (Abramowitz and Stegun's 7.1.26 is off by 1.5e-7 = 2.5 u in erf, halved in z (1 + erf) / 2: 1.3 u |z| of it).
     Where s has run down to 0, y is taken as 0: 2**-100 covers it (and subnormals).
   * a slope: below 1.2 and made of at most three terms of that size, each off by
     (4 |t| + 16) u with |t| < 80 where it counts (s (1 - s) |t| < 0.25): 64 u.
