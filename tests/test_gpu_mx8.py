@@ -205,3 +205,36 @@ def test_norm_grad_in_place(lib, shape):
         got = lib.ep_skip_rms_norm_grad(c[0], c[1], g, inv, dsum=c[2], dX=c[i], dbias=True)
         for u, v in zip(want, got):
             assert torch.equal(u, v)
+
+
+# rows that start on no 16-byte boundary: element by element below 8 million elements or 96 a row, else in
+# fragments that are cut at both ends (a row's phase repeats every 8 rows): rows of several slots a block, of whole
+# blocks, and (16378 on) too long for them
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 65), (9, 65), (8, 68), (300, 127), (3000, 66), (77, 132), (601, 1003), (17, 8191),
+                                   (88500, 95), (88000, 97), (84000, 100), (68000, 127),
+                                   (26000, 325), (8500, 1003), (3400, 2525), (2100, 4100), (1700, 5034), (1050, 8191),
+                                   (520, 16377), (520, 16378)], ids=str)
+def test_norm_grad_odd_rows(lib, shape, dtype):
+    grad_case(lib, shape, dtype, 31)
+    if dtype == "f16":
+        grad_case(lib, shape, dtype, 32, dsum=False, dbias=False)
+
+
+@pytest.mark.parametrize("shape", [(9, 65), (68000, 127), (1700, 5034)], ids=str)
+def test_norm_grad_odd_rows_ends(lib, shape):
+    """dX over dY in the middle of a larger tensor: what lies around it stays, and NaN there is not taken in."""
+    h = shape[-1]
+    g = torch.Generator().manual_seed(33)
+    s, ds, dy = (torch.randn(shape, generator=g).half().cuda() for _ in range(3))
+    gamma, inv = torch.ones(h, dtype=torch.float16, device="cuda"), torch.ones(shape[0], 1, device="cuda")
+    want = lib.ep_skip_rms_norm_grad(dy, s, gamma, inv, dsum=ds, dbias=True)
+    n = dy.numel()
+    bufs = [torch.full((n + 32,), float("nan"), dtype=torch.float16, device="cuda") for _ in range(3)]
+    ins = [b[16:16 + n].view(shape) for b in bufs]
+    for t, x in zip(ins, (dy, s, ds)):
+        t.copy_(x)
+    got = lib.ep_skip_rms_norm_grad(ins[0], ins[1], gamma, inv, dsum=ins[2], dX=ins[0], dbias=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for b in bufs:
+        assert b[:16].isnan().all() and b[16 + n:].isnan().all()

@@ -18,6 +18,7 @@
 // Rows too long for the registers are read twice by a block of 512 threads.
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -60,6 +61,13 @@ template <typename T> struct Raw<T, 8> {
   __device__ __forceinline__ void keep(const T* p) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = ld16_keep(reinterpret_cast<const uint4*>(p) + i);
+  }
+  // Elements lo <= e < hi, one by one.
+  __device__ __forceinline__ void part(const T* p, int lo, int hi) {
+    T t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = e >= lo && e < hi ? p[e] : from_float(0.f, T());
+    memcpy(v, t, sizeof(v));
   }
   __device__ __forceinline__ void add_to(float (&f)[8]) const {
     if constexpr (W == 1) {
@@ -506,7 +514,12 @@ k_norm_long(RmsNormArgs a) {
 // As k_norm; each thread adds up its columns, and the block's sums go to `partial`
 // (gridDim.x, H), dbias's behind dgamma's.  AHEAD: the next rows' loads are issued
 // before the present rows' reduction (where registers allow).
-template <typename T, int VW, int NF, bool LONG, bool DB>
+// ODD: rows that start on no 16-byte boundary, in a tensor that does.  A row's fragments
+// begin at the boundary in front of it, and rows 8 apart lie alike, so with steps of
+// 8 rows a thread keeps its columns; those of a fragment that are not in the row, at either
+// end, are left out one by one.  (f16 13331 x 5034: 207 us for 530 element by element, bf16
+// 26577 x 2525 with dbias 147 for 419.)
+template <typename T, int VW, int NF, bool LONG, bool DB, bool ODD>
 __global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, LONG ? 1 : NF * VW <= 4 ? 4 : 2)
 k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
   extern __shared__ float cols_sum[];  // blockDim.y > 1: threads x NF x VW
@@ -519,8 +532,12 @@ k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
   const T* gamma = static_cast<const T*>(a.gamma);
   const T* dsum = static_cast<const T*>(a.dsum);
   T* dx = static_cast<T*>(a.dx);
-  const int H = int(a.H), step = int(blockDim.x) * VW, c0 = int(threadIdx.x) * VW;
   const int64_t rows_step = int64_t(gridDim.x) * blockDim.y;
+  const int H = int(a.H), step = int(blockDim.x) * VW;
+  const int before = ODD ? int((int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * H % (16 / int(sizeof(T)))) : 0;
+  const int c0 = int(threadIdx.x) * VW - before;
+  // (a fragment with columns below 0 or from the row's end on)
+  auto ragged = [&](int c) { return ODD && (c < 0 || c + VW > H); };
 
   Raw<T, VW> gm[NF], ry[NF], rs[NF], rd[NF];
   float dg[NF][VW], db[DB ? NF : 1][VW];
@@ -534,11 +551,17 @@ k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
       ry[j].zero();
       rs[j].zero();
       rd[j].zero();
-      if (c < cols) {
-        ry[j].stream(dy + row * H + c);
-        rs[j].stream(sp + row * H + c);
-        if (dsum != nullptr) rd[j].stream(dsum + row * H + c);
-      }
+      if (c >= cols || (ODD && cols == 0)) continue;
+      if constexpr (ODD)
+        if (ragged(c)) {
+          ry[j].part(dy + row * H + c, -c, H - c);
+          rs[j].part(sp + row * H + c, -c, H - c);
+          if (dsum != nullptr) rd[j].part(dsum + row * H + c, -c, H - c);
+          continue;
+        }
+      ry[j].stream(dy + row * H + c);
+      rs[j].stream(sp + row * H + c);
+      if (dsum != nullptr) rd[j].stream(dsum + row * H + c);
     }
   };
 #pragma unroll
@@ -549,7 +572,9 @@ k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
       dg[j][e] = 0.f;
       if constexpr (DB) db[j][e] = 0.f;
     }
-    if (c0 + j * step < H) gm[j].keep(gamma + c0 + j * step);
+    const int c = c0 + j * step;
+    if constexpr (ODD) gm[j].part(gamma + c, -c, H - c);
+    else if (c < H) gm[j].keep(gamma + c);
   }
   int turn = 0;
   int64_t r0 = int64_t(blockIdx.x) * blockDim.y;
@@ -599,7 +624,16 @@ k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
         if constexpr (VW == 1) db[j][0] += d[0];
         else add_pairs(db[j], d);
       }
-      if (c0 + j * step < cols) store_row<T, VW>(dx + row * H + c0 + j * step, d);
+      const int at = c0 + j * step;
+      if (at >= cols || (ODD && cols == 0)) continue;
+      if constexpr (ODD)
+        if (ragged(at)) {
+#pragma unroll
+          for (int e = 0; e < VW; ++e)
+            if (at + e >= 0 && at + e < H) st1_stream(dx + row * H + at + e, d[e]);
+          continue;
+        }
+      store_row<T, VW>(dx + row * H + at, d);
     }
   }
   if (a.dgamma == nullptr && !DB) return;
@@ -607,6 +641,30 @@ k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
   const int tpr = int(blockDim.x), slots = int(blockDim.y), lane = int(threadIdx.x);
 #pragma unroll
   for (int b = 0; b < (DB ? 2 : 1); ++b) {
+    if constexpr (ODD) {  // the block's rows do not lie alike: by column
+      if (slots > 1) __syncthreads();
+      float* mine = partial + (int64_t(b) * gridDim.x + blockIdx.x) * H;
+      const int width = tpr * NF * VW;
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          float v = dg[j][e];
+          if constexpr (DB) v = b == 0 ? v : db[j][e];
+          const int c = c0 + j * step + e;
+          if (c < 0 || c >= H) continue;
+          if (slots > 1) cols_sum[int(threadIdx.y) * width + c] = v;
+          else mine[c] = v;
+        }
+      if (slots == 1) continue;
+      __syncthreads();
+      for (int c = int(threadIdx.y) * tpr + lane; c < H; c += tpr * slots) {
+        float v = cols_sum[c];
+        for (int r = 1; r < slots; ++r) v += cols_sum[r * width + c];
+        mine[c] = v;
+      }
+      continue;
+    }
     if (slots > 1) {  // the block's rows, added in their order
       __syncthreads();
 #pragma unroll
@@ -707,6 +765,7 @@ bool on(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) 
 struct RowPlan {
   int vw, nf, tpr, slots;  // nf 0: the long form
   bool wide;               // more than kRowThreads threads
+  bool odd;                // fragments of 8 in rows that start on no 16-byte boundary
 };
 
 // Fragments to threads: whole warps, of which as few lanes idle as the fragments a
@@ -731,7 +790,7 @@ void plan_threads(RowPlan* p, int64_t frags, int most_nf, int best_nf) {
 // 8192 x 8192: 76 with four, 104 with two).  The gradient has its column sums in
 // registers too: two, and four where two do not hold the row.
 RowPlan plan_rows(int64_t H, bool vec, bool grad) {
-  RowPlan p{vec ? 8 : 1, 0, 0, 1, false};
+  RowPlan p{vec ? 8 : 1, 0, 0, 1, false, false};
   const int64_t frags = (H + p.vw - 1) / p.vw;
   if (vec && frags <= 16) {
     p.nf = 1;
@@ -745,6 +804,20 @@ RowPlan plan_rows(int64_t H, bool vec, bool grad) {
   if (p.nf == 0) return p;
   p.slots = std::max(1, kRowThreads / p.tpr);
   p.wide = p.tpr > kRowThreads;
+  return p;
+}
+
+// The gradient's rows where the tensors (but not the rows) start on 16-byte boundaries: with up
+// to 7 elements in front, in fragments of 8, from 96 elements a row and 8 million in all on
+// (bf16 65536 x 129: 58 us for 89, f32 40775 x 325 50 for 55; where the elements left out one
+// by one and fewer warps are felt it loses: bf16 65536 x 101 34 for 30, f32 4300 x 1001 27 for 22).
+RowPlan plan_grad_rows(int64_t rows, int64_t H, bool aligned) {
+  RowPlan p = plan_rows(H, aligned && H % 8 == 0, true);
+  if (!aligned || H % 8 == 0 || H < 96 || rows * H < int64_t(8) << 20) return p;
+  const RowPlan odd = plan_rows(H + 7, true, true);
+  if (odd.nf == 0) return p;
+  p = odd;
+  p.odd = true;
   return p;
 }
 
@@ -776,24 +849,29 @@ int64_t grad_blocks(int64_t rows, const RowPlan& p, int es) {
   const int elements = p.nf * p.vw, regs = elements <= 4 ? 64 : elements <= 8 ? 112 : 128;
   const int64_t per_sm = p.wide ? 1 : std::max(1, 65536 / (regs * p.tpr * p.slots));
   const int64_t most = std::max<int64_t>(kPlanSms / 2, rows * es / 16);
-  return std::min({(rows + p.slots - 1) / p.slots, per_sm * kPlanSms, most});
+  const int64_t blocks = std::min({(rows + p.slots - 1) / p.slots, per_sm * kPlanSms, most});
+  return p.odd ? (blocks + 7) / 8 * 8 : blocks;  // (steps of a multiple of 8 rows)
 }
 int64_t grad_chunks(int64_t rows, int64_t H) {
   const int64_t want = std::max<int64_t>(1, 8 * kPlanSms / ((H + 31) / 32));
   return std::max<int64_t>(1, std::min({want, (rows + 31) / 32, int64_t(65535)}));
 }
 
-template <typename T, int VW, int NF, bool LONG, bool DB>
+template <typename T, int VW, int NF, bool LONG, bool DB, bool ODD>
 cudaError_t grad_form(const RmsNormGradArgs& a, const RowPlan& p, cudaStream_t stream) {
   const size_t smem = p.slots > 1 ? size_t(p.tpr) * p.slots * NF * VW * sizeof(float) : 0;
-  return launch(k_norm_grad<T, VW, NF, LONG, DB>, dim3(unsigned(grad_blocks(a.rows, p, dtype_size(a.t)))), dim3(p.tpr, p.slots),
-                smem, stream, a, 1.0f / float(a.H));
+  return launch(k_norm_grad<T, VW, NF, LONG, DB, ODD>, dim3(unsigned(grad_blocks(a.rows, p, dtype_size(a.t)))),
+                dim3(p.tpr, p.slots), smem, stream, a, 1.0f / float(a.H));
 }
 
 template <typename T, int VW, int NF, bool LONG>
 cudaError_t grad_form(const RmsNormGradArgs& a, const RowPlan& p, cudaStream_t stream) {
-  return a.dbias != nullptr ? grad_form<T, VW, NF, LONG, true>(a, p, stream)
-                            : grad_form<T, VW, NF, LONG, false>(a, p, stream);
+  if constexpr (VW == 8)
+    if (p.odd)
+      return a.dbias != nullptr ? grad_form<T, VW, NF, LONG, true, true>(a, p, stream)
+                                : grad_form<T, VW, NF, LONG, false, true>(a, p, stream);
+  return a.dbias != nullptr ? grad_form<T, VW, NF, LONG, true, false>(a, p, stream)
+                            : grad_form<T, VW, NF, LONG, false, false>(a, p, stream);
 }
 
 // f(VW, NF, LONG) of the plan, as constants.
@@ -876,9 +954,8 @@ cudaError_t launch_rms_norm_mx8(const RmsNormArgs& a, int sm_count, cudaStream_t
 
 size_t rms_norm_grad_workspace_bytes(DType t, int64_t rows, int64_t H) {
   size_t most = 0;
-  for (const bool vec : {false, true}) {
-    if (vec && H % 8 != 0) continue;
-    const RowPlan p = plan_rows(H, vec, true);
+  for (const bool aligned : {false, true}) {
+    const RowPlan p = plan_grad_rows(rows, H, aligned);
     const size_t sums = p.nf == 0 ? size_t(grad_chunks(rows, H)) : size_t(grad_blocks(rows, p, dtype_size(t)));
     most = std::max(most, 2 * sums * size_t(H) * 4 + (p.nf == 0 ? (size_t(rows) * 4 + 15) / 16 * 16 : 0));
   }
@@ -886,8 +963,8 @@ size_t rms_norm_grad_workspace_bytes(DType t, int64_t rows, int64_t H) {
 }
 
 cudaError_t launch_rms_norm_grad(const RmsNormGradArgs& a, int sm_count, cudaStream_t stream, int* launches) {
-  const bool vec = a.H % 8 == 0 && on(a.dy, 16) && on(a.s, 16) && on(a.gamma, 16) && on(a.dsum, 16) && on(a.dx, 16);
-  const RowPlan p = plan_rows(a.H, vec, true);
+  const bool aligned = on(a.dy, 16) && on(a.s, 16) && on(a.gamma, 16) && on(a.dsum, 16) && on(a.dx, 16);
+  const RowPlan p = plan_grad_rows(a.rows, a.H, aligned);
   return by_type(a.t, [&](auto tag) {
     using T = decltype(tag);
     float* partial = static_cast<float*>(a.workspace);
