@@ -479,7 +479,7 @@ ep_status ep_skip_rms_norm_mx8(ep_dtype t, const void* input, const int64_t* sha
  * dsum          the gradient that reaches input_skip_bias_sum by other ways (the residual stream), or NULL.
  * dX            the shape of dY; may be dY, s or dsum.
  * dgamma, dbias H elements of T, or NULL: float32 sums of the unrounded values in a fixed
- *               order, rounded once.  Of no rows they are set to 0.
+ *               order, rounded once (float16: infinite from 65520 on).  Of no rows they are set to 0.
  * workspace     ep_skip_rms_norm_grad_workspace_size() bytes, 16-byte aligned; its contents
  *               on entry do not matter.  Calls that may overlap on the GPU need one each.
  *
@@ -549,7 +549,8 @@ size_t ep_matmul_bias_act_workspace_size(int mx8, int64_t M, int64_t N, int64_t 
  * Z             as the forward call left it: (M, N) of T, or with Z_scales in MX8.
  *               Not read (and may be NULL) with EP_ACT_NONE.
  * dA, dW, dbias (M, K), (N, K) and N elements of T, or NULL where not wanted.  dz is rounded
- *               to T in front of the products of dA and dW (not of dbias); sums are float32.
+ *               to T in front of the products of dA and dW (not of dbias); sums are float32,
+ *               rounded once (float16: infinite from 65520 on).
  *               Sums over no rows (M = 0, or N = 0 for dA) are set to 0.
  * workspace     ep_matmul_bias_act_grad_workspace_size() bytes, 16-byte aligned (dz and the
  *               operands that are copied).  Calls that may overlap on the GPU need one each.
