@@ -259,3 +259,29 @@ def test_grad_many_calls(lib, mnk, act):
         for out in outs:
             assert all(torch.equal(x, y) for x, y in zip(out, first))
     assert lib.ep_pipeline_timeouts() == 0
+
+
+@pytest.mark.parametrize("mnk,mx8", [((2048, 2048, 1024), True), ((1300, 1001, 771), True), ((1300, 1001, 771), False),
+                                     ((16, 4096, 4096), True)], ids=str)
+def test_many_calls(lib, mnk, mx8):
+    """The same of the product, with the copies and arranged scales in front of it."""
+    a, w, b, r = cuda(*product_inputs(*mnk, "f16", 10))
+    kw = {}
+    if mx8:
+        (a, sa), (w, sw) = lib.ep_quantize_mx8(a), lib.ep_quantize_mx8(w)
+        kw = dict(A_scales=sa, W_scales=sw, dtype=r.dtype)
+
+    def call():
+        return lib.ep_matmul_bias_act(a, w, b, r, lib.EP_ACT_SILU, Z=E4M3, **kw)
+    first = [x.view(torch.uint8) for x in call()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for pause in (0, 20e-6, 60e-6):
+            for _ in range(200):
+                out = call()
+                t = time.perf_counter()
+                while time.perf_counter() - t < pause:
+                    pass
+            assert all(torch.equal(x.view(torch.uint8), y) for x, y in zip(out, first))
+    assert lib.ep_pipeline_timeouts() == 0
