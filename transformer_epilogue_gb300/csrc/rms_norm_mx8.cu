@@ -150,12 +150,10 @@ __device__ __forceinline__ float sum_all(const float (&f)[VW]) {
   return t;
 }
 
-// MX8 of m * r for a fragment m whose group is held by 32 / VW neighbouring lanes (all
-// of them here; `in`: the fragment lies in the row).  r and the scale's power of two
-// make one factor: the power scales exactly, so (m r) 2^e and m (r 2^e) round alike.
-// Returns the scale's byte.
+// MX8 of a fragment m whose group is held by 32 / VW neighbouring lanes (all of them
+// here; `in`: the fragment lies in the row).  Returns the scale's byte.
 template <int VW>
-__device__ __forceinline__ uint32_t store_elements(float (&m)[VW], float r, bool in, uint8_t* q) {
+__device__ __forceinline__ uint32_t store_elements(float (&m)[VW], bool in, uint8_t* q) {
   float amax;
   if constexpr (VW == 1) {  // magnitudes compare as their bits do; NaN is left out
     const float f = fabsf(m[0]);
@@ -169,8 +167,8 @@ __device__ __forceinline__ uint32_t store_elements(float (&m)[VW], float r, bool
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     amax = fmaxf(amax, 0.f);  // (eight NaN leave a NaN)
   }
-  const uint32_t b = mx_scale(amax * r);
-  scale_all(m, r * mx_factor(b));
+  const uint32_t b = mx_scale(amax);
+  scale_all(m, mx_factor(b));
   if (in) {
     if constexpr (VW == 8)
       __stcs(reinterpret_cast<uint2*>(q), make_uint2(e4m3x4(m[0], m[1], m[2], m[3]), e4m3x4(m[4], m[5], m[6], m[7])));
@@ -180,8 +178,8 @@ __device__ __forceinline__ uint32_t store_elements(float (&m)[VW], float r, bool
   return b;
 }
 template <int VW>
-__device__ __forceinline__ void store_mx8(float (&m)[VW], float r, bool in, bool first, uint8_t* q, uint8_t* scale) {
-  const uint32_t b = store_elements<VW>(m, r, in, q);
+__device__ __forceinline__ void store_mx8(float (&m)[VW], bool in, bool first, uint8_t* q, uint8_t* scale) {
+  const uint32_t b = store_elements<VW>(m, in, q);
   if (in && first) *scale = uint8_t(b);
 }
 
@@ -257,7 +255,7 @@ k_quantize(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict
   for (int u = 0; u < U; ++u) {
     float f[VW];
     raw[u].floats(f);
-    store_mx8<VW>(f, 1.0f, in[u], lane == 0, q + off[u], scales + i0 + u * (kRowThreads / L));
+    store_mx8<VW>(f, in[u], lane == 0, q + off[u], scales + i0 + u * (kRowThreads / L));
   }
 }
 
@@ -290,7 +288,7 @@ k_quantize_ragged(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __r
   for (int u = 0; u < 8; ++u) {
     float f[1];
     raw[u].floats(f);
-    const uint32_t b = store_elements<1>(f, 1.0f, 32u * u + lane < left, qs + 32 * u);
+    const uint32_t b = store_elements<1>(f, 32u * u + lane < left, qs + 32 * u);
     mine = lane == u ? b : mine;
   }
   if (lane < 8 && 32u * lane < left) scales[row * G + seg * 8 + lane] = uint8_t(mine);
@@ -446,11 +444,14 @@ k_norm(const __grid_constant__ RmsNormArgs a, float inv_h) {
       gm.zero();
       if (c < H) gm.keep(gamma + c);
       gm.floats(g);
+      // (s inv) gamma in this order: s inv is at most sqrt(H), whatever s.  (inv taken into the scale's power of two
+      // saved a multiplication in two elements and no time, and was infinite beside groups of 0.)
+      scale_all(s[j], inv);
       mul_all(s[j], g);
       if constexpr (VW == 8) {
-        store_mx8<VW>(s[j], inv, c < cols, c % kMxGroup == 0, qr + c, scale + c / kMxGroup);
+        store_mx8<VW>(s[j], c < cols, c % kMxGroup == 0, qr + c, scale + c / kMxGroup);
       } else {
-        const uint32_t b = store_elements<VW>(s[j], inv, c < cols, qr + c);
+        const uint32_t b = store_elements<VW>(s[j], c < cols, qr + c);
         mine = (c0 & 31) == j ? b : mine;
       }
     }
@@ -500,9 +501,9 @@ k_norm_long(RmsNormArgs a) {
       if (c < a.H) {
         const float s = sum_at(x, skip, bias, row, a.H, c);
         if (sum_out != nullptr) st1_stream(sum_out + row * a.H + c, s);
-        y[0] = s * (inv * to_float(gamma[c]));
+        y[0] = s * inv * to_float(gamma[c]);
       }
-      store_mx8<1>(y, 1.0f, c < a.H, c % kMxGroup == 0, a.q + row * a.H + c, a.scales + row * groups + c / kMxGroup);
+      store_mx8<1>(y, c < a.H, c % kMxGroup == 0, a.q + row * a.H + c, a.scales + row * groups + c / kMxGroup);
     }
   }
 }
