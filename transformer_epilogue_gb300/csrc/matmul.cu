@@ -575,7 +575,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
     int64_t i = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int acc = int(i & 1);
-      if (!mbar_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
+      if (!warp_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
       tmem_fence_after();
       const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
       int64_t tm, tn;
@@ -878,7 +878,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
       if (k0 + 4 * i < k1) ahead.fetch(i, sr, row, int64_t(k0 / 4 + i) * 16);
     Ring ring(kScaleQuads);
     for (int k = k0; k < k1; k += 4, ring.next()) {
-      if (k - k0 >= 4 * kScaleQuads && !mbar_wait(sempty + ring.st, ring.phase ^ 1)) break;
+      if (k - k0 >= 4 * kScaleQuads && !warp_wait(sempty + ring.st, ring.phase ^ 1)) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         ahead.store(i, reinterpret_cast<uint4*>(scales + ring.st * kSplitQuadBytes + 1024 * i + (warp == 2 ? 0 : 512)),
