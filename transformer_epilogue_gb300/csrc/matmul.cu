@@ -35,6 +35,7 @@
 #include "launch_util.h"
 #include "mx8.cuh"
 #include "mx8_internal.h"
+#include "ring_tail.h"
 #include "smem_limit.h"
 #include "umma.cuh"
 
@@ -507,13 +508,10 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
         issued = min(issued + 1, S::kStages);
       }
     }
-    // the last loads (of both CTAs) have landed before anyone leaves
-    if (rank == 0)
-      for (int i = 0; i < issued; ++i) {
-        ring.st = ring.st == 0 ? S::kStages - 1 : ring.st - 1;
-        if (ring.st == S::kStages - 1) ring.phase ^= 1;
-        if (!warp_wait(full + ring.st, ring.phase)) break;
-      }
+    // the last loads (of both CTAs) have landed before anyone leaves, and so have the arrivals that the
+    // last products send to both CTAs' barriers (a load is waited for also behind one that did not land)
+    if (rank == 0) last_uses(ring, issued, [&](int st, uint32_t parity) { return warp_wait(full + st, parity) || true; });
+    last_uses(ring, issued, [&](int st, uint32_t parity) { return warp_wait(empty + st, parity); });
   } else if (warp == 1) {
     if (rank == 0) {
       Ring ring(S::kStages);
@@ -564,7 +562,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
         }
       }
       if (!ok) {  // products in flight end before the tensor memory is given back
-        if (elect_one()) mma_commit<true>(drained);
+        if (elect_one()) mma_commit<true>(drained, 1);
         __syncwarp();
         warp_wait(drained, 0);
       }
@@ -575,7 +573,9 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
     int64_t i = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int acc = int(i & 1);
-      if (!warp_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
+      // (each lane's answer, all the same, by way of a shuffle: known to be the warp's, it made the loop's addresses
+      // uniform registers, and the epilogue slower: bf16 8192 x 1024 x 4096 with GELU and Z 132 us for 130)
+      if (!__shfl_sync(0xffffffffu, int(warp_wait(ready + acc, uint32_t(i >> 1) & 1)), lane)) break;
       tmem_fence_after();
       const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
       int64_t tm, tn;
@@ -820,11 +820,10 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
       __syncwarp();
       issued = min(issued + 1, a.stages);
     }
-    for (int i = 0; i < issued; ++i) {  // the last loads have landed before the stages serve for anything else
-      ring.st = ring.st == 0 ? a.stages - 1 : ring.st - 1;
-      if (ring.st == a.stages - 1) ring.phase ^= 1;
-      if (!warp_wait(full + ring.st, ring.phase)) break;
-    }
+    // the last loads have landed before the stages serve for anything else, the last products' arrivals before
+    // the barriers' memory may
+    last_uses(ring, issued, [&](int st, uint32_t parity) { return warp_wait(full + st, parity) || true; });
+    last_uses(ring, issued, [&](int st, uint32_t parity) { return warp_wait(empty + st, parity); });
   } else if (warp == 1) {
     Ring ring(a.stages);
     QuadRing quad;
@@ -877,6 +876,7 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
     for (int i = 0; i < 3; ++i)
       if (k0 + 4 * i < k1) ahead.fetch(i, sr, row, int64_t(k0 / 4 + i) * 16);
     Ring ring(kScaleQuads);
+    int issued = 0;
     for (int k = k0; k < k1; k += 4, ring.next()) {
       if (k - k0 >= 4 * kScaleQuads && !warp_wait(sempty + ring.st, ring.phase ^ 1)) break;
 #pragma unroll
@@ -888,7 +888,9 @@ k_mm_split(const __grid_constant__ SplitArgs a) {
       if (lane == 0) mbar_arrive(sfull + ring.st);
       ahead.shift();
       if (k + 12 < k1) ahead.fetch(2, sr, row, int64_t(k / 4 + 3) * 16);
+      issued = min(issued + 1, kScaleQuads);
     }
+    last_uses(ring, issued, [&](int st, uint32_t parity) { return warp_wait(sempty + st, parity); });
   }
   __syncwarp();
   __syncthreads();  // the products are done, the stages free

@@ -221,14 +221,15 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
   else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-// Arrives on `bar` (with PAIR on that of both CTAs) once this thread's matrix products so far are done.
+// Arrives on `bar` (with PAIR on that of the CTAs in `ctas`, a bit each) once this thread's matrix products so
+// far are done.  Someone in each of those CTAs waits for it before the CTA leaves.
 template <bool PAIR>
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint16_t ctas = 3) {
   if constexpr (PAIR) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
-        "h"(uint16_t(3))
+        "h"(ctas)
         : "memory");
   } else {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
