@@ -30,13 +30,13 @@
 #include <cuda_runtime.h>
 
 #include "activation.cuh"
+#include "cluster_launch.h"
 #include "column_walk.cuh"
 #include "device_common.cuh"
 #include "launch_util.h"
 #include "mx8.cuh"
 #include "mx8_internal.h"
 #include "ring_tail.h"
-#include "smem_limit.h"
 #include "umma.cuh"
 
 namespace ep {
@@ -1158,60 +1158,6 @@ cudaError_t make_scale_map(CUtensorMap* map, const void* p, int64_t blocks, int 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename Args>
-cudaError_t launch_cluster(void (*kernel)(Args), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
-                           cudaStream_t stream, const Args& args) {
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = EP_PDL ? 1 : 0;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
-}
-
-// Pairs of CTAs that fit on the device at once.
-template <typename Args>
-cudaError_t resident_pairs(void (*kernel)(Args), unsigned threads, size_t smem, int sm_count, int* pairs) {
-  static std::mutex mu;
-  static int known[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lk(mu);
-  if (dev < 64 && known[dev] != 0) {
-    *pairs = known[dev];
-    return cudaSuccess;
-  }
-  e = allow_smem(reinterpret_cast<const void*>(kernel));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(sm_count) / 2 * 2);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-  if (e != cudaSuccess) return e;
-  *pairs = std::max(1, n);
-  if (dev < 64) known[dev] = *pairs;
-  return cudaSuccess;
-}
-
 int64_t tiles_of(int64_t rows, int tile) { return (rows + tile - 1) / tile; }
 
 // Which kernel, tile and cut of K: the least of these estimates, in cycles, which
@@ -1307,7 +1253,7 @@ cudaError_t launch_pair(PairArgs* a, int sm_count, cudaStream_t stream, int* lau
   a->first = a->p[0].tiles_m * a->p[0].tiles_n;
   a->tiles = a->first + (TWO ? a->p[1].tiles_m * a->p[1].tiles_n : 0);
   int pairs = 1;
-  cudaError_t e = resident_pairs(kernel, kPairThreads, S::kSmem, sm_count, &pairs);
+  cudaError_t e = resident_clusters(kernel, kPairThreads, S::kSmem, 2, sm_count, &pairs);
   if (e != cudaSuccess) return e;
   e = launch_cluster(kernel, unsigned(2 * std::min<int64_t>(a->tiles, pairs)), kPairThreads, S::kSmem, 2, stream, *a);
   if (e == cudaSuccess) ++*launches;
