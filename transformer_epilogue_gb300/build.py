@@ -28,7 +28,7 @@ SOURCES = ["ep_api.cpp", "skip_layer_norm.cu", "bias_softmax.cu", "elementwise.c
            "group_norm_fused.cu", "bias_dropout.cu", "rms_norm_mx8.cu", "matmul.cu"]
 # Compiled in one piece: split, a kernel's code depends on what else the file holds and on the number of
 # cores (the same k_gn_token_staged ran f32 4096x1x1024 in 8.3 or 10.5 us from one build to the next).
-WHOLE = ("group_norm.cu", "group_norm_fused.cu")
+WHOLE = ("group_norm.cu", "group_norm_fused.cu", "matmul.cu", "rms_norm_mx8.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC,
           "--expt-relaxed-constexpr"]
