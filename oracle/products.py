@@ -15,7 +15,7 @@ GROUP = 32
 MOST = 448.0
 ACTS = ("none", "silu", "relu", "quick_gelu", "gelu", "fast_gelu")
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])  # 1 + erf has no digits left of its own below z = -8
 
 
 # ---------------------------------------------------------------------------
@@ -118,7 +118,7 @@ def activation(z, act, alpha=1.702):
     low = np.isneginf(z) if act != "quick_gelu" else np.isneginf(alpha * z)
     with np.errstate(invalid="ignore"):
         if act == "gelu":
-            y = 0.5 * z * (1.0 + _erf(z / math.sqrt(2.0)))
+            y = 0.5 * z * _erfc(-z / math.sqrt(2.0))
         else:
             y = z * _gate(_inner(z, act, alpha)[0])[0]
     return np.where(low, 0.0, y)
@@ -130,7 +130,7 @@ def activation_slope(z, act, alpha=1.702):
     if act == "relu":
         return np.where(z > 0, 1.0, 0.0)
     if act == "gelu":
-        return 0.5 * (1.0 + _erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+        return 0.5 * _erfc(-z / math.sqrt(2.0)) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
     t, d = _inner(z, act, alpha)
     s, r = _gate(t)
     return s + z * d * s * r
