@@ -573,9 +573,7 @@ k_mm_pair(const __grid_constant__ PairArgs a) {
     int64_t i = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int acc = int(i & 1);
-      // (each lane's answer, all the same, by way of a shuffle: known to be the warp's, it made the loop's addresses
-      // uniform registers, and the epilogue slower: bf16 8192 x 1024 x 4096 with GELU and Z 132 us for 130)
-      if (!__shfl_sync(0xffffffffu, int(warp_wait(ready + acc, uint32_t(i >> 1) & 1)), lane)) break;
+      if (!warp_wait(ready + acc, uint32_t(i >> 1) & 1)) break;
       tmem_fence_after();
       const PairProduct& p = a.p[TWO && t >= a.first ? 1 : 0];
       int64_t tm, tn;
