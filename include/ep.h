@@ -505,9 +505,11 @@ size_t ep_skip_rms_norm_grad_workspace_size(ep_dtype t, const int64_t* shape, in
  * bias          N elements, or NULL.  residual: (M, N), or NULL.
  * activation    EP_ACT_NONE; EP_ACT_SILU z s(z); EP_ACT_RELU; EP_ACT_QUICK_GELU z s(alpha z);
  *               EP_ACT_GELU z Phi(z) (the error function); EP_ACT_FAST_GELU its tanh form
- *               z s(2 sqrt(2/pi) (z + 0.044715 z^3)).  s(x) = 1 / (1 + e^-x); all are 0 at
- *               z = -infinity.  alpha: of EP_ACT_QUICK_GELU alone (the QuickGelu op's default
- *               is 1.702), finite.
+ *               z s(2 sqrt(2/pi) (z + 0.044715 z^3)).  s(x) = 1 / (1 + e^-x).  At z = -infinity
+ *               the last five are 0, EP_ACT_QUICK_GELU where alpha > 0: with alpha < 0 it is
+ *               0 at +infinity and -infinity at -infinity, with alpha = 0 NaN at both.
+ *               Results of theirs below 2^-100 in magnitude may be 0.
+ *               alpha: of EP_ACT_QUICK_GELU alone (the QuickGelu op's default is 1.702), finite.
  * Y             (M, N); may be residual.
  * Z             NULL, or the pre-activation as the gradient wants it: (M, N) of T, or with
  *               Z_scales (M, ceil(N / 32)) in MX8.
