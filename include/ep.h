@@ -451,7 +451,8 @@ ep_status ep_dequantize_mx8(ep_dtype t, const void* Q, const uint8_t* scales, co
  *
  *   s = (input + skip) + bias           (float32, in this order; skip and bias optional)
  *   input_skip_bias_sum = T(s)          (optional output)
- *   inv = 1 / sqrt(mean(s^2) + epsilon) over the last axis
+ *   inv = 1 / sqrt(mean(s^2) + epsilon) over the last axis (a float32 sum, in an order fixed
+ *         by the shape and by which operands start on 16-byte boundaries)
  *   Q, scales = MX8(s * inv * gamma)    (of the float32 values: not rounded to T before)
  *
  * input, skip   `rank` dims (1 <= rank <= 16); skip has input's shape, or is NULL.
@@ -478,8 +479,9 @@ ep_status ep_skip_rms_norm_mx8(ep_dtype t, const void* input, const int64_t* sha
  * s             input_skip_bias_sum as the forward call left it; inv_std_dev its float32 statistic.
  * dsum          the gradient that reaches input_skip_bias_sum by other ways (the residual stream), or NULL.
  * dX            the shape of dY; may be dY, s or dsum.
- * dgamma, dbias H elements of T, or NULL: float32 sums of the unrounded values in a fixed
- *               order, rounded once (float16: infinite from 65520 on).  Of no rows they are set to 0.
+ * dgamma, dbias H elements of T, or NULL: float32 sums of the unrounded values, rounded once
+ *               (float16: infinite from 65520 on).  Of no rows they are set to 0.  The order of all
+ *               sums is fixed by the shape and by which operands start on 16-byte boundaries.
  * workspace     ep_skip_rms_norm_grad_workspace_size() bytes, 16-byte aligned; its contents
  *               on entry do not matter.  Calls that may overlap on the GPU need one each.
  *
