@@ -13,7 +13,7 @@
 // latency (loads, reduction, stores: some 3000 cycles) is also the other rows of the
 // SM's blocks.  Beside the memory it is the instructions that bind (38 an element at
 // first, 70 % of the issue slots: bf16 16384 x 4096 in 88 us): products and sums go two
-// to an instruction, indexes are 32-bit within a row (73 us, 94 % of the copy rate).
+// to an instruction, indexes are 32-bit within a row (29 an element, 72 us, 96 % of the copy rate).
 // Rows that came through a ring of bulk copies took 104 us, blocks of one row each 91.
 // Rows too long for the registers are read twice by a block of 512 threads.
 #include <algorithm>
@@ -217,7 +217,7 @@ __device__ __forceinline__ void split_index(uint64_t i, uint32_t d, uint64_t* ro
 
 // A group of 32 to 32 / VW lanes, U groups each before the first is used.  VW 1: rows of
 // a few groups, which would leave most of k_quantize_ragged's 256 elements empty (f16
-// 60710 x 3: 8 us for 19).
+// 60710 x 3: 7 us for 18).
 template <typename T, int VW, int U>
 __global__ void __launch_bounds__(kRowThreads)
 k_quantize(const T* __restrict__ x, uint8_t* __restrict__ q, uint8_t* __restrict__ scales, int64_t items, uint32_t H,
@@ -518,8 +518,8 @@ k_norm_long(RmsNormArgs a) {
 // ODD: rows that start on no 16-byte boundary, in a tensor that does.  A row's fragments
 // begin at the boundary in front of it, and rows 8 apart lie alike, so with steps of
 // 8 rows a thread keeps its columns; those of a fragment that are not in the row, at either
-// end, are left out one by one.  (f16 13331 x 5034: 207 us for 530 element by element, bf16
-// 26577 x 2525 with dbias 147 for 419.)
+// end, are left out one by one.  (f16 13331 x 5034: 186 us for 488 element by element, bf16
+// 26577 x 2525 with dbias 154 for 207.)
 template <typename T, int VW, int NF, bool LONG, bool DB, bool ODD>
 __global__ void __launch_bounds__(LONG ? kLongThreads : kRowThreads, LONG ? 1 : NF * VW <= 4 ? 4 : 2)
 k_norm_grad(const __grid_constant__ RmsNormGradArgs a, float inv_h) {
@@ -786,9 +786,9 @@ void plan_threads(RowPlan* p, int64_t frags, int most_nf, int best_nf) {
 
 // 8 elements a fragment: rows of up to 128 elements share a warp (4, 8 or 16 threads
 // each); else two fragments a thread and four blocks an SM where that wastes no lanes
-// (bf16 16384 x 4096: 73 us; four fragments and two blocks 76), up to four where it
-// does or does not hold the row (f16 65536 x 768: 58 us with three, 68 with two; bf16
-// 8192 x 8192: 76 with four, 104 with two).  The gradient has its column sums in
+// (bf16 16384 x 4096: 72 us, as four fragments and two blocks), up to four where it
+// does or does not hold the row (f16 65536 x 768: 55 us with three, 86 with two; bf16
+// 8192 x 8192: 73 with four).  The gradient has its column sums in
 // registers too: two, and four where two do not hold the row.
 RowPlan plan_rows(int64_t H, bool vec, bool grad) {
   RowPlan p{vec ? 8 : 1, 0, 0, 1, false, false};
@@ -810,8 +810,9 @@ RowPlan plan_rows(int64_t H, bool vec, bool grad) {
 
 // The gradient's rows where the tensors (but not the rows) start on 16-byte boundaries: with up
 // to 7 elements in front, in fragments of 8, from 96 elements a row and 8 million in all on
-// (bf16 65536 x 129: 58 us for 89, f32 40775 x 325 50 for 55; where the elements left out one
-// by one and fewer warps are felt it loses: bf16 65536 x 101 34 for 30, f32 4300 x 1001 27 for 22).
+// (bf16 65536 x 129: 49 us for 78, f16 20000 x 1001 46 for 62, f32 40775 x 325 50 for 50; where the
+// elements left out one by one and fewer warps are felt it loses: f32 2053 x 1001 with dbias 18 for 15, bf16
+// 65536 x 101 28.7 for 27.5, and among those it takes f16 90000 x 97 37 for 35).
 RowPlan plan_grad_rows(int64_t rows, int64_t H, bool aligned) {
   RowPlan p = plan_rows(H, aligned && H % 8 == 0, true);
   if (!aligned || H % 8 == 0 || H < 96 || rows * H < int64_t(8) << 20) return p;
@@ -845,7 +846,7 @@ cudaError_t norm_form(const RmsNormArgs& a, const RowPlan& p, int sm_count, cuda
 // The gradient's blocks: as many as an SM's registers hold (up to 64, 112 and 128 a
 // thread), but no more than leave sums of a fourth of what is read (their sums are
 // written and read again); a number that follows from the shape alone, as the
-// workspace does.  (f16 65536 x 768: 76 us with three blocks of 192 threads an SM, 108 with two.)
+// workspace does.  (f16 65536 x 768: 82 us with three blocks of 192 threads an SM, 103 with two.)
 int64_t grad_blocks(int64_t rows, const RowPlan& p, int es) {
   const int elements = p.nf * p.vw, regs = elements <= 4 ? 64 : elements <= 8 ? 112 : 128;
   const int64_t per_sm = p.wide ? 1 : std::max(1, 65536 / (regs * p.tpr * p.slots));
