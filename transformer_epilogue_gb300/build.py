@@ -26,8 +26,9 @@ LIB = os.path.join(LIBDIR, "libtransformer_epilogue.so")
 
 SOURCES = ["ep_api.cpp", "skip_layer_norm.cu", "bias_softmax.cu", "elementwise.cu", "group_norm.cu",
            "group_norm_fused.cu", "bias_dropout.cu", "rms_norm_mx8.cu", "matmul.cu"]
-# Compiled in one piece: split, a kernel's code depends on what else the file holds and on the number of
-# cores (the same k_gn_token_staged ran f32 4096x1x1024 in 8.3 or 10.5 us from one build to the next).
+# Compiled in one piece: split, a kernel's code depends on what else the file holds, on the number of cores
+# and on the build (k_gn_token_staged ran f32 4096x1x1024 in 8.3 or 10.5 us from one build to the next,
+# k_mm_pair bf16 8192x1024x4096 with GELU and Z in 119.5 or 134.9; in one piece 126 to 130).
 WHOLE = ("group_norm.cu", "group_norm_fused.cu", "matmul.cu", "rms_norm_mx8.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC,
